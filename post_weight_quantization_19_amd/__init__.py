@@ -20,7 +20,8 @@ from ._lib import PwqError, check, lib, make_grid, parse_result
 
 __all__ = ["Grid", "hessian_accum", "damp_cholesky", "damp_cholesky_static", "grid_steps", "babai_sweep",
            "quant_layer", "column_entropy", "read_result", "PwqError", "KernelTimer",
-           "HessianTileTimer", "overflow_entries", "ssqr_quant_layer"]
+           "HessianTileTimer", "overflow_entries", "ssqr_quant_layer", "pack_weights", "rms_norm",
+           "packed_linear"]
 
 
 @dataclass(frozen=True)
@@ -486,3 +487,142 @@ def ssqr_quant_layer(W: torch.Tensor, X: Optional[torch.Tensor] = None,
     o.update(kappa=float(kappa.value), n_outliers=int(n_out.value), rows=rows[:k],
              cols=cols[:k], vals=vals[:k])
     return o
+
+
+# ------------------------------------------------------------ running a packed layer
+
+_DTYPES = {torch.float32: _lib.PWQ_F32, torch.bfloat16: _lib.PWQ_BF16, torch.int8: _lib.PWQ_I8}
+
+
+def pack_weights(codes: torch.Tensor, scales: torch.Tensor, grid: Grid,
+                 zeros: Optional[torch.Tensor] = None) -> dict:
+    """Codes [m, n] int32, steps and zero points of a SYM / ASYM grid of at
+    most 4 bits (as returned by quant_layer or ssqr_quant_layer) -> the packed
+    layer that packed_linear reads: dict(qweight, scales, zeros, n, group,
+    outlier_off, outliers).  Codes outside 4 bits go into the overflow list,
+    so nothing is clipped.  Raises ValueError where a lattice step exceeds
+    127.  Synchronous (the list's length is read on the host)."""
+    _require_cuda(codes, scales, zeros)
+    if codes.dtype != torch.int32:
+        raise TypeError("codes must be int32")
+    m, n = codes.shape
+    if grid.kind not in ("sym", "asym"):
+        raise ValueError("a packed layer has group steps: grid kind sym or asym")
+    if grid.group and n % grid.group:
+        raise ValueError(f"group {grid.group} does not divide n = {n}")
+    ng = n // (grid.group or n)
+    asym = grid.kind == "asym"
+    _check(scales, "scales", (m, ng), _F32)
+    _check(zeros, "zeros", (m, ng), _I32)
+    if asym and zeros is None:
+        raise ValueError("an asym grid needs zeros")
+    ldc = _row_major(codes) if m > 0 else n
+    dev = codes.device
+    L_ = lib()
+    g = grid.c_struct()
+    qweight = torch.empty((m, L_.pwq_packed_row_bytes(n)), dtype=torch.uint8, device=dev)
+    zeros8 = torch.empty((m, ng), dtype=torch.uint8, device=dev) if asym else None
+    off = torch.empty(L_.pwq_pack_tiles(m, n) + 1, dtype=torch.int32, device=dev)
+    info = torch.empty(2, dtype=torch.int32, device=dev)
+    check(L_.pwq_pack_codes(codes.data_ptr(), m, n, ldc, g, _ptr(zeros) if asym else None,
+                            qweight.data_ptr(), _ptr(zeros8), off.data_ptr(), info.data_ptr(),
+                            _stream()))
+    count, wide, bad = torch.cat((off[-1:], info)).tolist()
+    if wide or bad:
+        raise ValueError(f"{wide} codes are more than 127 steps from zero and {bad} zero points "
+                         "lie outside 0 .. 127: the layer cannot be packed")
+    outliers = None
+    if count:
+        outliers = torch.empty(count, dtype=torch.int32, device=dev)
+        check(L_.pwq_pack_overflow(codes.data_ptr(), m, n, ldc, g, off.data_ptr(),
+                                   outliers.data_ptr(), count, _stream()))
+    return {"qweight": qweight, "scales": scales, "zeros": zeros8, "n": n,
+            "group": grid.group or n, "outlier_off": off if count else None,
+            "outliers": outliers}
+
+
+def rms_norm(x: torch.Tensor, weight: torch.Tensor, residual: Optional[torch.Tensor] = None,
+             eps: float = 1e-6, out_dtype: Optional[torch.dtype] = None,
+             sum_out: Optional[torch.Tensor] = None):
+    """Root-mean-square norm of x (+ residual), [tokens, n] bf16 or fp32, per
+    token: (y, scales or None, sum or None).  ``out_dtype`` is bf16, fp32
+    (default: x's) or int8, which comes with a step per token (scales [tokens]
+    fp32, y = codes).  ``sum`` is x + residual in x's type, written to
+    ``sum_out`` where given (x or residual itself for in place)."""
+    _require_cuda(x, weight, residual, sum_out)
+    ldx = _row_major(x)
+    ntok, n = x.shape
+    xdt = _dtype_code(x)
+    if weight.shape != (n,) or not weight.is_contiguous():
+        raise ValueError(f"weight must be a contiguous [{n}] tensor")
+    wdt = _dtype_code(weight)
+    odt = x.dtype if out_dtype is None else out_dtype
+    if odt not in _DTYPES:
+        raise TypeError(f"unsupported output dtype {odt}")
+    if residual is None and sum_out is not None:
+        raise ValueError("sum_out goes with a residual")
+    for t, name in ((residual, "residual"), (sum_out, "sum_out")):
+        if t is not None and (t.shape != x.shape or t.dtype != x.dtype):
+            raise ValueError(f"{name} must have x's shape and type")
+    total = sum_out
+    if residual is not None and total is None:
+        total = torch.empty((ntok, n), dtype=x.dtype, device=x.device)
+    y = torch.empty((ntok, n), dtype=odt, device=x.device)
+    scales = (torch.empty(ntok, dtype=torch.float32, device=x.device) if odt == torch.int8
+              else None)
+    check(lib().pwq_rms_norm(x.data_ptr(), xdt, ntok, n, ldx, _ptr(residual),
+                             0 if residual is None else _row_major(residual), weight.data_ptr(),
+                             wdt, eps, _ptr(total), 0 if total is None else _row_major(total),
+                             y.data_ptr(), _DTYPES[odt], n, _ptr(scales), _stream()))
+    return y, scales, total
+
+
+def packed_linear(x: torch.Tensor, packed: dict, x_scales: Optional[torch.Tensor] = None,
+                  out_dtype: Optional[torch.dtype] = None,
+                  out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """y [tokens, m] = x [tokens, n] times a packed layer (pack_weights).  x is
+    bf16, fp32, or int8 with a step per token (``x_scales`` [tokens] fp32, as
+    from rms_norm).  ``out_dtype`` is bf16 or fp32 (default: x's; bf16 for
+    int8); ``out`` may pass the result's memory."""
+    q, scales, zeros = packed["qweight"], packed["scales"], packed["zeros"]
+    off, outliers = packed["outlier_off"], packed["outliers"]
+    n, group = packed["n"], packed["group"]
+    _require_cuda(x, q, scales, zeros, off, outliers, x_scales, out)
+    ldx = _row_major(x)
+    ntok, m = x.shape[0], q.shape[0]
+    if x.shape[1] != n:
+        raise ValueError(f"x has {x.shape[1]} columns, the layer {n}")
+    if x.dtype not in _DTYPES:
+        raise TypeError(f"unsupported dtype {x.dtype}")
+    if group <= 0 or n % group:
+        raise ValueError(f"group {group} does not divide n = {n}")
+    _check(q, "qweight", (m, (n + 31) // 32 * 16), (torch.uint8,))
+    _check(scales, "scales", (m, n // group), _F32)
+    _check(zeros, "zeros", (m, n // group), (torch.uint8,))
+    if outliers is not None:
+        _check(off, "outlier_off", ((m + 15) // 16 * ((n + 127) // 128) + 1,), _I32)
+        _check(outliers, "outliers", (outliers.numel(),), _I32)
+    if (x.dtype == torch.int8) != (x_scales is not None):
+        raise ValueError("x_scales goes with int8 x, and only with it")
+    _check(x_scales, "x_scales", (ntok,), _F32)
+    odt = out_dtype
+    if odt is None:
+        odt = out.dtype if out is not None else (torch.bfloat16 if x.dtype == torch.int8
+                                                 else x.dtype)
+    if odt not in (torch.bfloat16, torch.float32):
+        raise TypeError(f"unsupported output dtype {odt}")
+    if out is None:
+        out = torch.empty((ntok, m), dtype=odt, device=x.device)
+    elif out.shape != (ntok, m) or out.dtype != odt:
+        raise ValueError(f"out must be [{ntok}, {m}] {odt}")
+    L_ = lib()
+    xdt = _DTYPES[x.dtype]
+    nb = L_.pwq_packed_linear_workspace_size(ntok, m, n, group, xdt)
+    ws = _workspace(nb, x.device) if nb else None
+    check(L_.pwq_packed_linear(x.data_ptr(), xdt, ntok, ldx, _ptr(x_scales), q.data_ptr(), m, n,
+                               scales.data_ptr(), _ptr(zeros), group,
+                               _ptr(off) if outliers is not None else None, _ptr(outliers),
+                               0 if outliers is None else outliers.numel(), out.data_ptr(),
+                               _DTYPES[odt], _row_major(out) if ntok and m else m, _ptr(ws), nb,
+                               _stream()))
+    return out

@@ -13,6 +13,7 @@ LIB_PATH = os.path.join(HERE, "libpwq.so")
 
 PWQ_OK, PWQ_ERR_INVALID_ARG, PWQ_ERR_UNSUPPORTED, PWQ_ERR_WORKSPACE, PWQ_ERR_HIP = range(5)
 PWQ_F32, PWQ_BF16, PWQ_F64 = 0, 1, 2
+PWQ_I8 = 3                    # 8-bit integers (include/pwq_serve.h)
 PWQ_X_TOKEN_MAJOR = 0x100     # X stored ntok x n (one row per token)
 GRID_KINDS = {"sym": 0, "asym": 1, "colspacing": 2}
 ORDERS = {"back_to_front": 0, "front_to_back": 1, "perm": 2, "act_order": 3, "min_pivot": 4}
@@ -31,6 +32,11 @@ EXPORTS = [
     "pwq_ssqr_workspace_size", "pwq_ssqr_quant_layer",
     "pwq_min_pivot_workspace_size", "pwq_min_pivot_order",
     "pwq_oaem_workspace_size", "pwq_oaem_init",
+]
+# and include/pwq_serve.h (packed layers)
+SERVE_EXPORTS = [
+    "pwq_packed_row_bytes", "pwq_pack_tiles", "pwq_pack_codes", "pwq_pack_overflow",
+    "pwq_rms_norm", "pwq_packed_linear_workspace_size", "pwq_packed_linear",
 ]
 PWQ_TIMER_HESSIAN_TILES, PWQ_TIMER_LAZY_UPDATE, PWQ_TIMER_SWEEP_BLOCK = 0, 1, 2
 TIMED_KERNELS = {"hessian_tiles": PWQ_TIMER_HESSIAN_TILES, "lazy_update": PWQ_TIMER_LAZY_UPDATE,
@@ -91,6 +97,17 @@ _SIGS = {
                                     _vp, _vp, _vp, _vp, _i64, _vp, _vp, _vp,
                                     ctypes.POINTER(ctypes.c_int64),
                                     ctypes.POINTER(ctypes.c_double), _vp, _sz, _vp]),
+    "pwq_packed_row_bytes": (_i64, [_i64]),
+    "pwq_pack_tiles": (_i64, [_i64, _i64]),
+    "pwq_pack_codes": (_i32, [_vp, _i64, _i64, _i64, ctypes.POINTER(PwqGrid), _vp, _vp, _vp, _vp,
+                              _vp, _vp]),
+    "pwq_pack_overflow": (_i32, [_vp, _i64, _i64, _i64, ctypes.POINTER(PwqGrid), _vp, _vp, _i64,
+                                 _vp]),
+    "pwq_rms_norm": (_i32, [_vp, _i32, _i64, _i64, _i64, _vp, _i64, _vp, _i32, _f64, _vp, _i64,
+                            _vp, _i32, _i64, _vp, _vp]),
+    "pwq_packed_linear_workspace_size": (_sz, [_i64, _i64, _i64, _i32, _i32]),
+    "pwq_packed_linear": (_i32, [_vp, _i32, _i64, _i64, _vp, _vp, _i64, _i64, _vp, _vp, _i32,
+                                 _vp, _vp, _i64, _vp, _i32, _i64, _vp, _sz, _vp]),
     "pwq_kernel_timer_attach": (_i32, [_i32, _vp, _vp, _i64]),
     "pwq_kernel_timer_count": (_i64, [_i32]),
 }

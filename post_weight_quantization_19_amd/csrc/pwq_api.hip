@@ -841,4 +841,140 @@ pwq_status pwq_ssqr_quant_layer(const void* W, int32_t wdtype, int64_t m, int64_
   return ok();
 }
 
+// ------------------------------------------------------------ packed layers
+
+int64_t pwq_packed_row_bytes(int64_t n) { return n > 0 && n <= INT32_MAX ? packed_row_bytes(n) : 0; }
+
+int64_t pwq_pack_tiles(int64_t m, int64_t n) {
+  if (m < 0 || n <= 0 || m > INT32_MAX || n > INT32_MAX) return 0;
+  return (m + kPackRows - 1) / kPackRows * ((n + kPackCols - 1) / kPackCols);
+}
+
+static pwq_status check_pack(const void* codes, int64_t m, int64_t n, int64_t ldc,
+                             const pwq_grid* grid) {
+  if (m < 0 || n <= 0 || m > INT32_MAX || n > INT32_MAX)
+    return fail(PWQ_ERR_INVALID_ARG, "need 0 <= m < 2^31 and 1 <= n < 2^31");
+  if (m > 0 && !codes) return fail(PWQ_ERR_INVALID_ARG, "codes is NULL");
+  if (m > 0 && ldc < n) return fail(PWQ_ERR_INVALID_ARG, "ldc < n");
+  if (pwq_pack_tiles(m, n) >= INT32_MAX)
+    return fail(PWQ_ERR_UNSUPPORTED, "more than 2^31 - 2 tiles of 16 x 128");
+  pwq_status s = check_grid(grid, n, true);
+  if (s != PWQ_OK) return s;
+  if (grid->kind == PWQ_GRID_COLSPACING)
+    return fail(PWQ_ERR_UNSUPPORTED, "a packed layer has group steps: SYM or ASYM");
+  if (grid->bits > 4)
+    return fail(PWQ_ERR_UNSUPPORTED, "a packed layer holds grids of at most 4 bits (got %d)",
+                grid->bits);
+  return PWQ_OK;
+}
+
+pwq_status pwq_pack_codes(const int32_t* codes, int64_t m, int64_t n, int64_t ldc,
+                          const pwq_grid* grid, const int32_t* zeros, uint8_t* qweight,
+                          uint8_t* zeros8, int32_t* outlier_off, int32_t* info, void* stream) {
+  pwq_status s = check_pack(codes, m, n, ldc, grid);
+  if (s != PWQ_OK) return s;
+  if (!outlier_off || !info || (m > 0 && !qweight))
+    return fail(PWQ_ERR_INVALID_ARG, "qweight, outlier_off and info must be non-NULL");
+  if ((uintptr_t)qweight % 16) return fail(PWQ_ERR_INVALID_ARG, "qweight must be 16-byte aligned");
+  const bool asym = grid->kind == PWQ_GRID_ASYM;
+  if (asym && m > 0 && (!zeros || !zeros8))
+    return fail(PWQ_ERR_INVALID_ARG, "ASYM grid needs zeros and zeros8");
+  const int G = group_of(grid, n);
+  if (asym && m * (n / G) > (int64_t)INT32_MAX * 256)
+    return fail(PWQ_ERR_UNSUPPORTED, "too many zero points");
+  const hipError_t e = launch_pack_codes(codes, m, n, ldc, asym, zeros, G, qweight, zeros8,
+                                         outlier_off, info, (hipStream_t)stream);
+  if (e != hipSuccess) return hip_fail(e, "pack_codes launch");
+  return ok();
+}
+
+pwq_status pwq_pack_overflow(const int32_t* codes, int64_t m, int64_t n, int64_t ldc,
+                             const pwq_grid* grid, const int32_t* outlier_off,
+                             int32_t* outliers, int64_t max_out, void* stream) {
+  pwq_status s = check_pack(codes, m, n, ldc, grid);
+  if (s != PWQ_OK) return s;
+  if (max_out < 0) return fail(PWQ_ERR_INVALID_ARG, "max_out must be >= 0");
+  if (!outlier_off || (max_out > 0 && !outliers))
+    return fail(PWQ_ERR_INVALID_ARG, "outlier_off and outliers must be non-NULL");
+  if (max_out == 0) return ok();
+  const hipError_t e = launch_pack_overflow(codes, m, n, ldc, grid->kind == PWQ_GRID_ASYM,
+                                            outlier_off, outliers, max_out, (hipStream_t)stream);
+  if (e != hipSuccess) return hip_fail(e, "pack_overflow launch");
+  return ok();
+}
+
+pwq_status pwq_rms_norm(const void* x, int32_t xdtype, int64_t ntok, int64_t n, int64_t ldx,
+                        const void* residual, int64_t ldr, const void* weight, int32_t wdtype,
+                        double eps, void* sum, int64_t lds, void* y, int32_t ydtype,
+                        int64_t ldy, float* scales, void* stream) {
+  if (ntok < 0 || n <= 0 || ntok > INT32_MAX || n > INT32_MAX)
+    return fail(PWQ_ERR_INVALID_ARG, "need 0 <= ntok < 2^31 and 1 <= n < 2^31");
+  if (xdtype != PWQ_F32 && xdtype != PWQ_BF16)
+    return fail(PWQ_ERR_INVALID_ARG, "x must be PWQ_F32 or PWQ_BF16");
+  if (wdtype != PWQ_F32 && wdtype != PWQ_BF16)
+    return fail(PWQ_ERR_INVALID_ARG, "weight must be PWQ_F32 or PWQ_BF16");
+  if (ydtype != PWQ_F32 && ydtype != PWQ_BF16 && ydtype != PWQ_I8)
+    return fail(PWQ_ERR_INVALID_ARG, "y must be PWQ_F32, PWQ_BF16 or PWQ_I8");
+  if (!(eps >= 0.0) || !(eps < 1e30))
+    return fail(PWQ_ERR_INVALID_ARG, "eps must be finite and >= 0");
+  if (!weight || (ntok > 0 && (!x || !y)))
+    return fail(PWQ_ERR_INVALID_ARG, "x, weight and y must be non-NULL");
+  if (ntok > 0 && ydtype == PWQ_I8 && !scales)
+    return fail(PWQ_ERR_INVALID_ARG, "8-bit y needs scales");
+  if (ldx < n || ldy < n || (residual && ldr < n) || (sum && lds < n))
+    return fail(PWQ_ERR_INVALID_ARG, "row strides must be >= n");
+  if (ntok > 0 && (y == x || y == residual || y == sum))
+    return fail(PWQ_ERR_INVALID_ARG, "y must not be the memory of x, residual or sum");
+  if (sum && ((sum == x && lds != ldx) || (sum == residual && lds != ldr)))
+    return fail(PWQ_ERR_INVALID_ARG, "sum in place needs the same row stride");
+  RmsNormLaunch a{x, xdtype, ntok, n, ldx, residual, ldr, weight, wdtype, (float)eps, sum, lds,
+                  y, ydtype, ldy, scales};
+  const hipError_t e = launch_rms_norm(a, (hipStream_t)stream);
+  if (e != hipSuccess) return hip_fail(e, "rms_norm launch");
+  return ok();
+}
+
+size_t pwq_packed_linear_workspace_size(int64_t ntok, int64_t m, int64_t n, int32_t group,
+                                        int32_t xdtype) {
+  (void)ntok, (void)m, (void)n, (void)group, (void)xdtype;
+  return 0;
+}
+
+pwq_status pwq_packed_linear(const void* x, int32_t xdtype, int64_t ntok, int64_t ldx,
+                             const float* x_scales, const uint8_t* qweight, int64_t m, int64_t n,
+                             const float* scales, const uint8_t* zeros, int32_t group,
+                             const int32_t* outlier_off, const int32_t* outliers, int64_t n_out,
+                             void* y, int32_t ydtype, int64_t ldy, void* ws, size_t ws_bytes,
+                             void* stream) {
+  if (ntok < 0 || m < 0 || n <= 0 || ntok > INT32_MAX || m > INT32_MAX || n > INT32_MAX)
+    return fail(PWQ_ERR_INVALID_ARG, "need 0 <= ntok, m < 2^31 and 1 <= n < 2^31");
+  if (xdtype != PWQ_F32 && xdtype != PWQ_BF16 && xdtype != PWQ_I8)
+    return fail(PWQ_ERR_INVALID_ARG, "x must be PWQ_F32, PWQ_BF16 or PWQ_I8");
+  if (ydtype != PWQ_F32 && ydtype != PWQ_BF16)
+    return fail(PWQ_ERR_INVALID_ARG, "y must be PWQ_F32 or PWQ_BF16");
+  if (group < 0 || (group > 0 && n % group))
+    return fail(PWQ_ERR_INVALID_ARG, "group %d does not divide n = %lld", group, (long long)n);
+  if (ldx < n || ldy < m) return fail(PWQ_ERR_INVALID_ARG, "need ldx >= n and ldy >= m");
+  if (n_out < 0 || n_out > INT32_MAX)
+    return fail(PWQ_ERR_INVALID_ARG, "n_out must be in [0, 2^31)");
+  if ((outlier_off != nullptr) != (outliers != nullptr) || (n_out > 0 && !outliers))
+    return fail(PWQ_ERR_INVALID_ARG, "outlier_off and outliers go together");
+  if ((xdtype == PWQ_I8) != (x_scales != nullptr) && ntok > 0)
+    return fail(PWQ_ERR_INVALID_ARG, "x_scales goes with 8-bit x, and only with it");
+  if (ntok > 0 && m > 0) {
+    if (!x || !qweight || !scales || !y)
+      return fail(PWQ_ERR_INVALID_ARG, "x, qweight, scales and y must be non-NULL");
+    if ((uintptr_t)qweight % 16)
+      return fail(PWQ_ERR_INVALID_ARG, "qweight must be 16-byte aligned");
+  }
+  pwq_status s = check_ws(ws, ws_bytes, pwq_packed_linear_workspace_size(ntok, m, n, group, xdtype));
+  if (s != PWQ_OK) return s;
+  PackedLinearLaunch a{x, xdtype, ntok, ldx, x_scales, qweight, m, n, packed_row_bytes(n), scales,
+                       zeros, group > 0 ? group : (int32_t)n, n_out > 0 ? outlier_off : nullptr,
+                       outliers, n_out, y, ydtype, ldy};
+  const hipError_t e = launch_packed_linear(a, (hipStream_t)stream);
+  if (e != hipSuccess) return hip_fail(e, "packed_linear launch");
+  return ok();
+}
+
 }  // extern "C"

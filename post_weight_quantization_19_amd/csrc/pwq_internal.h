@@ -6,6 +6,7 @@
 #include <stdint.h>
 
 #include "../../include/pwq.h"
+#include "../../include/pwq_serve.h"
 #include "pwq_device.h"
 
 namespace pwq {
@@ -152,6 +153,53 @@ hipError_t launch_min_pivot(const float* H, int64_t n, const double* lam, const 
 hipError_t launch_column_entropy(const int32_t* codes, int64_t m, int64_t n, int64_t ldc,
                                  double* bits, double* mean, int64_t* huff, int32_t* cmin,
                                  int32_t* cmax, hipStream_t st);
+
+// Root-mean-square norm (pwq_rms_norm).
+struct RmsNormLaunch {
+  const void* x;
+  int32_t xdtype;
+  int64_t ntok, n, ldx;
+  const void* residual;
+  int64_t ldr;
+  const void* weight;
+  int32_t wdtype;
+  float eps;
+  void* sum;
+  int64_t lds;
+  void* y;
+  int32_t ydtype;
+  int64_t ldy;
+  float* scales;
+};
+hipError_t launch_rms_norm(const RmsNormLaunch& a, hipStream_t st);
+
+// Packed layers: tiles of the overflow list, bytes of a packed row.
+constexpr int kPackRows = 16, kPackCols = 128;
+inline int64_t packed_row_bytes(int64_t n) { return (n + 31) / 32 * 16; }
+hipError_t launch_pack_codes(const int32_t* codes, int64_t m, int64_t n, int64_t ldc, bool asym,
+                             const int32_t* zeros, int G, uint8_t* qweight, uint8_t* zeros8,
+                             int32_t* off, int32_t* info, hipStream_t st);
+hipError_t launch_pack_overflow(const int32_t* codes, int64_t m, int64_t n, int64_t ldc, bool asym,
+                                const int32_t* off, int32_t* outliers, int64_t max_out,
+                                hipStream_t st);
+struct PackedLinearLaunch {
+  const void* x;
+  int32_t xdtype;
+  int64_t ntok, ldx;
+  const float* x_scales;
+  const uint8_t* qweight;
+  int64_t m, n, ldq;
+  const float* scales;
+  const uint8_t* zeros;
+  int32_t G;
+  const int32_t* outlier_off;
+  const int32_t* outliers;
+  int64_t n_out;
+  void* y;
+  int32_t ydtype;
+  int64_t ldy;
+};
+hipError_t launch_packed_linear(const PackedLinearLaunch& a, hipStream_t st);
 
 // Event pairs recorded around launches of one kernel (pwq_kernel_timer_attach).
 struct KernelTimer {
