@@ -223,7 +223,7 @@ hipError_t launch_pack_overflow(const int32_t* codes, int64_t m, int64_t n, int6
   return hipGetLastError();
 }
 
-hipError_t launch_packed_linear(const PackedLinearLaunch& a, hipStream_t st) {
+hipError_t launch_linear_any(const PackedLinearLaunch& a, hipStream_t st) {
   if (a.ntok == 0 || a.m == 0) return hipSuccess;
   const dim3 grid((unsigned)((a.m + 3) / 4), (unsigned)std::min<int64_t>((a.ntok + TT - 1) / TT,
                                                                          65535));

@@ -934,10 +934,27 @@ pwq_status pwq_rms_norm(const void* x, int32_t xdtype, int64_t ntok, int64_t n, 
   return ok();
 }
 
+// Which kernel serves a product.
+static PromptPlan linear_plan(int64_t ntok, int64_t m, int64_t n, int32_t G, int32_t xdtype) {
+  PromptPlan p{};
+  if (ntok > 64) p = prompt_plan(ntok, m, n, G, xdtype);
+  return p;
+}
+
+static void carve_linear(Carver& c, const PromptPlan& p, void** staged, void** partial) {
+  *staged = p.staged_bytes ? c.take(p.staged_bytes) : nullptr;
+  *partial = p.partial_bytes ? c.take(p.partial_bytes) : nullptr;
+}
+
 size_t pwq_packed_linear_workspace_size(int64_t ntok, int64_t m, int64_t n, int32_t group,
                                         int32_t xdtype) {
-  (void)ntok, (void)m, (void)n, (void)group, (void)xdtype;
-  return 0;
+  if (ntok < 0 || m < 0 || n <= 0 || ntok > INT32_MAX || m > INT32_MAX || n > INT32_MAX) return 0;
+  if (group < 0 || (group > 0 && n % group)) return 0;
+  Carver c(nullptr);
+  void *staged, *partial;
+  carve_linear(c, linear_plan(ntok, m, n, group > 0 ? group : (int32_t)n, xdtype), &staged,
+               &partial);
+  return c.size();
 }
 
 pwq_status pwq_packed_linear(const void* x, int32_t xdtype, int64_t ntok, int64_t ldx,
@@ -972,7 +989,12 @@ pwq_status pwq_packed_linear(const void* x, int32_t xdtype, int64_t ntok, int64_
   PackedLinearLaunch a{x, xdtype, ntok, ldx, x_scales, qweight, m, n, packed_row_bytes(n), scales,
                        zeros, group > 0 ? group : (int32_t)n, n_out > 0 ? outlier_off : nullptr,
                        outliers, n_out, y, ydtype, ldy};
-  const hipError_t e = launch_packed_linear(a, (hipStream_t)stream);
+  const PromptPlan p = linear_plan(ntok, m, n, a.G, xdtype);
+  Carver c(ws);
+  void *staged, *partial;
+  carve_linear(c, p, &staged, &partial);
+  const hipError_t e = p.ok ? launch_prompt(a, p, staged, partial, (hipStream_t)stream)
+                            : launch_linear_any(a, (hipStream_t)stream);
   if (e != hipSuccess) return hip_fail(e, "packed_linear launch");
   return ok();
 }

@@ -199,7 +199,19 @@ struct PackedLinearLaunch {
   int32_t ydtype;
   int64_t ldy;
 };
-hipError_t launch_packed_linear(const PackedLinearLaunch& a, hipStream_t st);
+// Any shape, one wave per row and few tokens.
+hipError_t launch_linear_any(const PackedLinearLaunch& a, hipStream_t st);
+// Many tokens: the plan depends on the sizes alone, its workspace is
+// staged_bytes + partial_bytes.
+struct PromptPlan {
+  bool ok, i8, big;
+  int mode, reps;
+  int64_t steps, per, splits, tiles_t, tiles_r, staged_row;
+  size_t staged_bytes, partial_bytes;
+};
+PromptPlan prompt_plan(int64_t ntok, int64_t m, int64_t n, int32_t G, int32_t xdtype);
+hipError_t launch_prompt(const PackedLinearLaunch& a, const PromptPlan& p, void* staged,
+                         void* partial, hipStream_t st);
 
 // Event pairs recorded around launches of one kernel (pwq_kernel_timer_attach).
 struct KernelTimer {

@@ -99,6 +99,21 @@ def test_packed_linear(shape, x_kind):
             check_linear(y, x, xs, codes, scales, zeros)
 
 
+@pytest.mark.parametrize("x_kind", ["bf16", "f32", "int8"])
+@pytest.mark.parametrize("n,group", [(320, 64), (200, 0), (384, 128), (416, 32)])
+def test_packed_linear_many_tiles(n, group, x_kind):
+    """Enough tokens and rows for the largest tile, ragged in both."""
+    rng = np.random.default_rng([n, group])
+    tokens, m = 2100, 5500
+    codes, scales, zeros = layer(rng, m, n, group, "asym" if n != 384 else "sym", 0.003)
+    pk = packed_layer(codes, scales, zeros, group)
+    x, xs = activations(rng, tokens, n, x_kind)
+    print(f"[serve] many tiles {n} {group} {x_kind}", flush=True)
+    y = P.packed_linear(x.cuda(), pk, x_scales=None if xs is None else xs.cuda(),
+                        out_dtype=torch.float32)
+    check_linear(y, x, xs, codes, scales, zeros)
+
+
 def test_packed_linear_no_tokens_and_no_rows():
     rng = np.random.default_rng(1)
     codes, scales, zeros = layer(rng, 20, 64, 32, "asym", 0.0)
