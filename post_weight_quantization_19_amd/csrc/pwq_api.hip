@@ -937,7 +937,7 @@ pwq_status pwq_rms_norm(const void* x, int32_t xdtype, int64_t ntok, int64_t n, 
 // Which kernel serves a product.
 static PromptPlan linear_plan(int64_t ntok, int64_t m, int64_t n, int32_t G, int32_t xdtype) {
   PromptPlan p{};
-  if (ntok > 64) p = prompt_plan(ntok, m, n, G, xdtype);
+  if (ntok > kRowsTokens) p = prompt_plan(ntok, m, n, G, xdtype);
   return p;
 }
 
@@ -993,8 +993,11 @@ pwq_status pwq_packed_linear(const void* x, int32_t xdtype, int64_t ntok, int64_
   Carver c(ws);
   void *staged, *partial;
   carve_linear(c, p, &staged, &partial);
-  const hipError_t e = p.ok ? launch_prompt(a, p, staged, partial, (hipStream_t)stream)
-                            : launch_linear_any(a, (hipStream_t)stream);
+  hipStream_t st = (hipStream_t)stream;
+  hipError_t e = hipSuccess;
+  if (ntok > 0 && m > 0)
+    e = p.ok ? launch_prompt(a, p, staged, partial, st)
+             : (rows_ok(ntok, n, a.G) ? launch_rows(a, st) : launch_linear_any(a, st));
   if (e != hipSuccess) return hip_fail(e, "packed_linear launch");
   return ok();
 }

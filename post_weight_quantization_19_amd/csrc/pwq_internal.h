@@ -201,6 +201,10 @@ struct PackedLinearLaunch {
 };
 // Any shape, one wave per row and few tokens.
 hipError_t launch_linear_any(const PackedLinearLaunch& a, hipStream_t st);
+// Few tokens, each weight read once.
+constexpr int64_t kRowsTokens = 64;
+bool rows_ok(int64_t ntok, int64_t n, int32_t G);
+hipError_t launch_rows(const PackedLinearLaunch& a, hipStream_t st);
 // Many tokens: the plan depends on the sizes alone, its workspace is
 // staged_bytes + partial_bytes.
 struct PromptPlan {
