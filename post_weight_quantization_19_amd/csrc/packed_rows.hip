@@ -138,8 +138,11 @@ __global__ __launch_bounds__(1024) void packed_rows(const PackedLinearLaunch a) 
   const int k0 = wave * per, k1 = min(across, k0 + per);
   const uint8_t* q = a.qweight + row * a.ldq;
   const float* sp = a.scales + row * ng;
-  const uint8_t* zp = a.zeros ? a.zeros + row * ng : nullptr;
-  const uint32_t flip = zp ? 0u : 0x88888888u;
+  // SYM: the zero point is 8 once the signs are flipped (what is read in its
+  // place, the row's steps, is not used)
+  const bool asym = a.zeros != nullptr;
+  const uint8_t* zp = asym ? a.zeros + row * ng : (const uint8_t*)sp;
+  const uint32_t flip = asym ? 0u : 0x88888888u;
   const T* xp[NT];
 #pragma unroll
   for (int i = 0; i < NT; ++i)
@@ -149,16 +152,24 @@ __global__ __launch_bounds__(1024) void packed_rows(const PackedLinearLaunch a) 
 #pragma unroll
   for (int i = 0; i < NT; ++i) acc[i] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
 
-  for (int kt = k0; kt < k1; kt += U) {
-    uint32_t w[U][NB][NW];
-    float s[U][NB];
-    int z[U][NB];
+  // group of the next block, kept without divisions
+  int g = 128 * k0 / G, in_g = 128 * k0 % G;
+
+  // `count` <= UU tiles from kt on.  Every load is issued before the first is
+  // used, without branches: tiles past `count` load the last one again.
+  auto tiles = [&](auto uu, auto ragged, int kt, int count) {
+    constexpr int UU = decltype(uu)::value;
+    constexpr bool RAGGED = decltype(ragged)::value;
+    uint32_t w[UU][NB][NW];
+    float s[UU][NB];
+    int z[UU][NB];
+    Cols<NC, T> x[UU][NB][NT];
 #pragma unroll
-    for (int u = 0; u < U; ++u)
+    for (int u = 0; u < UU; ++u)
 #pragma unroll
       for (int h = 0; h < NB; ++h) {
-        const int k = 128 * (kt + u) + GB * h + NC * lq;
-        const uint8_t* p = q + (k / 2 < a.ldq ? k / 2 : 0);
+        const int k = 128 * (kt + min(u, count - 1)) + GB * h + NC * lq;
+        const uint8_t* p = q + (!RAGGED || k / 2 < a.ldq ? k / 2 : 0);
         if constexpr (NW == 4) {
           const uint4 v = *(const uint4*)p;
           w[u][h][0] = v.x, w[u][h][1] = v.y, w[u][h][2] = v.z, w[u][h][3] = v.w;
@@ -168,22 +179,26 @@ __global__ __launch_bounds__(1024) void packed_rows(const PackedLinearLaunch a) 
         } else {
           w[u][h][0] = *(const uint32_t*)p;
         }
-        const int g = min((128 * (kt + u) + GB * h) / G, (int)ng - 1);
-        s[u][h] = sp[g];
-        z[u][h] = zp ? zp[g] : 8;
+        const int gi = min(g, (int)ng - 1);
+        s[u][h] = sp[gi];
+        z[u][h] = zp[gi];
+        in_g += GB;
+        const bool next = in_g >= G;
+        g += next, in_g -= next ? G : 0;
       }
-    Cols<NC, T> x[U][NB][NT];
 #pragma unroll
-    for (int u = 0; u < U; ++u)
+    for (int u = 0; u < UU; ++u)
 #pragma unroll
       for (int h = 0; h < NB; ++h) {
-        const int k = 128 * (kt + u) + GB * h + NC * lq;
+        const int k = 128 * (kt + min(u, count - 1)) + GB * h + NC * lq;
 #pragma unroll
-        for (int i = 0; i < NT; ++i) x[u][h][i] = load_cols<NC>(xp[i] + k, n - k);
+        for (int i = 0; i < NT; ++i)
+          x[u][h][i] = load_cols<NC>(xp[i] + k, RAGGED ? n - k : NC);
       }
+    asm volatile("" ::: "memory");             // the loads stay in front of the sums
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      if (kt + u >= k1) break;
+    for (int u = 0; u < UU; ++u) {
+      if (u >= count) break;
       int e0 = 0, e1 = 0;
       if constexpr (OVER) {
         const int64_t tile = strip * across + kt + u;
@@ -192,11 +207,12 @@ __global__ __launch_bounds__(1024) void packed_rows(const PackedLinearLaunch a) 
       }
 #pragma unroll
       for (int h = 0; h < NB; ++h) {
+        const int zi = asym ? z[u][h] : 8;
         acc_t c[NT];
 #pragma unroll
         for (int i = 0; i < NT; ++i) c[i] = acc_t{0, 0, 0, 0};
         if constexpr (XK == X_I8) {
-          const uint32_t z4 = (uint32_t)z[u][h] * 0x01010101u;
+          const uint32_t z4 = (uint32_t)zi * 0x01010101u;
 #pragma unroll
           for (int j = 0; j < NW; j += 2) {
             const uint2 lo = steps_i8(w[u][h][j] ^ flip, z4);
@@ -210,7 +226,7 @@ __global__ __launch_bounds__(1024) void packed_rows(const PackedLinearLaunch a) 
             }
           }
         } else {
-          const float zf = (float)z[u][h];
+          const float zf = (float)zi;
 #pragma unroll
           for (int j = 0; j < NW; ++j) {
             const bf16x8_t b = steps_bf16(w[u][h][j] ^ flip, zf);
@@ -263,6 +279,13 @@ __global__ __launch_bounds__(1024) void packed_rows(const PackedLinearLaunch a) 
           for (int e = 0; e < 4; ++e) acc[i][e] = fmaf(s[u][h], (float)c[i][e], acc[i][e]);
       }
     }
+  };
+  const int kf = max(k0, min(k1, n >> 7));     // the first tile that is not whole
+  for (int kt = k0; kt < kf; kt += U)
+    tiles(std::integral_constant<int, U>{}, std::false_type{}, kt, min(U, kf - kt));
+  if (kf < k1) {
+    g = 128 * kf / G, in_g = 128 * kf % G;
+    tiles(std::integral_constant<int, 1>{}, std::true_type{}, kf, 1);
   }
 
   // join the waves' sums in their order; lane l: tokens 4 (l / 16) + e, row l % 16
@@ -283,19 +306,29 @@ __global__ __launch_bounds__(1024) void packed_rows(const PackedLinearLaunch a) 
   }
 }
 
-template <int XK, int NT, int GB>
-void launch_nt(const PackedLinearLaunch& a, hipStream_t st) {
-  constexpr int U = XK == X_F32 || GB == 32 ? 1 : std::max(1, (GB == 128 ? 4 : 2) / NT);
-  const int64_t strips = (a.m + kPackRows - 1) / kPackRows, across = (a.n + 127) / 128;
-  // about 16 waves per CU over the whole launch
-  int waves = 1;
-  while (waves < 16 && strips * waves < 4096 && waves < across) waves *= 2;
-  const dim3 grid((unsigned)strips, (unsigned)((a.ntok + 16 * NT - 1) / (16 * NT)));
-  if constexpr (NT <= 2) if (a.outlier_off) {
+template <int XK, int NT, int GB, int U>
+void launch_u(const PackedLinearLaunch& a, int waves, hipStream_t st) {
+  const dim3 grid((unsigned)((a.m + kPackRows - 1) / kPackRows),
+                  (unsigned)((a.ntok + 16 * NT - 1) / (16 * NT)));
+  if constexpr (NT <= 2 && U == 1) if (a.outlier_off) {
     packed_rows<XK, NT, GB, 1, true><<<grid, 64 * waves, waves * NT * 1024, st>>>(a);
     return;
   }
   packed_rows<XK, NT, GB, U, false><<<grid, 64 * waves, waves * NT * 1024, st>>>(a);
+}
+
+template <int XK, int NT, int GB>
+void launch_nt(const PackedLinearLaunch& a, hipStream_t st) {
+  // tiles in flight that the registers hold
+  constexpr int MOST = XK == X_F32 || GB == 32 ? 1 : std::max(1, 4 / NT);
+  const int64_t strips = (a.m + kPackRows - 1) / kPackRows, across = (a.n + 127) / 128;
+  // about 16 waves per CU over the whole launch
+  int waves = 1;
+  while (waves < 16 && strips * waves < 4096 && waves < across) waves *= 2;
+  const int64_t per = (across + waves - 1) / waves;
+  if constexpr (MOST >= 4) if (per > 2 && !a.outlier_off) return launch_u<XK, NT, GB, 4>(a, waves, st);
+  if constexpr (MOST >= 2) if (per > 1 && !a.outlier_off) return launch_u<XK, NT, GB, 2>(a, waves, st);
+  launch_u<XK, NT, GB, 1>(a, waves, st);
 }
 
 template <int XK, int NT>
