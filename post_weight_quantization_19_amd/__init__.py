@@ -617,7 +617,7 @@ def packed_linear(x: torch.Tensor, packed: dict, x_scales: Optional[torch.Tensor
         raise ValueError(f"out must be [{ntok}, {m}] {odt}")
     L_ = lib()
     xdt = _DTYPES[x.dtype]
-    nb = L_.pwq_packed_linear_workspace_size(ntok, m, n, group, xdt)
+    nb = L_.pwq_packed_linear_workspace_size(x.data_ptr(), xdt, ntok, ldx, m, n, group)
     ws = _workspace(nb, x.device) if nb else None
     check(L_.pwq_packed_linear(x.data_ptr(), xdt, ntok, ldx, _ptr(x_scales), q.data_ptr(), m, n,
                                scales.data_ptr(), _ptr(zeros), group,

@@ -403,7 +403,8 @@ void launch_tiles(const PromptArgs& p, int mode, int splits, hipStream_t st) {
 
 // What prompt_tiles makes of a product: 8-bit or bf16 operands, steps, tile,
 // splits and workspace.
-PromptPlan prompt_plan(int64_t ntok, int64_t m, int64_t n, int32_t G, int32_t xdtype) {
+PromptPlan prompt_plan(const void* x, int32_t xdtype, int64_t ntok, int64_t ldx, int64_t m,
+                       int64_t n, int32_t G) {
   PromptPlan p{};
   const bool row = G == n;
   p.ok = (row || G % 32 == 0) && ntok > 0 && m > 0;
@@ -427,7 +428,11 @@ PromptPlan prompt_plan(int64_t ntok, int64_t m, int64_t n, int32_t G, int32_t xd
   p.per = (p.steps + p.splits - 1) / p.splits;
   p.splits = (p.steps + p.per - 1) / p.per;
   p.partial_bytes = p.splits > 1 ? (size_t)p.splits * ntok * m * 4 : 0;
-  p.staged_bytes = (size_t)ntok * p.staged_row;
+  // read in place: whole steps, aligned rows, and 256 of them within 32 bits
+  const int64_t es = xdtype == PWQ_I8 ? 1 : (xdtype == PWQ_BF16 ? 2 : 4), xrow = ldx * es;
+  p.direct = p.reps == 1 && (xdtype == PWQ_I8) == p.i8 && p.staged_row == n * es &&
+             xrow % 16 == 0 && (uintptr_t)x % 16 == 0 && xrow < (int64_t(1) << 23);
+  p.staged_bytes = p.direct ? 0 : (size_t)ntok * p.staged_row;
   return p;
 }
 
@@ -437,11 +442,7 @@ hipError_t launch_prompt(const PackedLinearLaunch& a, const PromptPlan& pl, void
   PromptArgs p{};
   const int64_t es = a.xdtype == PWQ_I8 ? 1 : (a.xdtype == PWQ_BF16 ? 2 : 4);
   const int64_t xrow = a.ldx * es;
-  const bool same = pl.reps == 1 && (a.xdtype == PWQ_I8) == pl.i8;
-  // read in place: whole steps, aligned rows, and 256 of them within 32 bits
-  const bool direct = same && pl.staged_row == a.n * es && xrow % 16 == 0 &&
-                      (uintptr_t)a.x % 16 == 0 && xrow < (int64_t(1) << 23);
-  if (direct) {
+  if (pl.direct) {
     p.x = (const char*)a.x;
     p.xrow = xrow;
   } else {

@@ -1,14 +1,21 @@
-// y = x W^^T of a packed layer for few tokens (up to 64): every weight is
-// read once, spread in registers, and multiplied on the matrix cores.
+// y = x W^^T of a packed layer for up to 16 tokens: every weight is read once,
+// spread in registers, and multiplied on the matrix cores.
 //
 // A workgroup owns a strip of 16 rows; its waves split the columns in tiles of
-// 128 and their partial sums are joined in LDS in wave order.  In a tile the
-// operands are x (16 tokens) and the integer steps c - z of 16 rows: lane l
-// holds token l % 16 and row l % 16, and the GB / 4 columns GB h +
-// (GB / 4)(l / 16) .. of block h, GB <= G, so that the four lane groups of a
-// matrix instruction stay within one group of the steps.  The sum of a block
-// (int32 for 8-bit x, float32 for exact products of bf16 otherwise) is
-// multiplied by the step of the lane's row and added in float32.
+// 128 and their partial sums are joined in LDS in wave order.  A wave copies
+// its tiles (16 rows x 64 bytes of weights, and the tokens' x) to LDS of its
+// own by asynchronous copies, `depth` tiles ahead: lanes next to each other
+// read bytes next to each other, which the operand layout of the matrix
+// instructions does not.  (Loads straight into that layout cost a cache lookup
+// per lane and bound the kernel at 2 to 3 times its time: 16 us for up_proj's
+// 29 MB and one 8-bit token.)
+//
+// Operands: x (16 tokens) and the codes of 16 rows.  Lane l holds token l % 16
+// and row l % 16, and of block h of GB columns, GB <= G, the GB / 4 from
+// GB h + (GB / 4)(l / 16) on, so that a matrix instruction stays within one
+// group of the steps.  The sum of a block (int32 for 8-bit x, float32 for
+// exact products of bf16 otherwise) is multiplied by the step of the lane's
+// row and added in float32.
 //
 // Codes beyond 4 bits enter as further columns: up to 32 (64 for 8-bit x)
 // entries of a tile at a time, x gathered at their columns, the entry's value
@@ -21,8 +28,8 @@ namespace pwq {
 namespace {
 
 typedef __attribute__((__vector_size__(4 * sizeof(int)))) int i32x4_t;
-struct __attribute__((packed, aligned(1))) vec16 { uint4 v; };
-struct __attribute__((packed, aligned(1))) vec8 { uint2 v; };
+typedef __attribute__((address_space(3))) char lds_char;
+struct __attribute__((packed, aligned(4))) vec16f { float v[4]; };
 
 enum { X_BF16 = 0, X_I8 = 1, X_F32 = 2, X_I8_BF16 = 3 };
 template <int XK> struct XType { using T = uint16_t; };
@@ -30,334 +37,419 @@ template <> struct XType<X_I8> { using T = int8_t; };
 template <> struct XType<X_I8_BF16> { using T = int8_t; };
 template <> struct XType<X_F32> { using T = float; };
 
-template <int N, typename T>
-struct Cols { T v[N]; };
+// Asynchronous copy of 16 bytes per active lane, sbase + voff of each lane to
+// lds + 16 lane (lds and sbase wave-uniform).  M0 is restored.
+__device__ __forceinline__ void copy16(uint32_t voff, const void* sbase, uint32_t lds) {
+  uint32_t keep;
+  asm volatile(
+      "s_mov_b32 %0, m0\n\t"
+      "s_mov_b32 m0, %3\n\t"
+      "global_load_lds_dwordx4 %1, %2\n\t"
+      "s_mov_b32 m0, %0"
+      : "=&s"(keep)
+      : "v"(voff), "s"(sbase), "s"(lds)
+      : "memory");
+}
 
-// N consecutive elements (any alignment); those at or past `left` are 0.
-template <int N, typename T>
-__device__ __forceinline__ Cols<N, T> load_cols(const T* p, int left) {
-  Cols<N, T> c;
-  if (left >= N) {
-    constexpr int B = N * sizeof(T);
-    if constexpr (B % 16 == 0) {
-#pragma unroll
-      for (int i = 0; i < B / 16; ++i) {
-        const uint4 u = ((const vec16*)p)[i].v;
-        __builtin_memcpy((char*)&c + 16 * i, &u, 16);
-      }
-    } else {
-      static_assert(B == 8);
-      const uint2 u = ((const vec8*)p)->v;
-      __builtin_memcpy(&c, &u, 8);
-    }
-  } else {
-#pragma unroll
-    for (int e = 0; e < N; ++e) c.v[e] = e < left ? p[e] : T(0);
+// Waits until at most n of this wave's copies are in flight (n wave-uniform).
+__device__ __forceinline__ void wait_copies(int n) {
+  switch (n) {
+#define PWQ_WC(N) \
+    case N: asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory"); break;
+    PWQ_WC(1) PWQ_WC(2) PWQ_WC(3) PWQ_WC(4) PWQ_WC(5) PWQ_WC(6) PWQ_WC(7) PWQ_WC(8) PWQ_WC(9)
+    PWQ_WC(10) PWQ_WC(12) PWQ_WC(15) PWQ_WC(18)
+#undef PWQ_WC
+    default: asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); break;
   }
-  return c;
 }
 
 __device__ __forceinline__ uint32_t pack_hi(float a, float b) {   // exact for small integers
   return __builtin_amdgcn_perm(__float_as_uint(b), __float_as_uint(a), 0x07060302u);
 }
 
-// Eight 4-bit steps of a dword (codes 0 .. 15) minus z, to bf16 or bytes.
-__device__ __forceinline__ bf16x8_t steps_bf16(uint32_t w, float z) {
-  const uint32_t even = w & 0x0f0f0f0fu, odd = (w >> 4) & 0x0f0f0f0fu;
-  uint4 o;
-  uint32_t* q = (uint32_t*)&o;
-#pragma unroll
-  for (int i = 0; i < 4; ++i)
-    q[i] = pack_hi((float)((even >> (8 * i)) & 0xffu) - z, (float)((odd >> (8 * i)) & 0xffu) - z);
+// Eight 4-bit codes of a dword to bf16 16 + u, u = 0 .. 15 (`bias` 0x4180 per
+// half, or 0x41c0 for signed halves, whose top bit it flips): the code lands
+// in the top four of seven mantissa bits.  Order: columns 0 4 1 5 2 6 3 7.
+__device__ __forceinline__ bf16x8_t codes_bf16(uint32_t w, uint32_t bias) {
+  constexpr uint32_t M = 0x00780078u;
+  const uint4 o = make_uint4(((w << 3) & M) ^ bias, ((w >> 1) & M) ^ bias, ((w >> 5) & M) ^ bias,
+                             ((w >> 9) & M) ^ bias);
   return __builtin_bit_cast(bf16x8_t, o);
 }
+// Eight 4-bit codes to bytes.  Unsigned: u - z (every byte is at least 128
+// before the subtraction, so no borrow passes one).  Signed: 16 times the
+// code, its four bits at the top of the byte.
 __device__ __forceinline__ uint2 steps_i8(uint32_t w, uint32_t z4) {
   const uint32_t even = (((w & 0x0f0f0f0fu) | 0x80808080u) - z4) ^ 0x80808080u;
   const uint32_t odd = ((((w >> 4) & 0x0f0f0f0fu) | 0x80808080u) - z4) ^ 0x80808080u;
   return make_uint2(__builtin_amdgcn_perm(odd, even, 0x05010400u),
                     __builtin_amdgcn_perm(odd, even, 0x07030602u));
 }
-
-// Part `part` (0, 1, 2) of eight float32 in bf16, truncated: exact, and the
-// remainders are left in v.
-__device__ __forceinline__ bf16x8_t f32_part(float* v) {
-  uint4 o;
-  uint32_t* q = (uint32_t*)&o;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    q[i] = pack_hi(v[2 * i], v[2 * i + 1]);
-    v[2 * i] -= __uint_as_float(__float_as_uint(v[2 * i]) & 0xffff0000u);
-    v[2 * i + 1] -= __uint_as_float(__float_as_uint(v[2 * i + 1]) & 0xffff0000u);
-  }
-  return __builtin_bit_cast(bf16x8_t, o);
+__device__ __forceinline__ uint2 signed16_i8(uint32_t w) {
+  const uint32_t even = (w << 4) & 0xf0f0f0f0u, odd = w & 0xf0f0f0f0u;
+  return make_uint2(__builtin_amdgcn_perm(odd, even, 0x05010400u),
+                    __builtin_amdgcn_perm(odd, even, 0x07030602u));
 }
 
 __device__ __forceinline__ f32x4_t mma(bf16x8_t x, bf16x8_t w, f32x4_t c) {
   return __builtin_amdgcn_mfma_f32_16x16x32_bf16(x, w, c, 0, 0, 0);
 }
 
-// Eight columns of x (from `p`, its own type) against eight bf16 steps.
-template <int XK>
-__device__ __forceinline__ f32x4_t mma_x(const typename XType<XK>::T* p, bf16x8_t w, f32x4_t c) {
-  if constexpr (XK == X_F32) {
+// Eight columns of x as bf16 operands, in the order of codes_bf16 (PAIRED) or
+// their own; float32 x as three bf16 parts that add up to it: the top, middle
+// and last 8 bits of the significand (truncated: exact, and no overflow).
+template <int XK> constexpr int kParts = XK == X_F32 ? 3 : 1;
+template <int XK, bool PAIRED>
+__device__ __forceinline__ void x_parts(const typename XType<XK>::T* p,
+                                        bf16x8_t (&out)[kParts<XK>]) {
+  uint4 o;
+  uint32_t* q = (uint32_t*)&o;
+  if constexpr (XK == X_BF16) {
+    __builtin_memcpy(&o, p, 16);
+    if constexpr (PAIRED)
+      o = make_uint4(__builtin_amdgcn_perm(o.z, o.x, 0x05040100u),
+                     __builtin_amdgcn_perm(o.z, o.x, 0x07060302u),
+                     __builtin_amdgcn_perm(o.w, o.y, 0x05040100u),
+                     __builtin_amdgcn_perm(o.w, o.y, 0x07060302u));
+    out[0] = __builtin_bit_cast(bf16x8_t, o);
+  } else {
     float v[8];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) v[e] = p[e];
+    for (int e = 0; e < 8; ++e) v[e] = (float)p[e];
 #pragma unroll
-    for (int part = 0; part < 3; ++part) c = mma(f32_part(v), w, c);
-    return c;
-  } else if constexpr (XK == X_BF16) {
-    bf16x8_t x;
-    __builtin_memcpy(&x, p, 16);
-    return mma(x, w, c);
-  } else {
-    uint4 o;
-    uint32_t* q = (uint32_t*)&o;
+    for (int part = 0; part < kParts<XK>; ++part) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) q[i] = pack_hi((float)p[2 * i], (float)p[2 * i + 1]);
-    return mma(__builtin_bit_cast(bf16x8_t, o), w, c);
+      for (int i = 0; i < 4; ++i) {
+        float& lo = v[PAIRED ? i : 2 * i];
+        float& hi = v[PAIRED ? i + 4 : 2 * i + 1];
+        q[i] = pack_hi(lo, hi);
+        if (part + 1 < kParts<XK>) {
+          lo -= __uint_as_float(__float_as_uint(lo) & 0xffff0000u);
+          hi -= __uint_as_float(__float_as_uint(hi) & 0xffff0000u);
+        }
+      }
+      out[part] = __builtin_bit_cast(bf16x8_t, o);
+    }
   }
 }
 
-// NT blocks of 16 tokens from 16 NT blockIdx.y on; GB columns per block; U
-// tiles loaded at a time; OVER: with overflow entries.
-template <int XK, int NT, int GB, int U, bool OVER>
+// LDS of a wave: `depth` slots of a tile (weights 1 KB, x), the steps and zero
+// points of 16 rows x 16 groups, overflow entries.
+constexpr int kStepRow = 17;                         // 16 groups, off the bank stride
+constexpr int kSteps = 16 * kStepRow * 4;            // bytes of the steps; as many zero points
+constexpr int kEntries = 256;
+constexpr int wave_bytes(int depth, int xbytes, bool over) {
+  return depth * (1024 + xbytes) + 2 * kSteps + (over ? 4 * kEntries : 0);
+}
+
+template <int XK, int GB, bool OVER>
 __global__ __launch_bounds__(1024) void packed_rows(const PackedLinearLaunch a) {
   using T = typename XType<XK>::T;
   using acc_t = std::conditional_t<XK == X_I8, i32x4_t, f32x4_t>;
+  constexpr int ES = sizeof(T);
   constexpr int NB = 128 / GB, NC = GB / 4;     // blocks of a tile, columns of a lane in one
   constexpr int NW = NC / 8;                    // dwords of a lane per block
-  extern __shared__ float joined[];             // [wave][NT][4][64]
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, waves = blockDim.x >> 6;
+  constexpr int XROW = 128 * ES, UNITS = XROW / 16, RPC = 64 / UNITS;   // x rows per copy
+  constexpr int CH = 16 / NB;                   // tiles of a chunk: at most 16 groups
+  extern __shared__ __attribute__((aligned(16))) char smem[];
+  const int lane = threadIdx.x & 63, waves = blockDim.x >> 6;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int lr = lane & 15, lq = lane >> 4;
-  const int64_t strip = blockIdx.x, t0 = (int64_t)blockIdx.y * 16 * NT;
-  const int64_t row = min(strip * kPackRows + lr, a.m - 1);
-  const int64_t ng = a.n / a.G;
-  const int n = (int)a.n, G = a.G;
-  const int across = (n + 127) >> 7, per = (across + waves - 1) / waves;
+  const int64_t strip = blockIdx.x;
+  const int tok = (int)a.ntok, n = (int)a.n, G = a.G, ng = n / G, ldq = (int)a.ldq;
+  const int xcols = (int)a.xcols;
+  const int across = (n + 127) >> 7, per = a.per, depth = a.depth;
   const int k0 = wave * per, k1 = min(across, k0 + per);
-  const uint8_t* q = a.qweight + row * a.ldq;
-  const float* sp = a.scales + row * ng;
-  // SYM: the zero point is 8 once the signs are flipped (what is read in its
-  // place, the row's steps, is not used)
+  const int rows = (int)min(a.m - strip * kPackRows, (int64_t)kPackRows);
   const bool asym = a.zeros != nullptr;
-  const uint8_t* zp = asym ? a.zeros + row * ng : (const uint8_t*)sp;
-  const uint32_t flip = asym ? 0u : 0x88888888u;
-  const T* xp[NT];
-#pragma unroll
-  for (int i = 0; i < NT; ++i)
-    xp[i] = (const T*)a.x + min(t0 + 16 * i + lr, a.ntok - 1) * a.ldx;
+  const int xbytes = (tok + RPC - 1) / RPC * 1024, slot_bytes = 1024 + xbytes;
+  const int own = wave * wave_bytes(depth, xbytes, OVER);
+  char* const L = smem + own;
+  const uint32_t lbase = (uint32_t)(uintptr_t)(lds_char*)smem + own;
+  float* const steps = (float*)(L + depth * slot_bytes);
+  float* const zs = steps + 16 * kStepRow;
+  int* const ents = (int*)(zs + 16 * kStepRow);
 
-  f32x4_t acc[NT];
-#pragma unroll
-  for (int i = 0; i < NT; ++i) acc[i] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
-
-  // group of the next block, kept without divisions
-  int g = 128 * k0 / G, in_g = 128 * k0 % G;
-
-  // `count` <= UU tiles from kt on.  Every load is issued before the first is
-  // used, without branches: tiles past `count` load the last one again.
-  auto tiles = [&](auto uu, auto ragged, int kt, int count) {
-    constexpr int UU = decltype(uu)::value;
-    constexpr bool RAGGED = decltype(ragged)::value;
-    uint32_t w[UU][NB][NW];
-    float s[UU][NB];
-    int z[UU][NB];
-    Cols<NC, T> x[UU][NB][NT];
-#pragma unroll
-    for (int u = 0; u < UU; ++u)
-#pragma unroll
-      for (int h = 0; h < NB; ++h) {
-        const int k = 128 * (kt + min(u, count - 1)) + GB * h + NC * lq;
-        const uint8_t* p = q + (!RAGGED || k / 2 < a.ldq ? k / 2 : 0);
-        if constexpr (NW == 4) {
-          const uint4 v = *(const uint4*)p;
-          w[u][h][0] = v.x, w[u][h][1] = v.y, w[u][h][2] = v.z, w[u][h][3] = v.w;
-        } else if constexpr (NW == 2) {
-          const uint2 v = *(const uint2*)p;
-          w[u][h][0] = v.x, w[u][h][1] = v.y;
-        } else {
-          w[u][h][0] = *(const uint32_t*)p;
-        }
-        const int gi = min(g, (int)ng - 1);
-        s[u][h] = sp[gi];
-        z[u][h] = zp[gi];
-        in_g += GB;
-        const bool next = in_g >= G;
-        g += next, in_g -= next ? G : 0;
+  // copies: lane -> 16-byte unit.  Units of a row are permuted by the row so
+  // that the operand reads below spread over the banks.
+  const int wr = lane >> 2, wc = (lane & 3) ^ (wr >> 2);
+  const uint32_t woff = (uint32_t)(min(wr, rows - 1) * ldq + 16 * wc);
+  const uint8_t* const wbase = a.qweight + strip * kPackRows * a.ldq;
+  const int xr = lane / UNITS;
+  const uint32_t ldxb = (uint32_t)(a.ldx * ES);
+  auto swz = [](int t) { return ES == 1 ? (t >> 1) & 7 : t & 15; };
+  const int copies = 1 + (tok + RPC - 1) / RPC;
+  auto copy_tile = [&](int kt, int slot) {
+    const uint32_t dst = lbase + (uint32_t)(slot * slot_bytes);
+    const int wo = 64 * kt;
+    copy16(woff + (wo + 16 * wc < ldq ? (uint32_t)wo : 0u - 16u * wc), wbase, dst);
+    for (int j = 0; j * RPC < tok; ++j) {
+      const int t = j * RPC + xr, c = (lane % UNITS) ^ swz(t);
+      if (t < tok) {
+        if (kt * XROW + 16 * c < xcols * ES)
+          copy16(t * ldxb + 16u * c, (const char*)a.x + (int64_t)kt * XROW,
+                 dst + 1024u + 1024u * j);
+        else                                          // past the row: zeros
+          *(uint4*)(L + slot * slot_bytes + 1024 + 1024 * j + 16 * lane) = make_uint4(0, 0, 0, 0);
       }
+    }
+  };
+  const int tr = min(lr, tok - 1);                    // the lane's x row
+  auto x_unit = [&](const char* xs, int c) { return xs + tr * XROW + ((c ^ swz(tr)) << 4); };
+
+  f32x4_t acc = {0.0f, 0.0f, 0.0f, 0.0f};
+
+  // chunks of tiles whose steps fit LDS (one, unless a wave has many tiles)
+  for (int c0 = k0; c0 < k1; c0 += CH) {
+    const int c1 = min(k1, c0 + CH);
+    const int g0 = 128 * c0 / G;
+    float sv[4];
+    int zv[4] = {0, 0, 0, 0};
+    {
+      // lane: row lane / 4, groups g0 + 4 (lane % 4) ..
+      const int64_t r = (strip * kPackRows + min(wr, rows - 1)) * (int64_t)ng;
+      const int gl = g0 + 4 * (lane & 3);
+      if (g0 + 16 <= ng) {
+        const vec16f v = *(const vec16f*)(a.scales + r + gl);
 #pragma unroll
-    for (int u = 0; u < UU; ++u)
+        for (int i = 0; i < 4; ++i) sv[i] = v.v[i];
+      } else {
 #pragma unroll
-      for (int h = 0; h < NB; ++h) {
-        const int k = 128 * (kt + min(u, count - 1)) + GB * h + NC * lq;
-#pragma unroll
-        for (int i = 0; i < NT; ++i)
-          x[u][h][i] = load_cols<NC>(xp[i] + k, RAGGED ? n - k : NC);
+        for (int i = 0; i < 4; ++i) sv[i] = a.scales[r + min(gl + i, ng - 1)];
       }
-    asm volatile("" ::: "memory");             // the loads stay in front of the sums
+      if (asym)
 #pragma unroll
-    for (int u = 0; u < UU; ++u) {
-      if (u >= count) break;
+        for (int i = 0; i < 4; ++i) zv[i] = a.zeros[r + min(gl + i, ng - 1)];
+    }
+    int off = 0;
+    if constexpr (OVER)
+      off = max(a.outlier_off[strip * across + min(c0 + lane, c1)], 0);
+    for (int d = 0; d < depth && c0 + d < c1; ++d) copy_tile(c0 + d, d);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int at = wr * kStepRow + 4 * (lane & 3) + i;
+      steps[at] = XK == X_I8 && !asym ? 0.0625f * sv[i] : sv[i];
+      zs[at] = XK == X_I8 ? __int_as_float(zv[i]) : -(asym ? 16.0f + (float)zv[i] : 24.0f);
+    }
+    int ebase = 0;
+    if constexpr (OVER) {
+      ebase = __builtin_amdgcn_readlane(off, 0);
+      const int last = (int)min((int64_t)__builtin_amdgcn_readlane(off, c1 - c0), a.n_out);
+#pragma unroll
+      for (int i = 0; i < kEntries / 64; ++i)
+        if (ebase + 64 * i + lane < last) ents[64 * i + lane] = a.outliers[ebase + 64 * i + lane];
+    }
+    // group of the next block, without divisions
+    int g = 0, in_g = 128 * c0 - g0 * G;
+    int slot = 0;
+    for (int kt = c0; kt < c1; ++kt) {
+      wait_copies(copies * (min(c1, kt + depth) - kt - 1));
+      const char* ws = L + slot * slot_bytes;
+      const char* xs = ws + 1024;
       int e0 = 0, e1 = 0;
       if constexpr (OVER) {
-        const int64_t tile = strip * across + kt + u;
-        e0 = max(a.outlier_off[tile], 0);
-        e1 = (int)min((int64_t)a.outlier_off[tile + 1], a.n_out);
+        e0 = __builtin_amdgcn_readlane(off, kt - c0);
+        e1 = (int)min((int64_t)__builtin_amdgcn_readlane(off, kt - c0 + 1), a.n_out);
       }
 #pragma unroll
       for (int h = 0; h < NB; ++h) {
-        const int zi = asym ? z[u][h] : 8;
-        acc_t c[NT];
-#pragma unroll
-        for (int i = 0; i < NT; ++i) c[i] = acc_t{0, 0, 0, 0};
+        const float s = steps[lr * kStepRow + g];
+        const float zf = zs[lr * kStepRow + g];
+        in_g += GB;
+        if (in_g >= G) in_g -= G, ++g;
+        uint32_t w[NW];
+        {
+          const int o = (GB * h + NC * lq) / 2;
+          __builtin_memcpy(w, ws + lr * 64 + (((o >> 4) ^ (lr >> 2)) << 4) + (o & 15), 4 * NW);
+        }
+        acc_t c = {0, 0, 0, 0}, c1s = {0, 0, 0, 0};   // sums of the codes' terms, of x alone
         if constexpr (XK == X_I8) {
-          const uint32_t z4 = (uint32_t)zi * 0x01010101u;
+          const uint32_t z4 = __float_as_uint(zf) * 0x01010101u;
 #pragma unroll
           for (int j = 0; j < NW; j += 2) {
-            const uint2 lo = steps_i8(w[u][h][j] ^ flip, z4);
-            const uint2 hi = steps_i8(w[u][h][j + 1] ^ flip, z4);
-            const i32x4_t b = {(int)lo.x, (int)lo.y, (int)hi.x, (int)hi.y};
-#pragma unroll
-            for (int i = 0; i < NT; ++i) {
-              i32x4_t v;
-              __builtin_memcpy(&v, x[u][h][i].v + 8 * j, 16);
-              c[i] = __builtin_amdgcn_mfma_i32_16x16x64_i8(v, b, c[i], 0, 0, 0);
-            }
+            uint2 lo, hi;
+            if (asym) lo = steps_i8(w[j], z4), hi = steps_i8(w[j + 1], z4);
+            else lo = signed16_i8(w[j]), hi = signed16_i8(w[j + 1]);
+            const i32x4_t f = {(int)lo.x, (int)lo.y, (int)hi.x, (int)hi.y};
+            const i32x4_t v = *(const i32x4_t*)x_unit(xs, (GB * h + NC * lq + 8 * j) / 16);
+            c = __builtin_amdgcn_mfma_i32_16x16x64_i8(v, f, c, 0, 0, 0);
           }
         } else {
-          const float zf = (float)zi;
+          constexpr uint32_t kOne = 0x3f803f80u;
+          const bf16x8_t ones = __builtin_bit_cast(bf16x8_t, make_uint4(kOne, kOne, kOne, kOne));
+          const uint32_t bias = asym ? 0x41804180u : 0x41c041c0u;
 #pragma unroll
           for (int j = 0; j < NW; ++j) {
-            const bf16x8_t b = steps_bf16(w[u][h][j] ^ flip, zf);
+            const bf16x8_t f = codes_bf16(w[j], bias);
+            const int col = GB * h + NC * lq + 8 * j;
+            T xv[8];
+            if constexpr (XK == X_BF16) {
+              __builtin_memcpy(xv, x_unit(xs, col / 8), 16);
+            } else if constexpr (XK == X_F32) {
+              __builtin_memcpy(xv, x_unit(xs, col / 4), 16);
+              __builtin_memcpy(xv + 4, x_unit(xs, col / 4 + 1), 16);
+            } else {
+              __builtin_memcpy(xv, x_unit(xs, col / 16) + col % 16, 8);
+            }
+            bf16x8_t v[kParts<XK>];
+            x_parts<XK, true>(xv, v);
 #pragma unroll
-            for (int i = 0; i < NT; ++i) c[i] = mma_x<XK>(x[u][h][i].v + 8 * j, b, c[i]);
+            for (int part = 0; part < kParts<XK>; ++part) {
+              c = mma(v[part], f, c);
+              c1s = mma(v[part], ones, c1s);
+            }
           }
         }
+        acc_t ce = {0, 0, 0, 0};
         constexpr int PE = XK == X_I8 ? 16 : 8;          // entries of a lane at a time
         if constexpr (OVER) for (int e = e0; e < e1; e += 4 * PE) {
           int ent[PE];
+          T xe[PE];
 #pragma unroll
           for (int i = 0; i < PE; ++i) {
             const int at = e + PE * lq + i;
-            ent[i] = at < e1 ? a.outliers[at] : 0;       // 0: value 0 at column 0
-            if ((ent[i] & 127) / GB != h) ent[i] = 0;    // another block's
-            if (128 * (kt + u) + (ent[i] & 127) >= n) ent[i] = 0;
+            const uint32_t in = (uint32_t)(at - ebase);
+            ent[i] = at >= e1 ? 0 : (in < kEntries ? ents[in] : a.outliers[at]);
+            if ((ent[i] & 127) / GB != h) ent[i] = 0;    // another block's: value 0
+            const int col = ent[i] & 127;                // (columns past n hold zeros)
+            xe[i] = *(const T*)(x_unit(xs, col * ES / 16) + col * ES % 16);
           }
-          Cols<PE, T> xe[NT];
-#pragma unroll
-          for (int t = 0; t < NT; ++t)
-#pragma unroll
-            for (int i = 0; i < PE; ++i)
-              xe[t].v[i] = ent[i] ? xp[t][128 * (kt + u) + (ent[i] & 127)] : T(0);
           if constexpr (XK == X_I8) {
-            i32x4_t b = {0, 0, 0, 0};
+            i32x4_t f = {0, 0, 0, 0};
 #pragma unroll
             for (int i = 0; i < PE; ++i)
-              if (((ent[i] >> 7) & 15) == lr) b[i / 4] |= ((ent[i] >> 16) & 255) << (8 * (i % 4));
-#pragma unroll
-            for (int t = 0; t < NT; ++t) {
-              i32x4_t v;
-              __builtin_memcpy(&v, xe[t].v, 16);
-              c[t] = __builtin_amdgcn_mfma_i32_16x16x64_i8(v, b, c[t], 0, 0, 0);
-            }
+              if (((ent[i] >> 7) & 15) == lr) f[i / 4] |= ((ent[i] >> 16) & 255) << (8 * (i % 4));
+            i32x4_t v;
+            __builtin_memcpy(&v, xe, 16);
+            ce = __builtin_amdgcn_mfma_i32_16x16x64_i8(v, f, ce, 0, 0, 0);
           } else {
             float d[PE];
 #pragma unroll
             for (int i = 0; i < PE; ++i)
               d[i] = ((ent[i] >> 7) & 15) == lr ? (float)(ent[i] >> 16) : 0.0f;
-            uint4 o = make_uint4(pack_hi(d[0], d[1]), pack_hi(d[2], d[3]), pack_hi(d[4], d[5]),
-                                 pack_hi(d[6], d[7]));
+            const uint4 o = make_uint4(pack_hi(d[0], d[1]), pack_hi(d[2], d[3]),
+                                       pack_hi(d[4], d[5]), pack_hi(d[6], d[7]));
+            bf16x8_t v[kParts<XK>];
+            x_parts<XK, false>(xe, v);
 #pragma unroll
-            for (int t = 0; t < NT; ++t)
-              c[t] = mma_x<XK>(xe[t].v, __builtin_bit_cast(bf16x8_t, o), c[t]);
+            for (int part = 0; part < kParts<XK>; ++part)
+              ce = mma(v[part], __builtin_bit_cast(bf16x8_t, o), ce);
           }
         }
 #pragma unroll
-        for (int i = 0; i < NT; ++i)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) acc[i][e] = fmaf(s[u][h], (float)c[i][e], acc[i][e]);
+        for (int e = 0; e < 4; ++e) {
+          if constexpr (XK == X_I8) {
+            int v = c[e];
+            if constexpr (OVER) v += asym ? ce[e] : 16 * ce[e];
+            acc[e] = fmaf(s, (float)v, acc[e]);
+          } else {
+            float v = fmaf(zf, c1s[e], c[e]);
+            if constexpr (OVER) v += ce[e];
+            acc[e] = fmaf(s, v, acc[e]);
+          }
+        }
       }
+      if (kt + depth < c1) {
+        // the slot's reads are done before it is filled again
+        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+        copy_tile(kt + depth, slot);
+      }
+      if (++slot == depth) slot = 0;
     }
-  };
-  const int kf = max(k0, min(k1, n >> 7));     // the first tile that is not whole
-  for (int kt = k0; kt < kf; kt += U)
-    tiles(std::integral_constant<int, U>{}, std::false_type{}, kt, min(U, kf - kt));
-  if (kf < k1) {
-    g = 128 * kf / G, in_g = 128 * kf % G;
-    tiles(std::integral_constant<int, 1>{}, std::true_type{}, kf, 1);
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
   }
 
   // join the waves' sums in their order; lane l: tokens 4 (l / 16) + e, row l % 16
+  float* const joined = (float*)smem;
+  const int stride = wave_bytes(depth, xbytes, OVER) / 4;
 #pragma unroll
-  for (int i = 0; i < NT; ++i)
-#pragma unroll
-    for (int e = 0; e < 4; ++e) joined[((wave * NT + i) * 4 + e) * 64 + lane] = acc[i][e];
+  for (int e = 0; e < 4; ++e) joined[wave * stride + e * 64 + lane] = acc[e];
   __syncthreads();
-  for (int v = threadIdx.x; v < NT * 256; v += blockDim.x) {
-    const int i = v >> 8, e = (v >> 6) & 3, l = v & 63;
-    const int64_t t = t0 + 16 * i + 4 * (l >> 4) + e, r = strip * kPackRows + (l & 15);
-    if (t >= a.ntok || r >= a.m) continue;
+  for (int v = threadIdx.x; v < 256; v += blockDim.x) {
+    const int e = v >> 6, l = v & 63;
+    const int64_t t = 4 * (l >> 4) + e, r = strip * kPackRows + (l & 15);
+    if (t >= tok || r >= a.m) continue;
     float sum = joined[v];
-    for (int o = 1; o < waves; ++o) sum += joined[o * NT * 256 + v];
+    for (int o = 1; o < waves; ++o) sum += joined[o * stride + v];
     if (a.x_scales) sum *= a.x_scales[t];
     if (a.ydtype == PWQ_F32) ((float*)a.y)[t * a.ldy + r] = sum;
     else ((__bf16*)a.y)[t * a.ldy + r] = (__bf16)sum;
   }
 }
 
-template <int XK, int NT, int GB, int U>
-void launch_u(const PackedLinearLaunch& a, int waves, hipStream_t st) {
-  const dim3 grid((unsigned)((a.m + kPackRows - 1) / kPackRows),
-                  (unsigned)((a.ntok + 16 * NT - 1) / (16 * NT)));
-  if constexpr (NT <= 2 && U == 1) if (a.outlier_off) {
-    packed_rows<XK, NT, GB, 1, true><<<grid, 64 * waves, waves * NT * 1024, st>>>(a);
-    return;
-  }
-  packed_rows<XK, NT, GB, U, false><<<grid, 64 * waves, waves * NT * 1024, st>>>(a);
+// x to rows of `wide` columns, zeros past n.
+template <typename T>
+__global__ __launch_bounds__(256) void pad_rows(const T* __restrict__ x, int64_t ntok, int64_t n,
+                                                int64_t ldx, T* __restrict__ out, int64_t wide) {
+  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  if (i >= ntok * wide) return;
+  const int64_t t = i / wide, k = i % wide;
+  out[i] = k < n ? x[t * ldx + k] : T(0);
 }
 
-template <int XK, int NT, int GB>
-void launch_nt(const PackedLinearLaunch& a, hipStream_t st) {
-  // tiles in flight that the registers hold
-  constexpr int MOST = XK == X_F32 || GB == 32 ? 1 : std::max(1, 4 / NT);
-  const int64_t strips = (a.m + kPackRows - 1) / kPackRows, across = (a.n + 127) / 128;
+constexpr int kLdsBytes = 160 * 1024;
+
+template <int XK, int GB, bool OVER>
+void launch_gb(PackedLinearLaunch a, hipStream_t st) {
+  constexpr int ES = sizeof(typename XType<XK>::T), RPC = 64 / (128 * ES / 16);
+  const int xbytes = (int)(a.ntok + RPC - 1) / RPC * 1024;
+  // tiles ahead: what 16 waves of a CU have LDS for, 2 to 4
+  a.depth = 4;
+  while (a.depth > 2 && 16 * wave_bytes(a.depth, xbytes, OVER) > kLdsBytes) --a.depth;
+  const int bytes = wave_bytes(a.depth, xbytes, OVER);
   // about 16 waves per CU over the whole launch
-  int waves = 1;
-  while (waves < 16 && strips * waves < 4096 && waves < across) waves *= 2;
-  const int64_t per = (across + waves - 1) / waves;
-  if constexpr (MOST >= 4) if (per > 2 && !a.outlier_off) return launch_u<XK, NT, GB, 4>(a, waves, st);
-  if constexpr (MOST >= 2) if (per > 1 && !a.outlier_off) return launch_u<XK, NT, GB, 2>(a, waves, st);
-  launch_u<XK, NT, GB, 1>(a, waves, st);
-}
-
-template <int XK, int NT>
-void launch_gb(const PackedLinearLaunch& a, int gb, hipStream_t st) {
-  if constexpr (XK == X_I8_BF16) {
-    launch_nt<XK, NT, 32>(a, st);
-  } else {
-    if (gb == 128) launch_nt<XK, NT, 128>(a, st);
-    else if (gb == 64) launch_nt<XK, NT, 64>(a, st);
-    else if constexpr (XK != X_I8) launch_nt<XK, NT, 32>(a, st);
-  }
+  const int64_t strips = (a.m + kPackRows - 1) / kPackRows, across = (a.n + 127) / 128;
+  const int64_t most = std::clamp<int64_t>(4096 / strips, 1, std::min(16, kLdsBytes / bytes));
+  a.per = (int)((across + most - 1) / most);
+  const int waves = (int)((across + a.per - 1) / a.per);
+  packed_rows<XK, GB, OVER><<<dim3((unsigned)strips), 64 * waves, waves * bytes, st>>>(a);
 }
 
 template <int XK>
 void launch_x(const PackedLinearLaunch& a, int gb, hipStream_t st) {
-  // 64 tokens at once need more registers than float32 x or entries leave
-  if (a.ntok <= 16) return launch_gb<XK, 1>(a, gb, st);
-  if constexpr (XK == X_BF16 || XK == X_I8)
-    if (a.ntok > 32 && !a.outlier_off) return launch_gb<XK, 4>(a, gb, st);
-  launch_gb<XK, 2>(a, gb, st);
+  const bool over = a.outlier_off != nullptr;
+  if constexpr (XK != X_I8_BF16) {
+    if (gb == 128) return over ? launch_gb<XK, 128, true>(a, st) : launch_gb<XK, 128, false>(a, st);
+    if (gb == 64) return over ? launch_gb<XK, 64, true>(a, st) : launch_gb<XK, 64, false>(a, st);
+  }
+  if constexpr (XK != X_I8)
+    over ? launch_gb<XK, 32, true>(a, st) : launch_gb<XK, 32, false>(a, st);
 }
 
 }  // namespace
 
+// Up to 16 tokens, steps per 32 columns or more (or per row), offsets within
+// 32 bits.
 bool rows_ok(int64_t ntok, int64_t n, int32_t G) {
-  return ntok <= kRowsTokens && (G == n || G % 32 == 0);
+  return ntok <= kRowsTokens && (G == n || G % 32 == 0) && n < (1 << 24);
 }
 
-hipError_t launch_rows(const PackedLinearLaunch& a, hipStream_t st) {
+// Bytes of the padded copy of x; 0 where its rows can be copied in 16-byte
+// units as they are.
+size_t rows_staged_bytes(const void* x, int32_t xdtype, int64_t ntok, int64_t n, int64_t ldx) {
+  const int64_t es = xdtype == PWQ_I8 ? 1 : (xdtype == PWQ_BF16 ? 2 : 4);
+  const bool direct = ldx < (1 << 24) && ldx * es % 16 == 0 && n * es % 16 == 0 &&
+                      (uintptr_t)x % 16 == 0;
+  return direct ? 0 : (size_t)(ntok * ((n + 15) / 16 * 16) * es);
+}
+
+hipError_t launch_rows(PackedLinearLaunch a, void* staged, hipStream_t st) {
+  if (staged) {
+    const int64_t wide = (a.n + 15) / 16 * 16;
+    const dim3 grid((unsigned)((a.ntok * wide + 255) / 256));
+    if (a.xdtype == PWQ_I8)
+      pad_rows<<<grid, 256, 0, st>>>((const uint8_t*)a.x, a.ntok, a.n, a.ldx, (uint8_t*)staged,
+                                     wide);
+    else if (a.xdtype == PWQ_BF16)
+      pad_rows<<<grid, 256, 0, st>>>((const uint16_t*)a.x, a.ntok, a.n, a.ldx, (uint16_t*)staged,
+                                     wide);
+    else
+      pad_rows<<<grid, 256, 0, st>>>((const uint32_t*)a.x, a.ntok, a.n, a.ldx, (uint32_t*)staged,
+                                     wide);
+    a.x = staged;
+    a.ldx = wide;
+  }
+  a.xcols = staged ? a.ldx : a.n;
   const int gb = a.G == a.n || a.G % 128 == 0 ? 128 : (a.G % 64 == 0 ? 64 : 32);
   if (a.xdtype == PWQ_BF16) launch_x<X_BF16>(a, gb, st);
   else if (a.xdtype == PWQ_F32) launch_x<X_F32>(a, gb, st);

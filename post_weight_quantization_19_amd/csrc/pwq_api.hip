@@ -934,26 +934,40 @@ pwq_status pwq_rms_norm(const void* x, int32_t xdtype, int64_t ntok, int64_t n, 
   return ok();
 }
 
-// Which kernel serves a product.
-static PromptPlan linear_plan(int64_t ntok, int64_t m, int64_t n, int32_t G, int32_t xdtype) {
-  PromptPlan p{};
-  if (ntok > kRowsTokens) p = prompt_plan(ntok, m, n, G, xdtype);
+// Which kernel serves a product, and its workspace.
+struct LinearPlan {
+  bool rows = false;        // few tokens
+  PromptPlan prompt{};      // .ok: many tokens; neither: any shape
+  size_t staged = 0, partial = 0;
+};
+static LinearPlan linear_plan(const void* x, int32_t xdtype, int64_t ntok, int64_t ldx, int64_t m,
+                              int64_t n, int32_t G) {
+  LinearPlan p;
+  if (ntok == 0 || m == 0) return p;
+  p.rows = rows_ok(ntok, n, G);
+  if (p.rows) {
+    p.staged = rows_staged_bytes(x, xdtype, ntok, n, ldx);
+  } else {
+    p.prompt = prompt_plan(x, xdtype, ntok, ldx, m, n, G);
+    p.staged = p.prompt.staged_bytes;
+    p.partial = p.prompt.partial_bytes;
+  }
   return p;
 }
 
-static void carve_linear(Carver& c, const PromptPlan& p, void** staged, void** partial) {
-  *staged = p.staged_bytes ? c.take(p.staged_bytes) : nullptr;
-  *partial = p.partial_bytes ? c.take(p.partial_bytes) : nullptr;
+static void carve_linear(Carver& c, const LinearPlan& p, void** staged, void** partial) {
+  *staged = p.staged ? c.take(p.staged) : nullptr;
+  *partial = p.partial ? c.take(p.partial) : nullptr;
 }
 
-size_t pwq_packed_linear_workspace_size(int64_t ntok, int64_t m, int64_t n, int32_t group,
-                                        int32_t xdtype) {
+size_t pwq_packed_linear_workspace_size(const void* x, int32_t xdtype, int64_t ntok, int64_t ldx,
+                                        int64_t m, int64_t n, int32_t group) {
   if (ntok < 0 || m < 0 || n <= 0 || ntok > INT32_MAX || m > INT32_MAX || n > INT32_MAX) return 0;
-  if (group < 0 || (group > 0 && n % group)) return 0;
+  if (group < 0 || (group > 0 && n % group) || ldx < n) return 0;
   Carver c(nullptr);
   void *staged, *partial;
-  carve_linear(c, linear_plan(ntok, m, n, group > 0 ? group : (int32_t)n, xdtype), &staged,
-               &partial);
+  carve_linear(c, linear_plan(x, xdtype, ntok, ldx, m, n, group > 0 ? group : (int32_t)n),
+               &staged, &partial);
   return c.size();
 }
 
@@ -984,20 +998,22 @@ pwq_status pwq_packed_linear(const void* x, int32_t xdtype, int64_t ntok, int64_
     if ((uintptr_t)qweight % 16)
       return fail(PWQ_ERR_INVALID_ARG, "qweight must be 16-byte aligned");
   }
-  pwq_status s = check_ws(ws, ws_bytes, pwq_packed_linear_workspace_size(ntok, m, n, group, xdtype));
+  pwq_status s = check_ws(ws, ws_bytes,
+                          pwq_packed_linear_workspace_size(x, xdtype, ntok, ldx, m, n, group));
   if (s != PWQ_OK) return s;
   PackedLinearLaunch a{x, xdtype, ntok, ldx, x_scales, qweight, m, n, packed_row_bytes(n), scales,
                        zeros, group > 0 ? group : (int32_t)n, n_out > 0 ? outlier_off : nullptr,
-                       outliers, n_out, y, ydtype, ldy};
-  const PromptPlan p = linear_plan(ntok, m, n, a.G, xdtype);
+                       outliers, n_out, y, ydtype, ldy, 0, 0, 0};
+  const LinearPlan p = linear_plan(x, xdtype, ntok, ldx, m, n, a.G);
   Carver c(ws);
   void *staged, *partial;
   carve_linear(c, p, &staged, &partial);
   hipStream_t st = (hipStream_t)stream;
   hipError_t e = hipSuccess;
   if (ntok > 0 && m > 0)
-    e = p.ok ? launch_prompt(a, p, staged, partial, st)
-             : (rows_ok(ntok, n, a.G) ? launch_rows(a, st) : launch_linear_any(a, st));
+    e = p.rows ? launch_rows(a, staged, st)
+               : (p.prompt.ok ? launch_prompt(a, p.prompt, staged, partial, st)
+                              : launch_linear_any(a, st));
   if (e != hipSuccess) return hip_fail(e, "packed_linear launch");
   return ok();
 }

@@ -198,22 +198,28 @@ struct PackedLinearLaunch {
   void* y;
   int32_t ydtype;
   int64_t ldy;
+  // launch_rows: columns x has in memory, tiles of 128 per wave, tiles ahead
+  int64_t xcols;
+  int32_t per, depth;
 };
 // Any shape, one wave per row and few tokens.
 hipError_t launch_linear_any(const PackedLinearLaunch& a, hipStream_t st);
-// Few tokens, each weight read once.
-constexpr int64_t kRowsTokens = 64;
+// Few tokens, each weight read once; staged: rows_staged_bytes of workspace,
+// NULL where that is 0.
+constexpr int64_t kRowsTokens = 16;
 bool rows_ok(int64_t ntok, int64_t n, int32_t G);
-hipError_t launch_rows(const PackedLinearLaunch& a, hipStream_t st);
+size_t rows_staged_bytes(const void* x, int32_t xdtype, int64_t ntok, int64_t n, int64_t ldx);
+hipError_t launch_rows(PackedLinearLaunch a, void* staged, hipStream_t st);
 // Many tokens: the plan depends on the sizes alone, its workspace is
 // staged_bytes + partial_bytes.
 struct PromptPlan {
-  bool ok, i8, big;
+  bool ok, i8, big, direct;
   int mode, reps;
   int64_t steps, per, splits, tiles_t, tiles_r, staged_row;
   size_t staged_bytes, partial_bytes;
 };
-PromptPlan prompt_plan(int64_t ntok, int64_t m, int64_t n, int32_t G, int32_t xdtype);
+PromptPlan prompt_plan(const void* x, int32_t xdtype, int64_t ntok, int64_t ldx, int64_t m,
+                       int64_t n, int32_t G);
 hipError_t launch_prompt(const PackedLinearLaunch& a, const PromptPlan& p, void* staged,
                          void* partial, hipStream_t st);
 
