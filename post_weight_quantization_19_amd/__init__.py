@@ -491,7 +491,30 @@ def ssqr_quant_layer(W: torch.Tensor, X: Optional[torch.Tensor] = None,
 
 # ------------------------------------------------------------ running a packed layer
 
+# A serving step calls these once per layer, so they check with plain
+# comparisons and ask for a workspace only where the library wants one.
+
 _DTYPES = {torch.float32: _lib.PWQ_F32, torch.bfloat16: _lib.PWQ_BF16, torch.int8: _lib.PWQ_I8}
+
+
+def _raw_stream(t: torch.Tensor):
+    return torch._C._cuda_getCurrentRawStream(t.device.index)
+
+
+def _rows(t: torch.Tensor, name: str) -> int:
+    """Row stride of a 2-D GPU tensor with unit column stride."""
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be on the GPU")
+    return _row_major(t)
+
+
+def _expect(t: torch.Tensor, name: str, shape: tuple, dtype: torch.dtype) -> int:
+    """Address of a contiguous GPU tensor of this shape and type."""
+    if t.shape != shape or t.dtype is not dtype or not t.is_cuda or not t.is_contiguous():
+        if not t.is_cuda:
+            raise ValueError(f"{name} must be on the GPU")
+        _check(t, name, shape, (dtype,))
+    return t.data_ptr()
 
 
 def pack_weights(codes: torch.Tensor, scales: torch.Tensor, grid: Grid,
@@ -549,31 +572,36 @@ def rms_norm(x: torch.Tensor, weight: torch.Tensor, residual: Optional[torch.Ten
     (default: x's) or int8, which comes with a step per token (scales [tokens]
     fp32, y = codes).  ``sum`` is x + residual in x's type, written to
     ``sum_out`` where given (x or residual itself for in place)."""
-    _require_cuda(x, weight, residual, sum_out)
-    ldx = _row_major(x)
+    ldx = _rows(x, "x")
     ntok, n = x.shape
     xdt = _dtype_code(x)
-    if weight.shape != (n,) or not weight.is_contiguous():
-        raise ValueError(f"weight must be a contiguous [{n}] tensor")
     wdt = _dtype_code(weight)
+    wp = _expect(weight, "weight", (n,), weight.dtype)
     odt = x.dtype if out_dtype is None else out_dtype
-    if odt not in _DTYPES:
+    ydt = _DTYPES.get(odt)
+    if ydt is None:
         raise TypeError(f"unsupported output dtype {odt}")
-    if residual is None and sum_out is not None:
+    total, rp, ldr, tp, lds = sum_out, None, 0, None, 0
+    if residual is not None:
+        if residual.shape != x.shape or residual.dtype is not x.dtype:
+            raise ValueError("residual must have x's shape and type")
+        rp, ldr = residual.data_ptr(), _rows(residual, "residual")
+        if total is None:
+            total = torch.empty((ntok, n), dtype=x.dtype, device=x.device)
+        elif total.shape != x.shape or total.dtype is not x.dtype:
+            raise ValueError("sum_out must have x's shape and type")
+        tp, lds = total.data_ptr(), _rows(total, "sum_out")
+    elif sum_out is not None:
         raise ValueError("sum_out goes with a residual")
-    for t, name in ((residual, "residual"), (sum_out, "sum_out")):
-        if t is not None and (t.shape != x.shape or t.dtype != x.dtype):
-            raise ValueError(f"{name} must have x's shape and type")
-    total = sum_out
-    if residual is not None and total is None:
-        total = torch.empty((ntok, n), dtype=x.dtype, device=x.device)
     y = torch.empty((ntok, n), dtype=odt, device=x.device)
-    scales = (torch.empty(ntok, dtype=torch.float32, device=x.device) if odt == torch.int8
-              else None)
-    check(lib().pwq_rms_norm(x.data_ptr(), xdt, ntok, n, ldx, _ptr(residual),
-                             0 if residual is None else _row_major(residual), weight.data_ptr(),
-                             wdt, eps, _ptr(total), 0 if total is None else _row_major(total),
-                             y.data_ptr(), _DTYPES[odt], n, _ptr(scales), _stream()))
+    scales, sp = None, None
+    if ydt == _lib.PWQ_I8:
+        scales = torch.empty(ntok, dtype=torch.float32, device=x.device)
+        sp = scales.data_ptr()
+    status = lib().pwq_rms_norm(x.data_ptr(), xdt, ntok, n, ldx, rp, ldr, wp, wdt, eps, tp, lds,
+                                y.data_ptr(), ydt, n, sp, _raw_stream(x))
+    if status:
+        check(status)
     return y, scales, total
 
 
@@ -584,45 +612,56 @@ def packed_linear(x: torch.Tensor, packed: dict, x_scales: Optional[torch.Tensor
     bf16, fp32, or int8 with a step per token (``x_scales`` [tokens] fp32, as
     from rms_norm).  ``out_dtype`` is bf16 or fp32 (default: x's; bf16 for
     int8); ``out`` may pass the result's memory."""
-    q, scales, zeros = packed["qweight"], packed["scales"], packed["zeros"]
-    off, outliers = packed["outlier_off"], packed["outliers"]
+    q, zeros, outliers = packed["qweight"], packed["zeros"], packed["outliers"]
     n, group = packed["n"], packed["group"]
-    _require_cuda(x, q, scales, zeros, off, outliers, x_scales, out)
-    ldx = _row_major(x)
-    ntok, m = x.shape[0], q.shape[0]
-    if x.shape[1] != n:
-        raise ValueError(f"x has {x.shape[1]} columns, the layer {n}")
-    if x.dtype not in _DTYPES:
+    ldx = _rows(x, "x")
+    ntok, cols = x.shape
+    m = q.shape[0]
+    if cols != n:
+        raise ValueError(f"x has {cols} columns, the layer {n}")
+    xdt = _DTYPES.get(x.dtype)
+    if xdt is None:
         raise TypeError(f"unsupported dtype {x.dtype}")
     if group <= 0 or n % group:
         raise ValueError(f"group {group} does not divide n = {n}")
-    _check(q, "qweight", (m, (n + 31) // 32 * 16), (torch.uint8,))
-    _check(scales, "scales", (m, n // group), _F32)
-    _check(zeros, "zeros", (m, n // group), (torch.uint8,))
+    qp = _expect(q, "qweight", (m, (n + 31) // 32 * 16), torch.uint8)
+    sp = _expect(packed["scales"], "scales", (m, n // group), torch.float32)
+    zp = offp = outp = xsp = None
+    n_out = 0
+    if zeros is not None:
+        zp = _expect(zeros, "zeros", (m, n // group), torch.uint8)
     if outliers is not None:
-        _check(off, "outlier_off", ((m + 15) // 16 * ((n + 127) // 128) + 1,), _I32)
-        _check(outliers, "outliers", (outliers.numel(),), _I32)
-    if (x.dtype == torch.int8) != (x_scales is not None):
+        n_out = outliers.shape[0]
+        outp = _expect(outliers, "outliers", (n_out,), torch.int32)
+        offp = _expect(packed["outlier_off"], "outlier_off",
+                       ((m + 15) // 16 * ((n + 127) // 128) + 1,), torch.int32)
+    if x_scales is not None:
+        xsp = _expect(x_scales, "x_scales", (ntok,), torch.float32)
+    if (xdt == _lib.PWQ_I8) != (x_scales is not None):
         raise ValueError("x_scales goes with int8 x, and only with it")
-    _check(x_scales, "x_scales", (ntok,), _F32)
     odt = out_dtype
     if odt is None:
-        odt = out.dtype if out is not None else (torch.bfloat16 if x.dtype == torch.int8
+        odt = out.dtype if out is not None else (torch.bfloat16 if xdt == _lib.PWQ_I8
                                                  else x.dtype)
-    if odt not in (torch.bfloat16, torch.float32):
+    if odt is not torch.bfloat16 and odt is not torch.float32:
         raise TypeError(f"unsupported output dtype {odt}")
     if out is None:
-        out = torch.empty((ntok, m), dtype=odt, device=x.device)
-    elif out.shape != (ntok, m) or out.dtype != odt:
-        raise ValueError(f"out must be [{ntok}, {m}] {odt}")
+        out, ldy = torch.empty((ntok, m), dtype=odt, device=x.device), m
+    else:
+        if out.shape != (ntok, m) or out.dtype is not odt:
+            raise ValueError(f"out must be [{ntok}, {m}] {odt}")
+        ldy = _rows(out, "out") if ntok and m else m
     L_ = lib()
-    xdt = _DTYPES[x.dtype]
-    nb = L_.pwq_packed_linear_workspace_size(x.data_ptr(), xdt, ntok, ldx, m, n, group)
-    ws = _workspace(nb, x.device) if nb else None
-    check(L_.pwq_packed_linear(x.data_ptr(), xdt, ntok, ldx, _ptr(x_scales), q.data_ptr(), m, n,
-                               scales.data_ptr(), _ptr(zeros), group,
-                               _ptr(off) if outliers is not None else None, _ptr(outliers),
-                               0 if outliers is None else outliers.numel(), out.data_ptr(),
-                               _DTYPES[odt], _row_major(out) if ntok and m else m, _ptr(ws), nb,
-                               _stream()))
+    ws, nb = None, 0
+    while True:
+        status = L_.pwq_packed_linear(x.data_ptr(), xdt, ntok, ldx, xsp, qp, m, n, sp, zp, group,
+                                      offp, outp, n_out, out.data_ptr(), _DTYPES[odt], ldy,
+                                      None if ws is None else ws.data_ptr(), nb, _raw_stream(x))
+        if status != _lib.PWQ_ERR_WORKSPACE or ws is not None:
+            break
+        ws = _workspace(L_.pwq_packed_linear_workspace_size(x.data_ptr(), xdt, ntok, ldx, m, n,
+                                                            group), x.device)
+        nb = ws.numel()
+    if status:
+        check(status)
     return out

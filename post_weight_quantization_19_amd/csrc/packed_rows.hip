@@ -57,7 +57,8 @@ __device__ __forceinline__ void wait_copies(int n) {
 #define PWQ_WC(N) \
     case N: asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory"); break;
     PWQ_WC(1) PWQ_WC(2) PWQ_WC(3) PWQ_WC(4) PWQ_WC(5) PWQ_WC(6) PWQ_WC(7) PWQ_WC(8) PWQ_WC(9)
-    PWQ_WC(10) PWQ_WC(12) PWQ_WC(15) PWQ_WC(18)
+    PWQ_WC(10) PWQ_WC(11) PWQ_WC(12) PWQ_WC(13) PWQ_WC(14) PWQ_WC(15) PWQ_WC(16) PWQ_WC(18)
+    PWQ_WC(20) PWQ_WC(21) PWQ_WC(24) PWQ_WC(25) PWQ_WC(27) PWQ_WC(28)
 #undef PWQ_WC
     default: asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); break;
   }
@@ -134,12 +135,10 @@ __device__ __forceinline__ void x_parts(const typename XType<XK>::T* p,
 }
 
 // LDS of a wave: `depth` slots of a tile (weights 1 KB, x), the steps and zero
-// points of 16 rows x 16 groups, overflow entries.
-constexpr int kStepRow = 17;                         // 16 groups, off the bank stride
-constexpr int kSteps = 16 * kStepRow * 4;            // bytes of the steps; as many zero points
+// points of 16 rows x `srow` groups (odd: off the bank stride), overflow entries.
 constexpr int kEntries = 256;
-constexpr int wave_bytes(int depth, int xbytes, bool over) {
-  return depth * (1024 + xbytes) + 2 * kSteps + (over ? 4 * kEntries : 0);
+constexpr int wave_bytes(int depth, int xbytes, int srow, bool over) {
+  return depth * (1024 + xbytes) + (2 * 16 * srow * 4 + 15) / 16 * 16 + (over ? 4 * kEntries : 0);
 }
 
 template <int XK, int GB, bool OVER>
@@ -156,19 +155,19 @@ __global__ __launch_bounds__(1024) void packed_rows(const PackedLinearLaunch a) 
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int lr = lane & 15, lq = lane >> 4;
   const int64_t strip = blockIdx.x;
-  const int tok = (int)a.ntok, n = (int)a.n, G = a.G, ng = n / G, ldq = (int)a.ldq;
+  const int tok = (int)a.ntok, n = (int)a.n, G = a.G, ng = a.ng, ldq = (int)a.ldq;
   const int xcols = (int)a.xcols;
-  const int across = (n + 127) >> 7, per = a.per, depth = a.depth;
+  const int across = (n + 127) >> 7, per = a.per, depth = a.depth, srow = a.srow;
   const int k0 = wave * per, k1 = min(across, k0 + per);
   const int rows = (int)min(a.m - strip * kPackRows, (int64_t)kPackRows);
   const bool asym = a.zeros != nullptr;
   const int xbytes = (tok + RPC - 1) / RPC * 1024, slot_bytes = 1024 + xbytes;
-  const int own = wave * wave_bytes(depth, xbytes, OVER);
+  const int own = wave * wave_bytes(depth, xbytes, srow, OVER);
   char* const L = smem + own;
   const uint32_t lbase = (uint32_t)(uintptr_t)(lds_char*)smem + own;
   float* const steps = (float*)(L + depth * slot_bytes);
-  float* const zs = steps + 16 * kStepRow;
-  int* const ents = (int*)(zs + 16 * kStepRow);
+  float* const zs = steps + 16 * srow;
+  int* const ents = (int*)(L + wave_bytes(depth, xbytes, srow, false));
 
   // copies: lane -> 16-byte unit.  Units of a row are permuted by the row so
   // that the operand reads below spread over the banks.
@@ -227,9 +226,11 @@ __global__ __launch_bounds__(1024) void packed_rows(const PackedLinearLaunch a) 
     for (int d = 0; d < depth && c0 + d < c1; ++d) copy_tile(c0 + d, d);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const int at = wr * kStepRow + 4 * (lane & 3) + i;
-      steps[at] = XK == X_I8 && !asym ? 0.0625f * sv[i] : sv[i];
-      zs[at] = XK == X_I8 ? __int_as_float(zv[i]) : -(asym ? 16.0f + (float)zv[i] : 24.0f);
+      const int gi = 4 * (lane & 3) + i, at = wr * srow + gi;
+      if (gi < srow) {
+        steps[at] = XK == X_I8 && !asym ? 0.0625f * sv[i] : sv[i];
+        zs[at] = XK == X_I8 ? __int_as_float(zv[i]) : -(asym ? 16.0f + (float)zv[i] : 24.0f);
+      }
     }
     int ebase = 0;
     if constexpr (OVER) {
@@ -253,8 +254,8 @@ __global__ __launch_bounds__(1024) void packed_rows(const PackedLinearLaunch a) 
       }
 #pragma unroll
       for (int h = 0; h < NB; ++h) {
-        const float s = steps[lr * kStepRow + g];
-        const float zf = zs[lr * kStepRow + g];
+        const float s = steps[lr * srow + g];
+        const float zf = zs[lr * srow + g];
         in_g += GB;
         if (in_g >= G) in_g -= G, ++g;
         uint32_t w[NW];
@@ -361,7 +362,7 @@ __global__ __launch_bounds__(1024) void packed_rows(const PackedLinearLaunch a) 
 
   // join the waves' sums in their order; lane l: tokens 4 (l / 16) + e, row l % 16
   float* const joined = (float*)smem;
-  const int stride = wave_bytes(depth, xbytes, OVER) / 4;
+  const int stride = wave_bytes(depth, xbytes, srow, OVER) / 4;
 #pragma unroll
   for (int e = 0; e < 4; ++e) joined[wave * stride + e * 64 + lane] = acc[e];
   __syncthreads();
@@ -370,6 +371,7 @@ __global__ __launch_bounds__(1024) void packed_rows(const PackedLinearLaunch a) 
     const int64_t t = 4 * (l >> 4) + e, r = strip * kPackRows + (l & 15);
     if (t >= tok || r >= a.m) continue;
     float sum = joined[v];
+#pragma unroll 4
     for (int o = 1; o < waves; ++o) sum += joined[o * stride + v];
     if (a.x_scales) sum *= a.x_scales[t];
     if (a.ydtype == PWQ_F32) ((float*)a.y)[t * a.ldy + r] = sum;
@@ -393,14 +395,20 @@ template <int XK, int GB, bool OVER>
 void launch_gb(PackedLinearLaunch a, hipStream_t st) {
   constexpr int ES = sizeof(typename XType<XK>::T), RPC = 64 / (128 * ES / 16);
   const int xbytes = (int)(a.ntok + RPC - 1) / RPC * 1024;
-  // tiles ahead: what 16 waves of a CU have LDS for, 2 to 4
-  a.depth = 4;
-  while (a.depth > 2 && 16 * wave_bytes(a.depth, xbytes, OVER) > kLdsBytes) --a.depth;
-  const int bytes = wave_bytes(a.depth, xbytes, OVER);
-  // about 16 waves per CU over the whole launch
+  // about 16 waves per CU over the whole launch; as many tiles ahead as LDS
+  // holds for them, 8 at most (the whole range of a wave, mostly: what is in
+  // flight from the start is not waited for twice)
   const int64_t strips = (a.m + kPackRows - 1) / kPackRows, across = (a.n + 127) / 128;
-  const int64_t most = std::clamp<int64_t>(4096 / strips, 1, std::min(16, kLdsBytes / bytes));
-  a.per = (int)((across + most - 1) / most);
+  int most = (int)std::clamp<int64_t>(4096 / strips, 1, 16), bytes;
+  for (;; --most) {
+    a.per = (int)((across + most - 1) / most);
+    a.srow = std::min(16, a.per * (128 / GB)) | 1;
+    a.depth = std::min(8, a.per);
+    while (a.depth > 2 && 16 * wave_bytes(a.depth, xbytes, a.srow, OVER) > kLdsBytes) --a.depth;
+    bytes = wave_bytes(a.depth, xbytes, a.srow, OVER);
+    if (most * bytes <= kLdsBytes) break;
+  }
+  a.ng = (int)(a.n / a.G);
   const int waves = (int)((across + a.per - 1) / a.per);
   packed_rows<XK, GB, OVER><<<dim3((unsigned)strips), 64 * waves, waves * bytes, st>>>(a);
 }

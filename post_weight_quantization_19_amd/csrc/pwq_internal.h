@@ -198,9 +198,10 @@ struct PackedLinearLaunch {
   void* y;
   int32_t ydtype;
   int64_t ldy;
-  // launch_rows: columns x has in memory, tiles of 128 per wave, tiles ahead
+  // launch_rows: columns x has in memory, groups of a row, tiles of 128 columns
+  // per wave, tiles ahead, groups staged per row
   int64_t xcols;
-  int32_t per, depth;
+  int32_t ng, per, depth, srow;
 };
 // Any shape, one wave per row and few tokens.
 hipError_t launch_linear_any(const PackedLinearLaunch& a, hipStream_t st);
