@@ -1,7 +1,16 @@
 // Root-mean-square norm with the residual's addition and an 8-bit output:
 //   h = x + residual,  r = 1 / sqrt(mean(h^2) + eps),  y = h r w,
-//   8 bits: step = max|y| / 127 (1 if 0), q = rint(y / step).
+//   8 bits: step = max|y| / 127 (1 if that is 0), q = rint(y / step).
+//
+// rms_norm_regs keeps a token's row in registers: x and residual are read
+// once, the sum and y written once (7 bytes an element for bf16 in, 8 bits
+// out), with two reductions in between.  TPR threads share a row, 8
+// consecutive elements each NV times over; a workgroup keeps the weight of
+// its columns in registers and walks over tokens.  Rows longer than the
+// registers hold take rms_norm_rows, which reads them three times.
 #include "pwq_internal.h"
+
+#include <algorithm>
 
 namespace pwq {
 namespace {
@@ -37,6 +46,169 @@ __device__ __forceinline__ float block_max(float v, float* red) {
   return s;
 }
 
+struct __attribute__((packed, aligned(1))) pack16 { uint32_t v[4]; };
+struct __attribute__((packed, aligned(1))) pack8 { uint32_t v[2]; };
+
+// Eight elements from p (any alignment); those past `left` are 0.
+template <typename T>
+__device__ __forceinline__ void load8(const T* p, int left, float (&v)[8]) {
+  if (left >= 8) {
+    if constexpr (std::is_same_v<T, float>) {
+      const pack16 a = ((const pack16*)p)[0], b = ((const pack16*)p)[1];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) v[e] = __uint_as_float(a.v[e]), v[4 + e] = __uint_as_float(b.v[e]);
+    } else {
+      const pack16 a = *(const pack16*)p;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        v[2 * e] = __uint_as_float(a.v[e] << 16);
+        v[2 * e + 1] = __uint_as_float(a.v[e] & 0xffff0000u);
+      }
+    }
+  } else {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] = e < left ? load1<T>(p, e) : 0.0f;
+  }
+}
+
+__device__ __forceinline__ uint32_t two_bf16(float a, float b) {
+  const __bf16 x[2] = {(__bf16)a, (__bf16)b};
+  return __builtin_bit_cast(uint32_t, x);
+}
+
+template <typename T>
+__device__ __forceinline__ void store8(T* p, int left, const float (&v)[8]) {
+  if (left >= 8) {
+    if constexpr (std::is_same_v<T, float>) {
+      pack16 a, b;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) a.v[e] = __float_as_uint(v[e]), b.v[e] = __float_as_uint(v[4 + e]);
+      ((pack16*)p)[0] = a, ((pack16*)p)[1] = b;
+    } else if constexpr (std::is_same_v<T, uint16_t>) {
+      pack16 a;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) a.v[e] = two_bf16(v[2 * e], v[2 * e + 1]);
+      *(pack16*)p = a;
+    } else {
+      pack8 a;
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        a.v[h] = 0;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) a.v[h] |= ((uint32_t)(int)v[4 * h + e] & 255u) << (8 * e);
+      }
+      *(pack8*)p = a;
+    }
+  } else {
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+      if (e < left) {
+        if constexpr (std::is_same_v<T, float>) p[e] = v[e];
+        else if constexpr (std::is_same_v<T, uint16_t>) p[e] = (uint16_t)two_bf16(v[e], 0.0f);
+        else p[e] = (T)(int)v[e];
+      }
+  }
+}
+
+// Sum or maximum over the TPR threads of a row (the workgroup, or a wave).
+template <int TPR, typename Op>
+__device__ __forceinline__ float row_reduce(float v, float* red, Op op) {
+#pragma unroll
+  for (int o = 32; o >= 1; o >>= 1) v = op(v, __shfl_xor(v, o, 64));
+  if constexpr (TPR > 64) {
+    if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = v;
+    __syncthreads();
+    v = red[0];
+#pragma unroll
+    for (int i = 1; i < TPR / 64; ++i) v = op(v, red[i]);
+  }
+  return v;
+}
+
+template <typename T, int TPR, int NV, bool RES>
+__global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void rms_norm_regs(const RmsNormLaunch a) {
+  constexpr int RPB = TPR < 256 ? 256 / TPR : 1;       // rows of a workgroup at a time
+  __shared__ float red[2][2][16];                      // [token parity][sum, maximum]
+  const int in = threadIdx.x % TPR, n = (int)a.n;
+  float w[NV][8];
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    const int k = 8 * (in + TPR * i);
+    if (a.wdtype == PWQ_F32) load8((const float*)a.weight + k, n - k, w[i]);
+    else load8((const uint16_t*)a.weight + k, n - k, w[i]);
+  }
+  const float inv_n = 1.0f / (float)n;
+  int parity = 0;
+  for (int64_t t = (int64_t)blockIdx.x * RPB + threadIdx.x / TPR; t < a.ntok;
+       t += (int64_t)gridDim.x * RPB, parity ^= 1) {
+    float h[NV][8];
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int k = 8 * (in + TPR * i);
+      load8((const T*)a.x + t * a.ldx + k, n - k, h[i]);
+    }
+    if constexpr (RES) {
+      float q[NV][8];
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        const int k = 8 * (in + TPR * i);
+        load8((const T*)a.residual + t * a.ldr + k, n - k, q[i]);
+      }
+#pragma unroll
+      for (int i = 0; i < NV; ++i)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) h[i][e] += q[i][e];
+    }
+    if (a.sum) {
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        const int k = 8 * (in + TPR * i);
+        store8((T*)a.sum + t * a.lds + k, n - k, h[i]);
+      }
+    }
+    float ss = 0.0f;
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) ss = fmaf(h[i][e], h[i][e], ss);
+    ss = row_reduce<TPR>(ss, red[parity][0], [](float p, float q) { return p + q; });
+    const float r = rsqrtf(fmaf(ss, inv_n, a.eps));
+    float mx = 0.0f;
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        h[i][e] = h[i][e] * r * w[i][e];
+        mx = max_nan(mx, fabsf(h[i][e]));
+      }
+    if (a.ydtype == PWQ_I8) {
+      mx = row_reduce<TPR>(mx, red[parity][1], max_nan);
+      float step = mx / 127.0f;
+      if (step == 0.0f) step = 1.0f;
+      if (in == 0) a.scales[t] = step;
+      // the reciprocal of a step below 2^-126 is not finite: divide
+      const float inv = mx >= 1e-35f ? 127.0f / mx : 0.0f;
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        const int k = 8 * (in + TPR * i);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const float q = __builtin_rintf(inv != 0.0f ? h[i][e] * inv : h[i][e] / step);
+          h[i][e] = mx == mx ? q : 0.0f;
+        }
+        store8((int8_t*)a.y + t * a.ldy + k, n - k, h[i]);
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        const int k = 8 * (in + TPR * i);
+        if (a.ydtype == PWQ_F32) store8((float*)a.y + t * a.ldy + k, n - k, h[i]);
+        else store8((uint16_t*)a.y + t * a.ldy + k, n - k, h[i]);
+      }
+    }
+  }
+}
+
 // One workgroup per token, three passes over its row.
 template <typename T>
 __global__ __launch_bounds__(256) void rms_norm_rows(
@@ -64,7 +236,8 @@ __global__ __launch_bounds__(256) void rms_norm_rows(
     for (int64_t k = threadIdx.x; k < n; k += blockDim.x)
       mx = max_nan(mx, fabsf(h_at(k) * r * w_at(k)));
     mx = block_max(mx, red);
-    step = mx == 0.0f ? 1.0f : mx / 127.0f;
+    step = mx / 127.0f;
+    if (step == 0.0f) step = 1.0f;
     if (threadIdx.x == 0) scales[t] = step;
   }
   for (int64_t k = threadIdx.x; k < n; k += blockDim.x) {
@@ -83,20 +256,42 @@ __global__ __launch_bounds__(256) void rms_norm_rows(
   }
 }
 
+template <typename T, int TPR, int NV>
+void launch_regs(const RmsNormLaunch& a, hipStream_t st) {
+  constexpr int RPB = TPR < 256 ? 256 / TPR : 1;
+  // workgroups that run at once: the rest of the tokens are walked over
+  const int64_t blocks = std::min<int64_t>((a.ntok + RPB - 1) / RPB, 256 * (2048 / std::max(TPR, 256)));
+  const dim3 grid((unsigned)blocks), block(TPR < 256 ? 256 : TPR);
+  if (a.residual) rms_norm_regs<T, TPR, NV, true><<<grid, block, 0, st>>>(a);
+  else rms_norm_regs<T, TPR, NV, false><<<grid, block, 0, st>>>(a);
+}
+
+template <typename T>
+void launch_type(const RmsNormLaunch& a, hipStream_t st) {
+  const int64_t n = a.n;
+  // Few tokens: more threads a row, for latency.  Many: fewer, for fewer
+  // barriers.
+  if (n <= 512) return launch_regs<T, 64, 1>(a, st);
+  if (n <= 1024) return launch_regs<T, 64, 2>(a, st);
+  if (n <= 2048) return launch_regs<T, 64, 4>(a, st);
+  if (a.ntok >= 512) {
+    if (n <= 4096) return launch_regs<T, 256, 2>(a, st);
+    if (n <= 8192) return launch_regs<T, 256, 4>(a, st);
+  }
+  if (n <= 8192) return launch_regs<T, 1024, 1>(a, st);
+  if (n <= 16384) return launch_regs<T, 1024, 2>(a, st);
+  if (n <= 32768) return launch_regs<T, 1024, 4>(a, st);
+  rms_norm_rows<T><<<dim3((unsigned)a.ntok), 256, 0, st>>>(
+      a.x, a.n, a.ldx, a.residual, a.ldr, a.weight, a.wdtype == PWQ_F32, a.eps, a.sum, a.lds, a.y,
+      a.ydtype, a.ldy, a.scales);
+}
+
 }  // namespace
 
 hipError_t launch_rms_norm(const RmsNormLaunch& a, hipStream_t st) {
   if (a.ntok == 0) return hipSuccess;
-  const dim3 grid((unsigned)a.ntok), block(256);
-  const int wf32 = a.wdtype == PWQ_F32;
-  if (a.xdtype == PWQ_F32)
-    rms_norm_rows<float><<<grid, block, 0, st>>>(a.x, a.n, a.ldx, a.residual, a.ldr, a.weight,
-                                                 wf32, a.eps, a.sum, a.lds, a.y, a.ydtype, a.ldy,
-                                                 a.scales);
-  else
-    rms_norm_rows<uint16_t><<<grid, block, 0, st>>>(a.x, a.n, a.ldx, a.residual, a.ldr, a.weight,
-                                                    wf32, a.eps, a.sum, a.lds, a.y, a.ydtype,
-                                                    a.ldy, a.scales);
+  if (a.xdtype == PWQ_F32) launch_type<float>(a, st);
+  else launch_type<uint16_t>(a, st);
   return hipGetLastError();
 }
 
