@@ -49,25 +49,19 @@ __device__ __forceinline__ float block_max(float v, float* red) {
 struct __attribute__((packed, aligned(1))) pack16 { uint32_t v[4]; };
 struct __attribute__((packed, aligned(1))) pack8 { uint32_t v[2]; };
 
-// Eight elements from p (any alignment); those past `left` are 0.
+// Eight consecutive elements as they are in memory (any alignment).
+template <typename T> struct Raw { pack16 v[sizeof(T) / 2]; };
 template <typename T>
-__device__ __forceinline__ void load8(const T* p, int left, float (&v)[8]) {
-  if (left >= 8) {
-    if constexpr (std::is_same_v<T, float>) {
-      const pack16 a = ((const pack16*)p)[0], b = ((const pack16*)p)[1];
+__device__ __forceinline__ Raw<T> raw8(const T* p) { return *(const Raw<T>*)p; }
+__device__ __forceinline__ void widen(const Raw<float>& r, float (&v)[8]) {
 #pragma unroll
-      for (int e = 0; e < 4; ++e) v[e] = __uint_as_float(a.v[e]), v[4 + e] = __uint_as_float(b.v[e]);
-    } else {
-      const pack16 a = *(const pack16*)p;
+  for (int e = 0; e < 8; ++e) v[e] = __uint_as_float(r.v[e / 4].v[e % 4]);
+}
+__device__ __forceinline__ void widen(const Raw<uint16_t>& r, float (&v)[8]) {
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        v[2 * e] = __uint_as_float(a.v[e] << 16);
-        v[2 * e + 1] = __uint_as_float(a.v[e] & 0xffff0000u);
-      }
-    }
-  } else {
-#pragma unroll
-    for (int e = 0; e < 8; ++e) v[e] = e < left ? load1<T>(p, e) : 0.0f;
+  for (int e = 0; e < 4; ++e) {
+    v[2 * e] = __uint_as_float(r.v[0].v[e] << 16);
+    v[2 * e + 1] = __uint_as_float(r.v[0].v[e] & 0xffff0000u);
   }
 }
 
@@ -76,9 +70,10 @@ __device__ __forceinline__ uint32_t two_bf16(float a, float b) {
   return __builtin_bit_cast(uint32_t, x);
 }
 
+// Elements lo .. 7 to p .. p + 7.
 template <typename T>
-__device__ __forceinline__ void store8(T* p, int left, const float (&v)[8]) {
-  if (left >= 8) {
+__device__ __forceinline__ void store8(T* p, int lo, const float (&v)[8]) {
+  if (lo == 0) {
     if constexpr (std::is_same_v<T, float>) {
       pack16 a, b;
 #pragma unroll
@@ -101,8 +96,8 @@ __device__ __forceinline__ void store8(T* p, int left, const float (&v)[8]) {
     }
   } else {
 #pragma unroll
-    for (int e = 0; e < 8; ++e)
-      if (e < left) {
+    for (int e = 1; e < 8; ++e)
+      if (e >= lo) {
         if constexpr (std::is_same_v<T, float>) p[e] = v[e];
         else if constexpr (std::is_same_v<T, uint16_t>) p[e] = (uint16_t)two_bf16(v[e], 0.0f);
         else p[e] = (T)(int)v[e];
@@ -125,46 +120,56 @@ __device__ __forceinline__ float row_reduce(float v, float* red, Op op) {
   return v;
 }
 
+// The vector of a thread at or past the row's end starts 8 before the end
+// instead, and its first `lo` elements, a neighbour's, count as 0.
 template <typename T, int TPR, int NV, bool RES>
 __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void rms_norm_regs(const RmsNormLaunch a) {
   constexpr int RPB = TPR < 256 ? 256 / TPR : 1;       // rows of a workgroup at a time
   __shared__ float red[2][2][16];                      // [token parity][sum, maximum]
   const int in = threadIdx.x % TPR, n = (int)a.n;
+  const bool ragged = n < 8 * TPR * NV;
+  int at[NV], lo[NV];
   float w[NV][8];
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
     const int k = 8 * (in + TPR * i);
-    if (a.wdtype == PWQ_F32) load8((const float*)a.weight + k, n - k, w[i]);
-    else load8((const uint16_t*)a.weight + k, n - k, w[i]);
+    at[i] = min(k, n - 8);
+    lo[i] = min(k - at[i], 8);
+    if (a.wdtype == PWQ_F32) widen(raw8((const float*)a.weight + at[i]), w[i]);
+    else widen(raw8((const uint16_t*)a.weight + at[i]), w[i]);
   }
   const float inv_n = 1.0f / (float)n;
-  int parity = 0;
-  for (int64_t t = (int64_t)blockIdx.x * RPB + threadIdx.x / TPR; t < a.ntok;
-       t += (int64_t)gridDim.x * RPB, parity ^= 1) {
+  const int64_t step_t = (int64_t)gridDim.x * RPB;
+  int64_t t = (int64_t)blockIdx.x * RPB + threadIdx.x / TPR;
+  if (t >= a.ntok) return;
+  Raw<T> x[NV], q[RES ? NV : 1];
+  auto load = [&](int64_t row) {
+#pragma unroll
+    for (int i = 0; i < NV; ++i) x[i] = raw8((const T*)a.x + row * a.ldx + at[i]);
+    if constexpr (RES)
+#pragma unroll
+      for (int i = 0; i < NV; ++i) q[i] = raw8((const T*)a.residual + row * a.ldr + at[i]);
+  };
+  load(t);
+  for (int parity = 0; t < a.ntok; t += step_t, parity ^= 1) {
     float h[NV][8];
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      const int k = 8 * (in + TPR * i);
-      load8((const T*)a.x + t * a.ldx + k, n - k, h[i]);
-    }
-    if constexpr (RES) {
-      float q[NV][8];
+      widen(x[i], h[i]);
+      if constexpr (RES) {
+        float v[8];
+        widen(q[i], v);
 #pragma unroll
-      for (int i = 0; i < NV; ++i) {
-        const int k = 8 * (in + TPR * i);
-        load8((const T*)a.residual + t * a.ldr + k, n - k, q[i]);
+        for (int e = 0; e < 8; ++e) h[i][e] += v[e];
       }
+      if (ragged)
 #pragma unroll
-      for (int i = 0; i < NV; ++i)
-#pragma unroll
-        for (int e = 0; e < 8; ++e) h[i][e] += q[i][e];
+        for (int e = 0; e < 8; ++e) h[i][e] = e >= lo[i] ? h[i][e] : 0.0f;
     }
+    if (t + step_t < a.ntok) load(t + step_t);           // the next token's, behind this one
     if (a.sum) {
 #pragma unroll
-      for (int i = 0; i < NV; ++i) {
-        const int k = 8 * (in + TPR * i);
-        store8((T*)a.sum + t * a.lds + k, n - k, h[i]);
-      }
+      for (int i = 0; i < NV; ++i) store8((T*)a.sum + t * a.lds + at[i], lo[i], h[i]);
     }
     float ss = 0.0f;
 #pragma unroll
@@ -190,20 +195,18 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void rms_norm_regs(const Rms
       const float inv = mx >= 1e-35f ? 127.0f / mx : 0.0f;
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
-        const int k = 8 * (in + TPR * i);
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-          const float q = __builtin_rintf(inv != 0.0f ? h[i][e] * inv : h[i][e] / step);
-          h[i][e] = mx == mx ? q : 0.0f;
+          const float c = __builtin_rintf(inv != 0.0f ? h[i][e] * inv : h[i][e] / step);
+          h[i][e] = mx == mx ? c : 0.0f;
         }
-        store8((int8_t*)a.y + t * a.ldy + k, n - k, h[i]);
+        store8((int8_t*)a.y + t * a.ldy + at[i], lo[i], h[i]);
       }
     } else {
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
-        const int k = 8 * (in + TPR * i);
-        if (a.ydtype == PWQ_F32) store8((float*)a.y + t * a.ldy + k, n - k, h[i]);
-        else store8((uint16_t*)a.y + t * a.ldy + k, n - k, h[i]);
+        if (a.ydtype == PWQ_F32) store8((float*)a.y + t * a.ldy + at[i], lo[i], h[i]);
+        else store8((uint16_t*)a.y + t * a.ldy + at[i], lo[i], h[i]);
       }
     }
   }
@@ -260,10 +263,17 @@ template <typename T, int TPR, int NV>
 void launch_regs(const RmsNormLaunch& a, hipStream_t st) {
   constexpr int RPB = TPR < 256 ? 256 / TPR : 1;
   // workgroups that run at once: the rest of the tokens are walked over
-  const int64_t blocks = std::min<int64_t>((a.ntok + RPB - 1) / RPB, 256 * (2048 / std::max(TPR, 256)));
+  const int64_t blocks = std::min<int64_t>((a.ntok + RPB - 1) / RPB, 256 * (1536 / std::max(TPR, 256) + (TPR == 1024)));
   const dim3 grid((unsigned)blocks), block(TPR < 256 ? 256 : TPR);
   if (a.residual) rms_norm_regs<T, TPR, NV, true><<<grid, block, 0, st>>>(a);
   else rms_norm_regs<T, TPR, NV, false><<<grid, block, 0, st>>>(a);
+}
+
+template <typename T>
+void launch_loop(const RmsNormLaunch& a, hipStream_t st) {
+  rms_norm_rows<T><<<dim3((unsigned)a.ntok), 256, 0, st>>>(
+      a.x, a.n, a.ldx, a.residual, a.ldr, a.weight, a.wdtype == PWQ_F32, a.eps, a.sum, a.lds, a.y,
+      a.ydtype, a.ldy, a.scales);
 }
 
 template <typename T>
@@ -271,19 +281,19 @@ void launch_type(const RmsNormLaunch& a, hipStream_t st) {
   const int64_t n = a.n;
   // Few tokens: more threads a row, for latency.  Many: fewer, for fewer
   // barriers.
+  if (n < 8) return launch_loop<T>(a, st);
   if (n <= 512) return launch_regs<T, 64, 1>(a, st);
   if (n <= 1024) return launch_regs<T, 64, 2>(a, st);
   if (n <= 2048) return launch_regs<T, 64, 4>(a, st);
   if (a.ntok >= 512) {
     if (n <= 4096) return launch_regs<T, 256, 2>(a, st);
     if (n <= 8192) return launch_regs<T, 256, 4>(a, st);
+    if (n <= 16384) return launch_regs<T, 512, 4>(a, st);
   }
   if (n <= 8192) return launch_regs<T, 1024, 1>(a, st);
   if (n <= 16384) return launch_regs<T, 1024, 2>(a, st);
   if (n <= 32768) return launch_regs<T, 1024, 4>(a, st);
-  rms_norm_rows<T><<<dim3((unsigned)a.ntok), 256, 0, st>>>(
-      a.x, a.n, a.ldx, a.residual, a.ldr, a.weight, a.wdtype == PWQ_F32, a.eps, a.sum, a.lds, a.y,
-      a.ydtype, a.ldy, a.scales);
+  launch_loop<T>(a, st);
 }
 
 }  // namespace
