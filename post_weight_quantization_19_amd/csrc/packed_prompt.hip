@@ -56,18 +56,37 @@ __device__ __forceinline__ uint2 steps_i8(uint32_t w, uint32_t z4) {
                     __builtin_amdgcn_perm(odd, even, 0x07030602u));
 }
 
-// ... to bf16 (small integers: the upper half of their float32 is exact).
-__device__ __forceinline__ uint4 steps_bf16(uint32_t w, float z) {
-  const uint32_t even = w & 0x0f0f0f0fu, odd = (w >> 4) & 0x0f0f0f0fu;
-  uint32_t o[4];
+// Eight signed 4-bit codes to bytes of 16 times their value.
+__device__ __forceinline__ uint2 signed16_i8(uint32_t w) {
+  const uint32_t even = (w << 4) & 0xf0f0f0f0u, odd = w & 0xf0f0f0f0u;
+  return make_uint2(__builtin_amdgcn_perm(odd, even, 0x05010400u),
+                    __builtin_amdgcn_perm(odd, even, 0x07030602u));
+}
+
+// ... to bf16: a code's four bits are put at the top of the mantissa of 16,
+// and 16 + z is subtracted in float32, whose upper half holds the difference
+// exactly (no conversion instruction: those run at a quarter of the rate).
+// zb = 16 + z, or 24 with `bias` 0x41c0 for signed halves (it flips their top
+// bit; 0x4180 otherwise).
+__device__ __forceinline__ uint4 steps_bf16(uint32_t w, uint32_t bias, float zb) {
+  constexpr uint32_t M = 0x00780078u;
+  const uint32_t c[4] = {((w << 3) & M) ^ bias, ((w >> 1) & M) ^ bias, ((w >> 5) & M) ^ bias,
+                         ((w >> 9) & M) ^ bias};            // columns i and i + 4
+  float lo[4], hi[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const float a = (float)((even >> (8 * i)) & 0xffu) - z;
-    const float b = (float)((odd >> (8 * i)) & 0xffu) - z;
-    o[i] = __builtin_amdgcn_perm(__float_as_uint(b), __float_as_uint(a), 0x07060302u);
+    lo[i] = __uint_as_float(c[i] << 16) - zb;
+    hi[i] = __uint_as_float(c[i] & 0xffff0000u) - zb;
   }
-  return make_uint4(o[0], o[1], o[2], o[3]);
+  auto two = [](float x, float y) {
+    return __builtin_amdgcn_perm(__float_as_uint(y), __float_as_uint(x), 0x07060302u);
+  };
+  return make_uint4(two(lo[0], lo[1]), two(lo[2], lo[3]), two(hi[0], hi[1]), two(hi[2], hi[3]));
 }
+
+// 1.5 2^23 as an integer: int32 sums below 2^22 that start here read as
+// 1.5 2^23 + sum when taken for a float32.
+constexpr int kMagic = 0x4b400000;
 
 struct PromptArgs {
   const char* x;          // rows of `steps` * 128 bytes, 16-byte aligned
@@ -93,7 +112,9 @@ struct PromptArgs {
 
 // MODE: how often sums are multiplied by their step.  0: one step per row,
 // at the end; 1: every step (G a multiple of its columns); 2: twice a step.
-template <bool I8, int BT, int BR, int WT, int WR, int MODE>
+// PLAIN: signed codes without overflow entries (8-bit operands are then 16
+// times the code, which takes fewer instructions to spread).
+template <bool I8, int BT, int BR, int WT, int WR, int MODE, bool PLAIN>
 __global__ __launch_bounds__(64 * WT * WR) void prompt_tiles(const PromptArgs a) {
   constexpr int NT = 64 * WT * WR;
   constexpr int NI = BT / WT / 16, NJ = BR / WR / 16;
@@ -133,8 +154,8 @@ __global__ __launch_bounds__(64 * WT * WR) void prompt_tiles(const PromptArgs a)
     xoff[h] = (uint32_t)((min(t0 + r, a.ntok - 1) - t0) * a.xrow + 16 * c);
   }
   const char* xbase = a.x + (int64_t)t0 * a.xrow;
-  auto copy_x = [&](int s) {
-    const uint32_t dst = lbase + (uint32_t)(s % 3) * XB + 1024u * wave;
+  auto copy_x = [&](int s, int slot) {
+    const uint32_t dst = lbase + (uint32_t)slot * XB + 1024u * wave;
 #pragma unroll
     for (int h = 0; h < NC; ++h) copy16(xoff[h], xbase + (int64_t)s * KB, dst + 16u * NT * h);
   };
@@ -143,29 +164,41 @@ __global__ __launch_bounds__(64 * WT * WR) void prompt_tiles(const PromptArgs a)
   constexpr int TPR = WB / PER;               // threads per row
   const int wrow = tid / TPR, wpart = tid % TPR;
   const int grow = min(r0 + wrow, a.m - 1);
-  const uint8_t* wsrc = a.qweight + grow * a.ldq + wpart * PER;
+  const uint8_t* const wbase = a.qweight + r0 * a.ldq;
+  const uint32_t wsrc = (uint32_t)((grow - r0) * a.ldq + wpart * PER);
   const int wleft = (int)a.ldq - wpart * PER;   // bytes from wsrc to the row's end
   const uint32_t flip = a.zeros ? 0u : 0x88888888u;
+  // (SYM reads the steps' bytes in the zero points' place and uses 8)
+  const uint8_t* zsrc = a.zeros ? a.zeros + (int64_t)grow * a.ng
+                                : (const uint8_t*)(a.scales + (int64_t)grow * a.ng);
   uint4 wreg[PER / 16];
   int zreg = 8;
   auto load_w = [&](int s) {
     const int o = s / a.reps * WB;
 #pragma unroll
     for (int i = 0; i < PER / 16; ++i)
-      wreg[i] = *(const uint4*)(wsrc + (o + 16 * i < wleft ? o + 16 * i : 0));
-    if (a.zeros) {
-      const int k = min((o + wpart * PER) * 2, a.n - 1);
-      zreg = a.zeros[(int64_t)grow * a.ng + (MODE == 0 ? 0 : k / a.G)];
-    }
+      wreg[i] = *(const uint4*)(wbase + (wsrc + (uint32_t)(o + 16 * i < wleft ? o + 16 * i : 0)));
+    if constexpr (!PLAIN)
+      zreg = zsrc[MODE == 0 ? 0 : min((o + wpart * PER) * 2, a.n - 1) / a.G];
   };
   // overflow entries of the thread's strip of 16 rows
   const int across = (a.n + kPackCols - 1) / kPackCols;
   const int strip = min(r0 / kPackRows + wrow / kPackRows,
                         (a.m + kPackRows - 1) / kPackRows - 1);
-  auto put_w = [&](int s) {
-    const uint32_t dst = (uint32_t)(3 * XB + (s & 1) * WBUF);
-    if constexpr (I8) {
-      const uint32_t z4 = (uint32_t)zreg * 0x01010101u;
+  auto put_w = [&](int s, int slot) {
+    const uint32_t dst = (uint32_t)(3 * XB + slot * WBUF);
+    const int z = PLAIN || !a.zeros ? 8 : zreg;
+    if constexpr (I8 && PLAIN) {
+#pragma unroll
+      for (int i = 0; i < PER / 16; ++i) {
+        const uint2 p0 = signed16_i8(wreg[i].x), p1 = signed16_i8(wreg[i].y);
+        const uint2 p2 = signed16_i8(wreg[i].z), p3 = signed16_i8(wreg[i].w);
+        const int c = (wpart * PER + 16 * i) / 8;
+        *(uint4*)(smem + dst + unit_at(wrow, c)) = make_uint4(p0.x, p0.y, p1.x, p1.y);
+        *(uint4*)(smem + dst + unit_at(wrow, c + 1)) = make_uint4(p2.x, p2.y, p3.x, p3.y);
+      }
+    } else if constexpr (I8) {
+      const uint32_t z4 = (uint32_t)z * 0x01010101u;
 #pragma unroll
       for (int i = 0; i < PER / 16; ++i) {
         const uint2 p0 = steps_i8(wreg[i].x ^ flip, z4), p1 = steps_i8(wreg[i].y ^ flip, z4);
@@ -175,14 +208,15 @@ __global__ __launch_bounds__(64 * WT * WR) void prompt_tiles(const PromptArgs a)
         *(uint4*)(smem + dst + unit_at(wrow, c + 1)) = make_uint4(p2.x, p2.y, p3.x, p3.y);
       }
     } else {
-      const float z = (float)zreg;
+      const float zb = 16.0f + (float)z;
+      const uint32_t bias = !PLAIN && a.zeros ? 0x41804180u : 0x41c041c0u;
       const int c = wpart * PER / 4;
-      *(uint4*)(smem + dst + unit_at(wrow, c)) = steps_bf16(wreg[0].x ^ flip, z);
-      *(uint4*)(smem + dst + unit_at(wrow, c + 1)) = steps_bf16(wreg[0].y ^ flip, z);
-      *(uint4*)(smem + dst + unit_at(wrow, c + 2)) = steps_bf16(wreg[0].z ^ flip, z);
-      *(uint4*)(smem + dst + unit_at(wrow, c + 3)) = steps_bf16(wreg[0].w ^ flip, z);
+      *(uint4*)(smem + dst + unit_at(wrow, c)) = steps_bf16(wreg[0].x, bias, zb);
+      *(uint4*)(smem + dst + unit_at(wrow, c + 1)) = steps_bf16(wreg[0].y, bias, zb);
+      *(uint4*)(smem + dst + unit_at(wrow, c + 2)) = steps_bf16(wreg[0].z, bias, zb);
+      *(uint4*)(smem + dst + unit_at(wrow, c + 3)) = steps_bf16(wreg[0].w, bias, zb);
     }
-    if (a.n_out > 0) {
+    if constexpr (!PLAIN) if (a.n_out > 0) {
       // codes beyond 4 bits: the thread adds the entries of its own part of
       // its own row (its writes above are in order with these)
       const int k0 = s / a.reps * COLS;
@@ -207,10 +241,11 @@ __global__ __launch_bounds__(64 * WT * WR) void prompt_tiles(const PromptArgs a)
   };
 
   // step (scale) of the lane's column of every row block
-  const float* sp[NJ];
+  const float* const sbase = a.scales + (int64_t)r0 * a.ng;
+  uint32_t sp[NJ];
 #pragma unroll
   for (int j = 0; j < NJ; ++j)
-    sp[j] = a.scales + (int64_t)min(r0 + 16 * (wr * NJ + j) + (lane & 15), a.m - 1) * a.ng;
+    sp[j] = (uint32_t)((min(r0 + 16 * (wr * NJ + j) + (lane & 15), a.m - 1) - r0) * a.ng);
   constexpr int NS = MODE == 2 ? 2 : 1;
   float sc[NJ][NS], sn[NJ][NS];
   auto load_s = [&](int s) {
@@ -219,17 +254,18 @@ __global__ __launch_bounds__(64 * WT * WR) void prompt_tiles(const PromptArgs a)
     for (int h = 0; h < NS; ++h) {
       const int g = min((k0 + h * (COLS / 2)) / a.G, a.ng - 1);
 #pragma unroll
-      for (int j = 0; j < NJ; ++j) sn[j][h] = sp[j][g];
+      for (int j = 0; j < NJ; ++j) sn[j][h] = sbase[sp[j] + g] * (I8 && PLAIN ? 0.0625f : 1.0f);
     }
   };
 
-  f32x4_t acc[NI][NJ];
+  float acc[NI][NJ][4];
   acc_t dir[MODE == 0 ? NI : 1][MODE == 0 ? NJ : 1];
 #pragma unroll
   for (int i = 0; i < NI; ++i)
 #pragma unroll
     for (int j = 0; j < NJ; ++j) {
-      acc[i][j] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+      for (int e = 0; e < 4; ++e) acc[i][j][e] = 0.0f;
       if constexpr (MODE == 0) dir[i][j] = acc_t{0, 0, 0, 0};
     }
 
@@ -240,75 +276,111 @@ __global__ __launch_bounds__(64 * WT * WR) void prompt_tiles(const PromptArgs a)
                                                      __builtin_bit_cast(bf16x8_t, w), c, 0, 0, 0);
   };
   const int lr = lane & 15, lq = lane >> 4;
-  const acc_t zero = {0, 0, 0, 0};
+  // what a block's sum starts from, and its value
+  acc_t zero = {0, 0, 0, 0};
+  if constexpr (I8) zero = acc_t{kMagic, kMagic, kMagic, kMagic};
+  auto value = [](const acc_t& c, int e) {
+    if constexpr (I8) return __int_as_float(c[e]) - 12582912.0f;
+    else return c[e];
+  };
 
   // prologue: step s0 in LDS, step s0 + 1 on its way
+  const int last = s1 - 1;
   load_w(s0);
-  copy_x(s0);
-  put_w(s0);
+  copy_x(s0, s0 % 3);
+  put_w(s0, s0 & 1);
   load_s(s0);
-  if (s0 + 1 < s1) {
-    load_w(s0 + 1);
-    copy_x(s0 + 1);
-  }
+  load_w(min(s0 + 1, last));
+  copy_x(min(s0 + 1, last), (s0 + 1) % 3);
   asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
   lds_barrier();
 
-  for (int s = s0; s < s1; ++s) {
+  // The two waves of a SIMD spread the next step's weights at different
+  // times, one at the start of a step and one at its end, so that the matrix
+  // unit has work from the other.  (Past the last step they spread and
+  // load it again, without branches.)
+  const bool early = wave < WT * WR / 2;
+  auto next = [&](int s) {
     // the last step's loads: weights of step s + 1 in registers, its x in LDS
     // (every wave's, once the barrier at the end of this step is passed)
     asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    put_w(min(s + 1, last), (s + 1) & 1);
+    load_s(min(s + 1, last));
+    load_w(min(s + 2, last));
+    copy_x(min(s + 2, last), (s + 2) % 3);
+  };
+  for (int s = s0; s < s1; ++s) {
 #pragma unroll
     for (int j = 0; j < NJ; ++j)
 #pragma unroll
       for (int h = 0; h < NS; ++h) sc[j][h] = sn[j][h];
-    if (s + 1 < s1) put_w(s + 1);
-    if (s + 1 < s1) load_s(s + 1);
-    if (s + 2 < s1) {
-      load_w(s + 2);
-      copy_x(s + 2);
-    }
+    if (early) next(s);
     const char* xs = smem + s % 3 * XB;
     const char* ws = smem + 3 * XB + (s & 1) * WBUF;
-    i32x4_t w[NJ][2];
+    i32x4_t w[NJ][2], x[2][2];
 #pragma unroll
     for (int j = 0; j < NJ; ++j)
 #pragma unroll
       for (int h = 0; h < 2; ++h)
         w[j][h] = *(const i32x4_t*)(ws + unit_at(16 * (wr * NJ + j) + lr, 4 * h + lq));
-#pragma unroll
-    for (int i = 0; i < NI; ++i) {
-      i32x4_t x[2];
+    auto read_x = [&](int i) {
 #pragma unroll
       for (int h = 0; h < 2; ++h)
-        x[h] = *(const i32x4_t*)(xs + unit_at(16 * (wt * NI + i) + lr, 4 * h + lq));
+        x[i & 1][h] = *(const i32x4_t*)(xs + unit_at(16 * (wt * NI + i) + lr, 4 * h + lq));
+    };
+    read_x(0);
+    if constexpr (MODE == 0) {
 #pragma unroll
-      for (int j = 0; j < NJ; ++j) {
-        if constexpr (MODE == 0) {
-          dir[i][j] = mma(x[1], w[j][1], mma(x[0], w[j][0], dir[i][j]));
-        } else if constexpr (MODE == 1) {
-          const acc_t c = mma(x[1], w[j][1], mma(x[0], w[j][0], zero));
+      for (int i = 0; i < NI; ++i) {
+        if (i + 1 < NI) read_x(i + 1);
 #pragma unroll
-          for (int e = 0; e < 4; ++e) acc[i][j][e] = fmaf(sc[j][0], (float)c[e], acc[i][j][e]);
-        } else {
+        for (int h = 0; h < 2; ++h)
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const acc_t c = mma(x[h], w[j][h], zero);
-#pragma unroll
-            for (int e = 0; e < 4; ++e) acc[i][j][e] = fmaf(sc[j][h], (float)c[e], acc[i][j][e]);
-          }
-        }
+          for (int j = 0; j < NJ; ++j) dir[i][j] = mma(x[i & 1][h], w[j][h], dir[i][j]);
       }
+    } else {
+      // Blocks of 16 x 16 in turn: one starts, the one before gets its second
+      // half (MODE 1), the third before is multiplied by its step, so that
+      // neither waits for a matrix instruction's result.
+      constexpr int NU = NI * NJ * NS;
+      acc_t c[4];
+      auto scale = [&](auto uu, int e0) {
+        constexpr int u = decltype(uu)::value;
+        constexpr int i = u / NS / NJ, j = u / NS % NJ, h = u % NS;
+#pragma unroll
+        for (int e = e0; e < e0 + 2; ++e) {
+          acc[i][j][e] = fmaf(sc[j][h], value(c[u & 3], e), acc[i][j][e]);
+          pin(acc[i][j][e]);       // here: not moved behind the other products
+        }
+      };
+      static_for_up<NU + 3>([&](auto uu) {
+        constexpr int u = decltype(uu)::value;
+        constexpr int i = u / NS / NJ, j = u / NS % NJ, h = u % NS;
+        if constexpr (u < NU) {
+          c[u & 3] = mma(x[i & 1][h], w[j][h], zero);
+          if constexpr (j == 1 && h == 0 && i + 1 < NI) read_x(i + 1);
+        }
+        if constexpr (u >= 3) scale(std::integral_constant<int, u - 3>{}, 0);
+        __builtin_amdgcn_sched_barrier(0);
+        if constexpr (MODE == 1 && u > 0 && u <= NU) {
+          constexpr int v = u - 1, iv = v / NJ, jv = v % NJ;
+          c[v & 3] = mma(x[iv & 1][1], w[jv][1], c[v & 3]);
+        }
+        if constexpr (u >= 3) scale(std::integral_constant<int, u - 3>{}, 2);
+        __builtin_amdgcn_sched_barrier(0);
+      });
     }
+    if (!early) next(s);
     lds_barrier();
   }
+  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");   // nothing is in flight to LDS at the end
 
   // lane l holds tokens 4 (l / 16) + e, row l % 16 of every block
 #pragma unroll
   for (int j = 0; j < NJ; ++j) {
     const int r = r0 + 16 * (wr * NJ + j) + lr;
     if (r >= a.m) continue;
-    const float s = MODE == 0 ? sp[j][0] : 1.0f;
+    const float s = MODE == 0 ? sbase[sp[j]] * (I8 && PLAIN ? 0.0625f : 1.0f) : 1.0f;
 #pragma unroll
     for (int i = 0; i < NI; ++i)
 #pragma unroll
@@ -390,13 +462,19 @@ __global__ __launch_bounds__(256) void stage_x(const T* __restrict__ x, int64_t 
   }
 }
 
-template <bool I8, int BT, int BR, int WT, int WR>
-void launch_tiles(const PromptArgs& p, int mode, int splits, hipStream_t st) {
+template <bool I8, int BT, int BR, int WT, int WR, bool PLAIN>
+void launch_mode(const PromptArgs& p, int mode, int splits, hipStream_t st) {
   const dim3 grid((unsigned)((p.tiles_t * p.tiles_r + 7) / 8 * 8), (unsigned)splits);
   const int nt = 64 * WT * WR;
-  if (mode == 0) prompt_tiles<I8, BT, BR, WT, WR, 0><<<grid, nt, 0, st>>>(p);
-  else if (mode == 1) prompt_tiles<I8, BT, BR, WT, WR, 1><<<grid, nt, 0, st>>>(p);
-  else prompt_tiles<I8, BT, BR, WT, WR, 2><<<grid, nt, 0, st>>>(p);
+  if (mode == 0) prompt_tiles<I8, BT, BR, WT, WR, 0, PLAIN><<<grid, nt, 0, st>>>(p);
+  else if (mode == 1) prompt_tiles<I8, BT, BR, WT, WR, 1, PLAIN><<<grid, nt, 0, st>>>(p);
+  else prompt_tiles<I8, BT, BR, WT, WR, 2, PLAIN><<<grid, nt, 0, st>>>(p);
+}
+
+template <bool I8, int BT, int BR, int WT, int WR>
+void launch_tiles(const PromptArgs& p, int mode, int splits, hipStream_t st) {
+  if (!p.zeros && p.n_out == 0) launch_mode<I8, BT, BR, WT, WR, true>(p, mode, splits, st);
+  else launch_mode<I8, BT, BR, WT, WR, false>(p, mode, splits, st);
 }
 
 }  // namespace
