@@ -373,31 +373,88 @@ __global__ __launch_bounds__(64 * WT * WR) void prompt_tiles(const PromptArgs a)
     if (!early) next(s);
     lds_barrier();
   }
-  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");   // nothing is in flight to LDS at the end
+  // nothing is in flight to LDS, and no wave reads it, at the end
+  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+  lds_barrier();
+  if constexpr (MODE == 0) {
+#pragma unroll
+    for (int j = 0; j < NJ; ++j) {
+      const float s = sbase[sp[j]] * (I8 && PLAIN ? 0.0625f : 1.0f);
+#pragma unroll
+      for (int i = 0; i < NI; ++i)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) acc[i][j][e] = s * (float)dir[i][j][e];
+    }
+  }
 
   // lane l holds tokens 4 (l / 16) + e, row l % 16 of every block
+  const bool split_sum = a.partial != nullptr;
+  if (a.x_scales && !split_sum) {
 #pragma unroll
-  for (int j = 0; j < NJ; ++j) {
-    const int r = r0 + 16 * (wr * NJ + j) + lr;
-    if (r >= a.m) continue;
-    const float s = MODE == 0 ? sbase[sp[j]] * (I8 && PLAIN ? 0.0625f : 1.0f) : 1.0f;
+    for (int i = 0; i < NI; ++i) {
+      float xsc[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        xsc[e] = a.x_scales[min(t0 + 16 * (wt * NI + i) + 4 * lq + e, a.ntok - 1)];
+#pragma unroll
+      for (int j = 0; j < NJ; ++j)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) acc[i][j][e] *= xsc[e];
+    }
+  }
+  if (split_sum || a.ydtype == PWQ_F32) {
+    float* const y = split_sum ? a.partial + (int64_t)split * a.ntok * a.m : (float*)a.y;
+    const int64_t ld = split_sum ? a.m : a.ldy;
 #pragma unroll
     for (int i = 0; i < NI; ++i)
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         const int t = t0 + 16 * (wt * NI + i) + 4 * lq + e;
-        if (t >= a.ntok) continue;
-        float v;
-        if constexpr (MODE == 0) v = s * (float)dir[i][j][e];
-        else v = acc[i][j][e];
-        if (a.partial) {
-          a.partial[((int64_t)split * a.ntok + t) * a.m + r] = v;
-          continue;
-        }
-        if (a.x_scales) v *= a.x_scales[t];
-        if (a.ydtype == PWQ_F32) ((float*)a.y)[t * a.ldy + r] = v;
-        else ((__bf16*)a.y)[t * a.ldy + r] = (__bf16)v;
+        if (t < a.ntok)
+#pragma unroll
+          for (int j = 0; j < NJ; ++j) {
+            const int r = r0 + 16 * (wr * NJ + j) + lr;
+            if (r < a.m) y[t * ld + r] = acc[i][j][e];
+          }
       }
+    return;
+  }
+  // bf16: through LDS, so that rows of y are written 16 bytes a lane.  Two
+  // neighbouring lanes trade halves: the even one packs both their rows of
+  // token e, the odd one of token e + 1.
+  constexpr int YROW = 2 * BR + 32;                    // bytes of a token's row in LDS
+  static_assert(BT * YROW <= 3 * XB + 2 * WBUF, "the tile fits");
+  const bool odd = lane & 1;
+  const uint32_t sel = odd ? 0x03020706u : 0x05040100u;
+#pragma unroll
+  for (int i = 0; i < NI; ++i)
+#pragma unroll
+    for (int j = 0; j < NJ; ++j)
+#pragma unroll
+      for (int e = 0; e < 4; e += 2) {
+        const __bf16 two[2] = {(__bf16)acc[i][j][e], (__bf16)acc[i][j][e + 1]};
+        const uint32_t own = __builtin_bit_cast(uint32_t, two);
+        const uint32_t other = __builtin_amdgcn_update_dpp(own, own, 0xB1, 0xF, 0xF, false);
+        const int t = 16 * (wt * NI + i) + 4 * lq + e + odd;
+        const int r = 16 * (wr * NJ + j) + (lr & ~1);
+        *(uint32_t*)(smem + t * YROW + 2 * r) = __builtin_amdgcn_perm(other, own, sel);
+      }
+  lds_barrier();
+  constexpr int LPR = BR / 8;                          // lanes of a row
+  __bf16* const y = (__bf16*)a.y;
+  const bool whole = (a.ldy * 2) % 16 == 0 && (uintptr_t)a.y % 16 == 0;
+  for (int t = tid / LPR; t < BT; t += NT / LPR) {
+    const int r = r0 + 8 * (tid % LPR);
+    if (t0 + t >= a.ntok || r >= a.m) continue;
+    const char* src = smem + t * YROW + 16 * (tid % LPR);
+    __bf16* dst = y + (t0 + t) * a.ldy + r;
+    if (whole && r + 8 <= a.m) {
+      *(uint4*)dst = *(const uint4*)src;
+    } else {
+#pragma unroll
+      for (int e = 0; e < 8; ++e)
+        if (r + e < a.m) dst[e] = ((const __bf16*)src)[e];
+    }
   }
 }
 
