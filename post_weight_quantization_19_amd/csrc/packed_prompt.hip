@@ -240,22 +240,29 @@ __global__ __launch_bounds__(64 * WT * WR) void prompt_tiles(const PromptArgs a)
     }
   };
 
-  // step (scale) of the lane's column of every row block
+  // Steps (scales): lane l loads that of row l of the wave's 64, and lane
+  // l % 16 + 16 j hands it on for block j (a load in the operands' layout
+  // would look up each row four times).
+  static_assert(NJ == 4, "a lane per row of the wave");
   const float* const sbase = a.scales + (int64_t)r0 * a.ng;
-  uint32_t sp[NJ];
-#pragma unroll
-  for (int j = 0; j < NJ; ++j)
-    sp[j] = (uint32_t)((min(r0 + 16 * (wr * NJ + j) + (lane & 15), a.m - 1) - r0) * a.ng);
+  const uint32_t sp = (uint32_t)((min(r0 + 64 * wr + lane, a.m - 1) - r0) * a.ng);
   constexpr int NS = MODE == 2 ? 2 : 1;
-  float sc[NJ][NS], sn[NJ][NS];
+  float sc[NJ][NS], sn[NS];
   auto load_s = [&](int s) {
     const int k0 = s / a.reps * COLS;
 #pragma unroll
     for (int h = 0; h < NS; ++h) {
-      const int g = min((k0 + h * (COLS / 2)) / a.G, a.ng - 1);
-#pragma unroll
-      for (int j = 0; j < NJ; ++j) sn[j][h] = sbase[sp[j] + g] * (I8 && PLAIN ? 0.0625f : 1.0f);
+      const int g = MODE == 0 ? 0 : min((k0 + h * (COLS / 2)) / a.G, a.ng - 1);
+      sn[h] = sbase[sp + g] * (I8 && PLAIN ? 0.0625f : 1.0f);
     }
+  };
+  auto spread_s = [&]() {
+#pragma unroll
+    for (int h = 0; h < NS; ++h)
+#pragma unroll
+      for (int j = 0; j < NJ; ++j)
+        sc[j][h] = __int_as_float(__builtin_amdgcn_ds_bpermute(4 * (16 * j + (lane & 15)),
+                                                               __float_as_int(sn[h])));
   };
 
   float acc[NI][NJ][4];
@@ -305,15 +312,12 @@ __global__ __launch_bounds__(64 * WT * WR) void prompt_tiles(const PromptArgs a)
     // (every wave's, once the barrier at the end of this step is passed)
     asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
     put_w(min(s + 1, last), (s + 1) & 1);
-    load_s(min(s + 1, last));
+    if constexpr (MODE != 0) load_s(min(s + 1, last));
     load_w(min(s + 2, last));
     copy_x(min(s + 2, last), (s + 2) % 3);
   };
   for (int s = s0; s < s1; ++s) {
-#pragma unroll
-    for (int j = 0; j < NJ; ++j)
-#pragma unroll
-      for (int h = 0; h < NS; ++h) sc[j][h] = sn[j][h];
+    if constexpr (MODE != 0) spread_s();
     if (early) next(s);
     const char* xs = smem + s % 3 * XB;
     const char* ws = smem + 3 * XB + (s & 1) * WBUF;
@@ -377,14 +381,13 @@ __global__ __launch_bounds__(64 * WT * WR) void prompt_tiles(const PromptArgs a)
   asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
   lds_barrier();
   if constexpr (MODE == 0) {
+    spread_s();
 #pragma unroll
-    for (int j = 0; j < NJ; ++j) {
-      const float s = sbase[sp[j]] * (I8 && PLAIN ? 0.0625f : 1.0f);
+    for (int i = 0; i < NI; ++i)
 #pragma unroll
-      for (int i = 0; i < NI; ++i)
+      for (int j = 0; j < NJ; ++j)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) acc[i][j][e] = s * (float)dir[i][j][e];
-    }
+        for (int e = 0; e < 4; ++e) acc[i][j][e] = sc[j][0] * (float)dir[i][j][e];
   }
 
   // lane l holds tokens 4 (l / 16) + e, row l % 16 of every block
