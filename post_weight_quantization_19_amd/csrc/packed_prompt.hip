@@ -9,12 +9,18 @@
 // parts (the top, middle and last 8 bits of its significand), each of which
 // runs over the same weights.
 //
-// A step covers 128 bytes of every x row (128 8-bit or 64 bf16 columns).  x
-// goes HBM -> LDS by asynchronous copies one step ahead through three slots;
-// the packed weights go through registers, where they are spread to the type
-// of x, into one of two slots.  LDS rows are 128 bytes; their 16-byte units
-// are permuted by the row so that 16 rows' reads of one column block cover
-// every bank.
+// Two kernels.  spread_weights writes the integers c - z (overflow entries
+// added) once per call in the operands' order, a wave's operand a contiguous
+// kilobyte; prompt_tiles multiplies.  Spreading inside the product instead
+// was measured: every token tile repeats it on the vector unit, which the
+// multiplication by the steps already fills (1025 bf16 tokens of down_proj
+// 355 us, 2048 of up_proj 333 us).
+//
+// A step of prompt_tiles covers 128 bytes of every x row (128 8-bit or 64 bf16
+// columns).  x goes HBM -> LDS by asynchronous copies two steps ahead through
+// three slots; LDS rows are 128 bytes, their 16-byte units permuted by the row
+// so that 16 rows' reads of one column block cover every bank.  Weights go
+// straight to registers, a step ahead.
 #include "pwq_internal.h"
 
 #include <algorithm>
@@ -56,34 +62,6 @@ __device__ __forceinline__ uint2 steps_i8(uint32_t w, uint32_t z4) {
                     __builtin_amdgcn_perm(odd, even, 0x07030602u));
 }
 
-// Eight signed 4-bit codes to bytes of 16 times their value.
-__device__ __forceinline__ uint2 signed16_i8(uint32_t w) {
-  const uint32_t even = (w << 4) & 0xf0f0f0f0u, odd = w & 0xf0f0f0f0u;
-  return make_uint2(__builtin_amdgcn_perm(odd, even, 0x05010400u),
-                    __builtin_amdgcn_perm(odd, even, 0x07030602u));
-}
-
-// ... to bf16: a code's four bits are put at the top of the mantissa of 16,
-// and 16 + z is subtracted in float32, whose upper half holds the difference
-// exactly (no conversion instruction: those run at a quarter of the rate).
-// zb = 16 + z, or 24 with `bias` 0x41c0 for signed halves (it flips their top
-// bit; 0x4180 otherwise).
-__device__ __forceinline__ uint4 steps_bf16(uint32_t w, uint32_t bias, float zb) {
-  constexpr uint32_t M = 0x00780078u;
-  const uint32_t c[4] = {((w << 3) & M) ^ bias, ((w >> 1) & M) ^ bias, ((w >> 5) & M) ^ bias,
-                         ((w >> 9) & M) ^ bias};            // columns i and i + 4
-  float lo[4], hi[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    lo[i] = __uint_as_float(c[i] << 16) - zb;
-    hi[i] = __uint_as_float(c[i] & 0xffff0000u) - zb;
-  }
-  auto two = [](float x, float y) {
-    return __builtin_amdgcn_perm(__float_as_uint(y), __float_as_uint(x), 0x07060302u);
-  };
-  return make_uint4(two(lo[0], lo[1]), two(lo[2], lo[3]), two(hi[0], hi[1]), two(hi[2], hi[3]));
-}
-
 // 1.5 2^23 as an integer: int32 sums below 2^22 that start here read as
 // 1.5 2^23 + sum when taken for a float32.
 constexpr int kMagic = 0x4b400000;
@@ -96,13 +74,10 @@ struct PromptArgs {
   int per;                // steps per split
   int tiles_t, tiles_r;
   const float* x_scales;
-  const uint8_t* qweight;
-  int64_t ldq;
-  const float* scales;
-  const uint8_t* zeros;
-  const int32_t* off;
-  const int32_t* outliers;
-  int n_out;
+  const i32x4_t* spread;  // [strip of 16 rows][weight block][half][lane]
+  int blocks;             // weight blocks (steps / reps)
+  const float* steps_t;   // [group][16 strips' rows], times what the operands leave out
+  int64_t rows16;         // rows of it: 16 strips
   int ntok, m, n, G, ng;
   void* y;
   int ydtype;
@@ -110,22 +85,91 @@ struct PromptArgs {
   float* partial;         // splits x ntok x m, or NULL
 };
 
+// The operand integers of 16 rows x 128 columns (one wave each) in 8 bits or
+// bf16, and the steps of the groups that start there, group by group.
+template <bool I8>
+__global__ __launch_bounds__(256) void spread_weights(
+    const uint8_t* __restrict__ qweight, int64_t ldq, const float* __restrict__ scales,
+    const uint8_t* __restrict__ zeros, const int32_t* __restrict__ off,
+    const int32_t* __restrict__ outliers, int n_out, int64_t m, int n, int G, int ng,
+    int across, int64_t tiles, i32x4_t* __restrict__ spread, int blocks,
+    float* __restrict__ steps_t, int64_t rows16) {
+  constexpr int ROW = 128 + 16;                        // bytes of a row in LDS
+  __shared__ __attribute__((aligned(16))) char smem[4][16 * ROW];
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int64_t tile = (int64_t)blockIdx.x * 4 + wave;
+  if (tile >= tiles) return;
+  char* const L = smem[wave];
+  const int64_t strip = tile / across;
+  const int kt = (int)(tile - strip * across), k0 = kt * 128;
+  // packed bytes: lane -> row lane / 4, 32 columns
+  const int r = lane >> 2, kc = k0 + 32 * (lane & 3);
+  const int64_t row = min(strip * 16 + r, m - 1);
+  uint4 w = make_uint4(0, 0, 0, 0);
+  if (kc / 2 < ldq) w = *(const uint4*)(qweight + row * ldq + kc / 2);
+  const int z = zeros ? zeros[row * ng + min(kc / G, ng - 1)] : 8;
+  const uint32_t z4 = (uint32_t)z * 0x01010101u, flip = zeros ? 0u : 0x88888888u;
+  {
+    const uint2 p0 = steps_i8(w.x ^ flip, z4), p1 = steps_i8(w.y ^ flip, z4);
+    const uint2 p2 = steps_i8(w.z ^ flip, z4), p3 = steps_i8(w.w ^ flip, z4);
+    char* d = L + r * ROW + 32 * (lane & 3);
+    *(uint4*)d = make_uint4(p0.x, p0.y, p1.x, p1.y);
+    *(uint4*)(d + 16) = make_uint4(p2.x, p2.y, p3.x, p3.y);
+  }
+  if (n_out > 0) {
+    // the wave's own LDS: its writes above are in order with these
+    const int e0 = max(off[tile], 0), e1 = min(off[tile + 1], n_out);
+    for (int e = e0 + lane; e < e1; e += 64) {
+      const int v = outliers[e];
+      int8_t* d = (int8_t*)(L + ((v >> 7) & 15) * ROW + (v & 127));
+      *d = (int8_t)(*d + (v >> 16));
+    }
+  }
+  asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+  const int lr = lane & 15, lq = lane >> 4;
+  if constexpr (I8) {
+    i32x4_t* const o = spread + (strip * blocks + kt) * 128 + lane;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) o[64 * h] = *(const i32x4_t*)(L + lr * ROW + 64 * h + 16 * lq);
+  } else {
+#pragma unroll
+    for (int b = 0; b < 2; ++b) {
+      if (2 * kt + b >= blocks) break;
+      i32x4_t* const o = spread + (strip * blocks + 2 * kt + b) * 128 + lane;
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        int8_t c[8];
+        __builtin_memcpy(c, L + lr * ROW + 64 * b + 32 * h + 8 * lq, 8);
+        i32x4_t v;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)                    // (small integers: exact in bf16)
+          v[i] = (int)__builtin_amdgcn_perm(__float_as_uint((float)c[2 * i + 1]),
+                                            __float_as_uint((float)c[2 * i]), 0x07060302u);
+        o[64 * h] = v;
+      }
+    }
+  }
+  // steps, transposed: groups starting in the tile
+  for (int g = (k0 + G - 1) / G; g < ng && g * G < k0 + 128; ++g)
+    if (lane < 16) steps_t[g * rows16 + strip * 16 + lane] =
+        scales[min(strip * 16 + lane, m - 1) * ng + g];
+}
+
 // MODE: how often sums are multiplied by their step.  0: one step per row,
 // at the end; 1: every step (G a multiple of its columns); 2: twice a step.
-// PLAIN: signed codes without overflow entries (8-bit operands are then 16
-// times the code, which takes fewer instructions to spread).
-template <bool I8, int BT, int BR, int WT, int WR, int MODE, bool PLAIN>
+template <bool I8, int BT, int BR, int WT, int WR, int MODE>
 __global__ __launch_bounds__(64 * WT * WR) void prompt_tiles(const PromptArgs a) {
   constexpr int NT = 64 * WT * WR;
   constexpr int NI = BT / WT / 16, NJ = BR / WR / 16;
   constexpr int COLS = I8 ? 128 : 64;         // columns of a step
-  constexpr int WB = COLS / 2;                // packed bytes of a row per step
-  constexpr int PER = BR * WB / NT;           // packed bytes of a thread per step
-  constexpr int XB = BT * KB, WBUF = BR * KB;
+  constexpr int XB = BT * KB;
   constexpr int NC = XB / (16 * NT);          // copies of a wave per step
-  static_assert(PER == (I8 ? 32 : 16) && NC * 16 * NT == XB, "tile and threads fit");
+  constexpr int YROW = 2 * BR + 32;           // bytes of a token's row of y in LDS
+  constexpr int LDS = 3 * XB > BT * YROW ? 3 * XB : BT * YROW;
+  static_assert(NC * 16 * NT == XB, "tile and threads fit");
   using acc_t = std::conditional_t<I8, i32x4_t, f32x4_t>;
-  __shared__ __attribute__((aligned(16))) char smem[3 * XB + 2 * WBUF];
+  __shared__ __attribute__((aligned(16))) char smem[LDS];
   lds_char* L = (lds_char*)smem;
   const uint32_t lbase = (uint32_t)(uintptr_t)L;
 
@@ -160,109 +204,32 @@ __global__ __launch_bounds__(64 * WT * WR) void prompt_tiles(const PromptArgs a)
     for (int h = 0; h < NC; ++h) copy16(xoff[h], xbase + (int64_t)s * KB, dst + 16u * NT * h);
   };
 
-  // weights: thread -> row and part of the row's bytes
-  constexpr int TPR = WB / PER;               // threads per row
-  const int wrow = tid / TPR, wpart = tid % TPR;
-  const int grow = min(r0 + wrow, a.m - 1);
-  const uint8_t* const wbase = a.qweight + r0 * a.ldq;
-  const uint32_t wsrc = (uint32_t)((grow - r0) * a.ldq + wpart * PER);
-  const int wleft = (int)a.ldq - wpart * PER;   // bytes from wsrc to the row's end
-  const uint32_t flip = a.zeros ? 0u : 0x88888888u;
-  // (SYM reads the steps' bytes in the zero points' place and uses 8)
-  const uint8_t* zsrc = a.zeros ? a.zeros + (int64_t)grow * a.ng
-                                : (const uint8_t*)(a.scales + (int64_t)grow * a.ng);
-  uint4 wreg[PER / 16];
-  int zreg = 8;
-  auto load_w = [&](int s) {
-    const int o = s / a.reps * WB;
-#pragma unroll
-    for (int i = 0; i < PER / 16; ++i)
-      wreg[i] = *(const uint4*)(wbase + (wsrc + (uint32_t)(o + 16 * i < wleft ? o + 16 * i : 0)));
-    if constexpr (!PLAIN)
-      zreg = zsrc[MODE == 0 ? 0 : min((o + wpart * PER) * 2, a.n - 1) / a.G];
+  // weights: block j of this wave is strip r0 / 16 + wr NJ + j (the last one
+  // again past the end); wave-uniform bases, the lane's offset is the same
+  const int lr = lane & 15, lq = lane >> 4;
+  auto strip = [&](int j) {
+    return min(r0 / 16 + wr * NJ + j, (int)(a.rows16 / 16) - 1);
   };
-  // overflow entries of the thread's strip of 16 rows
-  const int across = (a.n + kPackCols - 1) / kPackCols;
-  const int strip = min(r0 / kPackRows + wrow / kPackRows,
-                        (a.m + kPackRows - 1) / kPackRows - 1);
-  auto put_w = [&](int s, int slot) {
-    const uint32_t dst = (uint32_t)(3 * XB + slot * WBUF);
-    const int z = PLAIN || !a.zeros ? 8 : zreg;
-    if constexpr (I8 && PLAIN) {
-#pragma unroll
-      for (int i = 0; i < PER / 16; ++i) {
-        const uint2 p0 = signed16_i8(wreg[i].x), p1 = signed16_i8(wreg[i].y);
-        const uint2 p2 = signed16_i8(wreg[i].z), p3 = signed16_i8(wreg[i].w);
-        const int c = (wpart * PER + 16 * i) / 8;
-        *(uint4*)(smem + dst + unit_at(wrow, c)) = make_uint4(p0.x, p0.y, p1.x, p1.y);
-        *(uint4*)(smem + dst + unit_at(wrow, c + 1)) = make_uint4(p2.x, p2.y, p3.x, p3.y);
-      }
-    } else if constexpr (I8) {
-      const uint32_t z4 = (uint32_t)z * 0x01010101u;
-#pragma unroll
-      for (int i = 0; i < PER / 16; ++i) {
-        const uint2 p0 = steps_i8(wreg[i].x ^ flip, z4), p1 = steps_i8(wreg[i].y ^ flip, z4);
-        const uint2 p2 = steps_i8(wreg[i].z ^ flip, z4), p3 = steps_i8(wreg[i].w ^ flip, z4);
-        const int c = (wpart * PER + 16 * i) / 8;
-        *(uint4*)(smem + dst + unit_at(wrow, c)) = make_uint4(p0.x, p0.y, p1.x, p1.y);
-        *(uint4*)(smem + dst + unit_at(wrow, c + 1)) = make_uint4(p2.x, p2.y, p3.x, p3.y);
-      }
-    } else {
-      const float zb = 16.0f + (float)z;
-      const uint32_t bias = !PLAIN && a.zeros ? 0x41804180u : 0x41c041c0u;
-      const int c = wpart * PER / 4;
-      *(uint4*)(smem + dst + unit_at(wrow, c)) = steps_bf16(wreg[0].x, bias, zb);
-      *(uint4*)(smem + dst + unit_at(wrow, c + 1)) = steps_bf16(wreg[0].y, bias, zb);
-      *(uint4*)(smem + dst + unit_at(wrow, c + 2)) = steps_bf16(wreg[0].z, bias, zb);
-      *(uint4*)(smem + dst + unit_at(wrow, c + 3)) = steps_bf16(wreg[0].w, bias, zb);
-    }
-    if constexpr (!PLAIN) if (a.n_out > 0) {
-      // codes beyond 4 bits: the thread adds the entries of its own part of
-      // its own row (its writes above are in order with these)
-      const int k0 = s / a.reps * COLS;
-      const int tl = strip * across + min(k0 / kPackCols, across - 1);
-      const int e0 = max(a.off[tl], 0), e1 = min(a.off[tl + 1], a.n_out);
-      const int first = k0 % kPackCols + 2 * wpart * PER;
-      for (int e = e0; e < e1; ++e) {
-        const int v = a.outliers[e], k = (v & 127) - first;
-        if (((v >> 7) & 15) == (wrow & 15) && k >= 0 && k < 2 * PER) {
-          const int at = 2 * wpart * PER + k;
-          if constexpr (I8) {
-            char* p = smem + dst + unit_at(wrow, at >> 4) + (at & 15);
-            *(int8_t*)p = (int8_t)(*(int8_t*)p + (v >> 16));
-          } else {
-            char* p = smem + dst + unit_at(wrow, at >> 3) + 2 * (at & 7);
-            const float f = bf16_to_f32(*(uint16_t*)p) + (float)(v >> 16);
-            *(uint16_t*)p = (uint16_t)(__float_as_uint(f) >> 16);
-          }
-        }
-      }
-    }
-  };
-
-  // Steps (scales): lane l loads that of row l of the wave's 64, and lane
-  // l % 16 + 16 j hands it on for block j (a load in the operands' layout
-  // would look up each row four times).
-  static_assert(NJ == 4, "a lane per row of the wave");
-  const float* const sbase = a.scales + (int64_t)r0 * a.ng;
-  const uint32_t sp = (uint32_t)((min(r0 + 64 * wr + lane, a.m - 1) - r0) * a.ng);
   constexpr int NS = MODE == 2 ? 2 : 1;
-  float sc[NJ][NS], sn[NS];
-  auto load_s = [&](int s) {
-    const int k0 = s / a.reps * COLS;
-#pragma unroll
-    for (int h = 0; h < NS; ++h) {
-      const int g = MODE == 0 ? 0 : min((k0 + h * (COLS / 2)) / a.G, a.ng - 1);
-      sn[h] = sbase[sp + g] * (I8 && PLAIN ? 0.0625f : 1.0f);
-    }
+  struct Weights {
+    i32x4_t w[NJ][2];
+    float s[NJ][NS];
   };
-  auto spread_s = [&]() {
+  auto load_w = [&](Weights& b, int s) {
+    const int blk = s / a.reps;
 #pragma unroll
-    for (int h = 0; h < NS; ++h)
+    for (int j = 0; j < NJ; ++j)
 #pragma unroll
-      for (int j = 0; j < NJ; ++j)
-        sc[j][h] = __int_as_float(__builtin_amdgcn_ds_bpermute(4 * (16 * j + (lane & 15)),
-                                                               __float_as_int(sn[h])));
+      for (int h = 0; h < 2; ++h)
+        b.w[j][h] = (a.spread + ((int64_t)strip(j) * a.blocks + blk) * 128 + 64 * h)[(uint32_t)lane];
+    if constexpr (MODE != 0)
+#pragma unroll
+      for (int h = 0; h < NS; ++h) {
+        const int g = min((blk * COLS + h * (COLS / 2)) / a.G, a.ng - 1);
+#pragma unroll
+        for (int j = 0; j < NJ; ++j)
+          b.s[j][h] = (a.steps_t + g * a.rows16 + 16 * strip(j))[(uint32_t)lr];
+      }
   };
 
   float acc[NI][NJ][4];
@@ -282,7 +249,6 @@ __global__ __launch_bounds__(64 * WT * WR) void prompt_tiles(const PromptArgs a)
       return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, x),
                                                      __builtin_bit_cast(bf16x8_t, w), c, 0, 0, 0);
   };
-  const int lr = lane & 15, lq = lane >> 4;
   // what a block's sum starts from, and its value
   acc_t zero = {0, 0, 0, 0};
   if constexpr (I8) zero = acc_t{kMagic, kMagic, kMagic, kMagic};
@@ -291,42 +257,25 @@ __global__ __launch_bounds__(64 * WT * WR) void prompt_tiles(const PromptArgs a)
     else return c[e];
   };
 
-  // prologue: step s0 in LDS, step s0 + 1 on its way
+  // prologue: steps s0 and s0 + 1 of x and the weights of s0 on their way
   const int last = s1 - 1;
-  load_w(s0);
+  Weights b0, b1;
   copy_x(s0, s0 % 3);
-  put_w(s0, s0 & 1);
-  load_s(s0);
-  load_w(min(s0 + 1, last));
   copy_x(min(s0 + 1, last), (s0 + 1) % 3);
-  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-  lds_barrier();
+  load_w(b0, s0);
 
-  // The two waves of a SIMD spread the next step's weights at different
-  // times, one at the start of a step and one at its end, so that the matrix
-  // unit has work from the other.  (Past the last step they spread and
-  // load it again, without branches.)
-  const bool early = wave < WT * WR / 2;
-  auto next = [&](int s) {
-    // the last step's loads: weights of step s + 1 in registers, its x in LDS
-    // (every wave's, once the barrier at the end of this step is passed)
+  auto step = [&](int s, Weights& b, Weights& bn) {
+    // What the last step asked for has arrived: this step's weights, the next
+    // one's x of this wave.  Past the barrier every wave's part of this step's
+    // x is there, and the slot before it is free.
     asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-    put_w(min(s + 1, last), (s + 1) & 1);
-    if constexpr (MODE != 0) load_s(min(s + 1, last));
-    load_w(min(s + 2, last));
+    lds_barrier();
     copy_x(min(s + 2, last), (s + 2) % 3);
-  };
-  for (int s = s0; s < s1; ++s) {
-    if constexpr (MODE != 0) spread_s();
-    if (early) next(s);
+    load_w(bn, min(s + 1, last));
     const char* xs = smem + s % 3 * XB;
-    const char* ws = smem + 3 * XB + (s & 1) * WBUF;
-    i32x4_t w[NJ][2], x[2][2];
-#pragma unroll
-    for (int j = 0; j < NJ; ++j)
-#pragma unroll
-      for (int h = 0; h < 2; ++h)
-        w[j][h] = *(const i32x4_t*)(ws + unit_at(16 * (wr * NJ + j) + lr, 4 * h + lq));
+    i32x4_t x[2][2];
+    i32x4_t(&w)[NJ][2] = b.w;
+    float(&sc)[NJ][NS] = b.s;
     auto read_x = [&](int i) {
 #pragma unroll
       for (int h = 0; h < 2; ++h)
@@ -374,20 +323,25 @@ __global__ __launch_bounds__(64 * WT * WR) void prompt_tiles(const PromptArgs a)
         __builtin_amdgcn_sched_barrier(0);
       });
     }
-    if (!early) next(s);
-    lds_barrier();
+  };
+  int s = s0;
+  for (; s + 1 < s1; s += 2) {
+    step(s, b0, b1);
+    step(s + 1, b1, b0);
   }
+  if (s < s1) step(s, b0, b1);
   // nothing is in flight to LDS, and no wave reads it, at the end
   asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
   lds_barrier();
   if constexpr (MODE == 0) {
-    spread_s();
 #pragma unroll
-    for (int i = 0; i < NI; ++i)
+    for (int j = 0; j < NJ; ++j) {
+      const float sj = a.steps_t[16 * strip(j) + lr];
 #pragma unroll
-      for (int j = 0; j < NJ; ++j)
+      for (int i = 0; i < NI; ++i)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) acc[i][j][e] = sc[j][0] * (float)dir[i][j][e];
+        for (int e = 0; e < 4; ++e) acc[i][j][e] = sj * (float)dir[i][j][e];
+    }
   }
 
   // lane l holds tokens 4 (l / 16) + e, row l % 16 of every block
@@ -425,8 +379,6 @@ __global__ __launch_bounds__(64 * WT * WR) void prompt_tiles(const PromptArgs a)
   // bf16: through LDS, so that rows of y are written 16 bytes a lane.  Two
   // neighbouring lanes trade halves: the even one packs both their rows of
   // token e, the odd one of token e + 1.
-  constexpr int YROW = 2 * BR + 32;                    // bytes of a token's row in LDS
-  static_assert(BT * YROW <= 3 * XB + 2 * WBUF, "the tile fits");
   const bool odd = lane & 1;
   const uint32_t sel = odd ? 0x03020706u : 0x05040100u;
 #pragma unroll
@@ -522,19 +474,13 @@ __global__ __launch_bounds__(256) void stage_x(const T* __restrict__ x, int64_t 
   }
 }
 
-template <bool I8, int BT, int BR, int WT, int WR, bool PLAIN>
-void launch_mode(const PromptArgs& p, int mode, int splits, hipStream_t st) {
-  const dim3 grid((unsigned)((p.tiles_t * p.tiles_r + 7) / 8 * 8), (unsigned)splits);
-  const int nt = 64 * WT * WR;
-  if (mode == 0) prompt_tiles<I8, BT, BR, WT, WR, 0, PLAIN><<<grid, nt, 0, st>>>(p);
-  else if (mode == 1) prompt_tiles<I8, BT, BR, WT, WR, 1, PLAIN><<<grid, nt, 0, st>>>(p);
-  else prompt_tiles<I8, BT, BR, WT, WR, 2, PLAIN><<<grid, nt, 0, st>>>(p);
-}
-
 template <bool I8, int BT, int BR, int WT, int WR>
 void launch_tiles(const PromptArgs& p, int mode, int splits, hipStream_t st) {
-  if (!p.zeros && p.n_out == 0) launch_mode<I8, BT, BR, WT, WR, true>(p, mode, splits, st);
-  else launch_mode<I8, BT, BR, WT, WR, false>(p, mode, splits, st);
+  const dim3 grid((unsigned)((p.tiles_t * p.tiles_r + 7) / 8 * 8), (unsigned)splits);
+  const int nt = 64 * WT * WR;
+  if (mode == 0) prompt_tiles<I8, BT, BR, WT, WR, 0><<<grid, nt, 0, st>>>(p);
+  else if (mode == 1) prompt_tiles<I8, BT, BR, WT, WR, 1><<<grid, nt, 0, st>>>(p);
+  else prompt_tiles<I8, BT, BR, WT, WR, 2><<<grid, nt, 0, st>>>(p);
 }
 
 }  // namespace
@@ -565,6 +511,9 @@ PromptPlan prompt_plan(const void* x, int32_t xdtype, int64_t ntok, int64_t ldx,
     p.splits = std::max<int64_t>(1, std::min<int64_t>(512 / tiles, p.steps / 8));
   p.per = (p.steps + p.splits - 1) / p.splits;
   p.splits = (p.steps + p.per - 1) / p.per;
+  p.rows16 = (m + 15) / 16 * 16;
+  p.spread_bytes = (size_t)(p.rows16 * (p.steps / p.reps) * KB);
+  p.steps_bytes = (size_t)(p.rows16 * (n / G) * 4);
   p.partial_bytes = p.splits > 1 ? (size_t)p.splits * ntok * m * 4 : 0;
   // read in place: whole steps, aligned rows, and 256 of them within 32 bits
   const int64_t es = xdtype == PWQ_I8 ? 1 : (xdtype == PWQ_BF16 ? 2 : 4), xrow = ldx * es;
@@ -575,8 +524,8 @@ PromptPlan prompt_plan(const void* x, int32_t xdtype, int64_t ntok, int64_t ldx,
 }
 
 // staged / partial: workspace of the plan's sizes.
-hipError_t launch_prompt(const PackedLinearLaunch& a, const PromptPlan& pl, void* staged,
-                         void* partial, hipStream_t st) {
+hipError_t launch_prompt(const PackedLinearLaunch& a, const PromptPlan& pl, const PromptWs& w,
+                         hipStream_t st) {
   PromptArgs p{};
   const int64_t es = a.xdtype == PWQ_I8 ? 1 : (a.xdtype == PWQ_BF16 ? 2 : 4);
   const int64_t xrow = a.ldx * es;
@@ -586,7 +535,7 @@ hipError_t launch_prompt(const PackedLinearLaunch& a, const PromptPlan& pl, void
   } else {
     const int64_t units = pl.staged_row / pl.reps / (pl.i8 ? 8 : 16);
     const dim3 grid((unsigned)((a.ntok * units + 255) / 256));
-    char* o = (char*)staged;
+    char* o = (char*)w.staged;
     if (a.xdtype == PWQ_I8 && pl.i8)
       stage_x<int8_t, true><<<grid, 256, 0, st>>>((const int8_t*)a.x, a.ntok, a.n, a.ldx, o, units);
     else if (a.xdtype == PWQ_I8)
@@ -606,13 +555,10 @@ hipError_t launch_prompt(const PackedLinearLaunch& a, const PromptPlan& pl, void
   p.tiles_t = (int)pl.tiles_t;
   p.tiles_r = (int)pl.tiles_r;
   p.x_scales = a.x_scales;
-  p.qweight = a.qweight;
-  p.ldq = a.ldq;
-  p.scales = a.scales;
-  p.zeros = a.zeros;
-  p.off = a.outlier_off;
-  p.outliers = a.outliers;
-  p.n_out = a.outlier_off ? (int)a.n_out : 0;
+  p.spread = (const i32x4_t*)w.spread;
+  p.blocks = (int)(pl.steps / pl.reps);
+  p.steps_t = w.steps;
+  p.rows16 = pl.rows16;
   p.ntok = (int)a.ntok;
   p.m = (int)a.m;
   p.n = (int)a.n;
@@ -621,7 +567,20 @@ hipError_t launch_prompt(const PackedLinearLaunch& a, const PromptPlan& pl, void
   p.y = a.y;
   p.ydtype = a.ydtype;
   p.ldy = a.ldy;
-  p.partial = pl.splits > 1 ? (float*)partial : nullptr;
+  p.partial = pl.splits > 1 ? (float*)w.partial : nullptr;
+  {
+    const int across = (int)((a.n + 127) / 128), n_out = a.outlier_off ? (int)a.n_out : 0;
+    const int64_t tiles = pl.rows16 / 16 * across;
+    const dim3 grid((unsigned)((tiles + 3) / 4));
+    if (pl.i8)
+      spread_weights<true><<<grid, 256, 0, st>>>(
+          a.qweight, a.ldq, a.scales, a.zeros, a.outlier_off, a.outliers, n_out, a.m, p.n, p.G,
+          p.ng, across, tiles, (i32x4_t*)w.spread, p.blocks, w.steps, pl.rows16);
+    else
+      spread_weights<false><<<grid, 256, 0, st>>>(
+          a.qweight, a.ldq, a.scales, a.zeros, a.outlier_off, a.outliers, n_out, a.m, p.n, p.G,
+          p.ng, across, tiles, (i32x4_t*)w.spread, p.blocks, w.steps, pl.rows16);
+  }
   if (pl.big) {
     if (pl.i8) launch_tiles<true, 256, 256, 2, 4>(p, pl.mode, (int)pl.splits, st);
     else launch_tiles<false, 256, 256, 2, 4>(p, pl.mode, (int)pl.splits, st);

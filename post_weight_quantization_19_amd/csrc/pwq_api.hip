@@ -938,7 +938,7 @@ pwq_status pwq_rms_norm(const void* x, int32_t xdtype, int64_t ntok, int64_t n, 
 struct LinearPlan {
   bool rows = false;        // few tokens
   PromptPlan prompt{};      // .ok: many tokens; neither: any shape
-  size_t staged = 0, partial = 0;
+  size_t staged = 0;
 };
 static LinearPlan linear_plan(const void* x, int32_t xdtype, int64_t ntok, int64_t ldx, int64_t m,
                               int64_t n, int32_t G) {
@@ -950,14 +950,15 @@ static LinearPlan linear_plan(const void* x, int32_t xdtype, int64_t ntok, int64
   } else {
     p.prompt = prompt_plan(x, xdtype, ntok, ldx, m, n, G);
     p.staged = p.prompt.staged_bytes;
-    p.partial = p.prompt.partial_bytes;
   }
   return p;
 }
 
-static void carve_linear(Carver& c, const LinearPlan& p, void** staged, void** partial) {
-  *staged = p.staged ? c.take(p.staged) : nullptr;
-  *partial = p.partial ? c.take(p.partial) : nullptr;
+static void carve_linear(Carver& c, const LinearPlan& p, PromptWs* w) {
+  w->staged = p.staged ? c.take(p.staged) : nullptr;
+  w->spread = p.prompt.ok ? c.take(p.prompt.spread_bytes) : nullptr;
+  w->steps = p.prompt.ok ? (float*)c.take(p.prompt.steps_bytes) : nullptr;
+  w->partial = p.prompt.partial_bytes ? c.take(p.prompt.partial_bytes) : nullptr;
 }
 
 size_t pwq_packed_linear_workspace_size(const void* x, int32_t xdtype, int64_t ntok, int64_t ldx,
@@ -965,9 +966,8 @@ size_t pwq_packed_linear_workspace_size(const void* x, int32_t xdtype, int64_t n
   if (ntok < 0 || m < 0 || n <= 0 || ntok > INT32_MAX || m > INT32_MAX || n > INT32_MAX) return 0;
   if (group < 0 || (group > 0 && n % group) || ldx < n) return 0;
   Carver c(nullptr);
-  void *staged, *partial;
-  carve_linear(c, linear_plan(x, xdtype, ntok, ldx, m, n, group > 0 ? group : (int32_t)n),
-               &staged, &partial);
+  PromptWs w;
+  carve_linear(c, linear_plan(x, xdtype, ntok, ldx, m, n, group > 0 ? group : (int32_t)n), &w);
   return c.size();
 }
 
@@ -1006,13 +1006,13 @@ pwq_status pwq_packed_linear(const void* x, int32_t xdtype, int64_t ntok, int64_
                        outliers, n_out, y, ydtype, ldy, 0, 0, 0, 0, 0};
   const LinearPlan p = linear_plan(x, xdtype, ntok, ldx, m, n, a.G);
   Carver c(ws);
-  void *staged, *partial;
-  carve_linear(c, p, &staged, &partial);
+  PromptWs w;
+  carve_linear(c, p, &w);
   hipStream_t st = (hipStream_t)stream;
   hipError_t e = hipSuccess;
   if (ntok > 0 && m > 0)
-    e = p.rows ? launch_rows(a, staged, st)
-               : (p.prompt.ok ? launch_prompt(a, p.prompt, staged, partial, st)
+    e = p.rows ? launch_rows(a, w.staged, st)
+               : (p.prompt.ok ? launch_prompt(a, p.prompt, w, st)
                               : launch_linear_any(a, st));
   if (e != hipSuccess) return hip_fail(e, "packed_linear launch");
   return ok();

@@ -211,18 +211,22 @@ constexpr int64_t kRowsTokens = 16;
 bool rows_ok(int64_t ntok, int64_t n, int32_t G);
 size_t rows_staged_bytes(const void* x, int32_t xdtype, int64_t ntok, int64_t n, int64_t ldx);
 hipError_t launch_rows(PackedLinearLaunch a, void* staged, hipStream_t st);
-// Many tokens: the plan depends on the sizes alone, its workspace is
-// staged_bytes + partial_bytes.
+// Many tokens: what the product is made of, and its workspace.
 struct PromptPlan {
   bool ok, i8, big, direct;
   int mode, reps;
-  int64_t steps, per, splits, tiles_t, tiles_r, staged_row;
-  size_t staged_bytes, partial_bytes;
+  int64_t steps, per, splits, tiles_t, tiles_r, staged_row, rows16;
+  size_t staged_bytes, spread_bytes, steps_bytes, partial_bytes;
+};
+struct PromptWs {
+  void *staged, *spread;
+  float* steps;
+  void* partial;
 };
 PromptPlan prompt_plan(const void* x, int32_t xdtype, int64_t ntok, int64_t ldx, int64_t m,
                        int64_t n, int32_t G);
-hipError_t launch_prompt(const PackedLinearLaunch& a, const PromptPlan& p, void* staged,
-                         void* partial, hipStream_t st);
+hipError_t launch_prompt(const PackedLinearLaunch& a, const PromptPlan& p, const PromptWs& w,
+                         hipStream_t st);
 
 // Event pairs recorded around launches of one kernel (pwq_kernel_timer_attach).
 struct KernelTimer {
