@@ -499,18 +499,38 @@ PromptPlan prompt_plan(const void* x, int32_t xdtype, int64_t ntok, int64_t ldx,
   p.reps = xdtype == PWQ_F32 ? 3 : 1;
   p.steps = (n + cols - 1) / cols * p.reps;
   p.staged_row = p.steps * KB;
-  p.big = ntok > 128 && m > 128 && ((ntok + 255) / 256) * ((m + 255) / 256) >= 192;
-  const int64_t edge = p.big ? 256 : 128;
-  p.tiles_t = (ntok + edge - 1) / edge;
-  p.tiles_r = (m + edge - 1) / edge;
-  // too few tiles for 256 CUs (512 workgroups of the small tile): split the
-  // columns, at least 4 steps a split
-  const int64_t tiles = p.tiles_t * p.tiles_r;
-  p.splits = 1;
-  if (!p.big && tiles < 256)
-    p.splits = std::max<int64_t>(1, std::min<int64_t>(512 / tiles, p.steps / 8));
-  p.per = (p.steps + p.splits - 1) / p.splits;
-  p.splits = (p.steps + p.per - 1) / p.per;
+  // Tile and column splits by their estimated time.  A step takes about
+  // the same whether a CU runs one 128 x 128 tile or two (1.2 to 1.3 us), and
+  // 2.1 us for one of 256 x 256 (bf16; 8-bit steps have twice the columns and
+  // more to multiply by the steps: 1.7 and 2.7 us, twice a step 2.2 and 3.6);
+  // the splits' float32 sums are written and read once at about 4.5 TB/s and
+  // joined by a launch of its own (3 us).  Measured where the two differ most:
+  // 1025 bf16 tokens of 4096 x 14336 213 us as 80 large tiles in 3 splits, 286
+  // as 288 small ones; 512 8-bit tokens of 4096 x 4096 39 us as 128 small
+  // tiles in 4 splits, 47 as 32 large ones in 4.
+  const double us_small = !p.i8 ? 1.3 : (p.mode == 2 ? 2.2 : 1.7);
+  const double us_big = !p.i8 ? 2.1 : (p.mode == 2 ? 3.6 : 2.7);
+  double best = 0;
+  for (int big = 0; big < 2; ++big) {
+    const int64_t edge = big ? 256 : 128, slots = big ? 256 : 512;
+    const int64_t tt = (ntok + edge - 1) / edge, tr = (m + edge - 1) / edge;
+    const int64_t most = std::min<int64_t>(16, std::max<int64_t>(1, p.steps / 4));
+    for (int64_t k = 1; k <= most; ++k) {
+      const int64_t per = (p.steps + k - 1) / k, splits = (p.steps + per - 1) / per;
+      if (splits != k) continue;
+      const int64_t rounds = (tt * tr * splits + slots - 1) / slots;
+      double us = (double)rounds * per * (big ? us_big : us_small);
+      if (splits > 1) us += 3.0 + 2.0 * splits * ntok * m * 4 / 4.5e6;
+      if (best == 0 || us < best) {
+        best = us;
+        p.big = big;
+        p.tiles_t = tt;
+        p.tiles_r = tr;
+        p.per = per;
+        p.splits = splits;
+      }
+    }
+  }
   p.rows16 = (m + 15) / 16 * 16;
   p.spread_bytes = (size_t)(p.rows16 * (p.steps / p.reps) * KB);
   p.steps_bytes = (size_t)(p.rows16 * (n / G) * 4);
