@@ -105,15 +105,15 @@ pwq_status pwq_rms_norm(const void* x, int32_t xdtype, int64_t ntok, int64_t n, 
  *               code overflows.  n_out = outlier_off[tiles].
  *   group     : G, 0 for one step per row; divides n.
  *   y         : out, ntok x m, row stride ldy >= m, ydtype PWQ_F32 or PWQ_BF16.
- *   ws        : pwq_packed_linear_workspace_size bytes, for this x, sizes and
- *               group (0 for few tokens whose rows of x are 16-byte aligned).
+ *   ws        : pwq_packed_linear_workspace_size bytes, for this x, sizes,
+ *               group and n_out (0 for few tokens whose rows of x are 16-byte aligned).
  * Steps c - z multiply x as integers and a group's sum is multiplied by its
  * step: sums are int32 (PWQ_I8) or float32 within a group and float32 over
  * the groups, in a fixed order.  A token with an infinity or NaN gives values
  * that are not finite; other tokens are unaffected.
  * ---------------------------------------------------------------------- */
 size_t pwq_packed_linear_workspace_size(const void* x, int32_t xdtype, int64_t ntok, int64_t ldx,
-                                        int64_t m, int64_t n, int32_t group);
+                                        int64_t m, int64_t n, int32_t group, int64_t n_out);
 pwq_status pwq_packed_linear(const void* x, int32_t xdtype, int64_t ntok, int64_t ldx,
                              const float* x_scales, const uint8_t* qweight, int64_t m, int64_t n,
                              const float* scales, const uint8_t* zeros, int32_t group,

@@ -660,7 +660,7 @@ def packed_linear(x: torch.Tensor, packed: dict, x_scales: Optional[torch.Tensor
         if status != _lib.PWQ_ERR_WORKSPACE or ws is not None:
             break
         ws = _workspace(L_.pwq_packed_linear_workspace_size(x.data_ptr(), xdt, ntok, ldx, m, n,
-                                                            group), x.device)
+                                                            group, n_out), x.device)
         nb = ws.numel()
     if status:
         check(status)

@@ -105,7 +105,7 @@ _SIGS = {
                                  _vp]),
     "pwq_rms_norm": (_i32, [_vp, _i32, _i64, _i64, _i64, _vp, _i64, _vp, _i32, _f64, _vp, _i64,
                             _vp, _i32, _i64, _vp, _vp]),
-    "pwq_packed_linear_workspace_size": (_sz, [_vp, _i32, _i64, _i64, _i64, _i64, _i32]),
+    "pwq_packed_linear_workspace_size": (_sz, [_vp, _i32, _i64, _i64, _i64, _i64, _i32, _i64]),
     "pwq_packed_linear": (_i32, [_vp, _i32, _i64, _i64, _vp, _vp, _i64, _i64, _vp, _vp, _i32,
                                  _vp, _vp, _i64, _vp, _i32, _i64, _vp, _sz, _vp]),
     "pwq_kernel_timer_attach": (_i32, [_i32, _vp, _vp, _i64]),

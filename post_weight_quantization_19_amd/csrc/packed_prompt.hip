@@ -32,6 +32,7 @@ typedef __attribute__((__vector_size__(4 * sizeof(int)))) int i32x4_t;
 typedef __attribute__((address_space(3))) char lds_char;
 
 constexpr int KB = 128;            // bytes of an x row per step
+constexpr int64_t kFusedTokens = 128;
 
 // Asynchronous copy of 16 bytes per lane, sbase + voff of each lane to
 // lds + 16 lane (lds and sbase wave-uniform).  M0 is restored.
@@ -62,6 +63,27 @@ __device__ __forceinline__ uint2 steps_i8(uint32_t w, uint32_t z4) {
                     __builtin_amdgcn_perm(odd, even, 0x07030602u));
 }
 
+// ... to bf16: a code's four bits are put at the top of the mantissa of 16,
+// and 16 + z is subtracted in float32, whose upper half holds the difference
+// exactly (no conversion instruction: those run at a quarter of the rate).
+// zb = 16 + z, or 24 with `bias` 0x41c0 for signed halves (it flips their top
+// bit; 0x4180 otherwise).
+__device__ __forceinline__ uint4 steps_bf16(uint32_t w, uint32_t bias, float zb) {
+  constexpr uint32_t M = 0x00780078u;
+  const uint32_t c[4] = {((w << 3) & M) ^ bias, ((w >> 1) & M) ^ bias, ((w >> 5) & M) ^ bias,
+                         ((w >> 9) & M) ^ bias};            // columns i and i + 4
+  float lo[4], hi[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    lo[i] = __uint_as_float(c[i] << 16) - zb;
+    hi[i] = __uint_as_float(c[i] & 0xffff0000u) - zb;
+  }
+  auto two = [](float x, float y) {
+    return __builtin_amdgcn_perm(__float_as_uint(y), __float_as_uint(x), 0x07060302u);
+  };
+  return make_uint4(two(lo[0], lo[1]), two(lo[2], lo[3]), two(hi[0], hi[1]), two(hi[2], hi[3]));
+}
+
 // 1.5 2^23 as an integer: int32 sums below 2^22 that start here read as
 // 1.5 2^23 + sum when taken for a float32.
 constexpr int kMagic = 0x4b400000;
@@ -74,6 +96,11 @@ struct PromptArgs {
   int per;                // steps per split
   int tiles_t, tiles_r;
   const float* x_scales;
+  // packed weights (FUSED)
+  const uint8_t* qweight;
+  int64_t ldq;
+  const float* scales;
+  const uint8_t* zeros;
   const i32x4_t* spread;  // [strip of 16 rows][weight block][half][lane]
   int blocks;             // weight blocks (steps / reps)
   const float* steps_t;   // [group][16 strips' rows], times what the operands leave out
@@ -158,7 +185,9 @@ __global__ __launch_bounds__(256) void spread_weights(
 
 // MODE: how often sums are multiplied by their step.  0: one step per row,
 // at the end; 1: every step (G a multiple of its columns); 2: twice a step.
-template <bool I8, int BT, int BR, int WT, int WR, int MODE>
+// FUSED: packed weights are read and spread by the wave that multiplies by
+// them.
+template <bool I8, int BT, int BR, int WT, int WR, int MODE, bool FUSED>
 __global__ __launch_bounds__(64 * WT * WR) void prompt_tiles(const PromptArgs a) {
   constexpr int NT = 64 * WT * WR;
   constexpr int NI = BT / WT / 16, NJ = BR / WR / 16;
@@ -211,25 +240,81 @@ __global__ __launch_bounds__(64 * WT * WR) void prompt_tiles(const PromptArgs a)
     return min(r0 / 16 + wr * NJ + j, (int)(a.rows16 / 16) - 1);
   };
   constexpr int NS = MODE == 2 ? 2 : 1;
+  // 16-byte unit of an LDS row that lane group lq of half h works on.  FUSED:
+  // both halves' packed codes next to each other in memory, unless a half has
+  // to stay within a group of its own.
+  constexpr bool PAIRED = FUSED && MODE != 2;
+  auto unit = [&](int h) { return PAIRED ? 2 * lq + h : 4 * h + lq; };
+  constexpr int PB = I8 ? 8 : 4;               // packed bytes of a lane's half
   struct Weights {
-    i32x4_t w[NJ][2];
+    i32x4_t w[FUSED ? 1 : NJ][FUSED ? 1 : 2];
+    uint32_t p[FUSED ? NJ : 1][FUSED ? PB / 2 : 1];   // FUSED: both halves' codes
     float s[NJ][NS];
+    int z[FUSED ? NJ : 1][NS];
   };
+  uint32_t row[NJ];                            // of the tile, the lane's in block j
+#pragma unroll
+  for (int j = 0; j < NJ; ++j) row[j] = (uint32_t)(min(r0 + 16 * (wr * NJ + j) + lr, a.m - 1) - r0);
+  const uint8_t* const qbase = FUSED ? a.qweight + r0 * a.ldq : nullptr;
+  const float* const sbase = FUSED ? a.scales + (int64_t)r0 * a.ng : nullptr;
+  // (SYM reads the steps' bytes in the zero points' place and uses 8)
+  const bool asym = FUSED && a.zeros != nullptr;
+  const uint8_t* const zbase = asym ? a.zeros + (int64_t)r0 * a.ng : (const uint8_t*)sbase;
   auto load_w = [&](Weights& b, int s) {
     const int blk = s / a.reps;
+    if constexpr (FUSED) {
 #pragma unroll
-    for (int j = 0; j < NJ; ++j)
+      for (int j = 0; j < NJ; ++j) {
+        const uint32_t at = row[j] * (uint32_t)a.ldq;
+        if constexpr (PAIRED) {
+          const uint32_t o = blk * (COLS / 2) + 2 * PB * lq;
+          __builtin_memcpy(b.p[j], qbase + (at + (o < a.ldq ? o : 0)), 2 * PB);
+        } else {
 #pragma unroll
-      for (int h = 0; h < 2; ++h)
-        b.w[j][h] = (a.spread + ((int64_t)strip(j) * a.blocks + blk) * 128 + 64 * h)[(uint32_t)lane];
-    if constexpr (MODE != 0)
+          for (int h = 0; h < 2; ++h) {
+            const uint32_t o = blk * (COLS / 2) + 4 * PB * h + PB * lq;
+            __builtin_memcpy(&b.p[j][h * (PB / 4)], qbase + (at + (o < a.ldq ? o : 0)), PB);
+          }
+        }
 #pragma unroll
-      for (int h = 0; h < NS; ++h) {
-        const int g = min((blk * COLS + h * (COLS / 2)) / a.G, a.ng - 1);
-#pragma unroll
-        for (int j = 0; j < NJ; ++j)
-          b.s[j][h] = (a.steps_t + g * a.rows16 + 16 * strip(j))[(uint32_t)lr];
+        for (int h = 0; h < NS; ++h) {
+          const int g = MODE == 0 ? 0 : min((blk * COLS + h * (COLS / 2)) / a.G, a.ng - 1);
+          b.s[j][h] = sbase[row[j] * a.ng + g];
+          b.z[j][h] = zbase[row[j] * a.ng + g];
+        }
       }
+    } else {
+#pragma unroll
+      for (int j = 0; j < NJ; ++j)
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+          b.w[j][h] =
+              (a.spread + ((int64_t)strip(j) * a.blocks + blk) * 128 + 64 * h)[(uint32_t)lane];
+      if constexpr (MODE != 0)
+#pragma unroll
+        for (int h = 0; h < NS; ++h) {
+          const int g = min((blk * COLS + h * (COLS / 2)) / a.G, a.ng - 1);
+#pragma unroll
+          for (int j = 0; j < NJ; ++j)
+            b.s[j][h] = (a.steps_t + g * a.rows16 + 16 * strip(j))[(uint32_t)lr];
+        }
+    }
+  };
+  const uint32_t flip = asym ? 0u : 0x88888888u, bias = asym ? 0x41804180u : 0x41c041c0u;
+  auto operand = [&](const Weights& b, int j, int h) -> i32x4_t {
+    if constexpr (!FUSED) {
+      return b.w[j][h];
+    } else {
+      const int z = asym ? b.z[j][NS == 2 ? h : 0] : 8;
+      if constexpr (I8) {
+        const uint32_t z4 = (uint32_t)z * 0x01010101u;
+        const uint2 lo = steps_i8(b.p[j][2 * h] ^ flip, z4);
+        const uint2 hi = steps_i8(b.p[j][2 * h + 1] ^ flip, z4);
+        return i32x4_t{(int)lo.x, (int)lo.y, (int)hi.x, (int)hi.y};
+      } else {
+        return __builtin_bit_cast(i32x4_t, steps_bf16(b.p[j][h], bias, 16.0f + (float)z));
+      }
+    }
   };
 
   float acc[NI][NJ][4];
@@ -274,12 +359,16 @@ __global__ __launch_bounds__(64 * WT * WR) void prompt_tiles(const PromptArgs a)
     load_w(bn, min(s + 1, last));
     const char* xs = smem + s % 3 * XB;
     i32x4_t x[2][2];
-    i32x4_t(&w)[NJ][2] = b.w;
+    i32x4_t w[NJ][2];
+#pragma unroll
+    for (int j = 0; j < NJ; ++j)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) w[j][h] = operand(b, j, h);
     float(&sc)[NJ][NS] = b.s;
     auto read_x = [&](int i) {
 #pragma unroll
       for (int h = 0; h < 2; ++h)
-        x[i & 1][h] = *(const i32x4_t*)(xs + unit_at(16 * (wt * NI + i) + lr, 4 * h + lq));
+        x[i & 1][h] = *(const i32x4_t*)(xs + unit_at(16 * (wt * NI + i) + lr, unit(h)));
     };
     read_x(0);
     if constexpr (MODE == 0) {
@@ -311,7 +400,7 @@ __global__ __launch_bounds__(64 * WT * WR) void prompt_tiles(const PromptArgs a)
         constexpr int i = u / NS / NJ, j = u / NS % NJ, h = u % NS;
         if constexpr (u < NU) {
           c[u & 3] = mma(x[i & 1][h], w[j][h], zero);
-          if constexpr (j == 1 && h == 0 && i + 1 < NI) read_x(i + 1);
+          if constexpr (j == (NJ > 1) && h == 0 && i + 1 < NI) read_x(i + 1);
         }
         if constexpr (u >= 3) scale(std::integral_constant<int, u - 3>{}, 0);
         __builtin_amdgcn_sched_barrier(0);
@@ -336,7 +425,7 @@ __global__ __launch_bounds__(64 * WT * WR) void prompt_tiles(const PromptArgs a)
   if constexpr (MODE == 0) {
 #pragma unroll
     for (int j = 0; j < NJ; ++j) {
-      const float sj = a.steps_t[16 * strip(j) + lr];
+      const float sj = FUSED ? sbase[row[j] * a.ng] : a.steps_t[16 * strip(j) + lr];
 #pragma unroll
       for (int i = 0; i < NI; ++i)
 #pragma unroll
@@ -474,13 +563,13 @@ __global__ __launch_bounds__(256) void stage_x(const T* __restrict__ x, int64_t 
   }
 }
 
-template <bool I8, int BT, int BR, int WT, int WR>
+template <bool I8, int BT, int BR, int WT, int WR, bool FUSED>
 void launch_tiles(const PromptArgs& p, int mode, int splits, hipStream_t st) {
   const dim3 grid((unsigned)((p.tiles_t * p.tiles_r + 7) / 8 * 8), (unsigned)splits);
   const int nt = 64 * WT * WR;
-  if (mode == 0) prompt_tiles<I8, BT, BR, WT, WR, 0><<<grid, nt, 0, st>>>(p);
-  else if (mode == 1) prompt_tiles<I8, BT, BR, WT, WR, 1><<<grid, nt, 0, st>>>(p);
-  else prompt_tiles<I8, BT, BR, WT, WR, 2><<<grid, nt, 0, st>>>(p);
+  if (mode == 0) prompt_tiles<I8, BT, BR, WT, WR, 0, FUSED><<<grid, nt, 0, st>>>(p);
+  else if (mode == 1) prompt_tiles<I8, BT, BR, WT, WR, 1, FUSED><<<grid, nt, 0, st>>>(p);
+  else prompt_tiles<I8, BT, BR, WT, WR, 2, FUSED><<<grid, nt, 0, st>>>(p);
 }
 
 }  // namespace
@@ -488,7 +577,7 @@ void launch_tiles(const PromptArgs& p, int mode, int splits, hipStream_t st) {
 // What prompt_tiles makes of a product: 8-bit or bf16 operands, steps, tile,
 // splits and workspace.
 PromptPlan prompt_plan(const void* x, int32_t xdtype, int64_t ntok, int64_t ldx, int64_t m,
-                       int64_t n, int32_t G) {
+                       int64_t n, int32_t G, int64_t n_out) {
   PromptPlan p{};
   const bool row = G == n;
   p.ok = (row || G % 32 == 0) && ntok > 0 && m > 0;
@@ -511,7 +600,17 @@ PromptPlan prompt_plan(const void* x, int32_t xdtype, int64_t ntok, int64_t ldx,
   const double us_small = !p.i8 ? 1.3 : (p.mode == 2 ? 2.2 : 1.7);
   const double us_big = !p.i8 ? 2.1 : (p.mode == 2 ? 3.6 : 2.7);
   double best = 0;
-  for (int big = 0; big < 2; ++big) {
+  p.fused = n_out == 0 && ntok <= kFusedTokens;
+  if (p.fused) {
+    // 64 x 128 tiles, four workgroups a CU; splits of at least 4 steps
+    p.tiles_t = (ntok + 63) / 64;
+    p.tiles_r = (m + 127) / 128;
+    const int64_t tiles = p.tiles_t * p.tiles_r;
+    p.splits = std::max<int64_t>(1, std::min<int64_t>(1024 / tiles, p.steps / 4));
+    p.per = (p.steps + p.splits - 1) / p.splits;
+    p.splits = (p.steps + p.per - 1) / p.per;
+  }
+  for (int big = 0; big < 2 && !p.fused; ++big) {
     const int64_t edge = big ? 256 : 128, slots = big ? 256 : 512;
     const int64_t tt = (ntok + edge - 1) / edge, tr = (m + edge - 1) / edge;
     const int64_t most = std::min<int64_t>(16, std::max<int64_t>(1, p.steps / 4));
@@ -532,8 +631,8 @@ PromptPlan prompt_plan(const void* x, int32_t xdtype, int64_t ntok, int64_t ldx,
     }
   }
   p.rows16 = (m + 15) / 16 * 16;
-  p.spread_bytes = (size_t)(p.rows16 * (p.steps / p.reps) * KB);
-  p.steps_bytes = (size_t)(p.rows16 * (n / G) * 4);
+  p.spread_bytes = p.fused ? 0 : (size_t)(p.rows16 * (p.steps / p.reps) * KB);
+  p.steps_bytes = p.fused ? 0 : (size_t)(p.rows16 * (n / G) * 4);
   p.partial_bytes = p.splits > 1 ? (size_t)p.splits * ntok * m * 4 : 0;
   // read in place: whole steps, aligned rows, and 256 of them within 32 bits
   const int64_t es = xdtype == PWQ_I8 ? 1 : (xdtype == PWQ_BF16 ? 2 : 4), xrow = ldx * es;
@@ -575,6 +674,10 @@ hipError_t launch_prompt(const PackedLinearLaunch& a, const PromptPlan& pl, cons
   p.tiles_t = (int)pl.tiles_t;
   p.tiles_r = (int)pl.tiles_r;
   p.x_scales = a.x_scales;
+  p.qweight = a.qweight;
+  p.ldq = a.ldq;
+  p.scales = a.scales;
+  p.zeros = a.zeros;
   p.spread = (const i32x4_t*)w.spread;
   p.blocks = (int)(pl.steps / pl.reps);
   p.steps_t = w.steps;
@@ -588,7 +691,7 @@ hipError_t launch_prompt(const PackedLinearLaunch& a, const PromptPlan& pl, cons
   p.ydtype = a.ydtype;
   p.ldy = a.ldy;
   p.partial = pl.splits > 1 ? (float*)w.partial : nullptr;
-  {
+  if (!pl.fused) {
     const int across = (int)((a.n + 127) / 128), n_out = a.outlier_off ? (int)a.n_out : 0;
     const int64_t tiles = pl.rows16 / 16 * across;
     const dim3 grid((unsigned)((tiles + 3) / 4));
@@ -601,12 +704,16 @@ hipError_t launch_prompt(const PackedLinearLaunch& a, const PromptPlan& pl, cons
           a.qweight, a.ldq, a.scales, a.zeros, a.outlier_off, a.outliers, n_out, a.m, p.n, p.G,
           p.ng, across, tiles, (i32x4_t*)w.spread, p.blocks, w.steps, pl.rows16);
   }
-  if (pl.big) {
-    if (pl.i8) launch_tiles<true, 256, 256, 2, 4>(p, pl.mode, (int)pl.splits, st);
-    else launch_tiles<false, 256, 256, 2, 4>(p, pl.mode, (int)pl.splits, st);
+  const int mode = pl.mode, k = (int)pl.splits;
+  if (pl.fused) {
+    if (pl.i8) launch_tiles<true, 64, 128, 1, 4, true>(p, mode, k, st);
+    else launch_tiles<false, 64, 128, 1, 4, true>(p, mode, k, st);
+  } else if (pl.big) {
+    if (pl.i8) launch_tiles<true, 256, 256, 2, 4, false>(p, mode, k, st);
+    else launch_tiles<false, 256, 256, 2, 4, false>(p, mode, k, st);
   } else {
-    if (pl.i8) launch_tiles<true, 128, 128, 2, 2>(p, pl.mode, (int)pl.splits, st);
-    else launch_tiles<false, 128, 128, 2, 2>(p, pl.mode, (int)pl.splits, st);
+    if (pl.i8) launch_tiles<true, 128, 128, 2, 2, false>(p, mode, k, st);
+    else launch_tiles<false, 128, 128, 2, 2, false>(p, mode, k, st);
   }
   if (p.partial)
     prompt_join<<<dim3((unsigned)((a.ntok * a.m + 255) / 256)), 256, 0, st>>>(

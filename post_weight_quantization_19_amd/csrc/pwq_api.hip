@@ -941,14 +941,14 @@ struct LinearPlan {
   size_t staged = 0;
 };
 static LinearPlan linear_plan(const void* x, int32_t xdtype, int64_t ntok, int64_t ldx, int64_t m,
-                              int64_t n, int32_t G) {
+                              int64_t n, int32_t G, int64_t n_out) {
   LinearPlan p;
   if (ntok == 0 || m == 0) return p;
   p.rows = rows_ok(ntok, n, G);
   if (p.rows) {
     p.staged = rows_staged_bytes(x, xdtype, ntok, n, ldx);
   } else {
-    p.prompt = prompt_plan(x, xdtype, ntok, ldx, m, n, G);
+    p.prompt = prompt_plan(x, xdtype, ntok, ldx, m, n, G, n_out);
     p.staged = p.prompt.staged_bytes;
   }
   return p;
@@ -956,18 +956,18 @@ static LinearPlan linear_plan(const void* x, int32_t xdtype, int64_t ntok, int64
 
 static void carve_linear(Carver& c, const LinearPlan& p, PromptWs* w) {
   w->staged = p.staged ? c.take(p.staged) : nullptr;
-  w->spread = p.prompt.ok ? c.take(p.prompt.spread_bytes) : nullptr;
-  w->steps = p.prompt.ok ? (float*)c.take(p.prompt.steps_bytes) : nullptr;
+  w->spread = p.prompt.spread_bytes ? c.take(p.prompt.spread_bytes) : nullptr;
+  w->steps = p.prompt.steps_bytes ? (float*)c.take(p.prompt.steps_bytes) : nullptr;
   w->partial = p.prompt.partial_bytes ? c.take(p.prompt.partial_bytes) : nullptr;
 }
 
 size_t pwq_packed_linear_workspace_size(const void* x, int32_t xdtype, int64_t ntok, int64_t ldx,
-                                        int64_t m, int64_t n, int32_t group) {
+                                        int64_t m, int64_t n, int32_t group, int64_t n_out) {
   if (ntok < 0 || m < 0 || n <= 0 || ntok > INT32_MAX || m > INT32_MAX || n > INT32_MAX) return 0;
   if (group < 0 || (group > 0 && n % group) || ldx < n) return 0;
   Carver c(nullptr);
   PromptWs w;
-  carve_linear(c, linear_plan(x, xdtype, ntok, ldx, m, n, group > 0 ? group : (int32_t)n), &w);
+  carve_linear(c, linear_plan(x, xdtype, ntok, ldx, m, n, group > 0 ? group : (int32_t)n, n_out), &w);
   return c.size();
 }
 
@@ -999,12 +999,12 @@ pwq_status pwq_packed_linear(const void* x, int32_t xdtype, int64_t ntok, int64_
       return fail(PWQ_ERR_INVALID_ARG, "qweight must be 16-byte aligned");
   }
   pwq_status s = check_ws(ws, ws_bytes,
-                          pwq_packed_linear_workspace_size(x, xdtype, ntok, ldx, m, n, group));
+                          pwq_packed_linear_workspace_size(x, xdtype, ntok, ldx, m, n, group, n_out));
   if (s != PWQ_OK) return s;
   PackedLinearLaunch a{x, xdtype, ntok, ldx, x_scales, qweight, m, n, packed_row_bytes(n), scales,
                        zeros, group > 0 ? group : (int32_t)n, n_out > 0 ? outlier_off : nullptr,
                        outliers, n_out, y, ydtype, ldy, 0, 0, 0, 0, 0};
-  const LinearPlan p = linear_plan(x, xdtype, ntok, ldx, m, n, a.G);
+  const LinearPlan p = linear_plan(x, xdtype, ntok, ldx, m, n, a.G, n_out);
   Carver c(ws);
   PromptWs w;
   carve_linear(c, p, &w);

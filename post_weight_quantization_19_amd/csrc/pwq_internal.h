@@ -213,7 +213,7 @@ size_t rows_staged_bytes(const void* x, int32_t xdtype, int64_t ntok, int64_t n,
 hipError_t launch_rows(PackedLinearLaunch a, void* staged, hipStream_t st);
 // Many tokens: what the product is made of, and its workspace.
 struct PromptPlan {
-  bool ok, i8, big, direct;
+  bool ok, i8, big, direct, fused;
   int mode, reps;
   int64_t steps, per, splits, tiles_t, tiles_r, staged_row, rows16;
   size_t staged_bytes, spread_bytes, steps_bytes, partial_bytes;
@@ -224,7 +224,7 @@ struct PromptWs {
   void* partial;
 };
 PromptPlan prompt_plan(const void* x, int32_t xdtype, int64_t ntok, int64_t ldx, int64_t m,
-                       int64_t n, int32_t G);
+                       int64_t n, int32_t G, int64_t n_out);
 hipError_t launch_prompt(const PackedLinearLaunch& a, const PromptPlan& p, const PromptWs& w,
                          hipStream_t st);
 
