@@ -587,13 +587,13 @@ def rms_norm(x: torch.Tensor, weight: torch.Tensor, residual: Optional[torch.Ten
             raise ValueError("residual must have x's shape and type")
         rp, ldr = residual.data_ptr(), _rows(residual, "residual")
         if total is None:
-            total = torch.empty((ntok, n), dtype=x.dtype, device=x.device)
+            total = torch.empty_like(x, memory_format=torch.contiguous_format)
         elif total.shape != x.shape or total.dtype is not x.dtype:
             raise ValueError("sum_out must have x's shape and type")
         tp, lds = total.data_ptr(), _rows(total, "sum_out")
     elif sum_out is not None:
         raise ValueError("sum_out goes with a residual")
-    y = torch.empty((ntok, n), dtype=odt, device=x.device)
+    y = torch.empty_like(x, dtype=odt, memory_format=torch.contiguous_format)
     scales, sp = None, None
     if ydt == _lib.PWQ_I8:
         scales = torch.empty(ntok, dtype=torch.float32, device=x.device)

@@ -77,6 +77,24 @@ __device__ __forceinline__ bf16x8_t codes_bf16(uint32_t w, uint32_t bias) {
                              ((w >> 9) & M) ^ bias);
   return __builtin_bit_cast(bf16x8_t, o);
 }
+// The same minus zb = 16 + z (24 for signed halves), in the columns' order:
+// the difference is taken in float32, whose upper half holds it exactly.
+// float32 x takes these: next to 16 + u, the correction by the sum of x costs
+// its result three bits.
+__device__ __forceinline__ bf16x8_t steps_bf16(uint32_t w, uint32_t bias, float zb) {
+  constexpr uint32_t M = 0x00780078u;
+  const uint32_t c[4] = {((w << 3) & M) ^ bias, ((w >> 1) & M) ^ bias, ((w >> 5) & M) ^ bias,
+                         ((w >> 9) & M) ^ bias};
+  float lo[4], hi[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    lo[i] = __uint_as_float(c[i] << 16) - zb;
+    hi[i] = __uint_as_float(c[i] & 0xffff0000u) - zb;
+  }
+  const uint4 o = make_uint4(pack_hi(lo[0], lo[1]), pack_hi(lo[2], lo[3]), pack_hi(hi[0], hi[1]),
+                             pack_hi(hi[2], hi[3]));
+  return __builtin_bit_cast(bf16x8_t, o);
+}
 // Eight 4-bit codes to bytes.  Unsigned: u - z (every byte is at least 128
 // before the subtraction, so no borrow passes one).  Signed: 16 times the
 // code, its four bits at the top of the byte.
@@ -146,6 +164,7 @@ __global__ __launch_bounds__(1024) void packed_rows(const PackedLinearLaunch a) 
   using T = typename XType<XK>::T;
   using acc_t = std::conditional_t<XK == X_I8, i32x4_t, f32x4_t>;
   constexpr int ES = sizeof(T);
+  constexpr bool BIASED = XK == X_BF16;
   constexpr int NB = 128 / GB, NC = GB / 4;     // blocks of a tile, columns of a lane in one
   constexpr int NW = NC / 8;                    // dwords of a lane per block
   constexpr int XROW = 128 * ES, UNITS = XROW / 16, RPC = 64 / UNITS;   // x rows per copy
@@ -281,7 +300,7 @@ __global__ __launch_bounds__(1024) void packed_rows(const PackedLinearLaunch a) 
           const uint32_t bias = asym ? 0x41804180u : 0x41c041c0u;
 #pragma unroll
           for (int j = 0; j < NW; ++j) {
-            const bf16x8_t f = codes_bf16(w[j], bias);
+            const bf16x8_t f = BIASED ? codes_bf16(w[j], bias) : steps_bf16(w[j], bias, -zf);
             const int col = GB * h + NC * lq + 8 * j;
             T xv[8];
             if constexpr (XK == X_BF16) {
@@ -293,11 +312,11 @@ __global__ __launch_bounds__(1024) void packed_rows(const PackedLinearLaunch a) 
               __builtin_memcpy(xv, x_unit(xs, col / 16) + col % 16, 8);
             }
             bf16x8_t v[kParts<XK>];
-            x_parts<XK, true>(xv, v);
+            x_parts<XK, BIASED>(xv, v);
 #pragma unroll
             for (int part = 0; part < kParts<XK>; ++part) {
               c = mma(v[part], f, c);
-              c1s = mma(v[part], ones, c1s);
+              if constexpr (BIASED) c1s = mma(v[part], ones, c1s);
             }
           }
         }
@@ -344,7 +363,7 @@ __global__ __launch_bounds__(1024) void packed_rows(const PackedLinearLaunch a) 
             if constexpr (OVER) v += asym ? ce[e] : 16 * ce[e];
             acc[e] = fmaf(s, (float)v, acc[e]);
           } else {
-            float v = fmaf(zf, c1s[e], c[e]);
+            float v = BIASED ? fmaf(zf, c1s[e], c[e]) : c[e];
             if constexpr (OVER) v += ce[e];
             acc[e] = fmaf(s, v, acc[e]);
           }
