@@ -362,3 +362,44 @@ def test_rms_norm_tokens_that_are_not_finite():
         y, s, _ = P.rms_norm(x, w, out_dtype=torch.int8)
         assert torch.isnan(s[[1, 3]]).all() and torch.all(y[[1, 3]] == 0)
         assert torch.equal(y[[0, 2, 4]], y0[[0, 2, 4]]) and torch.equal(s[[0, 2, 4]], s0[[0, 2, 4]])
+
+
+def test_quantized_layer_runs_end_to_end():
+    """Calibration to codes to packed layer to outputs, by the example's own
+    steps: the packed product is the product with the dequantized weights, and
+    its distance from the unquantized layer is what rounding W to those
+    weights gives (plus the 8-bit input's rounding)."""
+    import importlib.util
+    import os
+    path = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples",
+                        "packed_layer.py")
+    spec = importlib.util.spec_from_file_location("packed_layer", path)
+    ex = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(ex)
+    W, X, pk = ex.quantize(96, 256, 4096)
+    off = None if pk["outlier_off"] is None else pk["outlier_off"].cpu().numpy()
+    out = None if pk["outliers"] is None else pk["outliers"].cpu().numpy()
+    codes = S.unpack(pk["qweight"].cpu().numpy(), 256, True, off, out)
+    zeros, scales = pk["zeros"].cpu().numpy(), pk["scales"].cpu().numpy()
+    weight = torch.ones(256, device="cuda")
+    W64 = f64(W)
+    What = S.quantized_linear(np.eye(256), codes, scales, zeros)[0].T
+    for tokens in (1, 8, 40, 200):
+        for eight_bit in (False, True):
+            print(f"[serve] example {tokens} {eight_bit}", flush=True)
+            hidden, residual = X[:tokens], X[-tokens:]
+            y, steps, total = ex.layer_input(hidden, residual, weight, eight_bit)
+            got, total2 = ex.forward(pk, hidden, residual, weight, eight_bit)
+            assert torch.equal(total, total2)
+            check_linear(got, y, steps, codes, scales, zeros)
+            h = S.rms_norm(f64(hidden), f64(weight), f64(residual))[0]
+            want, rounded = h @ W64.T, h @ What.T
+            by_weights = np.linalg.norm(rounded - want) / np.linalg.norm(want)
+            err = ex.error_against_float(pk, W, hidden, residual, weight, eight_bit)
+            # the input's rounding, through the layer: half a step of 1 / 127 of the row's
+            # maximum in 8 bits, 2^-8 of each value in bf16; the output's: 2^-8 of it
+            dx = (np.max(np.abs(h), axis=1) / 254 * 16 if eight_bit
+                  else 2.0 ** -8 * np.linalg.norm(h, axis=1))
+            by_input = np.linalg.norm(dx) * np.linalg.norm(What, 2) / np.linalg.norm(want)
+            err = ex.error_against_float(pk, W, hidden, residual, weight, eight_bit)
+            assert err <= (by_weights + by_input) * (1 + 2.0 ** -8) + 2.0 ** -8 + 1e-5
