@@ -596,7 +596,7 @@ def rms_norm(x: torch.Tensor, weight: torch.Tensor, residual: Optional[torch.Ten
     y = torch.empty_like(x, dtype=odt, memory_format=torch.contiguous_format)
     scales, sp = None, None
     if ydt == _lib.PWQ_I8:
-        scales = torch.empty(ntok, dtype=torch.float32, device=x.device)
+        scales = x.new_empty(ntok, dtype=torch.float32)
         sp = scales.data_ptr()
     status = lib().pwq_rms_norm(x.data_ptr(), xdt, ntok, n, ldx, rp, ldr, wp, wdt, eps, tp, lds,
                                 y.data_ptr(), ydt, n, sp, _raw_stream(x))
@@ -646,7 +646,7 @@ def packed_linear(x: torch.Tensor, packed: dict, x_scales: Optional[torch.Tensor
     if odt is not torch.bfloat16 and odt is not torch.float32:
         raise TypeError(f"unsupported output dtype {odt}")
     if out is None:
-        out, ldy = torch.empty((ntok, m), dtype=odt, device=x.device), m
+        out, ldy = x.new_empty((ntok, m), dtype=odt), m
     else:
         if out.shape != (ntok, m) or out.dtype is not odt:
             raise ValueError(f"out must be [{ntok}, {m}] {odt}")

@@ -11,16 +11,27 @@
 //
 // Two kernels.  spread_weights writes the integers c - z (overflow entries
 // added) once per call in the operands' order, a wave's operand a contiguous
-// kilobyte; prompt_tiles multiplies.  Spreading inside the product instead
-// was measured: every token tile repeats it on the vector unit, which the
-// multiplication by the steps already fills (1025 bf16 tokens of down_proj
-// 355 us, 2048 of up_proj 333 us).
+// kilobyte; prompt_tiles multiplies.  Up to 128 tokens, where that writing
+// would cost more than the product, prompt_tiles reads the packed codes and
+// spreads them itself (FUSED; not with overflow entries, which would have to
+// be looked for in every lane's registers): q_proj 64 8-bit tokens 16 us
+// against 25, up_proj 32 bf16 tokens 33 against 60.  With more tokens every
+// tile of them would repeat it on the vector unit, which the multiplication
+// by the steps already fills (that way 2048 bf16 tokens of up_proj took 333 us
+// against 295).
 //
 // A step of prompt_tiles covers 128 bytes of every x row (128 8-bit or 64 bf16
 // columns).  x goes HBM -> LDS by asynchronous copies two steps ahead through
 // three slots; LDS rows are 128 bytes, their 16-byte units permuted by the row
 // so that 16 rows' reads of one column block cover every bank.  Weights go
 // straight to registers, a step ahead.
+//
+// What bounds it: the matrix unit at the clock that its power allows.  The
+// 256 x 256 tiles alone take 268 us for 2048 bf16 tokens of up_proj and 166 us
+// in 8 bits (0.90 and 1.45 P(FL)OP/s, 7 of 8 CUs busy over the two rounds of
+// 448 tiles); without the steps' multiplications 226 and 120 us, and without
+// any load of x or weights 245 and 161.  The library's products of the same
+// size take 207 us (bf16) and, at its 8192^3 rate, 115 us (8 bits).
 #include "pwq_internal.h"
 
 #include <algorithm>
@@ -580,9 +591,12 @@ PromptPlan prompt_plan(const void* x, int32_t xdtype, int64_t ntok, int64_t ldx,
                        int64_t n, int32_t G, int64_t n_out) {
   PromptPlan p{};
   const bool row = G == n;
-  p.ok = (row || G % 32 == 0) && ntok > 0 && m > 0;
+  // (256 rows of x within 32-bit offsets, three parts each)
+  p.ok = (row || G % 32 == 0) && ntok > 0 && m > 0 && n < (1 << 21);
   if (!p.ok) return p;
-  p.i8 = xdtype == PWQ_I8 && (row || G % 64 == 0);
+  // 8-bit operands: a group's sum is an int32, of at most 128 columns unless
+  // the whole row is one group (2^17 products of 128 x 127 fit)
+  p.i8 = xdtype == PWQ_I8 && (row ? n <= (1 << 17) : G % 64 == 0);
   const int cols = p.i8 ? 128 : 64;
   p.mode = row ? 0 : (G % cols == 0 ? 1 : 2);
   p.reps = xdtype == PWQ_F32 ? 3 : 1;

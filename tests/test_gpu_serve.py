@@ -114,6 +114,24 @@ def test_packed_linear_many_tiles(n, group, x_kind):
     check_linear(y, x, xs, codes, scales, zeros)
 
 
+@pytest.mark.parametrize("tokens", [1, 20, 200])
+@pytest.mark.parametrize("n,group", [(256, 128), (320, 64), (140032, 0)])
+def test_packed_linear_largest_integers(n, group, tokens):
+    """8-bit x of -128 against steps of -127: the sums of a group, and of a
+    row that is one group of 140032, at their largest.  All of it exact."""
+    m = 17
+    codes = np.zeros((m, n), np.int32)
+    zeros = np.full((m, n // (group or n)), 127, np.int32)
+    scales = np.full(zeros.shape, 0.5, np.float32)
+    pk = packed_layer(codes, scales, zeros, group)
+    x = torch.full((tokens, n), -128, dtype=torch.int8, device="cuda")
+    print(f"[serve] largest {n} {group} {tokens}", flush=True)
+    y = P.packed_linear(x, pk, x_scales=torch.ones(tokens, device="cuda"),
+                        out_dtype=torch.float32)
+    want = 0.5 * 128 * 127 * n
+    assert np.abs(f64(y) - want).max() <= want * (n / 16 + 32) * U
+
+
 def test_packed_linear_no_tokens_and_no_rows():
     rng = np.random.default_rng(1)
     codes, scales, zeros = layer(rng, 20, 64, 32, "asym", 0.0)
