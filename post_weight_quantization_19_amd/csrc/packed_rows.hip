@@ -29,7 +29,6 @@ namespace {
 
 typedef __attribute__((__vector_size__(4 * sizeof(int)))) int i32x4_t;
 typedef __attribute__((address_space(3))) char lds_char;
-struct __attribute__((packed, aligned(4))) vec16f { float v[4]; };
 
 enum { X_BF16 = 0, X_I8 = 1, X_F32 = 2, X_I8_BF16 = 3 };
 template <int XK> struct XType { using T = uint16_t; };
@@ -37,19 +36,25 @@ template <> struct XType<X_I8> { using T = int8_t; };
 template <> struct XType<X_I8_BF16> { using T = int8_t; };
 template <> struct XType<X_F32> { using T = float; };
 
-// Asynchronous copy of 16 bytes per active lane, sbase + voff of each lane to
-// lds + 16 lane (lds and sbase wave-uniform).  M0 is restored.
-__device__ __forceinline__ void copy16(uint32_t voff, const void* sbase, uint32_t lds) {
-  uint32_t keep;
-  asm volatile(
-      "s_mov_b32 %0, m0\n\t"
-      "s_mov_b32 m0, %3\n\t"
-      "global_load_lds_dwordx4 %1, %2\n\t"
-      "s_mov_b32 m0, %0"
-      : "=&s"(keep)
-      : "v"(voff), "s"(sbase), "s"(lds)
-      : "memory");
-}
+// Asynchronous copies of 16 bytes, 4 bytes, or one byte (to a dword) per
+// active lane: sbase + voff of each lane to lds + 16 lane, or lds + 4 lane (lds
+// and sbase wave-uniform).  M0 is restored.
+#define PWQ_COPY(NAME, OP)                                                                    \
+  __device__ __forceinline__ void NAME(uint32_t voff, const void* sbase, uint32_t lds) {     \
+    uint32_t keep;                                                                           \
+    asm volatile(                                                                            \
+        "s_mov_b32 %0, m0\n\t"                                                               \
+        "s_mov_b32 m0, %3\n\t" OP                                                            \
+        " %1, %2\n\t"                                                                        \
+        "s_mov_b32 m0, %0"                                                                   \
+        : "=&s"(keep)                                                                        \
+        : "v"(voff), "s"(sbase), "s"(lds)                                                    \
+        : "memory");                                                                         \
+  }
+PWQ_COPY(copy16, "global_load_lds_dwordx4")
+PWQ_COPY(copy4, "global_load_lds_dword")
+PWQ_COPY(copy1, "global_load_lds_ubyte")
+#undef PWQ_COPY
 
 // Waits until at most n of this wave's copies are in flight (n wave-uniform).
 __device__ __forceinline__ void wait_copies(int n) {
@@ -58,7 +63,7 @@ __device__ __forceinline__ void wait_copies(int n) {
     case N: asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory"); break;
     PWQ_WC(1) PWQ_WC(2) PWQ_WC(3) PWQ_WC(4) PWQ_WC(5) PWQ_WC(6) PWQ_WC(7) PWQ_WC(8) PWQ_WC(9)
     PWQ_WC(10) PWQ_WC(11) PWQ_WC(12) PWQ_WC(13) PWQ_WC(14) PWQ_WC(15) PWQ_WC(16) PWQ_WC(18)
-    PWQ_WC(20) PWQ_WC(21) PWQ_WC(24) PWQ_WC(25) PWQ_WC(27) PWQ_WC(28)
+    PWQ_WC(17) PWQ_WC(19) PWQ_WC(20) PWQ_WC(21) PWQ_WC(24) PWQ_WC(25) PWQ_WC(27) PWQ_WC(28)
 #undef PWQ_WC
     default: asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); break;
   }
@@ -153,10 +158,10 @@ __device__ __forceinline__ void x_parts(const typename XType<XK>::T* p,
 }
 
 // LDS of a wave: `depth` slots of a tile (weights 1 KB, x), the steps and zero
-// points of 16 rows x `srow` groups (odd: off the bank stride), overflow entries.
+// points of 16 rows x `sg` groups (4, 8 or 16), overflow entries.
 constexpr int kEntries = 256;
-constexpr int wave_bytes(int depth, int xbytes, int srow, bool over) {
-  return depth * (1024 + xbytes) + (2 * 16 * srow * 4 + 15) / 16 * 16 + (over ? 4 * kEntries : 0);
+constexpr int wave_bytes(int depth, int xbytes, int sg, bool over) {
+  return depth * (1024 + xbytes) + 2 * 16 * sg * 4 + (over ? 4 * kEntries : 0);
 }
 
 template <int XK, int GB, bool OVER>
@@ -176,17 +181,17 @@ __global__ __launch_bounds__(1024) void packed_rows(const PackedLinearLaunch a) 
   const int64_t strip = blockIdx.x;
   const int tok = (int)a.ntok, n = (int)a.n, G = a.G, ng = a.ng, ldq = (int)a.ldq;
   const int xcols = (int)a.xcols;
-  const int across = (n + 127) >> 7, per = a.per, depth = a.depth, srow = a.srow;
+  const int across = (n + 127) >> 7, per = a.per, depth = a.depth, sg = a.sg;
   const int k0 = wave * per, k1 = min(across, k0 + per);
   const int rows = (int)min(a.m - strip * kPackRows, (int64_t)kPackRows);
   const bool asym = a.zeros != nullptr;
   const int xbytes = (tok + RPC - 1) / RPC * 1024, slot_bytes = 1024 + xbytes;
-  const int own = wave * wave_bytes(depth, xbytes, srow, OVER);
+  const int own = wave * wave_bytes(depth, xbytes, sg, OVER);
   char* const L = smem + own;
   const uint32_t lbase = (uint32_t)(uintptr_t)(lds_char*)smem + own;
-  float* const steps = (float*)(L + depth * slot_bytes);
-  float* const zs = steps + 16 * srow;
-  int* const ents = (int*)(L + wave_bytes(depth, xbytes, srow, false));
+  const float* const steps = (float*)(L + depth * slot_bytes);
+  const int* const zs = (int*)(steps + 16 * sg);
+  int* const ents = (int*)(L + wave_bytes(depth, xbytes, sg, false));
 
   // copies: lane -> 16-byte unit.  Units of a row are permuted by the row so
   // that the operand reads below spread over the banks.
@@ -221,36 +226,18 @@ __global__ __launch_bounds__(1024) void packed_rows(const PackedLinearLaunch a) 
   for (int c0 = k0; c0 < k1; c0 += CH) {
     const int c1 = min(k1, c0 + CH);
     const int g0 = 128 * c0 / G;
-    float sv[4];
-    int zv[4] = {0, 0, 0, 0};
-    {
-      // lane: row lane / 4, groups g0 + 4 (lane % 4) ..
-      const int64_t r = (strip * kPackRows + min(wr, rows - 1)) * (int64_t)ng;
-      const int gl = g0 + 4 * (lane & 3);
-      if (g0 + 16 <= ng) {
-        const vec16f v = *(const vec16f*)(a.scales + r + gl);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) sv[i] = v.v[i];
-      } else {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) sv[i] = a.scales[r + min(gl + i, ng - 1)];
-      }
-      if (asym)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) zv[i] = a.zeros[r + min(gl + i, ng - 1)];
+    // steps and zero points, ahead of the tiles (a load into registers would
+    // be waited for together with every copy in flight)
+    for (int i = 0; i < sg / 4; ++i) {
+      const int at = 64 * i + lane, r = min(at / sg, rows - 1), g = min(g0 + at % sg, ng - 1);
+      const uint32_t dst = lbase + (uint32_t)(depth * slot_bytes + 256 * i);
+      copy4(4u * (r * ng + g), a.scales + strip * kPackRows * ng, dst);
+      if (asym) copy1(r * ng + g, a.zeros + strip * kPackRows * ng, dst + 64u * sg);
     }
     int off = 0;
     if constexpr (OVER)
       off = max(a.outlier_off[strip * across + min(c0 + lane, c1)], 0);
     for (int d = 0; d < depth && c0 + d < c1; ++d) copy_tile(c0 + d, d);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int gi = 4 * (lane & 3) + i, at = wr * srow + gi;
-      if (gi < srow) {
-        steps[at] = XK == X_I8 && !asym ? 0.0625f * sv[i] : sv[i];
-        zs[at] = XK == X_I8 ? __int_as_float(zv[i]) : -(asym ? 16.0f + (float)zv[i] : 24.0f);
-      }
-    }
     int ebase = 0;
     if constexpr (OVER) {
       ebase = __builtin_amdgcn_readlane(off, 0);
@@ -273,8 +260,8 @@ __global__ __launch_bounds__(1024) void packed_rows(const PackedLinearLaunch a) 
       }
 #pragma unroll
       for (int h = 0; h < NB; ++h) {
-        const float s = steps[lr * srow + g];
-        const float zf = zs[lr * srow + g];
+        const float s = steps[lr * sg + g] * (XK == X_I8 && !asym ? 0.0625f : 1.0f);
+        const int z = asym ? zs[lr * sg + g] : 8;
         in_g += GB;
         if (in_g >= G) in_g -= G, ++g;
         uint32_t w[NW];
@@ -284,7 +271,7 @@ __global__ __launch_bounds__(1024) void packed_rows(const PackedLinearLaunch a) 
         }
         acc_t c = {0, 0, 0, 0}, c1s = {0, 0, 0, 0};   // sums of the codes' terms, of x alone
         if constexpr (XK == X_I8) {
-          const uint32_t z4 = __float_as_uint(zf) * 0x01010101u;
+          const uint32_t z4 = (uint32_t)z * 0x01010101u;
 #pragma unroll
           for (int j = 0; j < NW; j += 2) {
             uint2 lo, hi;
@@ -300,7 +287,7 @@ __global__ __launch_bounds__(1024) void packed_rows(const PackedLinearLaunch a) 
           const uint32_t bias = asym ? 0x41804180u : 0x41c041c0u;
 #pragma unroll
           for (int j = 0; j < NW; ++j) {
-            const bf16x8_t f = BIASED ? codes_bf16(w[j], bias) : steps_bf16(w[j], bias, -zf);
+            const bf16x8_t f = BIASED ? codes_bf16(w[j], bias) : steps_bf16(w[j], bias, 16.0f + (float)z);
             const int col = GB * h + NC * lq + 8 * j;
             T xv[8];
             if constexpr (XK == X_BF16) {
@@ -363,7 +350,7 @@ __global__ __launch_bounds__(1024) void packed_rows(const PackedLinearLaunch a) 
             if constexpr (OVER) v += asym ? ce[e] : 16 * ce[e];
             acc[e] = fmaf(s, (float)v, acc[e]);
           } else {
-            float v = BIASED ? fmaf(zf, c1s[e], c[e]) : c[e];
+            float v = BIASED ? fmaf(-16.0f - (float)z, c1s[e], c[e]) : c[e];
             if constexpr (OVER) v += ce[e];
             acc[e] = fmaf(s, v, acc[e]);
           }
@@ -381,7 +368,7 @@ __global__ __launch_bounds__(1024) void packed_rows(const PackedLinearLaunch a) 
 
   // join the waves' sums in their order; lane l: tokens 4 (l / 16) + e, row l % 16
   float* const joined = (float*)smem;
-  const int stride = wave_bytes(depth, xbytes, srow, OVER) / 4;
+  const int stride = wave_bytes(depth, xbytes, sg, OVER) / 4;
 #pragma unroll
   for (int e = 0; e < 4; ++e) joined[wave * stride + e * 64 + lane] = acc[e];
   __syncthreads();
@@ -421,10 +408,11 @@ void launch_gb(PackedLinearLaunch a, hipStream_t st) {
   int most = (int)std::clamp<int64_t>(4096 / strips, 1, 16), bytes;
   for (;; --most) {
     a.per = (int)((across + most - 1) / most);
-    a.srow = std::min(16, a.per * (128 / GB)) | 1;
+    a.sg = 4;
+    while (a.sg < std::min(16, a.per * (128 / GB))) a.sg *= 2;
     a.depth = std::min(8, a.per);
-    while (a.depth > 2 && 16 * wave_bytes(a.depth, xbytes, a.srow, OVER) > kLdsBytes) --a.depth;
-    bytes = wave_bytes(a.depth, xbytes, a.srow, OVER);
+    while (a.depth > 2 && 16 * wave_bytes(a.depth, xbytes, a.sg, OVER) > kLdsBytes) --a.depth;
+    bytes = wave_bytes(a.depth, xbytes, a.sg, OVER);
     if (most * bytes <= kLdsBytes) break;
   }
   a.ng = (int)(a.n / a.G);
