@@ -56,19 +56,6 @@ PWQ_COPY(copy4, "global_load_lds_dword")
 PWQ_COPY(copy1, "global_load_lds_ubyte")
 #undef PWQ_COPY
 
-// Waits until at most n of this wave's copies are in flight (n wave-uniform).
-__device__ __forceinline__ void wait_copies(int n) {
-  switch (n) {
-#define PWQ_WC(N) \
-    case N: asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory"); break;
-    PWQ_WC(1) PWQ_WC(2) PWQ_WC(3) PWQ_WC(4) PWQ_WC(5) PWQ_WC(6) PWQ_WC(7) PWQ_WC(8) PWQ_WC(9)
-    PWQ_WC(10) PWQ_WC(11) PWQ_WC(12) PWQ_WC(13) PWQ_WC(14) PWQ_WC(15) PWQ_WC(16) PWQ_WC(18)
-    PWQ_WC(17) PWQ_WC(19) PWQ_WC(20) PWQ_WC(21) PWQ_WC(24) PWQ_WC(25) PWQ_WC(27) PWQ_WC(28)
-#undef PWQ_WC
-    default: asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); break;
-  }
-}
-
 __device__ __forceinline__ uint32_t pack_hi(float a, float b) {   // exact for small integers
   return __builtin_amdgcn_perm(__float_as_uint(b), __float_as_uint(a), 0x07060302u);
 }
@@ -157,14 +144,19 @@ __device__ __forceinline__ void x_parts(const typename XType<XK>::T* p,
   }
 }
 
-// LDS of a wave: `depth` slots of a tile (weights 1 KB, x), the steps and zero
-// points of 16 rows x `sg` groups (4, 8 or 16), overflow entries.
+// LDS of a wave: slots of tiles on their way (weights 1 KB, NX KB of x), the
+// steps and zero points of 16 rows x `sg` groups (4, 8 or 16), overflow
+// entries.  As many tiles ahead as leave about 16 waves' worth on a CU (two
+// more or two less made no difference).
 constexpr int kEntries = 256;
-constexpr int wave_bytes(int depth, int xbytes, int sg, bool over) {
-  return depth * (1024 + xbytes) + 2 * 16 * sg * 4 + (over ? 4 * kEntries : 0);
+constexpr int depth_of(int nx) { return nx == 1 ? 4 : (nx == 2 ? 3 : 2); }
+constexpr int wave_bytes(int nx, int sg, bool over) {
+  return depth_of(nx) * 1024 * (1 + nx) + 2 * 16 * sg * 4 + (over ? 4 * kEntries : 0);
 }
 
-template <int XK, int GB, bool OVER>
+// NX: copies of x per tile, 1 KB each; ASYM: read for 8-bit x only (the other
+// kinds go by the pointer).
+template <int XK, int GB, int NX, bool ASYM, bool OVER>
 __global__ __launch_bounds__(1024) void packed_rows(const PackedLinearLaunch a) {
   using T = typename XType<XK>::T;
   using acc_t = std::conditional_t<XK == X_I8, i32x4_t, f32x4_t>;
@@ -181,17 +173,17 @@ __global__ __launch_bounds__(1024) void packed_rows(const PackedLinearLaunch a) 
   const int64_t strip = blockIdx.x;
   const int tok = (int)a.ntok, n = (int)a.n, G = a.G, ng = a.ng, ldq = (int)a.ldq;
   const int xcols = (int)a.xcols;
-  const int across = (n + 127) >> 7, per = a.per, depth = a.depth, sg = a.sg;
+  const int across = (n + 127) >> 7, per = a.per, sg = a.sg;
+  constexpr int depth = depth_of(NX), slot_bytes = 1024 * (1 + NX);
   const int k0 = wave * per, k1 = min(across, k0 + per);
   const int rows = (int)min(a.m - strip * kPackRows, (int64_t)kPackRows);
-  const bool asym = a.zeros != nullptr;
-  const int xbytes = (tok + RPC - 1) / RPC * 1024, slot_bytes = 1024 + xbytes;
-  const int own = wave * wave_bytes(depth, xbytes, sg, OVER);
+  const bool asym = XK == X_I8 ? ASYM : a.zeros != nullptr;
+  const int own = wave * wave_bytes(NX, sg, OVER);
   char* const L = smem + own;
   const uint32_t lbase = (uint32_t)(uintptr_t)(lds_char*)smem + own;
   const float* const steps = (float*)(L + depth * slot_bytes);
   const int* const zs = (int*)(steps + 16 * sg);
-  int* const ents = (int*)(L + wave_bytes(depth, xbytes, sg, false));
+  int* const ents = (int*)(L + wave_bytes(NX, sg, false));
 
   // copies: lane -> 16-byte unit.  Units of a row are permuted by the row so
   // that the operand reads below spread over the banks.
@@ -201,18 +193,27 @@ __global__ __launch_bounds__(1024) void packed_rows(const PackedLinearLaunch a) 
   const int xr = lane / UNITS;
   const uint32_t ldxb = (uint32_t)(a.ldx * ES);
   auto swz = [](int t) { return ES == 1 ? (t >> 1) & 7 : t & 15; };
-  const int copies = 1 + (tok + RPC - 1) / RPC;
+  const bool ragged = xcols % 128 != 0;
   auto copy_tile = [&](int kt, int slot) {
     const uint32_t dst = lbase + (uint32_t)(slot * slot_bytes);
     const int wo = 64 * kt;
     copy16(woff + (wo + 16 * wc < ldq ? (uint32_t)wo : 0u - 16u * wc), wbase, dst);
-    for (int j = 0; j * RPC < tok; ++j) {
-      const int t = j * RPC + xr, c = (lane % UNITS) ^ swz(t);
-      if (t < tok) {
+    const char* const xt = (const char*)a.x + (int64_t)kt * XROW;
+    if (!ragged || kt + 1 < across) {
+#pragma unroll
+      for (int j = 0; j < NX; ++j) {
+        const int t = j * RPC + xr, c = (lane % UNITS) ^ swz(t);
+        if (NX > 1 || t < tok)
+          copy16(min(t, tok - 1) * ldxb + 16u * c, xt, dst + 1024u + 1024u * j);
+      }
+    } else {
+      // the last tile, past the row: zeros (waited for with everything else)
+#pragma unroll
+      for (int j = 0; j < NX; ++j) {
+        const int t = j * RPC + xr, c = (lane % UNITS) ^ swz(t);
         if (kt * XROW + 16 * c < xcols * ES)
-          copy16(t * ldxb + 16u * c, (const char*)a.x + (int64_t)kt * XROW,
-                 dst + 1024u + 1024u * j);
-        else                                          // past the row: zeros
+          copy16(min(t, tok - 1) * ldxb + 16u * c, xt, dst + 1024u + 1024u * j);
+        else
           *(uint4*)(L + slot * slot_bytes + 1024 + 1024 * j + 16 * lane) = make_uint4(0, 0, 0, 0);
       }
     }
@@ -237,7 +238,9 @@ __global__ __launch_bounds__(1024) void packed_rows(const PackedLinearLaunch a) 
     int off = 0;
     if constexpr (OVER)
       off = max(a.outlier_off[strip * across + min(c0 + lane, c1)], 0);
-    for (int d = 0; d < depth && c0 + d < c1; ++d) copy_tile(c0 + d, d);
+#pragma unroll
+    for (int d = 0; d < depth; ++d)
+      if (c0 + d < c1) copy_tile(c0 + d, d);
     int ebase = 0;
     if constexpr (OVER) {
       ebase = __builtin_amdgcn_readlane(off, 0);
@@ -250,7 +253,12 @@ __global__ __launch_bounds__(1024) void packed_rows(const PackedLinearLaunch a) 
     int g = 0, in_g = 128 * c0 - g0 * G;
     int slot = 0;
     for (int kt = c0; kt < c1; ++kt) {
-      wait_copies(copies * (min(c1, kt + depth) - kt - 1));
+      // this tile's copies have landed: all but those of depth - 1 more tiles,
+      // each of which issued every one of its copies
+      if (kt + depth <= c1)
+        asm volatile("s_waitcnt vmcnt(%0)" ::"n"((depth - 1) * (1 + NX)) : "memory");
+      else
+        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
       const char* ws = L + slot * slot_bytes;
       const char* xs = ws + 1024;
       int e0 = 0, e1 = 0;
@@ -261,7 +269,7 @@ __global__ __launch_bounds__(1024) void packed_rows(const PackedLinearLaunch a) 
 #pragma unroll
       for (int h = 0; h < NB; ++h) {
         const float s = steps[lr * sg + g] * (XK == X_I8 && !asym ? 0.0625f : 1.0f);
-        const int z = asym ? zs[lr * sg + g] : 8;
+        const int zv = zs[lr * sg + g], z = asym ? zv : 8;
         in_g += GB;
         if (in_g >= G) in_g -= G, ++g;
         uint32_t w[NW];
@@ -368,7 +376,7 @@ __global__ __launch_bounds__(1024) void packed_rows(const PackedLinearLaunch a) 
 
   // join the waves' sums in their order; lane l: tokens 4 (l / 16) + e, row l % 16
   float* const joined = (float*)smem;
-  const int stride = wave_bytes(depth, xbytes, sg, OVER) / 4;
+  const int stride = wave_bytes(NX, sg, OVER) / 4;
 #pragma unroll
   for (int e = 0; e < 4; ++e) joined[wave * stride + e * 64 + lane] = acc[e];
   __syncthreads();
@@ -397,38 +405,55 @@ __global__ __launch_bounds__(256) void pad_rows(const T* __restrict__ x, int64_t
 
 constexpr int kLdsBytes = 160 * 1024;
 
-template <int XK, int GB, bool OVER>
-void launch_gb(PackedLinearLaunch a, hipStream_t st) {
-  constexpr int ES = sizeof(typename XType<XK>::T), RPC = 64 / (128 * ES / 16);
-  const int xbytes = (int)(a.ntok + RPC - 1) / RPC * 1024;
-  // about 16 waves per CU over the whole launch; as many tiles ahead as LDS
-  // holds for them, 8 at most (the whole range of a wave, mostly: what is in
-  // flight from the start is not waited for twice)
+template <int XK, int GB, int NX, bool ASYM, bool OVER>
+void launch_waves(PackedLinearLaunch a, hipStream_t st) {
+  // about 16 waves per CU over the whole launch, as far as LDS goes
   const int64_t strips = (a.m + kPackRows - 1) / kPackRows, across = (a.n + 127) / 128;
   int most = (int)std::clamp<int64_t>(4096 / strips, 1, 16), bytes;
   for (;; --most) {
     a.per = (int)((across + most - 1) / most);
     a.sg = 4;
     while (a.sg < std::min(16, a.per * (128 / GB))) a.sg *= 2;
-    a.depth = std::min(8, a.per);
-    while (a.depth > 2 && 16 * wave_bytes(a.depth, xbytes, a.sg, OVER) > kLdsBytes) --a.depth;
-    bytes = wave_bytes(a.depth, xbytes, a.sg, OVER);
+    bytes = wave_bytes(NX, a.sg, OVER);
     if (most * bytes <= kLdsBytes) break;
   }
   a.ng = (int)(a.n / a.G);
   const int waves = (int)((across + a.per - 1) / a.per);
-  packed_rows<XK, GB, OVER><<<dim3((unsigned)strips), 64 * waves, waves * bytes, st>>>(a);
+  packed_rows<XK, GB, NX, ASYM, OVER>
+      <<<dim3((unsigned)strips), 64 * waves, waves * bytes, st>>>(a);
+}
+
+template <int XK, int GB, int NX>
+void launch_nx(const PackedLinearLaunch& a, hipStream_t st) {
+  const bool over = a.outlier_off != nullptr;
+  if constexpr (XK == X_I8) if (a.zeros)
+    return over ? launch_waves<XK, GB, NX, true, true>(a, st)
+                : launch_waves<XK, GB, NX, true, false>(a, st);
+  over ? launch_waves<XK, GB, NX, false, true>(a, st)
+       : launch_waves<XK, GB, NX, false, false>(a, st);
+}
+
+// Copies of x per tile: 1 KB holds 4 tokens of bf16, 8 of 8 bits, 2 of float32.
+template <int XK, int GB>
+void launch_gb(const PackedLinearLaunch& a, hipStream_t st) {
+  if constexpr (XK == X_BF16) {
+    if (a.ntok <= 4) return launch_nx<XK, GB, 1>(a, st);
+    a.ntok <= 8 ? launch_nx<XK, GB, 2>(a, st) : launch_nx<XK, GB, 4>(a, st);
+  } else if constexpr (XK == X_F32) {
+    if (a.ntok <= 4) return launch_nx<XK, GB, 2>(a, st);
+    a.ntok <= 8 ? launch_nx<XK, GB, 4>(a, st) : launch_nx<XK, GB, 8>(a, st);
+  } else {
+    a.ntok <= 8 ? launch_nx<XK, GB, 1>(a, st) : launch_nx<XK, GB, 2>(a, st);
+  }
 }
 
 template <int XK>
 void launch_x(const PackedLinearLaunch& a, int gb, hipStream_t st) {
-  const bool over = a.outlier_off != nullptr;
   if constexpr (XK != X_I8_BF16) {
-    if (gb == 128) return over ? launch_gb<XK, 128, true>(a, st) : launch_gb<XK, 128, false>(a, st);
-    if (gb == 64) return over ? launch_gb<XK, 64, true>(a, st) : launch_gb<XK, 64, false>(a, st);
+    if (gb == 128) return launch_gb<XK, 128>(a, st);
+    if (gb == 64) return launch_gb<XK, 64>(a, st);
   }
-  if constexpr (XK != X_I8)
-    over ? launch_gb<XK, 32, true>(a, st) : launch_gb<XK, 32, false>(a, st);
+  if constexpr (XK != X_I8) launch_gb<XK, 32>(a, st);
 }
 
 }  // namespace

@@ -1003,7 +1003,7 @@ pwq_status pwq_packed_linear(const void* x, int32_t xdtype, int64_t ntok, int64_
   if (s != PWQ_OK) return s;
   PackedLinearLaunch a{x, xdtype, ntok, ldx, x_scales, qweight, m, n, packed_row_bytes(n), scales,
                        zeros, group > 0 ? group : (int32_t)n, n_out > 0 ? outlier_off : nullptr,
-                       outliers, n_out, y, ydtype, ldy, 0, 0, 0, 0, 0};
+                       outliers, n_out, y, ydtype, ldy, 0, 0, 0, 0};
   const LinearPlan p = linear_plan(x, xdtype, ntok, ldx, m, n, a.G, n_out);
   Carver c(ws);
   PromptWs w;

@@ -199,9 +199,9 @@ struct PackedLinearLaunch {
   int32_t ydtype;
   int64_t ldy;
   // launch_rows: columns x has in memory, groups of a row, tiles of 128 columns
-  // per wave, tiles ahead, groups staged per row
+  // per wave, groups staged per row
   int64_t xcols;
-  int32_t ng, per, depth, sg;
+  int32_t ng, per, sg;
 };
 // Any shape, one wave per row and few tokens.
 hipError_t launch_linear_any(const PackedLinearLaunch& a, hipStream_t st);
