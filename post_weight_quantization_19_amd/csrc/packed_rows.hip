@@ -29,6 +29,7 @@ namespace {
 
 typedef __attribute__((__vector_size__(4 * sizeof(int)))) int i32x4_t;
 typedef __attribute__((address_space(3))) char lds_char;
+typedef __attribute__((address_space(4))) int const_int;
 
 enum { X_BF16 = 0, X_I8 = 1, X_F32 = 2, X_I8_BF16 = 3 };
 template <int XK> struct XType { using T = uint16_t; };
@@ -148,10 +149,10 @@ __device__ __forceinline__ void x_parts(const typename XType<XK>::T* p,
 // steps and zero points of 16 rows x `sg` groups (4, 8 or 16), overflow
 // entries.  As many tiles ahead as leave about 16 waves' worth on a CU (two
 // more or two less made no difference).
-constexpr int kEntries = 256;
+constexpr int kEntries = 256, kOffsets = 64;
 constexpr int depth_of(int nx) { return nx == 1 ? 4 : (nx == 2 ? 3 : 2); }
 constexpr int wave_bytes(int nx, int sg, bool over) {
-  return depth_of(nx) * 1024 * (1 + nx) + 2 * 16 * sg * 4 + (over ? 4 * kEntries : 0);
+  return depth_of(nx) * 1024 * (1 + nx) + 2 * 16 * sg * 4 + (over ? 4 * (kEntries + kOffsets) : 0);
 }
 
 // NX: copies of x per tile, 1 KB each; ASYM: read for 8-bit x only (the other
@@ -183,7 +184,8 @@ __global__ __launch_bounds__(1024) void packed_rows(const PackedLinearLaunch a) 
   const uint32_t lbase = (uint32_t)(uintptr_t)(lds_char*)smem + own;
   const float* const steps = (float*)(L + depth * slot_bytes);
   const int* const zs = (int*)(steps + 16 * sg);
-  int* const ents = (int*)(L + wave_bytes(NX, sg, false));
+  const int* const ents = (const int*)(L + wave_bytes(NX, sg, false));
+  const int* const offs = ents + kEntries;
 
   // copies: lane -> 16-byte unit.  Units of a row are permuted by the row so
   // that the operand reads below spread over the banks.
@@ -221,6 +223,18 @@ __global__ __launch_bounds__(1024) void packed_rows(const PackedLinearLaunch a) 
   const int tr = min(lr, tok - 1);                    // the lane's x row
   auto x_unit = [&](const char* xs, int c) { return xs + tr * XROW + ((c ^ swz(tr)) << 4); };
 
+  // the kEntries overflow entries from ebase on, in LDS
+  int ebase = 0;
+  auto hold_entries = [&](int from) {
+    ebase = from;
+    const int count = (int)min(a.n_out - from, (int64_t)kEntries);
+#pragma unroll
+    for (int i = 0; i < kEntries / 64; ++i)
+      if (64 * i + lane < count)
+        copy4(4u * (64 * i + lane), a.outliers + from,
+              lbase + wave_bytes(NX, sg, false) + 256u * i);
+  };
+
   f32x4_t acc = {0.0f, 0.0f, 0.0f, 0.0f};
 
   // chunks of tiles whose steps fit LDS (one, unless a wave has many tiles)
@@ -235,27 +249,26 @@ __global__ __launch_bounds__(1024) void packed_rows(const PackedLinearLaunch a) 
       copy4(4u * (r * ng + g), a.scales + strip * kPackRows * ng, dst);
       if (asym) copy1(r * ng + g, a.zeros + strip * kPackRows * ng, dst + 64u * sg);
     }
-    int off = 0;
-    if constexpr (OVER)
-      off = max(a.outlier_off[strip * across + min(c0 + lane, c1)], 0);
+    if constexpr (OVER) {
+      const int* const off = a.outlier_off + strip * across + c0;
+      copy4(4u * min(lane, c1 - c0), off, lbase + wave_bytes(NX, sg, false) + 4 * kEntries);
+    }
 #pragma unroll
     for (int d = 0; d < depth; ++d)
       if (c0 + d < c1) copy_tile(c0 + d, d);
-    int ebase = 0;
     if constexpr (OVER) {
-      ebase = __builtin_amdgcn_readlane(off, 0);
-      const int last = (int)min((int64_t)__builtin_amdgcn_readlane(off, c1 - c0), a.n_out);
-#pragma unroll
-      for (int i = 0; i < kEntries / 64; ++i)
-        if (ebase + 64 * i + lane < last) ents[64 * i + lane] = a.outliers[ebase + 64 * i + lane];
+      // the list's place by a scalar load, which waits for no copy
+      const const_int* const off = (const const_int*)(a.outlier_off + strip * across);
+      hold_entries(max(off[c0], 0));
     }
     // group of the next block, without divisions
     int g = 0, in_g = 128 * c0 - g0 * G;
     int slot = 0;
     for (int kt = c0; kt < c1; ++kt) {
       // this tile's copies have landed: all but those of depth - 1 more tiles,
-      // each of which issued every one of its copies
-      if (kt + depth <= c1)
+      // each of which issued every one of its copies (the list's entries came
+      // after the first tiles)
+      if (kt + depth <= c1 && !(OVER && kt == c0))
         asm volatile("s_waitcnt vmcnt(%0)" ::"n"((depth - 1) * (1 + NX)) : "memory");
       else
         asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
@@ -263,8 +276,8 @@ __global__ __launch_bounds__(1024) void packed_rows(const PackedLinearLaunch a) 
       const char* xs = ws + 1024;
       int e0 = 0, e1 = 0;
       if constexpr (OVER) {
-        e0 = __builtin_amdgcn_readlane(off, kt - c0);
-        e1 = (int)min((int64_t)__builtin_amdgcn_readlane(off, kt - c0 + 1), a.n_out);
+        e0 = max(__builtin_amdgcn_readfirstlane(offs[kt - c0]), 0);
+        e1 = (int)min((int64_t)__builtin_amdgcn_readfirstlane(offs[kt - c0 + 1]), a.n_out);
       }
 #pragma unroll
       for (int h = 0; h < NB; ++h) {
@@ -318,30 +331,37 @@ __global__ __launch_bounds__(1024) void packed_rows(const PackedLinearLaunch a) 
         acc_t ce = {0, 0, 0, 0};
         constexpr int PE = XK == X_I8 ? 16 : 8;          // entries of a lane at a time
         if constexpr (OVER) for (int e = e0; e < e1; e += 4 * PE) {
-          int ent[PE];
-          T xe[PE];
+          // the lane's entries e + 4 i + l / 16; most tiles have few, so by twos
+          int val[PE] = {};
+          T xe[PE] = {};
+          if (e < ebase || min(e + 4 * PE, e1) > ebase + kEntries) {
+            asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+            hold_entries(e);
+            asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+          }
 #pragma unroll
-          for (int i = 0; i < PE; ++i) {
-            const int at = e + PE * lq + i;
-            const uint32_t in = (uint32_t)(at - ebase);
-            ent[i] = at >= e1 ? 0 : (in < kEntries ? ents[in] : a.outliers[at]);
-            if ((ent[i] & 127) / GB != h) ent[i] = 0;    // another block's: value 0
-            const int col = ent[i] & 127;                // (columns past n hold zeros)
-            xe[i] = *(const T*)(x_unit(xs, col * ES / 16) + col * ES % 16);
+          for (int i = 0; i < PE; i += 2) {
+            if (e + 4 * i >= e1) break;
+#pragma unroll
+            for (int k = i; k < i + 2; ++k) {
+              const int ent = ents[min(e + 4 * k + lq, e1 - 1) - ebase];
+              const int col = ent & 127;                 // (columns past n hold zeros)
+              xe[k] = *(const T*)(x_unit(xs, col * ES / 16) + col * ES % 16);
+              val[k] = e + 4 * k + lq < e1 && col / GB == h && ((ent >> 7) & 15) == lr ? ent >> 16
+                                                                                      : 0;
+            }
           }
           if constexpr (XK == X_I8) {
             i32x4_t f = {0, 0, 0, 0};
 #pragma unroll
-            for (int i = 0; i < PE; ++i)
-              if (((ent[i] >> 7) & 15) == lr) f[i / 4] |= ((ent[i] >> 16) & 255) << (8 * (i % 4));
+            for (int i = 0; i < PE; ++i) f[i / 4] |= (val[i] & 255) << (8 * (i % 4));
             i32x4_t v;
             __builtin_memcpy(&v, xe, 16);
             ce = __builtin_amdgcn_mfma_i32_16x16x64_i8(v, f, ce, 0, 0, 0);
           } else {
             float d[PE];
 #pragma unroll
-            for (int i = 0; i < PE; ++i)
-              d[i] = ((ent[i] >> 7) & 15) == lr ? (float)(ent[i] >> 16) : 0.0f;
+            for (int i = 0; i < PE; ++i) d[i] = (float)val[i];
             const uint4 o = make_uint4(pack_hi(d[0], d[1]), pack_hi(d[2], d[3]),
                                        pack_hi(d[4], d[5]), pack_hi(d[6], d[7]));
             bf16x8_t v[kParts<XK>];
