@@ -1,5 +1,5 @@
-// y = x W^^T of a packed layer for many tokens: tiles of BT tokens x BR rows
-// on the matrix cores.
+// y = x W^^T of a packed layer for more than 16 tokens: tiles of BT tokens x
+// BR rows on the matrix cores.
 //
 //   y[t, r] = x_scale[t] * sum_g s[r, g] * sum_{k in g} x[t, k] (c - z)[r, k]
 //
@@ -14,24 +14,31 @@
 // kilobyte; prompt_tiles multiplies.  Up to 128 tokens, where that writing
 // would cost more than the product, prompt_tiles reads the packed codes and
 // spreads them itself (FUSED; not with overflow entries, which would have to
-// be looked for in every lane's registers): q_proj 64 8-bit tokens 16 us
+// be looked for in every lane's registers): q_proj 64 8-bit tokens 15 us
 // against 25, up_proj 32 bf16 tokens 33 against 60.  With more tokens every
 // tile of them would repeat it on the vector unit, which the multiplication
 // by the steps already fills (that way 2048 bf16 tokens of up_proj took 333 us
 // against 295).
 //
 // A step of prompt_tiles covers 128 bytes of every x row (128 8-bit or 64 bf16
-// columns).  x goes HBM -> LDS by asynchronous copies two steps ahead through
-// three slots; LDS rows are 128 bytes, their 16-byte units permuted by the row
-// so that 16 rows' reads of one column block cover every bank.  Weights go
-// straight to registers, a step ahead.
+// columns).  Two steps ahead of their use, x goes HBM -> LDS by asynchronous
+// copies through three slots (LDS rows are 128 bytes, their 16-byte units
+// permuted by the row so that 16 rows' reads of one column block cover every
+// bank) and weights straight to registers.  A wave works on all of the tile's
+// tokens and 32 rows, so that a workgroup reads every weight once; waves of 64
+// x 64 read each twice, and a CU's 2 x 24 instead of 2 x 16 KB of a step took
+// 512 bf16 tokens of up_proj from 63 to 72 us.  Two workgroups' waves to a
+// SIMD at most: with that bound the compiler sums in vector registers, without
+// it in accumulation registers, whose reads double the vector instructions (81
+// us).
 //
-// What bounds it: the matrix unit at the clock that its power allows.  The
-// 256 x 256 tiles alone take 268 us for 2048 bf16 tokens of up_proj and 166 us
-// in 8 bits (0.90 and 1.45 P(FL)OP/s, 7 of 8 CUs busy over the two rounds of
-// 448 tiles); without the steps' multiplications 226 and 120 us, and without
-// any load of x or weights 245 and 161.  The library's products of the same
-// size take 207 us (bf16) and, at its 8192^3 rate, 115 us (8 bits).
+// What bounds it: the matrix unit at the clock that its power allows, and the
+// multiplications of its sums by the steps, which overlap it in part.  Tiles
+// alone take 254 to 290 us (as the clock goes) for 2048 bf16 tokens of up_proj
+// and 146 to 163 us in 8 bits (0.95 and 1.65 P(FL)OP/s at best), 206 and 105
+// us with one step per row; 8192 tokens 927 and 585 us with everything (1.04
+// and 1.64 P(FL)OP/s).  The library's products of the first size take 207 us
+// (bf16) and, at its 8192^3 rate, 115 us (8 bits).
 #include "pwq_internal.h"
 
 #include <algorithm>
@@ -103,7 +110,7 @@ struct PromptArgs {
   const char* x;          // rows of `steps` * 128 bytes, 16-byte aligned
   int64_t xrow;           // bytes between x rows
   int steps;              // steps over the whole row
-  int reps;               // steps per weight block (3 for float32 parts)
+  int reps;               // steps per weight block: 1, or 3 parts of float32
   int per;                // steps per split
   int tiles_t, tiles_r;
   const float* x_scales;
@@ -116,7 +123,9 @@ struct PromptArgs {
   int blocks;             // weight blocks (steps / reps)
   const float* steps_t;   // [group][16 strips' rows], times what the operands leave out
   int64_t rows16;         // rows of it: 16 strips
-  int ntok, m, n, G, ng;
+  int ntok, m, ng;
+  uint32_t per_group;     // 2^31 / half steps of a group, rounded up: 2 u per_group / 2^32 is
+                          // the group of half step u < 2^16 (at most 2^15 to a group)
   void* y;
   int ydtype;
   int64_t ldy;
@@ -198,10 +207,10 @@ __global__ __launch_bounds__(256) void spread_weights(
 // at the end; 1: every step (G a multiple of its columns); 2: twice a step.
 // FUSED: packed weights are read and spread by the wave that multiplies by
 // them.
-template <bool I8, int BT, int BR, int WT, int WR, int MODE, bool FUSED>
-__global__ __launch_bounds__(64 * WT * WR) void prompt_tiles(const PromptArgs a) {
-  constexpr int NT = 64 * WT * WR;
-  constexpr int NI = BT / WT / 16, NJ = BR / WR / 16;
+template <bool I8, int BT, int BR, int WR, int MODE, bool FUSED>
+__global__ __launch_bounds__(64 * WR, 2) void prompt_tiles(const PromptArgs a) {
+  constexpr int NT = 64 * WR;
+  constexpr int NI = BT / 16, NJ = BR / WR / 16;
   constexpr int COLS = I8 ? 128 : 64;         // columns of a step
   constexpr int XB = BT * KB;
   constexpr int NC = XB / (16 * NT);          // copies of a wave per step
@@ -228,7 +237,6 @@ __global__ __launch_bounds__(64 * WT * WR) void prompt_tiles(const PromptArgs a)
 
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int wt = wave / WR, wr = wave % WR;
 
   // x copies: copy h of this lane fills unit 64 (NT / 64 h + wave) + lane
   uint32_t xoff[NC];
@@ -244,13 +252,14 @@ __global__ __launch_bounds__(64 * WT * WR) void prompt_tiles(const PromptArgs a)
     for (int h = 0; h < NC; ++h) copy16(xoff[h], xbase + (int64_t)s * KB, dst + 16u * NT * h);
   };
 
-  // weights: block j of this wave is strip r0 / 16 + wr NJ + j (the last one
+  // weights: block j of this wave is strip r0 / 16 + wave NJ + j (the last one
   // again past the end); wave-uniform bases, the lane's offset is the same
   const int lr = lane & 15, lq = lane >> 4;
   auto strip = [&](int j) {
-    return min(r0 / 16 + wr * NJ + j, (int)(a.rows16 / 16) - 1);
+    return min(r0 / 16 + wave * NJ + j, (int)(a.rows16 / 16) - 1);
   };
   constexpr int NS = MODE == 2 ? 2 : 1;
+  constexpr int NX = 4;                       // operands of x, read three ahead
   // 16-byte unit of an LDS row that lane group lq of half h works on.  FUSED:
   // both halves' packed codes next to each other in memory, unless a half has
   // to stay within a group of its own.
@@ -265,14 +274,15 @@ __global__ __launch_bounds__(64 * WT * WR) void prompt_tiles(const PromptArgs a)
   };
   uint32_t row[NJ];                            // of the tile, the lane's in block j
 #pragma unroll
-  for (int j = 0; j < NJ; ++j) row[j] = (uint32_t)(min(r0 + 16 * (wr * NJ + j) + lr, a.m - 1) - r0);
+  for (int j = 0; j < NJ; ++j) row[j] = (uint32_t)(min(r0 + 16 * (wave * NJ + j) + lr, a.m - 1) - r0);
   const uint8_t* const qbase = FUSED ? a.qweight + r0 * a.ldq : nullptr;
   const float* const sbase = FUSED ? a.scales + (int64_t)r0 * a.ng : nullptr;
   // (SYM reads the steps' bytes in the zero points' place and uses 8)
   const bool asym = FUSED && a.zeros != nullptr;
   const uint8_t* const zbase = asym ? a.zeros + (int64_t)r0 * a.ng : (const uint8_t*)sbase;
+  auto block_of = [&](int s) { return a.reps == 1 ? s : s / 3; };
   auto load_w = [&](Weights& b, int s) {
-    const int blk = s / a.reps;
+    const int blk = block_of(s);
     if constexpr (FUSED) {
 #pragma unroll
       for (int j = 0; j < NJ; ++j) {
@@ -287,12 +297,6 @@ __global__ __launch_bounds__(64 * WT * WR) void prompt_tiles(const PromptArgs a)
             __builtin_memcpy(&b.p[j][h * (PB / 4)], qbase + (at + (o < a.ldq ? o : 0)), PB);
           }
         }
-#pragma unroll
-        for (int h = 0; h < NS; ++h) {
-          const int g = MODE == 0 ? 0 : min((blk * COLS + h * (COLS / 2)) / a.G, a.ng - 1);
-          b.s[j][h] = sbase[row[j] * a.ng + g];
-          b.z[j][h] = zbase[row[j] * a.ng + g];
-        }
       }
     } else {
 #pragma unroll
@@ -301,14 +305,35 @@ __global__ __launch_bounds__(64 * WT * WR) void prompt_tiles(const PromptArgs a)
         for (int h = 0; h < 2; ++h)
           b.w[j][h] =
               (a.spread + ((int64_t)strip(j) * a.blocks + blk) * 128 + 64 * h)[(uint32_t)lane];
-      if constexpr (MODE != 0)
+    }
+  };
+  auto load_s = [&](Weights& b, int s) {
+    if constexpr (!FUSED && MODE == 0) return;
+    const int blk = block_of(s);
 #pragma unroll
-        for (int h = 0; h < NS; ++h) {
-          const int g = min((blk * COLS + h * (COLS / 2)) / a.G, a.ng - 1);
+    for (int h = 0; h < NS; ++h) {
+      const int g = MODE == 0 ? 0 : min((int)__umulhi(4 * blk + 2 * h, a.per_group), a.ng - 1);
 #pragma unroll
-          for (int j = 0; j < NJ; ++j)
-            b.s[j][h] = (a.steps_t + g * a.rows16 + 16 * strip(j))[(uint32_t)lr];
+      for (int j = 0; j < NJ; ++j) {
+        if constexpr (FUSED) {
+          b.s[j][h] = sbase[row[j] * a.ng + g];
+          b.z[j][h] = zbase[row[j] * a.ng + g];
+        } else {
+          b.s[j][h] = (a.steps_t + g * a.rows16 + 16 * strip(j))[(uint32_t)lr];
         }
+      }
+    }
+  };
+  // the compiler waits for the weights' registers here
+  auto arrived = [&](Weights& b) {
+#pragma unroll
+    for (int j = 0; j < NJ; ++j) {
+      if constexpr (FUSED) {
+#pragma unroll
+        for (int i = 0; i < PB / 2; ++i) asm volatile("" : "+v"(b.p[j][i])::"memory");
+      } else {
+        asm volatile("" : "+v"(b.w[j][0]), "+v"(b.w[j][1])::"memory");
+      }
     }
   };
   const uint32_t flip = asym ? 0u : 0x88888888u, bias = asym ? 0x41804180u : 0x41c041c0u;
@@ -353,23 +378,27 @@ __global__ __launch_bounds__(64 * WT * WR) void prompt_tiles(const PromptArgs a)
     else return c[e];
   };
 
-  // prologue: steps s0 and s0 + 1 of x and the weights of s0 on their way
+  // prologue: steps s0 and s0 + 1 on their way
   const int last = s1 - 1;
-  Weights b0, b1;
-  copy_x(s0, s0 % 3);
-  copy_x(min(s0 + 1, last), (s0 + 1) % 3);
-  load_w(b0, s0);
+  Weights b[3];
+  auto ask = [&](int s, int slot, Weights& b) {
+    load_s(b, s);
+    copy_x(s, slot);
+    load_w(b, s);
+  };
+  ask(s0, 0, b[0]);
+  ask(min(s0 + 1, last), 1, b[1]);
 
-  auto step = [&](int s, Weights& b, Weights& bn) {
-    // What the last step asked for has arrived: this step's weights, the next
-    // one's x of this wave.  Past the barrier every wave's part of this step's
-    // x is there, and the slot before it is free.
-    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+  auto step = [&](int s, int slot, Weights& b, Weights& bn) {
+    // This step's x and weights, asked for two steps ago, have arrived: the
+    // weights came last and loads return in order, so that the wait for the
+    // weights' registers covers the x of this wave.  Past the barrier every
+    // wave's part of this step's x is there, and the slot before it is free.
+    arrived(b);
     lds_barrier();
-    copy_x(min(s + 2, last), (s + 2) % 3);
-    load_w(bn, min(s + 1, last));
-    const char* xs = smem + s % 3 * XB;
-    i32x4_t x[2][2];
+    ask(min(s + 2, last), (slot + 2) % 3, bn);
+    const char* xs = smem + slot * XB;
+    i32x4_t x[NX][2];
     i32x4_t w[NJ][2];
 #pragma unroll
     for (int j = 0; j < NJ; ++j)
@@ -379,17 +408,18 @@ __global__ __launch_bounds__(64 * WT * WR) void prompt_tiles(const PromptArgs a)
     auto read_x = [&](int i) {
 #pragma unroll
       for (int h = 0; h < 2; ++h)
-        x[i & 1][h] = *(const i32x4_t*)(xs + unit_at(16 * (wt * NI + i) + lr, unit(h)));
+        x[i % NX][h] = *(const i32x4_t*)(xs + unit_at(16 * i + lr, unit(h)));
     };
-    read_x(0);
+#pragma unroll
+    for (int i = 0; i < NX - 1; ++i) read_x(i);
     if constexpr (MODE == 0) {
 #pragma unroll
       for (int i = 0; i < NI; ++i) {
-        if (i + 1 < NI) read_x(i + 1);
+        if (i + NX - 1 < NI) read_x(i + NX - 1);
 #pragma unroll
         for (int h = 0; h < 2; ++h)
 #pragma unroll
-          for (int j = 0; j < NJ; ++j) dir[i][j] = mma(x[i & 1][h], w[j][h], dir[i][j]);
+          for (int j = 0; j < NJ; ++j) dir[i][j] = mma(x[i % NX][h], w[j][h], dir[i][j]);
       }
     } else {
       // Blocks of 16 x 16 in turn: one starts, the one before gets its second
@@ -410,14 +440,14 @@ __global__ __launch_bounds__(64 * WT * WR) void prompt_tiles(const PromptArgs a)
         constexpr int u = decltype(uu)::value;
         constexpr int i = u / NS / NJ, j = u / NS % NJ, h = u % NS;
         if constexpr (u < NU) {
-          c[u & 3] = mma(x[i & 1][h], w[j][h], zero);
-          if constexpr (j == (NJ > 1) && h == 0 && i + 1 < NI) read_x(i + 1);
+          c[u & 3] = mma(x[i % NX][h], w[j][h], zero);
+          if constexpr (j == 1 && h == 0 && i + NX - 1 < NI) read_x(i + NX - 1);
         }
         if constexpr (u >= 3) scale(std::integral_constant<int, u - 3>{}, 0);
         __builtin_amdgcn_sched_barrier(0);
         if constexpr (MODE == 1 && u > 0 && u <= NU) {
           constexpr int v = u - 1, iv = v / NJ, jv = v % NJ;
-          c[v & 3] = mma(x[iv & 1][1], w[jv][1], c[v & 3]);
+          c[v & 3] = mma(x[iv % NX][1], w[jv][1], c[v & 3]);
         }
         if constexpr (u >= 3) scale(std::integral_constant<int, u - 3>{}, 2);
         __builtin_amdgcn_sched_barrier(0);
@@ -425,11 +455,13 @@ __global__ __launch_bounds__(64 * WT * WR) void prompt_tiles(const PromptArgs a)
     }
   };
   int s = s0;
-  for (; s + 1 < s1; s += 2) {
-    step(s, b0, b1);
-    step(s + 1, b1, b0);
+  for (; s + 2 < s1; s += 3) {
+    step(s, 0, b[0], b[2]);
+    step(s + 1, 1, b[1], b[0]);
+    step(s + 2, 2, b[2], b[1]);
   }
-  if (s < s1) step(s, b0, b1);
+  if (s < s1) step(s, 0, b[0], b[2]);
+  if (s + 1 < s1) step(s + 1, 1, b[1], b[0]);
   // nothing is in flight to LDS, and no wave reads it, at the end
   asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
   lds_barrier();
@@ -452,7 +484,7 @@ __global__ __launch_bounds__(64 * WT * WR) void prompt_tiles(const PromptArgs a)
       float xsc[4];
 #pragma unroll
       for (int e = 0; e < 4; ++e)
-        xsc[e] = a.x_scales[min(t0 + 16 * (wt * NI + i) + 4 * lq + e, a.ntok - 1)];
+        xsc[e] = a.x_scales[min(t0 + 16 * i + 4 * lq + e, a.ntok - 1)];
 #pragma unroll
       for (int j = 0; j < NJ; ++j)
 #pragma unroll
@@ -466,11 +498,11 @@ __global__ __launch_bounds__(64 * WT * WR) void prompt_tiles(const PromptArgs a)
     for (int i = 0; i < NI; ++i)
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        const int t = t0 + 16 * (wt * NI + i) + 4 * lq + e;
+        const int t = t0 + 16 * i + 4 * lq + e;
         if (t < a.ntok)
 #pragma unroll
           for (int j = 0; j < NJ; ++j) {
-            const int r = r0 + 16 * (wr * NJ + j) + lr;
+            const int r = r0 + 16 * (wave * NJ + j) + lr;
             if (r < a.m) y[t * ld + r] = acc[i][j][e];
           }
       }
@@ -490,8 +522,8 @@ __global__ __launch_bounds__(64 * WT * WR) void prompt_tiles(const PromptArgs a)
         const __bf16 two[2] = {(__bf16)acc[i][j][e], (__bf16)acc[i][j][e + 1]};
         const uint32_t own = __builtin_bit_cast(uint32_t, two);
         const uint32_t other = __builtin_amdgcn_update_dpp(own, own, 0xB1, 0xF, 0xF, false);
-        const int t = 16 * (wt * NI + i) + 4 * lq + e + odd;
-        const int r = 16 * (wr * NJ + j) + (lr & ~1);
+        const int t = 16 * i + 4 * lq + e + odd;
+        const int r = 16 * (wave * NJ + j) + (lr & ~1);
         *(uint32_t*)(smem + t * YROW + 2 * r) = __builtin_amdgcn_perm(other, own, sel);
       }
   lds_barrier();
@@ -513,19 +545,35 @@ __global__ __launch_bounds__(64 * WT * WR) void prompt_tiles(const PromptArgs a)
   }
 }
 
-// Sum of the splits in their order.
+// Sum of the splits in their order: a token and 1024 columns per workgroup,
+// four a thread (VEC: rows of whole 16-byte units).
+template <bool VEC>
 __global__ __launch_bounds__(256) void prompt_join(const float* __restrict__ partial, int splits,
                                                    int64_t ntok, int64_t m,
                                                    const float* __restrict__ x_scales, void* y,
                                                    int ydtype, int64_t ldy) {
-  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  if (i >= ntok * m) return;
-  const int64_t t = i / m, r = i % m;
-  float v = partial[i];
-  for (int s = 1; s < splits; ++s) v += partial[(int64_t)s * ntok * m + i];
+  const int64_t t = blockIdx.x, r = (int64_t)blockIdx.y * 1024 + 4 * threadIdx.x;
+  if (r >= m) return;
+  const int count = (int)min(m - r, (int64_t)4);
+  auto load = [&](int s) {
+    const float* p = partial + ((int64_t)s * ntok + t) * m + r;
+    if constexpr (VEC) return *(const f32x4_t*)p;
+    f32x4_t v = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      if (e < count) v[e] = p[e];
+    return v;
+  };
+  f32x4_t v = load(0);
+#pragma unroll 4
+  for (int s = 1; s < splits; ++s) v += load(s);
   if (x_scales) v *= x_scales[t];
-  if (ydtype == PWQ_F32) ((float*)y)[t * ldy + r] = v;
-  else ((__bf16*)y)[t * ldy + r] = (__bf16)v;
+#pragma unroll
+  for (int e = 0; e < 4; ++e)
+    if (e < count) {
+      if (ydtype == PWQ_F32) ((float*)y)[t * ldy + r + e] = v[e];
+      else ((__bf16*)y)[t * ldy + r + e] = (__bf16)v[e];
+    }
 }
 
 // x to the rows prompt_tiles reads: padded with zeros to whole steps, in
@@ -574,13 +622,13 @@ __global__ __launch_bounds__(256) void stage_x(const T* __restrict__ x, int64_t 
   }
 }
 
-template <bool I8, int BT, int BR, int WT, int WR, bool FUSED>
+template <bool I8, int BT, int BR, int WR, bool FUSED>
 void launch_tiles(const PromptArgs& p, int mode, int splits, hipStream_t st) {
   const dim3 grid((unsigned)((p.tiles_t * p.tiles_r + 7) / 8 * 8), (unsigned)splits);
-  const int nt = 64 * WT * WR;
-  if (mode == 0) prompt_tiles<I8, BT, BR, WT, WR, 0, FUSED><<<grid, nt, 0, st>>>(p);
-  else if (mode == 1) prompt_tiles<I8, BT, BR, WT, WR, 1, FUSED><<<grid, nt, 0, st>>>(p);
-  else prompt_tiles<I8, BT, BR, WT, WR, 2, FUSED><<<grid, nt, 0, st>>>(p);
+  const int nt = 64 * WR;
+  if (mode == 0) prompt_tiles<I8, BT, BR, WR, 0, FUSED><<<grid, nt, 0, st>>>(p);
+  else if (mode == 1) prompt_tiles<I8, BT, BR, WR, 1, FUSED><<<grid, nt, 0, st>>>(p);
+  else prompt_tiles<I8, BT, BR, WR, 2, FUSED><<<grid, nt, 0, st>>>(p);
 }
 
 }  // namespace
@@ -602,17 +650,18 @@ PromptPlan prompt_plan(const void* x, int32_t xdtype, int64_t ntok, int64_t ldx,
   p.reps = xdtype == PWQ_F32 ? 3 : 1;
   p.steps = (n + cols - 1) / cols * p.reps;
   p.staged_row = p.steps * KB;
-  // Tile and column splits by their estimated time.  A step takes about
-  // the same whether a CU runs one 128 x 128 tile or two (1.2 to 1.3 us), and
-  // 2.1 us for one of 256 x 256 (bf16; 8-bit steps have twice the columns and
-  // more to multiply by the steps: 1.7 and 2.7 us, twice a step 2.2 and 3.6);
-  // the splits' float32 sums are written and read once at about 4.5 TB/s and
-  // joined by a launch of its own (3 us).  Measured where the two differ most:
-  // 1025 bf16 tokens of 4096 x 14336 213 us as 80 large tiles in 3 splits, 286
-  // as 288 small ones; 512 8-bit tokens of 4096 x 4096 39 us as 128 small
-  // tiles in 4 splits, 47 as 32 large ones in 4.
-  const double us_small = !p.i8 ? 1.3 : (p.mode == 2 ? 2.2 : 1.7);
-  const double us_big = !p.i8 ? 2.1 : (p.mode == 2 ? 3.6 : 2.7);
+  // Tile and column splits by their estimated time: steps of a workgroup of 128
+  // x 128 that has its CU alone, of two that share it, and of one of 128 x 256
+  // (from 256 to 8192 tokens of q_proj, up_proj and down_proj; twice as many
+  // columns and sums in 8 bits, twice a step the most).  The splits' float32
+  // sums are written and read at about 8.5 TB/s, in the last-level cache, and
+  // joined by a launch of its own (3 us).  Where the two tiles differ most: 2048
+  // bf16 tokens of 4096 x 14336 take 266 us in wide ones and 298 in narrow
+  // ones, 700 8-bit tokens of 14336 x 4096 94 and 86; splits: 512 8-bit tokens
+  // of 4096 x 4096 take 28, 26, 28, 27 and 35 us (joined) in 1, 2, 3, 4 and 8.
+  const int kind = !p.i8 ? 0 : (p.mode == 2 ? 2 : 1);
+  const double us_one[] = {0.70, 0.78, 0.95}, us_two[] = {1.2, 1.37, 1.65};
+  const double us_wide[] = {1.05, 1.3, 1.6};
   double best = 0;
   p.fused = n_out == 0 && ntok <= kFusedTokens;
   if (p.fused) {
@@ -626,19 +675,21 @@ PromptPlan prompt_plan(const void* x, int32_t xdtype, int64_t ntok, int64_t ldx,
     p.per = (p.steps + p.splits - 1) / p.splits;
     p.splits = (p.steps + p.per - 1) / p.per;
   }
-  for (int big = 0; big < 2 && !p.fused; ++big) {
-    const int64_t edge = big ? 256 : 128, slots = big ? 256 : 512;
-    const int64_t tt = (ntok + edge - 1) / edge, tr = (m + edge - 1) / edge;
+  for (int wide = 0; wide < 2 && !p.fused; ++wide) {
+    const int64_t tt = (ntok + 127) / 128, edge = wide ? 256 : 128, tr = (m + edge - 1) / edge;
     const int64_t most = std::min<int64_t>(16, std::max<int64_t>(1, p.steps / 4));
     for (int64_t k = 1; k <= most; ++k) {
       const int64_t per = (p.steps + k - 1) / k, splits = (p.steps + per - 1) / per;
       if (splits != k) continue;
-      const int64_t rounds = (tt * tr * splits + slots - 1) / slots;
-      double us = (double)rounds * per * (big ? us_big : us_small);
-      if (splits > 1) us += 3.0 + 2.0 * splits * ntok * m * 4 / 4.5e6;
+      const int64_t groups = tt * tr * splits, left = groups % 512;
+      double us = wide ? (double)((groups + 255) / 256) * us_wide[kind]
+                       : (double)(groups / 512) * us_two[kind] +
+                             (left == 0 ? 0.0 : (left <= 256 ? us_one[kind] : us_two[kind]));
+      us *= per;
+      if (splits > 1) us += 3.0 + 2.0 * splits * ntok * m * 4 / 8.5e6;
       if (best == 0 || us < best) {
         best = us;
-        p.big = big;
+        p.wide = wide;
         p.tiles_t = tt;
         p.tiles_r = tr;
         p.per = per;
@@ -700,9 +751,11 @@ hipError_t launch_prompt(const PackedLinearLaunch& a, const PromptPlan& pl, cons
   p.rows16 = pl.rows16;
   p.ntok = (int)a.ntok;
   p.m = (int)a.m;
-  p.n = (int)a.n;
-  p.G = a.G;
   p.ng = (int)(a.n / a.G);
+  if (pl.mode != 0) {
+    const uint32_t halves = (uint32_t)a.G / (pl.i8 ? 64 : 32);
+    p.per_group = (uint32_t)(((int64_t(1) << 31) + halves - 1) / halves);
+  }
   p.y = a.y;
   p.ydtype = a.ydtype;
   p.ldy = a.ldy;
@@ -713,27 +766,28 @@ hipError_t launch_prompt(const PackedLinearLaunch& a, const PromptPlan& pl, cons
     const dim3 grid((unsigned)((tiles + 3) / 4));
     if (pl.i8)
       spread_weights<true><<<grid, 256, 0, st>>>(
-          a.qweight, a.ldq, a.scales, a.zeros, a.outlier_off, a.outliers, n_out, a.m, p.n, p.G,
-          p.ng, across, tiles, (i32x4_t*)w.spread, p.blocks, w.steps, pl.rows16);
+          a.qweight, a.ldq, a.scales, a.zeros, a.outlier_off, a.outliers, n_out, a.m, (int)a.n,
+          a.G, p.ng, across, tiles, (i32x4_t*)w.spread, p.blocks, w.steps, pl.rows16);
     else
       spread_weights<false><<<grid, 256, 0, st>>>(
-          a.qweight, a.ldq, a.scales, a.zeros, a.outlier_off, a.outliers, n_out, a.m, p.n, p.G,
-          p.ng, across, tiles, (i32x4_t*)w.spread, p.blocks, w.steps, pl.rows16);
+          a.qweight, a.ldq, a.scales, a.zeros, a.outlier_off, a.outliers, n_out, a.m, (int)a.n,
+          a.G, p.ng, across, tiles, (i32x4_t*)w.spread, p.blocks, w.steps, pl.rows16);
   }
   const int mode = pl.mode, k = (int)pl.splits;
   if (pl.fused) {
-    if (pl.i8) launch_tiles<true, 64, 128, 1, 4, true>(p, mode, k, st);
-    else launch_tiles<false, 64, 128, 1, 4, true>(p, mode, k, st);
-  } else if (pl.big) {
-    if (pl.i8) launch_tiles<true, 256, 256, 2, 4, false>(p, mode, k, st);
-    else launch_tiles<false, 256, 256, 2, 4, false>(p, mode, k, st);
+    if (pl.i8) launch_tiles<true, 64, 128, 4, true>(p, mode, k, st);
+    else launch_tiles<false, 64, 128, 4, true>(p, mode, k, st);
+  } else if (pl.wide) {
+    if (pl.i8) launch_tiles<true, 128, 256, 8, false>(p, mode, k, st);
+    else launch_tiles<false, 128, 256, 8, false>(p, mode, k, st);
   } else {
-    if (pl.i8) launch_tiles<true, 128, 128, 2, 2, false>(p, mode, k, st);
-    else launch_tiles<false, 128, 128, 2, 2, false>(p, mode, k, st);
+    if (pl.i8) launch_tiles<true, 128, 128, 4, false>(p, mode, k, st);
+    else launch_tiles<false, 128, 128, 4, false>(p, mode, k, st);
   }
   if (p.partial)
-    prompt_join<<<dim3((unsigned)((a.ntok * a.m + 255) / 256)), 256, 0, st>>>(
-        p.partial, (int)pl.splits, a.ntok, a.m, a.x_scales, a.y, a.ydtype, a.ldy);
+    (a.m % 4 == 0 ? prompt_join<true> : prompt_join<false>)
+        <<<dim3((unsigned)a.ntok, (unsigned)((a.m + 1023) / 1024)), 256, 0, st>>>(
+            p.partial, (int)pl.splits, a.ntok, a.m, a.x_scales, a.y, a.ydtype, a.ldy);
   return hipGetLastError();
 }
 

@@ -213,7 +213,7 @@ size_t rows_staged_bytes(const void* x, int32_t xdtype, int64_t ntok, int64_t n,
 hipError_t launch_rows(PackedLinearLaunch a, void* staged, hipStream_t st);
 // Many tokens: what the product is made of, and its workspace.
 struct PromptPlan {
-  bool ok, i8, big, direct, fused;
+  bool ok, i8, wide, direct, fused;
   int mode, reps;
   int64_t steps, per, splits, tiles_t, tiles_r, staged_row, rows16;
   size_t staged_bytes, spread_bytes, steps_bytes, partial_bytes;
