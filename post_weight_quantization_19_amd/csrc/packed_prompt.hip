@@ -52,19 +52,25 @@ typedef __attribute__((address_space(3))) char lds_char;
 constexpr int KB = 128;            // bytes of an x row per step
 constexpr int64_t kFusedTokens = 128;
 
-// Asynchronous copy of 16 bytes per lane, sbase + voff of each lane to
-// lds + 16 lane (lds and sbase wave-uniform).  M0 is restored.
-__device__ __forceinline__ void copy16(uint32_t voff, const void* sbase, uint32_t lds) {
-  uint32_t keep;
-  asm volatile(
-      "s_mov_b32 %0, m0\n\t"
-      "s_mov_b32 m0, %3\n\t"
-      "global_load_lds_dwordx4 %1, %2\n\t"
-      "s_mov_b32 m0, %0"
-      : "=&s"(keep)
-      : "v"(voff), "s"(sbase), "s"(lds)
-      : "memory");
-}
+// Asynchronous copies of 16 bytes, 4 bytes, or one byte (to a dword) per lane:
+// sbase + voff of each lane to lds + 16 lane, or lds + 4 lane (lds and sbase
+// wave-uniform).  M0 is restored.
+#define PWQ_COPY(NAME, OP)                                                                    \
+  __device__ __forceinline__ void NAME(uint32_t voff, const void* sbase, uint32_t lds) {     \
+    uint32_t keep;                                                                           \
+    asm volatile(                                                                            \
+        "s_mov_b32 %0, m0\n\t"                                                               \
+        "s_mov_b32 m0, %3\n\t" OP                                                            \
+        " %1, %2\n\t"                                                                        \
+        "s_mov_b32 m0, %0"                                                                   \
+        : "=&s"(keep)                                                                        \
+        : "v"(voff), "s"(sbase), "s"(lds)                                                    \
+        : "memory");                                                                         \
+  }
+PWQ_COPY(copy16, "global_load_lds_dwordx4")
+PWQ_COPY(copy4, "global_load_lds_dword")
+PWQ_COPY(copy1, "global_load_lds_ubyte")
+#undef PWQ_COPY
 
 // Byte of 16-byte unit c of LDS row r.
 __device__ __forceinline__ uint32_t unit_at(int r, int c) {
@@ -102,19 +108,38 @@ __device__ __forceinline__ uint4 steps_bf16(uint32_t w, uint32_t bias, float zb)
   return make_uint4(two(lo[0], lo[1]), two(lo[2], lo[3]), two(hi[0], hi[1]), two(hi[2], hi[3]));
 }
 
-// 1.5 2^23 as an integer: int32 sums below 2^22 that start here read as
-// 1.5 2^23 + sum when taken for a float32.
+template <bool I8> using sum_t = std::conditional_t<I8, i32x4_t, f32x4_t>;
+
+template <bool I8>
+__device__ __forceinline__ sum_t<I8> mma(const i32x4_t& x, const i32x4_t& w, const sum_t<I8>& c) {
+  if constexpr (I8) return __builtin_amdgcn_mfma_i32_16x16x64_i8(x, w, c, 0, 0, 0);
+  else
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, x),
+                                                   __builtin_bit_cast(bf16x8_t, w), c, 0, 0, 0);
+}
+
+// What a group's sum starts from, and its value.  1.5 2^23 as an integer: int32
+// sums below 2^22 that start here read as 1.5 2^23 + sum when taken for a
+// float32.
 constexpr int kMagic = 0x4b400000;
+template <bool I8> __device__ __forceinline__ sum_t<I8> sum_start() {
+  if constexpr (I8) return i32x4_t{kMagic, kMagic, kMagic, kMagic};
+  else return f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
+}
+__device__ __forceinline__ float sum_value(const i32x4_t& c, int e) {
+  return __int_as_float(c[e]) - 12582912.0f;
+}
+__device__ __forceinline__ float sum_value(const f32x4_t& c, int e) { return c[e]; }
 
 struct PromptArgs {
   const char* x;          // rows of `steps` * 128 bytes, 16-byte aligned
   int64_t xrow;           // bytes between x rows
   int steps;              // steps over the whole row
   int reps;               // steps per weight block: 1, or 3 parts of float32
-  int per;                // steps per split
+  int per;                // steps (batch_tiles: tiles of 128 columns) per split
   int tiles_t, tiles_r;
   const float* x_scales;
-  // packed weights (FUSED)
+  // packed weights (batch_tiles)
   const uint8_t* qweight;
   int64_t ldq;
   const float* scales;
@@ -131,6 +156,18 @@ struct PromptArgs {
   int64_t ldy;
   float* partial;         // splits x ntok x m, or NULL
 };
+
+// First token and row of this workgroup's tile; false past the last one.  XCD b
+// % 8 owns a contiguous range of tiles, tokens fastest, so that its L2 holds
+// the weights of a few row tiles.
+__device__ __forceinline__ bool tile_of(const PromptArgs& a, int bt, int br, int& t0, int& r0) {
+  const int tiles = a.tiles_t * a.tiles_r;
+  const int b = blockIdx.x, x = b & 7, q = tiles / 8, r = tiles % 8;
+  const int tile = x * q + min(x, r) + (b >> 3);
+  t0 = tile % a.tiles_t * bt;
+  r0 = tile / a.tiles_t * br;
+  return (b >> 3) < q + (x < r ? 1 : 0);
+}
 
 // The operand integers of 16 rows x 128 columns (one wave each) in 8 bits or
 // bf16, and the steps of the groups that start there, group by group.
@@ -203,280 +240,16 @@ __global__ __launch_bounds__(256) void spread_weights(
         scales[min(strip * 16 + lane, m - 1) * ng + g];
 }
 
-// MODE: how often sums are multiplied by their step.  0: one step per row,
-// at the end; 1: every step (G a multiple of its columns); 2: twice a step.
-// FUSED: packed weights are read and spread by the wave that multiplies by
-// them.
-template <bool I8, int BT, int BR, int WR, int MODE, bool FUSED>
-__global__ __launch_bounds__(64 * WR, 2) void prompt_tiles(const PromptArgs a) {
-  constexpr int NT = 64 * WR;
-  constexpr int NI = BT / 16, NJ = BR / WR / 16;
-  constexpr int COLS = I8 ? 128 : 64;         // columns of a step
-  constexpr int XB = BT * KB;
-  constexpr int NC = XB / (16 * NT);          // copies of a wave per step
-  constexpr int YROW = 2 * BR + 32;           // bytes of a token's row of y in LDS
-  constexpr int LDS = 3 * XB > BT * YROW ? 3 * XB : BT * YROW;
-  static_assert(NC * 16 * NT == XB, "tile and threads fit");
-  using acc_t = std::conditional_t<I8, i32x4_t, f32x4_t>;
-  __shared__ __attribute__((aligned(16))) char smem[LDS];
-  lds_char* L = (lds_char*)smem;
-  const uint32_t lbase = (uint32_t)(uintptr_t)L;
-
-  // tile of this workgroup: XCD b % 8 owns a contiguous range of tiles,
-  // tokens fastest, so that its L2 holds the weights of a few row tiles
-  const int tiles = a.tiles_t * a.tiles_r;
-  const int split = blockIdx.y;
-  int tile;
-  {
-    const int b = blockIdx.x, x = b & 7, q = tiles / 8, r = tiles % 8;
-    tile = x * q + min(x, r) + (b >> 3);
-    if ((b >> 3) >= q + (x < r ? 1 : 0)) return;
-  }
-  const int t0 = tile % a.tiles_t * BT, r0 = tile / a.tiles_t * BR;
-  const int s0 = split * a.per, s1 = min(a.steps, s0 + a.per);
-
-  const int tid = threadIdx.x, lane = tid & 63;
+// A tile's sums to y, or to its split's part of the partial sums.  Lane l holds
+// tokens 4 (l / 16) + e, row l % 16 of every block; smem: BT rows of y, free.
+template <int BT, int BR> constexpr int kYBytes = BT * (2 * BR + 32);
+template <int BT, int BR, int NT>
+__device__ __forceinline__ void store_tile(const PromptArgs& a,
+                                           float (&acc)[BT / 16][BR / 16 * 64 / NT][4], char* smem,
+                                           int t0, int r0, int split) {
+  constexpr int NI = BT / 16, NJ = BR / 16 * 64 / NT, YROW = 2 * BR + 32;
+  const int tid = threadIdx.x, lane = tid & 63, lr = lane & 15, lq = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-
-  // x copies: copy h of this lane fills unit 64 (NT / 64 h + wave) + lane
-  uint32_t xoff[NC];
-#pragma unroll
-  for (int h = 0; h < NC; ++h) {
-    const int u = NT * h + 64 * wave + lane, r = u >> 3, c = (u & 7) ^ ((r >> 1) & 7);
-    xoff[h] = (uint32_t)((min(t0 + r, a.ntok - 1) - t0) * a.xrow + 16 * c);
-  }
-  const char* xbase = a.x + (int64_t)t0 * a.xrow;
-  auto copy_x = [&](int s, int slot) {
-    const uint32_t dst = lbase + (uint32_t)slot * XB + 1024u * wave;
-#pragma unroll
-    for (int h = 0; h < NC; ++h) copy16(xoff[h], xbase + (int64_t)s * KB, dst + 16u * NT * h);
-  };
-
-  // weights: block j of this wave is strip r0 / 16 + wave NJ + j (the last one
-  // again past the end); wave-uniform bases, the lane's offset is the same
-  const int lr = lane & 15, lq = lane >> 4;
-  auto strip = [&](int j) {
-    return min(r0 / 16 + wave * NJ + j, (int)(a.rows16 / 16) - 1);
-  };
-  constexpr int NS = MODE == 2 ? 2 : 1;
-  constexpr int NX = 4;                       // operands of x, read three ahead
-  // 16-byte unit of an LDS row that lane group lq of half h works on.  FUSED:
-  // both halves' packed codes next to each other in memory, unless a half has
-  // to stay within a group of its own.
-  constexpr bool PAIRED = FUSED && MODE != 2;
-  auto unit = [&](int h) { return PAIRED ? 2 * lq + h : 4 * h + lq; };
-  constexpr int PB = I8 ? 8 : 4;               // packed bytes of a lane's half
-  struct Weights {
-    i32x4_t w[FUSED ? 1 : NJ][FUSED ? 1 : 2];
-    uint32_t p[FUSED ? NJ : 1][FUSED ? PB / 2 : 1];   // FUSED: both halves' codes
-    float s[NJ][NS];
-    int z[FUSED ? NJ : 1][NS];
-  };
-  uint32_t row[NJ];                            // of the tile, the lane's in block j
-#pragma unroll
-  for (int j = 0; j < NJ; ++j) row[j] = (uint32_t)(min(r0 + 16 * (wave * NJ + j) + lr, a.m - 1) - r0);
-  const uint8_t* const qbase = FUSED ? a.qweight + r0 * a.ldq : nullptr;
-  const float* const sbase = FUSED ? a.scales + (int64_t)r0 * a.ng : nullptr;
-  // (SYM reads the steps' bytes in the zero points' place and uses 8)
-  const bool asym = FUSED && a.zeros != nullptr;
-  const uint8_t* const zbase = asym ? a.zeros + (int64_t)r0 * a.ng : (const uint8_t*)sbase;
-  auto block_of = [&](int s) { return a.reps == 1 ? s : s / 3; };
-  auto load_w = [&](Weights& b, int s) {
-    const int blk = block_of(s);
-    if constexpr (FUSED) {
-#pragma unroll
-      for (int j = 0; j < NJ; ++j) {
-        const uint32_t at = row[j] * (uint32_t)a.ldq;
-        if constexpr (PAIRED) {
-          const uint32_t o = blk * (COLS / 2) + 2 * PB * lq;
-          __builtin_memcpy(b.p[j], qbase + (at + (o < a.ldq ? o : 0)), 2 * PB);
-        } else {
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const uint32_t o = blk * (COLS / 2) + 4 * PB * h + PB * lq;
-            __builtin_memcpy(&b.p[j][h * (PB / 4)], qbase + (at + (o < a.ldq ? o : 0)), PB);
-          }
-        }
-      }
-    } else {
-#pragma unroll
-      for (int j = 0; j < NJ; ++j)
-#pragma unroll
-        for (int h = 0; h < 2; ++h)
-          b.w[j][h] =
-              (a.spread + ((int64_t)strip(j) * a.blocks + blk) * 128 + 64 * h)[(uint32_t)lane];
-    }
-  };
-  auto load_s = [&](Weights& b, int s) {
-    if constexpr (!FUSED && MODE == 0) return;
-    const int blk = block_of(s);
-#pragma unroll
-    for (int h = 0; h < NS; ++h) {
-      const int g = MODE == 0 ? 0 : min((int)__umulhi(4 * blk + 2 * h, a.per_group), a.ng - 1);
-#pragma unroll
-      for (int j = 0; j < NJ; ++j) {
-        if constexpr (FUSED) {
-          b.s[j][h] = sbase[row[j] * a.ng + g];
-          b.z[j][h] = zbase[row[j] * a.ng + g];
-        } else {
-          b.s[j][h] = (a.steps_t + g * a.rows16 + 16 * strip(j))[(uint32_t)lr];
-        }
-      }
-    }
-  };
-  // the compiler waits for the weights' registers here
-  auto arrived = [&](Weights& b) {
-#pragma unroll
-    for (int j = 0; j < NJ; ++j) {
-      if constexpr (FUSED) {
-#pragma unroll
-        for (int i = 0; i < PB / 2; ++i) asm volatile("" : "+v"(b.p[j][i])::"memory");
-      } else {
-        asm volatile("" : "+v"(b.w[j][0]), "+v"(b.w[j][1])::"memory");
-      }
-    }
-  };
-  const uint32_t flip = asym ? 0u : 0x88888888u, bias = asym ? 0x41804180u : 0x41c041c0u;
-  auto operand = [&](const Weights& b, int j, int h) -> i32x4_t {
-    if constexpr (!FUSED) {
-      return b.w[j][h];
-    } else {
-      const int z = asym ? b.z[j][NS == 2 ? h : 0] : 8;
-      if constexpr (I8) {
-        const uint32_t z4 = (uint32_t)z * 0x01010101u;
-        const uint2 lo = steps_i8(b.p[j][2 * h] ^ flip, z4);
-        const uint2 hi = steps_i8(b.p[j][2 * h + 1] ^ flip, z4);
-        return i32x4_t{(int)lo.x, (int)lo.y, (int)hi.x, (int)hi.y};
-      } else {
-        return __builtin_bit_cast(i32x4_t, steps_bf16(b.p[j][h], bias, 16.0f + (float)z));
-      }
-    }
-  };
-
-  float acc[NI][NJ][4];
-  acc_t dir[MODE == 0 ? NI : 1][MODE == 0 ? NJ : 1];
-#pragma unroll
-  for (int i = 0; i < NI; ++i)
-#pragma unroll
-    for (int j = 0; j < NJ; ++j) {
-#pragma unroll
-      for (int e = 0; e < 4; ++e) acc[i][j][e] = 0.0f;
-      if constexpr (MODE == 0) dir[i][j] = acc_t{0, 0, 0, 0};
-    }
-
-  auto mma = [&](const i32x4_t& x, const i32x4_t& w, const acc_t& c) -> acc_t {
-    if constexpr (I8) return __builtin_amdgcn_mfma_i32_16x16x64_i8(x, w, c, 0, 0, 0);
-    else
-      return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, x),
-                                                     __builtin_bit_cast(bf16x8_t, w), c, 0, 0, 0);
-  };
-  // what a block's sum starts from, and its value
-  acc_t zero = {0, 0, 0, 0};
-  if constexpr (I8) zero = acc_t{kMagic, kMagic, kMagic, kMagic};
-  auto value = [](const acc_t& c, int e) {
-    if constexpr (I8) return __int_as_float(c[e]) - 12582912.0f;
-    else return c[e];
-  };
-
-  // prologue: steps s0 and s0 + 1 on their way
-  const int last = s1 - 1;
-  Weights b[3];
-  auto ask = [&](int s, int slot, Weights& b) {
-    load_s(b, s);
-    copy_x(s, slot);
-    load_w(b, s);
-  };
-  ask(s0, 0, b[0]);
-  ask(min(s0 + 1, last), 1, b[1]);
-
-  auto step = [&](int s, int slot, Weights& b, Weights& bn) {
-    // This step's x and weights, asked for two steps ago, have arrived: the
-    // weights came last and loads return in order, so that the wait for the
-    // weights' registers covers the x of this wave.  Past the barrier every
-    // wave's part of this step's x is there, and the slot before it is free.
-    arrived(b);
-    lds_barrier();
-    ask(min(s + 2, last), (slot + 2) % 3, bn);
-    const char* xs = smem + slot * XB;
-    i32x4_t x[NX][2];
-    i32x4_t w[NJ][2];
-#pragma unroll
-    for (int j = 0; j < NJ; ++j)
-#pragma unroll
-      for (int h = 0; h < 2; ++h) w[j][h] = operand(b, j, h);
-    float(&sc)[NJ][NS] = b.s;
-    auto read_x = [&](int i) {
-#pragma unroll
-      for (int h = 0; h < 2; ++h)
-        x[i % NX][h] = *(const i32x4_t*)(xs + unit_at(16 * i + lr, unit(h)));
-    };
-#pragma unroll
-    for (int i = 0; i < NX - 1; ++i) read_x(i);
-    if constexpr (MODE == 0) {
-#pragma unroll
-      for (int i = 0; i < NI; ++i) {
-        if (i + NX - 1 < NI) read_x(i + NX - 1);
-#pragma unroll
-        for (int h = 0; h < 2; ++h)
-#pragma unroll
-          for (int j = 0; j < NJ; ++j) dir[i][j] = mma(x[i % NX][h], w[j][h], dir[i][j]);
-      }
-    } else {
-      // Blocks of 16 x 16 in turn: one starts, the one before gets its second
-      // half (MODE 1), the third before is multiplied by its step, so that
-      // neither waits for a matrix instruction's result.
-      constexpr int NU = NI * NJ * NS;
-      acc_t c[4];
-      auto scale = [&](auto uu, int e0) {
-        constexpr int u = decltype(uu)::value;
-        constexpr int i = u / NS / NJ, j = u / NS % NJ, h = u % NS;
-#pragma unroll
-        for (int e = e0; e < e0 + 2; ++e) {
-          acc[i][j][e] = fmaf(sc[j][h], value(c[u & 3], e), acc[i][j][e]);
-          pin(acc[i][j][e]);       // here: not moved behind the other products
-        }
-      };
-      static_for_up<NU + 3>([&](auto uu) {
-        constexpr int u = decltype(uu)::value;
-        constexpr int i = u / NS / NJ, j = u / NS % NJ, h = u % NS;
-        if constexpr (u < NU) {
-          c[u & 3] = mma(x[i % NX][h], w[j][h], zero);
-          if constexpr (j == 1 && h == 0 && i + NX - 1 < NI) read_x(i + NX - 1);
-        }
-        if constexpr (u >= 3) scale(std::integral_constant<int, u - 3>{}, 0);
-        __builtin_amdgcn_sched_barrier(0);
-        if constexpr (MODE == 1 && u > 0 && u <= NU) {
-          constexpr int v = u - 1, iv = v / NJ, jv = v % NJ;
-          c[v & 3] = mma(x[iv % NX][1], w[jv][1], c[v & 3]);
-        }
-        if constexpr (u >= 3) scale(std::integral_constant<int, u - 3>{}, 2);
-        __builtin_amdgcn_sched_barrier(0);
-      });
-    }
-  };
-  int s = s0;
-  for (; s + 2 < s1; s += 3) {
-    step(s, 0, b[0], b[2]);
-    step(s + 1, 1, b[1], b[0]);
-    step(s + 2, 2, b[2], b[1]);
-  }
-  if (s < s1) step(s, 0, b[0], b[2]);
-  if (s + 1 < s1) step(s + 1, 1, b[1], b[0]);
-  // nothing is in flight to LDS, and no wave reads it, at the end
-  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-  lds_barrier();
-  if constexpr (MODE == 0) {
-#pragma unroll
-    for (int j = 0; j < NJ; ++j) {
-      const float sj = FUSED ? sbase[row[j] * a.ng] : a.steps_t[16 * strip(j) + lr];
-#pragma unroll
-      for (int i = 0; i < NI; ++i)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) acc[i][j][e] = sj * (float)dir[i][j][e];
-    }
-  }
-
-  // lane l holds tokens 4 (l / 16) + e, row l % 16 of every block
   const bool split_sum = a.partial != nullptr;
   if (a.x_scales && !split_sum) {
 #pragma unroll
@@ -543,6 +316,387 @@ __global__ __launch_bounds__(64 * WR, 2) void prompt_tiles(const PromptArgs a) {
         if (r + e < a.m) dst[e] = ((const __bf16*)src)[e];
     }
   }
+}
+
+// Up to 128 tokens: tiles of BT tokens x 128 rows that read the packed codes, in
+// tiles of 128 columns.  NP: x steps of such a tile (8-bit 1, bf16 2, float32
+// 6).  Everything comes by asynchronous copies two tiles ahead: x for the
+// workgroup, 32 rows of weights (2 KB), their steps and zero points for the
+// wave that spreads them and multiplies by them.  Lanes next to each other copy
+// bytes next to each other; loads in the operands' layout, one cache lookup a
+// lane, took 33 us for 32 bf16 tokens of up_proj, these 21.
+constexpr int batch_lds(int np, int bt, int sc, bool asym) {
+  return 3 * np * bt * KB + 12 * (2048 + sc * (asym ? 512 : 256));
+}
+constexpr int batch_steps(bool i8, int mode) {       // copies of 64 steps of a tile
+  return mode == 0 ? 0 : (!i8 && mode == 2 ? 2 : 1);
+}
+template <bool I8, int NP, int BT, int MODE, bool ASYM>
+__global__ __launch_bounds__(
+    256, batch_lds(NP, BT, batch_steps(I8, MODE), ASYM) <= 80 * 1024 ? 2 : 1)
+void batch_tiles(const PromptArgs a) {
+  constexpr int BR = 128, NI = BT / 16, NJ = 2;
+  constexpr int SUB = I8 ? 1 : 2, REPS = NP / SUB;      // blocks of a tile, x parts
+  constexpr int NS = MODE == 2 ? 2 : 1;                 // steps of a block
+  constexpr int SC = batch_steps(I8, MODE);             // SUB NS groups of 32 rows
+  constexpr int XS = NP * BT * KB, NC = BT / 32;        // x of a tile; copies of an x step
+  constexpr int WS = 2048 + SC * 256 * (ASYM ? 2 : 1);  // the wave's part of a tile
+  constexpr int COPIES = NP * NC + 2 + SC * (ASYM ? 2 : 1);
+  constexpr int LDS = batch_lds(NP, BT, SC, ASYM);
+  static_assert(LDS == 3 * XS + 12 * WS && LDS >= kYBytes<BT, BR>, "what is used");
+  using acc_t = sum_t<I8>;
+  __shared__ __attribute__((aligned(16))) char smem[LDS];
+  const uint32_t lbase = (uint32_t)(uintptr_t)(lds_char*)smem;
+  int t0, r0;
+  if (!tile_of(a, BT, BR, t0, r0)) return;
+  const int split = blockIdx.y;
+  const int tid = threadIdx.x, lane = tid & 63, lr = lane & 15, lq = lane >> 4;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int across = (a.blocks + SUB - 1) / SUB;
+  const int k0 = split * a.per, k1 = min(across, k0 + a.per), last = k1 - 1;
+
+  // copies
+  uint32_t xoff[NC], woff[2], wcol[2], row0[2];
+#pragma unroll
+  for (int h = 0; h < NC; ++h) {
+    const int u = 256 * h + tid, r = u >> 3, c = (u & 7) ^ ((r >> 1) & 7);
+    xoff[h] = (uint32_t)((min(t0 + r, a.ntok - 1) - t0) * a.xrow + 16 * c);
+  }
+  const int wr0 = r0 + 32 * wave;                       // the wave's rows
+  const int rbase = min(wr0, a.m - 1), rows = min(a.m - rbase, 32);
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const int r = lane >> 2, c = (lane & 3) ^ (r >> 2);
+    woff[h] = (uint32_t)(min(16 * h + r, rows - 1) * (int)a.ldq);
+    wcol[h] = 16u * c;
+  }
+  const uint32_t srow = (uint32_t)(min(lane & 31, rows - 1) * a.ng);
+  const char* const xbase = a.x + (int64_t)t0 * a.xrow;
+  const uint8_t* const qbase = a.qweight + (int64_t)rbase * a.ldq;
+  const float* const sbase = a.scales + (int64_t)rbase * a.ng;
+  const uint8_t* const zbase = ASYM ? a.zeros + (int64_t)rbase * a.ng : nullptr;
+  const uint32_t own = 3 * XS + wave * 3 * WS;
+  auto ask = [&](int kt, int slot) {
+#pragma unroll
+    for (int p = 0; p < NP; ++p)
+#pragma unroll
+      for (int h = 0; h < NC; ++h)
+        copy16(xoff[h], xbase + (int64_t)min(kt * NP + p, a.steps - 1) * KB,
+               lbase + slot * XS + p * BT * KB + 4096u * h + 1024u * wave);
+    const uint32_t dst = lbase + own + slot * WS;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const uint32_t o = 64u * kt + wcol[h];
+      copy16(woff[h] + (o < a.ldq ? o : 0), qbase, dst + 1024u * h);
+    }
+#pragma unroll
+    for (int h = 0; h < SC; ++h) {
+      // groups 2 h and 2 h + 1 of the tile, 32 rows each
+      const uint32_t half = (I8 ? 2 : 4) * kt + (2 / NS) * (2 * h + (lane >> 5));
+      const uint32_t at = srow + min((int)__umulhi(2 * half, a.per_group), a.ng - 1);
+      copy4(4 * at, sbase, dst + 2048u + 256u * h);
+      if constexpr (ASYM) copy1(at, zbase, dst + 2048u + 256u * (SC + h));
+    }
+  };
+
+  float acc[NI][NJ][4];
+  acc_t dir[MODE == 0 ? NI : 1][MODE == 0 ? NJ : 1];
+#pragma unroll
+  for (int i = 0; i < NI; ++i)
+#pragma unroll
+    for (int j = 0; j < NJ; ++j) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) acc[i][j][e] = 0.0f;
+      if constexpr (MODE == 0) dir[i][j] = acc_t{0, 0, 0, 0};
+    }
+  float s_row[NJ];                                      // MODE 0
+  int z_row[NJ];
+#pragma unroll
+  for (int j = 0; j < NJ; ++j) {
+    s_row[j] = MODE == 0 ? sbase[min(16 * j + lr, rows - 1)] : 0.0f;
+    z_row[j] = MODE == 0 && ASYM ? zbase[min(16 * j + lr, rows - 1)] : 8;
+  }
+
+  // 16-byte unit of an x row that lane group lq of half h works on: both
+  // halves' codes next to each other, unless a half has a step of its own
+  constexpr bool PAIRED = MODE != 2;
+  auto unit = [&](int h) { return PAIRED ? 2 * lq + h : 4 * h + lq; };
+  constexpr int PB = I8 ? 8 : 4;                        // packed bytes of a lane's half
+  constexpr uint32_t flip = ASYM ? 0u : 0x88888888u, bias = ASYM ? 0x41804180u : 0x41c041c0u;
+
+  ask(k0, 0);
+  ask(min(k0 + 1, last), 1);
+  for (int kt = k0, slot = 0; kt < k1; ++kt, slot = slot == 2 ? 0 : slot + 1) {
+    // All but the next tile's copies have landed; past the barrier every wave's
+    // have, and the slot before this one is free.
+    asm volatile("s_waitcnt vmcnt(%0)" ::"n"(COPIES) : "memory");
+    lds_barrier();
+    ask(min(kt + 2, last), slot == 0 ? 2 : slot - 1);
+    const char* const ws = smem + own + slot * WS;
+    const float* const steps = (const float*)(ws + 2048);
+    const int* const zeros = (const int*)(ws + 2048 + 256 * SC);
+#pragma unroll
+    for (int sub = 0; sub < SUB; ++sub) {
+      if (SUB * kt + sub >= a.blocks) break;
+      i32x4_t w[NJ][2];
+      float sc[NJ][NS];
+#pragma unroll
+      for (int j = 0; j < NJ; ++j) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const int o = 32 * sub + (PAIRED ? 2 * PB * lq + PB * h : 4 * PB * h + PB * lq);
+          uint32_t p[PB / 4];
+          __builtin_memcpy(p, ws + 1024 * j + 64 * lr + (((o >> 4) ^ (lr >> 2)) << 4) + (o & 15),
+                           PB);
+          const int at = 32 * (sub * NS + (NS == 2 ? h : 0)) + 16 * j + lr;
+          const int z = MODE != 0 && ASYM ? zeros[at] : z_row[j];
+          if (MODE != 0 && h < NS) sc[j][h] = steps[at];
+          if constexpr (I8) {
+            const uint32_t z4 = (uint32_t)z * 0x01010101u;
+            const uint2 lo = steps_i8(p[0] ^ flip, z4), hi = steps_i8(p[1] ^ flip, z4);
+            w[j][h] = i32x4_t{(int)lo.x, (int)lo.y, (int)hi.x, (int)hi.y};
+          } else {
+            w[j][h] = __builtin_bit_cast(i32x4_t, steps_bf16(p[0], bias, 16.0f + (float)z));
+          }
+        }
+      }
+      acc_t c[NI][NJ][NS];
+#pragma unroll
+      for (int part = 0; part < REPS; ++part) {
+        const char* const xs = smem + slot * XS + (sub * REPS + part) * BT * KB;
+#pragma unroll
+        for (int i = 0; i < NI; ++i) {
+          i32x4_t x[2];
+#pragma unroll
+          for (int h = 0; h < 2; ++h)
+            x[h] = *(const i32x4_t*)(xs + unit_at(16 * i + lr, unit(h)));
+#pragma unroll
+          for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int j = 0; j < NJ; ++j) {
+              if constexpr (MODE == 0) {
+                dir[i][j] = mma<I8>(x[h], w[j][h], dir[i][j]);
+              } else {
+                acc_t& o = c[i][j][NS == 2 ? h : 0];
+                const bool first = part == 0 && (NS == 2 || h == 0);
+                o = mma<I8>(x[h], w[j][h], first ? sum_start<I8>() : o);
+              }
+            }
+        }
+      }
+      if constexpr (MODE != 0)
+#pragma unroll
+        for (int i = 0; i < NI; ++i)
+#pragma unroll
+          for (int j = 0; j < NJ; ++j)
+#pragma unroll
+            for (int h = 0; h < NS; ++h)
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                acc[i][j][e] = fmaf(sc[j][h], sum_value(c[i][j][h], e), acc[i][j][e]);
+                pin(acc[i][j][e]);
+              }
+    }
+  }
+  // nothing is in flight to LDS, and no wave reads it, at the end
+  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+  lds_barrier();
+  if constexpr (MODE == 0) {
+#pragma unroll
+    for (int i = 0; i < NI; ++i)
+#pragma unroll
+      for (int j = 0; j < NJ; ++j)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) acc[i][j][e] = s_row[j] * (float)dir[i][j][e];
+  }
+  store_tile<BT, BR, 256>(a, acc, smem, t0, r0, split);
+}
+
+// MODE: how often sums are multiplied by their step.  0: one step per row,
+// at the end; 1: every step (G a multiple of its columns); 2: twice a step.
+template <bool I8, int BT, int BR, int WR, int MODE>
+__global__ __launch_bounds__(64 * WR, 2) void prompt_tiles(const PromptArgs a) {
+  constexpr int NT = 64 * WR;
+  constexpr int NI = BT / 16, NJ = BR / WR / 16;
+  constexpr int COLS = I8 ? 128 : 64;         // columns of a step
+  constexpr int XB = BT * KB;
+  constexpr int NC = XB / (16 * NT);          // copies of a wave per step
+  constexpr int LDS = 3 * XB > kYBytes<BT, BR> ? 3 * XB : kYBytes<BT, BR>;
+  static_assert(NC * 16 * NT == XB, "tile and threads fit");
+  using acc_t = sum_t<I8>;
+  __shared__ __attribute__((aligned(16))) char smem[LDS];
+  lds_char* L = (lds_char*)smem;
+  const uint32_t lbase = (uint32_t)(uintptr_t)L;
+
+  int t0, r0;
+  if (!tile_of(a, BT, BR, t0, r0)) return;
+  const int split = blockIdx.y;
+  const int s0 = split * a.per, s1 = min(a.steps, s0 + a.per);
+
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+
+  // x copies: copy h of this lane fills unit 64 (NT / 64 h + wave) + lane
+  uint32_t xoff[NC];
+#pragma unroll
+  for (int h = 0; h < NC; ++h) {
+    const int u = NT * h + 64 * wave + lane, r = u >> 3, c = (u & 7) ^ ((r >> 1) & 7);
+    xoff[h] = (uint32_t)((min(t0 + r, a.ntok - 1) - t0) * a.xrow + 16 * c);
+  }
+  const char* xbase = a.x + (int64_t)t0 * a.xrow;
+  auto copy_x = [&](int s, int slot) {
+    const uint32_t dst = lbase + (uint32_t)slot * XB + 1024u * wave;
+#pragma unroll
+    for (int h = 0; h < NC; ++h) copy16(xoff[h], xbase + (int64_t)s * KB, dst + 16u * NT * h);
+  };
+
+  // weights: block j of this wave is strip r0 / 16 + wave NJ + j (the last one
+  // again past the end); wave-uniform bases, the lane's offset is the same
+  const int lr = lane & 15, lq = lane >> 4;
+  auto strip = [&](int j) {
+    return min(r0 / 16 + wave * NJ + j, (int)(a.rows16 / 16) - 1);
+  };
+  constexpr int NS = MODE == 2 ? 2 : 1;
+  constexpr int NX = 4;                       // operands of x, read three ahead
+  struct Weights {
+    i32x4_t w[NJ][2];
+    float s[NJ][NS];
+  };
+  auto block_of = [&](int s) { return a.reps == 1 ? s : s / 3; };
+  auto load_w = [&](Weights& b, int s) {
+    const int blk = block_of(s);
+#pragma unroll
+    for (int j = 0; j < NJ; ++j)
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+        b.w[j][h] =
+            (a.spread + ((int64_t)strip(j) * a.blocks + blk) * 128 + 64 * h)[(uint32_t)lane];
+  };
+  auto load_s = [&](Weights& b, int s) {
+    if constexpr (MODE == 0) return;
+    const int blk = block_of(s);
+#pragma unroll
+    for (int h = 0; h < NS; ++h) {
+      const int g = min((int)__umulhi(4 * blk + 2 * h, a.per_group), a.ng - 1);
+#pragma unroll
+      for (int j = 0; j < NJ; ++j)
+        b.s[j][h] = (a.steps_t + g * a.rows16 + 16 * strip(j))[(uint32_t)lr];
+    }
+  };
+  // the compiler waits for the weights' registers here
+  auto arrived = [&](Weights& b) {
+#pragma unroll
+    for (int j = 0; j < NJ; ++j)
+      asm volatile("" : "+v"(b.w[j][0]), "+v"(b.w[j][1])::"memory");
+  };
+
+  float acc[NI][NJ][4];
+  acc_t dir[MODE == 0 ? NI : 1][MODE == 0 ? NJ : 1];
+#pragma unroll
+  for (int i = 0; i < NI; ++i)
+#pragma unroll
+    for (int j = 0; j < NJ; ++j) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) acc[i][j][e] = 0.0f;
+      if constexpr (MODE == 0) dir[i][j] = acc_t{0, 0, 0, 0};
+    }
+
+  const acc_t zero = sum_start<I8>();
+  // prologue: steps s0 and s0 + 1 on their way
+  const int last = s1 - 1;
+  Weights b[3];
+  auto ask = [&](int s, int slot, Weights& b) {
+    load_s(b, s);
+    copy_x(s, slot);
+    load_w(b, s);
+  };
+  ask(s0, 0, b[0]);
+  ask(min(s0 + 1, last), 1, b[1]);
+
+  auto step = [&](int s, int slot, Weights& b, Weights& bn) {
+    // This step's x and weights, asked for two steps ago, have arrived: the
+    // weights came last and loads return in order, so that the wait for the
+    // weights' registers covers the x of this wave.  Past the barrier every
+    // wave's part of this step's x is there, and the slot before it is free.
+    arrived(b);
+    lds_barrier();
+    ask(min(s + 2, last), (slot + 2) % 3, bn);
+    const char* xs = smem + slot * XB;
+    i32x4_t x[NX][2];
+    i32x4_t(&w)[NJ][2] = b.w;
+    float(&sc)[NJ][NS] = b.s;
+    auto read_x = [&](int i) {
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+        x[i % NX][h] = *(const i32x4_t*)(xs + unit_at(16 * i + lr, 4 * h + lq));
+    };
+#pragma unroll
+    for (int i = 0; i < NX - 1; ++i) read_x(i);
+    if constexpr (MODE == 0) {
+#pragma unroll
+      for (int i = 0; i < NI; ++i) {
+        if (i + NX - 1 < NI) read_x(i + NX - 1);
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+          for (int j = 0; j < NJ; ++j) dir[i][j] = mma<I8>(x[i % NX][h], w[j][h], dir[i][j]);
+      }
+    } else {
+      // Blocks of 16 x 16 in turn: one starts, the one before gets its second
+      // half (MODE 1), the third before is multiplied by its step, so that
+      // neither waits for a matrix instruction's result.
+      constexpr int NU = NI * NJ * NS;
+      acc_t c[4];
+      auto scale = [&](auto uu, int e0) {
+        constexpr int u = decltype(uu)::value;
+        constexpr int i = u / NS / NJ, j = u / NS % NJ, h = u % NS;
+#pragma unroll
+        for (int e = e0; e < e0 + 2; ++e) {
+          acc[i][j][e] = fmaf(sc[j][h], sum_value(c[u & 3], e), acc[i][j][e]);
+          pin(acc[i][j][e]);       // here: not moved behind the other products
+        }
+      };
+      static_for_up<NU + 3>([&](auto uu) {
+        constexpr int u = decltype(uu)::value;
+        constexpr int i = u / NS / NJ, j = u / NS % NJ, h = u % NS;
+        if constexpr (u < NU) {
+          c[u & 3] = mma<I8>(x[i % NX][h], w[j][h], zero);
+          if constexpr (j == 1 && h == 0 && i + NX - 1 < NI) read_x(i + NX - 1);
+        }
+        if constexpr (u >= 3) scale(std::integral_constant<int, u - 3>{}, 0);
+        __builtin_amdgcn_sched_barrier(0);
+        if constexpr (MODE == 1 && u > 0 && u <= NU) {
+          constexpr int v = u - 1, iv = v / NJ, jv = v % NJ;
+          c[v & 3] = mma<I8>(x[iv % NX][1], w[jv][1], c[v & 3]);
+        }
+        if constexpr (u >= 3) scale(std::integral_constant<int, u - 3>{}, 2);
+        __builtin_amdgcn_sched_barrier(0);
+      });
+    }
+  };
+  int s = s0;
+  for (; s + 2 < s1; s += 3) {
+    step(s, 0, b[0], b[2]);
+    step(s + 1, 1, b[1], b[0]);
+    step(s + 2, 2, b[2], b[1]);
+  }
+  if (s < s1) step(s, 0, b[0], b[2]);
+  if (s + 1 < s1) step(s + 1, 1, b[1], b[0]);
+  // nothing is in flight to LDS, and no wave reads it, at the end
+  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+  lds_barrier();
+  if constexpr (MODE == 0) {
+#pragma unroll
+    for (int j = 0; j < NJ; ++j) {
+      const float sj = a.steps_t[16 * strip(j) + lr];
+#pragma unroll
+      for (int i = 0; i < NI; ++i)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) acc[i][j][e] = sj * (float)dir[i][j][e];
+    }
+  }
+
+  store_tile<BT, BR, NT>(a, acc, smem, t0, r0, split);
 }
 
 // Sum of the splits in their order: a token and 1024 columns per workgroup,
@@ -622,13 +776,30 @@ __global__ __launch_bounds__(256) void stage_x(const T* __restrict__ x, int64_t 
   }
 }
 
-template <bool I8, int BT, int BR, int WR, bool FUSED>
+dim3 tile_grid(const PromptArgs& p, int splits) {
+  return dim3((unsigned)((p.tiles_t * p.tiles_r + 7) / 8 * 8), (unsigned)splits);
+}
+
+template <bool I8, int BT, int BR, int WR>
 void launch_tiles(const PromptArgs& p, int mode, int splits, hipStream_t st) {
-  const dim3 grid((unsigned)((p.tiles_t * p.tiles_r + 7) / 8 * 8), (unsigned)splits);
-  const int nt = 64 * WR;
-  if (mode == 0) prompt_tiles<I8, BT, BR, WR, 0, FUSED><<<grid, nt, 0, st>>>(p);
-  else if (mode == 1) prompt_tiles<I8, BT, BR, WR, 1, FUSED><<<grid, nt, 0, st>>>(p);
-  else prompt_tiles<I8, BT, BR, WR, 2, FUSED><<<grid, nt, 0, st>>>(p);
+  const dim3 grid = tile_grid(p, splits);
+  if (mode == 0) prompt_tiles<I8, BT, BR, WR, 0><<<grid, 64 * WR, 0, st>>>(p);
+  else if (mode == 1) prompt_tiles<I8, BT, BR, WR, 1><<<grid, 64 * WR, 0, st>>>(p);
+  else prompt_tiles<I8, BT, BR, WR, 2><<<grid, 64 * WR, 0, st>>>(p);
+}
+
+template <bool I8, int NP, int BT, bool ASYM>
+void launch_batch_mode(const PromptArgs& p, int mode, int splits, hipStream_t st) {
+  const dim3 grid = tile_grid(p, splits);
+  if (mode == 0) batch_tiles<I8, NP, BT, 0, ASYM><<<grid, 256, 0, st>>>(p);
+  else if (mode == 1) batch_tiles<I8, NP, BT, 1, ASYM><<<grid, 256, 0, st>>>(p);
+  else batch_tiles<I8, NP, BT, 2, ASYM><<<grid, 256, 0, st>>>(p);
+}
+
+template <bool I8, int NP, int BT>
+void launch_batch(const PromptArgs& p, int mode, int splits, hipStream_t st) {
+  p.zeros ? launch_batch_mode<I8, NP, BT, true>(p, mode, splits, st)
+          : launch_batch_mode<I8, NP, BT, false>(p, mode, splits, st);
 }
 
 }  // namespace
@@ -665,15 +836,14 @@ PromptPlan prompt_plan(const void* x, int32_t xdtype, int64_t ntok, int64_t ldx,
   double best = 0;
   p.fused = n_out == 0 && ntok <= kFusedTokens;
   if (p.fused) {
-    // 64 x 128 tiles; about 512 workgroups, splits of at least 512 columns (up_proj
-    // 64 8-bit tokens: 26.6 us so, 33.5 with 1024, 29.4 with 256; q_proj 64
-    // bf16 tokens 20.0 us with splits of 512 columns, 25.2 of 256)
-    p.tiles_t = (ntok + 63) / 64;
+    // 32 x 128 or 64 x 128 tiles; about 512 workgroups, splits of at least 512 columns
+    p.token_tile = ntok <= 32 || p.reps == 3 ? 32 : 64;
+    p.tiles_t = (ntok + p.token_tile - 1) / p.token_tile;
     p.tiles_r = (m + 127) / 128;
-    const int64_t tiles = p.tiles_t * p.tiles_r;
-    p.splits = std::max<int64_t>(1, std::min<int64_t>(512 / tiles, p.steps * cols / p.reps / 512));
-    p.per = (p.steps + p.splits - 1) / p.splits;
-    p.splits = (p.steps + p.per - 1) / p.per;
+    const int64_t tiles = p.tiles_t * p.tiles_r, across = (n + 127) / 128;
+    p.splits = std::max<int64_t>(1, std::min<int64_t>(512 / tiles, across / 4));
+    p.per = (across + p.splits - 1) / p.splits;
+    p.splits = (across + p.per - 1) / p.per;
   }
   for (int wide = 0; wide < 2 && !p.fused; ++wide) {
     const int64_t tt = (ntok + 127) / 128, edge = wide ? 256 : 128, tr = (m + edge - 1) / edge;
@@ -775,14 +945,16 @@ hipError_t launch_prompt(const PackedLinearLaunch& a, const PromptPlan& pl, cons
   }
   const int mode = pl.mode, k = (int)pl.splits;
   if (pl.fused) {
-    if (pl.i8) launch_tiles<true, 64, 128, 4, true>(p, mode, k, st);
-    else launch_tiles<false, 64, 128, 4, true>(p, mode, k, st);
+    const bool few = pl.token_tile == 32;
+    if (pl.i8) (few ? launch_batch<true, 1, 32> : launch_batch<true, 1, 64>)(p, mode, k, st);
+    else if (pl.reps == 3) launch_batch<false, 6, 32>(p, mode, k, st);
+    else (few ? launch_batch<false, 2, 32> : launch_batch<false, 2, 64>)(p, mode, k, st);
   } else if (pl.wide) {
-    if (pl.i8) launch_tiles<true, 128, 256, 8, false>(p, mode, k, st);
-    else launch_tiles<false, 128, 256, 8, false>(p, mode, k, st);
+    if (pl.i8) launch_tiles<true, 128, 256, 8>(p, mode, k, st);
+    else launch_tiles<false, 128, 256, 8>(p, mode, k, st);
   } else {
-    if (pl.i8) launch_tiles<true, 128, 128, 4, false>(p, mode, k, st);
-    else launch_tiles<false, 128, 128, 4, false>(p, mode, k, st);
+    if (pl.i8) launch_tiles<true, 128, 128, 4>(p, mode, k, st);
+    else launch_tiles<false, 128, 128, 4>(p, mode, k, st);
   }
   if (p.partial)
     (a.m % 4 == 0 ? prompt_join<true> : prompt_join<false>)

@@ -214,7 +214,7 @@ hipError_t launch_rows(PackedLinearLaunch a, void* staged, hipStream_t st);
 // Many tokens: what the product is made of, and its workspace.
 struct PromptPlan {
   bool ok, i8, wide, direct, fused;
-  int mode, reps;
+  int mode, reps, token_tile;               // token_tile: fused
   int64_t steps, per, splits, tiles_t, tiles_r, staged_row, rows16;
   size_t staged_bytes, spread_bytes, steps_bytes, partial_bytes;
 };
