@@ -9,16 +9,12 @@
 // parts (the top, middle and last 8 bits of its significand), each of which
 // runs over the same weights.
 //
-// Two kernels.  spread_weights writes the integers c - z (overflow entries
-// added) once per call in the operands' order, a wave's operand a contiguous
-// kilobyte; prompt_tiles multiplies.  Up to 128 tokens, where that writing
-// would cost more than the product, prompt_tiles reads the packed codes and
-// spreads them itself (FUSED; not with overflow entries, which would have to
-// be looked for in every lane's registers): q_proj 64 8-bit tokens 15 us
-// against 25, up_proj 32 bf16 tokens 33 against 60.  With more tokens every
-// tile of them would repeat it on the vector unit, which the multiplication
-// by the steps already fills (that way 2048 bf16 tokens of up_proj took 333 us
-// against 295).
+// Up to a few hundred tokens batch_tiles reads the packed codes and spreads them
+// itself.  With more, every tile of tokens would repeat that on the vector
+// unit, which the multiplication by the steps already fills: spread_weights
+// writes the integers c - z (overflow entries added) once per call in the
+// operands' order, a wave's operand a contiguous kilobyte, and prompt_tiles
+// multiplies.
 //
 // A step of prompt_tiles covers 128 bytes of every x row (128 8-bit or 64 bf16
 // columns).  Two steps ahead of their use, x goes HBM -> LDS by asynchronous
@@ -48,9 +44,9 @@ namespace {
 
 typedef __attribute__((__vector_size__(4 * sizeof(int)))) int i32x4_t;
 typedef __attribute__((address_space(3))) char lds_char;
+typedef __attribute__((address_space(4))) int const_int;
 
 constexpr int KB = 128;            // bytes of an x row per step
-constexpr int64_t kFusedTokens = 128;
 
 // Asynchronous copies of 16 bytes, 4 bytes, or one byte (to a dword) per lane:
 // sbase + voff of each lane to lds + 16 lane, or lds + 4 lane (lds and sbase
@@ -144,11 +140,14 @@ struct PromptArgs {
   int64_t ldq;
   const float* scales;
   const uint8_t* zeros;
+  const int32_t* off;
+  const int32_t* outliers;
+  int n_out;
   const i32x4_t* spread;  // [strip of 16 rows][weight block][half][lane]
   int blocks;             // weight blocks (steps / reps)
   const float* steps_t;   // [group][16 strips' rows], times what the operands leave out
   int64_t rows16;         // rows of it: 16 strips
-  int ntok, m, ng;
+  int ntok, m, n, ng;
   uint32_t per_group;     // 2^31 / half steps of a group, rounded up: 2 u per_group / 2^32 is
                           // the group of half step u < 2^16 (at most 2^15 to a group)
   void* y;
@@ -318,32 +317,39 @@ __device__ __forceinline__ void store_tile(const PromptArgs& a,
   }
 }
 
-// Up to 128 tokens: tiles of BT tokens x 128 rows that read the packed codes, in
+// Fewer tokens: tiles of BT tokens x 128 rows that read the packed codes, in
 // tiles of 128 columns.  NP: x steps of such a tile (8-bit 1, bf16 2, float32
 // 6).  Everything comes by asynchronous copies two tiles ahead: x for the
 // workgroup, 32 rows of weights (2 KB), their steps and zero points for the
 // wave that spreads them and multiplies by them.  Lanes next to each other copy
 // bytes next to each other; loads in the operands' layout, one cache lookup a
-// lane, took 33 us for 32 bf16 tokens of up_proj, these 21.
-constexpr int batch_lds(int np, int bt, int sc, bool asym) {
-  return 3 * np * bt * KB + 12 * (2048 + sc * (asym ? 512 : 256));
+// lane, took 33 us for 32 bf16 tokens of up_proj, these 21.  With overflow
+// entries (OVER) the codes become bytes in LDS first, where the entries' are
+// added (24 us; written to memory spread, 57).  What bounds it: latency with few
+// columns a split, then the vector unit's spreading; up_proj 64 8-bit tokens
+// 20 us, 1.6 TB/s.
+constexpr int kSpreadRow = 128 + 16;                  // bytes of a spread row (OVER)
+constexpr int batch_lds(int np, int bt, int sc, bool asym, bool over) {
+  return 3 * np * bt * KB + 12 * (2048 + sc * (asym ? 512 : 256) + (over ? 512 : 0)) +
+         (over ? 4 * 32 * kSpreadRow : 0);
 }
 constexpr int batch_steps(bool i8, int mode) {       // copies of 64 steps of a tile
   return mode == 0 ? 0 : (!i8 && mode == 2 ? 2 : 1);
 }
-template <bool I8, int NP, int BT, int MODE, bool ASYM>
+template <bool I8, int NP, int BT, int MODE, bool ASYM, bool OVER>
 __global__ __launch_bounds__(
-    256, batch_lds(NP, BT, batch_steps(I8, MODE), ASYM) <= 80 * 1024 ? 2 : 1)
+    256, batch_lds(NP, BT, batch_steps(I8, MODE), ASYM, OVER) <= 80 * 1024 ? 2 : 1)
 void batch_tiles(const PromptArgs a) {
   constexpr int BR = 128, NI = BT / 16, NJ = 2;
   constexpr int SUB = I8 ? 1 : 2, REPS = NP / SUB;      // blocks of a tile, x parts
   constexpr int NS = MODE == 2 ? 2 : 1;                 // steps of a block
   constexpr int SC = batch_steps(I8, MODE);             // SUB NS groups of 32 rows
   constexpr int XS = NP * BT * KB, NC = BT / 32;        // x of a tile; copies of an x step
-  constexpr int WS = 2048 + SC * 256 * (ASYM ? 2 : 1);  // the wave's part of a tile
-  constexpr int COPIES = NP * NC + 2 + SC * (ASYM ? 2 : 1);
-  constexpr int LDS = batch_lds(NP, BT, SC, ASYM);
-  static_assert(LDS == 3 * XS + 12 * WS && LDS >= kYBytes<BT, BR>, "what is used");
+  constexpr int ES = 2048 + SC * 256 * (ASYM ? 2 : 1);  // overflow entries, of the wave's part
+  constexpr int WS = ES + (OVER ? 512 : 0);             // of a tile
+  constexpr int COPIES = NP * NC + 2 + SC * (ASYM ? 2 : 1) + (OVER ? 2 : 0);
+  constexpr int LDS = batch_lds(NP, BT, SC, ASYM, OVER);
+  static_assert(3 * XS + 12 * WS <= LDS && kYBytes<BT, BR> <= LDS, "what is used");
   using acc_t = sum_t<I8>;
   __shared__ __attribute__((aligned(16))) char smem[LDS];
   const uint32_t lbase = (uint32_t)(uintptr_t)(lds_char*)smem;
@@ -352,7 +358,7 @@ void batch_tiles(const PromptArgs a) {
   const int split = blockIdx.y;
   const int tid = threadIdx.x, lane = tid & 63, lr = lane & 15, lq = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int across = (a.blocks + SUB - 1) / SUB;
+  const int across = (a.n + 127) / 128;
   const int k0 = split * a.per, k1 = min(across, k0 + a.per), last = k1 - 1;
 
   // copies
@@ -376,6 +382,14 @@ void batch_tiles(const PromptArgs a) {
   const float* const sbase = a.scales + (int64_t)rbase * a.ng;
   const uint8_t* const zbase = ASYM ? a.zeros + (int64_t)rbase * a.ng : nullptr;
   const uint32_t own = 3 * XS + wave * 3 * WS;
+  // the overflow list's range for strip j of the wave (nothing past the last)
+  const int strips = (a.m + 15) / 16;
+  auto range = [&](int kt, int j, int& e0, int& e1) {
+    const int st = min(wr0 / 16 + j, strips - 1);
+    const const_int* const off = (const const_int*)(a.off + (int64_t)st * across + kt);
+    e0 = max(off[0], 0);
+    e1 = wr0 / 16 + j < strips ? min(off[1], a.n_out) : e0;
+  };
   auto ask = [&](int kt, int slot) {
 #pragma unroll
     for (int p = 0; p < NP; ++p)
@@ -397,6 +411,15 @@ void batch_tiles(const PromptArgs a) {
       copy4(4 * at, sbase, dst + 2048u + 256u * h);
       if constexpr (ASYM) copy1(at, zbase, dst + 2048u + 256u * (SC + h));
     }
+    if constexpr (OVER) {
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        int e0, e1;
+        range(kt, j, e0, e1);
+        e0 = min(e0, a.n_out - 1);
+        copy4(4u * min(lane, a.n_out - 1 - e0), a.outliers + e0, dst + ES + 256u * j);
+      }
+    }
   };
 
   float acc[NI][NJ][4];
@@ -417,6 +440,11 @@ void batch_tiles(const PromptArgs a) {
     z_row[j] = MODE == 0 && ASYM ? zbase[min(16 * j + lr, rows - 1)] : 8;
   }
 
+  // OVER: a row of 64 columns of a lane, its zero point (MODE 0)
+  char* const spread = smem + 3 * XS + 12 * WS + wave * 32 * kSpreadRow;
+  const int sr = lane >> 1, sh = lane & 1;
+  const int z_lane = OVER && MODE == 0 && ASYM ? zbase[min(sr, rows - 1)] : 8;
+
   // 16-byte unit of an x row that lane group lq of half h works on: both
   // halves' codes next to each other, unless a half has a step of its own
   constexpr bool PAIRED = MODE != 2;
@@ -435,6 +463,34 @@ void batch_tiles(const PromptArgs a) {
     const char* const ws = smem + own + slot * WS;
     const float* const steps = (const float*)(ws + 2048);
     const int* const zeros = (const int*)(ws + 2048 + 256 * SC);
+    if constexpr (OVER) {
+      // the wave's integers as bytes, by rows, and the list's added to them
+#pragma unroll
+      for (int q = 0; q < 2; ++q) {
+        const int unit = (2 * sh + q) ^ ((sr & 15) >> 2);
+        const uint4 p = *(const uint4*)(ws + 1024 * (sr >> 4) + 64 * (sr & 15) + 16 * unit);
+        const int slot_z = (2 * sh + q) * SUB * NS / 4;
+        const int z = MODE != 0 && ASYM ? zeros[32 * slot_z + sr] : z_lane;
+        const uint32_t z4 = (uint32_t)z * 0x01010101u;
+        const uint2 p0 = steps_i8(p.x ^ flip, z4), p1 = steps_i8(p.y ^ flip, z4);
+        const uint2 p2 = steps_i8(p.z ^ flip, z4), p3 = steps_i8(p.w ^ flip, z4);
+        char* const d = spread + sr * kSpreadRow + 64 * sh + 32 * q;
+        *(uint4*)d = make_uint4(p0.x, p0.y, p1.x, p1.y);
+        *(uint4*)(d + 16) = make_uint4(p2.x, p2.y, p3.x, p3.y);
+      }
+      // (a wave's LDS accesses are in order)
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        int e0, e1;
+        range(kt, j, e0, e1);
+        for (int e = e0 + lane; e < e1; e += 64) {
+          const int v = e - e0 < 64 ? *(const int*)(ws + ES + 256 * j + 4 * lane) : a.outliers[e];
+          int8_t* const d = (int8_t*)(spread + (16 * j + ((v >> 7) & 15)) * kSpreadRow + (v & 127));
+          *d = (int8_t)(*d + (v >> 16));
+        }
+      }
+      asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+    }
 #pragma unroll
     for (int sub = 0; sub < SUB; ++sub) {
       if (SUB * kt + sub >= a.blocks) break;
@@ -449,8 +505,23 @@ void batch_tiles(const PromptArgs a) {
           __builtin_memcpy(p, ws + 1024 * j + 64 * lr + (((o >> 4) ^ (lr >> 2)) << 4) + (o & 15),
                            PB);
           const int at = 32 * (sub * NS + (NS == 2 ? h : 0)) + 16 * j + lr;
-          const int z = MODE != 0 && ASYM ? zeros[at] : z_row[j];
           if (MODE != 0 && h < NS) sc[j][h] = steps[at];
+          if constexpr (OVER) {
+            const char* const c = spread + (16 * j + lr) * kSpreadRow + 2 * o;
+            if constexpr (I8) {
+              w[j][h] = *(const i32x4_t*)c;
+            } else {
+              int8_t v[8];
+              __builtin_memcpy(v, c, 8);
+#pragma unroll
+              for (int i = 0; i < 4; ++i)            // (small integers: exact in bf16)
+                w[j][h][i] = (int)__builtin_amdgcn_perm(__float_as_uint((float)v[2 * i + 1]),
+                                                        __float_as_uint((float)v[2 * i]),
+                                                        0x07060302u);
+            }
+            continue;
+          }
+          const int z = MODE != 0 && ASYM ? zeros[at] : z_row[j];
           if constexpr (I8) {
             const uint32_t z4 = (uint32_t)z * 0x01010101u;
             const uint2 lo = steps_i8(p[0] ^ flip, z4), hi = steps_i8(p[1] ^ flip, z4);
@@ -788,18 +859,21 @@ void launch_tiles(const PromptArgs& p, int mode, int splits, hipStream_t st) {
   else prompt_tiles<I8, BT, BR, WR, 2><<<grid, 64 * WR, 0, st>>>(p);
 }
 
-template <bool I8, int NP, int BT, bool ASYM>
+template <bool I8, int NP, int BT, bool ASYM, bool OVER>
 void launch_batch_mode(const PromptArgs& p, int mode, int splits, hipStream_t st) {
   const dim3 grid = tile_grid(p, splits);
-  if (mode == 0) batch_tiles<I8, NP, BT, 0, ASYM><<<grid, 256, 0, st>>>(p);
-  else if (mode == 1) batch_tiles<I8, NP, BT, 1, ASYM><<<grid, 256, 0, st>>>(p);
-  else batch_tiles<I8, NP, BT, 2, ASYM><<<grid, 256, 0, st>>>(p);
+  if (mode == 0) batch_tiles<I8, NP, BT, 0, ASYM, OVER><<<grid, 256, 0, st>>>(p);
+  else if (mode == 1) batch_tiles<I8, NP, BT, 1, ASYM, OVER><<<grid, 256, 0, st>>>(p);
+  else batch_tiles<I8, NP, BT, 2, ASYM, OVER><<<grid, 256, 0, st>>>(p);
 }
 
 template <bool I8, int NP, int BT>
 void launch_batch(const PromptArgs& p, int mode, int splits, hipStream_t st) {
-  p.zeros ? launch_batch_mode<I8, NP, BT, true>(p, mode, splits, st)
-          : launch_batch_mode<I8, NP, BT, false>(p, mode, splits, st);
+  if (p.n_out > 0)
+    return p.zeros ? launch_batch_mode<I8, NP, BT, true, true>(p, mode, splits, st)
+                   : launch_batch_mode<I8, NP, BT, false, true>(p, mode, splits, st);
+  p.zeros ? launch_batch_mode<I8, NP, BT, true, false>(p, mode, splits, st)
+          : launch_batch_mode<I8, NP, BT, false, false>(p, mode, splits, st);
 }
 
 }  // namespace
@@ -833,17 +907,45 @@ PromptPlan prompt_plan(const void* x, int32_t xdtype, int64_t ntok, int64_t ldx,
   const int kind = !p.i8 ? 0 : (p.mode == 2 ? 2 : 1);
   const double us_one[] = {0.70, 0.78, 0.95}, us_two[] = {1.2, 1.37, 1.65};
   const double us_wide[] = {1.05, 1.3, 1.6};
+  auto join_us = [&](int64_t splits) {
+    return splits > 1 ? 3.0 + 2.0 * splits * ntok * m * 4 / 8.5e6 : 0.0;
+  };
   double best = 0;
-  p.fused = n_out == 0 && ntok <= kFusedTokens;
+  // batch_tiles as long as its spreading of the codes for every tile of tokens
+  // costs less than spread_weights and its traffic: 256 8-bit tokens of
+  // 14336 x 4096 37 us against 50, 512 65 both (q_proj 25 against 33); 256 bf16
+  // tokens 60 against 79, 384 93 against 97 to 102 (down_proj 100 against 93);
+  // with overflow entries 128 bf16 tokens 68 both, 256 117 against 81; float32
+  // 129 tokens 134 against 124.
+  p.fused = ntok <= (n_out > 0 || p.reps == 3 ? 128 : (p.i8 ? 512 : 320));
   if (p.fused) {
-    // 32 x 128 or 64 x 128 tiles; about 512 workgroups, splits of at least 512 columns
+    // 32 x 128 or 64 x 128 tiles and column splits by their estimated time, as
+    // above: microseconds of a tile's 128 columns for one workgroup on a CU and
+    // for two, the first ones' arrival as one and a half of them.  (64 bf16
+    // tokens of 14336 x 4096: 26 us in 4 splits, 29 in 2; 8-bit ones 22 and 20;
+    // 128 8-bit tokens of 4096 x 4096 17 us in 4 splits, 20 in 8; splits of
+    // fewer than 512 columns gained nothing.)
     p.token_tile = ntok <= 32 || p.reps == 3 ? 32 : 64;
+    const int of = p.reps == 3 ? 2 : (p.i8 ? 0 : 1);
+    const double one[2][3] = {{0.58, 1.05, 1.5}, {0.85, 1.45}};
+    const double two[2][3] = {{1.2, 1.6, 3.0}, {1.75, 2.2}};
     p.tiles_t = (ntok + p.token_tile - 1) / p.token_tile;
     p.tiles_r = (m + 127) / 128;
-    const int64_t tiles = p.tiles_t * p.tiles_r, across = (n + 127) / 128;
-    p.splits = std::max<int64_t>(1, std::min<int64_t>(512 / tiles, across / 4));
-    p.per = (across + p.splits - 1) / p.splits;
-    p.splits = (across + p.per - 1) / p.per;
+    const int64_t across = (n + 127) / 128, most = std::max<int64_t>(1, across / 4);
+    for (int64_t k = 1; k <= most; ++k) {
+      const int64_t per = (across + k - 1) / k, splits = (across + per - 1) / per;
+      if (splits != k) continue;
+      const int64_t groups = p.tiles_t * p.tiles_r * splits, left = groups % 512;
+      const int b = p.token_tile == 64;
+      double us = (double)(groups / 512) * two[b][of] +
+                  (left == 0 ? 0.0 : (left <= 256 ? one[b][of] : two[b][of]));
+      us = us * (per + 1.5) + join_us(splits);
+      if (best == 0 || us < best) {
+        best = us;
+        p.per = per;
+        p.splits = splits;
+      }
+    }
   }
   for (int wide = 0; wide < 2 && !p.fused; ++wide) {
     const int64_t tt = (ntok + 127) / 128, edge = wide ? 256 : 128, tr = (m + edge - 1) / edge;
@@ -856,7 +958,7 @@ PromptPlan prompt_plan(const void* x, int32_t xdtype, int64_t ntok, int64_t ldx,
                        : (double)(groups / 512) * us_two[kind] +
                              (left == 0 ? 0.0 : (left <= 256 ? us_one[kind] : us_two[kind]));
       us *= per;
-      if (splits > 1) us += 3.0 + 2.0 * splits * ntok * m * 4 / 8.5e6;
+      us += join_us(splits);
       if (best == 0 || us < best) {
         best = us;
         p.wide = wide;
@@ -915,12 +1017,16 @@ hipError_t launch_prompt(const PackedLinearLaunch& a, const PromptPlan& pl, cons
   p.ldq = a.ldq;
   p.scales = a.scales;
   p.zeros = a.zeros;
+  p.off = a.outlier_off;
+  p.outliers = a.outliers;
+  p.n_out = a.outlier_off ? (int)a.n_out : 0;
   p.spread = (const i32x4_t*)w.spread;
   p.blocks = (int)(pl.steps / pl.reps);
   p.steps_t = w.steps;
   p.rows16 = pl.rows16;
   p.ntok = (int)a.ntok;
   p.m = (int)a.m;
+  p.n = (int)a.n;
   p.ng = (int)(a.n / a.G);
   if (pl.mode != 0) {
     const uint32_t halves = (uint32_t)a.G / (pl.i8 ? 64 : 32);
@@ -931,16 +1037,16 @@ hipError_t launch_prompt(const PackedLinearLaunch& a, const PromptPlan& pl, cons
   p.ldy = a.ldy;
   p.partial = pl.splits > 1 ? (float*)w.partial : nullptr;
   if (!pl.fused) {
-    const int across = (int)((a.n + 127) / 128), n_out = a.outlier_off ? (int)a.n_out : 0;
+    const int across = (int)((a.n + 127) / 128);
     const int64_t tiles = pl.rows16 / 16 * across;
     const dim3 grid((unsigned)((tiles + 3) / 4));
     if (pl.i8)
       spread_weights<true><<<grid, 256, 0, st>>>(
-          a.qweight, a.ldq, a.scales, a.zeros, a.outlier_off, a.outliers, n_out, a.m, (int)a.n,
+          a.qweight, a.ldq, a.scales, a.zeros, a.outlier_off, a.outliers, p.n_out, a.m, (int)a.n,
           a.G, p.ng, across, tiles, (i32x4_t*)w.spread, p.blocks, w.steps, pl.rows16);
     else
       spread_weights<false><<<grid, 256, 0, st>>>(
-          a.qweight, a.ldq, a.scales, a.zeros, a.outlier_off, a.outliers, n_out, a.m, (int)a.n,
+          a.qweight, a.ldq, a.scales, a.zeros, a.outlier_off, a.outliers, p.n_out, a.m, (int)a.n,
           a.G, p.ng, across, tiles, (i32x4_t*)w.spread, p.blocks, w.steps, pl.rows16);
   }
   const int mode = pl.mode, k = (int)pl.splits;

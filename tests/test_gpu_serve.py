@@ -100,6 +100,36 @@ def test_packed_linear(shape, x_kind):
 
 
 @pytest.mark.parametrize("x_kind", ["bf16", "f32", "int8"])
+@pytest.mark.parametrize("kind,density", [("sym", 0.2), ("asym", 1.0)])
+@pytest.mark.parametrize("tokens", [2, 16, 24, 48, 140])
+def test_packed_linear_dense_overflow(tokens, kind, density, x_kind):
+    """More overflow codes in 16 rows x 128 columns than a wave holds at a time."""
+    m, n, group = 150, 1376, 32 if x_kind == "bf16" else 0
+    rng = np.random.default_rng([tokens, int(10 * density)])
+    codes, scales, zeros = layer(rng, m, n, group, kind, density)
+    pk = packed_layer(codes, scales, zeros, group)
+    assert pk["outliers"].shape[0] > 0.1 * m * n
+    x, xs = activations(rng, tokens, n, x_kind)
+    y = P.packed_linear(x.cuda(), pk, x_scales=None if xs is None else xs.cuda(),
+                        out_dtype=torch.float32)
+    check_linear(y, x, xs, codes, scales, zeros)
+
+
+@pytest.mark.parametrize("x_kind", ["bf16", "int8"])
+@pytest.mark.parametrize("tokens,m,n,group", [(200, 700, 1088, 64), (320, 260, 4096, 128),
+                                              (511, 129, 640, 32), (512, 1300, 896, 0)])
+def test_packed_linear_batches(tokens, m, n, group, x_kind):
+    """The most tokens that read the codes as packed, ragged tiles and splits."""
+    rng = np.random.default_rng([tokens, m, n])
+    for kind in ("sym", "asym"):
+        codes, scales, zeros = layer(rng, m, n, group, kind, 0.0)
+        pk = packed_layer(codes, scales, zeros, group)
+        x, xs = activations(rng, tokens, n, x_kind)
+        y = P.packed_linear(x.cuda(), pk, x_scales=None if xs is None else xs.cuda())
+        check_linear(y, x, xs, codes, scales, zeros)
+
+
+@pytest.mark.parametrize("x_kind", ["bf16", "f32", "int8"])
 @pytest.mark.parametrize("n,group", [(320, 64), (200, 0), (384, 128), (416, 32)])
 def test_packed_linear_many_tiles(n, group, x_kind):
     """Enough tokens and rows for the largest tile, ragged in both."""
