@@ -8,6 +8,12 @@
 // consecutive elements each NV times over; a workgroup keeps the weight of
 // its columns in registers and walks over tokens.  Rows longer than the
 // registers hold take rms_norm_rows, which reads them three times.
+//
+// What bounds it: HBM for many tokens (8192 x 4096 bf16 with residual to 8 bits
+// 50 us, 4.65 TB/s; 2048 x 14336 bf16 27.4 us, 4.3 TB/s; a large copy reaches
+// 5.1), a launch and two reductions for few (one token of 4096 4.5 us).  Rows
+// that are not 16-byte aligned read in smaller pieces (2047 x 4099 24 us, 2.5
+// TB/s).
 #include "pwq_internal.h"
 
 #include <algorithm>

@@ -1,5 +1,6 @@
-// Packing integer codes into 4 bits with an overflow list, and the product
-// of the packed layer with tokens for any shape.
+// Packing integer codes into 4 bits with an overflow list (once per layer), and
+// the product of the packed layer with tokens for what the other kernels leave:
+// groups that are no multiple of 32 columns, and the longest rows (a wave per row).
 #include "pwq_internal.h"
 
 #include <algorithm>

@@ -7,8 +7,16 @@
 // own by asynchronous copies, `depth` tiles ahead: lanes next to each other
 // read bytes next to each other, which the operand layout of the matrix
 // instructions does not.  (Loads straight into that layout cost a cache lookup
-// per lane and bound the kernel at 2 to 3 times its time: 16 us for up_proj's
-// 29 MB and one 8-bit token.)
+// per lane and bound the kernel: 16 us for up_proj's 29 MB and one 8-bit token.)
+// Every tile issues the same number of copies, so that the waits are constants;
+// waits chosen at run time and copies under branches took 11.2 us where these
+// take 8.8, and 19.5 against 13.4 for 16 bf16 tokens.
+//
+// What bounds it: with one token the weights' bytes, from a last-level cache
+// that holds the layer (up_proj one 8-bit token 8.8 us, 3.5 TB/s; a kernel that
+// only reads those bytes takes 5.4 to 6.3), or a launch and the first bytes'
+// way (q_proj 4.6 us; a launch alone 2.7).  bf16 x spends the vector unit on
+// spreading (11.0 us), 16 tokens read 128 KB of x for every 16 rows (13.4 us).
 //
 // Operands: x (16 tokens) and the codes of 16 rows.  Lane l holds token l % 16
 // and row l % 16, and of block h of GB columns, GB <= G, the GB / 4 from
@@ -19,7 +27,9 @@
 //
 // Codes beyond 4 bits enter as further columns: up to 32 (64 for 8-bit x)
 // entries of a tile at a time, x gathered at their columns, the entry's value
-// in its own row and 0 in the others.
+// in its own row and 0 in the others.  A wave holds 256 entries in LDS; they are
+// copied like the weights (q_proj one bf16 token with 0.2% of such codes 6.8
+// us; read by ordinary loads, which wait for the copies, 7.7).
 #include "pwq_internal.h"
 
 #include <algorithm>
@@ -427,7 +437,9 @@ constexpr int kLdsBytes = 160 * 1024;
 
 template <int XK, int GB, int NX, bool ASYM, bool OVER>
 void launch_waves(PackedLinearLaunch a, hipStream_t st) {
-  // about 16 waves per CU over the whole launch, as far as LDS goes
+  // about 16 waves per CU over the whole launch, as far as LDS goes (up_proj
+  // one bf16 token 10.9 us with 4096 waves, 13.2 with 6144; down_proj 11.0 with
+  // workgroups of up to 16 waves, 12.2 with 12)
   const int64_t strips = (a.m + kPackRows - 1) / kPackRows, across = (a.n + 127) / 128;
   int most = (int)std::clamp<int64_t>(4096 / strips, 1, 16), bytes;
   for (;; --most) {
