@@ -969,6 +969,8 @@ PromptPlan prompt_plan(const void* x, int32_t xdtype, int64_t ntok, int64_t ldx,
       }
     }
   }
+  // with the spreading: a launch and its bytes at 5 TB/s
+  p.us = best + (p.fused ? 0.0 : 3.0 + (double)m * n * (p.i8 ? 1.5 : 2.5) / 5e6);
   p.rows16 = (m + 15) / 16 * 16;
   p.spread_bytes = p.fused ? 0 : (size_t)(p.rows16 * (p.steps / p.reps) * KB);
   p.steps_bytes = p.fused ? 0 : (size_t)(p.rows16 * (n / G) * 4);

@@ -934,11 +934,12 @@ pwq_status pwq_rms_norm(const void* x, int32_t xdtype, int64_t ntok, int64_t n, 
   return ok();
 }
 
-// Which kernel serves a product, and its workspace.
+// Which kernel serves a product, its workspace, its estimated time.
 struct LinearPlan {
   bool rows = false;        // few tokens
   PromptPlan prompt{};      // .ok: many tokens; neither: any shape
   size_t staged = 0;
+  double us = 0;
 };
 static LinearPlan linear_plan(const void* x, int32_t xdtype, int64_t ntok, int64_t ldx, int64_t m,
                               int64_t n, int32_t G, int64_t n_out) {
@@ -947,9 +948,42 @@ static LinearPlan linear_plan(const void* x, int32_t xdtype, int64_t ntok, int64
   p.rows = rows_ok(ntok, n, G);
   if (p.rows) {
     p.staged = rows_staged_bytes(x, xdtype, ntok, n, ldx);
+    p.us = 0.5 * (double)m * n / 2.7e6;      // the weights at 2.7 TB/s
   } else {
     p.prompt = prompt_plan(x, xdtype, ntok, ldx, m, n, G, n_out);
     p.staged = p.prompt.staged_bytes;
+    p.us = p.prompt.us;
+  }
+  return p;
+}
+
+// A product as one plan, or as two: tokens past whole tiles of 128 cost a row
+// of tiles, and where that starts another round of them, much of their time.
+// The kernels for fewer tokens then take them, for a launch (3 us) and the
+// weights once more.  (1025 bf16 tokens of 4096 x 14336: 174 us so, 199 as one; 2049
+// 272 and 357.)
+struct LinearParts {
+  LinearPlan head, rest;
+  int64_t split = 0;        // first token of the rest; ntok: none
+};
+static const void* rows_from(const void* p, int64_t row, int64_t ld, int32_t dtype) {
+  const int64_t es = dtype == PWQ_I8 ? 1 : (dtype == PWQ_BF16 ? 2 : 4);
+  return (const char*)p + row * ld * es;
+}
+static LinearParts linear_parts(const void* x, int32_t xdtype, int64_t ntok, int64_t ldx,
+                                int64_t m, int64_t n, int32_t G, int64_t n_out) {
+  LinearParts p;
+  p.head = linear_plan(x, xdtype, ntok, ldx, m, n, G, n_out);
+  p.split = ntok;
+  const int64_t tail = ntok % 128;
+  if (!p.head.prompt.ok || p.head.prompt.fused || tail == 0 || ntok < 128) return p;
+  const LinearPlan head = linear_plan(x, xdtype, ntok - tail, ldx, m, n, G, n_out);
+  const LinearPlan rest = linear_plan(rows_from(x, ntok - tail, ldx, xdtype), xdtype, tail, ldx, m,
+                                      n, G, n_out);
+  if (head.us + rest.us + 3.0 < p.head.us) {
+    p.head = head;
+    p.rest = rest;
+    p.split = ntok - tail;
   }
   return p;
 }
@@ -961,13 +995,23 @@ static void carve_linear(Carver& c, const LinearPlan& p, PromptWs* w) {
   w->partial = p.prompt.partial_bytes ? c.take(p.prompt.partial_bytes) : nullptr;
 }
 
+static hipError_t launch_linear(const PackedLinearLaunch& a, const LinearPlan& p,
+                                const PromptWs& w, hipStream_t st) {
+  if (a.ntok == 0 || a.m == 0) return hipSuccess;
+  return p.rows ? launch_rows(a, w.staged, st)
+                : (p.prompt.ok ? launch_prompt(a, p.prompt, w, st) : launch_linear_any(a, st));
+}
+
 size_t pwq_packed_linear_workspace_size(const void* x, int32_t xdtype, int64_t ntok, int64_t ldx,
                                         int64_t m, int64_t n, int32_t group, int64_t n_out) {
   if (ntok < 0 || m < 0 || n <= 0 || ntok > INT32_MAX || m > INT32_MAX || n > INT32_MAX) return 0;
   if (group < 0 || (group > 0 && n % group) || ldx < n) return 0;
+  const LinearParts p =
+      linear_parts(x, xdtype, ntok, ldx, m, n, group > 0 ? group : (int32_t)n, n_out);
   Carver c(nullptr);
   PromptWs w;
-  carve_linear(c, linear_plan(x, xdtype, ntok, ldx, m, n, group > 0 ? group : (int32_t)n, n_out), &w);
+  carve_linear(c, p.head, &w);
+  carve_linear(c, p.rest, &w);
   return c.size();
 }
 
@@ -1004,16 +1048,20 @@ pwq_status pwq_packed_linear(const void* x, int32_t xdtype, int64_t ntok, int64_
   PackedLinearLaunch a{x, xdtype, ntok, ldx, x_scales, qweight, m, n, packed_row_bytes(n), scales,
                        zeros, group > 0 ? group : (int32_t)n, n_out > 0 ? outlier_off : nullptr,
                        outliers, n_out, y, ydtype, ldy, 0, 0, 0, 0};
-  const LinearPlan p = linear_plan(x, xdtype, ntok, ldx, m, n, a.G, n_out);
+  const LinearParts p = linear_parts(x, xdtype, ntok, ldx, m, n, a.G, n_out);
   Carver c(ws);
-  PromptWs w;
-  carve_linear(c, p, &w);
-  hipStream_t st = (hipStream_t)stream;
-  hipError_t e = hipSuccess;
-  if (ntok > 0 && m > 0)
-    e = p.rows ? launch_rows(a, w.staged, st)
-               : (p.prompt.ok ? launch_prompt(a, p.prompt, w, st)
-                              : launch_linear_any(a, st));
+  PromptWs head, rest;
+  carve_linear(c, p.head, &head);
+  carve_linear(c, p.rest, &rest);
+  a.ntok = p.split;
+  hipError_t e = launch_linear(a, p.head, head, (hipStream_t)stream);
+  if (e == hipSuccess && p.split < ntok) {
+    a.x = rows_from(x, p.split, ldx, xdtype);
+    a.y = (void*)rows_from(y, p.split, ldy, ydtype);
+    if (x_scales) a.x_scales = x_scales + p.split;
+    a.ntok = ntok - p.split;
+    e = launch_linear(a, p.rest, rest, (hipStream_t)stream);
+  }
   if (e != hipSuccess) return hip_fail(e, "packed_linear launch");
   return ok();
 }

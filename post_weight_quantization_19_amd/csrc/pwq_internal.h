@@ -215,6 +215,7 @@ hipError_t launch_rows(PackedLinearLaunch a, void* staged, hipStream_t st);
 struct PromptPlan {
   bool ok, i8, wide, direct, fused;
   int mode, reps, token_tile;               // token_tile: fused
+  double us;                                // estimated time
   int64_t steps, per, splits, tiles_t, tiles_r, staged_row, rows16;
   size_t staged_bytes, spread_bytes, steps_bytes, partial_bytes;
 };

@@ -129,6 +129,24 @@ def test_packed_linear_batches(tokens, m, n, group, x_kind):
         check_linear(y, x, xs, codes, scales, zeros)
 
 
+@pytest.mark.parametrize("tokens,m,n,x_kind", [(641, 4096, 4096, "bf16"), (1030, 4096, 4096, "int8"),
+                                               (1026, 1500, 3200, "f32"), (1100, 4096, 4096, "bf16")])
+@pytest.mark.parametrize("aligned", [True, False])
+def test_packed_linear_tokens_past_whole_tiles(tokens, m, n, x_kind, aligned):
+    """A few tokens more than tiles of 128 hold, in x and y with strides."""
+    rng = np.random.default_rng([tokens, n])
+    codes, scales, zeros = layer(rng, m, n, 128, "asym", 0.001)
+    pk = packed_layer(codes, scales, zeros, 128)
+    x, xs = activations(rng, tokens, n, x_kind)
+    wide = torch.zeros((tokens, n + (64 if aligned else 3)), dtype=x.dtype, device="cuda")
+    wide[:, :n] = x.cuda()
+    out = torch.full((tokens, m + 5), 7.0, device="cuda")
+    y = P.packed_linear(wide[:, :n], pk, x_scales=None if xs is None else xs.cuda(),
+                        out_dtype=torch.float32, out=out[:, :m])
+    check_linear(y, x, xs, codes, scales, zeros)
+    assert bool((out[:, m:] == 7.0).all())
+
+
 @pytest.mark.parametrize("x_kind", ["bf16", "f32", "int8"])
 @pytest.mark.parametrize("n,group", [(320, 64), (200, 0), (384, 128), (416, 32)])
 def test_packed_linear_many_tiles(n, group, x_kind):
