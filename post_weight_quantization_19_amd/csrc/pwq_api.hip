@@ -957,11 +957,11 @@ static LinearPlan linear_plan(const void* x, int32_t xdtype, int64_t ntok, int64
   return p;
 }
 
-// A product as one plan, or as two: tokens past whole tiles of 128 cost a row
-// of tiles, and where that starts another round of them, much of their time.
-// The kernels for fewer tokens then take them, for a launch (3 us) and the
-// weights once more.  (1025 bf16 tokens of 4096 x 14336: 174 us so, 199 as one; 2049
-// 272 and 357.)
+// A product as one plan, or as two: tokens past whole tiles cost a row of
+// tiles, and where that starts another round of workgroups, much of a round's
+// time.  Fewer than 512 of them then go to kernels (or tiles) of their own, for a
+// launch (3 us) and the weights once more.  (1025 bf16 tokens of 4096 x 14336:
+// 174 us so, 199 as one; 2049 272 and 357; 2300 334 and 381.)
 struct LinearParts {
   LinearPlan head, rest;
   int64_t split = 0;        // first token of the rest; ntok: none
@@ -975,15 +975,21 @@ static LinearParts linear_parts(const void* x, int32_t xdtype, int64_t ntok, int
   LinearParts p;
   p.head = linear_plan(x, xdtype, ntok, ldx, m, n, G, n_out);
   p.split = ntok;
-  const int64_t tail = ntok % 128;
-  if (!p.head.prompt.ok || p.head.prompt.fused || tail == 0 || ntok < 128) return p;
-  const LinearPlan head = linear_plan(x, xdtype, ntok - tail, ldx, m, n, G, n_out);
-  const LinearPlan rest = linear_plan(rows_from(x, ntok - tail, ldx, xdtype), xdtype, tail, ldx, m,
-                                      n, G, n_out);
-  if (head.us + rest.us + 3.0 < p.head.us) {
-    p.head = head;
-    p.rest = rest;
-    p.split = ntok - tail;
+  if (!p.head.prompt.ok || p.head.prompt.fused) return p;
+  double best = p.head.us;
+  for (int64_t tail = ntok % 128; tail < 512 && tail < ntok; tail += 128) {
+    if (tail == 0) continue;
+    const int64_t split = ntok - tail;
+    const LinearPlan head = linear_plan(x, xdtype, split, ldx, m, n, G, n_out);
+    const LinearPlan rest =
+        linear_plan(rows_from(x, split, ldx, xdtype), xdtype, tail, ldx, m, n, G, n_out);
+    const double us = head.us + rest.us + 3.0;
+    if (us < best) {
+      best = us;
+      p.head = head;
+      p.rest = rest;
+      p.split = split;
+    }
   }
   return p;
 }

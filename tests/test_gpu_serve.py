@@ -130,7 +130,8 @@ def test_packed_linear_batches(tokens, m, n, group, x_kind):
 
 
 @pytest.mark.parametrize("tokens,m,n,x_kind", [(641, 4096, 4096, "bf16"), (1030, 4096, 4096, "int8"),
-                                               (1026, 1500, 3200, "f32"), (1100, 4096, 4096, "bf16")])
+                                               (1026, 1500, 3200, "f32"), (1100, 4096, 4096, "bf16"),
+                                               (2300, 4096, 2048, "bf16")])
 @pytest.mark.parametrize("aligned", [True, False])
 def test_packed_linear_tokens_past_whole_tiles(tokens, m, n, x_kind, aligned):
     """A few tokens more than tiles of 128 hold, in x and y with strides."""
