@@ -42,48 +42,14 @@
 namespace pwq {
 namespace {
 
-typedef __attribute__((__vector_size__(4 * sizeof(int)))) int i32x4_t;
-typedef __attribute__((address_space(3))) char lds_char;
-typedef __attribute__((address_space(4))) int const_int;
-
 constexpr int KB = 128;            // bytes of an x row per step
-
-// Asynchronous copies of 16 bytes, 4 bytes, or one byte (to a dword) per lane:
-// sbase + voff of each lane to lds + 16 lane, or lds + 4 lane (lds and sbase
-// wave-uniform).  M0 is restored.
-#define PWQ_COPY(NAME, OP)                                                                    \
-  __device__ __forceinline__ void NAME(uint32_t voff, const void* sbase, uint32_t lds) {     \
-    uint32_t keep;                                                                           \
-    asm volatile(                                                                            \
-        "s_mov_b32 %0, m0\n\t"                                                               \
-        "s_mov_b32 m0, %3\n\t" OP                                                            \
-        " %1, %2\n\t"                                                                        \
-        "s_mov_b32 m0, %0"                                                                   \
-        : "=&s"(keep)                                                                        \
-        : "v"(voff), "s"(sbase), "s"(lds)                                                    \
-        : "memory");                                                                         \
-  }
-PWQ_COPY(copy16, "global_load_lds_dwordx4")
-PWQ_COPY(copy4, "global_load_lds_dword")
-PWQ_COPY(copy1, "global_load_lds_ubyte")
-#undef PWQ_COPY
 
 // Byte of 16-byte unit c of LDS row r.
 __device__ __forceinline__ uint32_t unit_at(int r, int c) {
   return (uint32_t)(r * KB + ((c ^ ((r >> 1) & 7)) << 4));
 }
 
-// Eight 4-bit steps of a dword to bytes: w has the codes 0 .. 15, z4 the zero
-// point in every byte (z <= 127: no borrow passes a byte, as every byte is at
-// least 128 before the subtraction).
-__device__ __forceinline__ uint2 steps_i8(uint32_t w, uint32_t z4) {
-  const uint32_t even = (((w & 0x0f0f0f0fu) | 0x80808080u) - z4) ^ 0x80808080u;
-  const uint32_t odd = ((((w >> 4) & 0x0f0f0f0fu) | 0x80808080u) - z4) ^ 0x80808080u;
-  return make_uint2(__builtin_amdgcn_perm(odd, even, 0x05010400u),
-                    __builtin_amdgcn_perm(odd, even, 0x07030602u));
-}
-
-// ... to bf16: a code's four bits are put at the top of the mantissa of 16,
+// Eight 4-bit steps of a dword to bf16: a code's four bits are put at the top of the mantissa of 16,
 // and 16 + z is subtracted in float32, whose upper half holds the difference
 // exactly (no conversion instruction: those run at a quarter of the rate).
 // zb = 16 + z, or 24 with `bias` 0x41c0 for signed halves (it flips their top
@@ -884,7 +850,7 @@ PromptPlan prompt_plan(const void* x, int32_t xdtype, int64_t ntok, int64_t ldx,
                        int64_t n, int32_t G, int64_t n_out) {
   PromptPlan p{};
   const bool row = G == n;
-  // (256 rows of x within 32-bit offsets, three parts each)
+  // (128 rows of x within 32-bit offsets, three parts each)
   p.ok = (row || G % 32 == 0) && ntok > 0 && m > 0 && n < (1 << 21);
   if (!p.ok) return p;
   // 8-bit operands: a group's sum is an int32, of at most 128 columns unless

@@ -37,35 +37,11 @@
 namespace pwq {
 namespace {
 
-typedef __attribute__((__vector_size__(4 * sizeof(int)))) int i32x4_t;
-typedef __attribute__((address_space(3))) char lds_char;
-typedef __attribute__((address_space(4))) int const_int;
-
 enum { X_BF16 = 0, X_I8 = 1, X_F32 = 2, X_I8_BF16 = 3 };
 template <int XK> struct XType { using T = uint16_t; };
 template <> struct XType<X_I8> { using T = int8_t; };
 template <> struct XType<X_I8_BF16> { using T = int8_t; };
 template <> struct XType<X_F32> { using T = float; };
-
-// Asynchronous copies of 16 bytes, 4 bytes, or one byte (to a dword) per
-// active lane: sbase + voff of each lane to lds + 16 lane, or lds + 4 lane (lds
-// and sbase wave-uniform).  M0 is restored.
-#define PWQ_COPY(NAME, OP)                                                                    \
-  __device__ __forceinline__ void NAME(uint32_t voff, const void* sbase, uint32_t lds) {     \
-    uint32_t keep;                                                                           \
-    asm volatile(                                                                            \
-        "s_mov_b32 %0, m0\n\t"                                                               \
-        "s_mov_b32 m0, %3\n\t" OP                                                            \
-        " %1, %2\n\t"                                                                        \
-        "s_mov_b32 m0, %0"                                                                   \
-        : "=&s"(keep)                                                                        \
-        : "v"(voff), "s"(sbase), "s"(lds)                                                    \
-        : "memory");                                                                         \
-  }
-PWQ_COPY(copy16, "global_load_lds_dwordx4")
-PWQ_COPY(copy4, "global_load_lds_dword")
-PWQ_COPY(copy1, "global_load_lds_ubyte")
-#undef PWQ_COPY
 
 __device__ __forceinline__ uint32_t pack_hi(float a, float b) {   // exact for small integers
   return __builtin_amdgcn_perm(__float_as_uint(b), __float_as_uint(a), 0x07060302u);
@@ -98,15 +74,7 @@ __device__ __forceinline__ bf16x8_t steps_bf16(uint32_t w, uint32_t bias, float 
                              pack_hi(hi[2], hi[3]));
   return __builtin_bit_cast(bf16x8_t, o);
 }
-// Eight 4-bit codes to bytes.  Unsigned: u - z (every byte is at least 128
-// before the subtraction, so no borrow passes one).  Signed: 16 times the
-// code, its four bits at the top of the byte.
-__device__ __forceinline__ uint2 steps_i8(uint32_t w, uint32_t z4) {
-  const uint32_t even = (((w & 0x0f0f0f0fu) | 0x80808080u) - z4) ^ 0x80808080u;
-  const uint32_t odd = ((((w >> 4) & 0x0f0f0f0fu) | 0x80808080u) - z4) ^ 0x80808080u;
-  return make_uint2(__builtin_amdgcn_perm(odd, even, 0x05010400u),
-                    __builtin_amdgcn_perm(odd, even, 0x07030602u));
-}
+// Eight signed halves to bytes of 16 times the code, its four bits at the top.
 __device__ __forceinline__ uint2 signed16_i8(uint32_t w) {
   const uint32_t even = (w << 4) & 0xf0f0f0f0u, odd = w & 0xf0f0f0f0u;
   return make_uint2(__builtin_amdgcn_perm(odd, even, 0x05010400u),

@@ -131,4 +131,38 @@ struct DevFlags {
   int32_t pad[63];
 };
 
+typedef __attribute__((__vector_size__(4 * sizeof(int)))) int i32x4_t;
+typedef __attribute__((address_space(3))) char lds_char;
+typedef __attribute__((address_space(4))) int const_int;
+
+// Asynchronous copies of 16 bytes, 4 bytes, or one byte (to a dword) per active
+// lane: sbase + voff of each lane to lds + 16 lane, or lds + 4 lane (lds and
+// sbase wave-uniform).  M0 is restored.
+#define PWQ_COPY(NAME, OP)                                                                    \
+  __device__ __forceinline__ void NAME(uint32_t voff, const void* sbase, uint32_t lds) {     \
+    uint32_t keep;                                                                           \
+    asm volatile(                                                                            \
+        "s_mov_b32 %0, m0\n\t"                                                               \
+        "s_mov_b32 m0, %3\n\t" OP                                                            \
+        " %1, %2\n\t"                                                                        \
+        "s_mov_b32 m0, %0"                                                                   \
+        : "=&s"(keep)                                                                        \
+        : "v"(voff), "s"(sbase), "s"(lds)                                                    \
+        : "memory");                                                                         \
+  }
+PWQ_COPY(copy16, "global_load_lds_dwordx4")
+PWQ_COPY(copy4, "global_load_lds_dword")
+PWQ_COPY(copy1, "global_load_lds_ubyte")
+#undef PWQ_COPY
+
+// Eight 4-bit steps of a dword to bytes: w has the codes 0 .. 15, z4 the zero
+// point in every byte (z <= 127: no borrow passes a byte, as every byte is at
+// least 128 before the subtraction).
+__device__ __forceinline__ uint2 steps_i8(uint32_t w, uint32_t z4) {
+  const uint32_t even = (((w & 0x0f0f0f0fu) | 0x80808080u) - z4) ^ 0x80808080u;
+  const uint32_t odd = ((((w >> 4) & 0x0f0f0f0fu) | 0x80808080u) - z4) ^ 0x80808080u;
+  return make_uint2(__builtin_amdgcn_perm(odd, even, 0x05010400u),
+                    __builtin_amdgcn_perm(odd, even, 0x07030602u));
+}
+
 }  // namespace pwq
