@@ -269,7 +269,8 @@ template <typename T, int TPR, int NV>
 void launch_regs(const RmsNormLaunch& a, hipStream_t st) {
   constexpr int RPB = TPR < 256 ? 256 / TPR : 1;
   // workgroups that run at once: the rest of the tokens are walked over
-  const int64_t blocks = std::min<int64_t>((a.ntok + RPB - 1) / RPB, 256 * (1536 / std::max(TPR, 256) + (TPR == 1024)));
+  const int64_t blocks = std::min<int64_t>(
+      (a.ntok + RPB - 1) / RPB, 256 * (1536 / std::max(TPR, 256) + (TPR == 1024)));
   const dim3 grid((unsigned)blocks), block(TPR < 256 ? 256 : TPR);
   if (a.residual) rms_norm_regs<T, TPR, NV, true><<<grid, block, 0, st>>>(a);
   else rms_norm_regs<T, TPR, NV, false><<<grid, block, 0, st>>>(a);

@@ -49,11 +49,11 @@ __device__ __forceinline__ uint32_t unit_at(int r, int c) {
   return (uint32_t)(r * KB + ((c ^ ((r >> 1) & 7)) << 4));
 }
 
-// Eight 4-bit steps of a dword to bf16: a code's four bits are put at the top of the mantissa of 16,
-// and 16 + z is subtracted in float32, whose upper half holds the difference
-// exactly (no conversion instruction: those run at a quarter of the rate).
-// zb = 16 + z, or 24 with `bias` 0x41c0 for signed halves (it flips their top
-// bit; 0x4180 otherwise).
+// Eight 4-bit steps of a dword to bf16: a code's four bits are put at the top of
+// the mantissa of 16, and 16 + z is subtracted in float32, whose upper half holds
+// the difference exactly (no conversion instruction: those run at a quarter of
+// the rate).  zb = 16 + z, or 24 with `bias` 0x41c0 for signed halves (it flips
+// their top bit; 0x4180 otherwise).
 __device__ __forceinline__ uint4 steps_bf16(uint32_t w, uint32_t bias, float zb) {
   constexpr uint32_t M = 0x00780078u;
   const uint32_t c[4] = {((w << 3) & M) ^ bias, ((w >> 1) & M) ^ bias, ((w >> 5) & M) ^ bias,
@@ -328,7 +328,7 @@ void batch_tiles(const PromptArgs a) {
   const int k0 = split * a.per, k1 = min(across, k0 + a.per), last = k1 - 1;
 
   // copies
-  uint32_t xoff[NC], woff[2], wcol[2], row0[2];
+  uint32_t xoff[NC], woff[2], wcol[2];
 #pragma unroll
   for (int h = 0; h < NC; ++h) {
     const int u = 256 * h + tid, r = u >> 3, c = (u & 7) ^ ((r >> 1) & 7);

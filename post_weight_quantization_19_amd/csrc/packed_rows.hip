@@ -286,7 +286,8 @@ __global__ __launch_bounds__(1024) void packed_rows(const PackedLinearLaunch a) 
           const uint32_t bias = asym ? 0x41804180u : 0x41c041c0u;
 #pragma unroll
           for (int j = 0; j < NW; ++j) {
-            const bf16x8_t f = BIASED ? codes_bf16(w[j], bias) : steps_bf16(w[j], bias, 16.0f + (float)z);
+            const bf16x8_t f =
+                BIASED ? codes_bf16(w[j], bias) : steps_bf16(w[j], bias, 16.0f + (float)z);
             const int col = GB * h + NC * lq + 8 * j;
             T xv[8];
             if constexpr (XK == X_BF16) {

@@ -843,7 +843,9 @@ pwq_status pwq_ssqr_quant_layer(const void* W, int32_t wdtype, int64_t m, int64_
 
 // ------------------------------------------------------------ packed layers
 
-int64_t pwq_packed_row_bytes(int64_t n) { return n > 0 && n <= INT32_MAX ? packed_row_bytes(n) : 0; }
+int64_t pwq_packed_row_bytes(int64_t n) {
+  return n > 0 && n <= INT32_MAX ? packed_row_bytes(n) : 0;
+}
 
 int64_t pwq_pack_tiles(int64_t m, int64_t n) {
   if (m < 0 || n <= 0 || m > INT32_MAX || n > INT32_MAX) return 0;
@@ -1048,8 +1050,8 @@ pwq_status pwq_packed_linear(const void* x, int32_t xdtype, int64_t ntok, int64_
     if ((uintptr_t)qweight % 16)
       return fail(PWQ_ERR_INVALID_ARG, "qweight must be 16-byte aligned");
   }
-  pwq_status s = check_ws(ws, ws_bytes,
-                          pwq_packed_linear_workspace_size(x, xdtype, ntok, ldx, m, n, group, n_out));
+  pwq_status s = check_ws(
+      ws, ws_bytes, pwq_packed_linear_workspace_size(x, xdtype, ntok, ldx, m, n, group, n_out));
   if (s != PWQ_OK) return s;
   PackedLinearLaunch a{x, xdtype, ntok, ldx, x_scales, qweight, m, n, packed_row_bytes(n), scales,
                        zeros, group > 0 ? group : (int32_t)n, n_out > 0 ? outlier_off : nullptr,
