@@ -27,7 +27,8 @@
  *   overflow : the codes outside the half's range, as a list sorted by tile
  *              of 16 rows x 128 columns (tiles row-major, pwq_pack_tiles(m, n)
  *              of them), then row, then column.  Entry = (c - clip(c)) * 65536
- *              + (row % 16) * 128 + column % 128.  outlier_off[t] is the first
+ *              + (row % 16) * 128 + column % 128 (with steps as below, c -
+ *              clip(c) lies in -127 .. 239).  outlier_off[t] is the first
  *              entry of tile t, outlier_off[tiles] their number.  The SSQR
  *              outliers of pwq_overflow_entries [GEOM 3] are such codes; here
  *              they stay integers, so the product of the packed layer is that

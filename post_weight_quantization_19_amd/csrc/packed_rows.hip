@@ -311,7 +311,7 @@ __global__ __launch_bounds__(1024) void packed_rows(const PackedLinearLaunch a) 
         constexpr int PE = XK == X_I8 ? 16 : 8;          // entries of a lane at a time
         if constexpr (OVER) for (int e = e0; e < e1; e += 4 * PE) {
           // the lane's entries e + 4 i + l / 16; most tiles have few, so by twos
-          int val[PE] = {};
+          int val[PE] = {}, most = 0;
           T xe[PE] = {};
           if (e < ebase || min(e + 4 * PE, e1) > ebase + kEntries) {
             asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
@@ -328,15 +328,26 @@ __global__ __launch_bounds__(1024) void packed_rows(const PackedLinearLaunch a) 
               xe[k] = *(const T*)(x_unit(xs, col * ES / 16) + col * ES % 16);
               val[k] = e + 4 * k + lq < e1 && col / GB == h && ((ent >> 7) & 15) == lr ? ent >> 16
                                                                                       : 0;
+              if constexpr (XK == X_I8 && ASYM) most = max(most, val[k]);
             }
           }
           if constexpr (XK == X_I8) {
-            i32x4_t f = {0, 0, 0, 0};
-#pragma unroll
-            for (int i = 0; i < PE; ++i) f[i / 4] |= (val[i] & 255) << (8 * (i % 4));
             i32x4_t v;
             __builtin_memcpy(&v, xe, 16);
-            ce = __builtin_amdgcn_mfma_i32_16x16x64_i8(v, f, ce, 0, 0, 0);
+            auto multiply = [&](auto of) {
+              i32x4_t f = {0, 0, 0, 0};
+#pragma unroll
+              for (int i = 0; i < PE; ++i) f[i / 4] |= (of(val[i]) & 255) << (8 * (i % 4));
+              ce = __builtin_amdgcn_mfma_i32_16x16x64_i8(v, f, ce, 0, 0, 0);
+            };
+            // an entry beside a zero point above 15 goes to 239: what a signed
+            // byte does not hold is multiplied on its own
+            if (ASYM && __any(most > 127)) {
+              multiply([](int e) { return min(e, 127); });
+              multiply([](int e) { return max(e - 127, 0); });
+            } else {
+              multiply([](int e) { return e; });
+            }
           } else {
             float d[PE];
 #pragma unroll

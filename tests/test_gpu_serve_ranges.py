@@ -1,12 +1,19 @@
 """The norm and the packed layer's product at the ends of what
 include/pwq_serve.h allows, each against its own definition.
+
+Linear tolerances, from the arithmetic: a matrix instruction adds the products
+of 32 columns (64 in 8 bits, exact) to a float32 with at most four roundings,
+three times over for float32 x in its three bf16 parts; steps, waves, splits
+and scales add fewer than n / 32 + 64 more.  A rounding is at most 2^-24 of the
+sum of the terms' absolute values.  A bf16 output adds half a unit in its last
+place, 2^-8 of the value.
 """
 import numpy as np
 import pytest
 import torch
 
 import post_weight_quantization_19_amd as P
-from test_gpu_serve import DT, hidden
+from test_gpu_serve import DT, HALF_BF16, U, activations, f64, hidden, packed_layer
 
 pytestmark = pytest.mark.gpu
 
@@ -26,3 +33,92 @@ def test_norm_codes_are_the_rounded_quotient(tokens, n, x_kind):
     want = np.abs(y).max(axis=1) / np.float32(127)
     assert np.array_equal(step.cpu().numpy(), want)
     assert np.array_equal(q.cpu().numpy(), np.rint(y / want[:, None]).astype(np.int8))
+
+
+def wide_layer(rng, m, n, group, density):
+    """ASYM codes with zero points 16 .. 127 and steps to +-127."""
+    ng = n // (group or n)
+    zeros = rng.integers(16, 128, (m, ng)).astype(np.int32)
+    zeros[rng.random((m, ng)) < 0.3] = 127
+    z = np.repeat(zeros, n // ng, axis=1)
+    codes = rng.integers(0, 16, (m, n))
+    far = rng.random((m, n)) < density
+    far[0, n // 2] = True
+    codes = np.where(far, z + rng.integers(-127, 128, (m, n)), codes)
+    codes = np.where(far & (rng.random((m, n)) < 0.3), z + 127, codes)
+    codes[0, n // 2] = z[0, n // 2] + 127
+    scales = (0.003 * np.exp(0.3 * rng.standard_normal((m, ng)))).astype(np.float32)
+    return codes.astype(np.int32), scales, zeros
+
+
+def product(x, xs, codes, scales, zeros):
+    """(y, sum of the terms' absolute values), float64, by the definition."""
+    step = codes.astype(np.float64)
+    ng = scales.shape[1]
+    if zeros is not None:
+        step = step - np.repeat(zeros.astype(np.float64), codes.shape[1] // ng, axis=1)
+    w = step * np.repeat(scales.astype(np.float64), codes.shape[1] // ng, axis=1)
+    x = f64(x) * (1 if xs is None else f64(xs)[:, None])
+    return x @ w.T, np.abs(x) @ np.abs(w).T
+
+
+def check(y, x, xs, codes, scales, zeros):
+    n = codes.shape[1]
+    want, size = product(x, xs, codes, scales, zeros)
+    parts = 3 if x.dtype == torch.float32 else 1
+    tol = (parts * n / 8 + n / 32 + 64) * U * size
+    if y.dtype == torch.bfloat16:
+        tol = tol + HALF_BF16 * np.abs(want)
+    worst = (np.abs(f64(y) - want) / np.maximum(tol, 1e-300)).max()
+    assert worst <= 1, float(worst)
+
+
+@pytest.mark.parametrize("x_kind", ["int8", "f32", "bf16"])
+@pytest.mark.parametrize("n,group", [(1024, 128), (640, 64), (1152, 192), (416, 32), (1000, 0),
+                                     (200, 20)])
+def test_overflow_entries_above_127(n, group, x_kind):
+    """With zero points above 15 an overflow entry, code - 15, goes to 239."""
+    m = 50
+    for density in (0.002, 0.05, 1.0):
+        rng = np.random.default_rng([n, group, int(1000 * density)])
+        codes, scales, zeros = wide_layer(rng, m, n, group, density)
+        pk = packed_layer(codes, scales, zeros, group)
+        assert int((pk["outliers"] >> 16).max()) > 127
+        for tokens in (1, 2, 8, 9, 16, 17, 40, 140):
+            print(f"[ranges] above 127 {n} {group} {x_kind} {density} {tokens}", flush=True)
+            x, xs = activations(rng, tokens, n, x_kind)
+            y = P.packed_linear(x.cuda(), pk, x_scales=None if xs is None else xs.cuda(),
+                                out_dtype=torch.float32)
+            check(y, x, xs, codes, scales, zeros)
+
+
+def test_overflow_entries_above_127_past_whole_tiles():
+    """The same layer for a prompt whose last tokens go to the kernels for few."""
+    rng = np.random.default_rng(127)
+    codes, scales, zeros = wide_layer(rng, 4096, 4096, 128, 0.001)
+    pk = packed_layer(codes, scales, zeros, 128)
+    x, xs = activations(rng, 1030, 4096, "int8")
+    y = P.packed_linear(x.cuda(), pk, x_scales=xs.cuda(), out_dtype=torch.float32)
+    check(y[-16:], x[-16:], xs[-16:], codes, scales, zeros)
+    check(y[:16], x[:16], xs[:16], codes, scales, zeros)
+
+
+@pytest.mark.parametrize("multiplier", [0.0625, 0.3])
+def test_layer_of_small_steps(multiplier):
+    """Steps made small by the grid's multiplier: zero points near 120, codes
+    to 240, quantized, packed and multiplied."""
+    rng = np.random.default_rng(16)
+    m, n = 48, 512
+    W = torch.from_numpy(rng.uniform(-1, 1, (m, n)).astype(np.float32)).cuda()
+    grid = P.Grid("asym", 4, 128, kappa=multiplier)
+    scales, zeros = P.grid_steps(W, grid)
+    s = f64(scales).repeat(128, axis=1)
+    z = zeros.cpu().numpy().astype(np.int64).repeat(128, axis=1)
+    codes = np.clip(np.rint(f64(W) / s), -127, 127).astype(np.int64) + z
+    pk = P.pack_weights(torch.from_numpy(codes.astype(np.int32)).cuda(), scales, grid, zeros)
+    for x_kind in ("int8", "bf16"):
+        for tokens in (1, 16, 17):
+            x, xs = activations(rng, tokens, n, x_kind)
+            y = P.packed_linear(x.cuda(), pk, x_scales=None if xs is None else xs.cuda(),
+                                out_dtype=torch.float32)
+            check(y, x, xs, codes, scales.cpu().numpy(), zeros.cpu().numpy())
