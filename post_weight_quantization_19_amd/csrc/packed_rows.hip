@@ -47,28 +47,22 @@ __device__ __forceinline__ uint32_t pack_hi(float a, float b) {   // exact for s
   return __builtin_amdgcn_perm(__float_as_uint(b), __float_as_uint(a), 0x07060302u);
 }
 
-// Eight 4-bit codes of a dword to bf16 16 + u, u = 0 .. 15 (`bias` 0x4180 per
-// half, or 0x41c0 for signed halves, whose top bit it flips): the code lands
-// in the top four of seven mantissa bits.  Order: columns 0 4 1 5 2 6 3 7.
-__device__ __forceinline__ bf16x8_t codes_bf16(uint32_t w, uint32_t bias) {
-  constexpr uint32_t M = 0x00780078u;
-  const uint4 o = make_uint4(((w << 3) & M) ^ bias, ((w >> 1) & M) ^ bias, ((w >> 5) & M) ^ bias,
-                             ((w >> 9) & M) ^ bias);
-  return __builtin_bit_cast(bf16x8_t, o);
-}
-// The same minus zb = 16 + z (24 for signed halves), in the columns' order:
-// the difference is taken in float32, whose upper half holds it exactly.
-// float32 x takes these: next to 16 + u, the correction by the sum of x costs
-// its result three bits.
+// Eight 4-bit steps of a dword to bf16.  A code, bits 0 .. 3 of a float16 64 +
+// u / 16 (`bias` 0x5400 per half, or 0x5408 for signed halves, whose top bit it
+// flips), becomes 1024 + u, less zb = 1024 + z (1032 for signed halves), in one
+// multiplication and addition; the upper half of that float32 holds the
+// difference exactly.  (Codes as 16 + u in bf16, corrected by 16 + z times the
+// sum of x, are 1 to 3% faster, but lose three bits of a small result and all
+// of one whose x is above 2^123.)
 __device__ __forceinline__ bf16x8_t steps_bf16(uint32_t w, uint32_t bias, float zb) {
-  constexpr uint32_t M = 0x00780078u;
-  const uint32_t c[4] = {((w << 3) & M) ^ bias, ((w >> 1) & M) ^ bias, ((w >> 5) & M) ^ bias,
-                         ((w >> 9) & M) ^ bias};
-  float lo[4], hi[4];
+  typedef _Float16 f16x2_t __attribute__((ext_vector_type(2)));
+  constexpr uint32_t M = 0x000f000fu;
+  float lo[4], hi[4];                                  // columns i and i + 4
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    lo[i] = __uint_as_float(c[i] << 16) - zb;
-    hi[i] = __uint_as_float(c[i] & 0xffff0000u) - zb;
+    const f16x2_t h = __builtin_bit_cast(f16x2_t, ((w >> (4 * i)) & M) ^ bias);
+    lo[i] = fmaf((float)h[0], 16.0f, -zb);
+    hi[i] = fmaf((float)h[1], 16.0f, -zb);
   }
   const uint4 o = make_uint4(pack_hi(lo[0], lo[1]), pack_hi(lo[2], lo[3]), pack_hi(hi[0], hi[1]),
                              pack_hi(hi[2], hi[3]));
@@ -85,22 +79,17 @@ __device__ __forceinline__ f32x4_t mma(bf16x8_t x, bf16x8_t w, f32x4_t c) {
   return __builtin_amdgcn_mfma_f32_16x16x32_bf16(x, w, c, 0, 0, 0);
 }
 
-// Eight columns of x as bf16 operands, in the order of codes_bf16 (PAIRED) or
-// their own; float32 x as three bf16 parts that add up to it: the top, middle
-// and last 8 bits of the significand (truncated: exact, and no overflow).
+// Eight columns of x as bf16 operands; float32 x as three bf16 parts that add up
+// to it: the top, middle and last 8 bits of the significand (truncated: exact,
+// and no overflow).
 template <int XK> constexpr int kParts = XK == X_F32 ? 3 : 1;
-template <int XK, bool PAIRED>
+template <int XK>
 __device__ __forceinline__ void x_parts(const typename XType<XK>::T* p,
                                         bf16x8_t (&out)[kParts<XK>]) {
   uint4 o;
   uint32_t* q = (uint32_t*)&o;
   if constexpr (XK == X_BF16) {
     __builtin_memcpy(&o, p, 16);
-    if constexpr (PAIRED)
-      o = make_uint4(__builtin_amdgcn_perm(o.z, o.x, 0x05040100u),
-                     __builtin_amdgcn_perm(o.z, o.x, 0x07060302u),
-                     __builtin_amdgcn_perm(o.w, o.y, 0x05040100u),
-                     __builtin_amdgcn_perm(o.w, o.y, 0x07060302u));
     out[0] = __builtin_bit_cast(bf16x8_t, o);
   } else {
     float v[8];
@@ -110,8 +99,8 @@ __device__ __forceinline__ void x_parts(const typename XType<XK>::T* p,
     for (int part = 0; part < kParts<XK>; ++part) {
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        float& lo = v[PAIRED ? i : 2 * i];
-        float& hi = v[PAIRED ? i + 4 : 2 * i + 1];
+        float& lo = v[2 * i];
+        float& hi = v[2 * i + 1];
         q[i] = pack_hi(lo, hi);
         if (part + 1 < kParts<XK>) {
           lo -= __uint_as_float(__float_as_uint(lo) & 0xffff0000u);
@@ -140,7 +129,6 @@ __global__ __launch_bounds__(1024) void packed_rows(const PackedLinearLaunch a) 
   using T = typename XType<XK>::T;
   using acc_t = std::conditional_t<XK == X_I8, i32x4_t, f32x4_t>;
   constexpr int ES = sizeof(T);
-  constexpr bool BIASED = XK == X_BF16;
   constexpr int NB = 128 / GB, NC = GB / 4;     // blocks of a tile, columns of a lane in one
   constexpr int NW = NC / 8;                    // dwords of a lane per block
   constexpr int XROW = 128 * ES, UNITS = XROW / 16, RPC = 64 / UNITS;   // x rows per copy
@@ -268,7 +256,7 @@ __global__ __launch_bounds__(1024) void packed_rows(const PackedLinearLaunch a) 
           const int o = (GB * h + NC * lq) / 2;
           __builtin_memcpy(w, ws + lr * 64 + (((o >> 4) ^ (lr >> 2)) << 4) + (o & 15), 4 * NW);
         }
-        acc_t c = {0, 0, 0, 0}, c1s = {0, 0, 0, 0};   // sums of the codes' terms, of x alone
+        acc_t c = {0, 0, 0, 0};
         if constexpr (XK == X_I8) {
           const uint32_t z4 = (uint32_t)z * 0x01010101u;
 #pragma unroll
@@ -281,13 +269,10 @@ __global__ __launch_bounds__(1024) void packed_rows(const PackedLinearLaunch a) 
             c = __builtin_amdgcn_mfma_i32_16x16x64_i8(v, f, c, 0, 0, 0);
           }
         } else {
-          constexpr uint32_t kOne = 0x3f803f80u;
-          const bf16x8_t ones = __builtin_bit_cast(bf16x8_t, make_uint4(kOne, kOne, kOne, kOne));
-          const uint32_t bias = asym ? 0x41804180u : 0x41c041c0u;
+          const uint32_t bias = asym ? 0x54005400u : 0x54085408u;
 #pragma unroll
           for (int j = 0; j < NW; ++j) {
-            const bf16x8_t f =
-                BIASED ? codes_bf16(w[j], bias) : steps_bf16(w[j], bias, 16.0f + (float)z);
+            const bf16x8_t f = steps_bf16(w[j], bias, 1024.0f + (float)z);
             const int col = GB * h + NC * lq + 8 * j;
             T xv[8];
             if constexpr (XK == X_BF16) {
@@ -299,12 +284,9 @@ __global__ __launch_bounds__(1024) void packed_rows(const PackedLinearLaunch a) 
               __builtin_memcpy(xv, x_unit(xs, col / 16) + col % 16, 8);
             }
             bf16x8_t v[kParts<XK>];
-            x_parts<XK, BIASED>(xv, v);
+            x_parts<XK>(xv, v);
 #pragma unroll
-            for (int part = 0; part < kParts<XK>; ++part) {
-              c = mma(v[part], f, c);
-              if constexpr (BIASED) c1s = mma(v[part], ones, c1s);
-            }
+            for (int part = 0; part < kParts<XK>; ++part) c = mma(v[part], f, c);
           }
         }
         acc_t ce = {0, 0, 0, 0};
@@ -355,7 +337,7 @@ __global__ __launch_bounds__(1024) void packed_rows(const PackedLinearLaunch a) 
             const uint4 o = make_uint4(pack_hi(d[0], d[1]), pack_hi(d[2], d[3]),
                                        pack_hi(d[4], d[5]), pack_hi(d[6], d[7]));
             bf16x8_t v[kParts<XK>];
-            x_parts<XK, false>(xe, v);
+            x_parts<XK>(xe, v);
 #pragma unroll
             for (int part = 0; part < kParts<XK>; ++part)
               ce = mma(v[part], __builtin_bit_cast(bf16x8_t, o), ce);
@@ -368,7 +350,7 @@ __global__ __launch_bounds__(1024) void packed_rows(const PackedLinearLaunch a) 
             if constexpr (OVER) v += asym ? ce[e] : 16 * ce[e];
             acc[e] = fmaf(s, (float)v, acc[e]);
           } else {
-            float v = BIASED ? fmaf(-16.0f - (float)z, c1s[e], c[e]) : c[e];
+            float v = c[e];
             if constexpr (OVER) v += ce[e];
             acc[e] = fmaf(s, v, acc[e]);
           }

@@ -122,3 +122,58 @@ def test_layer_of_small_steps(multiplier):
             y = P.packed_linear(x.cuda(), pk, x_scales=None if xs is None else xs.cuda(),
                                 out_dtype=torch.float32)
             check(y, x, xs, codes, scales.cpu().numpy(), zeros.cpu().numpy())
+
+
+@pytest.mark.parametrize("x_kind", ["bf16", "f32", "int8"])
+@pytest.mark.parametrize("tokens", [1, 7, 16, 17, 140])
+def test_rows_of_zero_steps_give_zero(tokens, x_kind):
+    """Every code at its zero point: the product is 0, not its rounding."""
+    rng = np.random.default_rng(tokens)
+    m, n = 40, 1000
+    for kind in ("sym", "asym"):
+        zeros = rng.integers(0, 16, (m, 1)).astype(np.int32) if kind == "asym" else None
+        codes = np.zeros((m, n), np.int32) if zeros is None else zeros.repeat(n, axis=1)
+        pk = packed_layer(codes.astype(np.int32), np.ones((m, 1), np.float32), zeros, 0)
+        x, xs = activations(rng, tokens, n, x_kind)
+        y = P.packed_linear(x.cuda(), pk, x_scales=None if xs is None else xs.cuda(),
+                            out_dtype=torch.float32)
+        assert torch.all(y == 0), (kind, float(y.abs().max()))
+
+
+@pytest.mark.parametrize("x_kind", ["bf16", "f32"])
+@pytest.mark.parametrize("tokens", [1, 5, 16, 17, 140])
+def test_large_finite_tokens(tokens, x_kind):
+    """x of 2^125 and steps of 1 and -1: finite, and exact."""
+    m, n = 33, 256
+    for kind in ("sym", "asym"):
+        codes = np.zeros((m, n), np.int32)
+        codes[:, 3], codes[:, 200] = 1, -1
+        zeros = None
+        if kind == "asym":
+            codes += 9
+            zeros = np.full((m, 2), 9, np.int32)
+        pk = packed_layer(codes, np.full((m, 2), 0.5, np.float32), zeros, 128)
+        x = torch.zeros((tokens, n), dtype=DT[x_kind])
+        x[:, 3], x[:, 200] = 2.0 ** 125, 2.0 ** 124
+        y = P.packed_linear(x.cuda(), pk, out_dtype=torch.float32)
+        assert torch.all(y == 2.0 ** 123), (kind, y.flatten()[:4].tolist())
+
+
+@pytest.mark.parametrize("x_kind", ["bf16", "f32", "int8"])
+@pytest.mark.parametrize("tokens", [1, 16, 33, 140])
+def test_small_steps_next_to_large_x(tokens, x_kind):
+    """Steps of a few units: the error follows |step| |x|, whatever the stored
+    code and zero point are."""
+    rng = np.random.default_rng([tokens, 5])
+    m, n, group = 64, 4096, 128
+    for kind in ("sym", "asym"):
+        step = rng.integers(-1, 2, (m, n)) * (rng.random((m, n)) < 0.05)
+        zeros = rng.integers(1, 15, (m, n // group)).astype(np.int32) if kind == "asym" else None
+        codes = step if zeros is None else step + zeros.repeat(group, axis=1)
+        scales = np.full((m, n // group), 0.25, np.float32)
+        codes = codes.astype(np.int32)
+        pk = packed_layer(codes, scales, zeros, group)
+        x, xs = activations(rng, tokens, n, x_kind)
+        y = P.packed_linear(x.cuda(), pk, x_scales=None if xs is None else xs.cuda(),
+                            out_dtype=torch.float32)
+        check(y, x, xs, codes, scales, zeros)
