@@ -85,9 +85,9 @@ pwq_status pwq_pack_overflow(const int32_t* codes, int64_t m, int64_t n, int64_t
  *              memory of x or of residual with the same stride.
  *   y        : out, row stride ldy >= n, ydtype PWQ_F32, PWQ_BF16 or PWQ_I8.
  *   scales   : PWQ_I8: out, ntok float32: the step max|y| / 127 of each token
- *              (1 where y is all zero); y = rint(value / step).  A token whose
- *              y holds a NaN gets the step NaN and the codes 0.  Unused
- *              otherwise.
+ *              (1 where that is 0); y = rint(value / step), within -127 ..
+ *              127.  A token whose y holds a NaN or an infinity gets that as
+ *              its step, and the codes 0.  Unused otherwise.
  * A square or their sum beyond float32's range (|h| above 1e19) gives 0.
  * ---------------------------------------------------------------------- */
 pwq_status pwq_rms_norm(const void* x, int32_t xdtype, int64_t ntok, int64_t n, int64_t ldx,

@@ -41,6 +41,13 @@ __device__ __forceinline__ float block_sum(float v, float* red) {
 // Maximum in which a NaN wins.
 __device__ __forceinline__ float max_nan(float a, float b) { return (a > b || a != a) ? a : b; }
 
+// The code of a rounded quotient; 0 in a token whose maximum (or step) is not
+// finite.  A step of a few units of the smallest float32 is rounded by up to a
+// half, so that quotients go to 190: they are cut at 127.
+__device__ __forceinline__ float code_of(float q, float mx) {
+  return mx <= __FLT_MAX__ ? fminf(fmaxf(q, -127.0f), 127.0f) : 0.0f;
+}
+
 __device__ __forceinline__ float block_max(float v, float* red) {
 #pragma unroll
   for (int o = 32; o >= 1; o >>= 1) v = max_nan(v, __shfl_xor(v, o, 64));
@@ -199,10 +206,11 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void rms_norm_regs(const Rms
       if (in == 0) a.scales[t] = step;
       // rint(h / step).  The product with the reciprocal is within 2^-16 of the
       // quotient (1.5 units of the last place of 127), so that it rounds alike
-      // unless it lies that near a tie; there, and with a reciprocal that may
-      // not be finite, divide.  (Always dividing: one token of 14336 6.0 us
-      // instead of 5.2, 2048 of them 59.5 instead of 56.5.)
-      const float inv = 1.0f / step, near = mx > 1e-30f ? 0.5f - 0x1p-15f : -1.0f;
+      // unless it lies that near a tie; there, and where the maximum or the
+      // reciprocal may not be finite, divide.  (Always dividing: one token of
+      // 14336 6.0 us instead of 5.2, 2048 of them 59.5 instead of 56.5.)
+      const float inv = 1.0f / step;
+      const float near = mx > 1e-30f && mx <= __FLT_MAX__ ? 0.5f - 0x1p-15f : -1.0f;
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
         float c[8], off = 0.0f;
@@ -214,10 +222,8 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void rms_norm_regs(const Rms
         }
         if (off > near)
 #pragma unroll
-          for (int e = 0; e < 8; ++e) c[e] = __builtin_rintf(h[i][e] / step);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) h[i][e] = mx == mx ? c[e] : 0.0f;
-        store8((int8_t*)a.y + t * a.ldy + at[i], lo[i], h[i]);
+          for (int e = 0; e < 8; ++e) c[e] = code_of(__builtin_rintf(h[i][e] / step), mx);
+        store8((int8_t*)a.y + t * a.ldy + at[i], lo[i], c);
       }
     } else {
 #pragma unroll
@@ -270,8 +276,7 @@ __global__ __launch_bounds__(256) void rms_norm_rows(
     if (ydtype == PWQ_F32) ((float*)y)[t * ldy + k] = v;
     else if (ydtype == PWQ_BF16) ((__bf16*)y)[t * ldy + k] = (__bf16)v;
     else {
-      const float q = __builtin_rintf(v / step);
-      ((int8_t*)y)[t * ldy + k] = q == q ? (int8_t)(int)q : (int8_t)0;
+      ((int8_t*)y)[t * ldy + k] = (int8_t)(int)code_of(__builtin_rintf(v / step), step);
     }
   }
 }

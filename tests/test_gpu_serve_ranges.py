@@ -35,6 +35,41 @@ def test_norm_codes_are_the_rounded_quotient(tokens, n, x_kind):
     assert np.array_equal(q.cpu().numpy(), np.rint(y / want[:, None]).astype(np.int8))
 
 
+@pytest.mark.parametrize("n", [6, 300, 4096, 40960])
+def test_norm_codes_of_the_smallest_values(n):
+    """A step of one or two units of the smallest float32 is far from 1 / 127
+    of the maximum: codes stay within -127 .. 127."""
+    tiny = 2.0 ** -149
+    for units in (1, 63, 64, 100, 190, 200, 300):
+        x = torch.ones((2, n), device="cuda")
+        x[1] = -1
+        w = torch.full((n,), units * tiny, device="cuda", dtype=torch.float32)
+        w[n // 2:] = 0
+        q, step, _ = P.rms_norm(x, w, eps=0.0, out_dtype=torch.int8)
+        s = np.float32(units * tiny) / np.float32(127)
+        s = np.float32(1) if s == 0 else s
+        want = min(127, int(np.rint(np.float32(units * tiny) / s)))
+        assert step.tolist() == [float(s)] * 2
+        print(f"[ranges] tiny {n} {units} {want}", flush=True)
+        assert torch.all(q[0, :n // 2] == want) and torch.all(q[1, :n // 2] == -want)
+        assert torch.all(q[:, n // 2:] == 0)
+
+
+@pytest.mark.parametrize("n", [6, 300, 4096, 40960])
+def test_norm_codes_beside_an_infinity(n):
+    """A value beyond float32's range: an infinite step and codes 0, in its
+    token alone."""
+    x = torch.ones((3, n), device="cuda")
+    x[1, 2], x[2, 2] = 0, -2
+    w = torch.ones(n, device="cuda")
+    w[2] = 3.4e38
+    x[0, 2] = 2
+    q, step, _ = P.rms_norm(x, w, eps=0.0, out_dtype=torch.int8)
+    print(f"[ranges] infinity {n}", flush=True)
+    assert torch.isinf(step[[0, 2]]).all() and torch.isfinite(step[1])
+    assert torch.all(q[[0, 2]] == 0) and torch.all(q[1, 3:] == 127) and q[1, 2] == 0
+
+
 def wide_layer(rng, m, n, group, density):
     """ASYM codes with zero points 16 .. 127 and steps to +-127."""
     ng = n // (group or n)
