@@ -82,8 +82,10 @@ pwq_status pwq_pack_overflow(const int32_t* codes, int64_t m, int64_t n, int64_t
  *   weight   : n values, wdtype PWQ_F32 or PWQ_BF16.
  *   eps      : finite, >= 0.
  *   sum      : NULL, or out: h in x's type, row stride lds >= n; may be the
- *              memory of x or of residual with the same stride.
- *   y        : out, row stride ldy >= n, ydtype PWQ_F32, PWQ_BF16 or PWQ_I8.
+ *              memory of x or of residual with the same stride, and else
+ *              overlaps neither.
+ *   y        : out, row stride ldy >= n, ydtype PWQ_F32, PWQ_BF16 or PWQ_I8;
+ *              overlaps no other argument.
  *   scales   : PWQ_I8: out, ntok float32: the step max|y| / 127 of each token
  *              (1 where that is 0); y = rint(value / step), within -127 ..
  *              127.  A token whose y holds a NaN or an infinity gets that as
@@ -105,7 +107,9 @@ pwq_status pwq_rms_norm(const void* x, int32_t xdtype, int64_t ntok, int64_t n, 
  *               NULL for SYM; outlier_off and outliers NULL (n_out 0) when no
  *               code overflows.  n_out = outlier_off[tiles].
  *   group     : G, 0 for one step per row; divides n.
- *   y         : out, ntok x m, row stride ldy >= m, ydtype PWQ_F32 or PWQ_BF16.
+ *   y         : out, ntok x m, row stride ldy >= m, ydtype PWQ_F32 or PWQ_BF16;
+ *               must not overlap x (rows of the two may lie side by side in a
+ *               wider matrix).
  *   ws        : pwq_packed_linear_workspace_size bytes, for this x, sizes,
  *               group and n_out (0 for few tokens whose rows of x are 16-byte aligned).
  * Steps c - z multiply x as integers and a group's sum is multiplied by its

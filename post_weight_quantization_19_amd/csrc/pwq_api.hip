@@ -905,6 +905,30 @@ pwq_status pwq_pack_overflow(const int32_t* codes, int64_t m, int64_t n, int64_t
   return ok();
 }
 
+static int64_t elem_bytes(int32_t dtype) {
+  return dtype == PWQ_I8 ? 1 : (dtype == PWQ_BF16 ? 2 : 4);
+}
+
+// Rows of a matrix in memory, bytes; NULL overlaps nothing.
+struct Rows {
+  const void* p;
+  int64_t rows, width, stride;
+  Rows(const void* p, int64_t rows, int64_t cols, int64_t ld, int32_t dtype)
+      : p(p), rows(rows), width(cols * elem_bytes(dtype)), stride(ld * elem_bytes(dtype)) {}
+};
+static bool overlap(const Rows& a, const Rows& b) {
+  if (!a.p || !b.p || a.rows == 0 || b.rows == 0) return false;
+  const uintptr_t pa = (uintptr_t)a.p, pb = (uintptr_t)b.p;
+  if (pa + (a.rows - 1) * a.stride + a.width <= pb || pb + (b.rows - 1) * b.stride + b.width <= pa)
+    return false;
+  // side by side in the rows of a wider matrix
+  if (a.rows > 1 && a.stride == b.stride) {
+    const int64_t d = ((int64_t)(pb - pa) % a.stride + a.stride) % a.stride;
+    return d < a.width || d + b.width > a.stride;
+  }
+  return true;
+}
+
 pwq_status pwq_rms_norm(const void* x, int32_t xdtype, int64_t ntok, int64_t n, int64_t ldx,
                         const void* residual, int64_t ldr, const void* weight, int32_t wdtype,
                         double eps, void* sum, int64_t lds, void* y, int32_t ydtype,
@@ -925,10 +949,14 @@ pwq_status pwq_rms_norm(const void* x, int32_t xdtype, int64_t ntok, int64_t n, 
     return fail(PWQ_ERR_INVALID_ARG, "8-bit y needs scales");
   if (ldx < n || ldy < n || (residual && ldr < n) || (sum && lds < n))
     return fail(PWQ_ERR_INVALID_ARG, "row strides must be >= n");
-  if (ntok > 0 && (y == x || y == residual || y == sum))
-    return fail(PWQ_ERR_INVALID_ARG, "y must not be the memory of x, residual or sum");
+  const Rows rx(x, ntok, n, ldx, xdtype), rr(residual, ntok, n, ldr, xdtype);
+  const Rows rs(sum, ntok, n, lds, xdtype), ry(y, ntok, n, ldy, ydtype);
+  if (overlap(ry, rx) || overlap(ry, rr) || overlap(ry, rs))
+    return fail(PWQ_ERR_INVALID_ARG, "y must not overlap x, residual or sum");
   if (sum && ((sum == x && lds != ldx) || (sum == residual && lds != ldr)))
     return fail(PWQ_ERR_INVALID_ARG, "sum in place needs the same row stride");
+  if ((sum != x && overlap(rs, rx)) || (sum != residual && overlap(rs, rr)))
+    return fail(PWQ_ERR_INVALID_ARG, "sum may be x or residual, or overlap neither");
   RmsNormLaunch a{x, xdtype, ntok, n, ldx, residual, ldr, weight, wdtype, (float)eps, sum, lds,
                   y, ydtype, ldy, scales};
   const hipError_t e = launch_rms_norm(a, (hipStream_t)stream);
@@ -969,8 +997,7 @@ struct LinearParts {
   int64_t split = 0;        // first token of the rest; ntok: none
 };
 static const void* rows_from(const void* p, int64_t row, int64_t ld, int32_t dtype) {
-  const int64_t es = dtype == PWQ_I8 ? 1 : (dtype == PWQ_BF16 ? 2 : 4);
-  return (const char*)p + row * ld * es;
+  return (const char*)p + row * ld * elem_bytes(dtype);
 }
 static LinearParts linear_parts(const void* x, int32_t xdtype, int64_t ntok, int64_t ldx,
                                 int64_t m, int64_t n, int32_t G, int64_t n_out) {
@@ -1049,6 +1076,8 @@ pwq_status pwq_packed_linear(const void* x, int32_t xdtype, int64_t ntok, int64_
       return fail(PWQ_ERR_INVALID_ARG, "x, qweight, scales and y must be non-NULL");
     if ((uintptr_t)qweight % 16)
       return fail(PWQ_ERR_INVALID_ARG, "qweight must be 16-byte aligned");
+    if (overlap(Rows(y, ntok, m, ldy, ydtype), Rows(x, ntok, n, ldx, xdtype)))
+      return fail(PWQ_ERR_INVALID_ARG, "y must not overlap x");
   }
   pwq_status s = check_ws(
       ws, ws_bytes, pwq_packed_linear_workspace_size(x, xdtype, ntok, ldx, m, n, group, n_out));
