@@ -497,24 +497,28 @@ def ssqr_quant_layer(W: torch.Tensor, X: Optional[torch.Tensor] = None,
 _DTYPES = {torch.float32: _lib.PWQ_F32, torch.bfloat16: _lib.PWQ_BF16, torch.int8: _lib.PWQ_I8}
 
 
-def _raw_stream(t: torch.Tensor):
-    return torch._C._cuda_getCurrentRawStream(t.device.index)
-
-
-def _rows(t: torch.Tensor, name: str) -> int:
-    """Row stride of a 2-D GPU tensor with unit column stride."""
-    if not t.is_cuda:
-        raise ValueError(f"{name} must be on the GPU")
+def _rows(t: torch.Tensor, name: str, device: int) -> int:
+    """Row stride of a 2-D tensor with unit column stride on this GPU."""
+    if t.get_device() != device:
+        raise ValueError(f"{name} must be on x's GPU")
     return _row_major(t)
 
 
-def _expect(t: torch.Tensor, name: str, shape: tuple, dtype: torch.dtype) -> int:
-    """Address of a contiguous GPU tensor of this shape and type."""
-    if t.shape != shape or t.dtype is not dtype or not t.is_cuda or not t.is_contiguous():
-        if not t.is_cuda:
-            raise ValueError(f"{name} must be on the GPU")
+def _expect(t: torch.Tensor, name: str, shape: tuple, dtype: torch.dtype, device: int) -> int:
+    """Address of a contiguous tensor of this shape and type on this GPU."""
+    if t.get_device() != device:
+        raise ValueError(f"{name} must be on x's GPU")
+    if t.shape != shape or t.dtype is not dtype or not t.is_contiguous():
         _check(t, name, shape, (dtype,))
     return t.data_ptr()
+
+
+def _device(x: torch.Tensor) -> int:
+    """Index of the GPU that x is on."""
+    device = x.get_device()
+    if device < 0:
+        raise ValueError("x must be on the GPU")
+    return device
 
 
 def pack_weights(codes: torch.Tensor, scales: torch.Tensor, grid: Grid,
@@ -524,8 +528,15 @@ def pack_weights(codes: torch.Tensor, scales: torch.Tensor, grid: Grid,
     layer that packed_linear reads: dict(qweight, scales, zeros, n, group,
     outlier_off, outliers).  Codes outside 4 bits go into the overflow list,
     so nothing is clipped.  Raises ValueError where a lattice step exceeds
-    127.  Synchronous (the list's length is read on the host)."""
+    127.  Synchronous (the list's length is read on the host); runs on codes'
+    GPU, on its current stream."""
     _require_cuda(codes, scales, zeros)
+    index = codes.get_device()
+    if any(t is not None and t.get_device() != index for t in (scales, zeros)):
+        raise ValueError("scales and zeros must be on codes' GPU")
+    if index != torch._C._cuda_getDevice():
+        with torch.cuda.device(index):
+            return pack_weights(codes, scales, grid, zeros)
     if codes.dtype != torch.int32:
         raise TypeError("codes must be int32")
     m, n = codes.shape
@@ -571,12 +582,17 @@ def rms_norm(x: torch.Tensor, weight: torch.Tensor, residual: Optional[torch.Ten
     token: (y, scales or None, sum or None).  ``out_dtype`` is bf16, fp32
     (default: x's) or int8, which comes with a step per token (scales [tokens]
     fp32, y = codes).  ``sum`` is x + residual in x's type, written to
-    ``sum_out`` where given (x or residual itself for in place)."""
-    ldx = _rows(x, "x")
+    ``sum_out`` where given (x or residual itself for in place).  Runs on x's
+    GPU, on its current stream."""
+    dev = _device(x)
+    if dev != torch._C._cuda_getDevice():
+        with torch.cuda.device(dev):
+            return rms_norm(x, weight, residual, eps, out_dtype, sum_out)
+    ldx = _rows(x, "x", dev)
     ntok, n = x.shape
     xdt = _dtype_code(x)
     wdt = _dtype_code(weight)
-    wp = _expect(weight, "weight", (n,), weight.dtype)
+    wp = _expect(weight, "weight", (n,), weight.dtype, dev)
     odt = x.dtype if out_dtype is None else out_dtype
     ydt = _DTYPES.get(odt)
     if ydt is None:
@@ -585,12 +601,12 @@ def rms_norm(x: torch.Tensor, weight: torch.Tensor, residual: Optional[torch.Ten
     if residual is not None:
         if residual.shape != x.shape or residual.dtype is not x.dtype:
             raise ValueError("residual must have x's shape and type")
-        rp, ldr = residual.data_ptr(), _rows(residual, "residual")
+        rp, ldr = residual.data_ptr(), _rows(residual, "residual", dev)
         if total is None:
             total = torch.empty_like(x, memory_format=torch.contiguous_format)
         elif total.shape != x.shape or total.dtype is not x.dtype:
             raise ValueError("sum_out must have x's shape and type")
-        tp, lds = total.data_ptr(), _rows(total, "sum_out")
+        tp, lds = total.data_ptr(), _rows(total, "sum_out", dev)
     elif sum_out is not None:
         raise ValueError("sum_out goes with a residual")
     y = torch.empty_like(x, dtype=odt, memory_format=torch.contiguous_format)
@@ -599,7 +615,7 @@ def rms_norm(x: torch.Tensor, weight: torch.Tensor, residual: Optional[torch.Ten
         scales = x.new_empty(ntok, dtype=torch.float32)
         sp = scales.data_ptr()
     status = lib().pwq_rms_norm(x.data_ptr(), xdt, ntok, n, ldx, rp, ldr, wp, wdt, eps, tp, lds,
-                                y.data_ptr(), ydt, n, sp, _raw_stream(x))
+                                y.data_ptr(), ydt, n, sp, torch._C._cuda_getCurrentRawStream(dev))
     if status:
         check(status)
     return y, scales, total
@@ -611,10 +627,15 @@ def packed_linear(x: torch.Tensor, packed: dict, x_scales: Optional[torch.Tensor
     """y [tokens, m] = x [tokens, n] times a packed layer (pack_weights).  x is
     bf16, fp32, or int8 with a step per token (``x_scales`` [tokens] fp32, as
     from rms_norm).  ``out_dtype`` is bf16 or fp32 (default: x's; bf16 for
-    int8); ``out`` may pass the result's memory."""
+    int8); ``out`` may pass the result's memory.  Runs on x's GPU, on its
+    current stream."""
+    dev = _device(x)
+    if dev != torch._C._cuda_getDevice():
+        with torch.cuda.device(dev):
+            return packed_linear(x, packed, x_scales, out_dtype, out)
     q, zeros, outliers = packed["qweight"], packed["zeros"], packed["outliers"]
     n, group = packed["n"], packed["group"]
-    ldx = _rows(x, "x")
+    ldx = _rows(x, "x", dev)
     ntok, cols = x.shape
     m = q.shape[0]
     if cols != n:
@@ -624,19 +645,19 @@ def packed_linear(x: torch.Tensor, packed: dict, x_scales: Optional[torch.Tensor
         raise TypeError(f"unsupported dtype {x.dtype}")
     if group <= 0 or n % group:
         raise ValueError(f"group {group} does not divide n = {n}")
-    qp = _expect(q, "qweight", (m, (n + 31) // 32 * 16), torch.uint8)
-    sp = _expect(packed["scales"], "scales", (m, n // group), torch.float32)
+    qp = _expect(q, "qweight", (m, (n + 31) // 32 * 16), torch.uint8, dev)
+    sp = _expect(packed["scales"], "scales", (m, n // group), torch.float32, dev)
     zp = offp = outp = xsp = None
     n_out = 0
     if zeros is not None:
-        zp = _expect(zeros, "zeros", (m, n // group), torch.uint8)
+        zp = _expect(zeros, "zeros", (m, n // group), torch.uint8, dev)
     if outliers is not None:
         n_out = outliers.shape[0]
-        outp = _expect(outliers, "outliers", (n_out,), torch.int32)
+        outp = _expect(outliers, "outliers", (n_out,), torch.int32, dev)
         offp = _expect(packed["outlier_off"], "outlier_off",
-                       ((m + 15) // 16 * ((n + 127) // 128) + 1,), torch.int32)
+                       ((m + 15) // 16 * ((n + 127) // 128) + 1,), torch.int32, dev)
     if x_scales is not None:
-        xsp = _expect(x_scales, "x_scales", (ntok,), torch.float32)
+        xsp = _expect(x_scales, "x_scales", (ntok,), torch.float32, dev)
     if (xdt == _lib.PWQ_I8) != (x_scales is not None):
         raise ValueError("x_scales goes with int8 x, and only with it")
     odt = out_dtype
@@ -650,13 +671,13 @@ def packed_linear(x: torch.Tensor, packed: dict, x_scales: Optional[torch.Tensor
     else:
         if out.shape != (ntok, m) or out.dtype is not odt:
             raise ValueError(f"out must be [{ntok}, {m}] {odt}")
-        ldy = _rows(out, "out") if ntok and m else m
-    L_ = lib()
+        ldy = _rows(out, "out", dev) if ntok and m else m
+    L_, stream = lib(), torch._C._cuda_getCurrentRawStream(dev)
     ws, nb = None, 0
     while True:
         status = L_.pwq_packed_linear(x.data_ptr(), xdt, ntok, ldx, xsp, qp, m, n, sp, zp, group,
                                       offp, outp, n_out, out.data_ptr(), _DTYPES[odt], ldy,
-                                      None if ws is None else ws.data_ptr(), nb, _raw_stream(x))
+                                      None if ws is None else ws.data_ptr(), nb, stream)
         if status != _lib.PWQ_ERR_WORKSPACE or ws is not None:
             break
         ws = _workspace(L_.pwq_packed_linear_workspace_size(x.data_ptr(), xdt, ntok, ldx, m, n,

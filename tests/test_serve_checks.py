@@ -1,7 +1,10 @@
 """What rms_norm and packed_linear refuse and accept, without a device: calls
-either fail validation or get as far as a workspace that is not there."""
+either fail validation, or get as far as a workspace that is not there, or reach
+a library that only records them."""
 import pytest
+import torch
 
+import post_weight_quantization_19_amd as P
 from post_weight_quantization_19_amd import _lib as B
 
 FAKE = 0x100000          # never dereferenced
@@ -52,3 +55,103 @@ def test_rms_norm_outputs_over_each_other():
             assert norm(total=other + shift) == INVALID, (hex(other), shift)
     assert norm(total=FAKE, lds=128) == INVALID
     assert norm(y=FAKE + 100, ldx=128, ldy=128) == INVALID
+
+
+# ------------------------------------------------------------------ several GPUs
+
+class OnGpu0(torch.Tensor):
+    """A tensor that says it is on a GPU (its memory is the host's: the library
+    is replaced)."""
+    index = 0
+
+    def get_device(self):
+        return self.index
+
+    is_cuda = property(lambda self: True)
+
+
+class OnGpu1(OnGpu0):
+    index = 1
+
+
+@pytest.fixture
+def gpus(monkeypatch):
+    """Calls of the library as (name, current GPU, stream); GPU 0 is current."""
+    state = {"current": 0, "calls": []}
+
+    class Device:
+        def __init__(self, index):
+            self.index = index
+
+        def __enter__(self):
+            self.before, state["current"] = state["current"], self.index
+
+        def __exit__(self, *error):
+            state["current"] = self.before
+
+    class Library:
+        def __getattr__(self, name):
+            def call(*args):
+                state["calls"].append((name, state["current"], args[-1]))
+                return 0
+            return call
+
+    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: state["current"], raising=False)
+    monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda index: 1000 + (index or 0),
+                        raising=False)
+    monkeypatch.setattr(torch.cuda, "device", Device)
+    monkeypatch.setattr(P, "lib", Library)
+    return state
+
+
+def of(gpu, *shape, dtype=torch.float32):
+    return torch.zeros(shape, dtype=dtype).as_subclass(gpu)
+
+
+def layer_on(gpu, m=32, n=64):
+    return {"qweight": of(gpu, m, n // 2, dtype=torch.uint8), "scales": of(gpu, m, 2),
+            "zeros": of(gpu, m, 2, dtype=torch.uint8), "n": n, "group": 32,
+            "outlier_off": of(gpu, 3, dtype=torch.int32),
+            "outliers": of(gpu, 5, dtype=torch.int32)}
+
+
+@pytest.mark.parametrize("gpu", [OnGpu0, OnGpu1])
+def test_calls_run_on_the_gpu_of_their_input(gpus, gpu):
+    P.rms_norm(of(gpu, 3, 64), of(gpu, 64), of(gpu, 3, 64), out_dtype=torch.int8)
+    P.packed_linear(of(gpu, 3, 64), layer_on(gpu))
+    assert gpus["calls"] == [("pwq_rms_norm", gpu.index, 1000 + gpu.index),
+                             ("pwq_packed_linear", gpu.index, 1000 + gpu.index)]
+    assert gpus["current"] == 0
+
+
+def test_tensors_of_another_gpu_are_refused(gpus):
+    a, b = OnGpu0, OnGpu1
+    x = of(a, 3, 64)
+    for args in ((of(b, 64),), (of(a, 64), of(b, 3, 64)),
+                 (of(a, 64), x, 1e-6, None, of(b, 3, 64))):
+        with pytest.raises(ValueError, match="GPU"):
+            P.rms_norm(x, *args)
+    packed = layer_on(a)
+    for name in ("qweight", "scales", "zeros", "outlier_off", "outliers"):
+        with pytest.raises(ValueError, match="GPU"):
+            P.packed_linear(x, dict(packed, **{name: layer_on(b)[name]}))
+    with pytest.raises(ValueError, match="GPU"):
+        P.packed_linear(x, packed, out=of(b, 3, 32))
+    with pytest.raises(ValueError, match="GPU"):
+        P.packed_linear(x.to(torch.int8).as_subclass(a), packed, x_scales=of(b, 3))
+    codes = of(a, 32, 64, dtype=torch.int32)
+    for scales, zeros in ((of(b, 32, 2), of(a, 32, 2, dtype=torch.int32)),
+                          (of(a, 32, 2), of(b, 32, 2, dtype=torch.int32))):
+        with pytest.raises(ValueError, match="GPU"):
+            P.pack_weights(codes, scales, P.Grid("asym", 4, 32), zeros)
+    assert gpus["calls"] == []
+
+
+def test_host_tensors_are_refused(gpus):
+    x = torch.zeros(3, 64)
+    with pytest.raises(ValueError, match="GPU"):
+        P.rms_norm(x, torch.ones(64))
+    with pytest.raises(ValueError, match="GPU"):
+        P.rms_norm(of(OnGpu0, 3, 64), torch.ones(64))
+    with pytest.raises(ValueError, match="GPU"):
+        P.packed_linear(x, layer_on(OnGpu0))
