@@ -521,6 +521,14 @@ def _device(x: torch.Tensor) -> int:
     return device
 
 
+def _no_gradient(*ts):
+    if torch.is_grad_enabled():
+        for t in ts:
+            if t is not None and t.requires_grad:
+                raise ValueError("a tensor requires a gradient, which this call does not give: "
+                                 "call it under torch.no_grad(), or detach the tensor")
+
+
 def pack_weights(codes: torch.Tensor, scales: torch.Tensor, grid: Grid,
                  zeros: Optional[torch.Tensor] = None) -> dict:
     """Codes [m, n] int32, steps and zero points of a SYM / ASYM grid of at
@@ -583,8 +591,10 @@ def rms_norm(x: torch.Tensor, weight: torch.Tensor, residual: Optional[torch.Ten
     (default: x's) or int8, which comes with a step per token (scales [tokens]
     fp32, y = codes).  ``sum`` is x + residual in x's type, written to
     ``sum_out`` where given (x or residual itself for in place).  Runs on x's
-    GPU, on its current stream."""
+    GPU, on its current stream.  Gives no gradients, and refuses tensors that
+    require one unless they are off (torch.no_grad())."""
     dev = _device(x)
+    _no_gradient(x, weight, residual, sum_out)
     if dev != torch._C._cuda_getDevice():
         with torch.cuda.device(dev):
             return rms_norm(x, weight, residual, eps, out_dtype, sum_out)
@@ -628,8 +638,10 @@ def packed_linear(x: torch.Tensor, packed: dict, x_scales: Optional[torch.Tensor
     bf16, fp32, or int8 with a step per token (``x_scales`` [tokens] fp32, as
     from rms_norm).  ``out_dtype`` is bf16 or fp32 (default: x's; bf16 for
     int8); ``out`` may pass the result's memory.  Runs on x's GPU, on its
-    current stream."""
+    current stream.  Gives no gradients, and refuses tensors that require one
+    unless they are off (torch.no_grad())."""
     dev = _device(x)
+    _no_gradient(x, x_scales, packed["scales"], out)
     if dev != torch._C._cuda_getDevice():
         with torch.cuda.device(dev):
             return packed_linear(x, packed, x_scales, out_dtype, out)

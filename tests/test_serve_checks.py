@@ -155,3 +155,34 @@ def test_host_tensors_are_refused(gpus):
         P.rms_norm(of(OnGpu0, 3, 64), torch.ones(64))
     with pytest.raises(ValueError, match="GPU"):
         P.packed_linear(x, layer_on(OnGpu0))
+
+
+# ------------------------------------------------------------------ gradients
+
+@pytest.mark.parametrize("which", range(4))
+def test_tensors_that_require_a_gradient(gpus, which):
+    """Refused while gradients are recorded: they would be lost in silence."""
+    def tensors(*shapes):
+        ts = [of(OnGpu0, *s) for s in shapes]
+        ts[which].requires_grad_()
+        return ts
+
+    def norm():
+        x, weight, residual, total = tensors((3, 64), (64,), (3, 64), (3, 64))
+        P.rms_norm(x, weight, residual, sum_out=total)
+
+    def linear():
+        x, out, scales, steps = tensors((3, 64), (3, 32), (32, 2), (3,))
+        if which == 3:
+            x = x.to(torch.int8).as_subclass(OnGpu0)
+        P.packed_linear(x, dict(layer_on(OnGpu0), scales=scales), out=out,
+                        x_scales=steps if which == 3 else None)
+
+    for call in (norm, linear):
+        with pytest.raises(ValueError, match="gradient"):
+            call()
+    assert gpus["calls"] == []
+    with torch.no_grad():
+        norm()
+        linear()
+    assert len(gpus["calls"]) == 2
