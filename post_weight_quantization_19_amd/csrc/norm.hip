@@ -238,10 +238,11 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void rms_norm_regs(const Rms
 // One workgroup per token, three passes over its row.
 template <typename T>
 __global__ __launch_bounds__(256) void rms_norm_rows(
-    const void* x, int64_t n, int64_t ldx, const void* residual, int64_t ldr, const void* weight,
+    const void* x, int64_t ntok, int64_t n, int64_t ldx, const void* residual, int64_t ldr, const void* weight,
     int wf32, float eps, void* sum, int64_t lds, void* y, int ydtype, int64_t ldy, float* scales) {
   __shared__ float red[4];
-  const int64_t t = blockIdx.x;
+  const int64_t t = block_index();
+  if (t >= ntok) return;
   auto h_at = [&](int64_t k) {
     float h = load1<T>(x, t * ldx + k);
     if (residual) h += load1<T>(residual, t * ldr + k);
@@ -294,8 +295,8 @@ void launch_regs(const RmsNormLaunch& a, hipStream_t st) {
 
 template <typename T>
 void launch_loop(const RmsNormLaunch& a, hipStream_t st) {
-  rms_norm_rows<T><<<dim3((unsigned)a.ntok), 256, 0, st>>>(
-      a.x, a.n, a.ldx, a.residual, a.ldr, a.weight, a.wdtype == PWQ_F32, a.eps, a.sum, a.lds, a.y,
+  rms_norm_rows<T><<<block_grid(a.ntok), 256, 0, st>>>(
+      a.x, a.ntok, a.n, a.ldx, a.residual, a.ldr, a.weight, a.wdtype == PWQ_F32, a.eps, a.sum, a.lds, a.y,
       a.ydtype, a.ldy, a.scales);
 }
 

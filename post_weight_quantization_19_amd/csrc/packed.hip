@@ -18,10 +18,11 @@ __global__ __launch_bounds__(64) void pack_tiles(const int32_t* __restrict__ cod
                                                  int64_t n, int64_t ldc, int asym,
                                                  const int32_t* __restrict__ zeros, int G,
                                                  int64_t ng, uint8_t* __restrict__ qweight,
-                                                 int64_t ldq, int64_t across,
+                                                 int64_t ldq, int64_t across, int64_t tiles,
                                                  int32_t* __restrict__ counts,
                                                  int32_t* __restrict__ info) {
-  const int64_t tile = blockIdx.x;
+  const int64_t tile = block_index();
+  if (tile >= tiles) return;
   const int64_t r0 = tile / across * kPackRows, c0 = tile % across * kPackCols;
   const int lane = threadIdx.x;
   int over = 0, bad = 0;
@@ -58,7 +59,7 @@ __global__ __launch_bounds__(64) void pack_tiles(const int32_t* __restrict__ cod
 __global__ __launch_bounds__(256) void pack_zeros(const int32_t* __restrict__ zeros, int64_t count,
                                                   uint8_t* __restrict__ zeros8,
                                                   int32_t* __restrict__ info) {
-  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  const int64_t i = block_index() * 256 + threadIdx.x;
   bool bad = false;
   if (i < count) {
     const int z = zeros[i];
@@ -102,11 +103,12 @@ __global__ __launch_bounds__(1024) void pack_scan(int32_t* __restrict__ off, int
 
 __global__ __launch_bounds__(64) void pack_entries(const int32_t* __restrict__ codes, int64_t m,
                                                    int64_t n, int64_t ldc, int asym,
-                                                   int64_t across,
+                                                   int64_t across, int64_t tiles,
                                                    const int32_t* __restrict__ off,
                                                    int32_t* __restrict__ outliers,
                                                    int64_t max_out) {
-  const int64_t tile = blockIdx.x;
+  const int64_t tile = block_index();
+  if (tile >= tiles) return;
   int64_t e = off[tile];
   if (off[tile + 1] == e) return;
   const int64_t r0 = tile / across * kPackRows, c0 = tile % across * kPackCols;
@@ -146,14 +148,14 @@ constexpr int TT = 4;
 template <typename T>
 __global__ __launch_bounds__(256) void linear_any(const PackedLinearLaunch a) {
   const int lane = threadIdx.x & 63;
-  const int64_t r = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
+  const int64_t r = block_index() * 4 + (threadIdx.x >> 6);
   if (r >= a.m) return;
   const int64_t ng = a.n / a.G;
   const float* s = a.scales + r * ng;
   const uint8_t* z = a.zeros ? a.zeros + r * ng : nullptr;
   const uint8_t* q = a.qweight + r * a.ldq;
   const int64_t across = (a.n + kPackCols - 1) / kPackCols;
-  for (int64_t t0 = (int64_t)blockIdx.y * TT; t0 < a.ntok; t0 += (int64_t)gridDim.y * TT) {
+  for (int64_t t0 = (int64_t)blockIdx.z * TT; t0 < a.ntok; t0 += (int64_t)gridDim.z * TT) {
     float acc[TT] = {0.0f, 0.0f, 0.0f, 0.0f};
     auto add = [&](int64_t k, float step) {
       const float sk = s[k / a.G];
@@ -203,13 +205,11 @@ hipError_t launch_pack_codes(const int32_t* codes, int64_t m, int64_t n, int64_t
   const int64_t tiles = (m + kPackRows - 1) / kPackRows * across;
   clear_info<<<1, 2, 0, st>>>(info);
   if (tiles > 0)
-    pack_tiles<<<dim3((unsigned)tiles), 64, 0, st>>>(codes, m, n, ldc, asym, zeros, G, ng,
-                                                     qweight, packed_row_bytes(n), across, off,
-                                                     info);
+    pack_tiles<<<block_grid(tiles), 64, 0, st>>>(codes, m, n, ldc, asym, zeros, G, ng, qweight,
+                                                 packed_row_bytes(n), across, tiles, off, info);
   pack_scan<<<1, 1024, 0, st>>>(off, tiles, info);
   if (asym && m > 0)
-    pack_zeros<<<dim3((unsigned)((m * ng + 255) / 256)), 256, 0, st>>>(zeros, m * ng, zeros8,
-                                                                       info);
+    pack_zeros<<<block_grid((m * ng + 255) / 256), 256, 0, st>>>(zeros, m * ng, zeros8, info);
   return hipGetLastError();
 }
 
@@ -219,15 +219,15 @@ hipError_t launch_pack_overflow(const int32_t* codes, int64_t m, int64_t n, int6
   const int64_t across = (n + kPackCols - 1) / kPackCols;
   const int64_t tiles = (m + kPackRows - 1) / kPackRows * across;
   if (tiles == 0) return hipSuccess;
-  pack_entries<<<dim3((unsigned)tiles), 64, 0, st>>>(codes, m, n, ldc, asym, across, off, outliers,
-                                                     max_out);
+  pack_entries<<<block_grid(tiles), 64, 0, st>>>(codes, m, n, ldc, asym, across, tiles, off,
+                                                 outliers, max_out);
   return hipGetLastError();
 }
 
 hipError_t launch_linear_any(const PackedLinearLaunch& a, hipStream_t st) {
   if (a.ntok == 0 || a.m == 0) return hipSuccess;
-  const dim3 grid((unsigned)((a.m + 3) / 4), (unsigned)std::min<int64_t>((a.ntok + TT - 1) / TT,
-                                                                         65535));
+  dim3 grid = block_grid((a.m + 3) / 4);
+  grid.z = (unsigned)std::min<int64_t>((a.ntok + TT - 1) / TT, 65535);
   if (a.xdtype == PWQ_F32) linear_any<float><<<grid, 256, 0, st>>>(a);
   else if (a.xdtype == PWQ_BF16) linear_any<uint16_t><<<grid, 256, 0, st>>>(a);
   else linear_any<int8_t><<<grid, 256, 0, st>>>(a);

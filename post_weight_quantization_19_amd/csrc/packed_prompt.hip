@@ -147,7 +147,7 @@ __global__ __launch_bounds__(256) void spread_weights(
   __shared__ __attribute__((aligned(16))) char smem[4][16 * ROW];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int64_t tile = (int64_t)blockIdx.x * 4 + wave;
+  const int64_t tile = block_index() * 4 + wave;
   if (tile >= tiles) return;
   char* const L = smem[wave];
   const int64_t strip = tile / across;
@@ -743,8 +743,8 @@ __global__ __launch_bounds__(256) void prompt_join(const float* __restrict__ par
                                                    int64_t ntok, int64_t m,
                                                    const float* __restrict__ x_scales, void* y,
                                                    int ydtype, int64_t ldy) {
-  const int64_t t = blockIdx.x, r = (int64_t)blockIdx.y * 1024 + 4 * threadIdx.x;
-  if (r >= m) return;
+  const int64_t t = block_index(), r = (int64_t)blockIdx.z * 1024 + 4 * threadIdx.x;
+  if (t >= ntok || r >= m) return;
   const int count = (int)min(m - r, (int64_t)4);
   auto load = [&](int s) {
     const float* p = partial + ((int64_t)s * ntok + t) * m + r;
@@ -774,7 +774,7 @@ template <typename T, bool KEEP8>
 __global__ __launch_bounds__(256) void stage_x(const T* __restrict__ x, int64_t ntok, int64_t n,
                                                int64_t ldx, char* __restrict__ out,
                                                int64_t units) {
-  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;   // 8 columns each
+  const int64_t i = block_index() * 256 + threadIdx.x;         // 8 columns each
   if (i >= ntok * units) return;
   const int64_t t = i / units, u = i % units, k0 = 8 * u;
   T v[8];
@@ -850,8 +850,10 @@ PromptPlan prompt_plan(const void* x, int32_t xdtype, int64_t ntok, int64_t ldx,
                        int64_t n, int32_t G, int64_t n_out) {
   PromptPlan p{};
   const bool row = G == n;
-  // (128 rows of x within 32-bit offsets, three parts each)
-  p.ok = (row || G % 32 == 0) && ntok > 0 && m > 0 && n < (1 << 21);
+  // (128 rows of x within 32-bit offsets, three parts each; what is joined
+  // within the extents of a launch)
+  p.ok = (row || G % 32 == 0) && ntok > 0 && m > 0 && n < (1 << 21) && ntok < (1 << 26) &&
+         m < (1 << 26);
   if (!p.ok) return p;
   // 8-bit operands: a group's sum is an int32, of at most 128 columns unless
   // the whole row is one group (2^17 products of 128 x 127 fit)
@@ -935,6 +937,8 @@ PromptPlan prompt_plan(const void* x, int32_t xdtype, int64_t ntok, int64_t ldx,
       }
     }
   }
+  // tiles of 512 threads within the x extent of a launch
+  if (p.tiles_t * p.tiles_r >= (1 << 22)) return PromptPlan{};
   // with the spreading: a launch and its bytes at 5 TB/s
   p.us = best + (p.fused ? 0.0 : 3.0 + (double)m * n * (p.i8 ? 1.5 : 2.5) / 5e6);
   p.rows16 = (m + 15) / 16 * 16;
@@ -960,7 +964,7 @@ hipError_t launch_prompt(const PackedLinearLaunch& a, const PromptPlan& pl, cons
     p.xrow = xrow;
   } else {
     const int64_t units = pl.staged_row / pl.reps / (pl.i8 ? 8 : 16);
-    const dim3 grid((unsigned)((a.ntok * units + 255) / 256));
+    const dim3 grid = block_grid((a.ntok * units + 255) / 256);
     char* o = (char*)w.staged;
     if (a.xdtype == PWQ_I8 && pl.i8)
       stage_x<int8_t, true><<<grid, 256, 0, st>>>((const int8_t*)a.x, a.ntok, a.n, a.ldx, o, units);
@@ -1007,7 +1011,7 @@ hipError_t launch_prompt(const PackedLinearLaunch& a, const PromptPlan& pl, cons
   if (!pl.fused) {
     const int across = (int)((a.n + 127) / 128);
     const int64_t tiles = pl.rows16 / 16 * across;
-    const dim3 grid((unsigned)((tiles + 3) / 4));
+    const dim3 grid = block_grid((tiles + 3) / 4);
     if (pl.i8)
       spread_weights<true><<<grid, 256, 0, st>>>(
           a.qweight, a.ldq, a.scales, a.zeros, a.outlier_off, a.outliers, p.n_out, a.m, (int)a.n,
@@ -1030,10 +1034,12 @@ hipError_t launch_prompt(const PackedLinearLaunch& a, const PromptPlan& pl, cons
     if (pl.i8) launch_tiles<true, 128, 128, 4>(p, mode, k, st);
     else launch_tiles<false, 128, 128, 4>(p, mode, k, st);
   }
-  if (p.partial)
-    (a.m % 4 == 0 ? prompt_join<true> : prompt_join<false>)
-        <<<dim3((unsigned)a.ntok, (unsigned)((a.m + 1023) / 1024)), 256, 0, st>>>(
-            p.partial, (int)pl.splits, a.ntok, a.m, a.x_scales, a.y, a.ydtype, a.ldy);
+  if (p.partial) {
+    dim3 grid = block_grid(a.ntok);
+    grid.z = (unsigned)((a.m + 1023) / 1024);
+    (a.m % 4 == 0 ? prompt_join<true> : prompt_join<false>)<<<grid, 256, 0, st>>>(
+        p.partial, (int)pl.splits, a.ntok, a.m, a.x_scales, a.y, a.ydtype, a.ldy);
+  }
   return hipGetLastError();
 }
 

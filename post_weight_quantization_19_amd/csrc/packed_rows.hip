@@ -452,10 +452,10 @@ void launch_x(const PackedLinearLaunch& a, int gb, hipStream_t st) {
 
 }  // namespace
 
-// Up to 16 tokens, steps per 32 columns or more (or per row), offsets within
-// 32 bits.
-bool rows_ok(int64_t ntok, int64_t n, int32_t G) {
-  return ntok <= kRowsTokens && (G == n || G % 32 == 0) && n < (1 << 24);
+// Up to 16 tokens, steps per 32 columns or more (or per row), offsets and the
+// launch's 4 m threads within 32 bits.
+bool rows_ok(int64_t ntok, int64_t m, int64_t n, int32_t G) {
+  return ntok <= kRowsTokens && (G == n || G % 32 == 0) && n < (1 << 24) && m < (1 << 29);
 }
 
 // Bytes of the padded copy of x; 0 where its rows can be copied in 16-byte

@@ -975,7 +975,7 @@ static LinearPlan linear_plan(const void* x, int32_t xdtype, int64_t ntok, int64
                               int64_t n, int32_t G, int64_t n_out) {
   LinearPlan p;
   if (ntok == 0 || m == 0) return p;
-  p.rows = rows_ok(ntok, n, G);
+  p.rows = rows_ok(ntok, m, n, G);
   if (p.rows) {
     p.staged = rows_staged_bytes(x, xdtype, ntok, n, ldx);
     p.us = 0.5 * (double)m * n / 2.7e6;      // the weights at 2.7 TB/s

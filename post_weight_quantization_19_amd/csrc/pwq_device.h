@@ -155,6 +155,12 @@ PWQ_COPY(copy4, "global_load_lds_dword")
 PWQ_COPY(copy1, "global_load_lds_ubyte")
 #undef PWQ_COPY
 
+// Index of a workgroup in a launch of block_grid workgroups.
+constexpr int kGridShift = 21;
+__device__ __forceinline__ int64_t block_index() {
+  return (int64_t)blockIdx.y << kGridShift | blockIdx.x;
+}
+
 // Eight 4-bit steps of a dword to bytes: w has the codes 0 .. 15, z4 the zero
 // point in every byte (z <= 127: no borrow passes a byte, as every byte is at
 // least 128 before the subtraction).

@@ -154,6 +154,15 @@ hipError_t launch_column_entropy(const int32_t* codes, int64_t m, int64_t n, int
                                  double* bits, double* mean, int64_t* huff, int32_t* cmin,
                                  int32_t* cmax, hipStream_t st);
 
+// A launch of many workgroups (block_index).  Its x extent is counted in
+// threads, in 32 bits, and what is over is dropped without an error: 2^24
+// workgroups of 256 threads run none.  Past 2^21 workgroups they go on in y, and
+// the last row of them may be past their number.
+inline dim3 block_grid(int64_t blocks) {
+  const int64_t x = blocks < (int64_t(1) << kGridShift) ? blocks : int64_t(1) << kGridShift;
+  return dim3((unsigned)x, (unsigned)((blocks + x - 1) / x));
+}
+
 // Root-mean-square norm (pwq_rms_norm).
 struct RmsNormLaunch {
   const void* x;
@@ -208,7 +217,7 @@ hipError_t launch_linear_any(const PackedLinearLaunch& a, hipStream_t st);
 // Few tokens, each weight read once; staged: rows_staged_bytes of workspace,
 // NULL where that is 0.
 constexpr int64_t kRowsTokens = 16;
-bool rows_ok(int64_t ntok, int64_t n, int32_t G);
+bool rows_ok(int64_t ntok, int64_t m, int64_t n, int32_t G);
 size_t rows_staged_bytes(const void* x, int32_t xdtype, int64_t ntok, int64_t n, int64_t ldx);
 hipError_t launch_rows(PackedLinearLaunch a, void* staged, hipStream_t st);
 // Many tokens: what the product is made of, and its workspace.

@@ -12,6 +12,7 @@ import numpy as np
 import pytest
 import torch
 
+import oracle.serve_oracle as S
 import post_weight_quantization_19_amd as P
 from test_gpu_serve import DT, HALF_BF16, U, activations, f64, hidden, packed_layer
 
@@ -212,3 +213,38 @@ def test_small_steps_next_to_large_x(tokens, x_kind):
         y = P.packed_linear(x.cuda(), pk, x_scales=None if xs is None else xs.cuda(),
                             out_dtype=torch.float32)
         check(y, x, xs, codes, scales, zeros)
+
+
+def test_norm_of_sixteen_million_tokens():
+    """More workgroups than a launch takes, of the kernel for short rows."""
+    tokens, n = 2 ** 24 + 5, 4
+    gen = torch.Generator(device="cuda").manual_seed(4)
+    x = torch.randn((tokens, n), generator=gen, device="cuda")
+    w = torch.tensor([0.5, 1.0, 2.0, -1.0], device="cuda")
+    print("[ranges] 2^24 tokens", flush=True)
+    y, _, _ = P.rms_norm(x, w)
+    q, step, _ = P.rms_norm(x, w, out_dtype=torch.int8)
+    rel = 16 * U                                       # a sum of 4 squares, root, 3 roundings
+    for part in (slice(0, 1000), slice(2 ** 24 - 500, None)):
+        want, s, _, _ = S.rms_norm(f64(x[part]), f64(w), None, 1e-6, True)
+        assert np.all(np.abs(f64(y[part]) - want) <= rel * np.abs(want))
+        assert np.all(np.abs(f64(step[part]) - s) <= rel * s)
+        assert np.all(np.abs(f64(q[part]) - want / s[:, None]) <= 0.5 + 254 * rel)
+    assert torch.isfinite(y).all() and int((step <= 0).sum()) == 0
+
+
+def test_product_of_sixty_million_rows():
+    """More workgroups than a launch takes, of the kernel for groups that are
+    no multiple of 32 columns."""
+    m, n, group = 2 ** 26 + 9, 6, 3
+    gen = torch.Generator(device="cuda").manual_seed(5)
+    q = torch.randint(0, 256, (m, 16), generator=gen, device="cuda", dtype=torch.uint8)
+    scales = torch.rand((m, 2), generator=gen, device="cuda")
+    x = torch.randn((2, n), generator=gen, device="cuda")
+    print("[ranges] 2^26 rows", flush=True)
+    y = P.packed_linear(x, {"qweight": q, "scales": scales, "zeros": None, "n": n, "group": group,
+                            "outlier_off": None, "outliers": None})
+    for part in (slice(0, 1000), slice(2 ** 26 - 500, None)):
+        codes = S.unpack(q[part].cpu().numpy(), n, False)
+        check(y[:, part], x, None, codes, f64(scales[part]), None)
+    assert torch.isfinite(y).all()
