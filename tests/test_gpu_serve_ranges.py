@@ -14,7 +14,8 @@ import torch
 
 import oracle.serve_oracle as S
 import post_weight_quantization_19_amd as P
-from test_gpu_serve import DT, HALF_BF16, U, activations, f64, hidden, packed_layer
+from test_gpu_serve import (DT, HALF_BF16, U, activations, f64, hidden, layer,
+                            packed_layer)
 
 pytestmark = pytest.mark.gpu
 
@@ -248,3 +249,139 @@ def test_product_of_sixty_million_rows():
         codes = S.unpack(q[part].cpu().numpy(), n, False)
         check(y[:, part], x, None, codes, f64(scales[part]), None)
     assert torch.isfinite(y).all()
+
+
+# ------------------------------------------------------------------ kernels by their sizes
+
+NORM_WALKS = [(1700, 4097), (1600, 8200), (900, 14336), (6200, 2047), (6200, 300), (600, 20001)]
+
+
+def norm_tolerance(n):
+    """Of a value: the sum of squares (halved by the root) and 8 roundings."""
+    return (0.5 * (n / 64 + 32) + 8) * U
+
+
+@pytest.mark.parametrize("x_kind", ["bf16", "f32"])
+@pytest.mark.parametrize("tokens,n", NORM_WALKS)
+def test_norm_walks_over_tokens(tokens, n, x_kind):
+    """More tokens than workgroups: each kernel for many tokens, every token
+    against 64 bits, in every output type, with a residual and without."""
+    gen = torch.Generator(device="cuda").manual_seed(n)
+    x = torch.randn((tokens, n), generator=gen, device="cuda").to(DT[x_kind])
+    res = (2 * torch.randn((tokens, n), generator=gen, device="cuda")).to(DT[x_kind])
+    w = 1 + 0.1 * torch.randn(n, generator=gen, device="cuda")
+    rel = norm_tolerance(n)
+    for residual in (None, res):
+        h = x.double() if residual is None else x.double() + residual.double()
+        want = h / (h.square().mean(1, keepdim=True) + 1e-6).sqrt() * w.double()
+        for out in ("int8", "bf16", "f32"):
+            print(f"[ranges] walk {tokens} {n} {x_kind} {residual is not None} {out}", flush=True)
+            y, step, total = P.rms_norm(x, w, residual, out_dtype=DT[out])
+            if residual is not None:
+                tol = h.abs() * (2 * U + (HALF_BF16 if x_kind == "bf16" else 0))
+                assert bool(((total.double() - h).abs() <= tol).all())
+            if out == "int8":
+                s = want.abs().amax(1) / 127
+                assert bool(((step.double() - s).abs() <= (rel + 2 * U) * s).all())
+                off = (y.double() - want / s[:, None]).abs()
+                assert float(off.max()) <= 0.5 + 127 * (2 * rel + 8 * U)
+            else:
+                tol = want.abs() * (rel + (HALF_BF16 if out == "bf16" else 0))
+                assert bool(((y.double() - want).abs() <= tol).all())
+
+
+@pytest.mark.parametrize("tokens,n", NORM_WALKS)
+def test_norm_walks_in_place(tokens, n):
+    """The sum on x's or the residual's memory, in rows of a wider tensor, and
+    tokens of NaN and infinity: the other tokens as without any of it."""
+    gen = torch.Generator(device="cuda").manual_seed(n + 1)
+    x = torch.randn((tokens, n), generator=gen, device="cuda").bfloat16()
+    res = torch.randn((tokens, n), generator=gen, device="cuda").bfloat16()
+    w = torch.rand(n, generator=gen, device="cuda")
+    y0, s0, t0 = P.rms_norm(x, w, res, out_dtype=torch.int8)
+    for shift, pad in ((0, 8), (3, 5)):
+        for place in ("x", "residual"):
+            print(f"[ranges] in place {tokens} {n} {shift} {place}", flush=True)
+            wide = torch.full((tokens, n + pad), 7.0, device="cuda", dtype=torch.bfloat16)
+            view = wide[:, shift:shift + n]
+            view.copy_(x if place == "x" else res)
+            args = (view, w, res) if place == "x" else (x, w, view)
+            y, s, t = P.rms_norm(*args, out_dtype=torch.int8, sum_out=view)
+            assert torch.equal(y, y0) and torch.equal(s, s0) and torch.equal(view, t0)
+            assert bool((wide[:, :shift] == 7).all()) and bool((wide[:, shift + n:] == 7).all())
+    bad = torch.tensor([0, tokens // 3, tokens // 2, tokens - 1], device="cuda")
+    x[bad, n - 1] = torch.tensor([float("nan"), float("inf"), float("-inf"), float("nan")],
+                                 device="cuda").bfloat16()
+    y, s, _ = P.rms_norm(x, w, res, out_dtype=torch.int8)
+    good = torch.ones(tokens, dtype=torch.bool, device="cuda")
+    good[bad] = False
+    assert torch.equal(y[good], y0[good]) and torch.equal(s[good], s0[good])
+    assert bool(torch.isnan(s[bad]).all()) and bool((y[bad] == 0).all())
+
+
+@pytest.mark.parametrize("x_kind", ["bf16", "f32", "int8"])
+@pytest.mark.parametrize("n,group", [(34560, 128), (34560, 192), (33792, 64), (10240, 32),
+                                     (34560, 0), (34470, 0)])
+def test_long_rows_for_few_tokens(n, group, x_kind):
+    """More tiles of columns to a wave than it stages the steps of at a time:
+    steps, zero points and overflow entries are staged again, in mid-group too."""
+    m = 33
+    for kind, density in (("sym", 0.02), ("asym", 0.02), ("sym", 0.6), ("asym", 0.0)):
+        rng = np.random.default_rng([n, group])
+        codes, scales, zeros = layer(rng, m, n, group, kind, density)
+        pk = packed_layer(codes, scales, zeros, group)
+        for tokens in (1, 6, 16):
+            print(f"[ranges] long rows {n} {group} {x_kind} {kind} {density} {tokens}", flush=True)
+            x, xs = activations(rng, tokens, n, x_kind)
+            y = P.packed_linear(x.cuda(), pk, x_scales=None if xs is None else xs.cuda(),
+                                out_dtype=torch.float32)
+            check(y, x, xs, codes, scales, zeros)
+
+
+def test_many_rows_and_long_rows_for_few_tokens():
+    """A layer of 8200 rows of 14336: several chunks of a wave in every strip."""
+    m, n, group = 8200, 14336, 64
+    rng = np.random.default_rng(14336)
+    codes, scales, zeros = layer(rng, m, n, group, "asym", 0.01)
+    pk = packed_layer(codes, scales, zeros, group)
+    rows = np.r_[0:40, 4000:4040, m - 40:m]
+    for x_kind in ("bf16", "int8", "f32"):
+        for tokens in (1, 16):
+            x, xs = activations(rng, tokens, n, x_kind)
+            y = P.packed_linear(x.cuda(), pk, x_scales=None if xs is None else xs.cuda(),
+                                out_dtype=torch.float32)
+            check(y[:, torch.from_numpy(rows).cuda()], x, xs, codes[rows], scales[rows],
+                  zeros[rows])
+
+
+@pytest.mark.parametrize("tokens", [1, 20, 200])
+@pytest.mark.parametrize("n,group", [(256, 128), (320, 64), (140032, 0)])
+def test_largest_integers_are_exact(n, group, tokens):
+    """8-bit x of -128 against steps of -127: partial sums are multiples of 128 x
+    127, and added by twos or more, at most 70016 of them, exact in 24 bits."""
+    m = 17
+    zeros = np.full((m, n // (group or n)), 127, np.int32)
+    pk = packed_layer(np.zeros((m, n), np.int32), np.full(zeros.shape, 0.5, np.float32), zeros,
+                      group)
+    x = torch.full((tokens, n), -128, dtype=torch.int8, device="cuda")
+    y = P.packed_linear(x, pk, x_scales=torch.ones(tokens, device="cuda"),
+                        out_dtype=torch.float32)
+    assert bool((y == 0.5 * 128 * 127 * n).all())
+
+
+@pytest.mark.parametrize("x_kind", ["bf16", "f32", "int8"])
+@pytest.mark.parametrize("tokens,m,n,group", [(1, 70, 4096, 128), (12, 70, 4096, 32),
+                                              (50, 200, 1408, 128), (200, 300, 2048, 64),
+                                              (700, 300, 2048, 0), (650, 700, 1152, 192),
+                                              (90, 40, 600, 20)])
+def test_error_follows_the_steps(tokens, m, n, group, x_kind):
+    """Every kernel within its roundings of |step| |x|."""
+    for kind, density in (("sym", 0.0), ("asym", 0.01)):
+        rng = np.random.default_rng([tokens, m, n])
+        codes, scales, zeros = layer(rng, m, n, group, kind, density)
+        pk = packed_layer(codes, scales, zeros, group)
+        x, xs = activations(rng, tokens, n, x_kind)
+        for out in ("f32", "bf16"):
+            y = P.packed_linear(x.cuda(), pk, x_scales=None if xs is None else xs.cuda(),
+                                out_dtype=DT[out])
+            check(y, x, xs, codes, scales, zeros)
