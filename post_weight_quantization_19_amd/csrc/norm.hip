@@ -21,12 +21,6 @@
 namespace pwq {
 namespace {
 
-template <typename T>
-__device__ __forceinline__ float load1(const void* p, int64_t i) {
-  if constexpr (std::is_same_v<T, float>) return ((const float*)p)[i];
-  else return bf16_to_f32(((const uint16_t*)p)[i]);
-}
-
 __device__ __forceinline__ float block_sum(float v, float* red) {
 #pragma unroll
   for (int o = 32; o >= 1; o >>= 1) v += __shfl_xor(v, o, 64);

@@ -136,13 +136,6 @@ __global__ __launch_bounds__(64) void pack_entries(const int32_t* __restrict__ c
 __global__ void clear_info(int32_t* info) { info[threadIdx.x] = 0; }
 
 // ---- the product, any shape: one wave per row and up to TT tokens
-template <typename T>
-__device__ __forceinline__ float load1(const void* p, int64_t i) {
-  if constexpr (std::is_same_v<T, float>) return ((const float*)p)[i];
-  else if constexpr (std::is_same_v<T, int8_t>) return (float)((const int8_t*)p)[i];
-  else return bf16_to_f32(((const uint16_t*)p)[i]);
-}
-
 constexpr int TT = 4;
 
 template <typename T>

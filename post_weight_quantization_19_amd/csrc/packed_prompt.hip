@@ -49,27 +49,6 @@ __device__ __forceinline__ uint32_t unit_at(int r, int c) {
   return (uint32_t)(r * KB + ((c ^ ((r >> 1) & 7)) << 4));
 }
 
-// Eight 4-bit steps of a dword to bf16: a code's four bits are put at the top of
-// the mantissa of 16, and 16 + z is subtracted in float32, whose upper half holds
-// the difference exactly (no conversion instruction: those run at a quarter of
-// the rate).  zb = 16 + z, or 24 with `bias` 0x41c0 for signed halves (it flips
-// their top bit; 0x4180 otherwise).
-__device__ __forceinline__ uint4 steps_bf16(uint32_t w, uint32_t bias, float zb) {
-  constexpr uint32_t M = 0x00780078u;
-  const uint32_t c[4] = {((w << 3) & M) ^ bias, ((w >> 1) & M) ^ bias, ((w >> 5) & M) ^ bias,
-                         ((w >> 9) & M) ^ bias};            // columns i and i + 4
-  float lo[4], hi[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    lo[i] = __uint_as_float(c[i] << 16) - zb;
-    hi[i] = __uint_as_float(c[i] & 0xffff0000u) - zb;
-  }
-  auto two = [](float x, float y) {
-    return __builtin_amdgcn_perm(__float_as_uint(y), __float_as_uint(x), 0x07060302u);
-  };
-  return make_uint4(two(lo[0], lo[1]), two(lo[2], lo[3]), two(hi[0], hi[1]), two(hi[2], hi[3]));
-}
-
 template <bool I8> using sum_t = std::conditional_t<I8, i32x4_t, f32x4_t>;
 
 template <bool I8>
@@ -416,7 +395,7 @@ void batch_tiles(const PromptArgs a) {
   constexpr bool PAIRED = MODE != 2;
   auto unit = [&](int h) { return PAIRED ? 2 * lq + h : 4 * h + lq; };
   constexpr int PB = I8 ? 8 : 4;                        // packed bytes of a lane's half
-  constexpr uint32_t flip = ASYM ? 0u : 0x88888888u, bias = ASYM ? 0x41804180u : 0x41c041c0u;
+  constexpr uint32_t flip = ASYM ? 0u : 0x88888888u, bias = ASYM ? kUnsignedHalves : kSignedHalves;
 
   ask(k0, 0);
   ask(min(k0 + 1, last), 1);
@@ -493,7 +472,7 @@ void batch_tiles(const PromptArgs a) {
             const uint2 lo = steps_i8(p[0] ^ flip, z4), hi = steps_i8(p[1] ^ flip, z4);
             w[j][h] = i32x4_t{(int)lo.x, (int)lo.y, (int)hi.x, (int)hi.y};
           } else {
-            w[j][h] = __builtin_bit_cast(i32x4_t, steps_bf16(p[0], bias, 16.0f + (float)z));
+            w[j][h] = __builtin_bit_cast(i32x4_t, steps_bf16(p[0], bias, z));
           }
         }
       }

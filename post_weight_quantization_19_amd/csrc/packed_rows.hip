@@ -43,31 +43,6 @@ template <> struct XType<X_I8> { using T = int8_t; };
 template <> struct XType<X_I8_BF16> { using T = int8_t; };
 template <> struct XType<X_F32> { using T = float; };
 
-__device__ __forceinline__ uint32_t pack_hi(float a, float b) {   // exact for small integers
-  return __builtin_amdgcn_perm(__float_as_uint(b), __float_as_uint(a), 0x07060302u);
-}
-
-// Eight 4-bit steps of a dword to bf16.  A code, bits 0 .. 3 of a float16 64 +
-// u / 16 (`bias` 0x5400 per half, or 0x5408 for signed halves, whose top bit it
-// flips), becomes 1024 + u, less zb = 1024 + z (1032 for signed halves), in one
-// multiplication and addition; the upper half of that float32 holds the
-// difference exactly.  (Codes as 16 + u in bf16, corrected by 16 + z times the
-// sum of x, are 1 to 3% faster, but lose three bits of a small result and all
-// of one whose x is above 2^123.)
-__device__ __forceinline__ bf16x8_t steps_bf16(uint32_t w, uint32_t bias, float zb) {
-  typedef _Float16 f16x2_t __attribute__((ext_vector_type(2)));
-  constexpr uint32_t M = 0x000f000fu;
-  float lo[4], hi[4];                                  // columns i and i + 4
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const f16x2_t h = __builtin_bit_cast(f16x2_t, ((w >> (4 * i)) & M) ^ bias);
-    lo[i] = fmaf((float)h[0], 16.0f, -zb);
-    hi[i] = fmaf((float)h[1], 16.0f, -zb);
-  }
-  const uint4 o = make_uint4(pack_hi(lo[0], lo[1]), pack_hi(lo[2], lo[3]), pack_hi(hi[0], hi[1]),
-                             pack_hi(hi[2], hi[3]));
-  return __builtin_bit_cast(bf16x8_t, o);
-}
 // Eight signed halves to bytes of 16 times the code, its four bits at the top.
 __device__ __forceinline__ uint2 signed16_i8(uint32_t w) {
   const uint32_t even = (w << 4) & 0xf0f0f0f0u, odd = w & 0xf0f0f0f0u;
@@ -269,10 +244,10 @@ __global__ __launch_bounds__(1024) void packed_rows(const PackedLinearLaunch a) 
             c = __builtin_amdgcn_mfma_i32_16x16x64_i8(v, f, c, 0, 0, 0);
           }
         } else {
-          const uint32_t bias = asym ? 0x54005400u : 0x54085408u;
+          const uint32_t bias = asym ? kUnsignedHalves : kSignedHalves;
 #pragma unroll
           for (int j = 0; j < NW; ++j) {
-            const bf16x8_t f = steps_bf16(w[j], bias, 1024.0f + (float)z);
+            const bf16x8_t f = __builtin_bit_cast(bf16x8_t, steps_bf16(w[j], bias, z));
             const int col = GB * h + NC * lq + 8 * j;
             T xv[8];
             if constexpr (XK == X_BF16) {
