@@ -501,7 +501,7 @@ def _rows(t: torch.Tensor, name: str, device: int) -> int:
     """Row stride of a 2-D tensor with unit column stride on this GPU."""
     if t.get_device() != device:
         raise ValueError(f"{name} must be on x's GPU")
-    return _row_major(t)
+    return t.shape[1] if t.dim() == 2 and t.is_contiguous() else _row_major(t)
 
 
 def _expect(t: torch.Tensor, name: str, shape: tuple, dtype: torch.dtype, device: int) -> int:
@@ -513,20 +513,18 @@ def _expect(t: torch.Tensor, name: str, shape: tuple, dtype: torch.dtype, device
     return t.data_ptr()
 
 
-def _device(x: torch.Tensor) -> int:
-    """Index of the GPU that x is on."""
-    device = x.get_device()
+def _on_device(device: int):
+    """The context of a call whose input is not on the current GPU."""
     if device < 0:
         raise ValueError("x must be on the GPU")
-    return device
+    return torch.cuda.device(device)
 
 
 def _no_gradient(*ts):
-    if torch.is_grad_enabled():
-        for t in ts:
-            if t is not None and t.requires_grad:
-                raise ValueError("a tensor requires a gradient, which this call does not give: "
-                                 "call it under torch.no_grad(), or detach the tensor")
+    for t in ts:
+        if t is not None and t.requires_grad:
+            raise ValueError("a tensor requires a gradient, which this call does not give: "
+                             "call it under torch.no_grad(), or detach the tensor")
 
 
 def pack_weights(codes: torch.Tensor, scales: torch.Tensor, grid: Grid,
@@ -593,11 +591,12 @@ def rms_norm(x: torch.Tensor, weight: torch.Tensor, residual: Optional[torch.Ten
     ``sum_out`` where given (x or residual itself for in place).  Runs on x's
     GPU, on its current stream.  Gives no gradients, and refuses tensors that
     require one unless they are off (torch.no_grad())."""
-    dev = _device(x)
-    _no_gradient(x, weight, residual, sum_out)
+    dev = x.get_device()
     if dev != torch._C._cuda_getDevice():
-        with torch.cuda.device(dev):
+        with _on_device(dev):
             return rms_norm(x, weight, residual, eps, out_dtype, sum_out)
+    if torch.is_grad_enabled():
+        _no_gradient(x, weight, residual, sum_out)
     ldx = _rows(x, "x", dev)
     ntok, n = x.shape
     xdt = _dtype_code(x)
@@ -613,10 +612,12 @@ def rms_norm(x: torch.Tensor, weight: torch.Tensor, residual: Optional[torch.Ten
             raise ValueError("residual must have x's shape and type")
         rp, ldr = residual.data_ptr(), _rows(residual, "residual", dev)
         if total is None:
-            total = torch.empty_like(x, memory_format=torch.contiguous_format)
+            total, lds = torch.empty_like(x, memory_format=torch.contiguous_format), n
         elif total.shape != x.shape or total.dtype is not x.dtype:
             raise ValueError("sum_out must have x's shape and type")
-        tp, lds = total.data_ptr(), _rows(total, "sum_out", dev)
+        else:
+            lds = _rows(total, "sum_out", dev)
+        tp = total.data_ptr()
     elif sum_out is not None:
         raise ValueError("sum_out goes with a residual")
     y = torch.empty_like(x, dtype=odt, memory_format=torch.contiguous_format)
@@ -640,11 +641,12 @@ def packed_linear(x: torch.Tensor, packed: dict, x_scales: Optional[torch.Tensor
     int8); ``out`` may pass the result's memory.  Runs on x's GPU, on its
     current stream.  Gives no gradients, and refuses tensors that require one
     unless they are off (torch.no_grad())."""
-    dev = _device(x)
-    _no_gradient(x, x_scales, packed["scales"], out)
+    dev = x.get_device()
     if dev != torch._C._cuda_getDevice():
-        with torch.cuda.device(dev):
+        with _on_device(dev):
             return packed_linear(x, packed, x_scales, out_dtype, out)
+    if torch.is_grad_enabled():
+        _no_gradient(x, x_scales, packed["scales"], out)
     q, zeros, outliers = packed["qweight"], packed["zeros"], packed["outliers"]
     n, group = packed["n"], packed["group"]
     ldx = _rows(x, "x", dev)
