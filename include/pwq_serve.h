@@ -80,7 +80,7 @@ pwq_status pwq_pack_overflow(const int32_t* codes, int64_t m, int64_t n, int64_t
  *   x        : ntok x n, xdtype PWQ_F32 or PWQ_BF16, row stride ldx >= n.
  *   residual : NULL, or ntok x n of the same type, row stride ldr >= n.
  *   weight   : n values, wdtype PWQ_F32 or PWQ_BF16.
- *   eps      : finite, >= 0.
+ *   eps      : 0 <= eps < 1e30, rounded to float32.
  *   sum      : NULL, or out: h in x's type, row stride lds >= n; may be the
  *              memory of x or of residual with the same stride, and else
  *              overlaps neither.
@@ -90,7 +90,8 @@ pwq_status pwq_pack_overflow(const int32_t* codes, int64_t m, int64_t n, int64_t
  *              (1 where that is 0); y = rint(value / step), within -127 ..
  *              127.  A token whose y holds a NaN or an infinity gets that as
  *              its step, and the codes 0.  Unused otherwise.
- * A square or their sum beyond float32's range (|h| above 1e19) gives 0.
+ * Squares and their sum are float32: beyond its range (|h| above 1e19) they give
+ * 0, and below it (|h| under 1e-22 with eps = 0) an infinity.
  * ---------------------------------------------------------------------- */
 pwq_status pwq_rms_norm(const void* x, int32_t xdtype, int64_t ntok, int64_t n, int64_t ldx,
                         const void* residual, int64_t ldr, const void* weight, int32_t wdtype,
@@ -112,10 +113,15 @@ pwq_status pwq_rms_norm(const void* x, int32_t xdtype, int64_t ntok, int64_t n, 
  *               wider matrix).
  *   ws        : pwq_packed_linear_workspace_size bytes, for this x, sizes,
  *               group and n_out (0 for few tokens whose rows of x are 16-byte aligned).
- * Steps c - z multiply x as integers and a group's sum is multiplied by its
- * step: sums are int32 (PWQ_I8) or float32 within a group and float32 over
- * the groups, in a fixed order.  A token with an infinity or NaN gives values
- * that are not finite; other tokens are unaffected.
+ * Steps c - z multiply x as integers.  With groups of a multiple of 32 columns,
+ * or one per row, the sum of a group, or of 32 or more of its columns, is
+ * multiplied by the group's step; that sum is float32, and exact for PWQ_I8
+ * (int32, or float32 below 2^24) but in rows of one group of more than 2^17
+ * columns.  Groups of other sizes multiply each product.  Sums beyond that are
+ * float32, and all of them in a fixed order; which kernel serves a token, and
+ * so the last bits of its result, depends on ntok.  A token with an infinity or
+ * NaN, or sums beyond float32's range, gives values that are not finite; other
+ * tokens are unaffected.
  * ---------------------------------------------------------------------- */
 size_t pwq_packed_linear_workspace_size(const void* x, int32_t xdtype, int64_t ntok, int64_t ldx,
                                         int64_t m, int64_t n, int32_t group, int64_t n_out);

@@ -232,8 +232,8 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void rms_norm_regs(const Rms
 // One workgroup per token, three passes over its row.
 template <typename T>
 __global__ __launch_bounds__(256) void rms_norm_rows(
-    const void* x, int64_t ntok, int64_t n, int64_t ldx, const void* residual, int64_t ldr, const void* weight,
-    int wf32, float eps, void* sum, int64_t lds, void* y, int ydtype, int64_t ldy, float* scales) {
+    const void* x, int64_t ntok, int64_t n, int64_t ldx, const void* residual, int64_t ldr,
+    const void* weight, int wf32, float eps, void* sum, int64_t lds, void* y, int ydtype, int64_t ldy, float* scales) {
   __shared__ float red[4];
   const int64_t t = block_index();
   if (t >= ntok) return;
@@ -279,7 +279,9 @@ __global__ __launch_bounds__(256) void rms_norm_rows(
 template <typename T, int TPR, int NV>
 void launch_regs(const RmsNormLaunch& a, hipStream_t st) {
   constexpr int RPB = TPR < 256 ? 256 / TPR : 1;
-  // workgroups that run at once: the rest of the tokens are walked over
+  // workgroups that run at once, 1536 threads a CU: the rest of the tokens are
+  // walked over (1024 and 2048 threads: 8192 x 8192 96 and 91 us instead of 89;
+  // 8192 x 4096 47.0 and 47.4 instead of 48.7; 8192 x 14336 169 and 173, 172)
   const int64_t blocks = std::min<int64_t>(
       (a.ntok + RPB - 1) / RPB, 256 * (1536 / std::max(TPR, 256) + (TPR == 1024)));
   const dim3 grid((unsigned)blocks), block(TPR < 256 ? 256 : TPR);
@@ -290,15 +292,23 @@ void launch_regs(const RmsNormLaunch& a, hipStream_t st) {
 template <typename T>
 void launch_loop(const RmsNormLaunch& a, hipStream_t st) {
   rms_norm_rows<T><<<block_grid(a.ntok), 256, 0, st>>>(
-      a.x, a.ntok, a.n, a.ldx, a.residual, a.ldr, a.weight, a.wdtype == PWQ_F32, a.eps, a.sum, a.lds, a.y,
-      a.ydtype, a.ldy, a.scales);
+      a.x, a.ntok, a.n, a.ldx, a.residual, a.ldr, a.weight, a.wdtype == PWQ_F32, a.eps, a.sum,
+      a.lds, a.y, a.ydtype, a.ldy, a.scales);
 }
 
 template <typename T>
 void launch_type(const RmsNormLaunch& a, hipStream_t st) {
   const int64_t n = a.n;
-  // Few tokens: more threads a row, for latency.  Many: fewer, for fewer
-  // barriers.
+  // Each form's width is what its registers hold.  Up to 2048 columns a wave a
+  // row, without barriers; above, few tokens: more threads a row, for latency;
+  // many: fewer, for fewer barriers.  us, bf16 with residual to 8 bits, this form
+  // and the other (1024 threads up to 256 tokens, 256 or 512 above):
+  //    columns   1 token     256 tokens   512 tokens   4096 tokens
+  //        512   2.5, 4.3    -            3.2, 3.7     6.0, 9.7
+  //       2048   4.1, 4.3    -            5.4, 4.4     15.9, 15.7
+  //       4096   4.4, 3.5    5.4, 4.8     6.6, 9.6     27, 45
+  //       8192   4.3, 4.5    6.8, 7.3     10.8, 12.2   48, 55
+  //      14336   5.8, 6.1    10.4, 10.9   19.0, 18.6   94, 90
   if (n < 8) return launch_loop<T>(a, st);
   if (n <= 512) return launch_regs<T, 64, 1>(a, st);
   if (n <= 1024) return launch_regs<T, 64, 2>(a, st);

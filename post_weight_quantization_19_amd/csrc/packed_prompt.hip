@@ -28,13 +28,15 @@
 // it in accumulation registers, whose reads double the vector instructions (81
 // us).
 //
-// What bounds it: the matrix unit at the clock that its power allows, and the
-// multiplications of its sums by the steps, which overlap it in part.  Tiles
-// alone take 254 to 290 us (as the clock goes) for 2048 bf16 tokens of up_proj
-// and 146 to 163 us in 8 bits (0.95 and 1.65 P(FL)OP/s at best), 206 and 105
-// us with one step per row; 8192 tokens 927 and 585 us with everything (1.04
-// and 1.64 P(FL)OP/s).  The library's products of the first size take 207 us
-// (bf16) and, at its 8192^3 rate, 115 us (8 bits).
+// What bounds it: the matrix instructions and the multiplications of their sums
+// by the steps on the vector unit, which follow each other more than they
+// overlap, and the wait at every step's barrier.  Of a tile's cycles the matrix
+// unit is busy 37% and the vector unit 44% for 2048 8-bit tokens of up_proj
+// (groups of 128), 44% and 26% for 1024 bf16 tokens of down_proj (64).  Tiles alone take 254 to 296 us (as the clock
+// goes) for 2048 bf16 tokens of up_proj and 146 to 163 us in 8 bits (0.95 and
+// 1.65 P(FL)OP/s at best), 206 and 105 us with one step per row; 8192 tokens 961
+// and 596 us with everything (1.00 and 1.61 P(FL)OP/s).  The library's products
+// of the first size take 207 us (bf16) and, at its 8192^3 rate, 115 us (8 bits).
 #include "pwq_internal.h"
 
 #include <algorithm>
@@ -268,9 +270,9 @@ __device__ __forceinline__ void store_tile(const PromptArgs& a,
 // workgroup, 32 rows of weights (2 KB), their steps and zero points for the
 // wave that spreads them and multiplies by them.  Lanes next to each other copy
 // bytes next to each other; loads in the operands' layout, one cache lookup a
-// lane, took 33 us for 32 bf16 tokens of up_proj, these 21.  With overflow
+// lane, took 33 us for 32 bf16 tokens of up_proj, these 20.  With overflow
 // entries (OVER) the codes become bytes in LDS first, where the entries' are
-// added (24 us; written to memory spread, 57).  What bounds it: latency with few
+// added (25 us; written to memory spread, 57).  What bounds it: latency with few
 // columns a split, then the vector unit's spreading; up_proj 64 8-bit tokens
 // 20 us, 1.6 TB/s.
 constexpr int kSpreadRow = 128 + 16;                  // bytes of a spread row (OVER)
@@ -860,10 +862,10 @@ PromptPlan prompt_plan(const void* x, int32_t xdtype, int64_t ntok, int64_t ldx,
   double best = 0;
   // batch_tiles as long as its spreading of the codes for every tile of tokens
   // costs less than spread_weights and its traffic: 256 8-bit tokens of
-  // 14336 x 4096 37 us against 50, 512 65 both (q_proj 25 against 33); 256 bf16
-  // tokens 60 against 79, 384 93 against 97 to 102 (down_proj 100 against 93);
-  // with overflow entries 128 bf16 tokens 68 both, 256 117 against 81; float32
-  // 129 tokens 134 against 124.
+  // 14336 x 4096 38 us against 52, 512 65 both (q_proj 26 against 33); 256 bf16
+  // tokens 56 against 79, 384 83 against 100 (down_proj 88 against 93), 512 103
+  // against 96; with overflow entries 128 bf16 tokens 69 both, 256 119 against
+  // 81; float32 128 tokens 91 against 90, 129 122 against 109.
   p.fused = ntok <= (n_out > 0 || p.reps == 3 ? 128 : (p.i8 ? 512 : 320));
   if (p.fused) {
     // 32 x 128 or 64 x 128 tiles and column splits by their estimated time, as

@@ -13,10 +13,10 @@
 // take 8.8, and 19.5 against 13.4 for 16 bf16 tokens.
 //
 // What bounds it: with one token the weights' bytes, from a last-level cache
-// that holds the layer (up_proj one 8-bit token 8.8 us, 3.5 TB/s; a kernel that
-// only reads those bytes takes 5.4 to 6.3), or a launch and the first bytes'
-// way (q_proj 4.6 us; a launch alone 2.7).  bf16 x spends the vector unit on
-// spreading (11.0 us), 16 tokens read 128 KB of x for every 16 rows (13.4 us).
+// that holds the layer (up_proj one 8-bit token 8.8 us, 3.6 TB/s; 10.0 from HBM; a
+// kernel that only reads those bytes takes 5.4 to 6.3), or a launch and the first
+// bytes' way (q_proj 4.6 us; a launch alone 2.7).  bf16 x spends the vector unit on
+// spreading (11.4 us), 16 tokens read 128 KB of x for every 16 rows (13.9 us).
 //
 // Operands: x (16 tokens) and the codes of 16 rows.  Lane l holds token l % 16
 // and row l % 16, and of block h of GB columns, GB <= G, the GB / 4 from
@@ -28,8 +28,8 @@
 // Codes beyond 4 bits enter as further columns: up to 32 (64 for 8-bit x)
 // entries of a tile at a time, x gathered at their columns, the entry's value
 // in its own row and 0 in the others.  A wave holds 256 entries in LDS; they are
-// copied like the weights (q_proj one bf16 token with 0.2% of such codes 6.8
-// us; read by ordinary loads, which wait for the copies, 7.7).
+// copied like the weights (q_proj one bf16 token with 0.2% of such codes 6.9
+// us, 5.1 without; read by ordinary loads, which wait for the copies, 7.7).
 #include "pwq_internal.h"
 
 #include <algorithm>
@@ -427,8 +427,11 @@ void launch_x(const PackedLinearLaunch& a, int gb, hipStream_t st) {
 
 }  // namespace
 
-// Up to 16 tokens, steps per 32 columns or more (or per row), offsets and the
-// launch's 4 m threads within 32 bits.
+// Up to 16 tokens, what a matrix operand holds (as batch_tiles, 16 bf16 tokens
+// of q_proj, up_proj and down_proj take 11.5, 20.1 and 21.1 us instead of 6.3, 16.3
+// and 17.1, 8-bit ones 9.9, 15.3 and 16.2 instead of 5.2, 12.5 and 13.3); steps
+// per 32 columns or more (or per row); offsets and the launch's 4 m threads
+// within 32 bits.
 bool rows_ok(int64_t ntok, int64_t m, int64_t n, int32_t G) {
   return ntok <= kRowsTokens && (G == n || G % 32 == 0) && n < (1 << 24) && m < (1 << 29);
 }
