@@ -5,7 +5,8 @@ Quantization: GPTQ as Babai's Nearest Plane Algorithm", technical summary
 2.1-2.3) and its successive-interference-cancellation form with per-column
 spacing ("WaterSIC: information-theoretically (near) optimal linear layer
 quantization", technical summary 2), behind the C ABI of ``libpwq.so``
-(``include/pwq.h``).  These wrappers only marshal torch tensors (device
+(``include/pwq.h``; ``include/pwq_serve.h`` and ``include/pwq_cache.h`` for
+running quantized layers and the cache between them).  These wrappers only marshal torch tensors (device
 memory) and the current stream into that ABI; the HIP kernels do all the
 work and there is no CPU fallback.
 """
@@ -21,7 +22,7 @@ from ._lib import PwqError, check, lib, make_grid, parse_result
 __all__ = ["Grid", "hessian_accum", "damp_cholesky", "damp_cholesky_static", "grid_steps", "babai_sweep",
            "quant_layer", "column_entropy", "read_result", "PwqError", "KernelTimer",
            "HessianTileTimer", "overflow_entries", "ssqr_quant_layer", "pack_weights", "rms_norm",
-           "packed_linear"]
+           "packed_linear", "new_cache", "cache_write", "cache_read", "cached_attention"]
 
 
 @dataclass(frozen=True)
@@ -697,6 +698,184 @@ def packed_linear(x: torch.Tensor, packed: dict, x_scales: Optional[torch.Tensor
         ws = _workspace(L_.pwq_packed_linear_workspace_size(x.data_ptr(), xdt, ntok, ldx, m, n,
                                                             group, n_out), x.device)
         nb = ws.numel()
+    if status:
+        check(status)
+    return out
+
+
+# ------------------------------------------------------------ the key-value cache
+
+def new_cache(pages: int, kv_heads: int, head_dim: int, bits: int = 8, page: int = 64,
+              device="cuda") -> dict:
+    """An empty key-value cache of ``pages`` pages of ``page`` tokens (a power of
+    two, 32 .. 4096), for heads of 64, 128 or 256 channels in 8 or 4 bits:
+    dict(records [pages, kv_heads, page / 32, bytes of a record] uint8, bits,
+    head_dim, page)."""
+    size = lib().pwq_cache_record_bytes(head_dim, bits)
+    if not size:
+        raise ValueError("a cache has head_dim 64, 128 or 256 and 4 or 8 bits")
+    if page < 32 or page > 4096 or page & (page - 1):
+        raise ValueError("page must be a power of two in 32 .. 4096")
+    if pages < 0 or kv_heads < 1:
+        raise ValueError("need pages >= 0 and kv_heads >= 1")
+    records = torch.zeros((pages, kv_heads, page // 32, size), dtype=torch.uint8, device=device)
+    return {"records": records, "bits": bits, "head_dim": head_dim, "page": page}
+
+
+def _cache_struct(cache: dict, device: int):
+    records, page = cache["records"], cache["page"]
+    if records.get_device() != device:
+        raise ValueError("the cache must be on the tensors' GPU")
+    bits, dim = cache["bits"], cache["head_dim"]
+    if records.dim() != 4 or records.dtype is not torch.uint8 or not records.is_contiguous():
+        raise ValueError("records must be a contiguous 4-D uint8 tensor")
+    pages, heads, blocks, size = records.shape
+    if blocks * 32 != page or size != 8 * dim * bits + 256:
+        raise ValueError(f"records of {tuple(records.shape)} do not fit pages of {page} tokens, "
+                         f"{dim} channels and {bits} bits")
+    return _lib.PwqCache(records.data_ptr(), pages, heads, dim, bits, page), heads, dim
+
+
+def _batch_struct(starts, lengths, table, device: int):
+    if table.dim() != 2 or table.dtype is not torch.int32 or table.get_device() != device:
+        raise ValueError("table must be a 2-D int32 tensor on the tensors' GPU")
+    nseq, width = table.shape
+    sp = _expect(starts, "starts", (nseq + 1,), torch.int32, device)
+    lp = _expect(lengths, "lengths", (nseq,), torch.int32, device)
+    ld = width
+    if not table.is_contiguous():
+        ld = table.stride(0)
+        if width > 1 and table.stride(1) != 1 or nseq > 1 and ld < width:
+            raise ValueError("table must be row-major")
+        ld = max(ld, width)
+    return _lib.PwqBatch(sp, lp, table.data_ptr(), ld, nseq, width)
+
+
+def _heads(t: torch.Tensor, name: str, shape: tuple, dtype, device: int):
+    """Strides of a [tokens, heads, head_dim] tensor with unit channel stride."""
+    if t.get_device() != device:
+        raise ValueError(f"{name} must be on the cache's GPU")
+    if t.shape != shape or t.dtype is not dtype:
+        raise ValueError(f"{name} must be {list(shape)} {dtype}")
+    ts, hs, ds = t.stride()
+    if ds != 1:
+        raise ValueError(f"{name} must have unit channel stride")
+    return ts, hs
+
+
+def cache_write(k: torch.Tensor, v: torch.Tensor, cache: dict, starts: torch.Tensor,
+                lengths: torch.Tensor, table: torch.Tensor) -> None:
+    """Quantizes keys and values [tokens, kv_heads, head_dim] (bf16 or fp32, any
+    token and head stride) into a cache, one step and zero point per token and
+    head.  The batch is ragged: rows starts[i] .. starts[i + 1] - 1 are the last
+    of the lengths[i] tokens of sequence i (these rows included), whose token p
+    lies in page table[i, p // page].  ``starts`` [n + 1], ``lengths`` [n] and
+    ``table`` [n, width] are int32 on the GPU; a captured call reads them anew on
+    every replay.  Rows of no sequence, and tokens whose page is none of the
+    cache's (-1, say), are left out.  Runs on k's GPU, on its current stream.
+    Gives no gradients, and refuses tensors that require one unless they are off
+    (torch.no_grad())."""
+    dev = k.get_device()
+    if dev != torch._C._cuda_getDevice():
+        with _on_device(dev):
+            return cache_write(k, v, cache, starts, lengths, table)
+    if torch.is_grad_enabled():
+        _no_gradient(k, v)
+    c, heads, dim = _cache_struct(cache, dev)
+    b = _batch_struct(starts, lengths, table, dev)
+    if k.dim() != 3:
+        raise ValueError("k must be [tokens, kv_heads, head_dim]")
+    shape = (k.shape[0], heads, dim)
+    kts, khs = _heads(k, "k", shape, k.dtype, dev)
+    vts, vhs = _heads(v, "v", shape, k.dtype, dev)
+    status = lib().pwq_cache_write(c, b, k.data_ptr(), kts, khs, v.data_ptr(), vts, vhs,
+                                   _dtype_code(k), shape[0],
+                                   torch._C._cuda_getCurrentRawStream(dev))
+    if status:
+        check(status)
+
+
+def cache_read(cache: dict, starts: torch.Tensor, lengths: torch.Tensor, table: torch.Tensor,
+               tokens: int, dtype: torch.dtype = torch.bfloat16, out: Optional[tuple] = None):
+    """(k, v) [tokens, kv_heads, head_dim] that a cache holds for the rows of a
+    batch as for cache_write (for whole sequences: starts that count all of their
+    tokens); fp32 is exact, bf16 rounded once.  Tokens of pages that are none of
+    the cache's read as 0.  ``out`` may pass (k, v); their rows of no sequence
+    keep what was there, and are unspecified where the call allocates.  Runs on
+    the cache's GPU, on its current stream."""
+    dev = cache["records"].get_device()
+    if dev != torch._C._cuda_getDevice():
+        with _on_device(dev):
+            return cache_read(cache, starts, lengths, table, tokens, dtype, out)
+    c, heads, dim = _cache_struct(cache, dev)
+    b = _batch_struct(starts, lengths, table, dev)
+    shape = (tokens, heads, dim)
+    if out is None:
+        k = cache["records"].new_empty(shape, dtype=dtype)
+        v = torch.empty_like(k)
+    else:
+        k, v = out
+        if torch.is_grad_enabled():
+            _no_gradient(k, v)
+        dtype = k.dtype
+    kts, khs = _heads(k, "k", shape, dtype, dev)
+    vts, vhs = _heads(v, "v", shape, dtype, dev)
+    status = lib().pwq_cache_read(c, b, k.data_ptr(), kts, khs, v.data_ptr(), vts, vhs,
+                                  _dtype_code(k), tokens, torch._C._cuda_getCurrentRawStream(dev))
+    if status:
+        check(status)
+    return k, v
+
+
+def cached_attention(q: torch.Tensor, cache: dict, starts: torch.Tensor, lengths: torch.Tensor,
+                     table: torch.Tensor, scale: Optional[float] = None, causal: bool = True,
+                     prefix: Optional[tuple] = None,
+                     out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """Attention of q [tokens, heads, head_dim] (bf16 or fp32, any token and head
+    stride; heads a multiple of the cache's) over a cache, for a batch as for
+    cache_write; query head h reads key head h // (heads / kv_heads).  A row sees
+    its sequence's tokens up to its own (``causal``), which have to be written, or
+    all of them.  ``scale`` defaults to head_dim ** -0.5.  ``prefix`` = (pages
+    int32 [n], length int32 [1], both on the GPU) names tokens of the cache that
+    come before those of every sequence: they are read once for the whole batch,
+    and neither ``table`` nor ``lengths`` counts them.  A row that sees no token
+    gives 0.  ``out`` may pass the result's memory (q's shape and type; must not
+    overlap q); rows of no sequence keep what was there, and are unspecified
+    where the call allocates.  Runs on q's GPU, on its current stream.  Gives no
+    gradients, and refuses tensors that require one unless they are off
+    (torch.no_grad())."""
+    dev = q.get_device()
+    if dev != torch._C._cuda_getDevice():
+        with _on_device(dev):
+            return cached_attention(q, cache, starts, lengths, table, scale, causal, prefix, out)
+    if torch.is_grad_enabled():
+        _no_gradient(q, out)
+    c, kv_heads, dim = _cache_struct(cache, dev)
+    b = _batch_struct(starts, lengths, table, dev)
+    if q.dim() != 3:
+        raise ValueError("q must be [tokens, heads, head_dim]")
+    shape = q.shape
+    tokens, heads = shape[0], shape[1]
+    qts, qhs = _heads(q, "q", (tokens, heads, dim), q.dtype, dev)
+    dtype = _dtype_code(q)
+    if out is None:
+        out, ots, ohs = q.new_empty(shape), heads * dim, dim
+    else:
+        ots, ohs = _heads(out, "out", shape, q.dtype, dev)
+    p = None
+    if prefix is not None:
+        pages, length = prefix
+        n = pages.shape[0] if pages.dim() == 1 else -1
+        p = _lib.PwqBatch(None, _expect(length, "the prefix's length", (1,), torch.int32, dev),
+                          _expect(pages, "the prefix's pages", (n,), torch.int32, dev), n, 1, n)
+    L_ = lib()
+    ws, nb = None, L_.pwq_cached_attention_workspace_size(c, b, p, heads, dtype, tokens)
+    if nb:
+        ws = torch.empty(nb, dtype=torch.uint8, device=q.device)
+    status = L_.pwq_cached_attention(c, b, p, q.data_ptr(), qts, qhs, out.data_ptr(), ots, ohs,
+                                     heads, dtype, tokens, dim ** -0.5 if scale is None else scale,
+                                     causal, None if ws is None else ws.data_ptr(), nb,
+                                     torch._C._cuda_getCurrentRawStream(dev))
     if status:
         check(status)
     return out

@@ -38,6 +38,11 @@ SERVE_EXPORTS = [
     "pwq_packed_row_bytes", "pwq_pack_tiles", "pwq_pack_codes", "pwq_pack_overflow",
     "pwq_rms_norm", "pwq_packed_linear_workspace_size", "pwq_packed_linear",
 ]
+# and include/pwq_cache.h (the key-value cache)
+CACHE_EXPORTS = [
+    "pwq_cache_record_bytes", "pwq_cache_write", "pwq_cache_read",
+    "pwq_cached_attention_workspace_size", "pwq_cached_attention",
+]
 PWQ_TIMER_HESSIAN_TILES, PWQ_TIMER_LAZY_UPDATE, PWQ_TIMER_SWEEP_BLOCK = 0, 1, 2
 TIMED_KERNELS = {"hessian_tiles": PWQ_TIMER_HESSIAN_TILES, "lazy_update": PWQ_TIMER_LAZY_UPDATE,
                  "sweep_block": PWQ_TIMER_SWEEP_BLOCK}
@@ -47,6 +52,18 @@ class PwqGrid(ctypes.Structure):
     _fields_ = [("kind", ctypes.c_int32), ("bits", ctypes.c_int32),
                 ("group_size", ctypes.c_int32), ("reserved", ctypes.c_int32),
                 ("c", ctypes.c_double), ("kappa", ctypes.c_double)]
+
+
+class PwqCache(ctypes.Structure):
+    _fields_ = [("records", ctypes.c_void_p), ("pages", ctypes.c_int64),
+                ("kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32),
+                ("bits", ctypes.c_int32), ("page", ctypes.c_int32)]
+
+
+class PwqBatch(ctypes.Structure):
+    _fields_ = [("starts", ctypes.c_void_p), ("lengths", ctypes.c_void_p),
+                ("table", ctypes.c_void_p), ("ldt", ctypes.c_int64),
+                ("nseq", ctypes.c_int32), ("width", ctypes.c_int32)]
 
 
 RESULT_BYTES = 64          # sizeof(pwq_result) = 56, padded
@@ -63,6 +80,7 @@ _lib = None
 
 _vp, _i32, _i64, _f64, _sz = (ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64,
                               ctypes.c_double, ctypes.c_size_t)
+_pcache, _pbatch = ctypes.POINTER(PwqCache), ctypes.POINTER(PwqBatch)
 _SIGS = {
     "pwq_status_string": (ctypes.c_char_p, [_i32]),
     "pwq_last_error": (ctypes.c_char_p, []),
@@ -108,6 +126,14 @@ _SIGS = {
     "pwq_packed_linear_workspace_size": (_sz, [_vp, _i32, _i64, _i64, _i64, _i64, _i32, _i64]),
     "pwq_packed_linear": (_i32, [_vp, _i32, _i64, _i64, _vp, _vp, _i64, _i64, _vp, _vp, _i32,
                                  _vp, _vp, _i64, _vp, _i32, _i64, _vp, _sz, _vp]),
+    "pwq_cache_record_bytes": (_i64, [_i32, _i32]),
+    "pwq_cache_write": (_i32, [_pcache, _pbatch, _vp, _i64, _i64, _vp, _i64, _i64, _i32, _i64,
+                               _vp]),
+    "pwq_cache_read": (_i32, [_pcache, _pbatch, _vp, _i64, _i64, _vp, _i64, _i64, _i32, _i64,
+                              _vp]),
+    "pwq_cached_attention_workspace_size": (_sz, [_pcache, _pbatch, _pbatch, _i32, _i32, _i64]),
+    "pwq_cached_attention": (_i32, [_pcache, _pbatch, _pbatch, _vp, _i64, _i64, _vp, _i64, _i64,
+                                    _i32, _i32, _i64, _f64, _i32, _vp, _sz, _vp]),
     "pwq_kernel_timer_attach": (_i32, [_i32, _vp, _vp, _i64]),
     "pwq_kernel_timer_count": (_i64, [_i32]),
 }

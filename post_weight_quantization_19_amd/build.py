@@ -14,7 +14,7 @@ LIB = os.path.join(HERE, "libpwq.so")
 PROBE = os.path.join(HERE, "peak_probe")
 SOURCES = ["pwq_api.hip", "hessian.hip", "cholesky.hip", "sweep.hip", "order.hip", "rate.hip",
            "ssqr.hip", "min_pivot.hip", "oaem.hip", "norm.hip", "packed.hip",
-           "packed_rows.hip", "packed_prompt.hip"]
+           "packed_rows.hip", "packed_prompt.hip", "cache.hip", "attention.hip"]
 ARCH = "gfx950"
 
 

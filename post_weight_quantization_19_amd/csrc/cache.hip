@@ -1,0 +1,220 @@
+// Writing to the key-value cache and reading it back (include/pwq_cache.h).
+#include "cache_device.h"
+
+namespace pwq {
+namespace {
+
+struct __attribute__((packed, aligned(1))) any16 { uint32_t v[4]; };
+
+// Eight consecutive elements (any alignment) in float32, and back.
+template <typename T>
+__device__ __forceinline__ void load8(const T* p, float (&x)[8]) {
+  if constexpr (std::is_same_v<T, float>) {
+    const any16 a = ((const any16*)p)[0], b = ((const any16*)p)[1];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) x[e] = __uint_as_float(a.v[e]), x[4 + e] = __uint_as_float(b.v[e]);
+  } else {
+    const any16 a = *(const any16*)p;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      x[2 * e] = __uint_as_float(a.v[e] << 16);
+      x[2 * e + 1] = __uint_as_float(a.v[e] & 0xffff0000u);
+    }
+  }
+}
+template <typename T>
+__device__ __forceinline__ void store8(T* p, const float (&x)[8]) {
+  if constexpr (std::is_same_v<T, float>) {
+    any16 a, b;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) a.v[e] = __float_as_uint(x[e]), b.v[e] = __float_as_uint(x[4 + e]);
+    ((any16*)p)[0] = a, ((any16*)p)[1] = b;
+  } else {
+    any16 a;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const __bf16 two[2] = {(__bf16)x[2 * e], (__bf16)x[2 * e + 1]};
+      a.v[e] = __builtin_bit_cast(uint32_t, two);
+    }
+    *(any16*)p = a;
+  }
+}
+
+// rint(x / s) of the exact quotient, |quotient| < 256, s of 16 significant bits
+// and at least 2^-100, inv = 1 / s.  r = rint(x inv) is at most one off, and only
+// where the quotient is within 2^-14 of a tie; x - r s is exact in float32 (r s has
+// 24 bits, and the difference is a multiple of the smaller unit, below s), so
+// that it says which side of the tie x is on.
+__device__ __forceinline__ float nearest(float x, float s, float inv) {
+  float r = __builtin_rintf(x * inv);
+  const float d = fabsf(fmaf(-r, s, x)) * 2.0f;
+  const float toward = copysignf(1.0f, fmaf(-r, s, x));
+  if (d > s || (d == s && (((int)r) & 1))) r += toward;
+  return r;
+}
+
+// A token's head: D / 8 lanes, eight channels each, codes of 8 channels in
+// `code`.  Returns the head's word.
+template <int D, int BITS>
+__device__ __forceinline__ uint32_t quantize(float (&x)[8], int (&code)[8]) {
+  constexpr float TOP = (1 << BITS) - 1;
+  float lo = 0.0f, hi = 0.0f, sum = 0.0f;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    lo = fminf(lo, x[e]), hi = fmaxf(hi, x[e]);
+    sum += x[e] * 0.0f;                                   // NaN after a NaN or an infinity
+  }
+#pragma unroll
+  for (int o = 1; o < D / 8; o <<= 1) {
+    lo = fminf(lo, __shfl_xor(lo, o, 64));
+    hi = fmaxf(hi, __shfl_xor(hi, o, 64));
+    sum += __shfl_xor(sum, o, 64);
+  }
+  const float range = hi - lo;
+  uint32_t word = (__float_as_uint(range / TOP) + 128u) & ~255u;
+  float s = __uint_as_float(word);
+  const bool bad = sum != 0.0f || !(range <= __FLT_MAX__);
+  if (bad || s == 0.0f) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) code[e] = 0;
+    return bad ? 0x7fc00000u : 0u;
+  }
+  // small steps: 2^64 times everything, so that 1 / s stays finite
+  const float up = s < 0x1p-100f ? 0x1p64f : 1.0f;
+  s *= up;
+  const float inv = 1.0f / s;
+  const float z = fminf(nearest(-lo * up, s, inv), TOP);
+#pragma unroll
+  for (int e = 0; e < 8; ++e)
+    code[e] = (int)fminf(fmaxf(nearest(x[e] * up, s, inv) + z, 0.0f), TOP);
+  return word | (uint32_t)(int)z;
+}
+
+// D / 8 threads write one token's head of keys, or of values.
+template <typename T, int D, int BITS>
+__global__ __launch_bounds__(256) void write_rows(const CacheRowsLaunch a) {
+  using R = Record<D, BITS>;
+  constexpr int TH = D / 8;                               // threads of a head
+  const int64_t head = block_index() * (256 / TH) + threadIdx.x / TH;
+  const int d = (int)(threadIdx.x % TH) * 8;
+  const int of = (int)(head & 1);
+  const int t = (int)((head >> 1) / a.cache.heads), h = (int)((head >> 1) % a.cache.heads);
+  if (t >= a.batch.ntok) return;                          // all threads of a head alike
+  const int s = find_sequence(a.batch, t);
+  if (s < 0) return;
+  const Seq q = sequence(a.batch, s);
+  const int p = q.len - (q.r1 - t);
+  if (p < 0) return;
+  const uint8_t* rec = record_of(a.cache, a.batch.table + s * a.batch.ldt, a.batch.width, p >> 5, h);
+  if (!rec) return;
+  uint8_t* out = a.cache.records + (rec - a.cache.records);
+  const CacheTensor& src = of ? a.v : a.k;
+  float x[8];
+  int c[8];
+  load8((const T*)src.p + t * src.ts + h * src.hs + d, x);
+  const uint32_t word = quantize<D, BITS>(x, c);
+  if (d == 0) ((uint32_t*)(out + R::words + of * 128))[p & 31] = word;
+  if (of == 0) {
+    uint32_t w[2] = {0, 0};
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      if constexpr (BITS == 8) w[e / 4] |= (uint32_t)c[e] << (8 * (e % 4));
+      else w[0] |= (uint32_t)c[e] << (4 * (e / 2) + 16 * (e % 2));
+    }
+    uint32_t* to = (uint32_t*)(out + R::key_at(p & 31, d));
+    if constexpr (BITS == 8) *(uint2*)to = make_uint2(w[0], w[1]);
+    else *to = w[0];
+  } else if constexpr (BITS == 8) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) out[R::codes + R::value_at(p & 31, d + e)] = (uint8_t)c[e];
+  } else {
+    // channels d .. d + 7 and d + 16 .. d + 23 share bytes
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const int other = __shfl_xor(c[e], 2, 64);
+      if (d % 32 < 16)
+        out[R::codes + R::value_at(p & 31, d + e)] = (uint8_t)(c[e] | other << 4);
+    }
+  }
+}
+
+template <typename T, int D, int BITS>
+__global__ __launch_bounds__(256) void read_rows(const CacheRowsLaunch a) {
+  using R = Record<D, BITS>;
+  constexpr int TH = D / 8;
+  const int64_t head = block_index() * (256 / TH) + threadIdx.x / TH;
+  const int d = (int)(threadIdx.x % TH) * 8;
+  const int of = (int)(head & 1);
+  const int t = (int)((head >> 1) / a.cache.heads), h = (int)((head >> 1) % a.cache.heads);
+  if (t >= a.batch.ntok) return;
+  const int s = find_sequence(a.batch, t);
+  if (s < 0) return;
+  const Seq q = sequence(a.batch, s);
+  const int p = q.len - (q.r1 - t);
+  const uint8_t* rec = p < 0 ? nullptr : record_of(a.cache, a.batch.table + s * a.batch.ldt,
+                                                   a.batch.width, p >> 5, h);
+  float x[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+  if (rec) {
+    const uint32_t word = ((const uint32_t*)(rec + R::words + of * 128))[p & 31];
+    const float step = word_step(word);
+    const int z = word_zero(word);
+    int c[8];
+    if (of == 0) {
+      const uint32_t* from = (const uint32_t*)(rec + R::key_at(p & 31, d));
+      uint32_t w[2] = {from[0], BITS == 8 ? from[1] : 0};
+#pragma unroll
+      for (int e = 0; e < 8; ++e)
+        c[e] = BITS == 8 ? (w[e / 4] >> (8 * (e % 4))) & 255
+                         : (w[0] >> (4 * (e / 2) + 16 * (e % 2))) & 15;
+    } else {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const int byte = rec[R::codes + R::value_at(p & 31, d + e)];
+        c[e] = BITS == 8 ? byte : (byte >> (d % 32 < 16 ? 0 : 4)) & 15;
+      }
+    }
+#pragma unroll
+    for (int e = 0; e < 8; ++e) x[e] = (float)(c[e] - z) * step;
+  }
+  const CacheTensor& dst = of ? a.v : a.k;
+  store8((T*)dst.p + t * dst.ts + h * dst.hs + d, x);
+}
+
+template <typename T, int D, int BITS>
+void launch_rows_of(const CacheRowsLaunch& a, bool write, hipStream_t st) {
+  const int64_t heads = (int64_t)a.batch.ntok * a.cache.heads * 2;
+  const dim3 grid = block_grid((heads * (D / 8) + 255) / 256);
+  if (write) write_rows<T, D, BITS><<<grid, 256, 0, st>>>(a);
+  else read_rows<T, D, BITS><<<grid, 256, 0, st>>>(a);
+}
+
+template <typename T, int D>
+void launch_bits(const CacheRowsLaunch& a, bool write, hipStream_t st) {
+  if (a.bits == 8) launch_rows_of<T, D, 8>(a, write, st);
+  else launch_rows_of<T, D, 4>(a, write, st);
+}
+
+template <typename T>
+void launch_dim(const CacheRowsLaunch& a, bool write, hipStream_t st) {
+  if (a.head_dim == 64) launch_bits<T, 64>(a, write, st);
+  else if (a.head_dim == 128) launch_bits<T, 128>(a, write, st);
+  else launch_bits<T, 256>(a, write, st);
+}
+
+hipError_t launch(const CacheRowsLaunch& a, bool write, hipStream_t st) {
+  if (a.batch.ntok == 0 || a.batch.nseq == 0) return hipSuccess;
+  if (a.dtype == PWQ_F32) launch_dim<float>(a, write, st);
+  else launch_dim<uint16_t>(a, write, st);
+  return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_cache_write(const CacheRowsLaunch& a, hipStream_t st) {
+  return launch(a, true, st);
+}
+hipError_t launch_cache_read(const CacheRowsLaunch& a, hipStream_t st) {
+  return launch(a, false, st);
+}
+
+}  // namespace pwq

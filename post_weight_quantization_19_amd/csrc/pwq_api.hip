@@ -1103,4 +1103,201 @@ pwq_status pwq_packed_linear(const void* x, int32_t xdtype, int64_t ntok, int64_
   return ok();
 }
 
+// ------------------------------------------------------------ key-value cache
+
+int64_t pwq_cache_record_bytes(int32_t head_dim, int32_t bits) {
+  if ((head_dim != 64 && head_dim != 128 && head_dim != 256) || (bits != 4 && bits != 8)) return 0;
+  return 8 * (int64_t)head_dim * bits + 256;
+}
+
+// A tensor ntok x heads x dim as rows of memory: a row per token where a token's
+// heads lie together, else one of everything.
+static Rows tensor_rows(const void* p, int64_t ntok, int64_t heads, int64_t dim, int64_t ts,
+                        int64_t hs, int32_t dtype) {
+  const int64_t width = (heads - 1) * hs + dim;
+  if (ts >= width) return Rows(p, ntok, width, ts, dtype);
+  return Rows(p, ntok > 0, (ntok - 1) * ts + width, 0, dtype);
+}
+// Whether all elements have places of their own (heads within tokens, or tokens
+// within heads).
+static bool distinct(int64_t ntok, int64_t heads, int64_t dim, int64_t ts, int64_t hs) {
+  if (ntok <= 1) return heads <= 1 || hs >= dim;
+  if (heads <= 1) return ts >= dim;
+  return (hs >= dim && ts >= (heads - 1) * hs + dim) || (ts >= dim && hs >= (ntok - 1) * ts + dim);
+}
+
+static pwq_status check_cache(const pwq_cache* c, const pwq_batch* b, int64_t ntok, int64_t heads,
+                              int32_t dtype) {
+  if (!c || !b) return fail(PWQ_ERR_INVALID_ARG, "cache and batch must be non-NULL");
+  if (!pwq_cache_record_bytes(c->head_dim, c->bits))
+    return fail(PWQ_ERR_UNSUPPORTED, "a cache has head_dim 64, 128 or 256 and 4 or 8 bits");
+  if (c->page < 32 || c->page > 4096 || (c->page & (c->page - 1)))
+    return fail(PWQ_ERR_INVALID_ARG, "page must be a power of two in 32 .. 4096");
+  if (c->kv_heads < 1 || c->pages < 0 || heads < 1 || heads % c->kv_heads)
+    return fail(PWQ_ERR_INVALID_ARG, "need kv_heads >= 1, pages >= 0, heads a multiple of kv_heads");
+  if (c->pages > ((int64_t)1 << 40) / c->kv_heads / (c->page / 32))
+    return fail(PWQ_ERR_INVALID_ARG, "more than 2^40 records");
+  if (dtype != PWQ_F32 && dtype != PWQ_BF16)
+    return fail(PWQ_ERR_INVALID_ARG, "tensors must be PWQ_F32 or PWQ_BF16");
+  if (ntok < 0 || ntok * 2 > INT32_MAX / heads)
+    return fail(PWQ_ERR_INVALID_ARG, "need ntok >= 0 and ntok * heads < 2^30");
+  if (b->nseq < 0 || b->width < 0 || b->ldt < b->width)
+    return fail(PWQ_ERR_INVALID_ARG, "need nseq >= 0 and ldt >= width >= 0");
+  if (ntok > 0 && b->nseq > 0) {
+    if (!b->starts || !b->lengths || (b->width > 0 && !b->table))
+      return fail(PWQ_ERR_INVALID_ARG, "starts, lengths and table must be non-NULL");
+    if (c->pages > 0 && (!c->records || (uintptr_t)c->records % 16))
+      return fail(PWQ_ERR_INVALID_ARG, "records must be non-NULL and 16-byte aligned");
+  }
+  return PWQ_OK;
+}
+
+static CacheView cache_view(const pwq_cache* c) {
+  int shift = 0;
+  while ((32 << shift) < c->page) ++shift;
+  return CacheView{(uint8_t*)c->records, c->pages, c->kv_heads, shift,
+                   pwq_cache_record_bytes(c->head_dim, c->bits)};
+}
+static CacheBatch cache_batch(const pwq_batch* b, int64_t ntok) {
+  return CacheBatch{b->starts, b->lengths, b->table, b->ldt, b->nseq, b->width, (int32_t)ntok, 1};
+}
+static Rows cache_rows(const pwq_cache* c) {
+  return Rows(c->records, 1, c->pages * c->kv_heads * (c->page / 32) *
+              pwq_cache_record_bytes(c->head_dim, c->bits), 0, PWQ_I8);
+}
+
+static pwq_status check_heads(const pwq_cache* c, const void* k, int64_t kts, int64_t khs,
+                              const void* v, int64_t vts, int64_t vhs, int64_t ntok) {
+  if (kts < 0 || khs < 0 || vts < 0 || vhs < 0)
+    return fail(PWQ_ERR_INVALID_ARG, "strides must be >= 0");
+  if (ntok > 0 && (!k || !v)) return fail(PWQ_ERR_INVALID_ARG, "k and v must be non-NULL");
+  return PWQ_OK;
+}
+
+pwq_status pwq_cache_write(const pwq_cache* cache, const pwq_batch* batch, const void* k,
+                           int64_t k_tstride, int64_t k_hstride, const void* v, int64_t v_tstride,
+                           int64_t v_hstride, int32_t dtype, int64_t ntok, void* stream) {
+  pwq_status s = check_cache(cache, batch, ntok, cache ? cache->kv_heads : 1, dtype);
+  if (s != PWQ_OK) return s;
+  s = check_heads(cache, k, k_tstride, k_hstride, v, v_tstride, v_hstride, ntok);
+  if (s != PWQ_OK) return s;
+  const int64_t heads = cache->kv_heads, dim = cache->head_dim;
+  const Rows rc = cache_rows(cache);
+  if (overlap(rc, tensor_rows(k, ntok, heads, dim, k_tstride, k_hstride, dtype)) ||
+      overlap(rc, tensor_rows(v, ntok, heads, dim, v_tstride, v_hstride, dtype)))
+    return fail(PWQ_ERR_INVALID_ARG, "the cache must not overlap k or v");
+  CacheRowsLaunch a{cache_view(cache), cache_batch(batch, ntok),
+                    {(void*)k, k_tstride, k_hstride}, {(void*)v, v_tstride, v_hstride},
+                    dtype, cache->head_dim, cache->bits};
+  const hipError_t e = launch_cache_write(a, (hipStream_t)stream);
+  if (e != hipSuccess) return hip_fail(e, "cache_write launch");
+  return ok();
+}
+
+pwq_status pwq_cache_read(const pwq_cache* cache, const pwq_batch* batch, void* k,
+                          int64_t k_tstride, int64_t k_hstride, void* v, int64_t v_tstride,
+                          int64_t v_hstride, int32_t dtype, int64_t ntok, void* stream) {
+  pwq_status s = check_cache(cache, batch, ntok, cache ? cache->kv_heads : 1, dtype);
+  if (s != PWQ_OK) return s;
+  s = check_heads(cache, k, k_tstride, k_hstride, v, v_tstride, v_hstride, ntok);
+  if (s != PWQ_OK) return s;
+  const int64_t heads = cache->kv_heads, dim = cache->head_dim;
+  if (!distinct(ntok, heads, dim, k_tstride, k_hstride) ||
+      !distinct(ntok, heads, dim, v_tstride, v_hstride))
+    return fail(PWQ_ERR_INVALID_ARG, "elements of k, or of v, share a place");
+  const Rows rk = tensor_rows(k, ntok, heads, dim, k_tstride, k_hstride, dtype);
+  const Rows rv = tensor_rows(v, ntok, heads, dim, v_tstride, v_hstride, dtype);
+  const Rows rc = cache_rows(cache);
+  if (overlap(rk, rv) || overlap(rc, rk) || overlap(rc, rv))
+    return fail(PWQ_ERR_INVALID_ARG, "k, v and the cache must not overlap");
+  CacheRowsLaunch a{cache_view(cache), cache_batch(batch, ntok), {k, k_tstride, k_hstride},
+                    {v, v_tstride, v_hstride}, dtype, cache->head_dim, cache->bits};
+  const hipError_t e = launch_cache_read(a, (hipStream_t)stream);
+  if (e != hipSuccess) return hip_fail(e, "cache_read launch");
+  return ok();
+}
+
+static AttentionLaunch attention_launch(const pwq_cache* cache, const pwq_batch* batch,
+                                        const pwq_batch* prefix, int32_t heads, int32_t dtype,
+                                        int64_t ntok) {
+  AttentionLaunch a{};
+  a.cache = cache_view(cache);
+  a.batch = cache_batch(batch, ntok);
+  if (prefix) a.prefix = cache_batch(prefix, ntok);
+  a.heads = heads, a.head_dim = cache->head_dim, a.bits = cache->bits, a.dtype = dtype;
+  return a;
+}
+
+static pwq_status check_attention(const pwq_cache* cache, const pwq_batch* batch,
+                                  const pwq_batch* prefix, int32_t heads, int32_t dtype,
+                                  int64_t ntok) {
+  pwq_status s = check_cache(cache, batch, ntok, heads, dtype);
+  if (s != PWQ_OK || !prefix) return s;
+  if (prefix->nseq != 1) return fail(PWQ_ERR_INVALID_ARG, "a prefix is one sequence");
+  pwq_batch p = *prefix;
+  p.starts = batch->starts;
+  if (batch->nseq == 0) p.nseq = 0;                // nothing is launched
+  return check_cache(cache, &p, ntok, heads, dtype);
+}
+
+static void* carve_attention(Carver& c, const AttentionPlan& p, void** prefix) {
+  void* own = c.take(p.own_bytes);
+  *prefix = p.prefix_bytes ? c.take(p.prefix_bytes) : nullptr;
+  return own;
+}
+
+size_t pwq_cached_attention_workspace_size(const pwq_cache* cache, const pwq_batch* batch,
+                                           const pwq_batch* prefix, int32_t heads, int32_t dtype,
+                                           int64_t ntok) {
+  if (!cache || !batch) return 0;
+  pwq_cache c = *cache;                            // no addresses are needed for a size
+  pwq_batch b = *batch;
+  c.records = (void*)16, b.starts = b.lengths = b.table = (const int32_t*)16;
+  pwq_batch p = prefix ? *prefix : b;
+  p.lengths = p.table = (const int32_t*)16;
+  if (check_attention(&c, &b, prefix ? &p : nullptr, heads, dtype, ntok) != PWQ_OK) return 0;
+  if (ntok == 0 || b.nseq == 0) return 0;
+  Carver carve(nullptr);
+  void* unused;
+  carve_attention(carve, attention_plan(attention_launch(&c, &b, prefix ? &p : nullptr, heads,
+                                                         dtype, ntok)), &unused);
+  return carve.size();
+}
+
+pwq_status pwq_cached_attention(const pwq_cache* cache, const pwq_batch* batch,
+                                const pwq_batch* prefix, const void* q, int64_t q_tstride,
+                                int64_t q_hstride, void* out, int64_t out_tstride,
+                                int64_t out_hstride, int32_t heads, int32_t dtype, int64_t ntok,
+                                double scale, int32_t causal, void* ws, size_t ws_bytes,
+                                void* stream) {
+  pwq_status s = check_attention(cache, batch, prefix, heads, dtype, ntok);
+  if (s != PWQ_OK) return s;
+  if (q_tstride < 0 || q_hstride < 0 || out_tstride < 0 || out_hstride < 0)
+    return fail(PWQ_ERR_INVALID_ARG, "strides must be >= 0");
+  if (ntok > 0 && (!q || !out)) return fail(PWQ_ERR_INVALID_ARG, "q and out must be non-NULL");
+  if (!((float)scale >= 1e-30f) || !((float)scale <= 1e30f))
+    return fail(PWQ_ERR_INVALID_ARG, "scale must be in 1e-30 .. 1e30");
+  const int64_t dim = cache->head_dim;
+  if (!distinct(ntok, heads, dim, out_tstride, out_hstride))
+    return fail(PWQ_ERR_INVALID_ARG, "elements of out share a place");
+  const Rows ro = tensor_rows(out, ntok, heads, dim, out_tstride, out_hstride, dtype);
+  if (overlap(ro, tensor_rows(q, ntok, heads, dim, q_tstride, q_hstride, dtype)) ||
+      overlap(ro, cache_rows(cache)))
+    return fail(PWQ_ERR_INVALID_ARG, "out must not overlap q or the cache");
+  if (ntok == 0 || batch->nseq == 0) return ok();
+  AttentionLaunch a = attention_launch(cache, batch, prefix, heads, dtype, ntok);
+  a.q = {(void*)q, q_tstride, q_hstride}, a.out = {out, out_tstride, out_hstride};
+  a.causal = causal != 0, a.scale = (float)scale;
+  const AttentionPlan p = attention_plan(a);
+  Carver measure(nullptr), carve(ws);
+  void* before;
+  carve_attention(measure, p, &before);
+  s = check_ws(ws, ws_bytes, measure.size());
+  if (s != PWQ_OK) return s;
+  void* own = carve_attention(carve, p, &before);
+  const hipError_t e = launch_cached_attention(a, p, own, before, (hipStream_t)stream);
+  if (e != hipSuccess) return hip_fail(e, "cached_attention launch");
+  return ok();
+}
+
 }  // extern "C"

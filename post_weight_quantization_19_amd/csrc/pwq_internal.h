@@ -6,6 +6,7 @@
 #include <stdint.h>
 
 #include "../../include/pwq.h"
+#include "../../include/pwq_cache.h"
 #include "../../include/pwq_serve.h"
 #include "pwq_device.h"
 
@@ -237,6 +238,51 @@ PromptPlan prompt_plan(const void* x, int32_t xdtype, int64_t ntok, int64_t ldx,
                        int64_t n, int32_t G, int64_t n_out);
 hipError_t launch_prompt(const PackedLinearLaunch& a, const PromptPlan& p, const PromptWs& w,
                          hipStream_t st);
+
+// The key-value cache (pwq_cache.h): a cache, a batch, and tensors of ntok x
+// heads x head_dim with strides in elements.
+struct CacheView {
+  uint8_t* records;
+  int64_t pages;
+  int32_t heads, blocks_shift;      // records of a page and head: 1 << blocks_shift
+  int64_t record_bytes;
+};
+struct CacheBatch {
+  const int32_t* starts;
+  const int32_t* lengths;
+  const int32_t* table;
+  int64_t ldt;
+  int32_t nseq, width, ntok;
+  int32_t starts_step;              // sequence s starts at starts[s * starts_step]
+};
+struct CacheTensor {
+  void* p;
+  int64_t ts, hs;
+};
+struct CacheRowsLaunch {
+  CacheView cache;
+  CacheBatch batch;
+  CacheTensor k, v;
+  int32_t dtype, head_dim, bits;
+};
+hipError_t launch_cache_write(const CacheRowsLaunch& a, hipStream_t st);
+hipError_t launch_cache_read(const CacheRowsLaunch& a, hipStream_t st);
+
+struct AttentionLaunch {
+  CacheView cache;
+  CacheBatch batch, prefix;         // prefix.nseq 0: none
+  CacheTensor q, out;
+  int32_t heads, head_dim, bits, dtype, causal;
+  float scale;
+};
+struct AttentionPlan {
+  int64_t workers;                  // workgroups per key head
+  int64_t items, prefix_items;      // at most, per key head
+  size_t own_bytes, prefix_bytes;   // partial results
+};
+AttentionPlan attention_plan(const AttentionLaunch& a);
+hipError_t launch_cached_attention(const AttentionLaunch& a, const AttentionPlan& p, void* own,
+                                   void* prefix, hipStream_t st);
 
 // Event pairs recorded around launches of one kernel (pwq_kernel_timer_attach).
 struct KernelTimer {

@@ -1,0 +1,552 @@
+"""The key-value cache's kernels against the fp64 oracle: codes and words bit for
+bit, what is read back exactly (bf16: rounded once), attention within bounds
+from the arithmetic.
+
+Attention's bound.  Per row, with A the largest scale * sum |q| |k| of a token it
+sees, W = sum w |v| of the normalised weights and n tokens:
+  scores    D float32 additions (2^-24 A each at most), four roundings of the score
+            and its factors, q in two parts (float32: 2^-22 A; bf16: exact)
+  exp       two units in the last place, and the exponent's rounding: 2^-24 times
+            the score in base 2, at most 1.45 A; weights are off by the error
+            of their score twice (numerator and sum)
+  weights   in one float16 part 2^-12 (bf16), two 2^-22 (float32); below 2^-14 of
+            256 times ref, where float16 is spaced 2^-24: 2^-33 ref, ref at most
+            the largest step, for each token, times a code of at most 255
+  sums      n / 16 + 64 float32 additions and rescalings in a row
+and the output is rounded once (bf16: 2^-8 of the value, a half of its spacing).
+"""
+import numpy as np
+import pytest
+import torch
+
+import oracle.cache_oracle as C
+import post_weight_quantization_19_amd as P
+
+pytestmark = pytest.mark.gpu
+
+DT = {"f32": torch.float32, "bf16": torch.bfloat16}
+
+
+def f64(t):
+    return t.detach().double().cpu().numpy()
+
+
+def batch_of(rng, lens, new, page, spare=2, extra=0, before=0, pages=0):
+    """(starts, lengths, table, pages): rows new[i], the sequences' pages in random
+    order; `before` rows of no sequence in front."""
+    need = [-(-n // page) for n in lens]
+    pages = pages or sum(need) + spare
+    order = rng.permutation(pages)
+    table = np.full((len(lens), max(need + [0]) + extra), -1, np.int32)
+    at = 0
+    for i, n in enumerate(need):
+        table[i, :n] = order[at:at + n]
+        at += n
+    starts = np.concatenate([[0], np.cumsum(new)]).astype(np.int32) + before
+    return starts, np.array(lens, np.int32), table, pages
+
+
+def up(*xs):
+    return [torch.from_numpy(np.ascontiguousarray(x)).cuda() for x in xs]
+
+
+def keys_values(rng, shape, dtype):
+    x = rng.standard_normal((2, *shape)) * np.exp(0.5 * rng.standard_normal(shape[-1]))
+    return [t.to(dtype) for t in up(*x.astype(np.float32))]
+
+
+def filled(rng, pages, heads, dim, bits, page):
+    """A cache of random records, and the records on the host."""
+    x = rng.standard_normal((pages, heads, page // 32, 2, 32, dim)).astype(np.float32)
+    x *= np.exp(0.4 * rng.standard_normal((heads, 1, 1, 1, dim))).astype(np.float32)
+    records = C.pack(*C.quantize(x, bits), dim, bits)
+    cache = P.new_cache(pages, heads, dim, bits, page)
+    cache["records"].copy_(torch.from_numpy(records))
+    return cache, records
+
+
+def rows_of(starts, lens, nseq):
+    """(row, sequence, token) of every row of a batch."""
+    return [(t, i, lens[i] - (starts[i + 1] - t)) for i in range(nseq)
+            for t in range(starts[i], starts[i + 1])]
+
+
+# ------------------------------------------------------------------ write and read
+
+BATCHES = [  # tokens of each sequence, new ones of each, page
+    ([1], [1], 32), ([33], [1], 32), ([1000], [1], 64), ([64, 1, 0, 31], [64, 1, 0, 31], 32),
+    ([70, 5, 200], [33, 2, 7], 32), ([129], [129], 128), ([40] * 70, [1] * 70, 32),
+    ([300, 0, 17], [90, 0, 17], 256), ([32, 64, 96], [32, 32, 32], 32), ([95, 63], [94, 60], 32),
+]
+
+
+@pytest.mark.parametrize("lens,new,page", BATCHES)
+@pytest.mark.parametrize("heads,dim,bits,dtype", [(2, 64, 8, "bf16"), (1, 128, 4, "bf16"),
+                                                  (3, 128, 8, "f32"), (2, 256, 4, "f32"),
+                                                  (5, 64, 4, "bf16"), (1, 256, 8, "bf16")])
+def test_write_and_read(lens, new, page, heads, dim, bits, dtype):
+    rng = np.random.default_rng(len(lens) * 1000 + dim + bits)
+    starts, lengths, table, pages = batch_of(rng, lens, new, page)
+    k, v = keys_values(rng, (sum(new), heads, dim), DT[dtype])
+    cache, before = filled(rng, pages, heads, dim, bits, page)
+    b = up(starts, lengths, table)
+    P.cache_write(k, v, cache, *b)
+    after = cache["records"].cpu().numpy()
+    want = [list(x) for x in (C.unpack(before, dim, bits),)][0]
+    for of, x in enumerate((k, v)):
+        c, s, z = C.quantize(x.float().cpu().numpy(), bits)
+        for t, i, p in rows_of(starts, lens, len(lens)):
+            at = (table[i, p // page], slice(None), p % page // 32, of, p % 32)
+            want[0][at], want[1][at], want[2][at] = c[t], s[t], z[t]
+    for got, exp, what in zip(C.unpack(after, dim, bits), want, ("codes", "steps", "zeros")):
+        assert np.array_equal(got, exp), what
+    # read back: exact in float32, rounded once in bf16
+    for out in ("f32", "bf16"):
+        got = P.cache_read(cache, *b, sum(new), dtype=DT[out])
+        for of, x in enumerate((k, v)):
+            val = torch.from_numpy(C.values(*C.quantize(x.float().cpu().numpy(), bits)))
+            assert torch.equal(got[of].cpu(), val.to(DT[out]))
+
+
+@pytest.mark.parametrize("bits", [4, 8])
+def test_ties_and_special_values(bits):
+    """Ties, NaN, infinities, zeros, the largest and the smallest values."""
+    rng = np.random.default_rng(3)
+    top, dim = 2 ** bits - 1, 64
+    x = np.zeros((24, 1, dim), np.float32)
+    x[0, 0] = np.arange(dim) / 2
+    x[0, 0, 0] = top
+    x[1, 0, :] = -np.arange(dim) / 2
+    x[1, 0, 0] = -top
+    x[2, 0, :] = np.arange(dim) - 20.5
+    x[3, 0, 5] = np.nan
+    x[4, 0, 5] = np.inf
+    x[5, 0, 5] = -np.inf
+    x[6, 0, :2] = 3e38, -3e38
+    x[7, 0, :] = 3.4028235e38 * rng.random(dim)
+    x[8, 0, :] = -3.4028235e38 * rng.random(dim)
+    for i, e in enumerate((-149, -146, -141, -140, -138, -133, -130, -126, -110, -100, -99, 100)):
+        x[9 + i, 0] = np.ldexp(rng.standard_normal(dim), e)
+    x[21, 0, 0], x[22, 0, 0] = 1e-45, -1e-45
+    x[23, 0] = 7.0
+    starts, lengths, table, pages = batch_of(rng, [24], [24], 32)
+    cache = P.new_cache(pages, 1, dim, bits, 32)
+    k, v = up(x, x[::-1])
+    P.cache_write(k, v, cache, *up(starts, lengths, table))
+    got = C.unpack(cache["records"][int(table[0, 0]), :, 0].cpu().numpy(), dim, bits)
+    for of, src in enumerate((x, x[::-1])):
+        c, s, z = C.quantize(src[:, 0], bits)
+        assert np.array_equal(got[0][0, of, :24], c)
+        assert np.array_equal(got[1][0, of, :24], s, equal_nan=True)
+        assert np.array_equal(got[2][0, of, :24], z)
+    back, _ = P.cache_read(cache, *up(starts, lengths, table), 24, dtype=torch.float32)
+    assert torch.isnan(back[3:7]).all() and not torch.isnan(back[7:]).any()
+
+
+def test_random_ties_bf16():
+    """bf16 heads whose quotients fall on ties often: small integers times 2^-k."""
+    rng = np.random.default_rng(11)
+    for bits in (4, 8):
+        x = rng.integers(-300, 301, (500, 2, 64)) * np.exp2(rng.integers(-9, 3, (500, 2, 1)))
+        x = torch.from_numpy(x.astype(np.float32)).bfloat16()
+        starts, lengths, table, pages = batch_of(rng, [500], [500], 64)
+        cache = P.new_cache(pages, 2, 64, bits, 64)
+        b = up(starts, lengths, table)
+        P.cache_write(x.cuda(), x.cuda(), cache, *b)
+        k, v = P.cache_read(cache, *b, 500, dtype=torch.float32)
+        want = torch.from_numpy(C.values(*C.quantize(x.float().numpy(), bits))).float()
+        assert torch.equal(k.cpu(), want) and torch.equal(v.cpu(), want)
+
+
+@pytest.mark.parametrize("bits", [4, 8])
+def test_rows_of_no_sequence_and_holes(bits):
+    """Rows before the first and behind the last sequence, tokens whose page is
+    none, lengths shorter than the rows: nothing else changes."""
+    rng = np.random.default_rng(5)
+    heads, dim, page = 2, 64, 32
+    lens, new = [70, 10, 40], [70, 20, 8]
+    starts, lengths, table, pages = batch_of(rng, lens, new, page, before=3)
+    table[0, 1], table[2, 1] = pages, -5            # tokens 32 .. 63; 32 .. 39
+    rows = sum(new) + 3 + 6
+    k, v = keys_values(rng, (rows, heads, dim), torch.float32)
+    cache, before = filled(rng, pages, heads, dim, bits, page)
+    b = up(starts, lengths, table)
+    P.cache_write(k, v, cache, *b)
+    want = C.unpack(before, dim, bits)
+    vals = [C.quantize(x.cpu().numpy(), bits) for x in (k, v)]
+    out = [np.full((rows, heads, dim), 7.0) for _ in range(2)]
+    for t, i, p in rows_of(starts, lens, 3):
+        for of in range(2):
+            out[of][t] = 0
+            if p < 0 or not 0 <= table[i, p // page] < pages:
+                continue
+            at = (table[i, p // page], slice(None), p % page // 32, of, p % 32)
+            for dst, src in zip(want, vals[of]):
+                dst[at] = src[t]
+            out[of][t] = C.values(*(x[t] for x in vals[of]))
+    for got, exp in zip(C.unpack(cache["records"].cpu().numpy(), dim, bits), want):
+        assert np.array_equal(got, exp)
+    dst = [torch.full((rows, heads, dim), 7.0, device="cuda") for _ in range(2)]
+    P.cache_read(cache, *b, rows, out=tuple(dst))
+    for got, exp in zip(dst, out):
+        assert np.array_equal(f64(got), exp)
+
+
+def test_strides():
+    """k and v as slices of one projection, outputs with heads outside tokens,
+    addresses of two bytes' alignment."""
+    rng = np.random.default_rng(6)
+    heads, dim, bits, rows = 3, 64, 8, 45
+    starts, lengths, table, pages = batch_of(rng, [45], [45], 32, extra=3)
+    wide = torch.from_numpy(rng.standard_normal((rows, 2 * heads * dim + 7)).astype(np.float32))
+    wide = wide.bfloat16().cuda()
+    k = wide[:, 1:1 + heads * dim].unflatten(1, (heads, dim))
+    v = wide[:, 1 + heads * dim:1 + 2 * heads * dim].unflatten(1, (heads, dim))
+    cache = P.new_cache(pages, heads, dim, bits, 32)
+    b = up(starts, lengths, table)
+    b[2] = torch.nn.functional.pad(b[2], (2, 1), value=99)[:, 2:-1]
+    P.cache_write(k, v, cache, *b)
+    ok = torch.zeros((heads, rows, dim), device="cuda").transpose(0, 1)
+    ov = torch.zeros((rows, heads, dim + 5), device="cuda")[:, :, 3:dim + 3]
+    P.cache_read(cache, *b, rows, out=(ok, ov))
+    for got, x in ((ok, k), (ov, v)):
+        assert np.array_equal(f64(got), C.values(*C.quantize(x.float().cpu().numpy(), bits)))
+
+
+# ------------------------------------------------------------------ attention
+
+def check_attention(y, q, records, b, dim, bits, page, scale=None, causal=True, prefix=None,
+                    pages=None):
+    starts, lens, table = b
+    scale = dim ** -0.5 if scale is None else scale
+    group = q.shape[1] // records.shape[1]
+    qn, got = f64(q), f64(y)
+    bf16 = q.dtype == torch.bfloat16
+    pre = C.stored(records, *prefix, dim, bits, page) if prefix else None
+    for i in range(len(lens)):
+        new = starts[i + 1] - starts[i]
+        if new == 0:
+            continue
+        k, v, there = C.stored(records, table[i], lens[i], dim, bits, page)
+        pos = np.arange(lens[i])
+        seen = there & ((pos <= (lens[i] - new + np.arange(new))[:, None]) if causal
+                        else np.ones((new, 1), bool))
+        if pre:
+            k, v = np.concatenate((pre[0], k), 1), np.concatenate((pre[1], v), 1)
+            seen = np.concatenate((np.broadcast_to(pre[2], (new, len(pre[2]))), seen), 1)
+        n = k.shape[1]
+        for h in range(q.shape[1]):
+            r = slice(starts[i], starts[i + 1])
+            want, size, score = C.attention(qn[r, h], k[h // group], v[h // group], scale, seen)
+            # v's largest step, from what it stands for
+            step = (v[h // group].max(-1, initial=0) - v[h // group].min(-1, initial=0)).max(
+                initial=0) / (2 ** bits - 1) * 1.02
+            off = score * ((dim + 4 + 1.45) * 2.0 ** -24 + (0 if bf16 else 2.0 ** -22))
+            rel = 2 * off + 2.0 ** -21 + (2.0 ** -12 if bf16 else 2.0 ** -22)
+            rel = rel + (n / 16 + 64) * 2.0 ** -24
+            tol = rel[:, None] * (size + np.abs(want)) + n * 2.0 ** -33 * step * 255
+            tol = tol * 1.01 + (2.0 ** -8 * 1.01 if bf16 else 2.0 ** -23) * np.abs(want)
+            err = np.abs(got[r, h] - want)
+            assert np.all(err <= tol), (i, h, float((err / np.maximum(tol, 1e-300)).max()),
+                                        float(err.max()))
+
+
+def queries(rng, rows, heads, dim, dtype, scale=1.5):
+    return torch.from_numpy((scale * rng.standard_normal((rows, heads, dim))).astype(
+        np.float32)).to(DT[dtype]).cuda()
+
+
+ATTENTION = [  # tokens, new ones, page
+    ([1], [1], 32), ([31], [1], 32), ([513], [1], 64), ([2000], [1], 256), ([5, 33, 64], [5, 1, 3], 32),
+    ([100, 0, 7, 300], [3, 0, 7, 1], 64), ([77], [77], 32), ([200, 129], [130, 129], 128),
+    ([10, 10], [1, 2], 32), ([40] * 300, [1] * 300, 32), ([700, 1], [20, 1], 32),
+]
+HEADS = [  # query heads, key heads, dim, bits, type
+    (4, 1, 128, 8, "bf16"), (4, 2, 64, 4, "bf16"), (7, 1, 64, 8, "f32"), (2, 2, 128, 4, "f32"),
+    (6, 2, 256, 8, "bf16"), (3, 3, 256, 4, "bf16"), (17, 1, 128, 8, "bf16"), (2, 1, 256, 8, "f32"),
+]
+
+
+@pytest.mark.parametrize("lens,new,page", ATTENTION)
+@pytest.mark.parametrize("heads,kv_heads,dim,bits,dtype", HEADS)
+def test_attention(lens, new, page, heads, kv_heads, dim, bits, dtype):
+    rng = np.random.default_rng(sum(lens) + dim + heads)
+    if len(lens) > 100 and dim > 64:
+        lens, new = lens[:40], new[:40]                  # time of the oracle
+    b = batch_of(rng, lens, new, page)
+    cache, records = filled(rng, b[3], kv_heads, dim, bits, page)
+    q = queries(rng, sum(new), heads, dim, dtype)
+    y = P.cached_attention(q, cache, *up(*b[:3]))
+    check_attention(y, q, records, b[:3], dim, bits, page)
+
+
+@pytest.mark.parametrize("lens,new,page", [([40, 3], [2, 3], 32), ([300], [70], 64)])
+def test_attention_to_all_tokens(lens, new, page):
+    rng = np.random.default_rng(1)
+    b = batch_of(rng, lens, new, page)
+    cache, records = filled(rng, b[3], 2, 64, 8, page)
+    q = queries(rng, sum(new), 6, 64, "f32")
+    y = P.cached_attention(q, cache, *up(*b[:3]), causal=False, scale=0.3)
+    check_attention(y, q, records, b[:3], 64, 8, page, causal=False, scale=0.3)
+
+
+@pytest.mark.parametrize("before", [0, 1, 32, 100, 1500])
+@pytest.mark.parametrize("heads,kv_heads,dim,bits,dtype", HEADS)
+def test_attention_with_prefix(before, heads, kv_heads, dim, bits, dtype):
+    rng = np.random.default_rng(before + dim)
+    lens, new, page = [3, 65, 1, 40, 0], [3, 1, 1, 30, 0], 32
+    starts, lengths, table, pages = batch_of(rng, lens, new, page, spare=before // page + 3)
+    used = set(table.ravel())
+    free = np.array([p for p in range(pages) if p not in used], np.int32)[:-(-before // page) + 1]
+    cache, records = filled(rng, pages, kv_heads, dim, bits, page)
+    q = queries(rng, sum(new), heads, dim, dtype)
+    y = P.cached_attention(q, cache, *up(starts, lengths, table),
+                           prefix=tuple(up(free, np.array([before], np.int32))))
+    check_attention(y, q, records, (starts, lengths, table), dim, bits, page,
+                    prefix=(free, before))
+
+
+def test_rows_without_tokens_and_holes():
+    """Rows that see nothing give 0; holes are left out; rows of no sequence keep
+    what is there."""
+    rng = np.random.default_rng(2)
+    lens, new, page = [2, 100, 0, 64], [5, 1, 2, 1], 32
+    starts, lengths, table, pages = batch_of(rng, lens, new, page, before=2)
+    table[1, 1], table[3] = -1, 10 ** 6
+    cache, records = filled(rng, pages, 2, 64, 8, page)
+    rows = sum(new) + 2 + 3
+    q = queries(rng, rows, 4, 64, "f32")
+    out = torch.full((rows, 4, 64), 5.0, device="cuda")
+    y = P.cached_attention(q, cache, *up(starts, lengths, table), out=out)
+    assert y is out
+    check_attention(y, q, records, (starts, lengths, table), 64, 8, page)
+    assert (y[:2] == 5).all() and (y[-3:] == 5).all()
+    assert not y[2:5].any() and y[5:7].any() and not y[8:11].any()
+
+
+def test_nan_and_infinity():
+    """A NaN query, and a token that reads as NaN: the rows that see it and no
+    others."""
+    rng = np.random.default_rng(4)
+    lens, new, page = [90], [40], 32
+    b = batch_of(rng, lens, new, page)
+    cache, records = filled(rng, b[3], 1, 64, 8, page)
+    starts, lengths, table = up(*b[:3])
+    k, v = keys_values(rng, (10, 1, 64), torch.float32)
+    k[3, 0, 7] = float("inf")            # token 83, seen by rows 33 .. 39
+    v[5, 0, 9] = float("nan")            # token 85
+    P.cache_write(k, v, cache, up(np.array([0, 10], np.int32))[0], lengths, table)
+    records = cache["records"].cpu().numpy()
+    q = queries(rng, 40, 2, 64, "bf16")
+    q[4, 1, 3] = float("nan")
+    q[6, 0, 3] = float("-inf")
+    y = P.cached_attention(q, cache, starts, lengths, table)
+    bad = torch.zeros((40, 2), dtype=torch.bool)
+    bad[33:] = True
+    bad[4, 1] = bad[6, 0] = True
+    assert torch.equal(torch.isnan(y).any(-1).cpu(), bad)
+    assert torch.equal(torch.isnan(y).all(-1).cpu(), bad)
+    clean = torch.where(bad[:, :, None].cuda(), 0.0, q.float()).bfloat16()
+    ok = P.cached_attention(clean, cache, starts, lengths, table)
+    assert torch.equal(torch.where(bad[:, :, None].cuda(), 0, y)[:33],
+                       torch.where(bad[:, :, None].cuda(), 0, ok)[:33])
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_values_of_very_different_sizes(dtype):
+    """Steps of the values that grow and shrink by powers of ten along a sequence,
+    and scores that leave one token."""
+    rng = np.random.default_rng(8)
+    n, page = 1000, 64
+    b = batch_of(rng, [n], [2], page)
+    cache = P.new_cache(b[3], 1, 64, 8, page)
+    k, v = keys_values(rng, (n, 1, 64), torch.float32)
+    v *= torch.from_numpy(10.0 ** rng.integers(-9, 10, n)).float().cuda()[:, None, None]
+    v[300:400] = 0
+    P.cache_write(k, v, cache, up(np.array([0, n], np.int32))[0], *up(*b[1:3]))
+    records = cache["records"].cpu().numpy()
+    for size in (1.0, 40.0):
+        q = queries(rng, 2, 3, 64, dtype, size)
+        y = P.cached_attention(q, cache, *up(*b[:3]))
+        check_attention(y, q, records, b[:3], 64, 8, page)
+
+
+def test_queries_of_very_different_sizes():
+    rng = np.random.default_rng(9)
+    b = batch_of(rng, [200], [6], 32)
+    cache, records = filled(rng, b[3], 1, 128, 4, 32)
+    for dtype in ("bf16", "f32"):
+        q = queries(rng, 6, 4, 128, "f32")
+        q *= torch.tensor([1e-38, 1e-20, 1e-3, 1.0, 8.0, 30.0], device="cuda")[:, None, None]
+        q[5, 0], q[0, 1] = 0, 0
+        q = q.to(DT[dtype])
+        y = P.cached_attention(q, cache, *up(*b[:3]))
+        check_attention(y, q, records, b[:3], 128, 4, 32)
+
+
+def test_strided_queries_and_output():
+    rng = np.random.default_rng(10)
+    b = batch_of(rng, [50, 9], [20, 9], 32)
+    cache, records = filled(rng, b[3], 2, 64, 8, 32)
+    wide = torch.from_numpy(rng.standard_normal((29, 4 * 64 * 2 + 3)).astype(np.float32))
+    wide = wide.bfloat16().cuda()
+    keep = wide.clone()
+    q = wide[:, 3:3 + 256].unflatten(1, (4, 64))
+    out = wide[:, 3 + 256:].unflatten(1, (4, 64))        # beside q, in the same rows
+    y = P.cached_attention(q, cache, *up(*b[:3]), out=out)
+    check_attention(y, q, records, b[:3], 64, 8, 32)
+    assert torch.equal(wide[:, :3 + 256], keep[:, :3 + 256])
+    y2 = torch.zeros((4, 29, 64), device="cuda", dtype=torch.bfloat16).transpose(0, 1)
+    P.cached_attention(q.clone(), cache, *up(*b[:3]), out=y2)
+    assert torch.equal(y2, y)
+
+
+def test_same_results_again():
+    rng = np.random.default_rng(12)
+    b = batch_of(rng, [3000, 17, 900], [1, 4, 2], 64)
+    cache, _ = filled(rng, b[3], 2, 64, 4, 64)
+    q = queries(rng, 7, 8, 64, "bf16")
+    args = up(*b[:3])
+    y = P.cached_attention(q, cache, *args)
+    for _ in range(5):
+        assert torch.equal(P.cached_attention(q, cache, *args), y)
+
+
+# ------------------------------------------------------------------ together
+
+def test_together_as_in_a_model():
+    """A prompt in two chunks, then tokens one by one behind a shared prefix:
+    written, attended to, read back."""
+    rng = np.random.default_rng(13)
+    heads, kv_heads, dim, bits, page = 4, 2, 64, 8, 32
+    cache = P.new_cache(24, kv_heads, dim, bits, page)
+    order = rng.permutation(24).astype(np.int32)
+    pre, table = order[:3], order[3:].reshape(3, 7)
+    kp, vp = keys_values(rng, (80, kv_heads, dim), torch.bfloat16)
+    one = lambda *x: up(*(np.array(v, np.int32) for v in x))
+    P.cache_write(kp, vp, cache, *one([0, 80], [80]), *up(pre[None]))
+    prefix = (up(pre)[0], one([80])[0])
+    have = np.zeros(3, np.int32)
+    for new in ([40, 7, 33], [20, 0, 64], [1, 1, 1], [1, 1, 1], [3, 2, 1]):
+        have += np.array(new, np.int32)
+        starts = np.concatenate([[0], np.cumsum(new)]).astype(np.int32)
+        k, v = keys_values(rng, (sum(new), kv_heads, dim), torch.bfloat16)
+        q = queries(rng, sum(new), heads, dim, "bf16")
+        args = up(starts, have, table)
+        P.cache_write(k, v, cache, *args)
+        y = P.cached_attention(q, cache, *args, prefix=prefix)
+        records = cache["records"].cpu().numpy()
+        check_attention(y, q, records, (starts, have, table), dim, bits, page, prefix=(pre, 80))
+        ks, _ = P.cache_read(cache, *args, sum(new), dtype=torch.float32)
+        assert np.array_equal(f64(ks), C.values(*C.quantize(k.float().cpu().numpy(), bits)))
+
+
+def test_captured_graph_with_other_batches():
+    """A captured write and attention, replayed with other tokens, lengths, pages
+    and fewer sequences; another graph and eager calls in between."""
+    rng = np.random.default_rng(14)
+    heads, kv_heads, dim, bits, page, most = 4, 1, 64, 8, 32, 6
+    cache, _ = filled(rng, 40, kv_heads, dim, bits, page)
+    starts = torch.zeros(most + 1, dtype=torch.int32, device="cuda")
+    lengths = torch.zeros(most, dtype=torch.int32, device="cuda")
+    table = torch.full((most, 6), -1, dtype=torch.int32, device="cuda")
+    q = torch.zeros((most, heads, dim), device="cuda")
+    k = torch.zeros((most, kv_heads, dim), device="cuda")
+    v = torch.zeros_like(k)
+    out = torch.zeros_like(q)
+
+    def step():
+        P.cache_write(k, v, cache, starts, lengths, table)
+        P.cached_attention(q, cache, starts, lengths, table, out=out)
+
+    graphs = []
+    for _ in range(2):
+        stream = torch.cuda.Stream()
+        stream.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(stream):
+            step()
+        torch.cuda.current_stream().wait_stream(stream)
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            step()
+        graphs.append(g)
+    for turn in range(6):
+        n = int(rng.integers(1, most + 1))
+        lens = rng.integers(1, 180, n)
+        st, ln, tb, _ = batch_of(rng, list(lens), [1] * n, page, pages=40)
+        starts.fill_(n)
+        starts[:n + 1].copy_(torch.from_numpy(st))
+        lengths.zero_()
+        lengths[:n].copy_(torch.from_numpy(ln))
+        table.fill_(-1)
+        table[:n, :tb.shape[1]].copy_(torch.from_numpy(tb))
+        for x in (q, k, v):
+            x.copy_(torch.from_numpy(rng.standard_normal(tuple(x.shape)).astype(np.float32)))
+        out.fill_(9)
+        torch.cuda.synchronize()
+        graphs[turn % 2].replay()
+        torch.cuda.synchronize()
+        records = cache["records"].cpu().numpy()
+        check_attention(out[:n], q[:n], records, (st, ln, tb), dim, bits, page)
+        assert (out[n:] == 9).all()
+        eager = P.cached_attention(q, cache, starts, lengths, table)
+        assert torch.equal(eager[:n], out[:n])
+
+
+def test_another_stream():
+    rng = np.random.default_rng(15)
+    b = batch_of(rng, [400, 30], [1, 1], 32)
+    cache, records = filled(rng, b[3], 1, 128, 4, 32)
+    q = queries(rng, 2, 4, 128, "bf16")
+    args = up(*b[:3])
+    want = P.cached_attention(q, cache, *args)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        got = [P.cached_attention(q, cache, *args) for _ in range(4)]
+    here = [P.cached_attention(q, cache, *args) for _ in range(4)]
+    torch.cuda.synchronize()
+    assert all(torch.equal(y, want) for y in got + here)
+
+
+# ------------------------------------------------------------------ refusals
+
+def test_binding_refusals():
+    cache = P.new_cache(4, 2, 64, 8, 32)
+    i32 = lambda *x: torch.tensor(x, dtype=torch.int32, device="cuda")
+    b = (i32(0, 2), i32(2), i32(0)[None])
+    k = torch.zeros((2, 2, 64), device="cuda")
+    P.cache_write(k, k, cache, *b)
+    q = torch.zeros((2, 4, 64), device="cuda")
+    P.cached_attention(q, cache, *b)
+    for args in ((k, k.bfloat16()), (k, k[:1]), (k[:, :1], k[:, :1]), (k.half(), k.half()),
+                 (k.cpu(), k.cpu()), (k, k.cpu()), (k[0], k[0]),
+                 (k.transpose(1, 2).contiguous().transpose(1, 2), k)):
+        with pytest.raises((ValueError, TypeError)):
+            P.cache_write(*args, cache, *b)
+    for bad in ((b[0].long(), *b[1:]), (b[0][:1], *b[1:]), (b[0], b[1].float(), b[2]),
+                (*b[:2], b[2][0]), (*b[:2], b[2].long()), (b[0].cpu(), *b[1:]),
+                (*b[:2], b[2].cpu())):
+        with pytest.raises((ValueError, TypeError)):
+            P.cache_write(k, k, cache, *bad)
+        with pytest.raises((ValueError, TypeError)):
+            P.cached_attention(q, cache, *bad)
+        with pytest.raises((ValueError, TypeError)):
+            P.cache_read(cache, *bad, 2)
+    for change in (dict(bits=4), dict(head_dim=128), dict(page=64), dict(page=48),
+                   dict(records=cache["records"].cpu()), dict(records=cache["records"][0]),
+                   dict(records=cache["records"].view(torch.int8))):
+        with pytest.raises((ValueError, P.PwqError)):
+            P.cached_attention(q, {**cache, **change}, *b)
+    for kw in (dict(scale=0.0), dict(scale=float("nan")), dict(out=q), dict(out=q[:1]),
+               dict(out=q.bfloat16()), dict(prefix=(i32(0), i32(1, 2))),
+               dict(prefix=(i32(0).long(), i32(1))), dict(prefix=(i32(0)[None], i32(1)))):
+        with pytest.raises((ValueError, TypeError, P.PwqError)):
+            P.cached_attention(q, cache, *b, **kw)
+    with pytest.raises((ValueError, P.PwqError)):
+        P.cached_attention(torch.zeros((2, 3, 64), device="cuda"), cache, *b)
+    for t in (q.requires_grad_(),):
+        with pytest.raises(ValueError):
+            P.cached_attention(t, cache, *b)
+        with torch.no_grad():
+            P.cached_attention(t, cache, *b)
