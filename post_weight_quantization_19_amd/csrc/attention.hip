@@ -18,9 +18,22 @@
 namespace pwq {
 namespace {
 
+// Native vectors: what is stored as one type and loaded as another goes through
+// these, which alias everything.
+typedef uint32_t u32x2_t __attribute__((ext_vector_type(2)));
+typedef uint32_t u32x4_t __attribute__((ext_vector_type(4)));
+
 constexpr int kRows = 16;              // rows of an item: query heads of a sequence's tokens
 constexpr int kTile = 128;             // tokens of a tile: 32 for each of the four waves
 constexpr float kNone = -__builtin_inff();
+
+// Between LDS writes of a wave's lanes and reads by its other lanes: the LDS takes a
+// wave's accesses in order, but the compiler must be told that they meet.
+__device__ __forceinline__ void wave_meets() {
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+}
 
 __device__ __forceinline__ f32x4_t mfma(f16x8_t a, f16x8_t b, f32x4_t c) {
   return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0);
@@ -56,12 +69,51 @@ __device__ __forceinline__ uint32_t bias4(int z0, int z1) {
   return 0xd400d400u | (uint32_t)(z0 & 15) << 4 | (uint32_t)(z1 & 15) << 20;
 }
 
-// The rows of an item.
-struct Item {
-  int seq, first;          // row `first` of the sequence's (r1 - r0) * group rows
-  Seq s;
-  int keys;                // tokens that any row sees, within the table
-};
+// Weights of a record's tokens 4 g + i (x[i]) and 16 + 4 g + i (x[4 + i]) in the order of
+// a value fragment; x becomes what float16 leaves of it.  (REST: x is held in a register
+// first.  Where the compiler sees the product that x is, it rounds it to float16 twice,
+// once through float32 and once not, and loses a last place of the first part.)
+template <int BITS, bool REST>
+__device__ __forceinline__ uint4 weight_part(float (&x)[8]) {
+  constexpr int B = BITS == 8 ? 1 : 2, C = BITS == 8 ? 2 : 1;
+  if constexpr (REST)
+#pragma unroll
+    for (int i = 0; i < 8; ++i) pin(x[i]);
+  uint32_t w[4];
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const int a = k / 2 * 4 + (k % 2 ? C : 0), b = k / 2 * 4 + (k % 2 ? 3 : B);
+    w[k] = two_halves(x[a], x[b]);
+    const f16x2_t h = as_half2(w[k]);
+    x[a] -= (float)h[0], x[b] -= (float)h[1];
+  }
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+struct __attribute__((packed, aligned(1))) any16 { uint32_t v[4]; };
+struct __attribute__((packed, aligned(1))) any8 { uint32_t v[2]; };
+// Eight elements of q in float32, and four of out (any alignment).
+__device__ __forceinline__ void load_row8(const float* p, float (&x)[8]) {
+  const any16 a = ((const any16*)p)[0], b = ((const any16*)p)[1];
+#pragma unroll
+  for (int e = 0; e < 4; ++e) x[e] = __uint_as_float(a.v[e]), x[4 + e] = __uint_as_float(b.v[e]);
+}
+__device__ __forceinline__ void load_row8(const uint16_t* p, float (&x)[8]) {
+  const any16 a = *(const any16*)p;
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    x[2 * e] = __uint_as_float(a.v[e] << 16);
+    x[2 * e + 1] = __uint_as_float(a.v[e] & 0xffff0000u);
+  }
+}
+__device__ __forceinline__ void store_row4(float* p, const float (&y)[4]) {
+  *(any16*)p = any16{{__float_as_uint(y[0]), __float_as_uint(y[1]), __float_as_uint(y[2]),
+                      __float_as_uint(y[3])}};
+}
+__device__ __forceinline__ void store_row4(uint16_t* p, const float (&y)[4]) {
+  const __bf16 v[4] = {(__bf16)y[0], (__bf16)y[1], (__bf16)y[2], (__bf16)y[3]};
+  *(any8*)p = __builtin_bit_cast(any8, v);
+}
 
 // Partial results: a slot has 16 rows of D sums, then 16 maxima, then 16 totals.
 template <int D> constexpr int kSlot = kRows * (D + 2);
@@ -79,7 +131,7 @@ struct Walk {
   }
 };
 
-// Sums over the workgroup's 256 threads of two numbers; before: the sums of the
+// Sums over the workgroup's first 256 threads of two numbers (others give 0); before: the sums of the
 // threads before this one.
 __device__ __forceinline__ void scan2(int64_t a, int64_t b, int64_t* before_a, int64_t* before_b,
                                       int64_t* all_a, int64_t* all_b, int64_t (*red)[2]) {
@@ -109,7 +161,7 @@ struct Place {
   int64_t item, tile;      // first item and first tile of the sequence
 };
 struct Scan {
-  int64_t red[4][2];
+  int64_t red[8][2];
   int64_t found[3];
 };
 // Total tiles of a key head.
@@ -331,7 +383,7 @@ __global__ __launch_bounds__(256) void attend_rows(const RowsArgs a) {
       m = next;
       uint4 pf[PARTS];
       {
-        float x[8], y[8];
+        float x[8];
 #pragma unroll
         for (int t = 0; t < 2; ++t)
 #pragma unroll
@@ -341,17 +393,8 @@ __global__ __launch_bounds__(256) void attend_rows(const RowsArgs a) {
             const bool seen = p0 + 16 * t + 4 * g + i < visible;
             x[4 * t + i] = seen ? e * (word_step(vx[t][i]) * inv_ref) : 0.0f;
           }
-        // the order of a value fragment's tokens
-        constexpr int B = BITS == 8 ? 1 : 2, C = BITS == 8 ? 2 : 1;
 #pragma unroll
-        for (int part = 0; part < PARTS; ++part) {
-#pragma unroll
-          for (int e = 0; e < 8; ++e) y[e] = (float)(_Float16)x[e];
-          pf[part] = make_uint4(two_halves(x[0], x[B]), two_halves(x[C], x[3]),
-                                two_halves(x[4], x[4 + B]), two_halves(x[4 + C], x[7]));
-#pragma unroll
-          for (int e = 0; e < 8; ++e) x[e] -= y[e];
-        }
+        for (int part = 0; part < PARTS; ++part) pf[part] = weight_part<BITS, PARTS == 2>(x);
       }
       // values
       uint32_t z0[4], z4[4];
@@ -434,35 +477,576 @@ __global__ __launch_bounds__(256) void attend_rows(const RowsArgs a) {
   }
 }
 
+struct TilesArgs {
+  CacheView cache;
+  CacheBatch batch;
+  CacheTensor q, out;
+  int group, heads, causal, capacity;
+  int64_t splits, items;
+  float scale;
+  float* slots;            // NULL: one split, results written to out
+};
+
+// The sequence of an item (in units of ROWS rows), and the item's number in it; -1
+// past the last.
+template <int ROWS>
+__device__ __forceinline__ int64_t items_of(const Seq& q, int group) {
+  return ((int64_t)(q.r1 - q.r0) * group + ROWS - 1) / ROWS;
+}
+template <int ROWS>
+__device__ __forceinline__ int find_item(const CacheBatch& b, int group, int64_t item, int* in,
+                                         Scan& sc) {
+  if (threadIdx.x == 0) sc.found[0] = -1;
+  int64_t before = 0;
+  for (int base = 0; base < b.nseq; base += 256) {
+    const int s = threadIdx.x < 256 ? base + (int)threadIdx.x : b.nseq;
+    const int64_t n = s < b.nseq ? items_of<ROWS>(sequence(b, s), group) : 0;
+    int64_t at, unused, all, none;
+    scan2(n, 0, &at, &unused, &all, &none, sc.red);
+    at += before;
+    if (item >= at && item < at + n) sc.found[0] = s, sc.found[1] = item - at;
+    before += all;
+  }
+  __syncthreads();
+  *in = (int)sc.found[1];
+  return (int)sc.found[0];
+}
+
+__device__ __forceinline__ float wave_top(float v) {
+#pragma unroll
+  for (int o = 32; o >= 1; o >>= 1) v = fmaxf(v, __shfl_xor(v, o, 64));
+  return v;
+}
+
+// Attention of 128 RT rows, 16 RT to each of eight waves: all waves take the same
+// records of 32 tokens one after the other, spread to float16 by the workgroup once and
+// kept in LDS as fragments.  The waves of a SIMD, w and w + 4, take turns: one
+// multiplies (values of the record before, keys of this) while the other turns its
+// scores into weights and spreads its share of the record after next.
+template <typename T, int D, int BITS, int RT>
+__global__ __launch_bounds__(512, 1) void attend_tiles(const TilesArgs a) {
+  using R = Record<D, BITS>;
+  constexpr int PARTS = std::is_same_v<T, float> ? 2 : 1;
+  constexpr int J = D / 32, N = D / 16, WAVES = 8, ROWS = 16 * RT * WAVES;
+  constexpr int REGION = R::codes / 1024;      // pieces of 1 KB of a record's keys (or values)
+  constexpr int PIECES = (2 * REGION + WAVES - 1) / WAVES;    // 16-byte pieces of a thread
+  constexpr int FR = BITS == 8 ? 2 : 4;        // fragments of a piece
+  // A weight is held as 2^8 of them (up to 2^12), a value's step over ref as kUnit (up to
+  // 8 kUnit, which times 255 has to stay in float16 where the steps are folded in).
+  constexpr float kUnit = PARTS == 1 ? 32.0f : 1.0f;
+  __shared__ Scan sc;
+  __shared__ float tops[WAVES];
+  __shared__ uint4 frags[4][2 * J + N][64];    // [record % 4][keys (t, j), values n]
+  __shared__ __align__(16) float step_k[4][32];      // keys' steps times f
+  __shared__ __align__(16) float step_v[4][32];      // values' steps, PARTS 2
+  // A wave's own: table entries, the words of the record that it spreads.
+  __shared__ int entries[WAVES][64];
+  __shared__ __align__(16) uint32_t words[WAVES][64];
+  __shared__ __align__(16) _Float16 step_h[WAVES][32];   // values' steps, PARTS 1: a wave's own
+  const int h = (int)(block_index() % a.cache.heads);
+  const int64_t rest = block_index() / a.cache.heads;
+  const int64_t split = rest % a.splits, item = a.items - 1 - rest / a.splits;
+  if (item < 0) return;
+  int in;
+  const int s = find_item<ROWS>(a.batch, a.group, item, &in, sc);
+  if (s < 0) return;
+  const int lane = threadIdx.x & 63, g = lane >> 4, col = lane & 15;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6) & 7;
+  const Seq q = sequence(a.batch, s);
+  const int rows = (int)min((int64_t)ROWS, (int64_t)(q.r1 - q.r0) * a.group - (int64_t)in * ROWS);
+  const int first = in * ROWS;
+  const int held = a.cache.pages > 0 ? min(q.len, a.capacity) : 0;
+  auto visible_of = [&](int row) {               // tokens that a row of the item sees
+    return min(held, a.causal ? q.len - (q.r1 - q.r0) + (first + row) / a.group + 1 : q.len);
+  };
+  const int most = max(visible_of(rows - 1), 0);
+  const int records = (most + 31) / 32;
+  const int i0 = (int)(records * split / a.splits), i1 = (int)(records * (split + 1) / a.splits);
+
+  // queries: this wave's rows, all rows scaled alike
+  f16x8_t qf[RT][PARTS][J];
+  int visible[RT];
+  float f;
+  {
+    float top = 0.0f;
+    bool bad[RT];
+    const T* src[RT];
+#pragma unroll
+    for (int rt = 0; rt < RT; ++rt) {
+      const int row = min((rt * WAVES + wave) * 16 + col, rows - 1);
+      visible[rt] = visible_of(row);
+      const int r = first + row;
+      src[rt] = (const T*)a.q.p + (int64_t)(q.r0 + r / a.group) * a.q.ts +
+                (int64_t)(h * a.group + r % a.group) * a.q.hs + 8 * g;
+      float mine = 0.0f;
+#pragma unroll
+      for (int j = 0; j < J; ++j) {
+        float x[8];
+        load_row8(src[rt] + 32 * j, x);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          mine = fmaxf(mine, fabsf(x[e]));
+          if (x[e] != x[e]) mine = __builtin_inff();
+        }
+      }
+      mine = fmaxf(mine, __shfl_xor(mine, 16, 64));
+      mine = fmaxf(mine, __shfl_xor(mine, 32, 64));
+      bad[rt] = !(mine <= __FLT_MAX__);
+      if (!bad[rt]) top = fmaxf(top, mine);
+    }
+    top = wave_top(top);
+    __syncthreads();
+    if (lane == 0) tops[wave] = top;
+    __syncthreads();
+    top = tops[0];
+#pragma unroll
+    for (int i = 1; i < WAVES; ++i) top = fmaxf(top, tops[i]);
+    const int field = max(min(267 - (int)(__float_as_uint(top) >> 23), 253), 1);
+    const float up = __uint_as_float((uint32_t)field << 23);
+    f = __uint_as_float((uint32_t)(254 - field) << 23) * a.scale * 1.44269504088896340736f;
+#pragma unroll
+    for (int rt = 0; rt < RT; ++rt)
+#pragma unroll
+      for (int j = 0; j < J; ++j) {
+        float x[8];
+        load_row8(src[rt] + 32 * j, x);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const float v = bad[rt] ? __builtin_nanf("") : x[e] * up;
+          const _Float16 hi = (_Float16)v;
+          qf[rt][0][j][e] = hi;
+          if constexpr (PARTS == 2) qf[rt][1][j][e] = (_Float16)(v - (float)hi);
+        }
+      }
+  }
+  const int least = __builtin_amdgcn_readfirstlane(visible[0]);   // the first row sees least
+
+  // ---- staging
+  // The record of a block.  Table entries come 64 at a time.
+  const int32_t* table = a.batch.table + s * a.batch.ldt;
+  int entries_from = -64;
+  auto record = [&](int block) __attribute__((always_inline)) -> const uint8_t* {  // NULL: a hole
+    const int entry = block >> a.cache.blocks_shift;
+    if (entry - entries_from >= 64) {
+      entries_from = entry & ~63;
+      wave_meets();
+      entries[wave][lane] = entries_from + lane < a.batch.width ? table[entries_from + lane] : -1;
+      wave_meets();
+    }
+    const int page = __builtin_amdgcn_readfirstlane(entries[wave][entry - entries_from]);
+    if (page < 0 || page >= a.cache.pages) return nullptr;
+    const int64_t at = ((int64_t)page * a.cache.heads + h) << a.cache.blocks_shift;
+    return a.cache.records + (at + (block & ((1 << a.cache.blocks_shift) - 1))) * R::bytes;
+  };
+  // What a wave loads of a record, two records ahead of spreading it.  Every wave loads
+  // alike, without branches, and indexes past the last record are brought back to it:
+  // otherwise the compiler waits for all loads in flight at each use (576 instead of
+  // XXX us for 2048 bf16 tokens behind 8192).
+  struct Staged {
+    uint4 codes[PIECES];
+    uint32_t word;                         // lanes 0 .. 31 a token's key word, 32 .. its value's
+    int there;                             // tokens that are there
+  };
+  float ref = 0.0f, staged_ref = 0.0f;     // of the sums, of the values staged
+  auto load = [&](Staged& st, int block) __attribute__((always_inline)) {
+    const uint8_t* rec = record(block);
+    st.there = rec ? min(most - block * 32, 32) : 0;
+    if (!rec) rec = a.cache.records;         // any record: its tokens count for nothing
+    st.word = ((const uint32_t*)(rec + R::words))[lane];
+#pragma unroll
+    for (int i = 0; i < PIECES; ++i)
+      st.codes[i] = *(const uint4*)(rec + min(wave + WAVES * i, 2 * REGION - 1) * 1024 + lane * 16);
+  };
+  // Steps of a record, and ref raised where one is above 8 of it.
+  auto steps = [&](const Staged& st, int buf) __attribute__((always_inline)) {
+    wave_meets();
+    words[wave][lane] = st.word;
+    const float step = word_step(st.word);
+    const uint64_t nan = __ballot(step != step);
+    const bool there = (lane & 31) < st.there;
+    const float sv = lane >= 32 && there && step == step ? step : 0.0f;
+    if (__any(sv > staged_ref * 8.0f))
+      staged_ref = __uint_as_float(
+          __float_as_uint(fminf(fmaxf(wave_top(sv), 0x1p-100f), 0x1p100f)) & 0x7f800000u);
+    const float inv = staged_ref > 0.0f ? kUnit / staged_ref : 0.0f;
+    if (wave == 0) {
+      // whoever sees a token whose values are NaN gets a NaN
+      if (lane < 32)
+        step_k[buf][lane] =
+            !there ? 0.0f : nan >> (lane + 32) & 1 ? __builtin_nanf("") : step * f;
+      else if (PARTS == 2)
+        step_v[buf][lane - 32] = sv * inv;
+    }
+    if constexpr (PARTS == 1) {
+      const int k = lane & 31;                 // in the order of a fragment's tokens
+      if (lane >= 32)
+        step_h[wave][BITS == 8 ? k : (k & ~3) | (k & 1) << 1 | (k & 2) >> 1] = (_Float16)(sv * inv);
+    }
+  };
+  auto spread = [&](const Staged& st, int buf) __attribute__((always_inline)) {
+    wave_meets();
+#pragma unroll
+    for (int i = 0; i < PIECES; ++i) {
+      const int at = wave + WAVES * i, piece = at % REGION;
+      if (at >= 2 * REGION) break;
+      const uint32_t c[4] = {st.codes[i].x, st.codes[i].y, st.codes[i].z, st.codes[i].w};
+      if (at >= REGION) {
+        uint32_t z0[4], z4[4], y[4] = {}, word[8];
+        const u32x4_t word0 = *(const u32x4_t*)&words[wave][32 + 4 * g];
+        const u32x4_t word1 = *(const u32x4_t*)&words[wave][48 + 4 * g];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) word[k] = word0[k], word[4 + k] = word1[k];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {          // zero points of two tokens of a fragment
+          const int e = k / 2 * 4 + (BITS == 8 ? k % 2 * 2 : k % 2), other = BITS == 8 ? 1 : 2;
+          const uint32_t z = __builtin_amdgcn_perm(word[e + other], word[e], 0x0c040c00u);
+          z0[k] = z | 0xe400e400u, z4[k] = (z & 0x000f000fu) << 4 | 0xd400d400u;
+        }
+        if constexpr (PARTS == 1) {
+          const u32x2_t y0 = *(const u32x2_t*)&step_h[wave][4 * g];
+          const u32x2_t y1 = *(const u32x2_t*)&step_h[wave][16 + 4 * g];
+          y[0] = y0[0], y[1] = y0[1], y[2] = y1[0], y[3] = y1[1];
+        }
+#pragma unroll
+        for (int k = 0; k < FR; ++k) {
+          const uint32_t w0 = BITS == 8 ? c[2 * k] : c[k / 2 * 2];
+          const uint32_t w1 = BITS == 8 ? c[2 * k + 1] : c[k / 2 * 2 + 1];
+          uint32_t v[4];
+          if constexpr (BITS == 8) {
+            v[0] = bytes_less(w0, 0x04010400u, z0[0]), v[1] = bytes_less(w0, 0x04030402u, z0[1]);
+            v[2] = bytes_less(w1, 0x04010400u, z0[2]), v[3] = bytes_less(w1, 0x04030402u, z0[3]);
+          } else if (k % 2 == 0) {
+            v[0] = low_less(w0, z0[0]), v[1] = low_less(w0 >> 8, z0[1]);
+            v[2] = low_less(w1, z0[2]), v[3] = low_less(w1 >> 8, z0[3]);
+          } else {
+            v[0] = high_less(w0, z4[0]), v[1] = high_less(w0 >> 8, z4[1]);
+            v[2] = high_less(w1, z4[2]), v[3] = high_less(w1 >> 8, z4[3]);
+          }
+          if constexpr (PARTS == 1)
+#pragma unroll
+            for (int n = 0; n < 4; ++n) v[n] = as_word(as_half2(v[n]) * as_half2(y[n]));
+          frags[buf][2 * J + piece * FR + k][lane] = make_uint4(v[0], v[1], v[2], v[3]);
+        }
+      } else {
+#pragma unroll
+        for (int k = 0; k < FR; ++k) {
+          const int F = piece * FR + k;
+          const int z = word_zero(words[wave][F / J * 16 + col]);
+          const uint32_t b0 = bias0(z, z), b4 = bias4(z, z);
+          uint4 v;
+          if constexpr (BITS == 8)
+            v = make_uint4(bytes_less(c[2 * k], 0x04010400u, b0),
+                           bytes_less(c[2 * k], 0x04030402u, b0),
+                           bytes_less(c[2 * k + 1], 0x04010400u, b0),
+                           bytes_less(c[2 * k + 1], 0x04030402u, b0));
+          else
+            v = make_uint4(low_less(c[k], b0), high_less(c[k], b4), low_less(c[k] >> 8, b0),
+                           high_less(c[k] >> 8, b4));
+          frags[buf][F][lane] = v;
+        }
+      }
+    }
+  };
+
+  // ---- sums
+  f32x4_t o[RT][N], l[RT];
+  float base[RT];
+#pragma unroll
+  for (int rt = 0; rt < RT; ++rt) {
+    base[rt] = kNone;
+    l[rt] = f32x4_t{0, 0, 0, 0};
+#pragma unroll
+    for (int n = 0; n < N; ++n) o[rt][n] = f32x4_t{0, 0, 0, 0};
+  }
+  const f16x8_t ones = as_half8(make_uint4(0x3c003c00u, 0x3c003c00u, 0x3c003c00u, 0x3c003c00u));
+  const bool busy = wave * 16 < rows;
+
+  f32x4_t score[RT][2], sk[2];             // of a record's tokens, and the tokens' steps
+  auto scores = [&](int buf) __attribute__((always_inline)) {
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+      sk[t] = *(const f32x4_t*)&step_k[buf][16 * t + 4 * g];
+#pragma unroll
+      for (int rt = 0; rt < RT; ++rt) score[rt][t] = f32x4_t{0, 0, 0, 0};
+    }
+#pragma unroll
+    for (int j = 0; j < J; ++j)
+#pragma unroll
+      for (int t = 0; t < 2; ++t) {
+        const f16x8_t k = as_half8(frags[buf][t * J + j][lane]);
+#pragma unroll
+        for (int part = 0; part < PARTS; ++part)
+#pragma unroll
+          for (int rt = 0; rt < RT; ++rt) score[rt][t] = mfma(k, qf[rt][part][j], score[rt][t]);
+      }
+  };
+  float e[RT][8];
+  auto exps = [&](int rt) __attribute__((always_inline)) {
+#pragma unroll
+    for (int t = 0; t < 2; ++t)
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        e[rt][4 * t + i] = __builtin_amdgcn_exp2f(fmaf(score[rt][t][i], sk[t][i], -base[rt]));
+  };
+  auto hide = [&](int rt, int p0, int n) __attribute__((always_inline)) {
+    const int end = min(visible[rt] - p0, n) - 4 * g;
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (i / 4 * 16 + i % 4 >= end) e[rt][i] = 0.0f;
+  };
+  // Weights 2^(score - maximum + 8) of a record's tokens; p0 its first token, n those
+  // that are there.  The maximum is raised once a score is 4 above it.
+  uint4 weight[RT][PARTS];
+  auto weights = [&](int buf, int p0, int n) __attribute__((always_inline)) {
+    const bool masked = p0 + 32 > least || n < 32;
+#pragma unroll
+    for (int rt = 0; rt < RT; ++rt) exps(rt);
+    if (masked)
+#pragma unroll
+      for (int rt = 0; rt < RT; ++rt) hide(rt, p0, n);
+    float top = 0.0f;
+#pragma unroll
+    for (int rt = 0; rt < RT; ++rt)
+#pragma unroll
+      for (int i = 0; i < 8; ++i) top = fmaxf(top, e[rt][i]);
+    if (__builtin_expect(__any(top > 4096.0f), 0)) {
+#pragma unroll
+      for (int rt = 0; rt < RT; ++rt) {
+        const int end = min(visible[rt] - p0, n) - 4 * g;
+        float m = kNone;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const float x = score[rt][i / 4][i % 4] * sk[i / 4][i % 4];
+          if (i / 4 * 16 + i % 4 < end) m = fmaxf(m, x);
+        }
+        m = fmaxf(m, __shfl_xor(m, 16, 64));
+        m = fmaxf(m, __shfl_xor(m, 32, 64));
+        const float next = fmaxf(base[rt], m - 8.0f);
+        const float factor = base[rt] == kNone ? 0.0f : __builtin_amdgcn_exp2f(base[rt] - next);
+        base[rt] = next;
+        l[rt] *= factor;
+#pragma unroll
+        for (int nn = 0; nn < N; ++nn) o[rt][nn] *= factor;
+        exps(rt);
+        if (masked) hide(rt, p0, n);
+      }
+    }
+#pragma unroll
+    for (int rt = 0; rt < RT; ++rt) {
+      float x[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) x[i] = e[rt][i];
+      if constexpr (PARTS == 1) {
+        weight[rt][0] = weight_part<BITS, false>(x);
+        l[rt] = mfma(ones, as_half8(weight[rt][0]), l[rt]);
+      } else {
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+          const f32x4_t y = *(const f32x4_t*)&step_v[buf][16 * t + 4 * g];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            l[rt][0] += x[4 * t + i];
+            x[4 * t + i] *= y[i];
+          }
+        }
+#pragma unroll
+        for (int part = 0; part < PARTS; ++part) weight[rt][part] = weight_part<BITS, true>(x);
+      }
+    }
+  };
+  auto add_values = [&](int buf) __attribute__((always_inline)) {
+#pragma unroll
+    for (int n = 0; n < N; ++n) {
+      const f16x8_t v = as_half8(frags[buf][2 * J + n][lane]);
+#pragma unroll
+      for (int part = 0; part < PARTS; ++part)
+#pragma unroll
+        for (int rt = 0; rt < RT; ++rt) o[rt][n] = mfma(v, as_half8(weight[rt][part]), o[rt][n]);
+    }
+  };
+
+  auto turn = [&]() __attribute__((always_inline)) {
+    __builtin_amdgcn_sched_barrier(0);
+    lds_barrier();
+    __builtin_amdgcn_sched_barrier(0);
+  };
+  if (i0 < i1) {
+    // A record is spread two records ahead of its turn, into the place of the one two
+    // before: the last reads of that were a barrier ago, the first reads are one ahead.
+    // ref of a record's values, as its sums need it: of the last four records.
+    Staged st[2];
+    int there[4];
+    float refs[4];
+    auto stage = [&](Staged& from, int i) __attribute__((always_inline)) {
+      steps(from, (i - i0) & 3);
+      spread(from, (i - i0) & 3);
+    };
+    load(st[0], i0);
+    load(st[1], min(i0 + 1, i1 - 1));
+    stage(st[0], i0);
+    there[0] = st[0].there, refs[0] = staged_ref;
+    load(st[0], min(i0 + 2, i1 - 1));
+    stage(st[1], i0 + 1);
+    there[1] = st[1].there, refs[1] = staged_ref;
+    load(st[1], min(i0 + 3, i1 - 1));
+    lds_barrier();
+    if (wave >= 4) turn();
+    auto one = [&](int i, auto u) __attribute__((always_inline)) {
+      constexpr int U = decltype(u)::value;             // (i - i0) % 4
+      if (busy) {
+        __builtin_amdgcn_s_setprio(1);
+        if (i > i0) {
+          if (refs[(U + 3) & 3] != ref) {      // larger values: the sums in their unit
+            const float factor = ref / refs[(U + 3) & 3];
+#pragma unroll
+            for (int rt = 0; rt < RT; ++rt)
+#pragma unroll
+              for (int n = 0; n < N; ++n) o[rt][n] *= factor;
+            ref = refs[(U + 3) & 3];
+          }
+          add_values((U + 3) & 3);
+        }
+        scores(U);
+        __builtin_amdgcn_s_setprio(0);
+      }
+      turn();
+      steps(st[U & 1], (U + 2) & 3);
+      if (busy) weights(U, i * 32, there[U]);
+      spread(st[U & 1], (U + 2) & 3);
+      there[(U + 2) & 3] = st[U & 1].there, refs[(U + 2) & 3] = staged_ref;
+      load(st[U & 1], min(i + 4, i1 - 1));
+      turn();
+    };
+    int i = i0;
+    for (;;) {
+      one(i, std::integral_constant<int, 0>{});
+      if (++i == i1) break;
+      one(i, std::integral_constant<int, 1>{});
+      if (++i == i1) break;
+      one(i, std::integral_constant<int, 2>{});
+      if (++i == i1) break;
+      one(i, std::integral_constant<int, 3>{});
+      if (++i == i1) break;
+    }
+    if (wave < 4) turn();
+    if (busy) {
+      const int last = (i1 - 1 - i0) & 3;
+      const float r = last == 0 ? refs[0] : last == 1 ? refs[1] : last == 2 ? refs[2] : refs[3];
+      if (r != ref) {
+        const float factor = ref / r;
+#pragma unroll
+        for (int rt = 0; rt < RT; ++rt)
+#pragma unroll
+          for (int n = 0; n < N; ++n) o[rt][n] *= factor;
+        ref = r;
+      }
+      add_values(last);
+    }
+  }
+  if (!busy) return;
+  const float back = ref / (kUnit * 256.0f);
+  float* slot = a.slots + (((int64_t)h * a.items + item) * a.splits + split) * (ROWS * (D + 2));
+#pragma unroll
+  for (int rt = 0; rt < RT; ++rt) {
+    const int row = (rt * WAVES + wave) * 16 + col;
+    float sum = l[rt][0];
+    if constexpr (PARTS == 2) {
+      sum += __shfl_xor(sum, 16, 64);
+      sum += __shfl_xor(sum, 32, 64);
+    }
+    sum *= 1.0f / 256.0f;
+    if (row >= rows) continue;
+    if (a.slots == nullptr) {
+      const float unit = sum == 0.0f ? 0.0f : back / sum;
+      const int r = first + row;
+      const int64_t to = (int64_t)(q.r0 + r / a.group) * a.out.ts +
+                         (int64_t)(h * a.group + r % a.group) * a.out.hs + 4 * g;
+#pragma unroll
+      for (int n = 0; n < N; ++n) {
+        float y[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) y[i] = sum == 0.0f ? 0.0f : o[rt][n][i] * unit;
+        store_row4((T*)a.out.p + to + 16 * n, y);
+      }
+    } else {
+#pragma unroll
+      for (int n = 0; n < N; ++n)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) slot[row * D + 16 * n + 4 * g + i] = o[rt][n][i] * back;
+      if (g == 0) {
+        slot[ROWS * D + row] = base[rt] == kNone ? kNone : base[rt] + 8.0f;
+        slot[ROWS * (D + 1) + row] = sum;
+      }
+    }
+  }
+}
+
+// Where a row's results are: those of attend_rows, or of attend_tiles.
+struct Parts {
+  CacheView cache;
+  CacheBatch batch;
+  int group, capacity, direct, tile_rows;      // tile_rows 0: attend_rows
+  int64_t workers, items, splits;
+  const float* slots;
+};
 struct JoinArgs {
-  RowsArgs own, before;        // before.workers 0: no prefix
+  Parts own, before;           // before.slots NULL: no prefix
+  CacheTensor out;
+  int heads;
 };
 
 // A row's results from the workers that had tiles of its item, and from those of
 // the prefix: a workgroup per row.
 template <typename T, int D>
 __global__ __launch_bounds__(256) void join_rows(const JoinArgs j) {
-  const RowsArgs& a = j.own;
   __shared__ Scan sc;
   __shared__ float sm[4], sl[4], so[4][D];
   const int64_t b = block_index();
-  const int head = (int)(b % a.heads), h = head / a.group;
-  if (b / a.heads >= a.batch.ntok) return;
-  const int t = (int)(b / a.heads);
-  const int s = find_sequence(a.batch, t);
+  const int head = (int)(b % j.heads), h = head / j.own.group;
+  if (b / j.heads >= j.own.batch.ntok) return;
+  const int t = (int)(b / j.heads);
+  const int s = find_sequence(j.own.batch, t);
   if (s < 0) return;
   const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
   constexpr int E = D / 64;
   float m = kNone, l = 0.0f, o[E] = {};
-  bool any = false;
+  auto add = [&](const float* sums, float pm, float pl) {
+    const float next = fmaxf(m, pm), base = next == kNone ? 0.0f : next;
+    const float fm = exp2f(m - base), fp = pm == kNone ? 1.0f : exp2f(pm - base);
+    l = l * fm + pl * fp;
+#pragma unroll
+    for (int e = 0; e < E; ++e) o[e] = o[e] * fm + sums[lane * E + e] * fp;
+    m = next;
+  };
   for (int of = 0; of < 2; ++of) {
-    const RowsArgs& r = of ? j.before : j.own;
-    if (r.workers == 0) continue;
-    const Walk walk{r.batch, &r.cache, r.group, r.capacity};
+    const Parts& r = of ? j.before : j.own;
+    if (!r.slots) continue;
     const int own = of ? 0 : s;
-    const Seq q = walk.seq(own);
-    const int per = walk.tiles(q);
+    const Seq q = sequence(r.batch, own);
     const int64_t row = (int64_t)(t - q.r0) * r.group + head % r.group;
+    const Walk walk{r.batch, &r.cache, r.group, r.capacity};
+    if (r.tile_rows) {
+      int64_t item0 = 0;
+      if (own > 0) {
+        int64_t mine = 0, x, y, none;
+        for (int i = threadIdx.x; i < own; i += 256) {
+          const Seq p = sequence(r.batch, i);
+          mine += ((int64_t)(p.r1 - p.r0) * r.group + r.tile_rows - 1) / r.tile_rows;
+        }
+        scan2(mine, 0, &x, &y, &item0, &none, sc.red);
+        __syncthreads();
+      }
+      const int64_t item = item0 + row / r.tile_rows;
+      const int k = (int)(row % r.tile_rows);
+      if (item >= r.items) continue;
+      for (int64_t i = wave; i < r.splits; i += 4) {
+        const float* slot = r.slots + (((int64_t)h * r.items + item) * r.splits + i) *
+                                          ((int64_t)r.tile_rows * (D + 2));
+        add(slot + k * D, slot[r.tile_rows * D + k], slot[r.tile_rows * (D + 1) + k]);
+      }
+      continue;
+    }
+    const int per = walk.tiles(q);
     const int64_t total = total_tiles(walk, sc);
     __syncthreads();
     const Place place = locate(walk, 0, own, sc);
@@ -473,17 +1057,10 @@ __global__ __launch_bounds__(256) void join_rows(const JoinArgs j) {
     const int64_t w0 = first / c, w1 = (first + per - 1) / c;
     if (item >= r.items) continue;
     if (w0 == w1 && r.direct) return;                  // written already
-    any = true;
     for (int64_t w = w0 + wave; w <= w1; w += 4) {
       const float* slot = r.slots + ((int64_t)h * (r.workers + r.items) + w + item) * kSlot<D>;
       const int k = (int)(row % kRows);
-      const float pm = slot[kRows * D + k], pl = slot[kRows * D + kRows + k];
-      const float next = fmaxf(m, pm), base = next == kNone ? 0.0f : next;
-      const float fm = exp2f(m - base), fp = pm == kNone ? 1.0f : exp2f(pm - base);
-      l = l * fm + pl * fp;
-#pragma unroll
-      for (int e = 0; e < E; ++e) o[e] = o[e] * fm + slot[k * D + lane * E + e] * fp;
-      m = next;
+      add(slot + k * D, slot[kRows * D + k], slot[kRows * D + kRows + k]);
     }
   }
   if (lane == 0) sm[wave] = m, sl[wave] = l;
@@ -500,73 +1077,125 @@ __global__ __launch_bounds__(256) void join_rows(const JoinArgs j) {
   for (int d = threadIdx.x; d < D; d += 256) {
     float v = 0.0f;
     for (int i = 0; i < 4; ++i) v += so[i][d] * fac[i];
-    const float y = !any || sum == 0.0f ? 0.0f : v / sum;
-    const int64_t to = (int64_t)t * a.out.ts + (int64_t)head * a.out.hs + d;
-    if constexpr (std::is_same_v<T, float>) ((float*)a.out.p)[to] = y;
-    else ((__bf16*)a.out.p)[to] = (__bf16)y;
+    const float y = sum == 0.0f ? 0.0f : v / sum;
+    const int64_t to = (int64_t)t * j.out.ts + (int64_t)head * j.out.hs + d;
+    if constexpr (std::is_same_v<T, float>) ((float*)j.out.p)[to] = y;
+    else ((__bf16*)j.out.p)[to] = (__bf16)y;
   }
+}
+
+// 16 rows of attend_tiles' waves: what the registers hold of queries and sums.
+template <typename T, int D>
+struct Shape {
+  static constexpr int rt = D == 256 || (D == 128 && std::is_same_v<T, float>) ? 1 : 2;
+  static constexpr int rows = 128 * rt;
+};
+template <typename T>
+int rows_of_dim(int dim) {
+  return dim == 64 ? Shape<T, 64>::rows : dim == 128 ? Shape<T, 128>::rows : Shape<T, 256>::rows;
+}
+int tile_rows_of(int32_t dtype, int dim) {
+  return dtype == PWQ_F32 ? rows_of_dim<float>(dim) : rows_of_dim<uint16_t>(dim);
 }
 
 int capacity_of(const CacheBatch& b, int blocks_shift) {
   return (int)std::min<int64_t>((int64_t)b.width << (blocks_shift + 5), INT32_MAX - 65535);
 }
 
+struct Launch {
+  JoinArgs join;
+  RowsArgs rows;
+  TilesArgs tiles[2];          // the batch's, the prefix's; splits 0: none
+  bool joined;
+};
+
 template <typename T, int D, int BITS>
-void launch_all(const JoinArgs& j, hipStream_t st) {
-  for (const RowsArgs* r : {&j.before, &j.own})
-    if (r->workers)
-      attend_rows<T, D, BITS><<<block_grid(r->workers * r->cache.heads), 256, 0, st>>>(*r);
-  join_rows<T, D><<<block_grid((int64_t)j.own.batch.ntok * j.own.heads), 256, 0, st>>>(j);
+void launch_all(const Launch& l, hipStream_t st) {
+  for (const TilesArgs& t : l.tiles)
+    if (t.splits)
+      attend_tiles<T, D, BITS, Shape<T, D>::rt>
+          <<<block_grid(t.items * t.splits * t.cache.heads), 512, 0, st>>>(t);
+  if (l.rows.workers)
+    attend_rows<T, D, BITS><<<block_grid(l.rows.workers * l.rows.cache.heads), 256, 0, st>>>(l.rows);
+  if (l.joined)
+    join_rows<T, D><<<block_grid((int64_t)l.join.own.batch.ntok * l.join.heads), 256, 0, st>>>(
+        l.join);
 }
 
 template <typename T, int D>
-void launch_bits(const JoinArgs& j, int bits, hipStream_t st) {
-  if (bits == 8) launch_all<T, D, 8>(j, st);
-  else launch_all<T, D, 4>(j, st);
+void launch_bits(const Launch& l, int bits, hipStream_t st) {
+  if (bits == 8) launch_all<T, D, 8>(l, st);
+  else launch_all<T, D, 4>(l, st);
 }
 
 template <typename T>
-void launch_dim(const JoinArgs& j, int dim, int bits, hipStream_t st) {
-  if (dim == 64) launch_bits<T, 64>(j, bits, st);
-  else if (dim == 128) launch_bits<T, 128>(j, bits, st);
-  else launch_bits<T, 256>(j, bits, st);
+void launch_dim(const Launch& l, int dim, int bits, hipStream_t st) {
+  if (dim == 64) launch_bits<T, 64>(l, bits, st);
+  else if (dim == 128) launch_bits<T, 128>(l, bits, st);
+  else launch_bits<T, 256>(l, bits, st);
 }
 
 }  // namespace
 
 AttentionPlan attention_plan(const AttentionLaunch& a) {
   AttentionPlan p{};
-  const int64_t group = a.heads / a.cache.heads, rows = (int64_t)a.batch.ntok * group;
-  p.workers = std::max<int64_t>(1, 512 / a.cache.heads);
-  p.items = rows / kRows + std::min<int64_t>(a.batch.nseq, a.batch.ntok) + 1;
-  p.prefix_items = a.prefix.nseq ? (rows + kRows - 1) / kRows : 0;
-  const int64_t slot = kRows * (a.head_dim + 2) * 4;
-  p.own_bytes = (p.workers + p.items) * a.cache.heads * slot;
-  p.prefix_bytes = p.prefix_items ? (p.workers + p.prefix_items) * a.cache.heads * slot : 0;
+  const int64_t heads = a.cache.heads, group = a.heads / heads;
+  const int64_t rows = a.batch.ntok * group, seqs = std::min(a.batch.nseq, a.batch.ntok);
+  const int64_t tile = tile_rows_of(a.dtype, a.head_dim);
+  // Splits of the tokens: workgroups for every CU, where items alone are fewer, of
+  // at least four stages of 64 tokens.
+  auto splits = [&](int64_t items, const CacheBatch& b) {
+    const int64_t most = std::max<int64_t>(
+        1, capacity_of(b, a.cache.blocks_shift) / (64 * 4));
+    return std::min(std::max<int64_t>(1, 256 / (items * heads)), most);
+  };
+  p.tiles = rows > 32 * seqs;
+  if (p.tiles) {
+    p.items = rows / tile + seqs;
+    p.splits = splits((rows + tile - 1) / tile, a.batch);
+    if (p.splits > 1 || a.prefix.nseq)
+      p.own_bytes = p.items * p.splits * heads * tile * (a.head_dim + 2) * 4;
+  } else {
+    p.workers = std::max<int64_t>(1, 512 / heads);
+    p.items = rows / kRows + seqs;
+    p.own_bytes = (p.workers + p.items) * heads * kRows * (a.head_dim + 2) * 4;
+  }
+  if (a.prefix.nseq) {
+    p.prefix_items = (rows + tile - 1) / tile;
+    p.prefix_splits = splits(p.prefix_items, a.prefix);
+    p.prefix_bytes = p.prefix_items * p.prefix_splits * heads * tile * (a.head_dim + 2) * 4;
+  }
   return p;
 }
 
 hipError_t launch_cached_attention(const AttentionLaunch& a, const AttentionPlan& p, void* own,
                                    void* prefix, hipStream_t st) {
   if (a.batch.ntok == 0 || a.batch.nseq == 0) return hipSuccess;
-  JoinArgs j{};
-  j.own = RowsArgs{a.cache, a.batch, a.q, a.out, a.heads / a.cache.heads, a.heads, a.causal,
-                   capacity_of(a.batch, a.cache.blocks_shift), a.prefix.nseq == 0, p.workers,
-                   p.items, a.scale, (float*)own};
+  const int group = a.heads / a.cache.heads;
+  const int tile = tile_rows_of(a.dtype, a.head_dim);
+  const int capacity = capacity_of(a.batch, a.cache.blocks_shift);
+  Launch l{};
+  l.joined = p.own_bytes > 0;
+  l.join.out = a.out, l.join.heads = a.heads;
+  l.join.own = Parts{a.cache, a.batch, group, capacity, a.prefix.nseq == 0, p.tiles ? tile : 0,
+                     p.workers, p.items, p.splits, (const float*)own};
+  if (p.tiles)
+    l.tiles[0] = TilesArgs{a.cache, a.batch, a.q, a.out, group, a.heads, a.causal, capacity,
+                           p.splits, p.items, a.scale, p.own_bytes ? (float*)own : nullptr};
+  else
+    l.rows = RowsArgs{a.cache, a.batch, a.q, a.out, group, a.heads, a.causal, capacity,
+                      a.prefix.nseq == 0, p.workers, p.items, a.scale, (float*)own};
   if (a.prefix.nseq) {
-    j.before = j.own;
-    j.before.batch = a.prefix;
-    j.before.batch.starts = a.batch.starts;
-    j.before.batch.starts_step = a.batch.nseq;
-    j.before.batch.ntok = a.batch.ntok;
-    j.before.causal = 0;
-    j.before.direct = 0;
-    j.before.capacity = capacity_of(a.prefix, a.cache.blocks_shift);
-    j.before.items = p.prefix_items;
-    j.before.slots = (float*)prefix;
+    CacheBatch b = a.prefix;
+    b.starts = a.batch.starts, b.starts_step = a.batch.nseq, b.ntok = a.batch.ntok;
+    const int cap = capacity_of(a.prefix, a.cache.blocks_shift);
+    l.tiles[1] = TilesArgs{a.cache, b, a.q, a.out, group, a.heads, 0, cap, p.prefix_splits,
+                           p.prefix_items, a.scale, (float*)prefix};
+    l.join.before = Parts{a.cache, b, group, cap, 0, tile, 0, p.prefix_items, p.prefix_splits,
+                          (const float*)prefix};
   }
-  if (a.dtype == PWQ_F32) launch_dim<float>(j, a.head_dim, a.bits, st);
-  else launch_dim<uint16_t>(j, a.head_dim, a.bits, st);
+  if (a.dtype == PWQ_F32) launch_dim<float>(l, a.head_dim, a.bits, st);
+  else launch_dim<uint16_t>(l, a.head_dim, a.bits, st);
   return hipGetLastError();
 }
 

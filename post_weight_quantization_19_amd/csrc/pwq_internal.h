@@ -276,8 +276,10 @@ struct AttentionLaunch {
   float scale;
 };
 struct AttentionPlan {
-  int64_t workers;                  // workgroups per key head
-  int64_t items, prefix_items;      // at most, per key head
+  bool tiles;                       // many rows to a sequence: tiles of rows, else 16 rows
+  int64_t workers;                  // 16 rows: workgroups per key head
+  int64_t items, splits;            // items per key head, at most; splits of an item's tokens
+  int64_t prefix_items, prefix_splits;
   size_t own_bytes, prefix_bytes;   // partial results
 };
 AttentionPlan attention_plan(const AttentionLaunch& a);

@@ -9,9 +9,13 @@ sees, W = sum w |v| of the normalised weights and n tokens:
   exp       two units in the last place, and the exponent's rounding: 2^-24 times
             the score in base 2, at most 1.45 A; weights are off by the error
             of their score twice (numerator and sum)
-  weights   in one float16 part 2^-12 (bf16), two 2^-22 (float32); below 2^-14 of
-            256 times ref, where float16 is spaced 2^-24: 2^-33 ref, ref at most
-            the largest step, for each token, times a code of at most 255
+  weights   in one float16 part 2^-12 (bf16), two 2^-22 (float32); a weight is held
+            as 256 of them, a token's step as up to 8 of a unit that is at most the
+            largest step: below 2^-14, where float16 is spaced 2^-24, a token is off
+            by 2^-33 of that step times a code of at most 255
+  values    bf16, many rows: the step over the unit, and its product with the code less
+            the zero point, in one float16 part each: 2^-12 twice, or, of the unit,
+            2^-30 times such a code, and 2^-30 (together less than 2^-33 * 8 * 256)
   sums      n / 16 + 64 float32 additions and rescalings in a row
 and the output is rounded once (bf16: 2^-8 of the value, a half of its spacing).
 """
@@ -242,9 +246,9 @@ def check_attention(y, q, records, b, dim, bits, page, scale=None, causal=True, 
             step = (v[h // group].max(-1, initial=0) - v[h // group].min(-1, initial=0)).max(
                 initial=0) / (2 ** bits - 1) * 1.02
             off = score * ((dim + 4 + 1.45) * 2.0 ** -24 + (0 if bf16 else 2.0 ** -22))
-            rel = 2 * off + 2.0 ** -21 + (2.0 ** -12 if bf16 else 2.0 ** -22)
+            rel = 2 * off + 2.0 ** -21 + (3 * 2.0 ** -12 if bf16 else 2.0 ** -22)
             rel = rel + (n / 16 + 64) * 2.0 ** -24
-            tol = rel[:, None] * (size + np.abs(want)) + n * 2.0 ** -33 * step * 255
+            tol = rel[:, None] * (size + np.abs(want)) + (n + 9) * 2.0 ** -33 * step * 255
             tol = tol * 1.01 + (2.0 ** -8 * 1.01 if bf16 else 2.0 ** -23) * np.abs(want)
             err = np.abs(got[r, h] - want)
             assert np.all(err <= tol), (i, h, float((err / np.maximum(tol, 1e-300)).max()),
