@@ -539,10 +539,7 @@ __global__ __launch_bounds__(512, 1) void attend_tiles(const TilesArgs a) {
   __shared__ uint4 frags[4][2 * J + N][64];    // [record % 4][keys (t, j), values n]
   __shared__ __align__(16) float step_k[4][32];      // keys' steps times f
   __shared__ __align__(16) float step_v[4][32];      // values' steps, PARTS 2
-  // A wave's own: table entries, the words of the record that it spreads.
-  __shared__ int entries[WAVES][64];
-  __shared__ __align__(16) uint32_t words[WAVES][64];
-  __shared__ __align__(16) _Float16 step_h[WAVES][32];   // values' steps, PARTS 1: a wave's own
+  __shared__ int entries[WAVES][64];           // table entries, a wave's own
   const int h = (int)(block_index() % a.cache.heads);
   const int64_t rest = block_index() / a.cache.heads;
   const int64_t split = rest % a.splits, item = a.items - 1 - rest / a.splits;
@@ -622,21 +619,29 @@ __global__ __launch_bounds__(512, 1) void attend_tiles(const TilesArgs a) {
   const int least = __builtin_amdgcn_readfirstlane(visible[0]);   // the first row sees least
 
   // ---- staging
-  // The record of a block.  Table entries come 64 at a time.
+  // Records one after the other, up to the last.  Table entries come 64 at a time, and
+  // that of the next record is read from LDS while this one is loaded.
   const int32_t* table = a.batch.table + s * a.batch.ldt;
-  int entries_from = -64;
-  auto record = [&](int block) __attribute__((always_inline)) -> const uint8_t* {  // NULL: a hole
-    const int entry = block >> a.cache.blocks_shift;
-    if (entry - entries_from >= 64) {
+  int entries_from = -64, next_page = -1, next_block = i0;
+  auto look_up = [&]() __attribute__((always_inline)) {
+    const int entry = next_block >> a.cache.blocks_shift;
+    if (__builtin_expect(entry - entries_from >= 64, 0)) {
       entries_from = entry & ~63;
       wave_meets();
       entries[wave][lane] = entries_from + lane < a.batch.width ? table[entries_from + lane] : -1;
       wave_meets();
     }
-    const int page = __builtin_amdgcn_readfirstlane(entries[wave][entry - entries_from]);
-    if (page < 0 || page >= a.cache.pages) return nullptr;
+    next_page = entries[wave][entry - entries_from];
+  };
+  auto next_record = [&](int* block) __attribute__((always_inline)) -> const uint8_t* {
+    const int page = __builtin_amdgcn_readfirstlane(next_page);
+    *block = next_block;
     const int64_t at = ((int64_t)page * a.cache.heads + h) << a.cache.blocks_shift;
-    return a.cache.records + (at + (block & ((1 << a.cache.blocks_shift) - 1))) * R::bytes;
+    const uint8_t* rec =
+        a.cache.records + (at + (next_block & ((1 << a.cache.blocks_shift) - 1))) * R::bytes;
+    next_block = min(next_block + 1, i1 - 1);
+    look_up();
+    return page < 0 || page >= a.cache.pages ? nullptr : rec;          // a hole
   };
   // What a wave loads of a record, two records ahead of spreading it.  Every wave loads
   // alike, without branches, and indexes past the last record are brought back to it:
@@ -644,68 +649,74 @@ __global__ __launch_bounds__(512, 1) void attend_tiles(const TilesArgs a) {
   // XXX us for 2048 bf16 tokens behind 8192).
   struct Staged {
     uint4 codes[PIECES];
+    u32x4_t words[2];                      // whose zero points and steps its codes need
+    uint32_t key;                          // and that of its keys, where PIECES is 2
     uint32_t word;                         // lanes 0 .. 31 a token's key word, 32 .. its value's
     int there;                             // tokens that are there
   };
+  // Values need the words of tokens 4 g .. and 16 + 4 g .., keys those of col and 16 + col.
+  typedef u32x4_t __attribute__((aligned(4))) words_t;
+  const bool two = PIECES > 1;               // keys and values alike
+  const int words_at = R::words + (two || wave >= REGION ? 128 + 16 * g : 4 * col);
   float ref = 0.0f, staged_ref = 0.0f;     // of the sums, of the values staged
-  auto load = [&](Staged& st, int block) __attribute__((always_inline)) {
-    const uint8_t* rec = record(block);
+  auto unit_over = [&](float r) { return r > 0.0f ? kUnit / r : 0.0f; };
+  auto load = [&](Staged& st) __attribute__((always_inline)) {
+    int block;
+    const uint8_t* rec = next_record(&block);
     st.there = rec ? min(most - block * 32, 32) : 0;
     if (!rec) rec = a.cache.records;         // any record: its tokens count for nothing
     st.word = ((const uint32_t*)(rec + R::words))[lane];
+    st.words[0] = *(const words_t*)(rec + words_at);
+    st.words[1] = *(const words_t*)(rec + words_at + 64);
+    if constexpr (PIECES == 2)
+      st.key = ((const uint32_t*)(rec + R::words))[2 * wave / J * 16 + col];
 #pragma unroll
     for (int i = 0; i < PIECES; ++i)
       st.codes[i] = *(const uint4*)(rec + min(wave + WAVES * i, 2 * REGION - 1) * 1024 + lane * 16);
   };
-  // Steps of a record, and ref raised where one is above 8 of it.
+  // Keys' steps of a record for all, and ref raised where a value's is above 8 of it.
   auto steps = [&](const Staged& st, int buf) __attribute__((always_inline)) {
-    wave_meets();
-    words[wave][lane] = st.word;
     const float step = word_step(st.word);
-    const uint64_t nan = __ballot(step != step);
     const bool there = (lane & 31) < st.there;
-    const float sv = lane >= 32 && there && step == step ? step : 0.0f;
-    if (__any(sv > staged_ref * 8.0f))
+    const float sv = lane >= 32 && there ? fmaxf(step, 0.0f) : 0.0f;       // 0 for a NaN
+    if (__builtin_expect(__any(sv > staged_ref * 8.0f), 0))
       staged_ref = __uint_as_float(
           __float_as_uint(fminf(fmaxf(wave_top(sv), 0x1p-100f), 0x1p100f)) & 0x7f800000u);
-    const float inv = staged_ref > 0.0f ? kUnit / staged_ref : 0.0f;
     if (wave == 0) {
+      const uint64_t nan = __ballot(step != step) >> 32;
       // whoever sees a token whose values are NaN gets a NaN
       if (lane < 32)
-        step_k[buf][lane] =
-            !there ? 0.0f : nan >> (lane + 32) & 1 ? __builtin_nanf("") : step * f;
+        step_k[buf][lane] = !there ? 0.0f : nan >> lane & 1 ? __builtin_nanf("") : step * f;
       else if (PARTS == 2)
-        step_v[buf][lane - 32] = sv * inv;
-    }
-    if constexpr (PARTS == 1) {
-      const int k = lane & 31;                 // in the order of a fragment's tokens
-      if (lane >= 32)
-        step_h[wave][BITS == 8 ? k : (k & ~3) | (k & 1) << 1 | (k & 2) >> 1] = (_Float16)(sv * inv);
+        step_v[buf][lane - 32] = sv * unit_over(staged_ref);
     }
   };
   auto spread = [&](const Staged& st, int buf) __attribute__((always_inline)) {
-    wave_meets();
 #pragma unroll
     for (int i = 0; i < PIECES; ++i) {
       const int at = wave + WAVES * i, piece = at % REGION;
       if (at >= 2 * REGION) break;
       const uint32_t c[4] = {st.codes[i].x, st.codes[i].y, st.codes[i].z, st.codes[i].w};
       if (at >= REGION) {
-        uint32_t z0[4], z4[4], y[4] = {}, word[8];
-        const u32x4_t word0 = *(const u32x4_t*)&words[wave][32 + 4 * g];
-        const u32x4_t word1 = *(const u32x4_t*)&words[wave][48 + 4 * g];
+        const uint32_t word[8] = {st.words[0][0], st.words[0][1], st.words[0][2], st.words[0][3],
+                                  st.words[1][0], st.words[1][1], st.words[1][2], st.words[1][3]};
+        uint32_t z0[4], z4[4], y[4] = {};
+        const float inv = unit_over(staged_ref);
+        float step[8];
+        if constexpr (PARTS == 1) {
 #pragma unroll
-        for (int k = 0; k < 4; ++k) word[k] = word0[k], word[4 + k] = word1[k];
+          for (int k = 0; k < 8; ++k) step[k] = fmaxf(word_step(word[k]), 0.0f) * inv;
+          if (__builtin_expect(st.there < 32, 0))
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {          // zero points of two tokens of a fragment
+            for (int k = 0; k < 8; ++k)
+              if (k / 4 * 16 + 4 * g + k % 4 >= st.there) step[k] = 0.0f;
+        }
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {          // two tokens of a fragment
           const int e = k / 2 * 4 + (BITS == 8 ? k % 2 * 2 : k % 2), other = BITS == 8 ? 1 : 2;
           const uint32_t z = __builtin_amdgcn_perm(word[e + other], word[e], 0x0c040c00u);
           z0[k] = z | 0xe400e400u, z4[k] = (z & 0x000f000fu) << 4 | 0xd400d400u;
-        }
-        if constexpr (PARTS == 1) {
-          const u32x2_t y0 = *(const u32x2_t*)&step_h[wave][4 * g];
-          const u32x2_t y1 = *(const u32x2_t*)&step_h[wave][16 + 4 * g];
-          y[0] = y0[0], y[1] = y0[1], y[2] = y1[0], y[3] = y1[1];
+          if constexpr (PARTS == 1) y[k] = two_halves(step[e], step[e + other]);
         }
 #pragma unroll
         for (int k = 0; k < FR; ++k) {
@@ -731,7 +742,7 @@ __global__ __launch_bounds__(512, 1) void attend_tiles(const TilesArgs a) {
 #pragma unroll
         for (int k = 0; k < FR; ++k) {
           const int F = piece * FR + k;
-          const int z = word_zero(words[wave][F / J * 16 + col]);
+          const int z = word_zero(PIECES == 2 ? st.key : F / J ? st.words[1][0] : st.words[0][0]);
           const uint32_t b0 = bias0(z, z), b4 = bias4(z, z);
           uint4 v;
           if constexpr (BITS == 8)
@@ -762,24 +773,6 @@ __global__ __launch_bounds__(512, 1) void attend_tiles(const TilesArgs a) {
   const bool busy = wave * 16 < rows;
 
   f32x4_t score[RT][2], sk[2];             // of a record's tokens, and the tokens' steps
-  auto scores = [&](int buf) __attribute__((always_inline)) {
-#pragma unroll
-    for (int t = 0; t < 2; ++t) {
-      sk[t] = *(const f32x4_t*)&step_k[buf][16 * t + 4 * g];
-#pragma unroll
-      for (int rt = 0; rt < RT; ++rt) score[rt][t] = f32x4_t{0, 0, 0, 0};
-    }
-#pragma unroll
-    for (int j = 0; j < J; ++j)
-#pragma unroll
-      for (int t = 0; t < 2; ++t) {
-        const f16x8_t k = as_half8(frags[buf][t * J + j][lane]);
-#pragma unroll
-        for (int part = 0; part < PARTS; ++part)
-#pragma unroll
-          for (int rt = 0; rt < RT; ++rt) score[rt][t] = mfma(k, qf[rt][part][j], score[rt][t]);
-      }
-  };
   float e[RT][8];
   auto exps = [&](int rt) __attribute__((always_inline)) {
 #pragma unroll
@@ -854,68 +847,115 @@ __global__ __launch_bounds__(512, 1) void attend_tiles(const TilesArgs a) {
       }
     }
   };
-  auto add_values = [&](int buf) __attribute__((always_inline)) {
+  // Values of record `vb` (of 4) times weights into o, keys of `kb` times queries into
+  // score: fragments come from LDS kAhead before they are used, the first of them before
+  // the barrier that starts the turn.
+  constexpr int kAhead = 4, kFrags = N + 2 * J;
+  f16x8_t ahead[kAhead];
+  auto fragment = [&](int k, int vb, int kb) __attribute__((always_inline)) {
+    const int i = k - N;                       // keys: j, then t
+    return k < N ? as_half8(frags[vb][2 * J + k][lane])
+                 : as_half8(frags[kb][i % 2 * J + i / 2][lane]);
+  };
+  auto fetch = [&](int vb) __attribute__((always_inline)) {
 #pragma unroll
-    for (int n = 0; n < N; ++n) {
-      const f16x8_t v = as_half8(frags[buf][2 * J + n][lane]);
+    for (int k = 0; k < kAhead; ++k) ahead[k] = fragment(k, vb, 0);
+  };
+  auto multiply = [&](int vb, int kb, auto keys) __attribute__((always_inline)) {
+    constexpr int TOTAL = decltype(keys)::value ? kFrags : N;
+    if constexpr (TOTAL > N)
+#pragma unroll
+      for (int t = 0; t < 2; ++t) {
+        sk[t] = *(const f32x4_t*)&step_k[kb][16 * t + 4 * g];
+#pragma unroll
+        for (int rt = 0; rt < RT; ++rt) score[rt][t] = f32x4_t{0, 0, 0, 0};
+      }
+    static_for_up<TOTAL>([&](auto kc) __attribute__((always_inline)) {
+      constexpr int k = decltype(kc)::value;
+      const f16x8_t x = ahead[k % kAhead];
+      if constexpr (k + kAhead < TOTAL) ahead[k % kAhead] = fragment(k + kAhead, vb, kb);
 #pragma unroll
       for (int part = 0; part < PARTS; ++part)
 #pragma unroll
-        for (int rt = 0; rt < RT; ++rt) o[rt][n] = mfma(v, as_half8(weight[rt][part]), o[rt][n]);
-    }
+        for (int rt = 0; rt < RT; ++rt) {
+          if constexpr (k < N) o[rt][k] = mfma(x, as_half8(weight[rt][part]), o[rt][k]);
+          else
+            score[rt][(k - N) % 2] = mfma(x, qf[rt][part][(k - N) / 2], score[rt][(k - N) % 2]);
+        }
+      __builtin_amdgcn_sched_barrier(0);
+    });
   };
 
-  auto turn = [&]() __attribute__((always_inline)) {
+  auto turn = [&](auto wait) __attribute__((always_inline)) {
     __builtin_amdgcn_sched_barrier(0);
-    lds_barrier();
+    if constexpr (decltype(wait)::value) lds_barrier();
+    else {
+      __atomic_signal_fence(__ATOMIC_SEQ_CST);
+      __builtin_amdgcn_s_barrier();
+      __atomic_signal_fence(__ATOMIC_SEQ_CST);
+    }
     __builtin_amdgcn_sched_barrier(0);
   };
+  const auto yes = std::true_type{};
+  const auto no = std::false_type{};
   if (i0 < i1) {
     // A record is spread two records ahead of its turn, into the place of the one two
     // before: the last reads of that were a barrier ago, the first reads are one ahead.
-    // ref of a record's values, as its sums need it: of the last four records.
+    // What a turn of weights writes to LDS is waited for at the end of the next turn, of
+    // products, still a barrier before it is read.  ref of a record's values, as its sums
+    // need it: of the last four records.
     Staged st[2];
     int there[4];
-    float refs[4];
+    float refs[4] = {};
     auto stage = [&](Staged& from, int i) __attribute__((always_inline)) {
       steps(from, (i - i0) & 3);
       spread(from, (i - i0) & 3);
     };
-    load(st[0], i0);
-    load(st[1], min(i0 + 1, i1 - 1));
+    look_up();
+    load(st[0]);
+    load(st[1]);
     stage(st[0], i0);
     there[0] = st[0].there, refs[0] = staged_ref;
-    load(st[0], min(i0 + 2, i1 - 1));
+    ref = refs[3] = staged_ref;
+    load(st[0]);
     stage(st[1], i0 + 1);
     there[1] = st[1].there, refs[1] = staged_ref;
-    load(st[1], min(i0 + 3, i1 - 1));
-    lds_barrier();
-    if (wave >= 4) turn();
+    load(st[1]);
+    // the first turn multiplies weights of 0 by values of a record before the first
+#pragma unroll
+    for (int rt = 0; rt < RT; ++rt)
+#pragma unroll
+      for (int part = 0; part < PARTS; ++part) weight[rt][part] = make_uint4(0, 0, 0, 0);
+    for (int n = wave; n < N; n += WAVES) frags[3][2 * J + n][lane] = make_uint4(0, 0, 0, 0);
+    turn(yes);
+    fetch(3);
+    if (wave >= 4) turn(no);
+    auto rescale = [&](float to) __attribute__((always_inline)) {
+      if (__builtin_expect(to != ref, 0)) {    // larger values: the sums in their unit
+        const float factor = ref / to;
+#pragma unroll
+        for (int rt = 0; rt < RT; ++rt)
+#pragma unroll
+          for (int n = 0; n < N; ++n) o[rt][n] *= factor;
+        ref = to;
+      }
+    };
     auto one = [&](int i, auto u) __attribute__((always_inline)) {
       constexpr int U = decltype(u)::value;             // (i - i0) % 4
       if (busy) {
+        rescale(refs[(U + 3) & 3]);
         __builtin_amdgcn_s_setprio(1);
-        if (i > i0) {
-          if (refs[(U + 3) & 3] != ref) {      // larger values: the sums in their unit
-            const float factor = ref / refs[(U + 3) & 3];
-#pragma unroll
-            for (int rt = 0; rt < RT; ++rt)
-#pragma unroll
-              for (int n = 0; n < N; ++n) o[rt][n] *= factor;
-            ref = refs[(U + 3) & 3];
-          }
-          add_values((U + 3) & 3);
-        }
-        scores(U);
+        multiply((U + 3) & 3, U, yes);
         __builtin_amdgcn_s_setprio(0);
       }
-      turn();
+      turn(yes);
       steps(st[U & 1], (U + 2) & 3);
-      if (busy) weights(U, i * 32, there[U]);
       spread(st[U & 1], (U + 2) & 3);
       there[(U + 2) & 3] = st[U & 1].there, refs[(U + 2) & 3] = staged_ref;
-      load(st[U & 1], min(i + 4, i1 - 1));
-      turn();
+      load(st[U & 1]);
+      if (busy) weights(U, i * 32, there[U]);
+      fetch(U);
+      turn(no);
     };
     int i = i0;
     for (;;) {
@@ -928,19 +968,11 @@ __global__ __launch_bounds__(512, 1) void attend_tiles(const TilesArgs a) {
       one(i, std::integral_constant<int, 3>{});
       if (++i == i1) break;
     }
-    if (wave < 4) turn();
+    if (wave < 4) turn(no);
     if (busy) {
       const int last = (i1 - 1 - i0) & 3;
-      const float r = last == 0 ? refs[0] : last == 1 ? refs[1] : last == 2 ? refs[2] : refs[3];
-      if (r != ref) {
-        const float factor = ref / r;
-#pragma unroll
-        for (int rt = 0; rt < RT; ++rt)
-#pragma unroll
-          for (int n = 0; n < N; ++n) o[rt][n] *= factor;
-        ref = r;
-      }
-      add_values(last);
+      rescale(last == 0 ? refs[0] : last == 1 ? refs[1] : last == 2 ? refs[2] : refs[3]);
+      multiply(last, 0, no);
     }
   }
   if (!busy) return;
