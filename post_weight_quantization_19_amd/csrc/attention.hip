@@ -537,8 +537,13 @@ __global__ __launch_bounds__(512, 1) void attend_tiles(const TilesArgs a) {
   __shared__ Scan sc;
   __shared__ float tops[WAVES];
   __shared__ uint4 frags[4][2 * J + N][64];    // [record % 4][keys (t, j), values n]
-  __shared__ __align__(16) float step_k[4][32];      // keys' steps times f
-  __shared__ __align__(16) float step_v[4][32];      // values' steps, PARTS 2
+  // Of a record's tokens: keys' steps times f, zero points of keys and values as -(1024 +
+  // z), values' steps over ref (float16: folded into the values, PARTS 1).  Values' in the
+  // order of a fragment's tokens, but for float32.
+  __shared__ __align__(16) float step_k[4][32], step_v[4][32];
+  __shared__ __align__(16) uint16_t zero_k[4][32], zero_v[4][32];
+  __shared__ __align__(16) _Float16 step_h[4][32];
+  __shared__ float2 about[4];                  // its ref; its tokens that are there
   __shared__ int entries[WAVES][64];           // table entries, a wave's own
   const int h = (int)(block_index() % a.cache.heads);
   const int64_t rest = block_index() / a.cache.heads;
@@ -622,6 +627,9 @@ __global__ __launch_bounds__(512, 1) void attend_tiles(const TilesArgs a) {
   // Records one after the other, up to the last.  Table entries come 64 at a time, and
   // that of the next record is read from LDS while this one is loaded.
   const int32_t* table = a.batch.table + s * a.batch.ldt;
+  const uint8_t* head_base = a.cache.records + (((int64_t)h << a.cache.blocks_shift) * R::bytes);
+  const int64_t page_bytes = ((int64_t)a.cache.heads << a.cache.blocks_shift) * R::bytes;
+  const int in_page = (1 << a.cache.blocks_shift) - 1;
   int entries_from = -64, next_page = -1, next_block = i0;
   auto look_up = [&]() __attribute__((always_inline)) {
     const int entry = next_block >> a.cache.blocks_shift;
@@ -633,90 +641,88 @@ __global__ __launch_bounds__(512, 1) void attend_tiles(const TilesArgs a) {
     }
     next_page = entries[wave][entry - entries_from];
   };
-  auto next_record = [&](int* block) __attribute__((always_inline)) -> const uint8_t* {
+  struct Where {
+    const uint8_t* rec;
+    int there;                               // its tokens that are there
+  };
+  auto next_record = [&]() __attribute__((always_inline)) {
     const int page = __builtin_amdgcn_readfirstlane(next_page);
-    *block = next_block;
-    const int64_t at = ((int64_t)page * a.cache.heads + h) << a.cache.blocks_shift;
-    const uint8_t* rec =
-        a.cache.records + (at + (next_block & ((1 << a.cache.blocks_shift) - 1))) * R::bytes;
+    const bool hole = page < 0 || page >= a.cache.pages;
+    Where w;
+    w.there = hole ? 0 : min(most - next_block * 32, 32);
+    // (a hole: any record, its tokens count for nothing)
+    w.rec = head_base + (hole ? 0 : page) * page_bytes + (next_block & in_page) * R::bytes;
     next_block = min(next_block + 1, i1 - 1);
     look_up();
-    return page < 0 || page >= a.cache.pages ? nullptr : rec;          // a hole
+    return w;
   };
-  // What a wave loads of a record, two records ahead of spreading it.  Every wave loads
-  // alike, without branches, and indexes past the last record are brought back to it:
-  // otherwise the compiler waits for all loads in flight at each use (576 instead of
-  // XXX us for 2048 bf16 tokens behind 8192).
-  struct Staged {
-    uint4 codes[PIECES];
-    u32x4_t words[2];                      // whose zero points and steps its codes need
-    uint32_t key;                          // and that of its keys, where PIECES is 2
-    uint32_t word;                         // lanes 0 .. 31 a token's key word, 32 .. its value's
-    int there;                             // tokens that are there
+  // What a wave loads of a record: its part of the codes, two records ahead of spreading
+  // it, and the words, three ahead.  Every wave loads alike, without branches, and indexes
+  // past the last record are brought back to it: otherwise the compiler waits for all
+  // loads in flight at each use (576 instead of 484 us for 2048 bf16 tokens behind 8192).
+  struct Codes {
+    uint4 c[PIECES];
   };
-  // Values need the words of tokens 4 g .. and 16 + 4 g .., keys those of col and 16 + col.
-  typedef u32x4_t __attribute__((aligned(4))) words_t;
-  const bool two = PIECES > 1;               // keys and values alike
-  const int words_at = R::words + (two || wave >= REGION ? 128 + 16 * g : 4 * col);
-  float ref = 0.0f, staged_ref = 0.0f;     // of the sums, of the values staged
-  auto unit_over = [&](float r) { return r > 0.0f ? kUnit / r : 0.0f; };
-  auto load = [&](Staged& st) __attribute__((always_inline)) {
-    int block;
-    const uint8_t* rec = next_record(&block);
-    st.there = rec ? min(most - block * 32, 32) : 0;
-    if (!rec) rec = a.cache.records;         // any record: its tokens count for nothing
-    st.word = ((const uint32_t*)(rec + R::words))[lane];
-    st.words[0] = *(const words_t*)(rec + words_at);
-    st.words[1] = *(const words_t*)(rec + words_at + 64);
-    if constexpr (PIECES == 2)
-      st.key = ((const uint32_t*)(rec + R::words))[2 * wave / J * 16 + col];
+  struct Words {
+    uint32_t word;                           // lanes 0 .. 31 a token's key word, 32 .. its value's
+    int there;
+  };
+  auto load_codes = [&](Codes& st, const Where& w) __attribute__((always_inline)) {
 #pragma unroll
     for (int i = 0; i < PIECES; ++i)
-      st.codes[i] = *(const uint4*)(rec + min(wave + WAVES * i, 2 * REGION - 1) * 1024 + lane * 16);
+      st.c[i] = *(const uint4*)(w.rec +
+                                (uint32_t)(min(wave + WAVES * i, 2 * REGION - 1) * 1024 + lane * 16));
   };
-  // Keys' steps of a record for all, and ref raised where a value's is above 8 of it.
-  auto steps = [&](const Staged& st, int buf) __attribute__((always_inline)) {
+  auto load_words = [&](Words& st, const Where& w) __attribute__((always_inline)) {
+    st.word = *(const uint32_t*)(w.rec + (uint32_t)(R::words + 4 * lane));
+    st.there = w.there;
+  };
+  // Wave 0: a record's steps and zero points for all; ref is raised where a value's step is
+  // above 8 of it.
+  float ref = 0.0f, staged_ref = 0.0f, unit = 0.0f;     // of the sums; of the values staged
+  auto steps = [&](const Words& st, int buf) __attribute__((always_inline)) {
+    if (wave != 0) return;
     const float step = word_step(st.word);
-    const bool there = (lane & 31) < st.there;
-    const float sv = lane >= 32 && there ? fmaxf(step, 0.0f) : 0.0f;       // 0 for a NaN
-    if (__builtin_expect(__any(sv > staged_ref * 8.0f), 0))
+    const int k = lane & 31;
+    const bool there = k < st.there;
+    const uint64_t nan = __ballot(step != step) >> 32;
+    const float sv = lane >= 32 && there && step == step ? step : 0.0f;
+    if (__builtin_expect(__any(sv > staged_ref * 8.0f), 0)) {
       staged_ref = __uint_as_float(
           __float_as_uint(fminf(fmaxf(wave_top(sv), 0x1p-100f), 0x1p100f)) & 0x7f800000u);
-    if (wave == 0) {
-      const uint64_t nan = __ballot(step != step) >> 32;
-      // whoever sees a token whose values are NaN gets a NaN
-      if (lane < 32)
-        step_k[buf][lane] = !there ? 0.0f : nan >> lane & 1 ? __builtin_nanf("") : step * f;
-      else if (PARTS == 2)
-        step_v[buf][lane - 32] = sv * unit_over(staged_ref);
+      unit = kUnit / staged_ref;
     }
+    const uint16_t zero = (uint16_t)(0xe400 | word_zero(st.word));
+    const int at = BITS == 8 ? k : (k & ~3) | (k & 1) << 1 | (k & 2) >> 1;
+    if (lane < 32) {
+      // whoever sees a token whose values are NaN gets a NaN
+      step_k[buf][k] = !there ? 0.0f : nan >> k & 1 ? __builtin_nanf("") : step * f;
+      zero_k[buf][k] = zero;
+    } else {
+      if constexpr (PARTS == 2) step_v[buf][k] = sv * unit;
+      else step_h[buf][at] = (_Float16)(sv * unit);
+      zero_v[buf][at] = zero;
+    }
+    if (lane == 0) about[buf] = make_float2(staged_ref, (float)st.there);
   };
-  auto spread = [&](const Staged& st, int buf) __attribute__((always_inline)) {
+  auto spread = [&](const Codes& st, int buf) __attribute__((always_inline)) {
 #pragma unroll
     for (int i = 0; i < PIECES; ++i) {
       const int at = wave + WAVES * i, piece = at % REGION;
       if (at >= 2 * REGION) break;
-      const uint32_t c[4] = {st.codes[i].x, st.codes[i].y, st.codes[i].z, st.codes[i].w};
+      const uint32_t c[4] = {st.c[i].x, st.c[i].y, st.c[i].z, st.c[i].w};
       if (at >= REGION) {
-        const uint32_t word[8] = {st.words[0][0], st.words[0][1], st.words[0][2], st.words[0][3],
-                                  st.words[1][0], st.words[1][1], st.words[1][2], st.words[1][3]};
-        uint32_t z0[4], z4[4], y[4] = {};
-        const float inv = unit_over(staged_ref);
-        float step[8];
+        const u32x2_t za = *(const u32x2_t*)&zero_v[buf][4 * g];
+        const u32x2_t zb = *(const u32x2_t*)&zero_v[buf][16 + 4 * g];
+        const uint32_t z0[4] = {za[0], za[1], zb[0], zb[1]};
+        uint32_t z4[4], y[4] = {};
+        if constexpr (BITS == 4)
+#pragma unroll
+          for (int k = 0; k < 4; ++k) z4[k] = (z0[k] & 0x000f000fu) << 4 | 0xd400d400u;
         if constexpr (PARTS == 1) {
-#pragma unroll
-          for (int k = 0; k < 8; ++k) step[k] = fmaxf(word_step(word[k]), 0.0f) * inv;
-          if (__builtin_expect(st.there < 32, 0))
-#pragma unroll
-            for (int k = 0; k < 8; ++k)
-              if (k / 4 * 16 + 4 * g + k % 4 >= st.there) step[k] = 0.0f;
-        }
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {          // two tokens of a fragment
-          const int e = k / 2 * 4 + (BITS == 8 ? k % 2 * 2 : k % 2), other = BITS == 8 ? 1 : 2;
-          const uint32_t z = __builtin_amdgcn_perm(word[e + other], word[e], 0x0c040c00u);
-          z0[k] = z | 0xe400e400u, z4[k] = (z & 0x000f000fu) << 4 | 0xd400d400u;
-          if constexpr (PARTS == 1) y[k] = two_halves(step[e], step[e + other]);
+          const u32x2_t ya = *(const u32x2_t*)&step_h[buf][4 * g];
+          const u32x2_t yb = *(const u32x2_t*)&step_h[buf][16 + 4 * g];
+          y[0] = ya[0], y[1] = ya[1], y[2] = yb[0], y[3] = yb[1];
         }
 #pragma unroll
         for (int k = 0; k < FR; ++k) {
@@ -742,8 +748,8 @@ __global__ __launch_bounds__(512, 1) void attend_tiles(const TilesArgs a) {
 #pragma unroll
         for (int k = 0; k < FR; ++k) {
           const int F = piece * FR + k;
-          const int z = word_zero(PIECES == 2 ? st.key : F / J ? st.words[1][0] : st.words[0][0]);
-          const uint32_t b0 = bias0(z, z), b4 = bias4(z, z);
+          const uint32_t z = zero_k[buf][F / J * 16 + col];
+          const uint32_t b0 = z | z << 16, b4 = (b0 & 0x000f000fu) << 4 | 0xd400d400u;
           uint4 v;
           if constexpr (BITS == 8)
             v = make_uint4(bytes_less(c[2 * k], 0x04010400u, b0),
@@ -769,10 +775,13 @@ __global__ __launch_bounds__(512, 1) void attend_tiles(const TilesArgs a) {
 #pragma unroll
     for (int n = 0; n < N; ++n) o[rt][n] = f32x4_t{0, 0, 0, 0};
   }
-  const f16x8_t ones = as_half8(make_uint4(0x3c003c00u, 0x3c003c00u, 0x3c003c00u, 0x3c003c00u));
+  u32x4_t one_words = {0x3c003c00u, 0x3c003c00u, 0x3c003c00u, 0x3c003c00u};
+  asm("" : "+v"(one_words));                 // kept, not made again for each record
+  const f16x8_t ones = __builtin_bit_cast(f16x8_t, one_words);
   const bool busy = wave * 16 < rows;
 
   f32x4_t score[RT][2], sk[2];             // of a record's tokens, and the tokens' steps
+  float2 now = make_float2(0.0f, 0.0f);    // about the record
   float e[RT][8];
   auto exps = [&](int rt) __attribute__((always_inline)) {
 #pragma unroll
@@ -863,13 +872,15 @@ __global__ __launch_bounds__(512, 1) void attend_tiles(const TilesArgs a) {
   };
   auto multiply = [&](int vb, int kb, auto keys) __attribute__((always_inline)) {
     constexpr int TOTAL = decltype(keys)::value ? kFrags : N;
-    if constexpr (TOTAL > N)
+    if constexpr (TOTAL > N) {
+      now = about[kb];
 #pragma unroll
       for (int t = 0; t < 2; ++t) {
         sk[t] = *(const f32x4_t*)&step_k[kb][16 * t + 4 * g];
 #pragma unroll
         for (int rt = 0; rt < RT; ++rt) score[rt][t] = f32x4_t{0, 0, 0, 0};
       }
+    }
     static_for_up<TOTAL>([&](auto kc) __attribute__((always_inline)) {
       constexpr int k = decltype(kc)::value;
       const f16x8_t x = ahead[k % kAhead];
@@ -899,28 +910,24 @@ __global__ __launch_bounds__(512, 1) void attend_tiles(const TilesArgs a) {
   const auto yes = std::true_type{};
   const auto no = std::false_type{};
   if (i0 < i1) {
-    // A record is spread two records ahead of its turn, into the place of the one two
-    // before: the last reads of that were a barrier ago, the first reads are one ahead.
-    // What a turn of weights writes to LDS is waited for at the end of the next turn, of
-    // products, still a barrier before it is read.  ref of a record's values, as its sums
-    // need it: of the last four records.
-    Staged st[2];
-    int there[4];
-    float refs[4] = {};
-    auto stage = [&](Staged& from, int i) __attribute__((always_inline)) {
-      steps(from, (i - i0) & 3);
-      spread(from, (i - i0) & 3);
-    };
+    // Wave 0 prepares a record's steps three records ahead of its turn, and the record is
+    // spread two ahead, into the place of the one two before: the last reads of that
+    // were a barrier ago, the first reads are one ahead.  What a turn of weights writes to
+    // LDS is waited for at the end of the next turn, of products.
+    Codes st[2];
+    Words wq[4];                             // two from the loop on
     look_up();
-    load(st[0]);
-    load(st[1]);
-    stage(st[0], i0);
-    there[0] = st[0].there, refs[0] = staged_ref;
-    ref = refs[3] = staged_ref;
-    load(st[0]);
-    stage(st[1], i0 + 1);
-    there[1] = st[1].there, refs[1] = staged_ref;
-    load(st[1]);
+    Where at[5];
+#pragma unroll
+    for (int k = 0; k < 5; ++k) {
+      at[k] = next_record();
+      if (k < 4) load_words(wq[k], at[k]);
+      if (k < 2) load_codes(st[k], at[k]);
+    }
+#pragma unroll
+    for (int k = 0; k < 3; ++k) steps(wq[k], k);
+    wq[1] = wq[3];                           // of the fourth record; the fifth's
+    load_words(wq[0], at[4]);
     // the first turn multiplies weights of 0 by values of a record before the first
 #pragma unroll
     for (int rt = 0; rt < RT; ++rt)
@@ -928,32 +935,40 @@ __global__ __launch_bounds__(512, 1) void attend_tiles(const TilesArgs a) {
       for (int part = 0; part < PARTS; ++part) weight[rt][part] = make_uint4(0, 0, 0, 0);
     for (int n = wave; n < N; n += WAVES) frags[3][2 * J + n][lane] = make_uint4(0, 0, 0, 0);
     turn(yes);
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      spread(st[k], k);
+      load_codes(st[k], at[k + 2]);
+    }
+    Where ahead_of = at[4];
+    turn(yes);
     fetch(3);
     if (wave >= 4) turn(no);
-    auto rescale = [&](float to) __attribute__((always_inline)) {
-      if (__builtin_expect(to != ref, 0)) {    // larger values: the sums in their unit
-        const float factor = ref / to;
+    auto rescale = [&]() __attribute__((always_inline)) {
+      if (__builtin_expect(now.x != ref, 0)) {   // larger values: the sums in their unit
+        const float factor = ref / now.x;
 #pragma unroll
         for (int rt = 0; rt < RT; ++rt)
 #pragma unroll
           for (int n = 0; n < N; ++n) o[rt][n] *= factor;
-        ref = to;
+        ref = now.x;
       }
     };
     auto one = [&](int i, auto u) __attribute__((always_inline)) {
       constexpr int U = decltype(u)::value;             // (i - i0) % 4
       if (busy) {
-        rescale(refs[(U + 3) & 3]);
+        rescale();
         __builtin_amdgcn_s_setprio(1);
         multiply((U + 3) & 3, U, yes);
         __builtin_amdgcn_s_setprio(0);
       }
       turn(yes);
-      steps(st[U & 1], (U + 2) & 3);
       spread(st[U & 1], (U + 2) & 3);
-      there[(U + 2) & 3] = st[U & 1].there, refs[(U + 2) & 3] = staged_ref;
-      load(st[U & 1]);
-      if (busy) weights(U, i * 32, there[U]);
+      load_codes(st[U & 1], ahead_of);
+      steps(wq[(U + 3) & 1], (U + 3) & 3);
+      ahead_of = next_record();
+      load_words(wq[(U + 3) & 1], ahead_of);
+      if (busy) weights(U, i * 32, __builtin_amdgcn_readfirstlane((int)now.y));
       fetch(U);
       turn(no);
     };
@@ -971,7 +986,7 @@ __global__ __launch_bounds__(512, 1) void attend_tiles(const TilesArgs a) {
     if (wave < 4) turn(no);
     if (busy) {
       const int last = (i1 - 1 - i0) & 3;
-      rescale(last == 0 ? refs[0] : last == 1 ? refs[1] : last == 2 ? refs[2] : refs[3]);
+      rescale();
       multiply(last, 0, no);
     }
   }
