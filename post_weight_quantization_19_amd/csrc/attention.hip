@@ -528,22 +528,26 @@ __global__ __launch_bounds__(512, 1) void attend_tiles(const TilesArgs a) {
   using R = Record<D, BITS>;
   constexpr int PARTS = std::is_same_v<T, float> ? 2 : 1;
   constexpr int J = D / 32, N = D / 16, WAVES = 8, ROWS = 16 * RT * WAVES;
-  constexpr int REGION = R::codes / 1024;      // pieces of 1 KB of a record's keys (or values)
-  constexpr int PIECES = (2 * REGION + WAVES - 1) / WAVES;    // 16-byte pieces of a thread
-  constexpr int FR = BITS == 8 ? 2 : 4;        // fragments of a piece
+  // A record's codes are spread in tasks of FT fragments from 4 WORDS bytes a lane: the
+  // keys', then the values', eight or more where there are as many.
+  constexpr int PIECES = 2 * R::codes / 1024, SPLIT = PIECES < WAVES ? 2 : 1;
+  constexpr int TASKS = PIECES * SPLIT, TURNS = (TASKS + WAVES - 1) / WAVES, WORDS = 4 / SPLIT;
+  constexpr int FT = (BITS == 8 ? 2 : 4) / SPLIT;
   // A weight is held as 2^8 of them (up to 2^12), a value's step over ref as kUnit (up to
   // 8 kUnit, which times 255 has to stay in float16 where the steps are folded in).
   constexpr float kUnit = PARTS == 1 ? 32.0f : 1.0f;
   __shared__ Scan sc;
   __shared__ float tops[WAVES];
-  __shared__ uint4 frags[4][2 * J + N][64];    // [record % 4][keys (t, j), values n]
-  // Of a record's tokens: keys' steps times f, zero points of keys and values as -(1024 +
-  // z), values' steps over ref (float16: folded into the values, PARTS 1).  Values' in the
-  // order of a fragment's tokens, but for float32.
+  __shared__ u32x4_t frags[4][2 * J + N][64];    // [record % 4][keys (t, j), values n]
+  // Of a record's tokens: keys' steps times f; zero points as -(1024 + z), a key's four times
+  // twice, values' in the order of a fragment's tokens; values' steps over ref, float16 in
+  // that order (folded into the values, PARTS 1) or float32.
   __shared__ __align__(16) float step_k[4][32], step_v[4][32];
-  __shared__ __align__(16) uint16_t zero_k[4][32], zero_v[4][32];
+  __shared__ __align__(16) uint32_t zero_k[4][32][4];
+  __shared__ __align__(16) uint16_t zero_v[4][32];
   __shared__ __align__(16) _Float16 step_h[4][32];
-  __shared__ float2 about[4];                  // its ref; its tokens that are there
+  __shared__ __align__(16) uint32_t one_h[4];  // four times two ones
+  __shared__ float2 about[4];                  // of a record: its ref; its tokens that are there
   __shared__ int entries[WAVES][64];           // table entries, a wave's own
   const int h = (int)(block_index() % a.cache.heads);
   const int64_t rest = block_index() / a.cache.heads;
@@ -653,7 +657,6 @@ __global__ __launch_bounds__(512, 1) void attend_tiles(const TilesArgs a) {
     // (a hole: any record, its tokens count for nothing)
     w.rec = head_base + (hole ? 0 : page) * page_bytes + (next_block & in_page) * R::bytes;
     next_block = min(next_block + 1, i1 - 1);
-    look_up();
     return w;
   };
   // What a wave loads of a record: its part of the codes, two records ahead of spreading
@@ -661,7 +664,7 @@ __global__ __launch_bounds__(512, 1) void attend_tiles(const TilesArgs a) {
   // past the last record are brought back to it: otherwise the compiler waits for all
   // loads in flight at each use (576 instead of 484 us for 2048 bf16 tokens behind 8192).
   struct Codes {
-    uint4 c[PIECES];
+    uint32_t c[TURNS][WORDS];
   };
   struct Words {
     uint32_t word;                           // lanes 0 .. 31 a token's key word, 32 .. its value's
@@ -669,9 +672,18 @@ __global__ __launch_bounds__(512, 1) void attend_tiles(const TilesArgs a) {
   };
   auto load_codes = [&](Codes& st, const Where& w) __attribute__((always_inline)) {
 #pragma unroll
-    for (int i = 0; i < PIECES; ++i)
-      st.c[i] = *(const uint4*)(w.rec +
-                                (uint32_t)(min(wave + WAVES * i, 2 * REGION - 1) * 1024 + lane * 16));
+    for (int i = 0; i < TURNS; ++i) {
+      const int task = min(wave + WAVES * i, TASKS - 1);
+      const uint8_t* from = w.rec + (uint32_t)(task / SPLIT * 1024 + task % SPLIT * (4 * WORDS) +
+                                               lane * 16);
+      if constexpr (SPLIT == 1) {
+        const u32x4_t x = *(const u32x4_t*)from;
+        st.c[i][0] = x[0], st.c[i][1] = x[1], st.c[i][2] = x[2], st.c[i][3] = x[3];
+      } else {
+        const u32x2_t x = *(const u32x2_t*)from;
+        st.c[i][0] = x[0], st.c[i][1] = x[1];
+      }
+    }
   };
   auto load_words = [&](Words& st, const Where& w) __attribute__((always_inline)) {
     st.word = *(const uint32_t*)(w.rec + (uint32_t)(R::words + 4 * lane));
@@ -692,75 +704,78 @@ __global__ __launch_bounds__(512, 1) void attend_tiles(const TilesArgs a) {
           __float_as_uint(fminf(fmaxf(wave_top(sv), 0x1p-100f), 0x1p100f)) & 0x7f800000u);
       unit = kUnit / staged_ref;
     }
-    const uint16_t zero = (uint16_t)(0xe400 | word_zero(st.word));
-    const int at = BITS == 8 ? k : (k & ~3) | (k & 1) << 1 | (k & 2) >> 1;
+    const uint32_t zero = 0xe400u | (uint32_t)word_zero(st.word);
+    // token 16 t + 4 g + i of a fragment: 8 g + 4 t, then the order of weight_part
+    const int i = BITS == 8 ? k & 3 : (k & 1) << 1 | (k & 2) >> 1;
+    const int at = (k >> 2 & 3) * 8 + (k >> 4) * 4 + i;
     if (lane < 32) {
       // whoever sees a token whose values are NaN gets a NaN
       step_k[buf][k] = !there ? 0.0f : nan >> k & 1 ? __builtin_nanf("") : step * f;
-      zero_k[buf][k] = zero;
+      const uint32_t two = zero | zero << 16;
+      *(u32x4_t*)&zero_k[buf][k][0] = u32x4_t{two, two, two, two};
     } else {
       if constexpr (PARTS == 2) step_v[buf][k] = sv * unit;
       else step_h[buf][at] = (_Float16)(sv * unit);
-      zero_v[buf][at] = zero;
+      zero_v[buf][at] = (uint16_t)zero;
     }
     if (lane == 0) about[buf] = make_float2(staged_ref, (float)st.there);
+    __builtin_amdgcn_s_waitcnt(0xc07f);        // there before the barrier (lgkmcnt(0))
   };
-  auto spread = [&](const Codes& st, int buf) __attribute__((always_inline)) {
+  // What a task needs of them, read a turn ahead.
+  struct Zeros {
+    u32x4_t zero[TURNS], step[TURNS];
+  };
+  Zeros zs;
+  auto fetch_zeros = [&](int buf) __attribute__((always_inline)) {
 #pragma unroll
-    for (int i = 0; i < PIECES; ++i) {
-      const int at = wave + WAVES * i, piece = at % REGION;
-      if (at >= 2 * REGION) break;
-      const uint32_t c[4] = {st.c[i].x, st.c[i].y, st.c[i].z, st.c[i].w};
-      if (at >= REGION) {
-        const u32x2_t za = *(const u32x2_t*)&zero_v[buf][4 * g];
-        const u32x2_t zb = *(const u32x2_t*)&zero_v[buf][16 + 4 * g];
-        const uint32_t z0[4] = {za[0], za[1], zb[0], zb[1]};
-        uint32_t z4[4], y[4] = {};
-        if constexpr (BITS == 4)
+    for (int i = 0; i < TURNS; ++i) {
+      const int first = min(wave + WAVES * i, TASKS - 1) * FT;
+      const bool values = first >= 2 * J;
+      zs.zero[i] = *(const u32x4_t*)(values ? (const void*)&zero_v[buf][8 * g]
+                                            : (const void*)&zero_k[buf][first / J * 16 + col][0]);
+      if constexpr (PARTS == 1)
+        zs.step[i] =
+            *(const u32x4_t*)(values ? (const void*)&step_h[buf][8 * g] : (const void*)&one_h[0]);
+    }
+  };
+  auto spread = [&](const Codes& st, int buf, int i) __attribute__((always_inline)) {
+    {
+      const int task = min(wave + WAVES * i, TASKS - 1), first = task * FT;
+      const uint32_t(&c)[WORDS] = st.c[i];
+      const u32x4_t z0 = zs.zero[i];
+      u32x4_t v[FT];
+      if constexpr (BITS == 8) {
 #pragma unroll
-          for (int k = 0; k < 4; ++k) z4[k] = (z0[k] & 0x000f000fu) << 4 | 0xd400d400u;
-        if constexpr (PARTS == 1) {
-          const u32x2_t ya = *(const u32x2_t*)&step_h[buf][4 * g];
-          const u32x2_t yb = *(const u32x2_t*)&step_h[buf][16 + 4 * g];
-          y[0] = ya[0], y[1] = ya[1], y[2] = yb[0], y[3] = yb[1];
-        }
-#pragma unroll
-        for (int k = 0; k < FR; ++k) {
-          const uint32_t w0 = BITS == 8 ? c[2 * k] : c[k / 2 * 2];
-          const uint32_t w1 = BITS == 8 ? c[2 * k + 1] : c[k / 2 * 2 + 1];
-          uint32_t v[4];
-          if constexpr (BITS == 8) {
-            v[0] = bytes_less(w0, 0x04010400u, z0[0]), v[1] = bytes_less(w0, 0x04030402u, z0[1]);
-            v[2] = bytes_less(w1, 0x04010400u, z0[2]), v[3] = bytes_less(w1, 0x04030402u, z0[3]);
-          } else if (k % 2 == 0) {
-            v[0] = low_less(w0, z0[0]), v[1] = low_less(w0 >> 8, z0[1]);
-            v[2] = low_less(w1, z0[2]), v[3] = low_less(w1 >> 8, z0[3]);
-          } else {
-            v[0] = high_less(w0, z4[0]), v[1] = high_less(w0 >> 8, z4[1]);
-            v[2] = high_less(w1, z4[2]), v[3] = high_less(w1 >> 8, z4[3]);
-          }
-          if constexpr (PARTS == 1)
-#pragma unroll
-            for (int n = 0; n < 4; ++n) v[n] = as_word(as_half2(v[n]) * as_half2(y[n]));
-          frags[buf][2 * J + piece * FR + k][lane] = make_uint4(v[0], v[1], v[2], v[3]);
-        }
+        for (int k = 0; k < FT; ++k)
+          v[k] = u32x4_t{bytes_less(c[2 * k], 0x04010400u, z0[0]),
+                         bytes_less(c[2 * k], 0x04030402u, z0[1]),
+                         bytes_less(c[2 * k + 1], 0x04010400u, z0[2]),
+                         bytes_less(c[2 * k + 1], 0x04030402u, z0[3])};
       } else {
+        u32x4_t z4;
 #pragma unroll
-        for (int k = 0; k < FR; ++k) {
-          const int F = piece * FR + k;
-          const uint32_t z = zero_k[buf][F / J * 16 + col];
-          const uint32_t b0 = z | z << 16, b4 = (b0 & 0x000f000fu) << 4 | 0xd400d400u;
-          uint4 v;
-          if constexpr (BITS == 8)
-            v = make_uint4(bytes_less(c[2 * k], 0x04010400u, b0),
-                           bytes_less(c[2 * k], 0x04030402u, b0),
-                           bytes_less(c[2 * k + 1], 0x04010400u, b0),
-                           bytes_less(c[2 * k + 1], 0x04030402u, b0));
-          else
-            v = make_uint4(low_less(c[k], b0), high_less(c[k], b4), low_less(c[k] >> 8, b0),
-                           high_less(c[k] >> 8, b4));
-          frags[buf][F][lane] = v;
+        for (int k = 0; k < 4; ++k) z4[k] = (z0[k] & 0x000f000fu) << 4 | 0xd400d400u;
+        if (first >= 2 * J) {
+#pragma unroll
+          for (int k = 0; k < FT; k += 2) {
+            v[k] = u32x4_t{low_less(c[k], z0[0]), low_less(c[k] >> 8, z0[1]),
+                           low_less(c[k + 1], z0[2]), low_less(c[k + 1] >> 8, z0[3])};
+            v[k + 1] = u32x4_t{high_less(c[k], z4[0]), high_less(c[k] >> 8, z4[1]),
+                               high_less(c[k + 1], z4[2]), high_less(c[k + 1] >> 8, z4[3])};
+          }
+        } else {
+#pragma unroll
+          for (int k = 0; k < FT; ++k)
+            v[k] = u32x4_t{low_less(c[k], z0[0]), high_less(c[k], z4[0]),
+                           low_less(c[k] >> 8, z0[0]), high_less(c[k] >> 8, z4[0])};
         }
+      }
+#pragma unroll
+      for (int k = 0; k < FT; ++k) {
+        if constexpr (PARTS == 1)              // (keys: times 1)
+#pragma unroll
+          for (int n = 0; n < 4; ++n) v[k][n] = as_word(as_half2(v[k][n]) * as_half2(zs.step[i][n]));
+        frags[buf][first + k][lane] = v[k];
       }
     }
   };
@@ -799,10 +814,9 @@ __global__ __launch_bounds__(512, 1) void attend_tiles(const TilesArgs a) {
   // Weights 2^(score - maximum + 8) of a record's tokens; p0 its first token, n those
   // that are there.  The maximum is raised once a score is 4 above it.
   uint4 weight[RT][PARTS];
+  // (e as exps left them)
   auto weights = [&](int buf, int p0, int n) __attribute__((always_inline)) {
     const bool masked = p0 + 32 > least || n < 32;
-#pragma unroll
-    for (int rt = 0; rt < RT; ++rt) exps(rt);
     if (masked)
 #pragma unroll
       for (int rt = 0; rt < RT; ++rt) hide(rt, p0, n);
@@ -863,14 +877,14 @@ __global__ __launch_bounds__(512, 1) void attend_tiles(const TilesArgs a) {
   f16x8_t ahead[kAhead];
   auto fragment = [&](int k, int vb, int kb) __attribute__((always_inline)) {
     const int i = k - N;                       // keys: j, then t
-    return k < N ? as_half8(frags[vb][2 * J + k][lane])
-                 : as_half8(frags[kb][i % 2 * J + i / 2][lane]);
+    return __builtin_bit_cast(
+        f16x8_t, k < N ? frags[vb][2 * J + k][lane] : frags[kb][i % 2 * J + i / 2][lane]);
   };
   auto fetch = [&](int vb) __attribute__((always_inline)) {
 #pragma unroll
     for (int k = 0; k < kAhead; ++k) ahead[k] = fragment(k, vb, 0);
   };
-  auto multiply = [&](int vb, int kb, auto keys) __attribute__((always_inline)) {
+  auto multiply = [&](int vb, int kb, auto keys, auto&& between) __attribute__((always_inline)) {
     constexpr int TOTAL = decltype(keys)::value ? kFrags : N;
     if constexpr (TOTAL > N) {
       now = about[kb];
@@ -893,6 +907,7 @@ __global__ __launch_bounds__(512, 1) void attend_tiles(const TilesArgs a) {
           else
             score[rt][(k - N) % 2] = mfma(x, qf[rt][part][(k - N) / 2], score[rt][(k - N) % 2]);
         }
+      between(kc);
       __builtin_amdgcn_sched_barrier(0);
     });
   };
@@ -921,6 +936,7 @@ __global__ __launch_bounds__(512, 1) void attend_tiles(const TilesArgs a) {
 #pragma unroll
     for (int k = 0; k < 5; ++k) {
       at[k] = next_record();
+      look_up();
       if (k < 4) load_words(wq[k], at[k]);
       if (k < 2) load_codes(st[k], at[k]);
     }
@@ -933,11 +949,14 @@ __global__ __launch_bounds__(512, 1) void attend_tiles(const TilesArgs a) {
     for (int rt = 0; rt < RT; ++rt)
 #pragma unroll
       for (int part = 0; part < PARTS; ++part) weight[rt][part] = make_uint4(0, 0, 0, 0);
-    for (int n = wave; n < N; n += WAVES) frags[3][2 * J + n][lane] = make_uint4(0, 0, 0, 0);
+    for (int n = wave; n < N; n += WAVES) frags[3][2 * J + n][lane] = u32x4_t{0, 0, 0, 0};
+    if (threadIdx.x < 4) one_h[threadIdx.x] = 0x3c003c00u;
     turn(yes);
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
-      spread(st[k], k);
+      fetch_zeros(k);
+#pragma unroll
+      for (int n = 0; n < TURNS; ++n) spread(st[k], k, n);
       load_codes(st[k], at[k + 2]);
     }
     Where ahead_of = at[4];
@@ -956,19 +975,27 @@ __global__ __launch_bounds__(512, 1) void attend_tiles(const TilesArgs a) {
     };
     auto one = [&](int i, auto u) __attribute__((always_inline)) {
       constexpr int U = decltype(u)::value;             // (i - i0) % 4
-      if (busy) {
-        rescale();
-        __builtin_amdgcn_s_setprio(1);
-        multiply((U + 3) & 3, U, yes);
-        __builtin_amdgcn_s_setprio(0);
-      }
+      rescale();
+      __builtin_amdgcn_s_setprio(1);
+      fetch_zeros((U + 2) & 3);
+      Words& wn = wq[(U + 3) & 1];
+      const Words old = wn;
+      multiply((U + 3) & 3, U, yes, [&](auto kc) __attribute__((always_inline)) {
+        constexpr int k = decltype(kc)::value;
+        // between the products, once the zero points have come from LDS
+        if constexpr (k >= kFrags / 2 && k < kFrags / 2 + TURNS)
+          spread(st[U & 1], (U + 2) & 3, k - kFrags / 2);
+        if constexpr (k == kFrags / 2 + TURNS) load_codes(st[U & 1], ahead_of);
+        if constexpr (k == kFrags / 2 + TURNS + 1) ahead_of = next_record();
+        if constexpr (k == kFrags / 2 + TURNS + 2) load_words(wn, ahead_of);
+      });
+      __builtin_amdgcn_s_setprio(0);
       turn(yes);
-      spread(st[U & 1], (U + 2) & 3);
-      load_codes(st[U & 1], ahead_of);
-      steps(wq[(U + 3) & 1], (U + 3) & 3);
-      ahead_of = next_record();
-      load_words(wq[(U + 3) & 1], ahead_of);
-      if (busy) weights(U, i * 32, __builtin_amdgcn_readfirstlane((int)now.y));
+#pragma unroll
+      for (int rt = 0; rt < RT; ++rt) exps(rt);
+      weights(U, i * 32, __builtin_amdgcn_readfirstlane((int)now.y));
+      steps(old, (U + 3) & 3);
+      look_up();
       fetch(U);
       turn(no);
     };
@@ -984,10 +1011,10 @@ __global__ __launch_bounds__(512, 1) void attend_tiles(const TilesArgs a) {
       if (++i == i1) break;
     }
     if (wave < 4) turn(no);
-    if (busy) {
+    {
       const int last = (i1 - 1 - i0) & 3;
       rescale();
-      multiply(last, 0, no);
+      multiply(last, 0, no, [](auto) {});
     }
   }
   if (!busy) return;
