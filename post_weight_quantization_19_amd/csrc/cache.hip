@@ -180,8 +180,188 @@ __global__ __launch_bounds__(256) void read_rows(const CacheRowsLaunch a) {
   store8((T*)dst.p + t * dst.ts + h * dst.hs + d, x);
 }
 
+// Blocks of 32 tokens that a batch's rows touch, sequence after sequence: at least one of
+// a sequence with rows, at most rows / 32 + 2.
+__device__ __forceinline__ int blocks_of(const Seq& q) {
+  const int rows = q.r1 - q.r0, from = max(q.len - rows, 0);
+  return rows > 0 ? (max(q.len - 1, 0) >> 5) - (from >> 5) + 1 : 0;
+}
+struct Window {
+  int seq, block;
+};
+// The window-th block; seq -1 past the last.
+__device__ __forceinline__ Window find_window(const CacheBatch& b, int64_t window) {
+  __shared__ int64_t sums[4];
+  __shared__ Window found;
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  if (threadIdx.x == 0) found.seq = -1;
+  int64_t before = 0;
+  for (int base = 0; base < b.nseq; base += 256) {
+    const int s = base + threadIdx.x;
+    Seq q{0, 0, 0};
+    if (s < b.nseq) q = sequence(b, s);
+    const int64_t n = blocks_of(q);
+    int64_t in = n;
+#pragma unroll
+    for (int o = 1; o < 64; o <<= 1) {
+      const int64_t u = __shfl_up(in, o, 64);
+      if (lane >= o) in += u;
+    }
+    __syncthreads();
+    if (lane == 63) sums[wave] = in;
+    __syncthreads();
+    int64_t at = before + in - n;
+    for (int w = 0; w < 4; ++w) {
+      if (w < wave) at += sums[w];
+      before += sums[w];
+    }
+    if (window >= at && window < at + n)
+      found = Window{s, (int)(window - at) + (max(q.len - (q.r1 - q.r0), 0) >> 5)};
+    if (before > window) break;
+  }
+  __syncthreads();
+  return found;
+}
+
+// A workgroup per block and head: its record is put together in LDS, and written in pieces
+// of 16 bytes where all of its tokens are the call's.
+template <typename T, int D, int BITS>
+__global__ __launch_bounds__(256) void write_blocks(const CacheRowsLaunch a) {
+  using R = Record<D, BITS>;
+  constexpr int TH = D / 8, AT_ONCE = 256 / TH, TURNS = 32 / AT_ONCE;
+  __shared__ __align__(16) uint8_t image[R::bytes];
+  const int h = (int)(block_index() % a.cache.heads);
+  const Window w = find_window(a.batch, block_index() / a.cache.heads);
+  if (w.seq < 0) return;
+  const Seq q = sequence(a.batch, w.seq);
+  const uint8_t* rec = record_of(a.cache, a.batch.table + w.seq * a.batch.ldt, a.batch.width,
+                                 w.block, h);
+  if (!rec) return;
+  const int first = q.len - (q.r1 - q.r0) - w.block * 32;    // tokens first .. end - 1 are new
+  const int end = min(q.len - w.block * 32, 32);
+  if (end <= max(first, 0)) return;
+  const int d = (int)(threadIdx.x % TH) * 8, p0 = (int)threadIdx.x / TH;
+  float x[2][TURNS][8];
+#pragma unroll
+  for (int of = 0; of < 2; ++of)
+#pragma unroll
+    for (int i = 0; i < TURNS; ++i) {
+      const int p = min(max(p0 + AT_ONCE * i, first), end - 1);
+      const CacheTensor& src = of ? a.v : a.k;
+      load8((const T*)src.p + (int64_t)(q.r0 + p - first) * src.ts + h * src.hs + d, x[of][i]);
+    }
+#pragma unroll
+  for (int of = 0; of < 2; ++of)
+#pragma unroll
+    for (int i = 0; i < TURNS; ++i) {
+      const int p = p0 + AT_ONCE * i;
+      int c[8];
+      const uint32_t word = quantize<D, BITS>(x[of][i], c);
+      if (d == 0) *(uint32_t*)(image + R::words + of * 128 + 4 * p) = word;
+      if (of == 0) {
+        uint32_t v[2] = {0, 0};
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          if constexpr (BITS == 8) v[e / 4] |= (uint32_t)c[e] << (8 * (e % 4));
+          else v[0] |= (uint32_t)c[e] << (4 * (e / 2) + 16 * (e % 2));
+        }
+#pragma unroll
+        for (int e = 0; e < BITS / 4; ++e) *(uint32_t*)(image + R::key_at(p, d) + 4 * e) = v[e];
+      } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          int byte = c[e];
+          if constexpr (BITS == 4) byte |= __shfl_xor(c[e], 2, 64) << 4;
+          if (BITS == 8 || d % 32 < 16)
+            image[R::codes + R::value_at(p, d + e)] = (uint8_t)byte;
+        }
+      }
+    }
+  __syncthreads();
+  uint8_t* out = a.cache.records + (rec - a.cache.records);
+  if (first <= 0 && end == 32) {
+    for (int i = threadIdx.x; i < R::bytes / 16; i += 256)
+      ((uint4*)out)[i] = ((const uint4*)image)[i];
+    return;
+  }
+  // the new tokens' words and key codes, and single bytes of the value codes
+  for (int i = threadIdx.x; i < 64; i += 256)
+    if ((i & 31) >= first && (i & 31) < end)
+      ((uint32_t*)(out + R::words))[i] = ((const uint32_t*)(image + R::words))[i];
+  for (int i = threadIdx.x; i < 32 * TH; i += 256) {
+    const int p = i / TH;
+    if (p < first || p >= end) continue;
+    const int at = R::key_at(p, i % TH * 8);
+#pragma unroll
+    for (int e = 0; e < BITS / 4; ++e)
+      *(uint32_t*)(out + at + 4 * e) = *(const uint32_t*)(image + at + 4 * e);
+  }
+  for (int i = threadIdx.x; i < R::codes; i += 256) {
+    const int n = i / 1024 * 16 + i % 16;                    // byte of lane i / 16 % 64
+    const int p = n % 8 / 4 * 16 + i / 256 % 4 * 4 + n % 4;
+    if (p >= first && p < end) out[R::codes + i] = image[R::codes + i];
+  }
+}
+
+// A workgroup per block and head: the record through LDS.
+template <typename T, int D, int BITS>
+__global__ __launch_bounds__(256) void read_blocks(const CacheRowsLaunch a) {
+  using R = Record<D, BITS>;
+  constexpr int TH = D / 8, AT_ONCE = 256 / TH, TURNS = 32 / AT_ONCE;
+  __shared__ __align__(16) uint8_t image[R::bytes];
+  const int h = (int)(block_index() % a.cache.heads);
+  const Window w = find_window(a.batch, block_index() / a.cache.heads);
+  if (w.seq < 0) return;
+  const Seq q = sequence(a.batch, w.seq);
+  const uint8_t* rec = record_of(a.cache, a.batch.table + w.seq * a.batch.ldt, a.batch.width,
+                                 w.block, h);
+  const int first = q.len - (q.r1 - q.r0) - w.block * 32, end = min(q.len - w.block * 32, 32);
+  for (int i = threadIdx.x; i < R::bytes / 16; i += 256)
+    ((uint4*)image)[i] = rec ? ((const uint4*)rec)[i] : make_uint4(0, 0, 0, 0);
+  __syncthreads();
+  const int d = (int)(threadIdx.x % TH) * 8, p0 = (int)threadIdx.x / TH;
+  if (w.block == 0 && first < 0) {                    // rows before the first token
+    const float none[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+    for (int p = first + p0; p < 0 && p - first < q.r1 - q.r0; p += AT_ONCE) {
+      store8((T*)a.k.p + (int64_t)(q.r0 + p - first) * a.k.ts + h * a.k.hs + d, none);
+      store8((T*)a.v.p + (int64_t)(q.r0 + p - first) * a.v.ts + h * a.v.hs + d, none);
+    }
+  }
+#pragma unroll
+  for (int of = 0; of < 2; ++of)
+#pragma unroll
+    for (int i = 0; i < TURNS; ++i) {
+      const int p = p0 + AT_ONCE * i;
+      if (p < first || p >= end) continue;
+      const uint32_t word = *(const uint32_t*)(image + R::words + of * 128 + 4 * p);
+      float x[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        int c;
+        if (of == 0) {
+          const uint32_t v = *(const uint32_t*)(image + R::key_at(p, d) + (BITS == 8 ? e / 4 * 4 : 0));
+          c = BITS == 8 ? (v >> (8 * (e % 4))) & 255 : (v >> (4 * (e / 2) + 16 * (e % 2))) & 15;
+        } else {
+          c = image[R::codes + R::value_at(p, d + e)];
+          if constexpr (BITS == 4) c = (c >> (d % 32 < 16 ? 0 : 4)) & 15;
+        }
+        x[e] = (float)(c - word_zero(word)) * word_step(word);
+      }
+      const CacheTensor& dst = of ? a.v : a.k;
+      store8((T*)dst.p + (int64_t)(q.r0 + p - first) * dst.ts + h * dst.hs + d, x);
+    }
+}
+
 template <typename T, int D, int BITS>
 void launch_rows_of(const CacheRowsLaunch& a, bool write, hipStream_t st) {
+  // Many rows to a sequence: whole blocks.  (XXX)
+  if (a.batch.ntok >= 4 * (int64_t)a.batch.nseq) {
+    const int64_t windows = a.batch.ntok / 32 + 2 * (int64_t)a.batch.nseq;
+    const dim3 grid = block_grid(windows * a.cache.heads);
+    if (write) write_blocks<T, D, BITS><<<grid, 256, 0, st>>>(a);
+    else read_blocks<T, D, BITS><<<grid, 256, 0, st>>>(a);
+    return;
+  }
   const int64_t heads = (int64_t)a.batch.ntok * a.cache.heads * 2;
   const dim3 grid = block_grid((heads * (D / 8) + 255) / 256);
   if (write) write_rows<T, D, BITS><<<grid, 256, 0, st>>>(a);
