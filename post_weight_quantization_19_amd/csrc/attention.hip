@@ -115,12 +115,16 @@ __device__ __forceinline__ void store_row4(uint16_t* p, const float (&y)[4]) {
   *(any8*)p = __builtin_bit_cast(any8, v);
 }
 
-// Partial results: a slot has 16 rows of D sums, then 16 maxima, then 16 totals.
+// Partial results: a slot has ROWS rows of D sums, then their maxima, then their totals.
 template <int D> constexpr int kSlot = kRows * (D + 2);
+// Where the slots of a row are: n of them from `first` on (of its key head), row k of each.
+// n -1: the result is in out already.
+struct __attribute__((aligned(16))) Found {
+  int first, n, k, unused;
+};
 
 struct Walk {
   CacheBatch batch;
-  const CacheView* cache;
   int group, capacity;
   __device__ __forceinline__ Seq seq(int s) const { return sequence(batch, s); }
   __device__ __forceinline__ int items(const Seq& q) const {
@@ -131,8 +135,8 @@ struct Walk {
   }
 };
 
-// Sums over the workgroup's first 256 threads of two numbers (others give 0); before: the sums of the
-// threads before this one.
+// Sums over the workgroup's first 256 threads of two numbers (others give 0); before: the
+// sums of the threads before this one.
 __device__ __forceinline__ void scan2(int64_t a, int64_t b, int64_t* before_a, int64_t* before_b,
                                       int64_t* all_a, int64_t* all_b, int64_t (*red)[2]) {
   int64_t ia = a, ib = b;
@@ -155,46 +159,60 @@ __device__ __forceinline__ void scan2(int64_t a, int64_t b, int64_t* before_a, i
   *all_a = ta, *all_b = tb;
 }
 
-// Where a tile, or a sequence, stands among all items of a key head.
-struct Place {
-  int seq;                 // -1: past the end
-  int64_t item, tile;      // first item and first tile of the sequence
-};
 struct Scan {
   int64_t red[8][2];
   int64_t found[3];
 };
-// Total tiles of a key head.
-__device__ __forceinline__ int64_t total_tiles(const Walk& w, Scan& sc) {
-  int64_t mine = 0;
-  for (int s = threadIdx.x; s < w.batch.nseq; s += 256) {
-    const Seq q = w.seq(s);
-    mine += (int64_t)w.items(q) * w.tiles(q);
-  }
-  int64_t b0, b1, all, none;
-  scan2(mine, 0, &b0, &b1, &all, &none, sc.red);
-  return all;
-}
-// The sequence that holds tile `tile` (want < 0), or the place of sequence `want`.
-__device__ __forceinline__ Place locate(const Walk& w, int64_t tile, int want, Scan& sc) {
-  if (threadIdx.x == 0) sc.found[0] = -1;
-  int64_t item0 = 0, tile0 = 0;
-  for (int base = 0; base < w.batch.nseq; base += 256) {
-    const int s = base + threadIdx.x;
-    int64_t it = 0, ti = 0;
+
+// Worker w's share of all tiles of a key head: c tiles (at least one) from w c on.
+struct Share {
+  int seq;                 // that holds the first of them; -1: there are none
+  int64_t c, total;
+  int64_t item, tile;      // the sequence's first item and tile
+};
+__device__ __forceinline__ Share share_of(const Walk& w, int64_t worker, int64_t workers,
+                                          Scan& sc) {
+  auto counts = [&](int s, int64_t* it, int64_t* ti) {
+    *it = *ti = 0;
     if (s < w.batch.nseq) {
       const Seq q = w.seq(s);
-      it = w.items(q), ti = it * w.tiles(q);
+      *it = w.items(q), *ti = *it * w.tiles(q);
     }
-    int64_t bi, bt, ai, at;
-    scan2(it, ti, &bi, &bt, &ai, &at, sc.red);
+  };
+  if (threadIdx.x == 0) sc.found[0] = -1;
+  int64_t it, ti, bi, bt, ai, at;
+  counts(threadIdx.x, &it, &ti);
+  scan2(it, ti, &bi, &bt, &ai, &at, sc.red);
+  int64_t total = at;
+  if (w.batch.nseq > 256) {
+    int64_t mine = 0, x, y, none;
+    for (int s = 256 + threadIdx.x; s < w.batch.nseq; s += 256) {
+      counts(s, &x, &y);
+      mine += y;
+    }
+    int64_t all;
+    scan2(mine, 0, &x, &y, &all, &none, sc.red);
+    total += all;
+  }
+  Share r;
+  r.total = total;
+  r.c = max((total + workers - 1) / workers, (int64_t)1);
+  const int64_t tile = worker * r.c;
+  int64_t item0 = 0, tile0 = 0;
+  for (int base = 0;; base += 256) {
+    if (base > 0) {
+      counts(base + threadIdx.x, &it, &ti);
+      scan2(it, ti, &bi, &bt, &ai, &at, sc.red);
+    }
     bi += item0, bt += tile0;
-    if (s < w.batch.nseq && (want >= 0 ? s == want : tile >= bt && tile < bt + ti))
-      sc.found[0] = s, sc.found[1] = bi, sc.found[2] = bt;
+    if (tile >= bt && tile < bt + ti)
+      sc.found[0] = base + threadIdx.x, sc.found[1] = bi, sc.found[2] = bt;
     item0 += ai, tile0 += at;
+    if (tile < tile0 || base + 256 >= w.batch.nseq) break;
   }
   __syncthreads();
-  return Place{(int)sc.found[0], sc.found[1], sc.found[2]};
+  r.seq = (int)sc.found[0], r.item = sc.found[1], r.tile = sc.found[2];
+  return r;
 }
 
 struct RowsArgs {
@@ -205,40 +223,42 @@ struct RowsArgs {
   int64_t workers, items;
   float scale;
   float* slots;
+  Found* found;            // of each row: token * group + query head of the key head's
 };
 
-// Tiles of a worker: at least one.
-__device__ __forceinline__ int64_t share(int64_t total, int64_t workers) {
-  return max((total + workers - 1) / workers, (int64_t)1);
-}
-
-// Attention of 16 rows at a time: worker w of a key head takes the tiles w c ..
-// w c + c - 1 of all items in a row, and each of its waves 32 tokens of a tile.
+// Attention of 16 rows at a time: worker w of a key head takes the tiles w c .. w c + c - 1
+// of all items in a row, and each of its waves 32 tokens of a tile, by itself: a record
+// is spread in the registers of the wave that multiplies by it, with the next one's codes
+// on the way.
+#ifndef XOCC
+#define XOCC 2
+#endif
 template <typename T, int D, int BITS>
-__global__ __launch_bounds__(256) void attend_rows(const RowsArgs a) {
+__global__ __launch_bounds__(256, D == 256 ? 1 : XOCC) void attend_rows(const RowsArgs a) {
   using R = Record<D, BITS>;
   constexpr int PARTS = std::is_same_v<T, float> ? 2 : 1;
-  constexpr int J = D / 32, N = D / 16, KW = R::lane_bytes / 4;
+  constexpr int J = D / 32, N = D / 16, KW = R::lane_bytes / 16;
   __shared__ Scan sc;
+  __shared__ int entries[4][64];
   __shared__ float sm[4][kRows], sl[4][kRows];
   __shared__ float so[4][kRows][D + 4];
   const int h = (int)(block_index() % a.cache.heads);
   const int64_t w = block_index() / a.cache.heads;
   if (w >= a.workers) return;
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, g = lane >> 4, col = lane & 15;
-  const Walk walk{a.batch, &a.cache, a.group, a.capacity};
-  const int64_t total = total_tiles(walk, sc);
-  const int64_t c = share(total, a.workers);
-  const int64_t end = min(total, (w + 1) * c);
-  int64_t at = w * c;
-  if (at >= end) return;
-  __syncthreads();
-  const Place place = locate(walk, at, -1, sc);
-  if (place.seq < 0) return;
-  int s = place.seq;
-  int64_t item0 = place.item, tile0 = place.tile;
+  const int lane = threadIdx.x & 63, g = lane >> 4, col = lane & 15;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6) & 3;
+  const Walk walk{a.batch, a.group, a.capacity};
+  const Share sh = share_of(walk, w, a.workers, sc);
+  const int64_t end = min(sh.total, (w + 1) * sh.c);
+  int64_t at = w * sh.c;
+  if (at >= end || sh.seq < 0) return;
+  int s = sh.seq;
+  int64_t item0 = sh.item, tile0 = sh.tile;
   Seq q = walk.seq(s);
   int per = walk.tiles(q), count = walk.items(q);
+  const uint8_t* head_base = a.cache.records + (((int64_t)h << a.cache.blocks_shift) * R::bytes);
+  const int64_t page_bytes = ((int64_t)a.cache.heads << a.cache.blocks_shift) * R::bytes;
+  const int in_page = (1 << a.cache.blocks_shift) - 1;
   while (at < end) {
     while (at >= tile0 + (int64_t)per * count) {       // the next sequence with tiles
       tile0 += (int64_t)per * count, item0 += count;
@@ -246,196 +266,266 @@ __global__ __launch_bounds__(256) void attend_rows(const RowsArgs a) {
       q = walk.seq(s);
       per = walk.tiles(q), count = walk.items(q);
     }
-    const int in = (int)((at - tile0) / per);          // item of the sequence
+    const int in = count == 1 ? 0 : (int)((at - tile0) / per);     // item of the sequence
     const int64_t item_tile = tile0 + (int64_t)in * per;
     const int ta = (int)(at - item_tile), tb = (int)min((int64_t)per, end - item_tile);
     const int64_t item = item0 + in;
     at = item_tile + tb;
     if (item >= a.items) return;                       // starts that descend
     const int rows = (int)min((int64_t)kRows, (int64_t)(q.r1 - q.r0) * a.group - in * kRows);
+    const bool whole = a.direct && ta == 0 && tb == per;
+    if (ta == 0 && h == 0 && threadIdx.x < rows) {
+      const int64_t last = (item_tile + per - 1) / sh.c;
+      a.found[(int64_t)q.r0 * a.group + in * kRows + threadIdx.x] =
+          Found{(int)(w + item), whole ? -1 : (int)(last - w) + 1, (int)threadIdx.x, 0};
+    }
     // this lane's row
     const int r = in * kRows + min(col, rows - 1);
     const int token = r / a.group, head = h * a.group + r % a.group;
-    const int visible = min(min(q.len, a.capacity),
-                            a.causal ? q.len - (q.r1 - q.r0) + token + 1 : q.len);
-    const int least = __shfl(visible, 0, 64), most = __shfl(visible, rows - 1, 64);
+    const int held = min(q.len, a.capacity);
+    const int visible = min(held, a.causal ? q.len - (q.r1 - q.r0) + token + 1 : q.len);
+    const int least = __builtin_amdgcn_readfirstlane(visible);
+    const int most = __builtin_amdgcn_readlane(visible, rows - 1);
     f16x8_t qf[PARTS][J];
     float f;
     {
-      const T* src = (const T*)a.q.p + (int64_t)(q.r0 + token) * a.q.ts + head * a.q.hs;
-      float x[J][8], top = 0.0f;
+      const T* src = (const T*)a.q.p + (int64_t)(q.r0 + token) * a.q.ts +
+                     (int64_t)head * a.q.hs + 8 * g;
+      float x[J][8], mine = 0.0f;
+#pragma unroll
+      for (int j = 0; j < J; ++j) load_row8(src + 32 * j, x[j]);
 #pragma unroll
       for (int j = 0; j < J; ++j)
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-          x[j][e] = load1<T>(src, 32 * j + 8 * g + e);
-          top = fmaxf(top, fabsf(x[j][e]));
-          if (x[j][e] != x[j][e]) top = __builtin_inff();
+          mine = fmaxf(mine, fabsf(x[j][e]));
+          if (x[j][e] != x[j][e]) mine = __builtin_inff();
         }
-      top = fmaxf(top, __shfl_xor(top, 16, 64));
-      top = fmaxf(top, __shfl_xor(top, 32, 64));
-      const int field = min(267 - (int)(__float_as_uint(top) >> 23), 253);
-      const float up = __uint_as_float((uint32_t)max(field, 1) << 23);
-      f = top <= __FLT_MAX__ ? fmaxf(__uint_as_float((uint32_t)(254 - max(field, 1)) << 23) *
-                                         a.scale * 1.44269504088896340736f, __FLT_MIN__)
-                             : __builtin_nanf("");
+      mine = fmaxf(mine, __shfl_xor(mine, 16, 64));
+      mine = fmaxf(mine, __shfl_xor(mine, 32, 64));
+      const bool bad = !(mine <= __FLT_MAX__);
+      const float top = wave_max(bad ? 0.0f : mine);
+      const int field = max(min(267 - (int)(__float_as_uint(top) >> 23), 253), 1);
+      const float up = __uint_as_float((uint32_t)field << 23);
+      f = __uint_as_float((uint32_t)(254 - field) << 23) * a.scale * 1.44269504088896340736f;
 #pragma unroll
       for (int j = 0; j < J; ++j)
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-          const float v = x[j][e] * up;
+          const float v = bad ? __builtin_nanf("") : x[j][e] * up;
           const _Float16 hi = (_Float16)v;
           qf[0][j][e] = hi;
           if constexpr (PARTS == 2) qf[1][j][e] = (_Float16)(v - (float)hi);
         }
     }
-    float m = kNone, l = 0.0f, ref = 0.0f, inv_ref = 0.0f;
+    float base = kNone, l = 0.0f, ref = 0.0f, unit = 0.0f;
     f32x4_t o[N];
 #pragma unroll
     for (int n = 0; n < N; ++n) o[n] = f32x4_t{0, 0, 0, 0};
+    // this wave's records: block 4 tile + wave of every tile, up to the last that a row sees
     const int32_t* table = a.batch.table + s * a.batch.ldt;
-    for (int tile = ta; tile < tb; ++tile) {
-      const int block = tile * 4 + wave, p0 = block * 32;
-      if (p0 >= most) continue;
-      const uint8_t* rec = record_of(a.cache, table, a.batch.width, block, h);
-      if (!rec) continue;
-      uint32_t kr[KW], vr[KW], kw[2], kx[2][4], vx[2][4];
-#pragma unroll
-      for (int i = 0; i < KW; ++i) {
-        kr[i] = ((const uint32_t*)(rec + i / 4 * 1024 + lane * 16))[i % 4];
-        vr[i] = ((const uint32_t*)(rec + R::codes + i / 4 * 1024 + lane * 16))[i % 4];
+    const int records = min(tb, (max(most, 0) + 31 - 32 * wave + 96) / 128);
+    int entries_from = -64, next_page = -1, next_tile = ta;
+    auto look_up = [&]() __attribute__((always_inline)) {
+      const int entry = (4 * next_tile + wave) >> a.cache.blocks_shift;
+      if (__builtin_expect(entry - entries_from >= 64, 0)) {
+        entries_from = entry & ~63;
+        wave_meets();
+        entries[wave][lane] = entries_from + lane < a.batch.width ? table[entries_from + lane] : -1;
+        wave_meets();
       }
-      const uint32_t* words = (const uint32_t*)(rec + R::words);
+      next_page = entries[wave][entry - entries_from];
+    };
+    struct Where {
+      const uint8_t* rec;
+      int there, p0;
+    };
+    auto next_record = [&]() __attribute__((always_inline)) {
+      const int page = __builtin_amdgcn_readfirstlane(next_page), block = 4 * next_tile + wave;
+      const bool hole = page < 0 || page >= a.cache.pages;
+      Where at;
+      at.p0 = block * 32;
+      at.there = hole ? 0 : min(most - block * 32, 32);
+      // (a hole: any record, its tokens count for nothing)
+      at.rec = head_base + (hole ? 0 : page) * page_bytes + (block & in_page) * R::bytes;
+      next_tile = min(next_tile + 1, records - 1);
+      return at;
+    };
+    // Loads are the same for every record, without branches, and past the last record
+    // repeat it: the compiler can wait for exactly those that are used.
+    u32x4_t kr[KW], vr[KW], kx[2], vx[2];
+    uint32_t kw[2];
+    auto load_keys = [&](const Where& at) __attribute__((always_inline)) {
+#pragma unroll
+      for (int i = 0; i < KW; ++i)
+        kr[i] = *(const u32x4_t*)(at.rec + (uint32_t)(i * 1024 + lane * 16));
 #pragma unroll
       for (int t = 0; t < 2; ++t) {
-        kw[t] = words[16 * t + col];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          kx[t][i] = words[16 * t + 4 * g + i];
-          vx[t][i] = words[32 + 16 * t + 4 * g + i];
-        }
+        kw[t] = *(const uint32_t*)(at.rec + (uint32_t)(R::words + 64 * t + 4 * col));
+        kx[t] = *(const u32x4_t*)(at.rec + (uint32_t)(R::words + 64 * t + 16 * g));
       }
-      if (p0 + 32 > most) {                              // tokens that no row sees
-#pragma unroll
-        for (int t = 0; t < 2; ++t)
-#pragma unroll
-          for (int i = 0; i < 4; ++i)
-            if (p0 + 16 * t + 4 * g + i >= most) kx[t][i] = vx[t][i] = 0;
-      }
-      // scores
-      float p[2][4];
-#pragma unroll
-      for (int t = 0; t < 2; ++t) {
-        f32x4_t acc{0, 0, 0, 0};
-        const int z = word_zero(kw[t]);
-        const uint32_t b0 = bias0(z, z), b4 = bias4(z, z);
-#pragma unroll
-        for (int j = 0; j < J; ++j) {
-          uint4 frag;
-          if constexpr (BITS == 8) {
-            const uint32_t w0 = kr[(t * J + j) * 2], w1 = kr[(t * J + j) * 2 + 1];
-            frag = make_uint4(bytes_less(w0, 0x04010400u, b0), bytes_less(w0, 0x04030402u, b0),
-                              bytes_less(w1, 0x04010400u, b0), bytes_less(w1, 0x04030402u, b0));
-          } else {
-            const uint32_t w0 = kr[t * J + j], w1 = w0 >> 8;
-            frag = make_uint4(low_less(w0, b0), high_less(w0, b4), low_less(w1, b0),
-                              high_less(w1, b4));
-          }
-#pragma unroll
-          for (int part = 0; part < PARTS; ++part) acc = mfma(as_half8(frag), qf[part][j], acc);
-        }
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          p[t][i] = acc[i] * word_step(kx[t][i]);
-          if (p0 + 16 * t + 4 * g + i >= visible) p[t][i] = kNone;
-        }
-      }
-      float top = kNone;
+    };
+    auto load_values = [&](const Where& at) __attribute__((always_inline)) {
 #pragma unroll
       for (int t = 0; t < 2; ++t)
+        vx[t] = *(const u32x4_t*)(at.rec + (uint32_t)(R::words + 128 + 64 * t + 16 * g));
 #pragma unroll
-        for (int i = 0; i < 4; ++i) top = fmaxf(top, p[t][i]);
-      top = fmaxf(top, __shfl_xor(top, 16, 64));
-      top = fmaxf(top, __shfl_xor(top, 32, 64));
-      const float next = fmaxf(m, top), base = next == kNone ? 0.0f : next * f;
-      // larger steps of the values than ref allows
-      float most_step = 0.0f;
-#pragma unroll
-      for (int t = 0; t < 2; ++t)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) most_step = fmaxf(most_step, word_step(vx[t][i]));
-      float scale_o = m == kNone ? 0.0f : exp2f(fmaf(m, f, -base));
-      l *= scale_o;
-      if (__any(most_step > ref * 128.0f)) {
-        most_step = fmaxf(most_step, __shfl_xor(most_step, 16, 64));
-        most_step = fmaxf(most_step, __shfl_xor(most_step, 32, 64));
-        const float old = ref;
-        // 2^e <= most_step, within 2^-100 .. 2^100
-        ref = __uint_as_float(__float_as_uint(fminf(fmaxf(most_step, 0x1p-100f), 0x1p100f)) &
-                              0x7f800000u);
-        inv_ref = 256.0f / ref;
-        scale_o *= old / ref;
-      }
-#pragma unroll
-      for (int n = 0; n < N; ++n)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) o[n][i] *= scale_o;
-      m = next;
-      uint4 pf[PARTS];
-      {
-        float x[8];
-#pragma unroll
-        for (int t = 0; t < 2; ++t)
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const float e = exp2f(fmaf(p[t][i], f, -base));
-            l += e;
-            const bool seen = p0 + 16 * t + 4 * g + i < visible;
-            x[4 * t + i] = seen ? e * (word_step(vx[t][i]) * inv_ref) : 0.0f;
-          }
-#pragma unroll
-        for (int part = 0; part < PARTS; ++part) pf[part] = weight_part<BITS, PARTS == 2>(x);
-      }
-      // values
-      uint32_t z0[4], z4[4];
-      {
-        constexpr int B = BITS == 8 ? 1 : 2, C = BITS == 8 ? 2 : 1;
+      for (int i = 0; i < KW; ++i)
+        vr[i] = *(const u32x4_t*)(at.rec + (uint32_t)(R::codes + i * 1024 + lane * 16));
+    };
+    if (ta < records) {
+      look_up();
+      Where now = next_record();
+      load_keys(now);
+      load_values(now);
+      look_up();
+      for (int tile = ta; tile < records; ++tile) {
+        const int p0 = now.p0, n = now.there;
+        // scores
+        f32x4_t acc[2], sk[2];
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
-          int z[4];
+          acc[t] = f32x4_t{0, 0, 0, 0};
+          const int z = word_zero(kw[t]);
+          const uint32_t b0 = bias0(z, z), b4 = bias4(z, z);
 #pragma unroll
-          for (int i = 0; i < 4; ++i) z[i] = word_zero(vx[t][i]);
-          z0[2 * t] = bias0(z[0], z[B]), z0[2 * t + 1] = bias0(z[C], z[3]);
-          z4[2 * t] = bias4(z[0], z[B]), z4[2 * t + 1] = bias4(z[C], z[3]);
+          for (int j = 0; j < J; ++j) {
+            uint4 frag;
+            if constexpr (BITS == 8) {
+              const int k = (t * J + j) * 2;
+              const uint32_t w0 = kr[k / 4][k % 4], w1 = kr[k / 4][k % 4 + 1];
+              frag = make_uint4(bytes_less(w0, 0x04010400u, b0), bytes_less(w0, 0x04030402u, b0),
+                                bytes_less(w1, 0x04010400u, b0), bytes_less(w1, 0x04030402u, b0));
+            } else {
+              const int k = t * J + j;
+              const uint32_t w0 = kr[k / 4][k % 4], w1 = w0 >> 8;
+              frag = make_uint4(low_less(w0, b0), high_less(w0, b4), low_less(w1, b0),
+                                high_less(w1, b4));
+            }
+#pragma unroll
+            for (int part = 0; part < PARTS; ++part)
+              acc[t] = mfma(as_half8(frag), qf[part][j], acc[t]);
+          }
+#pragma unroll
+          for (int i = 0; i < 4; ++i) sk[t][i] = word_step(kx[t][i]) * f;
         }
-      }
+        const Where ahead = next_record();
+        load_keys(ahead);
+        float e[8];
+        auto exps = [&]() __attribute__((always_inline)) {
 #pragma unroll
-      for (int n = 0; n < N; ++n) {
-        uint4 frag;
-        if constexpr (BITS == 8) {
-          const uint32_t w0 = vr[2 * n], w1 = vr[2 * n + 1];
-          frag = make_uint4(bytes_less(w0, 0x04010400u, z0[0]), bytes_less(w0, 0x04030402u, z0[1]),
-                            bytes_less(w1, 0x04010400u, z0[2]), bytes_less(w1, 0x04030402u, z0[3]));
-        } else {
-          const uint32_t w0 = vr[n / 2 * 2], w1 = vr[n / 2 * 2 + 1];
-          if (n % 2 == 0)
-            frag = make_uint4(low_less(w0, z0[0]), low_less(w0 >> 8, z0[1]), low_less(w1, z0[2]),
-                              low_less(w1 >> 8, z0[3]));
-          else
-            frag = make_uint4(high_less(w0, z4[0]), high_less(w0 >> 8, z4[1]),
-                              high_less(w1, z4[2]), high_less(w1 >> 8, z4[3]));
+          for (int i = 0; i < 8; ++i)
+            e[i] = __builtin_amdgcn_exp2f(fmaf(acc[i / 4][i % 4], sk[i / 4][i % 4], -base));
+        };
+        const int seen = min(visible - p0, n) - 4 * g;
+        auto hide = [&]() __attribute__((always_inline)) {
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            if (i / 4 * 16 + i % 4 >= seen) e[i] = 0.0f;
+        };
+        exps();
+        const bool masked = p0 + 32 > least || n < 32;
+        if (masked) hide();
+        float top = 0.0f, sv[8], most_step = 0.0f;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          top = fmaxf(top, e[i]);
+          sv[i] = word_step(vx[i / 4][i % 4]);
+        }
+        if (masked) {
+          // tokens that are not there, or whom some rows do not see: those that read as
+          // NaN must not meet a weight of 0
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            if (i / 4 * 16 + i % 4 + 4 * g >= n) sv[i] = 0.0f;
+            if (sv[i] != sv[i]) {
+              if (i / 4 * 16 + i % 4 < seen) e[i] = sv[i];
+              sv[i] = 0.0f;
+            }
+          }
         }
 #pragma unroll
-        for (int part = 0; part < PARTS; ++part)
-          o[n] = mfma(as_half8(frag), as_half8(pf[part]), o[n]);
+        for (int i = 0; i < 8; ++i) most_step = fmaxf(most_step, sv[i]);
+        if (__builtin_expect(__any(top > 4096.0f || most_step > ref * 8.0f), 0)) {
+          // the maximum is raised once a score is 4 above it, ref where a step is 8 of it
+          float m = kNone;
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            if (i / 4 * 16 + i % 4 < seen) m = fmaxf(m, acc[i / 4][i % 4] * sk[i / 4][i % 4]);
+          m = fmaxf(m, __shfl_xor(m, 16, 64));
+          m = fmaxf(m, __shfl_xor(m, 32, 64));
+          const float next = __any(top > 4096.0f) ? fmaxf(base, m - 8.0f) : base;
+          float factor = base == kNone ? 0.0f : __builtin_amdgcn_exp2f(base - next);
+          l *= factor;
+          base = next;
+          const float largest = wave_max(most_step);
+          if (largest > ref * 8.0f) {
+            const float to = __uint_as_float(
+                __float_as_uint(fminf(fmaxf(largest, 0x1p-100f), 0x1p100f)) & 0x7f800000u);
+            factor *= ref / to;
+            ref = to, unit = 1.0f / to;
+          }
+#pragma unroll
+          for (int k = 0; k < N; ++k) o[k] *= factor;
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const bool poisoned = e[i] != e[i];
+            const float x =
+                __builtin_amdgcn_exp2f(fmaf(acc[i / 4][i % 4], sk[i / 4][i % 4], -base));
+            if (!poisoned) e[i] = masked && i / 4 * 16 + i % 4 >= seen ? 0.0f : x;
+          }
+        }
+        uint4 pf[PARTS];
+        float x[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          l += e[i];
+          x[i] = e[i] * (sv[i] * unit);
+        }
+#pragma unroll
+        for (int part = 0; part < PARTS; ++part) pf[part] = weight_part<BITS, PARTS == 2>(x);
+        // values
+        uint32_t z0[4], z4[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const int first = BITS == 8 ? k % 2 * 2 : k % 2, other = BITS == 8 ? 1 : 2;
+          const uint32_t z = __builtin_amdgcn_perm(vx[k / 2][first + other], vx[k / 2][first],
+                                                   0x0c040c00u);
+          z0[k] = z | 0xe400e400u, z4[k] = (z & 0x000f000fu) << 4 | 0xd400d400u;
+        }
+#pragma unroll
+        for (int k = 0; k < N; ++k) {
+          uint4 frag;
+          if constexpr (BITS == 8) {
+            const uint32_t w0 = vr[k / 2][k % 2 * 2], w1 = vr[k / 2][k % 2 * 2 + 1];
+            frag = make_uint4(bytes_less(w0, 0x04010400u, z0[0]),
+                              bytes_less(w0, 0x04030402u, z0[1]),
+                              bytes_less(w1, 0x04010400u, z0[2]),
+                              bytes_less(w1, 0x04030402u, z0[3]));
+          } else {
+            const uint32_t w0 = vr[k / 4][k / 2 % 2 * 2], w1 = vr[k / 4][k / 2 % 2 * 2 + 1];
+            if (k % 2 == 0)
+              frag = make_uint4(low_less(w0, z0[0]), low_less(w0 >> 8, z0[1]),
+                                low_less(w1, z0[2]), low_less(w1 >> 8, z0[3]));
+            else
+              frag = make_uint4(high_less(w0, z4[0]), high_less(w0 >> 8, z4[1]),
+                                high_less(w1, z4[2]), high_less(w1 >> 8, z4[3]));
+          }
+#pragma unroll
+          for (int part = 0; part < PARTS; ++part)
+            o[k] = mfma(as_half8(frag), as_half8(pf[part]), o[k]);
+        }
+        load_values(ahead);
+        look_up();
+        now = ahead;
       }
     }
     // the four waves' results
     l += __shfl_xor(l, 16, 64);
     l += __shfl_xor(l, 32, 64);
-    const float m2 = m == kNone ? kNone : m * f;
+    const float m2 = base == kNone ? kNone : base + 8.0f;
     __syncthreads();
-    if (g == 0) sm[wave][col] = m2, sl[wave][col] = l;
+    if (g == 0) sm[wave][col] = m2, sl[wave][col] = l * (1.0f / 256.0f);
     __syncthreads();
     float all = kNone, sum = 0.0f;
 #pragma unroll
@@ -443,31 +533,28 @@ __global__ __launch_bounds__(256) void attend_rows(const RowsArgs a) {
 #pragma unroll
     for (int i = 0; i < 4; ++i)
       sum += sm[i][col] == kNone ? sl[i][col] : sl[i][col] * exp2f(sm[i][col] - all);
-    const float part = m2 == kNone ? 1.0f : exp2f(m2 - all);
+    // the whole result's weights are divided by here
+    const float part = (m2 == kNone ? 1.0f : exp2f(m2 - all)) *
+                       (whole ? (sum == 0.0f ? 0.0f : 1.0f / sum) : 1.0f);
     const float back = ref * (1.0f / 256.0f);
 #pragma unroll
     for (int n = 0; n < N; ++n)
-#pragma unroll
-      for (int i = 0; i < 4; ++i) so[wave][col][16 * n + 4 * g + i] = o[n][i] * part * back;
+      *(f32x4_t*)&so[wave][col][16 * n + 4 * g] = o[n] * part * back;
     __syncthreads();
-    const bool whole = a.direct && ta == 0 && tb == per;
     float* slot = a.slots + ((int64_t)h * (a.workers + a.items) + w + item) * kSlot<D>;
-    for (int i = threadIdx.x; i < rows * D; i += 256) {
-      const int row = i / D, d = i % D;
-      const float v = so[0][row][d] + so[1][row][d] + so[2][row][d] + so[3][row][d];
+    for (int i = threadIdx.x; i < rows * (D / 4); i += 256) {
+      const int row = i / (D / 4), d = i % (D / 4) * 4;
+      f32x4_t v = *(const f32x4_t*)&so[0][row][d];
+#pragma unroll
+      for (int k = 1; k < 4; ++k) v += *(const f32x4_t*)&so[k][row][d];
       if (whole) {
-        float total_l = 0.0f, top = kNone;
-        for (int k = 0; k < 4; ++k) top = fmaxf(top, sm[k][row]);
-        for (int k = 0; k < 4; ++k)
-          total_l += sm[k][row] == kNone ? sl[k][row] : sl[k][row] * exp2f(sm[k][row] - top);
         const int rr = in * kRows + row;
         const int64_t to = (int64_t)(q.r0 + rr / a.group) * a.out.ts +
                            (int64_t)(h * a.group + rr % a.group) * a.out.hs + d;
-        const float y = total_l == 0.0f ? 0.0f : v / total_l;
-        if constexpr (std::is_same_v<T, float>) ((float*)a.out.p)[to] = y;
-        else ((__bf16*)a.out.p)[to] = (__bf16)y;
+        const float y[4] = {v[0], v[1], v[2], v[3]};
+        store_row4((T*)a.out.p + to, y);
       } else {
-        slot[i] = v;
+        *(f32x4_t*)&slot[row * D + d] = v;
       }
     }
     if (!whole && wave == 0 && g == 0) {
@@ -485,6 +572,7 @@ struct TilesArgs {
   int64_t splits, items;
   float scale;
   float* slots;            // NULL: one split, results written to out
+  Found* found;            // as for attend_rows; NULL: not wanted
 };
 
 // The sequence of an item (in units of ROWS rows), and the item's number in it; -1
@@ -510,12 +598,6 @@ __device__ __forceinline__ int find_item(const CacheBatch& b, int group, int64_t
   __syncthreads();
   *in = (int)sc.found[1];
   return (int)sc.found[0];
-}
-
-__device__ __forceinline__ float wave_top(float v) {
-#pragma unroll
-  for (int o = 32; o >= 1; o >>= 1) v = fmaxf(v, __shfl_xor(v, o, 64));
-  return v;
 }
 
 // Attention of 128 RT rows, 16 RT to each of eight waves: all waves take the same
@@ -561,11 +643,15 @@ __global__ __launch_bounds__(512, 1) void attend_tiles(const TilesArgs a) {
   const Seq q = sequence(a.batch, s);
   const int rows = (int)min((int64_t)ROWS, (int64_t)(q.r1 - q.r0) * a.group - (int64_t)in * ROWS);
   const int first = in * ROWS;
-  const int held = a.cache.pages > 0 ? min(q.len, a.capacity) : 0;
+  const int held = min(q.len, a.capacity);
   auto visible_of = [&](int row) {               // tokens that a row of the item sees
     return min(held, a.causal ? q.len - (q.r1 - q.r0) + (first + row) / a.group + 1 : q.len);
   };
   const int most = max(visible_of(rows - 1), 0);
+  if (a.found && h == 0 && split == 0)
+    for (int i = threadIdx.x; i < rows; i += 512)
+      a.found[(int64_t)q.r0 * a.group + first + i] =
+          Found{(int)(item * a.splits), (int)a.splits, i, 0};
   const int records = (most + 31) / 32;
   const int i0 = (int)(records * split / a.splits), i1 = (int)(records * (split + 1) / a.splits);
 
@@ -600,7 +686,7 @@ __global__ __launch_bounds__(512, 1) void attend_tiles(const TilesArgs a) {
       bad[rt] = !(mine <= __FLT_MAX__);
       if (!bad[rt]) top = fmaxf(top, mine);
     }
-    top = wave_top(top);
+    top = wave_max(top);
     __syncthreads();
     if (lane == 0) tops[wave] = top;
     __syncthreads();
@@ -701,7 +787,7 @@ __global__ __launch_bounds__(512, 1) void attend_tiles(const TilesArgs a) {
     const float sv = lane >= 32 && there && step == step ? step : 0.0f;
     if (__builtin_expect(__any(sv > staged_ref * 8.0f), 0)) {
       staged_ref = __uint_as_float(
-          __float_as_uint(fminf(fmaxf(wave_top(sv), 0x1p-100f), 0x1p100f)) & 0x7f800000u);
+          __float_as_uint(fminf(fmaxf(wave_max(sv), 0x1p-100f), 0x1p100f)) & 0x7f800000u);
       unit = kUnit / staged_ref;
     }
     const uint32_t zero = 0xe400u | (uint32_t)word_zero(st.word);
@@ -1055,102 +1141,119 @@ __global__ __launch_bounds__(512, 1) void attend_tiles(const TilesArgs a) {
   }
 }
 
-// Where a row's results are: those of attend_rows, or of attend_tiles.
-struct Parts {
-  CacheView cache;
-  CacheBatch batch;
-  int group, capacity, direct, tile_rows;      // tile_rows 0: attend_rows
-  int64_t workers, items, splits;
-  const float* slots;
-};
 struct JoinArgs {
-  Parts own, before;           // before.slots NULL: no prefix
+  CacheBatch batch;
   CacheTensor out;
-  int heads;
+  int heads, group, capacity;
+  // the batch's own slots: per key head, rows of a slot, where a row's are
+  const float* own;
+  const Found* found;
+  int64_t own_per_head;
+  int own_rows, own_tiles;     // own_tiles: by attend_tiles, which has slots for every row
+  // the prefix's: all of its splits, of the row's tile; NULL: none
+  const float* before;
+  int64_t before_items;
+  int before_rows, before_splits;
 };
+constexpr int kMostParts = 1024;   // of a row
 
-// A row's results from the workers that had tiles of its item, and from those of
-// the prefix: a workgroup per row.
+// A row's results from the workers that had tiles of its item, and from the splits of the
+// prefix: a workgroup per row.  All maxima and totals are read at once, then the sums
+// with as many loads in flight.
 template <typename T, int D>
 __global__ __launch_bounds__(256) void join_rows(const JoinArgs j) {
-  __shared__ Scan sc;
-  __shared__ float sm[4], sl[4], so[4][D];
+  __shared__ float fac[kMostParts], red[2][4], so[4][D];
   const int64_t b = block_index();
-  const int head = (int)(b % j.heads), h = head / j.own.group;
-  if (b / j.heads >= j.own.batch.ntok) return;
+  const int head = (int)(b % j.heads), h = head / j.group;
+  if (b / j.heads >= j.batch.ntok) return;
   const int t = (int)(b / j.heads);
-  const int s = find_sequence(j.own.batch, t);
+  const int s = find_sequence(j.batch, t);
   if (s < 0) return;
   const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
-  constexpr int E = D / 64;
-  float m = kNone, l = 0.0f, o[E] = {};
-  auto add = [&](const float* sums, float pm, float pl) {
-    const float next = fmaxf(m, pm), base = next == kNone ? 0.0f : next;
-    const float fm = exp2f(m - base), fp = pm == kNone ? 1.0f : exp2f(pm - base);
-    l = l * fm + pl * fp;
-#pragma unroll
-    for (int e = 0; e < E; ++e) o[e] = o[e] * fm + sums[lane * E + e] * fp;
-    m = next;
+  const int64_t row = (int64_t)t * j.group + head % j.group;
+  int n = 0, k = 0;
+  const float* own = nullptr;
+  const int64_t own_slot = (int64_t)j.own_rows * (D + 2);
+  if (j.own_tiles || min(sequence(j.batch, s).len, j.capacity) > 0) {
+    const Found at = j.found[row];
+    if (at.n == -1) return;                            // written already
+    // (with starts that descend, nothing may have been found)
+    if (at.first >= 0 && at.n >= 0 && at.k >= 0 && at.k < j.own_rows &&
+        at.first + (int64_t)at.n <= j.own_per_head && at.n <= kMostParts / 2) {
+      n = at.n, k = at.k;
+      own = j.own + ((int64_t)h * j.own_per_head + at.first) * own_slot;
+    }
+  }
+  int m = 0, kb = 0;
+  const float* before = nullptr;
+  const int64_t before_slot = (int64_t)j.before_rows * (D + 2);
+  if (j.before) {
+    const int64_t r = row - (int64_t)clamp_row(j.batch.starts[0], j.batch.ntok) * j.group;
+    const int64_t item = r / j.before_rows;
+    kb = (int)(r % j.before_rows);
+    if (item < j.before_items) {
+      m = j.before_splits;
+      before = j.before + ((int64_t)h * j.before_items + item) * m * before_slot;
+    }
+  }
+  auto part = [&](int i, int* rows, int* at) {
+    *rows = i < n ? j.own_rows : j.before_rows;
+    *at = i < n ? k : kb;
+    return i < n ? own + i * own_slot : before + (i - n) * before_slot;
   };
-  for (int of = 0; of < 2; ++of) {
-    const Parts& r = of ? j.before : j.own;
-    if (!r.slots) continue;
-    const int own = of ? 0 : s;
-    const Seq q = sequence(r.batch, own);
-    const int64_t row = (int64_t)(t - q.r0) * r.group + head % r.group;
-    const Walk walk{r.batch, &r.cache, r.group, r.capacity};
-    if (r.tile_rows) {
-      int64_t item0 = 0;
-      if (own > 0) {
-        int64_t mine = 0, x, y, none;
-        for (int i = threadIdx.x; i < own; i += 256) {
-          const Seq p = sequence(r.batch, i);
-          mine += ((int64_t)(p.r1 - p.r0) * r.group + r.tile_rows - 1) / r.tile_rows;
-        }
-        scan2(mine, 0, &x, &y, &item0, &none, sc.red);
-        __syncthreads();
-      }
-      const int64_t item = item0 + row / r.tile_rows;
-      const int k = (int)(row % r.tile_rows);
-      if (item >= r.items) continue;
-      for (int64_t i = wave; i < r.splits; i += 4) {
-        const float* slot = r.slots + (((int64_t)h * r.items + item) * r.splits + i) *
-                                          ((int64_t)r.tile_rows * (D + 2));
-        add(slot + k * D, slot[r.tile_rows * D + k], slot[r.tile_rows * (D + 1) + k]);
-      }
-      continue;
-    }
-    const int per = walk.tiles(q);
-    const int64_t total = total_tiles(walk, sc);
-    __syncthreads();
-    const Place place = locate(walk, 0, own, sc);
-    __syncthreads();
-    if (per == 0) continue;
-    const int64_t c = share(total, r.workers), item = place.item + row / kRows;
-    const int64_t first = place.tile + row / kRows * per;
-    const int64_t w0 = first / c, w1 = (first + per - 1) / c;
-    if (item >= r.items) continue;
-    if (w0 == w1 && r.direct) return;                  // written already
-    for (int64_t w = w0 + wave; w <= w1; w += 4) {
-      const float* slot = r.slots + ((int64_t)h * (r.workers + r.items) + w + item) * kSlot<D>;
-      const int k = (int)(row % kRows);
-      add(slot + k * D, slot[kRows * D + k], slot[kRows * D + kRows + k]);
-    }
-  }
-  if (lane == 0) sm[wave] = m, sl[wave] = l;
+  float mx[kMostParts / 256], lx[kMostParts / 256], top = kNone;
 #pragma unroll
-  for (int e = 0; e < E; ++e) so[wave][lane * E + e] = o[e];
-  __syncthreads();
-  float all = kNone, sum = 0.0f;
-  for (int i = 0; i < 4; ++i) all = fmaxf(all, sm[i]);
-  float fac[4];
-  for (int i = 0; i < 4; ++i) {
-    fac[i] = sm[i] == kNone ? 1.0f : exp2f(sm[i] - all);
-    sum += sl[i] * fac[i];
+  for (int c = 0; c < kMostParts / 256; ++c) {
+    const int i = threadIdx.x + 256 * c;
+    mx[c] = kNone, lx[c] = 0.0f;
+    if (i < n + m) {
+      int rows, at;
+      const float* slot = part(i, &rows, &at);
+      mx[c] = slot[(int64_t)rows * D + at], lx[c] = slot[(int64_t)rows * (D + 1) + at];
+    }
+    top = fmaxf(top, mx[c]);
   }
-  for (int d = threadIdx.x; d < D; d += 256) {
-    float v = 0.0f;
-    for (int i = 0; i < 4; ++i) v += so[i][d] * fac[i];
+  top = wave_max(top);
+  if (lane == 0) red[0][wave] = top;
+  __syncthreads();
+  top = fmaxf(fmaxf(red[0][0], red[0][1]), fmaxf(red[0][2], red[0][3]));
+  float sum = 0.0f;
+#pragma unroll
+  for (int c = 0; c < kMostParts / 256; ++c) {
+    const int i = threadIdx.x + 256 * c;
+    if (i >= n + m) break;
+    const float x = mx[c] == kNone ? 1.0f : exp2f(mx[c] - top);     // (NaN sums stay)
+    fac[i] = x;
+    sum += lx[c] * x;
+  }
+#pragma unroll
+  for (int o = 32; o >= 1; o >>= 1) sum += __shfl_xor(sum, o, 64);
+  if (lane == 0) red[1][wave] = sum;
+  __syncthreads();
+  sum = red[1][0] + red[1][1] + red[1][2] + red[1][3];
+  constexpr int E = D / 64, AT_ONCE = 8;
+  float o[E] = {};
+  for (int i0 = wave; i0 < n + m; i0 += 4 * AT_ONCE) {
+    float x[AT_ONCE][E];
+#pragma unroll
+    for (int c = 0; c < AT_ONCE; ++c) {
+      int rows, at;
+      const float* slot = part(min(i0 + 4 * c, n + m - 1), &rows, &at);
+#pragma unroll
+      for (int e = 0; e < E; ++e) x[c][e] = slot[(int64_t)at * D + 64 * e + lane];
+    }
+#pragma unroll
+    for (int c = 0; c < AT_ONCE; ++c)
+      if (i0 + 4 * c < n + m)
+#pragma unroll
+        for (int e = 0; e < E; ++e) o[e] = fmaf(x[c][e], fac[i0 + 4 * c], o[e]);
+  }
+#pragma unroll
+  for (int e = 0; e < E; ++e) so[wave][64 * e + lane] = o[e];
+  __syncthreads();
+  const int d = threadIdx.x;
+  if (d < D) {
+    const float v = so[0][d] + so[1][d] + so[2][d] + so[3][d];
     const float y = sum == 0.0f ? 0.0f : v / sum;
     const int64_t to = (int64_t)t * j.out.ts + (int64_t)head * j.out.hs + d;
     if constexpr (std::is_same_v<T, float>) ((float*)j.out.p)[to] = y;
@@ -1172,8 +1275,10 @@ int tile_rows_of(int32_t dtype, int dim) {
   return dtype == PWQ_F32 ? rows_of_dim<float>(dim) : rows_of_dim<uint16_t>(dim);
 }
 
-int capacity_of(const CacheBatch& b, int blocks_shift) {
-  return (int)std::min<int64_t>((int64_t)b.width << (blocks_shift + 5), INT32_MAX - 65535);
+// Tokens that a table row's pages hold.
+int capacity_of(const CacheBatch& b, const CacheView& c) {
+  if (c.pages == 0) return 0;
+  return (int)std::min<int64_t>((int64_t)b.width << (c.blocks_shift + 5), INT32_MAX - 65535);
 }
 
 struct Launch {
@@ -1192,7 +1297,7 @@ void launch_all(const Launch& l, hipStream_t st) {
   if (l.rows.workers)
     attend_rows<T, D, BITS><<<block_grid(l.rows.workers * l.rows.cache.heads), 256, 0, st>>>(l.rows);
   if (l.joined)
-    join_rows<T, D><<<block_grid((int64_t)l.join.own.batch.ntok * l.join.heads), 256, 0, st>>>(
+    join_rows<T, D><<<block_grid((int64_t)l.join.batch.ntok * l.join.heads), 256, 0, st>>>(
         l.join);
 }
 
@@ -1217,10 +1322,9 @@ AttentionPlan attention_plan(const AttentionLaunch& a) {
   const int64_t rows = a.batch.ntok * group, seqs = std::min(a.batch.nseq, a.batch.ntok);
   const int64_t tile = tile_rows_of(a.dtype, a.head_dim);
   // Splits of the tokens: workgroups for every CU, where items alone are fewer, of
-  // at least four stages of 64 tokens.
+  // at least 256 tokens.
   auto splits = [&](int64_t items, const CacheBatch& b) {
-    const int64_t most = std::max<int64_t>(
-        1, capacity_of(b, a.cache.blocks_shift) / (64 * 4));
+    const int64_t most = std::max<int64_t>(1, capacity_of(b, a.cache) / 256);
     return std::min(std::max<int64_t>(1, 256 / (items * heads)), most);
   };
   p.tiles = rows > 32 * seqs;
@@ -1234,6 +1338,7 @@ AttentionPlan attention_plan(const AttentionLaunch& a) {
     p.items = rows / kRows + seqs;
     p.own_bytes = (p.workers + p.items) * heads * kRows * (a.head_dim + 2) * 4;
   }
+  if (p.own_bytes) p.found_bytes = rows * sizeof(Found);
   if (a.prefix.nseq) {
     p.prefix_items = (rows + tile - 1) / tile;
     p.prefix_splits = splits(p.prefix_items, a.prefix);
@@ -1243,30 +1348,34 @@ AttentionPlan attention_plan(const AttentionLaunch& a) {
 }
 
 hipError_t launch_cached_attention(const AttentionLaunch& a, const AttentionPlan& p, void* own,
-                                   void* prefix, hipStream_t st) {
+                                   void* found, void* prefix, hipStream_t st) {
   if (a.batch.ntok == 0 || a.batch.nseq == 0) return hipSuccess;
   const int group = a.heads / a.cache.heads;
   const int tile = tile_rows_of(a.dtype, a.head_dim);
-  const int capacity = capacity_of(a.batch, a.cache.blocks_shift);
+  const int capacity = capacity_of(a.batch, a.cache);
   Launch l{};
   l.joined = p.own_bytes > 0;
-  l.join.out = a.out, l.join.heads = a.heads;
-  l.join.own = Parts{a.cache, a.batch, group, capacity, a.prefix.nseq == 0, p.tiles ? tile : 0,
-                     p.workers, p.items, p.splits, (const float*)own};
+  l.join.batch = a.batch, l.join.out = a.out;
+  l.join.heads = a.heads, l.join.group = group, l.join.capacity = capacity;
+  l.join.own = (const float*)own, l.join.found = (const Found*)found;
+  l.join.own_per_head = p.tiles ? p.items * p.splits : p.workers + p.items;
+  l.join.own_rows = p.tiles ? tile : kRows, l.join.own_tiles = p.tiles;
   if (p.tiles)
     l.tiles[0] = TilesArgs{a.cache, a.batch, a.q, a.out, group, a.heads, a.causal, capacity,
-                           p.splits, p.items, a.scale, p.own_bytes ? (float*)own : nullptr};
+                           p.splits, p.items, a.scale, p.own_bytes ? (float*)own : nullptr,
+                           p.own_bytes ? (Found*)found : nullptr};
   else
     l.rows = RowsArgs{a.cache, a.batch, a.q, a.out, group, a.heads, a.causal, capacity,
-                      a.prefix.nseq == 0, p.workers, p.items, a.scale, (float*)own};
+                      a.prefix.nseq == 0, p.workers, p.items, a.scale, (float*)own,
+                      (Found*)found};
   if (a.prefix.nseq) {
     CacheBatch b = a.prefix;
     b.starts = a.batch.starts, b.starts_step = a.batch.nseq, b.ntok = a.batch.ntok;
-    const int cap = capacity_of(a.prefix, a.cache.blocks_shift);
-    l.tiles[1] = TilesArgs{a.cache, b, a.q, a.out, group, a.heads, 0, cap, p.prefix_splits,
-                           p.prefix_items, a.scale, (float*)prefix};
-    l.join.before = Parts{a.cache, b, group, cap, 0, tile, 0, p.prefix_items, p.prefix_splits,
-                          (const float*)prefix};
+    l.tiles[1] = TilesArgs{a.cache, b, a.q, a.out, group, a.heads, 0,
+                           capacity_of(a.prefix, a.cache), p.prefix_splits,
+                           p.prefix_items, a.scale, (float*)prefix, nullptr};
+    l.join.before = (const float*)prefix, l.join.before_items = p.prefix_items;
+    l.join.before_rows = tile, l.join.before_splits = (int)p.prefix_splits;
   }
   if (a.dtype == PWQ_F32) launch_dim<float>(l, a.head_dim, a.bits, st);
   else launch_dim<uint16_t>(l, a.head_dim, a.bits, st);

@@ -1240,8 +1240,9 @@ static pwq_status check_attention(const pwq_cache* cache, const pwq_batch* batch
   return check_cache(cache, &p, ntok, heads, dtype);
 }
 
-static void* carve_attention(Carver& c, const AttentionPlan& p, void** prefix) {
+static void* carve_attention(Carver& c, const AttentionPlan& p, void** found, void** prefix) {
   void* own = c.take(p.own_bytes);
+  *found = c.take(p.found_bytes);
   *prefix = p.prefix_bytes ? c.take(p.prefix_bytes) : nullptr;
   return own;
 }
@@ -1258,9 +1259,9 @@ size_t pwq_cached_attention_workspace_size(const pwq_cache* cache, const pwq_bat
   if (check_attention(&c, &b, prefix ? &p : nullptr, heads, dtype, ntok) != PWQ_OK) return 0;
   if (ntok == 0 || b.nseq == 0) return 0;
   Carver carve(nullptr);
-  void* unused;
+  void *found, *before;
   carve_attention(carve, attention_plan(attention_launch(&c, &b, prefix ? &p : nullptr, heads,
-                                                         dtype, ntok)), &unused);
+                                                         dtype, ntok)), &found, &before);
   return carve.size();
 }
 
@@ -1290,12 +1291,12 @@ pwq_status pwq_cached_attention(const pwq_cache* cache, const pwq_batch* batch,
   a.causal = causal != 0, a.scale = (float)scale;
   const AttentionPlan p = attention_plan(a);
   Carver measure(nullptr), carve(ws);
-  void* before;
-  carve_attention(measure, p, &before);
+  void *found, *before;
+  carve_attention(measure, p, &found, &before);
   s = check_ws(ws, ws_bytes, measure.size());
   if (s != PWQ_OK) return s;
-  void* own = carve_attention(carve, p, &before);
-  const hipError_t e = launch_cached_attention(a, p, own, before, (hipStream_t)stream);
+  void* own = carve_attention(carve, p, &found, &before);
+  const hipError_t e = launch_cached_attention(a, p, own, found, before, (hipStream_t)stream);
   if (e != hipSuccess) return hip_fail(e, "cached_attention launch");
   return ok();
 }

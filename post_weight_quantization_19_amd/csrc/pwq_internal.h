@@ -281,10 +281,11 @@ struct AttentionPlan {
   int64_t items, splits;            // items per key head, at most; splits of an item's tokens
   int64_t prefix_items, prefix_splits;
   size_t own_bytes, prefix_bytes;   // partial results
+  size_t found_bytes;               // where a row's are
 };
 AttentionPlan attention_plan(const AttentionLaunch& a);
 hipError_t launch_cached_attention(const AttentionLaunch& a, const AttentionPlan& p, void* own,
-                                   void* prefix, hipStream_t st);
+                                   void* found, void* prefix, hipStream_t st);
 
 // Event pairs recorded around launches of one kernel (pwq_kernel_timer_attach).
 struct KernelTimer {
