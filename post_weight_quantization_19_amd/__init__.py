@@ -11,6 +11,8 @@ memory) and the current stream into that ABI; the HIP kernels do all the
 work and there is no CPU fallback.
 """
 import ctypes
+import functools
+import struct
 from dataclasses import dataclass
 from typing import Optional
 
@@ -722,41 +724,54 @@ def new_cache(pages: int, kv_heads: int, head_dim: int, bits: int = 8, page: int
     return {"records": records, "bits": bits, "head_dim": head_dim, "page": page}
 
 
-def _cache_struct(cache: dict, device: int):
-    records, page = cache["records"], cache["page"]
-    if records.get_device() != device:
-        raise ValueError("the cache must be on the tensors' GPU")
-    bits, dim = cache["bits"], cache["head_dim"]
-    if records.dim() != 4 or records.dtype is not torch.uint8 or not records.is_contiguous():
+# pwq_cache and pwq_batch of include/pwq_cache.h, packed (half the time of filling
+# ctypes structures)
+_PACK_CACHE = struct.Struct("@Pqiiii").pack
+_PACK_BATCH = struct.Struct("@PPPqii").pack
+
+
+def _cache_args(cache: dict, starts, lengths, table, device: int):
+    """(pwq_cache, pwq_batch, kv_heads, head_dim, sizes that the workspace goes by) of
+    tensors on this GPU."""
+    records, page, bits, dim = cache["records"], cache["page"], cache["bits"], cache["head_dim"]
+    rs, ts = records.shape, table.shape
+    if len(rs) != 4 or records.dtype is not torch.uint8 or not records.is_contiguous():
         raise ValueError("records must be a contiguous 4-D uint8 tensor")
-    pages, heads, blocks, size = records.shape
+    pages, heads, blocks, size = rs
     if blocks * 32 != page or size != 8 * dim * bits + 256:
-        raise ValueError(f"records of {tuple(records.shape)} do not fit pages of {page} tokens, "
+        raise ValueError(f"records of {tuple(rs)} do not fit pages of {page} tokens, "
                          f"{dim} channels and {bits} bits")
-    return _lib.PwqCache(records.data_ptr(), pages, heads, dim, bits, page), heads, dim
-
-
-def _batch_struct(starts, lengths, table, device: int):
-    if table.dim() != 2 or table.dtype is not torch.int32 or table.get_device() != device:
-        raise ValueError("table must be a 2-D int32 tensor on the tensors' GPU")
-    nseq, width = table.shape
-    sp = _expect(starts, "starts", (nseq + 1,), torch.int32, device)
-    lp = _expect(lengths, "lengths", (nseq,), torch.int32, device)
+    if len(ts) != 2 or table.dtype is not torch.int32:
+        raise ValueError("table must be a 2-D int32 tensor")
+    nseq, width = ts
+    if not (records.get_device() == table.get_device() == device):
+        raise ValueError("the cache and the table must be on the tensors' GPU")
     ld = width
     if not table.is_contiguous():
         ld = table.stride(0)
         if width > 1 and table.stride(1) != 1 or nseq > 1 and ld < width:
             raise ValueError("table must be row-major")
         ld = max(ld, width)
-    return _lib.PwqBatch(sp, lp, table.data_ptr(), ld, nseq, width)
+    return (_PACK_CACHE(records.data_ptr(), pages, heads, dim, bits, page),
+            _PACK_BATCH(_expect(starts, "starts", (nseq + 1,), torch.int32, device),
+                        _expect(lengths, "lengths", (nseq,), torch.int32, device),
+                        table.data_ptr(), ld, nseq, width),
+            heads, dim, (pages, heads, dim, bits, page, nseq, width))
+
+
+@functools.lru_cache(maxsize=256)
+def _attention_workspace(sizes, prefix_width, heads, dtype, tokens) -> int:
+    pages, kv_heads, dim, bits, page, nseq, width = sizes
+    p = None if prefix_width < 0 else _PACK_BATCH(0, 0, 0, prefix_width, 1, prefix_width)
+    return lib().pwq_cached_attention_workspace_size(
+        _PACK_CACHE(0, pages, kv_heads, dim, bits, page),
+        _PACK_BATCH(0, 0, 0, width, nseq, width), p, heads, dtype, tokens)
 
 
 def _heads(t: torch.Tensor, name: str, shape: tuple, dtype, device: int):
     """Strides of a [tokens, heads, head_dim] tensor with unit channel stride."""
-    if t.get_device() != device:
-        raise ValueError(f"{name} must be on the cache's GPU")
-    if t.shape != shape or t.dtype is not dtype:
-        raise ValueError(f"{name} must be {list(shape)} {dtype}")
+    if t.get_device() != device or t.shape != shape or t.dtype is not dtype:
+        raise ValueError(f"{name} must be {list(shape)} {dtype} on the cache's GPU")
     ts, hs, ds = t.stride()
     if ds != 1:
         raise ValueError(f"{name} must have unit channel stride")
@@ -779,12 +794,9 @@ def cache_write(k: torch.Tensor, v: torch.Tensor, cache: dict, starts: torch.Ten
     if dev != torch._C._cuda_getDevice():
         with _on_device(dev):
             return cache_write(k, v, cache, starts, lengths, table)
-    if torch.is_grad_enabled():
+    if (k.requires_grad or v.requires_grad) and torch.is_grad_enabled():
         _no_gradient(k, v)
-    c, heads, dim = _cache_struct(cache, dev)
-    b = _batch_struct(starts, lengths, table, dev)
-    if k.dim() != 3:
-        raise ValueError("k must be [tokens, kv_heads, head_dim]")
+    c, b, heads, dim, _ = _cache_args(cache, starts, lengths, table, dev)
     shape = (k.shape[0], heads, dim)
     kts, khs = _heads(k, "k", shape, k.dtype, dev)
     vts, vhs = _heads(v, "v", shape, k.dtype, dev)
@@ -807,19 +819,19 @@ def cache_read(cache: dict, starts: torch.Tensor, lengths: torch.Tensor, table: 
     if dev != torch._C._cuda_getDevice():
         with _on_device(dev):
             return cache_read(cache, starts, lengths, table, tokens, dtype, out)
-    c, heads, dim = _cache_struct(cache, dev)
-    b = _batch_struct(starts, lengths, table, dev)
+    c, b, heads, dim, _ = _cache_args(cache, starts, lengths, table, dev)
     shape = (tokens, heads, dim)
     if out is None:
         k = cache["records"].new_empty(shape, dtype=dtype)
         v = torch.empty_like(k)
+        kts = vts = heads * dim
+        khs = vhs = dim
     else:
         k, v = out
-        if torch.is_grad_enabled():
+        if (k.requires_grad or v.requires_grad) and torch.is_grad_enabled():
             _no_gradient(k, v)
-        dtype = k.dtype
-    kts, khs = _heads(k, "k", shape, dtype, dev)
-    vts, vhs = _heads(v, "v", shape, dtype, dev)
+        kts, khs = _heads(k, "k", shape, k.dtype, dev)
+        vts, vhs = _heads(v, "v", shape, k.dtype, dev)
     status = lib().pwq_cache_read(c, b, k.data_ptr(), kts, khs, v.data_ptr(), vts, vhs,
                                   _dtype_code(k), tokens, torch._C._cuda_getCurrentRawStream(dev))
     if status:
@@ -848,34 +860,32 @@ def cached_attention(q: torch.Tensor, cache: dict, starts: torch.Tensor, lengths
     if dev != torch._C._cuda_getDevice():
         with _on_device(dev):
             return cached_attention(q, cache, starts, lengths, table, scale, causal, prefix, out)
-    if torch.is_grad_enabled():
+    if (q.requires_grad or out is not None and out.requires_grad) and torch.is_grad_enabled():
         _no_gradient(q, out)
-    c, kv_heads, dim = _cache_struct(cache, dev)
-    b = _batch_struct(starts, lengths, table, dev)
-    if q.dim() != 3:
-        raise ValueError("q must be [tokens, heads, head_dim]")
+    c, b, _, dim, sizes = _cache_args(cache, starts, lengths, table, dev)
     shape = q.shape
-    tokens, heads = shape[0], shape[1]
+    if len(shape) != 3:
+        raise ValueError("q must be [tokens, heads, head_dim]")
+    tokens, heads, _ = shape
     qts, qhs = _heads(q, "q", (tokens, heads, dim), q.dtype, dev)
     dtype = _dtype_code(q)
     if out is None:
         out, ots, ohs = q.new_empty(shape), heads * dim, dim
     else:
         ots, ohs = _heads(out, "out", shape, q.dtype, dev)
-    p = None
+    p, n = None, -1
     if prefix is not None:
         pages, length = prefix
         n = pages.shape[0] if pages.dim() == 1 else -1
-        p = _lib.PwqBatch(None, _expect(length, "the prefix's length", (1,), torch.int32, dev),
-                          _expect(pages, "the prefix's pages", (n,), torch.int32, dev), n, 1, n)
-    L_ = lib()
-    ws, nb = None, L_.pwq_cached_attention_workspace_size(c, b, p, heads, dtype, tokens)
+        p = _PACK_BATCH(0, _expect(length, "the prefix's length", (1,), torch.int32, dev),
+                        _expect(pages, "the prefix's pages", (n,), torch.int32, dev), n, 1, n)
+    ws, nb = None, _attention_workspace(sizes, n, heads, dtype, tokens)
     if nb:
-        ws = torch.empty(nb, dtype=torch.uint8, device=q.device)
-    status = L_.pwq_cached_attention(c, b, p, q.data_ptr(), qts, qhs, out.data_ptr(), ots, ohs,
-                                     heads, dtype, tokens, dim ** -0.5 if scale is None else scale,
-                                     causal, None if ws is None else ws.data_ptr(), nb,
-                                     torch._C._cuda_getCurrentRawStream(dev))
+        ws = q.new_empty(nb, dtype=torch.uint8)
+    status = lib().pwq_cached_attention(
+        c, b, p, q.data_ptr(), qts, qhs, out.data_ptr(), ots, ohs, heads, dtype, tokens,
+        dim ** -0.5 if scale is None else scale, causal, None if ws is None else ws.data_ptr(),
+        nb, torch._C._cuda_getCurrentRawStream(dev))
     if status:
         check(status)
     return out

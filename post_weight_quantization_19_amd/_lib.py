@@ -80,7 +80,6 @@ _lib = None
 
 _vp, _i32, _i64, _f64, _sz = (ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64,
                               ctypes.c_double, ctypes.c_size_t)
-_pcache, _pbatch = ctypes.POINTER(PwqCache), ctypes.POINTER(PwqBatch)
 _SIGS = {
     "pwq_status_string": (ctypes.c_char_p, [_i32]),
     "pwq_last_error": (ctypes.c_char_p, []),
@@ -127,12 +126,12 @@ _SIGS = {
     "pwq_packed_linear": (_i32, [_vp, _i32, _i64, _i64, _vp, _vp, _i64, _i64, _vp, _vp, _i32,
                                  _vp, _vp, _i64, _vp, _i32, _i64, _vp, _sz, _vp]),
     "pwq_cache_record_bytes": (_i64, [_i32, _i32]),
-    "pwq_cache_write": (_i32, [_pcache, _pbatch, _vp, _i64, _i64, _vp, _i64, _i64, _i32, _i64,
+    "pwq_cache_write": (_i32, [_vp, _vp, _vp, _i64, _i64, _vp, _i64, _i64, _i32, _i64,
                                _vp]),
-    "pwq_cache_read": (_i32, [_pcache, _pbatch, _vp, _i64, _i64, _vp, _i64, _i64, _i32, _i64,
+    "pwq_cache_read": (_i32, [_vp, _vp, _vp, _i64, _i64, _vp, _i64, _i64, _i32, _i64,
                               _vp]),
-    "pwq_cached_attention_workspace_size": (_sz, [_pcache, _pbatch, _pbatch, _i32, _i32, _i64]),
-    "pwq_cached_attention": (_i32, [_pcache, _pbatch, _pbatch, _vp, _i64, _i64, _vp, _i64, _i64,
+    "pwq_cached_attention_workspace_size": (_sz, [_vp, _vp, _vp, _i32, _i32, _i64]),
+    "pwq_cached_attention": (_i32, [_vp, _vp, _vp, _vp, _i64, _i64, _vp, _i64, _i64,
                                     _i32, _i32, _i64, _f64, _i32, _vp, _sz, _vp]),
     "pwq_kernel_timer_attach": (_i32, [_i32, _vp, _vp, _i64]),
     "pwq_kernel_timer_count": (_i64, [_i32]),

@@ -671,39 +671,42 @@ __global__ __launch_bounds__(512, 1) void attend_tiles(const TilesArgs a) {
   const int records = (most + 31) / 32;
   const int i0 = (int)(records * split / a.splits), i1 = (int)(records * (split + 1) / a.splits);
 
-  // queries: this wave's rows, all rows scaled alike
+  // This wave's rows of queries: on their way while the first records are found.
   f16x8_t qf[RT][PARTS][J];
   int visible[RT];
-  float f;
-  {
+  float raw[RT][J][8];
+#pragma unroll
+  for (int rt = 0; rt < RT; ++rt) {
+    const int row = min((rt * WAVES + wave) * 16 + col, rows - 1);
+    visible[rt] = visible_of(row);
+    const int r = first + row;
+    const T* src = (const T*)a.q.p + (int64_t)(q.r0 + r / a.group) * a.q.ts +
+                   (int64_t)(h * a.group + r % a.group) * a.q.hs + 8 * g;
+#pragma unroll
+    for (int j = 0; j < J; ++j) load_row8(src + 32 * j, raw[rt][j]);
+  }
+  const int least = __builtin_amdgcn_readfirstlane(visible[0]);   // the first row sees least
+  float f = 0.0f;
+  // (all rows of the workgroup scaled alike)
+  auto scale_queries = [&]() __attribute__((always_inline)) {
     float top = 0.0f;
     bool bad[RT];
-    const T* src[RT];
 #pragma unroll
     for (int rt = 0; rt < RT; ++rt) {
-      const int row = min((rt * WAVES + wave) * 16 + col, rows - 1);
-      visible[rt] = visible_of(row);
-      const int r = first + row;
-      src[rt] = (const T*)a.q.p + (int64_t)(q.r0 + r / a.group) * a.q.ts +
-                (int64_t)(h * a.group + r % a.group) * a.q.hs + 8 * g;
       float mine = 0.0f;
 #pragma unroll
-      for (int j = 0; j < J; ++j) {
-        float x[8];
-        load_row8(src[rt] + 32 * j, x);
+      for (int j = 0; j < J; ++j)
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-          mine = fmaxf(mine, fabsf(x[e]));
-          if (x[e] != x[e]) mine = __builtin_inff();
+          mine = fmaxf(mine, fabsf(raw[rt][j][e]));
+          if (raw[rt][j][e] != raw[rt][j][e]) mine = __builtin_inff();
         }
-      }
       mine = fmaxf(mine, __shfl_xor(mine, 16, 64));
       mine = fmaxf(mine, __shfl_xor(mine, 32, 64));
       bad[rt] = !(mine <= __FLT_MAX__);
       if (!bad[rt]) top = fmaxf(top, mine);
     }
     top = wave_max(top);
-    __syncthreads();
     if (lane == 0) tops[wave] = top;
     __syncthreads();
     top = tops[0];
@@ -715,19 +718,15 @@ __global__ __launch_bounds__(512, 1) void attend_tiles(const TilesArgs a) {
 #pragma unroll
     for (int rt = 0; rt < RT; ++rt)
 #pragma unroll
-      for (int j = 0; j < J; ++j) {
-        float x[8];
-        load_row8(src[rt] + 32 * j, x);
+      for (int j = 0; j < J; ++j)
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-          const float v = bad[rt] ? __builtin_nanf("") : x[e] * up;
+          const float v = bad[rt] ? __builtin_nanf("") : raw[rt][j][e] * up;
           const _Float16 hi = (_Float16)v;
           qf[rt][0][j][e] = hi;
           if constexpr (PARTS == 2) qf[rt][1][j][e] = (_Float16)(v - (float)hi);
         }
-      }
-  }
-  const int least = __builtin_amdgcn_readfirstlane(visible[0]);   // the first row sees least
+  };
 
   // ---- staging
   // Records one after the other, up to the last.  Table entries come 64 at a time, and
@@ -1042,6 +1041,7 @@ __global__ __launch_bounds__(512, 1) void attend_tiles(const TilesArgs a) {
       if (k < 4) load_words(wq[k], at[k]);
       if (k < 2) load_codes(st[k], at[k]);
     }
+    scale_queries();
 #pragma unroll
     for (int k = 0; k < 3; ++k) steps(wq[k], k);
     wq[1] = wq[3];                           // of the fourth record; the fifth's
@@ -1078,7 +1078,6 @@ __global__ __launch_bounds__(512, 1) void attend_tiles(const TilesArgs a) {
     auto one = [&](int i, auto u) __attribute__((always_inline)) {
       constexpr int U = decltype(u)::value;             // (i - i0) % 4
       rescale();
-      __builtin_amdgcn_s_setprio(1);
       fetch_zeros((U + 2) & 3);
       Words& wn = wq[(U + 3) & 1];
       const Words old = wn;
@@ -1091,7 +1090,6 @@ __global__ __launch_bounds__(512, 1) void attend_tiles(const TilesArgs a) {
         if constexpr (k == kFrags / 2 + TURNS + 1) ahead_of = next_record();
         if constexpr (k == kFrags / 2 + TURNS + 2) load_words(wn, ahead_of);
       });
-      __builtin_amdgcn_s_setprio(0);
       turn(yes);
 #pragma unroll
       for (int rt = 0; rt < RT; ++rt) exps(rt);
@@ -1174,18 +1172,21 @@ struct JoinArgs {
 constexpr int kMostParts = 1024;   // of a row
 
 // A row's results from the workers that had tiles of its item, and from the splits of the
-// prefix: a workgroup per row.  All maxima and totals are read at once, then the sums
-// with as many loads in flight.
-template <typename T, int D>
+// prefix: WAVES waves a row, 4 / WAVES rows a workgroup.  All maxima and totals are read at
+// once, then the sums with as many loads in flight.
+template <typename T, int D, int WAVES>
 __global__ __launch_bounds__(256) void join_rows(const JoinArgs j) {
-  __shared__ float fac[kMostParts], red[2][4], so[4][D];
-  const int64_t b = block_index();
+  constexpr int ROWS = 4 / WAVES, MOST = kMostParts / ROWS, PER = MOST / (64 * WAVES);
+  __shared__ float fac[ROWS][MOST], red[2][4], so[4][D];
+  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
+  const int mine = ROWS == 1 ? 0 : wave, first = ROWS == 1 ? wave : 0;
+  const int64_t b = block_index() * ROWS + mine;
   const int head = (int)(b % j.heads), h = head / j.group;
+  // (rows of one workgroup are independent: no barrier between them)
   if (b / j.heads >= j.batch.ntok) return;
   const int t = (int)(b / j.heads);
-  const int s = find_sequence(j.batch, t);
+  const int s = find_sequence_wave(j.batch, t, lane);
   if (s < 0) return;
-  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
   const int64_t row = (int64_t)t * j.group + head % j.group;
   int n = 0, k = 0;
   const float* own = nullptr;
@@ -1217,63 +1218,90 @@ __global__ __launch_bounds__(256) void join_rows(const JoinArgs j) {
     *at = i < n ? k : kb;
     return i < n ? own + i * own_slot : before + (i - n) * before_slot;
   };
-  float mx[kMostParts / 256], lx[kMostParts / 256], top = kNone;
+  const int all = n + m, step = 64 * WAVES, me = first * 64 + lane;
+  float top = kNone, sum = 0.0f;
+  float o[D / 64] = {};
+  // (one wave takes parts MOST at a time, with the maximum and total so far)
+  for (int from = 0; from < all; from += MOST) {
+    const int count = min(all - from, MOST);
+    float mx[PER], lx[PER], next = kNone;
 #pragma unroll
-  for (int c = 0; c < kMostParts / 256; ++c) {
-    const int i = threadIdx.x + 256 * c;
-    mx[c] = kNone, lx[c] = 0.0f;
-    if (i < n + m) {
-      int rows, at;
-      const float* slot = part(i, &rows, &at);
-      mx[c] = slot[(int64_t)rows * D + at], lx[c] = slot[(int64_t)rows * (D + 1) + at];
+    for (int c = 0; c < PER; ++c) {
+      const int i = me + step * c;
+      mx[c] = kNone, lx[c] = 0.0f;
+      if (i < count) {
+        int rows, at;
+        const float* slot = part(from + i, &rows, &at);
+        mx[c] = slot[(int64_t)rows * D + at], lx[c] = slot[(int64_t)rows * (D + 1) + at];
+      }
+      next = fmaxf(next, mx[c]);
     }
-    top = fmaxf(top, mx[c]);
-  }
-  top = wave_max(top);
-  if (lane == 0) red[0][wave] = top;
-  __syncthreads();
-  top = fmaxf(fmaxf(red[0][0], red[0][1]), fmaxf(red[0][2], red[0][3]));
-  float sum = 0.0f;
+    next = wave_max(next);
+    if constexpr (WAVES > 1) {
+      __syncthreads();
+      if (lane == 0) red[0][wave] = next;
+      __syncthreads();
+      next = fmaxf(fmaxf(red[0][0], red[0][1]), fmaxf(red[0][2], red[0][3]));
+    }
+    next = fmaxf(next, top);
+    const float before_factor = top == kNone ? 1.0f : exp2f(top - next);
+    float add = 0.0f;
+    if constexpr (WAVES == 1) wave_meets();
 #pragma unroll
-  for (int c = 0; c < kMostParts / 256; ++c) {
-    const int i = threadIdx.x + 256 * c;
-    if (i >= n + m) break;
-    const float x = mx[c] == kNone ? 1.0f : exp2f(mx[c] - top);     // (NaN sums stay)
-    fac[i] = x;
-    sum += lx[c] * x;
-  }
-#pragma unroll
-  for (int o = 32; o >= 1; o >>= 1) sum += __shfl_xor(sum, o, 64);
-  if (lane == 0) red[1][wave] = sum;
-  __syncthreads();
-  sum = red[1][0] + red[1][1] + red[1][2] + red[1][3];
-  constexpr int E = D / 64, AT_ONCE = 8;
-  float o[E] = {};
-  for (int i0 = wave; i0 < n + m; i0 += 4 * AT_ONCE) {
-    float x[AT_ONCE][E];
-#pragma unroll
-    for (int c = 0; c < AT_ONCE; ++c) {
-      int rows, at;
-      const float* slot = part(min(i0 + 4 * c, n + m - 1), &rows, &at);
-#pragma unroll
-      for (int e = 0; e < E; ++e) x[c][e] = slot[(int64_t)at * D + 64 * e + lane];
+    for (int c = 0; c < PER; ++c) {
+      const int i = me + step * c;
+      if (i >= count) break;
+      const float x = mx[c] == kNone ? 1.0f : exp2f(mx[c] - next);     // (NaN sums stay)
+      fac[mine][i] = x;
+      add += lx[c] * x;
     }
 #pragma unroll
-    for (int c = 0; c < AT_ONCE; ++c)
-      if (i0 + 4 * c < n + m)
+    for (int u = 32; u >= 1; u >>= 1) add += __shfl_xor(add, u, 64);
+    if constexpr (WAVES > 1) {
+      if (lane == 0) red[1][wave] = add;
+      __syncthreads();
+      add = red[1][0] + red[1][1] + red[1][2] + red[1][3];
+    } else {
+      wave_meets();
+    }
+    sum = sum * before_factor + add;
+    top = next;
 #pragma unroll
-        for (int e = 0; e < E; ++e) o[e] = fmaf(x[c][e], fac[i0 + 4 * c], o[e]);
+    for (int e = 0; e < D / 64; ++e) o[e] *= before_factor;
+    constexpr int AT_ONCE = 8;
+    for (int i0 = first; i0 < count; i0 += WAVES * AT_ONCE) {
+      float x[AT_ONCE][D / 64];
+#pragma unroll
+      for (int c = 0; c < AT_ONCE; ++c) {
+        int rows, at;
+        const float* slot = part(from + min(i0 + WAVES * c, count - 1), &rows, &at);
+#pragma unroll
+        for (int e = 0; e < D / 64; ++e) x[c][e] = slot[(int64_t)at * D + 64 * e + lane];
+      }
+#pragma unroll
+      for (int c = 0; c < AT_ONCE; ++c)
+        if (i0 + WAVES * c < count)
+#pragma unroll
+          for (int e = 0; e < D / 64; ++e) o[e] = fmaf(x[c][e], fac[mine][i0 + WAVES * c], o[e]);
+    }
   }
+  if constexpr (WAVES > 1) {
 #pragma unroll
-  for (int e = 0; e < E; ++e) so[wave][64 * e + lane] = o[e];
-  __syncthreads();
-  const int d = threadIdx.x;
-  if (d < D) {
-    const float v = so[0][d] + so[1][d] + so[2][d] + so[3][d];
-    const float y = sum == 0.0f ? 0.0f : v / sum;
-    const int64_t to = (int64_t)t * j.out.ts + (int64_t)head * j.out.hs + d;
-    if constexpr (std::is_same_v<T, float>) ((float*)j.out.p)[to] = y;
-    else ((__bf16*)j.out.p)[to] = (__bf16)y;
+    for (int e = 0; e < D / 64; ++e) so[wave][64 * e + lane] = o[e];
+    __syncthreads();
+    if (wave != 0) return;
+#pragma unroll
+    for (int e = 0; e < D / 64; ++e) {
+      const int d = 64 * e + lane;
+      o[e] = so[0][d] + so[1][d] + so[2][d] + so[3][d];
+    }
+  }
+  const int64_t to = (int64_t)t * j.out.ts + (int64_t)head * j.out.hs + lane;
+#pragma unroll
+  for (int e = 0; e < D / 64; ++e) {
+    const float y = sum == 0.0f ? 0.0f : o[e] / sum;
+    if constexpr (std::is_same_v<T, float>) ((float*)j.out.p)[to + 64 * e] = y;
+    else ((__bf16*)j.out.p)[to + 64 * e] = (__bf16)y;
   }
 }
 
@@ -1302,6 +1330,7 @@ struct Launch {
   RowsArgs rows;
   TilesArgs tiles[2];          // the batch's, the prefix's; splits 0: none
   bool joined;
+  int64_t parts;               // of a row, about
 };
 
 template <typename T, int D, int BITS>
@@ -1312,9 +1341,10 @@ void launch_all(const Launch& l, hipStream_t st) {
           <<<block_grid(t.items * t.splits * t.cache.heads), 512, 0, st>>>(t);
   if (l.rows.workers)
     attend_rows<T, D, BITS><<<block_grid(l.rows.workers * l.rows.cache.heads), 256, 0, st>>>(l.rows);
-  if (l.joined)
-    join_rows<T, D><<<block_grid((int64_t)l.join.batch.ntok * l.join.heads), 256, 0, st>>>(
-        l.join);
+  if (!l.joined) return;
+  const int64_t rows = (int64_t)l.join.batch.ntok * l.join.heads;
+  if (l.parts > 32) join_rows<T, D, 4><<<block_grid(rows), 256, 0, st>>>(l.join);
+  else join_rows<T, D, 1><<<block_grid((rows + 3) / 4), 256, 0, st>>>(l.join);
 }
 
 template <typename T, int D>
@@ -1332,6 +1362,12 @@ void launch_dim(const Launch& l, int dim, int bits, hipStream_t st) {
 
 }  // namespace
 
+#ifndef XMIN
+#define XMIN 64
+#endif
+#ifndef XTH
+#define XTH 32
+#endif
 AttentionPlan attention_plan(const AttentionLaunch& a) {
   AttentionPlan p{};
   const int64_t heads = a.cache.heads, group = a.heads / heads;
@@ -1340,10 +1376,10 @@ AttentionPlan attention_plan(const AttentionLaunch& a) {
   // Splits of the tokens: workgroups for every CU, where items alone are fewer, of
   // at least 256 tokens.
   auto splits = [&](int64_t items, const CacheBatch& b) {
-    const int64_t most = std::max<int64_t>(1, capacity_of(b, a.cache) / 256);
+    const int64_t most = std::max<int64_t>(1, capacity_of(b, a.cache) / XMIN);
     return std::min(std::max<int64_t>(1, 256 / (items * heads)), most);
   };
-  p.tiles = rows > 32 * seqs;
+  p.tiles = rows > XTH * seqs;
   if (p.tiles) {
     p.items = rows / tile + seqs;
     p.splits = splits((rows + tile - 1) / tile, a.batch);
@@ -1371,6 +1407,8 @@ hipError_t launch_cached_attention(const AttentionLaunch& a, const AttentionPlan
   const int capacity = capacity_of(a.batch, a.cache);
   Launch l{};
   l.joined = p.own_bytes > 0;
+  l.parts = (p.tiles ? p.splits : p.workers / std::max<int64_t>(1, p.items)) +
+            (a.prefix.nseq ? p.prefix_splits : 0);
   l.join.batch = a.batch, l.join.out = a.out;
   l.join.heads = a.heads, l.join.group = group, l.join.capacity = capacity;
   l.join.own = (const float*)own, l.join.found = (const Found*)found;

@@ -57,6 +57,20 @@ __device__ __forceinline__ int find_sequence(const CacheBatch& b, int t) {
   return lo;
 }
 
+// The same for a wave whose lanes all ask for row t: 64 starts at a time.
+__device__ __forceinline__ int find_sequence_wave(const CacheBatch& b, int t, int lane) {
+  int lo = 0, count = b.nseq;
+  while (count > 1) {
+    const int step = (count + 63) >> 6, at = lane * step;
+    const int below = __popcll(__ballot(at < count && b.starts[lo + min(at, count - 1)] <= t));
+    if (below == 0) return -1;
+    lo += (below - 1) * step;
+    count = min(step, count - (below - 1) * step);
+  }
+  if (count < 1 || t < b.starts[lo] || t >= b.starts[lo + 1]) return -1;
+  return lo;
+}
+
 // Address of the record of head h that holds block `block` (of 32 tokens) of a
 // table row; NULL for a hole.
 __device__ __forceinline__ const uint8_t* record_of(const CacheView& c, const int32_t* row,

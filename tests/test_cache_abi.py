@@ -1,5 +1,6 @@
 """include/pwq_cache.h without a device: exports, sizes and refusals, the oracle's
 own pins, and what the binding refuses."""
+import ctypes
 import os
 import re
 
@@ -34,11 +35,11 @@ def test_record_bytes(dim, bits, want):
 
 
 def cache(records=FAR, pages=10, kv_heads=2, head_dim=128, bits=8, page=64):
-    return B.PwqCache(records, pages, kv_heads, head_dim, bits, page)
+    return ctypes.byref(B.PwqCache(records, pages, kv_heads, head_dim, bits, page))
 
 
 def batch(starts=FAKE, lengths=FAKE, table=FAKE, ldt=4, nseq=3, width=4):
-    return B.PwqBatch(starts, lengths, table, ldt, nseq, width)
+    return ctypes.byref(B.PwqBatch(starts, lengths, table, ldt, nseq, width))
 
 
 BAD_CACHES = [dict(records=None), dict(records=FAR + 8), dict(pages=-1), dict(pages=1 << 39),
