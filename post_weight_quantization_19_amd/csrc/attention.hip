@@ -240,15 +240,17 @@ struct RowsArgs {
   Found* found;            // of each row: token * group + query head of the key head's
 };
 
+// The batch's, and the prefix's (workers 0: none).
+struct RowsPair {
+  RowsArgs a[2];
+};
+
 // Attention of 16 rows at a time: worker w of a key head takes the tiles w c .. w c + c - 1
 // of all items in a row, and each of its waves 32 tokens of a tile, by itself: a record
 // is spread in the registers of the wave that multiplies by it, with the next one's codes
 // on the way.
-#ifndef XOCC
-#define XOCC 2
-#endif
 template <typename T, int D, int BITS>
-__global__ __launch_bounds__(256, D == 256 ? 1 : XOCC) void attend_rows(const RowsArgs a) {
+__global__ __launch_bounds__(256, D == 256 ? 1 : 2) void attend_rows(const RowsPair both) {
   using R = Record<D, BITS>;
   constexpr int PARTS = std::is_same_v<T, float> ? 2 : 1;
   constexpr int J = D / 32, N = D / 16, KW = R::lane_bytes / 16;
@@ -256,8 +258,11 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : XOCC) void attend_rows(const Ro
   __shared__ int entries[4][64];
   __shared__ float sm[4][kRows], sl[4][kRows];
   __shared__ float so[4][kRows][D + 4];
-  const int h = (int)(block_index() % a.cache.heads);
-  const int64_t w = block_index() / a.cache.heads;
+  const int64_t own_blocks = both.a[0].workers * both.a[0].cache.heads;
+  const RowsArgs& a = both.a[block_index() >= own_blocks];
+  const int64_t block = block_index() - (block_index() >= own_blocks ? own_blocks : 0);
+  const int h = (int)(block % a.cache.heads);
+  const int64_t w = block / a.cache.heads;
   if (w >= a.workers) return;
   const int lane = threadIdx.x & 63, g = lane >> 4, col = lane & 15;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6) & 3;
@@ -1164,10 +1169,13 @@ struct JoinArgs {
   const Found* found;
   int64_t own_per_head;
   int own_rows, own_tiles;     // own_tiles: by attend_tiles, which has slots for every row
-  // the prefix's: all of its splits, of the row's tile; NULL: none
+  // the prefix's, NULL: none: all of its splits of the row's tile, or (before_found) as
+  // the batch's own
   const float* before;
-  int64_t before_items;
-  int before_rows, before_splits;
+  const Found* before_found;
+  int64_t before_per_head;
+  int before_rows, before_splits, before_capacity;
+  const int32_t* before_length;
 };
 constexpr int kMostParts = 1024;   // of a row
 
@@ -1188,29 +1196,38 @@ __global__ __launch_bounds__(256) void join_rows(const JoinArgs j) {
   const int s = find_sequence_wave(j.batch, t, lane);
   if (s < 0) return;
   const int64_t row = (int64_t)t * j.group + head % j.group;
-  int n = 0, k = 0;
-  const float* own = nullptr;
+  int n = 0, k = 0, m = 0, kb = 0;
+  const float *own = nullptr, *before = nullptr;
   const int64_t own_slot = (int64_t)j.own_rows * (D + 2);
+  const int64_t before_slot = (int64_t)j.before_rows * (D + 2);
+  // (with starts that descend, nothing may have been found)
+  auto good = [](const Found& at, int rows, int64_t per_head) {
+    return at.first >= 0 && at.n >= 0 && at.k >= 0 && at.k < rows &&
+           at.first + (int64_t)at.n <= per_head && at.n <= kMostParts / 2;
+  };
   if (j.own_tiles || min(sequence(j.batch, s).len, j.capacity) > 0) {
     const Found at = j.found[row];
     if (at.n == -1) return;                            // written already
-    // (with starts that descend, nothing may have been found)
-    if (at.first >= 0 && at.n >= 0 && at.k >= 0 && at.k < j.own_rows &&
-        at.first + (int64_t)at.n <= j.own_per_head && at.n <= kMostParts / 2) {
+    if (good(at, j.own_rows, j.own_per_head)) {
       n = at.n, k = at.k;
       own = j.own + ((int64_t)h * j.own_per_head + at.first) * own_slot;
     }
   }
-  int m = 0, kb = 0;
-  const float* before = nullptr;
-  const int64_t before_slot = (int64_t)j.before_rows * (D + 2);
-  if (j.before) {
+  if (j.before_found) {
+    if (min(j.before_length[0], j.before_capacity) > 0) {
+      const Found at = j.before_found[row];
+      if (good(at, j.before_rows, j.before_per_head)) {
+        m = at.n, kb = at.k;
+        before = j.before + ((int64_t)h * j.before_per_head + at.first) * before_slot;
+      }
+    }
+  } else if (j.before) {
     const int64_t r = row - (int64_t)clamp_row(j.batch.starts[0], j.batch.ntok) * j.group;
-    const int64_t item = r / j.before_rows;
+    const int64_t first_slot = r / j.before_rows * j.before_splits;
     kb = (int)(r % j.before_rows);
-    if (item < j.before_items) {
+    if (first_slot < j.before_per_head) {
       m = j.before_splits;
-      before = j.before + ((int64_t)h * j.before_items + item) * m * before_slot;
+      before = j.before + ((int64_t)h * j.before_per_head + first_slot) * before_slot;
     }
   }
   auto part = [&](int i, int* rows, int* at) {
@@ -1327,7 +1344,7 @@ int capacity_of(const CacheBatch& b, const CacheView& c) {
 
 struct Launch {
   JoinArgs join;
-  RowsArgs rows;
+  RowsPair rows;               // workers 0: none
   TilesArgs tiles[2];          // the batch's, the prefix's; splits 0: none
   bool joined;
   int64_t parts;               // of a row, about
@@ -1339,8 +1356,9 @@ void launch_all(const Launch& l, hipStream_t st) {
     if (t.splits)
       attend_tiles<T, D, BITS, Shape<T, D>::rt>
           <<<block_grid(t.items * t.splits * t.cache.heads), 512, 0, st>>>(t);
-  if (l.rows.workers)
-    attend_rows<T, D, BITS><<<block_grid(l.rows.workers * l.rows.cache.heads), 256, 0, st>>>(l.rows);
+  const int64_t blocks = l.rows.a[0].workers * l.rows.a[0].cache.heads +
+                         l.rows.a[1].workers * l.rows.a[1].cache.heads;
+  if (blocks) attend_rows<T, D, BITS><<<block_grid(blocks), 256, 0, st>>>(l.rows);
   if (!l.joined) return;
   const int64_t rows = (int64_t)l.join.batch.ntok * l.join.heads;
   if (l.parts > 32) join_rows<T, D, 4><<<block_grid(rows), 256, 0, st>>>(l.join);
@@ -1362,45 +1380,65 @@ void launch_dim(const Launch& l, int dim, int bits, hipStream_t st) {
 
 }  // namespace
 
-#ifndef XMIN
-#define XMIN 64
-#endif
-#ifndef XTH
-#define XTH 32
-#endif
 AttentionPlan attention_plan(const AttentionLaunch& a) {
   AttentionPlan p{};
   const int64_t heads = a.cache.heads, group = a.heads / heads;
   const int64_t rows = a.batch.ntok * group, seqs = std::min(a.batch.nseq, a.batch.ntok);
-  const int64_t tile = tile_rows_of(a.dtype, a.head_dim);
-  // Splits of the tokens: workgroups for every CU, where items alone are fewer, of
-  // at least 256 tokens.
-  auto splits = [&](int64_t items, const CacheBatch& b) {
-    const int64_t most = std::max<int64_t>(1, capacity_of(b, a.cache) / XMIN);
-    return std::min(std::max<int64_t>(1, 256 / (items * heads)), most);
+  const int64_t tile = tile_rows_of(a.dtype, a.head_dim), slot = (a.head_dim + 2) * 4;
+  // Tiles of rows, or 16 rows at a time, by their estimated time, us, for the tokens that the
+  // tables have room for: per row and token in float16 products of 128 channels, tiles
+  // half of the other's, but of whole tiles and 12 us longer to start; an item of 16 rows
+  // starts in the time of 384 tokens.  Measured, us, 16 rows at a time and tiles (bf16,
+  // 8 key heads of 128 channels in 8 bits):
+  //   rows of a sequence      64         128        256        512        1024
+  //   1 sequence, 2500 tokens 18, 25     19, 27     23, 35     32, 37     43, 45
+  //   1, 16000                29, 43     41, 46     63, 53     106, 72    185, 107
+  //   8, 2500                 34, 45     41, 53     77, 65     148, 101   299, 124
+  //   64, 300                 52, 50     94, 58     178, 70    351, 138   759, 299
+  auto by_tiles = [&](int64_t rows_each, int64_t n, int64_t tokens) {
+    const double unit = a.head_dim / 128.0 * (a.dtype == PWQ_F32 ? 2 : 1) * n * heads;
+    const double whole = (double)((rows_each + tile - 1) / tile * tile);
+    return 1.25e-6 * unit * rows_each * (tokens + 384) > 0.65e-6 * unit * whole * tokens + 12;
   };
-  p.tiles = rows > XTH * seqs;
+  // Splits of the tokens: workgroups for every CU, where items alone are fewer, of
+  // at least 64 tokens (128: 1111 tokens before 8 sequences 28.9 us instead of 28.3, 256:
+  // 33.7).
+  auto splits = [&](int64_t items, int64_t tokens) {
+    return std::min(std::max<int64_t>(1, 256 / (items * heads)),
+                    std::max<int64_t>(1, tokens / 64));
+  };
+  const int64_t workers = std::max<int64_t>(1, 512 / heads);
+  const int64_t tokens = capacity_of(a.batch, a.cache);
+  p.tiles = by_tiles((rows + seqs - 1) / seqs, seqs, tokens);
   if (p.tiles) {
     p.items = rows / tile + seqs;
-    p.splits = splits((rows + tile - 1) / tile, a.batch);
-    if (p.splits > 1 || a.prefix.nseq)
-      p.own_bytes = p.items * p.splits * heads * tile * (a.head_dim + 2) * 4;
+    p.splits = splits((rows / seqs + tile - 1) / tile * seqs, tokens);
+    if (p.splits > 1 || a.prefix.nseq) p.own_bytes = p.items * p.splits * heads * tile * slot;
   } else {
-    p.workers = std::max<int64_t>(1, 512 / heads);
+    p.workers = workers;
     p.items = rows / kRows + seqs;
-    p.own_bytes = (p.workers + p.items) * heads * kRows * (a.head_dim + 2) * 4;
+    p.own_bytes = (p.workers + p.items) * heads * kRows * slot;
   }
   if (p.own_bytes) p.found_bytes = rows * sizeof(Found);
   if (a.prefix.nseq) {
-    p.prefix_items = (rows + tile - 1) / tile;
-    p.prefix_splits = splits(p.prefix_items, a.prefix);
-    p.prefix_bytes = p.prefix_items * p.prefix_splits * heads * tile * (a.head_dim + 2) * 4;
+    const int64_t before = capacity_of(a.prefix, a.cache);
+    p.prefix_tiles = by_tiles(rows, 1, before);
+    if (p.prefix_tiles) {
+      p.prefix_items = (rows + tile - 1) / tile;
+      p.prefix_splits = splits(p.prefix_items, before);
+      p.prefix_bytes = p.prefix_items * p.prefix_splits * heads * tile * slot;
+    } else {
+      p.prefix_workers = workers;
+      p.prefix_items = (rows + kRows - 1) / kRows;
+      p.prefix_bytes = (workers + p.prefix_items) * heads * kRows * slot;
+      p.prefix_found_bytes = rows * sizeof(Found);
+    }
   }
   return p;
 }
 
-hipError_t launch_cached_attention(const AttentionLaunch& a, const AttentionPlan& p, void* own,
-                                   void* found, void* prefix, hipStream_t st) {
+hipError_t launch_cached_attention(const AttentionLaunch& a, const AttentionPlan& p,
+                                   const AttentionWs& w, hipStream_t st) {
   if (a.batch.ntok == 0 || a.batch.nseq == 0) return hipSuccess;
   const int group = a.heads / a.cache.heads;
   const int tile = tile_rows_of(a.dtype, a.head_dim);
@@ -1408,28 +1446,38 @@ hipError_t launch_cached_attention(const AttentionLaunch& a, const AttentionPlan
   Launch l{};
   l.joined = p.own_bytes > 0;
   l.parts = (p.tiles ? p.splits : p.workers / std::max<int64_t>(1, p.items)) +
-            (a.prefix.nseq ? p.prefix_splits : 0);
+            p.prefix_splits + p.prefix_workers / std::max<int64_t>(1, p.prefix_items);
   l.join.batch = a.batch, l.join.out = a.out;
   l.join.heads = a.heads, l.join.group = group, l.join.capacity = capacity;
-  l.join.own = (const float*)own, l.join.found = (const Found*)found;
+  l.join.own = (const float*)w.own, l.join.found = (const Found*)w.found;
   l.join.own_per_head = p.tiles ? p.items * p.splits : p.workers + p.items;
   l.join.own_rows = p.tiles ? tile : kRows, l.join.own_tiles = p.tiles;
   if (p.tiles)
     l.tiles[0] = TilesArgs{a.cache, a.batch, a.q, a.out, group, a.heads, a.causal, capacity,
-                           p.splits, p.items, a.scale, p.own_bytes ? (float*)own : nullptr,
-                           p.own_bytes ? (Found*)found : nullptr};
+                           p.splits, p.items, a.scale, p.own_bytes ? (float*)w.own : nullptr,
+                           p.own_bytes ? (Found*)w.found : nullptr};
   else
-    l.rows = RowsArgs{a.cache, a.batch, a.q, a.out, group, a.heads, a.causal, capacity,
-                      a.prefix.nseq == 0, p.workers, p.items, a.scale, (float*)own,
-                      (Found*)found};
+    l.rows.a[0] = RowsArgs{a.cache, a.batch, a.q, a.out, group, a.heads, a.causal, capacity,
+                           a.prefix.nseq == 0, p.workers, p.items, a.scale, (float*)w.own,
+                           (Found*)w.found};
   if (a.prefix.nseq) {
     CacheBatch b = a.prefix;
     b.starts = a.batch.starts, b.starts_step = a.batch.nseq, b.ntok = a.batch.ntok;
-    l.tiles[1] = TilesArgs{a.cache, b, a.q, a.out, group, a.heads, 0,
-                           capacity_of(a.prefix, a.cache), p.prefix_splits,
-                           p.prefix_items, a.scale, (float*)prefix, nullptr};
-    l.join.before = (const float*)prefix, l.join.before_items = p.prefix_items;
-    l.join.before_rows = tile, l.join.before_splits = (int)p.prefix_splits;
+    const int before = capacity_of(a.prefix, a.cache);
+    if (p.prefix_tiles)
+      l.tiles[1] = TilesArgs{a.cache, b, a.q, a.out, group, a.heads, 0, before, p.prefix_splits,
+                             p.prefix_items, a.scale, (float*)w.prefix, nullptr};
+    else
+      l.rows.a[1] = RowsArgs{a.cache, b, a.q, a.out, group, a.heads, 0, before, 0,
+                             p.prefix_workers, p.prefix_items, a.scale, (float*)w.prefix,
+                             (Found*)w.prefix_found};
+    l.join.before = (const float*)w.prefix;
+    l.join.before_found = (const Found*)w.prefix_found;
+    l.join.before_per_head = p.prefix_tiles ? p.prefix_items * p.prefix_splits
+                                            : p.prefix_workers + p.prefix_items;
+    l.join.before_rows = p.prefix_tiles ? tile : kRows;
+    l.join.before_splits = (int)p.prefix_splits;
+    l.join.before_capacity = before, l.join.before_length = a.prefix.lengths;
   }
   if (a.dtype == PWQ_F32) launch_dim<float>(l, a.head_dim, a.bits, st);
   else launch_dim<uint16_t>(l, a.head_dim, a.bits, st);

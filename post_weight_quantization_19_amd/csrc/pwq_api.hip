@@ -1240,11 +1240,12 @@ static pwq_status check_attention(const pwq_cache* cache, const pwq_batch* batch
   return check_cache(cache, &p, ntok, heads, dtype);
 }
 
-static void* carve_attention(Carver& c, const AttentionPlan& p, void** found, void** prefix) {
-  void* own = c.take(p.own_bytes);
-  *found = c.take(p.found_bytes);
-  *prefix = p.prefix_bytes ? c.take(p.prefix_bytes) : nullptr;
-  return own;
+static AttentionWs carve_attention(Carver& c, const AttentionPlan& p) {
+  auto take = [&](size_t bytes) { return bytes ? c.take(bytes) : nullptr; };
+  AttentionWs w;
+  w.own = take(p.own_bytes), w.found = take(p.found_bytes);
+  w.prefix = take(p.prefix_bytes), w.prefix_found = take(p.prefix_found_bytes);
+  return w;
 }
 
 size_t pwq_cached_attention_workspace_size(const pwq_cache* cache, const pwq_batch* batch,
@@ -1259,9 +1260,8 @@ size_t pwq_cached_attention_workspace_size(const pwq_cache* cache, const pwq_bat
   if (check_attention(&c, &b, prefix ? &p : nullptr, heads, dtype, ntok) != PWQ_OK) return 0;
   if (ntok == 0 || b.nseq == 0) return 0;
   Carver carve(nullptr);
-  void *found, *before;
   carve_attention(carve, attention_plan(attention_launch(&c, &b, prefix ? &p : nullptr, heads,
-                                                         dtype, ntok)), &found, &before);
+                                                         dtype, ntok)));
   return carve.size();
 }
 
@@ -1291,12 +1291,11 @@ pwq_status pwq_cached_attention(const pwq_cache* cache, const pwq_batch* batch,
   a.causal = causal != 0, a.scale = (float)scale;
   const AttentionPlan p = attention_plan(a);
   Carver measure(nullptr), carve(ws);
-  void *found, *before;
-  carve_attention(measure, p, &found, &before);
+  carve_attention(measure, p);
   s = check_ws(ws, ws_bytes, measure.size());
   if (s != PWQ_OK) return s;
-  void* own = carve_attention(carve, p, &found, &before);
-  const hipError_t e = launch_cached_attention(a, p, own, found, before, (hipStream_t)stream);
+  const hipError_t e =
+      launch_cached_attention(a, p, carve_attention(carve, p), (hipStream_t)stream);
   if (e != hipSuccess) return hip_fail(e, "cached_attention launch");
   return ok();
 }

@@ -276,16 +276,19 @@ struct AttentionLaunch {
   float scale;
 };
 struct AttentionPlan {
-  bool tiles;                       // many rows to a sequence: tiles of rows, else 16 rows
-  int64_t workers;                  // 16 rows: workgroups per key head
-  int64_t items, splits;            // items per key head, at most; splits of an item's tokens
-  int64_t prefix_items, prefix_splits;
+  bool tiles, prefix_tiles;         // many rows to a sequence: tiles of rows, else 16 rows
+  int64_t workers, prefix_workers;  // 16 rows: workgroups per key head
+  int64_t items, prefix_items;      // items per key head, at most
+  int64_t splits, prefix_splits;    // tiles: of an item's tokens
   size_t own_bytes, prefix_bytes;   // partial results
-  size_t found_bytes;               // where a row's are
+  size_t found_bytes, prefix_found_bytes;   // where a row's are
+};
+struct AttentionWs {
+  void *own, *found, *prefix, *prefix_found;
 };
 AttentionPlan attention_plan(const AttentionLaunch& a);
-hipError_t launch_cached_attention(const AttentionLaunch& a, const AttentionPlan& p, void* own,
-                                   void* found, void* prefix, hipStream_t st);
+hipError_t launch_cached_attention(const AttentionLaunch& a, const AttentionPlan& p,
+                                   const AttentionWs& w, hipStream_t st);
 
 // Event pairs recorded around launches of one kernel (pwq_kernel_timer_attach).
 struct KernelTimer {
