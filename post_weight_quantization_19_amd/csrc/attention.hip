@@ -229,11 +229,36 @@ __device__ __forceinline__ Share share_of(const Walk& w, int64_t worker, int64_t
   return r;
 }
 
+// The sequence of an item (in units of ROWS rows), and the item's number in it; -1
+// past the last.
+template <int ROWS>
+__device__ __forceinline__ int64_t items_of(const Seq& q, int group) {
+  return ((int64_t)(q.r1 - q.r0) * group + ROWS - 1) / ROWS;
+}
+template <int ROWS>
+__device__ __forceinline__ int find_item(const CacheBatch& b, int group, int64_t item, int* in,
+                                         Scan& sc) {
+  if (threadIdx.x == 0) sc.found[0] = -1;
+  int64_t before = 0;
+  for (int base = 0; base < b.nseq; base += 256) {
+    const int s = threadIdx.x < 256 ? base + (int)threadIdx.x : b.nseq;
+    const int64_t n = s < b.nseq ? items_of<ROWS>(sequence(b, s), group) : 0;
+    int64_t at, unused, all, none;
+    scan2(n, 0, &at, &unused, &all, &none, sc.red);
+    at += before;
+    if (item >= at && item < at + n) sc.found[0] = s, sc.found[1] = item - at;
+    before += all;
+  }
+  __syncthreads();
+  *in = (int)sc.found[1];
+  return (int)sc.found[0];
+}
+
 struct RowsArgs {
   CacheView cache;
   CacheBatch batch;
   CacheTensor q, out;
-  int group, heads, causal, capacity, direct;
+  int group, heads, causal, capacity, direct, whole;   // whole: a worker for each item
   int64_t workers, items;
   float scale;
   float* slots;
@@ -259,7 +284,7 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void attend_rows(const RowsP
   __shared__ float sm[4][kRows], sl[4][kRows];
   __shared__ float so[4][kRows][D + 4];
   const int64_t own_blocks = both.a[0].workers * both.a[0].cache.heads;
-  const RowsArgs& a = both.a[block_index() >= own_blocks];
+  const RowsArgs a = both.a[block_index() >= own_blocks];
   const int64_t block = block_index() - (block_index() >= own_blocks ? own_blocks : 0);
   const int h = (int)(block % a.cache.heads);
   const int64_t w = block / a.cache.heads;
@@ -267,14 +292,26 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void attend_rows(const RowsP
   const int lane = threadIdx.x & 63, g = lane >> 4, col = lane & 15;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6) & 3;
   const Walk walk{a.batch, a.group, a.capacity};
-  const Share sh = share_of(walk, w, a.workers, sc);
-  const int64_t end = min(sh.total, (w + 1) * sh.c);
-  int64_t at = w * sh.c;
-  if (at >= end || sh.seq < 0) return;
+  Share sh;
+  int64_t at, end;
+  if (a.whole) {                                       // item w
+    int in;
+    sh.seq = find_item<kRows>(a.batch, a.group, w, &in, sc);
+    if (sh.seq < 0) return;
+    const Seq mine = walk.seq(sh.seq);
+    const int per = max(walk.tiles(mine), kStart + 1);
+    sh.item = w - in, sh.tile = 0, sh.c = per;
+    at = (int64_t)in * per, end = at + per;
+  } else {
+    sh = share_of(walk, w, a.workers, sc);
+    end = min(sh.total, (w + 1) * sh.c);
+    at = w * sh.c;
+    if (at >= end || sh.seq < 0) return;
+  }
   int s = sh.seq;
   int64_t item0 = sh.item, tile0 = sh.tile;
   Seq q = walk.seq(s);
-  int per = walk.tiles(q), count = walk.items(q);
+  int per = a.whole ? (int)sh.c : walk.tiles(q), count = walk.items(q);
   const uint8_t* head_base = a.cache.records + (((int64_t)h << a.cache.blocks_shift) * R::bytes);
   const int64_t page_bytes = ((int64_t)a.cache.heads << a.cache.blocks_shift) * R::bytes;
   const int in_page = (1 << a.cache.blocks_shift) - 1;
@@ -295,7 +332,7 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void attend_rows(const RowsP
     if (tb <= 0) return;                               // the next worker starts it
     const int rows = (int)min((int64_t)kRows, (int64_t)(q.r1 - q.r0) * a.group - in * kRows);
     const bool whole = a.direct && ta == 0 && tb == per - kStart;
-    if (ta == 0 && h == 0 && threadIdx.x < rows) {
+    if (!a.whole && ta == 0 && h == 0 && threadIdx.x < rows) {
       const int64_t last = (item_tile + per - 1) / sh.c;
       a.found[(int64_t)q.r0 * a.group + in * kRows + threadIdx.x] =
           Found{(int)(w + item), whole ? -1 : (int)(last - w) + 1, (int)threadIdx.x, 0};
@@ -595,31 +632,6 @@ struct TilesArgs {
   float* slots;            // NULL: one split, results written to out
   Found* found;            // as for attend_rows; NULL: not wanted
 };
-
-// The sequence of an item (in units of ROWS rows), and the item's number in it; -1
-// past the last.
-template <int ROWS>
-__device__ __forceinline__ int64_t items_of(const Seq& q, int group) {
-  return ((int64_t)(q.r1 - q.r0) * group + ROWS - 1) / ROWS;
-}
-template <int ROWS>
-__device__ __forceinline__ int find_item(const CacheBatch& b, int group, int64_t item, int* in,
-                                         Scan& sc) {
-  if (threadIdx.x == 0) sc.found[0] = -1;
-  int64_t before = 0;
-  for (int base = 0; base < b.nseq; base += 256) {
-    const int s = threadIdx.x < 256 ? base + (int)threadIdx.x : b.nseq;
-    const int64_t n = s < b.nseq ? items_of<ROWS>(sequence(b, s), group) : 0;
-    int64_t at, unused, all, none;
-    scan2(n, 0, &at, &unused, &all, &none, sc.red);
-    at += before;
-    if (item >= at && item < at + n) sc.found[0] = s, sc.found[1] = item - at;
-    before += all;
-  }
-  __syncthreads();
-  *in = (int)sc.found[1];
-  return (int)sc.found[0];
-}
 
 // Attention of 128 RT rows, 16 RT to each of eight waves: all waves take the same
 // records of 32 tokens one after the other, spread to float16 by the workgroup once and
@@ -1415,9 +1427,14 @@ AttentionPlan attention_plan(const AttentionLaunch& a) {
     p.splits = splits((rows / seqs + tile - 1) / tile * seqs, tokens);
     if (p.splits > 1 || a.prefix.nseq) p.own_bytes = p.items * p.splits * heads * tile * slot;
   } else {
-    p.workers = workers;
     p.items = rows / kRows + seqs;
-    p.own_bytes = (p.workers + p.items) * heads * kRows * slot;
+    // Few tokens: a worker for each item and nothing to join.  Us, joined and so (bf16, 8 key
+    // heads of 128 channels in 8 bits): one sequence of 250 tokens 13.6, 9.7, of 500 13.8,
+    // 11.5, of 900 14.0, 14.8, of 1900 14.2, 20.2; 64 of 900 29.6, 26.3, of 1900 48.9, 44.0;
+    // of 256 channels one of 250 15.3, 12.0, of 900 15.8, 19.6.
+    p.whole = tokens <= std::min<int64_t>(1024, 131072 / a.head_dim) && !a.prefix.nseq;
+    p.workers = p.whole ? p.items : workers;
+    if (!p.whole) p.own_bytes = (p.workers + p.items) * heads * kRows * slot;
   }
   if (p.own_bytes) p.found_bytes = rows * sizeof(Found);
   if (a.prefix.nseq) {
@@ -1458,8 +1475,9 @@ hipError_t launch_cached_attention(const AttentionLaunch& a, const AttentionPlan
                            p.own_bytes ? (Found*)w.found : nullptr};
   else
     l.rows.a[0] = RowsArgs{a.cache, a.batch, a.q, a.out, group, a.heads, a.causal, capacity,
-                           a.prefix.nseq == 0, p.workers, p.items, a.scale, (float*)w.own,
-                           (Found*)w.found};
+                           a.prefix.nseq == 0, p.whole, p.workers, p.items, a.scale,
+                           (float*)w.own, (Found*)w.found};
+  l.rows.a[1].cache = a.cache;
   if (a.prefix.nseq) {
     CacheBatch b = a.prefix;
     b.starts = a.batch.starts, b.starts_step = a.batch.nseq, b.ntok = a.batch.ntok;
@@ -1468,7 +1486,7 @@ hipError_t launch_cached_attention(const AttentionLaunch& a, const AttentionPlan
       l.tiles[1] = TilesArgs{a.cache, b, a.q, a.out, group, a.heads, 0, before, p.prefix_splits,
                              p.prefix_items, a.scale, (float*)w.prefix, nullptr};
     else
-      l.rows.a[1] = RowsArgs{a.cache, b, a.q, a.out, group, a.heads, 0, before, 0,
+      l.rows.a[1] = RowsArgs{a.cache, b, a.q, a.out, group, a.heads, 0, before, 0, 0,
                              p.prefix_workers, p.prefix_items, a.scale, (float*)w.prefix,
                              (Found*)w.prefix_found};
     l.join.before = (const float*)w.prefix;

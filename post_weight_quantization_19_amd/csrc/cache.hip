@@ -62,7 +62,7 @@ __device__ __forceinline__ uint32_t quantize(float (&x)[8], int (&code)[8]) {
 #pragma unroll
   for (int e = 0; e < 8; ++e) {
     lo = fminf(lo, x[e]), hi = fmaxf(hi, x[e]);
-    sum += x[e] * 0.0f;                                   // NaN after a NaN or an infinity
+    sum = fmaf(x[e], 0.0f, sum);                          // NaN after a NaN or an infinity
   }
 #pragma unroll
   for (int o = 1; o < D / 8; o <<= 1) {
@@ -84,9 +84,18 @@ __device__ __forceinline__ uint32_t quantize(float (&x)[8], int (&code)[8]) {
   s *= up;
   const float inv = 1.0f / s;
   const float z = fminf(nearest(-lo * up, s, inv), TOP);
+  // Away from ties the product with 1 / s rounds like the quotient.
+  float off = 0.0f;
 #pragma unroll
-  for (int e = 0; e < 8; ++e)
-    code[e] = (int)fminf(fmaxf(nearest(x[e] * up, s, inv) + z, 0.0f), TOP);
+  for (int e = 0; e < 8; ++e) {
+    const float v = x[e] * up * inv, r = __builtin_rintf(v);
+    off = fmaxf(off, fabsf(v - r));
+    code[e] = (int)__builtin_amdgcn_fmed3f(r + z, 0.0f, TOP);
+  }
+  if (off > 0.5f - 0x1p-13f)
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+      code[e] = (int)__builtin_amdgcn_fmed3f(nearest(x[e] * up, s, inv) + z, 0.0f, TOP);
   return word | (uint32_t)(int)z;
 }
 

@@ -277,6 +277,7 @@ struct AttentionLaunch {
 };
 struct AttentionPlan {
   bool tiles, prefix_tiles;         // many rows to a sequence: tiles of rows, else 16 rows
+  bool whole;                       // 16 rows: a workgroup for each item, nothing to join
   int64_t workers, prefix_workers;  // 16 rows: workgroups per key head
   int64_t items, prefix_items;      // items per key head, at most
   int64_t splits, prefix_splits;    // tiles: of an item's tokens
