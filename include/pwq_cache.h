@@ -119,16 +119,21 @@ pwq_status pwq_cache_read(const pwq_cache* cache, const pwq_batch* batch, void* 
  *            cache and has no two elements in one place.
  *   scale  : 1e-30 .. 1e30.
  *   ws     : pwq_cached_attention_workspace_size bytes, 256-byte aligned.
- * Keys and values multiply as their codes, exactly.  Queries multiply in one
- * float16 part of a row scaled by a power of two (PWQ_BF16: exact where an
- * element is above 2^-38 of its row's largest) or in two (PWQ_F32: within 2^-22
- * of the element).  The softmax's weight of a token, times its step, multiplies
- * values in one float16 part (PWQ_BF16: off by 2^-12 at most) or in two (PWQ_F32:
- * 2^-22).  Sums, maxima and totals are float32, in a fixed order; how a sequence
- * is split, and so the last bits of its rows, depends on the whole batch.  A row
- * of q with an infinity or NaN, or with a token it sees that reads as NaN, gives
- * NaN; other rows are unaffected.  Scores, and steps times 2^44, have to stay
- * within float32.
+ * Keys multiply as their codes, exactly, and values too but where said.  Rows of a
+ * sequence are taken 16 together, or 128 or 256 where there are many, and a power of
+ * two scales those rows' queries so that the largest element fits float16:
+ *   PWQ_BF16 : an element is exact where it is above 2^-30 of that largest, else
+ *              off by 2^-38 of it.  A token's weight times its step is rounded to
+ *              float16 once (2^-12).  Where rows are taken 128 or 256 together weight, step and
+ *              step times code are each rounded (3 times 2^-12).
+ *   PWQ_F32  : two float16 parts, for elements as for weights: within 2^-22, or 2^-38
+ *              of the largest element.
+ * A weight is off by 2^-33 of the largest so far at least, and a step (128 or 256 together,
+ * PWQ_BF16) by 2^-30 of the largest of the sequence's steps.  Sums, maxima and totals
+ * are float32, in a fixed order; how a sequence is split, and so the last bits of
+ * its rows, depends on the sizes and starts and lengths of the whole batch.  A row of q with an
+ * infinity or NaN, or with a token it sees that reads as NaN, gives NaN; other rows are
+ * unaffected.  Scores, and steps times 2^44, have to stay within float32.
  * ---------------------------------------------------------------------- */
 size_t pwq_cached_attention_workspace_size(const pwq_cache* cache, const pwq_batch* batch,
                                            const pwq_batch* prefix, int32_t heads, int32_t dtype,

@@ -1,4 +1,19 @@
 // Writing to the key-value cache and reading it back (include/pwq_cache.h).
+//
+// A head of a token becomes codes of one step and zero point, which depend on its own
+// values only: everything is read once, reduced over the D / 8 lanes that hold the head, and
+// written once.  The bound is memory for many tokens, and the time of a launch with its chain
+// of three dependent loads (starts, table, record) for few.  Codes lie as the matrix
+// cores take them, a token's value codes in single bytes 8 or 16 apart: row by row those are
+// stores of single bytes, which is right for a token or two per record, and a block of 32
+// tokens is put together in LDS and leaves in whole pieces of 16 bytes where there are many.
+//
+// Measured with the caches' own bytes warm, us (writing, reading; bf16, 8 key heads of 128
+// channels in 8 bits unless said otherwise): one token 3.5, 2.5; 256 sequences' next tokens in
+// 4 bits 5.8, 4.6; 8192 tokens of 4 prompts 24.0 and 15.2 (50 MB each, 2.1 and 3.3 TB/s;
+// writing's quantization, not memory, is what is left: two divisions' worth of work per head
+// and eight byte stores to LDS per lane); 65536 tokens read 89.7 (403 MB, 4.5 TB/s, where a large
+// copy reaches 5.03).
 #include "cache_device.h"
 
 namespace pwq {
@@ -363,8 +378,20 @@ __global__ __launch_bounds__(256) void read_blocks(const CacheRowsLaunch a) {
 
 template <typename T, int D, int BITS>
 void launch_rows_of(const CacheRowsLaunch& a, bool write, hipStream_t st) {
-  // Many rows to a sequence: whole blocks.  (XXX)
-  if (a.batch.ntok >= 4 * (int64_t)a.batch.nseq) {
+  // Whole blocks where there are enough values to fill the card with them and enough rows to
+  // a sequence to fill most of a block; else row by row.  Measured, us, rows and blocks (bf16,
+  // 8 key heads of 128 channels in 8 bits; f32 with 2 of 64 crosses at as many values):
+  //   write, sequences x rows    1x256     8x128     64x32       64x64       8x1024
+  //                              4.9, 8.9  8.7, 9.9  13.6, 13.8  22.2, 16.8  34.1, 21.5
+  //                              256x4      256x16      256x32
+  //                              9.5, 19.4  24.4, 33.3  39.2, 34.0
+  //   read                       1x256     8x64      1x1024    64x32      8x1024
+  //                              3.9, 4.8  4.7, 4.8  5.8, 5.1  10.2, 6.2  29.2, 12.2
+  //                              256x4     256x8      256x32
+  //                              7.1, 8.2  11.8, 9.5  34.1, 15.3
+  const int64_t values = (int64_t)a.batch.ntok * a.cache.heads * D;
+  if (values >= (write ? 3 << 19 : 1 << 19) &&
+      a.batch.ntok >= (write ? 32 : 8) * (int64_t)a.batch.nseq) {
     const int64_t windows = a.batch.ntok / 32 + 2 * (int64_t)a.batch.nseq;
     const dim3 grid = block_grid(windows * a.cache.heads);
     if (write) write_blocks<T, D, BITS><<<grid, 256, 0, st>>>(a);
