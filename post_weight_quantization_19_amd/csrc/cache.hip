@@ -10,10 +10,9 @@
 //
 // Measured with the caches' own bytes warm, us (writing, reading; bf16, 8 key heads of 128
 // channels in 8 bits unless said otherwise): one token 3.5, 2.5; 256 sequences' next tokens in
-// 4 bits 5.8, 4.6; 8192 tokens of 4 prompts 24.0 and 15.2 (50 MB each, 2.1 and 3.3 TB/s;
-// writing's quantization, not memory, is what is left: two divisions' worth of work per head
-// and eight byte stores to LDS per lane); 65536 tokens read 89.7 (403 MB, 4.5 TB/s, where a large
-// copy reaches 5.03).
+// 4 bits 5.9, 4.6; 10589 tokens of 6 prompts 24.0 and 15.3 (66 MB each, 2.7 and 4.3 TB/s;
+// writing's quantization, and its byte stores to LDS, not memory, are what is left); 65536
+// tokens read 89.8 (407 MB, 4.5 TB/s, where a large copy reaches 5.03).
 #include "cache_device.h"
 
 namespace pwq {
