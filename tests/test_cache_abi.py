@@ -38,7 +38,8 @@ def cache(records=FAR, pages=10, kv_heads=2, head_dim=128, bits=8, page=64):
     return ctypes.byref(B.PwqCache(records, pages, kv_heads, head_dim, bits, page))
 
 
-def batch(starts=FAKE, lengths=FAKE, table=FAKE, ldt=4, nseq=3, width=4):
+# Tables with room for so many tokens that attention needs a workspace.
+def batch(starts=FAKE, lengths=FAKE, table=FAKE, ldt=40, nseq=3, width=40):
     return ctypes.byref(B.PwqBatch(starts, lengths, table, ldt, nseq, width))
 
 
@@ -128,6 +129,7 @@ def test_workspace_size():
     need = size(cache(records=None), batch(starts=None, lengths=None, table=None), None, 8, 1, 9)
     assert need > 0 and need % 256 == 0
     assert size(cache(), batch(), batch(nseq=1), 8, 1, 9) > need
+    assert size(cache(), batch(width=4), None, 8, 1, 9) == 0          # 256 tokens: no join
     assert size(cache(), batch(), None, 8, 1, 0) == 0
     assert size(cache(), batch(nseq=0), None, 8, 1, 9) == 0
     assert size(cache(head_dim=80), batch(), None, 8, 1, 9) == 0
