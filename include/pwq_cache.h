@@ -87,7 +87,8 @@ int64_t pwq_cache_record_bytes(int32_t head_dim, int32_t bits);
 /* ---------------------------------------------------------------------- *
  * Quantizes the rows of a batch into the cache.
  *   k, v : ntok x kv_heads x D, dtype PWQ_F32 or PWQ_BF16; element (t, h, d) at
- *          t * tstride + h * hstride + d (strides >= 0, in elements).
+ *          t * tstride + h * hstride + d (strides >= 0, in elements; those of
+ *          several tokens or heads times their number at most 2^56).
  *          ntok * kv_heads < 2^30 (and ntok * heads below).
  * ---------------------------------------------------------------------- */
 pwq_status pwq_cache_write(const pwq_cache* cache, const pwq_batch* batch, const void* k,

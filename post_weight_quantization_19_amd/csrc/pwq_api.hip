@@ -1114,9 +1114,14 @@ int64_t pwq_cache_record_bytes(int32_t head_dim, int32_t bits) {
 // heads lie together, else one of everything.
 static Rows tensor_rows(const void* p, int64_t ntok, int64_t heads, int64_t dim, int64_t ts,
                         int64_t hs, int32_t dtype) {
+  if (ntok <= 1) ts = 0;                           // any stride: it is never used
   const int64_t width = (heads - 1) * hs + dim;
   if (ts >= width) return Rows(p, ntok, width, ts, dtype);
   return Rows(p, ntok > 0, (ntok - 1) * ts + width, 0, dtype);
+}
+// Whether n items lie so near that sums of two such distances, in bytes, fit 64 bits.
+static bool near_enough(int64_t n, int64_t stride) {
+  return stride >= 0 && (n <= 1 || stride <= ((int64_t)1 << 56) / n);
 }
 // Whether all elements have places of their own (heads within tokens, or tokens
 // within heads).
@@ -1139,7 +1144,7 @@ static pwq_status check_cache(const pwq_cache* c, const pwq_batch* b, int64_t nt
     return fail(PWQ_ERR_INVALID_ARG, "more than 2^40 records");
   if (dtype != PWQ_F32 && dtype != PWQ_BF16)
     return fail(PWQ_ERR_INVALID_ARG, "tensors must be PWQ_F32 or PWQ_BF16");
-  if (ntok < 0 || ntok * 2 > INT32_MAX / heads)
+  if (ntok < 0 || ntok > INT32_MAX / heads / 2)
     return fail(PWQ_ERR_INVALID_ARG, "need ntok >= 0 and ntok * heads < 2^30");
   if (b->nseq < 0 || b->width < 0 || b->ldt < b->width)
     return fail(PWQ_ERR_INVALID_ARG, "need nseq >= 0 and ldt >= width >= 0");
@@ -1168,8 +1173,9 @@ static Rows cache_rows(const pwq_cache* c) {
 
 static pwq_status check_heads(const pwq_cache* c, const void* k, int64_t kts, int64_t khs,
                               const void* v, int64_t vts, int64_t vhs, int64_t ntok) {
-  if (kts < 0 || khs < 0 || vts < 0 || vhs < 0)
-    return fail(PWQ_ERR_INVALID_ARG, "strides must be >= 0");
+  if (!near_enough(ntok, kts) || !near_enough(c->kv_heads, khs) || !near_enough(ntok, vts) ||
+      !near_enough(c->kv_heads, vhs))
+    return fail(PWQ_ERR_INVALID_ARG, "strides must be >= 0, and a tensor within 2^56 elements");
   if (ntok > 0 && (!k || !v)) return fail(PWQ_ERR_INVALID_ARG, "k and v must be non-NULL");
   return PWQ_OK;
 }
@@ -1273,8 +1279,9 @@ pwq_status pwq_cached_attention(const pwq_cache* cache, const pwq_batch* batch,
                                 void* stream) {
   pwq_status s = check_attention(cache, batch, prefix, heads, dtype, ntok);
   if (s != PWQ_OK) return s;
-  if (q_tstride < 0 || q_hstride < 0 || out_tstride < 0 || out_hstride < 0)
-    return fail(PWQ_ERR_INVALID_ARG, "strides must be >= 0");
+  if (!near_enough(ntok, q_tstride) || !near_enough(heads, q_hstride) ||
+      !near_enough(ntok, out_tstride) || !near_enough(heads, out_hstride))
+    return fail(PWQ_ERR_INVALID_ARG, "strides must be >= 0, and a tensor within 2^56 elements");
   if (ntok > 0 && (!q || !out)) return fail(PWQ_ERR_INVALID_ARG, "q and out must be non-NULL");
   if (!((float)scale >= 1e-30f) || !((float)scale <= 1e30f))
     return fail(PWQ_ERR_INVALID_ARG, "scale must be in 1e-30 .. 1e30");
