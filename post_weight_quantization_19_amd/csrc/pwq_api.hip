@@ -1110,14 +1110,41 @@ int64_t pwq_cache_record_bytes(int32_t head_dim, int32_t bits) {
   return 8 * (int64_t)head_dim * bits + 256;
 }
 
-// A tensor ntok x heads x dim as rows of memory: a row per token where a token's
-// heads lie together, else one of everything.
-static Rows tensor_rows(const void* p, int64_t ntok, int64_t heads, int64_t dim, int64_t ts,
-                        int64_t hs, int32_t dtype) {
-  if (ntok <= 1) ts = 0;                           // any stride: it is never used
-  const int64_t width = (heads - 1) * hs + dim;
-  if (ts >= width) return Rows(p, ntok, width, ts, dtype);
-  return Rows(p, ntok > 0, (ntok - 1) * ts + width, 0, dtype);
+// A tensor ntok x heads x dim.
+struct Heads {
+  const void* p;
+  int64_t ntok, heads, dim, ts, hs;
+  int32_t dtype;
+  Heads(const void* p, int64_t ntok, int64_t heads, int64_t dim, int64_t ts, int64_t hs,
+        int32_t dtype)
+      : p(p), ntok(ntok), heads(heads), dim(dim), ts(ntok > 1 ? ts : 0), hs(heads > 1 ? hs : 0),
+        dtype(dtype) {}
+  // As rows of memory: a row per token where a token's heads lie together, else one of
+  // everything.
+  Rows rows() const {
+    const int64_t width = (heads - 1) * hs + dim;
+    if (ts >= width) return Rows(p, ntok, width, ts, dtype);
+    return Rows(p, ntok > 0, (ntok - 1) * ts + width, 0, dtype);
+  }
+};
+// (Tensors of the same strides may lie between each other: by whole heads, or by the
+// tokens of a head.)
+static bool overlap(const Heads& a, const Heads& b) {
+  if (!overlap(a.rows(), b.rows())) return false;
+  if (a.ts != b.ts || a.hs != b.hs || a.dim != b.dim || a.dtype != b.dtype) return true;
+  const int64_t near = std::min(a.ts, a.hs), far = std::max(a.ts, a.hs);
+  if (near >= a.dim && far % near == 0) {
+    auto pieces = [&](const Heads& t) {
+      const int64_t n = a.ts == near ? t.ntok : t.heads, m = a.ts == near ? t.heads : t.ntok;
+      return Rows(t.p, (m - 1) * (far / near) + n, t.dim, near, t.dtype);
+    };
+    if (!overlap(pieces(a), pieces(b))) return false;
+  }
+  auto head_rows = [](const Heads& t) {
+    return Rows(t.p, t.heads, (t.ntok - 1) * t.ts + t.dim, t.hs, t.dtype);
+  };
+  return a.hs * elem_bytes(a.dtype) < std::max(head_rows(a).width, head_rows(b).width) ||
+         overlap(head_rows(a), head_rows(b));
 }
 // Whether n items lie so near that sums of two such distances, in bytes, fit 64 bits.
 static bool near_enough(int64_t n, int64_t stride) {
@@ -1189,8 +1216,8 @@ pwq_status pwq_cache_write(const pwq_cache* cache, const pwq_batch* batch, const
   if (s != PWQ_OK) return s;
   const int64_t heads = cache->kv_heads, dim = cache->head_dim;
   const Rows rc = cache_rows(cache);
-  if (overlap(rc, tensor_rows(k, ntok, heads, dim, k_tstride, k_hstride, dtype)) ||
-      overlap(rc, tensor_rows(v, ntok, heads, dim, v_tstride, v_hstride, dtype)))
+  if (overlap(rc, Heads(k, ntok, heads, dim, k_tstride, k_hstride, dtype).rows()) ||
+      overlap(rc, Heads(v, ntok, heads, dim, v_tstride, v_hstride, dtype).rows()))
     return fail(PWQ_ERR_INVALID_ARG, "the cache must not overlap k or v");
   CacheRowsLaunch a{cache_view(cache), cache_batch(batch, ntok),
                     {(void*)k, k_tstride, k_hstride}, {(void*)v, v_tstride, v_hstride},
@@ -1211,10 +1238,10 @@ pwq_status pwq_cache_read(const pwq_cache* cache, const pwq_batch* batch, void* 
   if (!distinct(ntok, heads, dim, k_tstride, k_hstride) ||
       !distinct(ntok, heads, dim, v_tstride, v_hstride))
     return fail(PWQ_ERR_INVALID_ARG, "elements of k, or of v, share a place");
-  const Rows rk = tensor_rows(k, ntok, heads, dim, k_tstride, k_hstride, dtype);
-  const Rows rv = tensor_rows(v, ntok, heads, dim, v_tstride, v_hstride, dtype);
+  const Heads hk(k, ntok, heads, dim, k_tstride, k_hstride, dtype);
+  const Heads hv(v, ntok, heads, dim, v_tstride, v_hstride, dtype);
   const Rows rc = cache_rows(cache);
-  if (overlap(rk, rv) || overlap(rc, rk) || overlap(rc, rv))
+  if (overlap(hk, hv) || overlap(rc, hk.rows()) || overlap(rc, hv.rows()))
     return fail(PWQ_ERR_INVALID_ARG, "k, v and the cache must not overlap");
   CacheRowsLaunch a{cache_view(cache), cache_batch(batch, ntok), {k, k_tstride, k_hstride},
                     {v, v_tstride, v_hstride}, dtype, cache->head_dim, cache->bits};
@@ -1288,9 +1315,9 @@ pwq_status pwq_cached_attention(const pwq_cache* cache, const pwq_batch* batch,
   const int64_t dim = cache->head_dim;
   if (!distinct(ntok, heads, dim, out_tstride, out_hstride))
     return fail(PWQ_ERR_INVALID_ARG, "elements of out share a place");
-  const Rows ro = tensor_rows(out, ntok, heads, dim, out_tstride, out_hstride, dtype);
-  if (overlap(ro, tensor_rows(q, ntok, heads, dim, q_tstride, q_hstride, dtype)) ||
-      overlap(ro, cache_rows(cache)))
+  const Heads ho(out, ntok, heads, dim, out_tstride, out_hstride, dtype);
+  if (overlap(ho, Heads(q, ntok, heads, dim, q_tstride, q_hstride, dtype)) ||
+      overlap(ho.rows(), cache_rows(cache)))
     return fail(PWQ_ERR_INVALID_ARG, "out must not overlap q or the cache");
   if (ntok == 0 || batch->nseq == 0) return ok();
   AttentionLaunch a = attention_launch(cache, batch, prefix, heads, dtype, ntok);
