@@ -129,12 +129,13 @@ pwq_status pwq_cache_read(const pwq_cache* cache, const pwq_batch* batch, void* 
  *              step times code are each rounded (3 times 2^-12).
  *   PWQ_F32  : two float16 parts, for elements as for weights: within 2^-22, or 2^-38
  *              of the largest element.
- * A weight is off by 2^-33 of the largest so far at least, and a step (128 or 256 together,
- * PWQ_BF16) by 2^-30 of the largest of the sequence's steps.  Sums, maxima and totals
- * are float32, in a fixed order; how a sequence is split, and so the last bits of
- * its rows, depends on the sizes and starts and lengths of the whole batch.  A row of q with an
- * infinity or NaN, or with a token it sees that reads as NaN, gives NaN; other rows are
- * unaffected.  Scores, and steps times 2^44, have to stay within float32.
+ * A weight is off by 2^-33 of the largest so far at least (2^-25 where scores pass
+ * 2^25), and a step (128 or 256 together, PWQ_BF16) by 2^-30 of the largest of the
+ * sequence's steps.  Sums, maxima and totals are float32, in a fixed order; how a
+ * sequence is split, and so the last bits of its rows, depends on the sizes and starts
+ * and lengths of the whole batch.  A row of q with an infinity or NaN, or with a token
+ * it sees that reads as NaN, gives NaN; other rows are unaffected.  Scores, and steps
+ * times 2^44, have to stay within float32.
  * ---------------------------------------------------------------------- */
 size_t pwq_cached_attention_workspace_size(const pwq_cache* cache, const pwq_batch* batch,
                                            const pwq_batch* prefix, int32_t heads, int32_t dtype,

@@ -11,7 +11,8 @@
 // float16 parts).  The result has a lane for four keys of one row, which is where the
 // next product, values times weights, wants its weights: P never leaves the
 // registers.  Weights are held as 2^8 at the running maximum, up to 2^12 before it is
-// raised, so that sums are rescaled rarely.
+// raised, so that sums are rescaled rarely.  A partial result is the maximum less 8, and the
+// total and the sums of weights of 1 there.
 //
 // Two kernels, for few rows of a sequence and for many, and one that joins what the
 // workers of a row have found.  attend_rows is bound by memory where the cache is long,
@@ -56,6 +57,30 @@ __device__ __forceinline__ void wave_meets() {
 __device__ __forceinline__ f32x4_t mfma(f16x8_t a, f16x8_t b, f32x4_t c) {
   return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0);
 }
+// Weights 2^(t - base) of scores t = acc sk, two ways.  One fma gives the exact product less
+// base.  The maximum is a rounded product, off by half of float32's spacing: from 2^25 on
+// that is 2 and more, and at 2^30 the largest weight may be anything in 2^-56 .. 2^72 (a
+// single token gave 0 or NaN).  weight_of takes the rounded product too, so that the largest
+// score less the maximum is exact.  It is for rows whose maximum is that far from 0, and used where
+// a maximum has just been raised.  Weights are held as 2^8 at the maximum as far as float32
+// tells scores 8 apart.
+constexpr float kFar = 0x1p25f;
+__device__ __forceinline__ bool is_far(float base) {
+  return fabsf(base) >= kFar && base != kNone;
+}
+__device__ __forceinline__ float weight_of(float acc, float sk, float base) {
+  float t = acc * sk;
+  pin(t);                              // (not an fma after all)
+  return __builtin_amdgcn_exp2f(t - base);
+}
+__device__ __forceinline__ float base_of(float most) {
+  return fabsf(most) < 4.0f * kFar ? most - 8.0f : most;
+}
+// In place of the tokens that all rows see: every record is looked at as one with hidden
+// tokens, where weights are taken by weight_of.  (Another branch for each record, or
+// more instructions in these, made prompts 1 to 2% slower; so it is up to 1%.)
+constexpr int kAlways = INT32_MIN;
+
 __device__ __forceinline__ f16x2_t as_half2(uint32_t w) { return __builtin_bit_cast(f16x2_t, w); }
 __device__ __forceinline__ uint32_t as_word(f16x2_t h) { return __builtin_bit_cast(uint32_t, h); }
 __device__ __forceinline__ f16x8_t as_half8(uint4 w) { return __builtin_bit_cast(f16x8_t, w); }
@@ -356,7 +381,7 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void attend_rows(const RowsP
     const int token = r / a.group, head = h * a.group + r % a.group;
     const int held = min(q.len, a.capacity);
     const int visible = min(held, a.causal ? q.len - (q.r1 - q.r0) + token + 1 : q.len);
-    const int least = __builtin_amdgcn_readfirstlane(visible);
+    int least = __builtin_amdgcn_readfirstlane(visible);
     const int most = __builtin_amdgcn_readlane(visible, rows - 1);
     f16x8_t qf[PARTS][J];
     float f;
@@ -497,7 +522,12 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void attend_rows(const RowsP
         };
         exps();
         const bool masked = p0 + 32 > least || n < 32;
-        if (masked) hide();
+        if (masked) {
+          if (least == kAlways)
+#pragma unroll
+            for (int i = 0; i < 8; ++i) e[i] = weight_of(acc[i / 4][i % 4], sk[i / 4][i % 4], base);
+          hide();
+        }
         float top = 0.0f, sv[8], most_step = 0.0f;
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
@@ -526,10 +556,11 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void attend_rows(const RowsP
             if (i / 4 * 16 + i % 4 < seen) m = fmaxf(m, acc[i / 4][i % 4] * sk[i / 4][i % 4]);
           m = fmaxf(m, __shfl_xor(m, 16, 64));
           m = fmaxf(m, __shfl_xor(m, 32, 64));
-          const float next = __any(top > 4096.0f) ? fmaxf(base, m - 8.0f) : base;
+          const float next = __any(top > 4096.0f) ? fmaxf(base, base_of(m)) : base;
           float factor = base == kNone ? 0.0f : __builtin_amdgcn_exp2f(base - next);
           l *= factor;
           base = next;
+          if (__any(is_far(base))) least = kAlways;
           const float largest = wave_max(most_step);
           if (largest > ref * 8.0f) {
             const float to = __uint_as_float(
@@ -542,8 +573,7 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void attend_rows(const RowsP
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
             const bool poisoned = e[i] != e[i];
-            const float x =
-                __builtin_amdgcn_exp2f(fmaf(acc[i / 4][i % 4], sk[i / 4][i % 4], -base));
+            const float x = weight_of(acc[i / 4][i % 4], sk[i / 4][i % 4], base);
             if (!poisoned) e[i] = masked && i / 4 * 16 + i % 4 >= seen ? 0.0f : x;
           }
         }
@@ -595,9 +625,8 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void attend_rows(const RowsP
     // the four waves' results
     l += __shfl_xor(l, 16, 64);
     l += __shfl_xor(l, 32, 64);
-    const float m2 = base == kNone ? kNone : base + 8.0f;
     __syncthreads();
-    if (g == 0) sm[wave][col] = m2, sl[wave][col] = l * (1.0f / 256.0f);
+    if (g == 0) sm[wave][col] = base, sl[wave][col] = l;
     __syncthreads();
     float all = kNone, sum = 0.0f;
 #pragma unroll
@@ -606,12 +635,11 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void attend_rows(const RowsP
     for (int i = 0; i < 4; ++i)
       sum += sm[i][col] == kNone ? sl[i][col] : sl[i][col] * exp2f(sm[i][col] - all);
     // the whole result's weights are divided by here
-    const float part = (m2 == kNone ? 1.0f : exp2f(m2 - all)) *
+    const float part = (base == kNone ? 1.0f : exp2f(base - all)) *
                        (whole ? (sum == 0.0f ? 0.0f : 1.0f / sum) : 1.0f);
-    const float back = ref * (1.0f / 256.0f);
 #pragma unroll
     for (int n = 0; n < N; ++n)
-      *(f32x4_t*)&so[wave][col][16 * n + 4 * g] = o[n] * part * back;
+      *(f32x4_t*)&so[wave][col][16 * n + 4 * g] = o[n] * part * ref;
     __syncthreads();
     float* slot = a.slots + ((int64_t)h * (a.workers + a.items) + w + item) * kSlot<D>;
     for (int i = threadIdx.x; i < rows * (D / 4); i += 256) {
@@ -716,7 +744,7 @@ __global__ __launch_bounds__(512, 1) void attend_tiles(const TilesArgs a) {
 #pragma unroll
     for (int j = 0; j < J; ++j) load_row8(src + 32 * j, raw[rt][j]);
   }
-  const int least = __builtin_amdgcn_readfirstlane(visible[0]);   // the first row sees least
+  int least = __builtin_amdgcn_readfirstlane(visible[0]);   // the first row sees least
   float f = 0.0f;
   // (all rows of the workgroup scaled alike)
   auto scale_queries = [&]() __attribute__((always_inline)) {
@@ -930,6 +958,11 @@ __global__ __launch_bounds__(512, 1) void attend_tiles(const TilesArgs a) {
   f32x4_t score[RT][2], sk[2];             // of a record's tokens, and the tokens' steps
   float2 now = make_float2(0.0f, 0.0f);    // about the record
   float e[RT][8];
+  auto far_exps = [&](int rt) __attribute__((always_inline)) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      e[rt][i] = weight_of(score[rt][i / 4][i % 4], sk[i / 4][i % 4], base[rt]);
+  };
   auto exps = [&](int rt) __attribute__((always_inline)) {
 #pragma unroll
     for (int t = 0; t < 2; ++t)
@@ -951,7 +984,10 @@ __global__ __launch_bounds__(512, 1) void attend_tiles(const TilesArgs a) {
     const bool masked = p0 + 32 > least || n < 32;
     if (masked)
 #pragma unroll
-      for (int rt = 0; rt < RT; ++rt) hide(rt, p0, n);
+      for (int rt = 0; rt < RT; ++rt) {
+        if (least == kAlways) far_exps(rt);
+        hide(rt, p0, n);
+      }
     float top = 0.0f;
 #pragma unroll
     for (int rt = 0; rt < RT; ++rt)
@@ -969,13 +1005,14 @@ __global__ __launch_bounds__(512, 1) void attend_tiles(const TilesArgs a) {
         }
         m = fmaxf(m, __shfl_xor(m, 16, 64));
         m = fmaxf(m, __shfl_xor(m, 32, 64));
-        const float next = fmaxf(base[rt], m - 8.0f);
+        const float next = fmaxf(base[rt], base_of(m));
         const float factor = base[rt] == kNone ? 0.0f : __builtin_amdgcn_exp2f(base[rt] - next);
         base[rt] = next;
+        if (__any(is_far(next))) least = kAlways;
         l[rt] *= factor;
 #pragma unroll
         for (int nn = 0; nn < N; ++nn) o[rt][nn] *= factor;
-        exps(rt);
+        far_exps(rt);
         if (masked) hide(rt, p0, n);
       }
     }
@@ -1149,7 +1186,7 @@ __global__ __launch_bounds__(512, 1) void attend_tiles(const TilesArgs a) {
     }
   }
   if (!busy) return;
-  const float back = ref / (kUnit * 256.0f);
+  const float back = ref / kUnit;
   float* slot = a.slots + (((int64_t)h * a.items + item) * a.splits + split) * (ROWS * (D + 2));
 #pragma unroll
   for (int rt = 0; rt < RT; ++rt) {
@@ -1159,7 +1196,6 @@ __global__ __launch_bounds__(512, 1) void attend_tiles(const TilesArgs a) {
       sum += __shfl_xor(sum, 16, 64);
       sum += __shfl_xor(sum, 32, 64);
     }
-    sum *= 1.0f / 256.0f;
     if (row >= rows) continue;
     if (a.slots == nullptr) {
       const float unit = sum == 0.0f ? 0.0f : back / sum;
@@ -1179,7 +1215,7 @@ __global__ __launch_bounds__(512, 1) void attend_tiles(const TilesArgs a) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) slot[row * D + 16 * n + 4 * g + i] = o[rt][n][i] * back;
       if (g == 0) {
-        slot[ROWS * D + row] = base[rt] == kNone ? kNone : base[rt] + 8.0f;
+        slot[ROWS * D + row] = base[rt];
         slot[ROWS * (D + 1) + row] = sum;
       }
     }

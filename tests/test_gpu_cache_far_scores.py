@@ -1,0 +1,59 @@
+"""Attention whose scores are far from zero.  Bounds as in test_gpu_cache.py."""
+import numpy as np
+import pytest
+import torch
+
+import post_weight_quantization_19_amd as P
+from test_gpu_cache import batch_of, check_attention, f64, keys_values, queries, up
+
+pytestmark = pytest.mark.gpu
+
+WIDE = 40000      # pages of a table whose entries are none: room for many tokens, so tiles of rows
+
+
+@pytest.mark.parametrize("power", [20, 28, 31, 50, 100])
+@pytest.mark.parametrize("sign", [1, -1])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("new,extra", [(1, 0), (1, WIDE), (100, WIDE)])
+def test_scores_far_from_zero(new, extra, dtype, sign, power):
+    """All keys alike: whatever the scores, every token that a row sees weighs the same,
+    and a single one gives its value.  (Scores are some 2^power; the sums of equal weights
+    are exact, so what is left is the values' part of the bound.)"""
+    rng = np.random.default_rng(power)
+    dim = 128
+    for n in (new, new + 50):
+        b = batch_of(rng, [n], [new], 32, extra=extra)
+        cache = P.new_cache(b[3], 1, dim, 8, 32)
+        _, v = keys_values(rng, (n, 1, dim), torch.float32)
+        key = torch.from_numpy(np.abs(rng.standard_normal(dim)).astype(np.float32)).cuda()
+        P.cache_write(key.expand(n, 1, dim), v, cache, up(np.array([0, n], np.int32))[0],
+                      *up(*b[1:3]))
+        records = cache["records"].cpu().numpy()
+        q = queries(rng, new, 4, dim, dtype).abs() * (sign * 2.0 ** power)
+        y = P.cached_attention(q, cache, *up(*b[:3]))
+        check_attention(y, q * 0, records, b[:3], dim, 8, 32)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("new,extra", [(2, 0), (2, WIDE), (90, WIDE)])
+def test_one_token_far_above_the_others(new, extra, dtype):
+    """A key whose score is 2^30 or more above all others takes all of the weight."""
+    rng = np.random.default_rng(new)
+    n, at, dim = 300, 40, 64
+    b = batch_of(rng, [n], [new], 32, extra=extra)
+    cache = P.new_cache(b[3], 1, dim, 8, 32)
+    k, v = keys_values(rng, (n, 1, dim), torch.float32)
+    k = -k.abs()
+    k[at] *= -1
+    P.cache_write(k, v, cache, up(np.array([0, n], np.int32))[0], *up(*b[1:3]))
+    _, held = P.cache_read(cache, up(np.array([0, n], np.int32))[0], *up(*b[1:3]), n,
+                           dtype=torch.float32)
+    for power in (30, 60):
+        q = queries(rng, new, 3, dim, dtype).abs() * 2.0 ** power
+        y = P.cached_attention(q, cache, *up(*b[:3]))
+        want = f64(held[at])[None]
+        err = np.abs(f64(y) - want)
+        step = f64(held).max() * 2 / 255
+        tol = (3 * 2.0 ** -12 if dtype == "bf16" else 2.0 ** -21) * np.abs(want)
+        tol = tol + 2.0 ** -25 * step * 255 + (2.0 ** -8 if dtype == "bf16" else 0) * np.abs(want)
+        assert np.all(err <= tol * 1.01)
