@@ -57,3 +57,28 @@ def test_one_token_far_above_the_others(new, extra, dtype):
         tol = (3 * 2.0 ** -12 if dtype == "bf16" else 2.0 ** -21) * np.abs(want)
         tol = tol + 2.0 ** -25 * step * 255 + (2.0 ** -8 if dtype == "bf16" else 0) * np.abs(want)
         assert np.all(err <= tol * 1.01)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("extra", [0, WIDE])
+def test_far_scores_behind_a_prefix(extra, dtype):
+    """The prefix's keys like the sequences' own: its tokens and theirs weigh the same."""
+    rng = np.random.default_rng(50)
+    n, own, before, dim, page = 40, 20, 70, 64, 32
+    starts, lengths, table, pages = batch_of(rng, [own] * n, [1] * n, page, spare=4)
+    free = np.array([p for p in range(pages) if p not in set(table.ravel())][:3], np.int32)
+    cache = P.new_cache(pages, 1, dim, 8, page)
+    key = torch.from_numpy(np.abs(rng.standard_normal(dim)).astype(np.float32)).cuda()
+    for tab, count in ((table, [own] * n), (free[None], [before])):
+        _, v = keys_values(rng, (sum(count), 1, dim), torch.float32)
+        P.cache_write(key.expand(sum(count), 1, dim), v, cache,
+                      *up(np.concatenate([[0], np.cumsum(count)]).astype(np.int32),
+                          np.array(count, np.int32), tab))
+    records = cache["records"].cpu().numpy()
+    wide = np.concatenate([free, np.full(extra, -1, np.int32)])
+    for power in (24, 27, 30, 33, 80):
+        q = queries(rng, n, 8, dim, dtype).abs() * 2.0 ** power
+        y = P.cached_attention(q, cache, *up(starts, lengths, table),
+                               prefix=tuple(up(wide, np.array([before], np.int32))))
+        check_attention(y, q * 0, records, (starts, lengths, table), dim, 8, page,
+                        prefix=(free, before))
