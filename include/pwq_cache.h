@@ -122,7 +122,8 @@ pwq_status pwq_cache_read(const pwq_cache* cache, const pwq_batch* batch, void* 
  *   ws     : pwq_cached_attention_workspace_size bytes, 256-byte aligned.
  * Keys multiply as their codes, exactly, and values too but where said.  Rows of a
  * sequence are taken 16 together, or 128 or 256 where there are many, and a power of
- * two scales those rows' queries so that the largest element fits float16:
+ * two scales a row's queries (128 or 256: those of all of these rows) so that the largest
+ * element fits float16:
  *   PWQ_BF16 : an element is exact where it is above 2^-30 of that largest, else
  *              off by 2^-38 of it.  A token's weight times its step is rounded to
  *              float16 once (2^-12).  Where rows are taken 128 or 256 together weight, step and

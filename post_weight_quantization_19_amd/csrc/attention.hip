@@ -6,9 +6,9 @@
 // query head of a token; the rows of one key head and sequence share its keys.
 //
 // Keys times queries: 16x16x32 float16 matrix products, 16 keys x 32 channels of
-// codes (exact: |c - z| <= 255) by 32 channels x 16 rows of q' (scaled so that the
-// largest of the rows taken together is in 2^13 .. 2^14; float32 queries in two
-// float16 parts).  The result has a lane for four keys of one row, which is where the
+// codes (exact: |c - z| <= 255) by 32 channels x 16 rows of q' (scaled so that a row's
+// largest is in 2^13 .. 2^14, in attend_tiles that of the rows taken together; float32
+// queries in two float16 parts).  The result has a lane for four keys of one row, which is where the
 // next product, values times weights, wants its weights: P never leaves the
 // registers.  Weights are held as 2^8 at the running maximum, up to 2^12 before it is
 // raised, so that sums are rescaled rarely.  A partial result is the maximum less 8, and the
@@ -131,6 +131,11 @@ __device__ __forceinline__ uint4 weight_part(float (&x)[8]) {
     x[a] -= (float)h[0], x[b] -= (float)h[1];
   }
   return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// Exponent field of the power of two that brings `top` to 2^13 .. 2^14.
+__device__ __forceinline__ int up_field(float top) {
+  return max(min(267 - (int)(__float_as_uint(top) >> 23), 253), 1);
 }
 
 struct __attribute__((packed, aligned(1))) any16 { uint32_t v[4]; };
@@ -401,8 +406,8 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void attend_rows(const RowsP
       mine = fmaxf(mine, __shfl_xor(mine, 16, 64));
       mine = fmaxf(mine, __shfl_xor(mine, 32, 64));
       const bool bad = !(mine <= __FLT_MAX__);
-      const float top = wave_max(bad ? 0.0f : mine);
-      const int field = max(min(267 - (int)(__float_as_uint(top) >> 23), 253), 1);
+      // (the row's own largest: its neighbours may be of any size)
+      const int field = up_field(bad ? 0.0f : mine);
       const float up = __uint_as_float((uint32_t)field << 23);
       f = __uint_as_float((uint32_t)(254 - field) << 23) * a.scale * 1.44269504088896340736f;
 #pragma unroll
@@ -771,7 +776,7 @@ __global__ __launch_bounds__(512, 1) void attend_tiles(const TilesArgs a) {
     top = tops[0];
 #pragma unroll
     for (int i = 1; i < WAVES; ++i) top = fmaxf(top, tops[i]);
-    const int field = max(min(267 - (int)(__float_as_uint(top) >> 23), 253), 1);
+    const int field = up_field(top);
     const float up = __uint_as_float((uint32_t)field << 23);
     f = __uint_as_float((uint32_t)(254 - field) << 23) * a.scale * 1.44269504088896340736f;
 #pragma unroll
