@@ -121,15 +121,16 @@ pwq_status pwq_cache_read(const pwq_cache* cache, const pwq_batch* batch, void* 
  *   scale  : 1e-30 .. 1e30.
  *   ws     : pwq_cached_attention_workspace_size bytes, 256-byte aligned.
  * Keys multiply as their codes, exactly, and values too but where said.  Rows of a
- * sequence are taken 16 together, or 128 or 256 where there are many, and a power of
- * two scales a row's queries (128 or 256: those of all of these rows) so that the largest
- * element fits float16:
- *   PWQ_BF16 : an element is exact where it is above 2^-30 of that largest, else
- *              off by 2^-38 of it.  A token's weight times its step is rounded to
+ * sequence are taken 16 together, or 128 or 256 where there are many.  A power of two
+ * scales a row's queries so that the largest element fits float16 (128 or 256: scales
+ * all of these rows' alike, where the largest of none but rows of zeros is more than 2^8 below
+ * another's):
+ *   PWQ_BF16 : an element is exact where it is above 2^-22 of the row's largest, else
+ *              off by 2^-30 of it.  A token's weight times its step is rounded to
  *              float16 once (2^-12).  Where rows are taken 128 or 256 together weight, step and
  *              step times code are each rounded (3 times 2^-12).
- *   PWQ_F32  : two float16 parts, for elements as for weights: within 2^-22, or 2^-38
- *              of the largest element.
+ *   PWQ_F32  : two float16 parts, for elements as for weights: within 2^-22, or 2^-30
+ *              of the row's largest element.
  * A weight is off by 2^-33 of the largest so far at least (2^-25 where scores pass
  * 2^25), and a step (128 or 256 together, PWQ_BF16) by 2^-30 of the largest of the
  * sequence's steps.  Sums, maxima and totals are float32, in a fixed order; how a

@@ -7,8 +7,8 @@
 //
 // Keys times queries: 16x16x32 float16 matrix products, 16 keys x 32 channels of
 // codes (exact: |c - z| <= 255) by 32 channels x 16 rows of q' (scaled so that a row's
-// largest is in 2^13 .. 2^14, in attend_tiles that of the rows taken together; float32
-// queries in two float16 parts).  The result has a lane for four keys of one row, which is where the
+// largest is in 2^13 .. 2^14, in attend_tiles the largest of rows taken together where all
+// are near it; float32 queries in two float16 parts).  The result has a lane for four keys of one row, which is where the
 // next product, values times weights, wants its weights: P never leaves the
 // registers.  Weights are held as 2^8 at the running maximum, up to 2^12 before it is
 // raised, so that sums are rescaled rarely.  A partial result is the maximum less 8, and the
@@ -699,7 +699,8 @@ __global__ __launch_bounds__(512, 1) void attend_tiles(const TilesArgs a) {
   // 8 kUnit, which times 255 has to stay in float16 where the steps are folded in).
   constexpr float kUnit = PARTS == 1 ? 32.0f : 1.0f;
   __shared__ Scan sc;
-  __shared__ float tops[WAVES];
+  __shared__ float tops[WAVES], lows[WAVES];
+  __shared__ float row_scale[ROWS];
   __shared__ u32x4_t frags[4][2 * J + N][64];    // [record % 4][keys (t, j), values n]
   // Of a record's tokens: keys' steps times f; zero points as -(1024 + z), a key's four times
   // twice, values' in the order of a fragment's tokens; values' steps over ref, float16 in
@@ -751,45 +752,57 @@ __global__ __launch_bounds__(512, 1) void attend_tiles(const TilesArgs a) {
   }
   int least = __builtin_amdgcn_readfirstlane(visible[0]);   // the first row sees least
   float f = 0.0f;
-  // (all rows of the workgroup scaled alike)
+  // All rows are scaled alike, by their largest, where none is more than 2^8 below it (rows of
+  // zeros aside): f goes into the keys' steps, for all.  Else each by its own, scores are brought
+  // back by row_scale, and f is of a size that neither they nor the steps leave float32:
+  // a row 2^40 below another would be zeros.  Records then go the way of those with hidden
+  // tokens, so that even rows pay nothing.
   auto scale_queries = [&]() __attribute__((always_inline)) {
-    float top = 0.0f;
-    bool bad[RT];
+    float top = 0.0f, low = __FLT_MAX__, mine[RT];
 #pragma unroll
     for (int rt = 0; rt < RT; ++rt) {
-      float mine = 0.0f;
+      mine[rt] = 0.0f;
 #pragma unroll
       for (int j = 0; j < J; ++j)
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-          mine = fmaxf(mine, fabsf(raw[rt][j][e]));
-          if (raw[rt][j][e] != raw[rt][j][e]) mine = __builtin_inff();
+          mine[rt] = fmaxf(mine[rt], fabsf(raw[rt][j][e]));
+          if (raw[rt][j][e] != raw[rt][j][e]) mine[rt] = __builtin_inff();
         }
-      mine = fmaxf(mine, __shfl_xor(mine, 16, 64));
-      mine = fmaxf(mine, __shfl_xor(mine, 32, 64));
-      bad[rt] = !(mine <= __FLT_MAX__);
-      if (!bad[rt]) top = fmaxf(top, mine);
+      mine[rt] = fmaxf(mine[rt], __shfl_xor(mine[rt], 16, 64));
+      mine[rt] = fmaxf(mine[rt], __shfl_xor(mine[rt], 32, 64));
+      if (mine[rt] > 0.0f && mine[rt] <= __FLT_MAX__) {
+        top = fmaxf(top, mine[rt]);
+        low = fminf(low, mine[rt]);
+      }
     }
     top = wave_max(top);
-    if (lane == 0) tops[wave] = top;
+    low = wave_min(low);
+    if (lane == 0) tops[wave] = top, lows[wave] = low;
     __syncthreads();
-    top = tops[0];
+    top = tops[0], low = lows[0];
 #pragma unroll
-    for (int i = 1; i < WAVES; ++i) top = fmaxf(top, tops[i]);
-    const int field = up_field(top);
-    const float up = __uint_as_float((uint32_t)field << 23);
+    for (int i = 1; i < WAVES; ++i) top = fmaxf(top, tops[i]), low = fminf(low, lows[i]);
+    const bool uneven = __builtin_amdgcn_readfirstlane(low < top * 0x1p-8f);
+    const int field = uneven ? min(up_field(top) + 96, 127) : up_field(top);
+    if (uneven) least = kAlways;
     f = __uint_as_float((uint32_t)(254 - field) << 23) * a.scale * 1.44269504088896340736f;
 #pragma unroll
-    for (int rt = 0; rt < RT; ++rt)
+    for (int rt = 0; rt < RT; ++rt) {
+      const bool bad = !(mine[rt] <= __FLT_MAX__);
+      const int own = uneven ? up_field(bad ? 0.0f : mine[rt]) : field;
+      const float up = __uint_as_float((uint32_t)own << 23);
+      if (g == 0) row_scale[(rt * WAVES + wave) * 16 + col] = ldexpf(1.0f, field - own);
 #pragma unroll
       for (int j = 0; j < J; ++j)
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-          const float v = bad[rt] ? __builtin_nanf("") : raw[rt][j][e] * up;
+          const float v = bad ? __builtin_nanf("") : raw[rt][j][e] * up;
           const _Float16 hi = (_Float16)v;
           qf[rt][0][j][e] = hi;
           if constexpr (PARTS == 2) qf[rt][1][j][e] = (_Float16)(v - (float)hi);
         }
+    }
   };
 
   // ---- staging
@@ -990,7 +1003,12 @@ __global__ __launch_bounds__(512, 1) void attend_tiles(const TilesArgs a) {
     if (masked)
 #pragma unroll
       for (int rt = 0; rt < RT; ++rt) {
-        if (least == kAlways) far_exps(rt);
+        if (least == kAlways) {
+          const float scale = row_scale[(rt * WAVES + wave) * 16 + col];
+#pragma unroll
+          for (int t = 0; t < 2; ++t) score[rt][t] *= scale;
+          far_exps(rt);
+        }
         hide(rt, p0, n);
       }
     float top = 0.0f;

@@ -5,9 +5,11 @@ import pytest
 import torch
 
 import post_weight_quantization_19_amd as P
-from test_gpu_cache import batch_of, check_attention, filled, queries, up
+from test_gpu_cache import DT, batch_of, check_attention, filled, keys_values, queries, up
 
 pytestmark = pytest.mark.gpu
+
+WIDE = 40000      # pages of a table whose entries are none: room for many tokens, so tiles of rows
 
 
 @pytest.mark.parametrize("power", [40, 110])
@@ -39,3 +41,61 @@ def test_a_query_far_above_those_of_other_sequences(dtype):
     y = P.cached_attention(q, cache, *up(starts, lengths, table),
                            prefix=tuple(up(free, np.array([before], np.int32))))
     check_attention(y, q, records, (starts, lengths, table), dim, 8, page, prefix=(free, before))
+
+
+@pytest.mark.parametrize("power", [7, 9, 40, 110])
+@pytest.mark.parametrize("heads,kv_heads,dim,bits,dtype", [
+    (4, 1, 128, 8, "bf16"), (14, 2, 64, 4, "f32"), (6, 2, 256, 8, "bf16"), (3, 1, 128, 4, "f32"),
+    (2, 1, 64, 8, "bf16")])
+def test_a_query_far_above_those_of_its_tile(heads, kv_heads, dim, bits, dtype, power):
+    """The same in tiles of many rows, with rows of zeros and a NaN among them."""
+    rng = np.random.default_rng(dim + power)
+    lens, new, page = [300, 140], [150, 100], 32
+    b = batch_of(rng, lens, new, page, extra=WIDE)
+    cache, records = filled(rng, b[3], kv_heads, dim, bits, page)
+    q = queries(rng, 250, heads, dim, dtype)
+    q[2, heads - 1] *= 2.0 ** power
+    q[200, 0] *= 2.0 ** power
+    q[5] = 0
+    args = up(*b[:3])
+    y = P.cached_attention(q, cache, *args)
+    check_attention(y, q, records, b[:3], dim, bits, page)
+    q[9, 0, 3] = float("nan")
+    z = P.cached_attention(q, cache, *args)
+    assert torch.isnan(z[9, 0]).all()
+    z[9, 0] = y[9, 0]
+    assert torch.equal(y, z)
+
+
+@pytest.mark.parametrize("dtype,dim", [("bf16", 128), ("f32", 64)])
+def test_a_query_far_above_others_behind_a_prefix_in_tiles(dtype, dim):
+    rng = np.random.default_rng(32)
+    n, page, before = 40, 32, 200
+    starts, lengths, table, pages = batch_of(rng, [9] * n, [1] * n, page, spare=9)
+    free = np.array([p for p in range(pages) if p not in set(table.ravel())][:7], np.int32)
+    wide = np.concatenate([free, np.full(WIDE, -1, np.int32)])
+    cache, records = filled(rng, pages, 1, dim, 8, page)
+    q = queries(rng, n, 8, dim, dtype)
+    q[30] *= 2.0 ** 50
+    y = P.cached_attention(q, cache, *up(starts, lengths, table),
+                           prefix=tuple(up(wide, np.array([before], np.int32))))
+    check_attention(y, q, records, (starts, lengths, table), dim, 8, page, prefix=(free, before))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_queries_of_all_sizes_in_a_tile(dtype):
+    """Rows from 2^-100 to 2^44 and from 2^-60 to 2^120, with keys for which some of the
+    scores are of ordinary size."""
+    rng = np.random.default_rng(33)
+    n, page, dim = 130, 32, 64
+    b = batch_of(rng, [n], [n], page, extra=WIDE)
+    for lo, hi, size in ((-100, 44, 2.0 ** 70), (-60, 120, 2.0 ** -100)):
+        cache = P.new_cache(b[3], 1, dim, 8, page)
+        k, v = keys_values(rng, (n, 1, dim), torch.float32)
+        P.cache_write(k * size, v, cache, *up(*b[:3]))
+        records = cache["records"].cpu().numpy()
+        q = queries(rng, n, 2, dim, "f32")
+        q *= torch.from_numpy(np.exp2(np.linspace(lo, hi, n))).float().cuda()[:, None, None]
+        q = q.to(DT[dtype])
+        y = P.cached_attention(q, cache, *up(*b[:3]))
+        check_attention(y, q, records, b[:3], dim, 8, page)
