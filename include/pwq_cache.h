@@ -133,7 +133,8 @@ pwq_status pwq_cache_read(const pwq_cache* cache, const pwq_batch* batch, void* 
  *              of the row's largest element.
  * A weight is off by 2^-33 of the largest so far at least (2^-25 where scores pass
  * 2^25), and a step (128 or 256 together, PWQ_BF16) by 2^-30 of the largest of the
- * sequence's steps.  Sums, maxima and totals are float32, in a fixed order; how a
+ * sequence's steps: of the tokens that the row sees, and where 128 or 256 are taken together
+ * also of up to 31 behind them, to the next multiple of 32.  Sums, maxima and totals are float32, in a fixed order; how a
  * sequence is split, and so the last bits of its rows, depends on the sizes and starts
  * and lengths of the whole batch.  A row of q with an infinity or NaN, or with a token
  * it sees that reads as NaN, gives NaN; other rows are unaffected.  Scores, and steps

@@ -540,21 +540,18 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void attend_rows(const RowsP
           sv[i] = word_step(vx[i / 4][i % 4]);
         }
         if (masked) {
-          // tokens that are not there, or whom some rows do not see: those that read as
-          // NaN must not meet a weight of 0
+          // tokens that are not there, or that the row does not see: their steps do not count
+          // for its unit, and those that read as NaN must not meet a weight of 0
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
-            if (i / 4 * 16 + i % 4 + 4 * g >= n) sv[i] = 0.0f;
-            if (sv[i] != sv[i]) {
-              if (i / 4 * 16 + i % 4 < seen) e[i] = sv[i];
-              sv[i] = 0.0f;
-            }
+            if (i / 4 * 16 + i % 4 >= seen) sv[i] = 0.0f;
+            if (sv[i] != sv[i]) e[i] = sv[i], sv[i] = 0.0f;
           }
         }
 #pragma unroll
         for (int i = 0; i < 8; ++i) most_step = fmaxf(most_step, sv[i]);
         if (__builtin_expect(__any(top > 4096.0f || most_step > ref * 8.0f), 0)) {
-          // the maximum is raised once a score is 4 above it, ref where a step is 8 of it
+          // the maximum is raised once a score is 4 above it, a row's ref where a step is 8 of it
           float m = kNone;
 #pragma unroll
           for (int i = 0; i < 8; ++i)
@@ -566,7 +563,8 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void attend_rows(const RowsP
           l *= factor;
           base = next;
           if (__any(is_far(base))) least = kAlways;
-          const float largest = wave_max(most_step);
+          float largest = fmaxf(most_step, __shfl_xor(most_step, 16, 64));
+          largest = fmaxf(largest, __shfl_xor(largest, 32, 64));
           if (largest > ref * 8.0f) {
             const float to = __uint_as_float(
                 __float_as_uint(fminf(fmaxf(largest, 0x1p-100f), 0x1p100f)) & 0x7f800000u);

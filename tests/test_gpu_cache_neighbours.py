@@ -4,8 +4,9 @@ import numpy as np
 import pytest
 import torch
 
+import oracle.cache_oracle as C
 import post_weight_quantization_19_amd as P
-from test_gpu_cache import DT, batch_of, check_attention, filled, keys_values, queries, up
+from test_gpu_cache import DT, batch_of, check_attention, f64, filled, keys_values, queries, up
 
 pytestmark = pytest.mark.gpu
 
@@ -99,3 +100,44 @@ def test_queries_of_all_sizes_in_a_tile(dtype):
         q = q.to(DT[dtype])
         y = P.cached_attention(q, cache, *up(*b[:3]))
         check_attention(y, q, records, b[:3], dim, 8, page)
+
+
+def check_by_what_is_seen(y, q, records, b, dim, bits, page):
+    """check_attention of one sequence, where a row's bound counts the steps of the values
+    that it sees (a step of 2^-33 of the largest so far, times a code of at most 255)."""
+    starts, lens, table = b
+    new, group, bf16 = starts[1], q.shape[1] // records.shape[1], q.dtype == torch.bfloat16
+    k, v, there = C.stored(records, table[0], lens[0], dim, bits, page)
+    n, qn, got = lens[0], f64(q), f64(y)
+    seen = there & (np.arange(n) <= (n - new + np.arange(new))[:, None])
+    for h in range(q.shape[1]):
+        vh = v[h // group]
+        want, size, score = C.attention(qn[:new, h], k[h // group], vh, dim ** -0.5, seen)
+        steps = (vh.max(-1).clip(0) - vh.min(-1).clip(max=0)) / (2 ** bits - 1) * 1.02
+        step = np.where(seen, steps, 0).max(1)[:, None]
+        off = score * ((dim + 4 + 1.45) * 2.0 ** -24 + (0 if bf16 else 2.0 ** -22))
+        rel = 2 * off + 2.0 ** -21 + (3 * 2.0 ** -12 if bf16 else 2.0 ** -22)
+        rel = rel + (n / 16 + 64) * 2.0 ** -24
+        tol = rel[:, None] * (size + np.abs(want)) + (n + 9) * 2.0 ** -33 * step * 255
+        tol = tol * 1.01 + (2.0 ** -8 * 1.01 if bf16 else 2.0 ** -23) * np.abs(want)
+        err = np.abs(got[:new, h] - want)
+        assert np.all(err <= tol), (h, float((err / np.maximum(tol, 1e-300)).max()))
+
+
+@pytest.mark.parametrize("power", [20, 34, 60])
+@pytest.mark.parametrize("heads,kv_heads,dim,bits,dtype", [
+    (4, 1, 128, 8, "bf16"), (2, 2, 64, 4, "f32"), (3, 1, 256, 8, "f32"), (8, 8, 64, 8, "bf16")])
+def test_values_of_tokens_that_a_row_does_not_see(heads, kv_heads, dim, bits, dtype, power):
+    """The last two of eight new tokens have values 2^power above the others': the rows
+    before them are as exact as without."""
+    rng = np.random.default_rng(dim + power)
+    for n in (20, 90, 1500):
+        b = batch_of(rng, [n], [8], 32)
+        cache = P.new_cache(b[3], kv_heads, dim, bits, 32)
+        k, v = keys_values(rng, (n, kv_heads, dim), torch.float32)
+        v[-2:] *= 2.0 ** power
+        P.cache_write(k, v, cache, up(np.array([0, n], np.int32))[0], *up(*b[1:3]))
+        records = cache["records"].cpu().numpy()
+        q = queries(rng, 8, heads, dim, dtype)
+        y = P.cached_attention(q, cache, *up(*b[:3]))
+        check_by_what_is_seen(y, q, records, b[:3], dim, bits, 32)
