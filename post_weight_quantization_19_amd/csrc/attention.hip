@@ -567,7 +567,7 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void attend_rows(const RowsP
           largest = fmaxf(largest, __shfl_xor(largest, 32, 64));
           if (largest > ref * 8.0f) {
             const float to = __uint_as_float(
-                __float_as_uint(fminf(fmaxf(largest, 0x1p-100f), 0x1p100f)) & 0x7f800000u);
+                __float_as_uint(fminf(fmaxf(largest, 0x1p-126f), 0x1p100f)) & 0x7f800000u);
             factor *= ref / to;
             ref = to, unit = 1.0f / to;
           }
@@ -877,7 +877,7 @@ __global__ __launch_bounds__(512, 1) void attend_tiles(const TilesArgs a) {
     const float sv = lane >= 32 && there && step == step ? step : 0.0f;
     if (__builtin_expect(__any(sv > staged_ref * 8.0f), 0)) {
       staged_ref = __uint_as_float(
-          __float_as_uint(fminf(fmaxf(wave_max(sv), 0x1p-100f), 0x1p100f)) & 0x7f800000u);
+          __float_as_uint(fminf(fmaxf(wave_max(sv), 0x1p-126f * kUnit), 0x1p100f)) & 0x7f800000u);
       unit = kUnit / staged_ref;
     }
     const uint32_t zero = 0xe400u | (uint32_t)word_zero(st.word);
@@ -1219,7 +1219,7 @@ __global__ __launch_bounds__(512, 1) void attend_tiles(const TilesArgs a) {
     }
     if (row >= rows) continue;
     if (a.slots == nullptr) {
-      const float unit = sum == 0.0f ? 0.0f : back / sum;
+      const float part = sum == 0.0f ? 0.0f : 1.0f / sum;
       const int r = first + row;
       const int64_t to = (int64_t)(q.r0 + r / a.group) * a.out.ts +
                          (int64_t)(h * a.group + r % a.group) * a.out.hs + 4 * g;
@@ -1227,7 +1227,7 @@ __global__ __launch_bounds__(512, 1) void attend_tiles(const TilesArgs a) {
       for (int n = 0; n < N; ++n) {
         float y[4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) y[i] = sum == 0.0f ? 0.0f : o[rt][n][i] * unit;
+        for (int i = 0; i < 4; ++i) y[i] = sum == 0.0f ? 0.0f : o[rt][n][i] * part * back;
         store_row4((T*)a.out.p + to + 16 * n, y);
       }
     } else {
