@@ -698,7 +698,7 @@ __global__ __launch_bounds__(512, 1) void attend_tiles(const TilesArgs a) {
   constexpr float kUnit = PARTS == 1 ? 32.0f : 1.0f;
   __shared__ Scan sc;
   __shared__ float tops[WAVES], lows[WAVES];
-  __shared__ float row_scale[ROWS];
+  __shared__ float row_scale[ROWS], row_ref[ROWS];   // (ref of a row's sums: of what it sees)
   __shared__ u32x4_t frags[4][2 * J + N][64];    // [record % 4][keys (t, j), values n]
   // Of a record's tokens: keys' steps times f; zero points as -(1024 + z), a key's four times
   // twice, values' in the order of a fragment's tokens; values' steps over ref, float16 in
@@ -790,7 +790,8 @@ __global__ __launch_bounds__(512, 1) void attend_tiles(const TilesArgs a) {
       const bool bad = !(mine[rt] <= __FLT_MAX__);
       const int own = uneven ? up_field(bad ? 0.0f : mine[rt]) : field;
       const float up = __uint_as_float((uint32_t)own << 23);
-      if (g == 0) row_scale[(rt * WAVES + wave) * 16 + col] = ldexpf(1.0f, field - own);
+      row_scale[(rt * WAVES + wave) * 16 + col] = ldexpf(1.0f, field - own);
+      row_ref[(rt * WAVES + wave) * 16 + col] = 0.0f;
 #pragma unroll
       for (int j = 0; j < J; ++j)
 #pragma unroll
@@ -1154,19 +1155,23 @@ __global__ __launch_bounds__(512, 1) void attend_tiles(const TilesArgs a) {
     turn(yes);
     fetch(3);
     if (wave >= 4) turn(no);
-    auto rescale = [&]() __attribute__((always_inline)) {
-      if (__builtin_expect(now.x != ref, 0)) {   // larger values: the sums in their unit
+    // Larger values in record i: the sums in their unit, but for rows that are done.
+    auto rescale = [&](int i) __attribute__((always_inline)) {
+      if (__builtin_expect(now.x != ref, 0)) {
         const float factor = ref / now.x;
 #pragma unroll
         for (int rt = 0; rt < RT; ++rt)
+          if (visible[rt] > 32 * i) {
+            row_ref[(rt * WAVES + wave) * 16 + col] = now.x;
 #pragma unroll
-          for (int n = 0; n < N; ++n) o[rt][n] *= factor;
+            for (int n = 0; n < N; ++n) o[rt][n] *= factor;
+          }
         ref = now.x;
       }
     };
     auto one = [&](int i, auto u) __attribute__((always_inline)) {
       constexpr int U = decltype(u)::value;             // (i - i0) % 4
-      rescale();
+      rescale(i - 1);
       fetch_zeros((U + 2) & 3);
       Words& wn = wq[(U + 3) & 1];
       const Words old = wn;
@@ -1202,17 +1207,17 @@ __global__ __launch_bounds__(512, 1) void attend_tiles(const TilesArgs a) {
     if (wave < 4) turn(no);
     {
       const int last = (i1 - 1 - i0) & 3;
-      rescale();
+      rescale(i1 - 1);
       multiply(last, 0, no, [](auto) {});
     }
   }
   if (!busy) return;
-  const float back = ref / kUnit;
   float* slot = a.slots + (((int64_t)h * a.items + item) * a.splits + split) * (ROWS * (D + 2));
 #pragma unroll
   for (int rt = 0; rt < RT; ++rt) {
     const int row = (rt * WAVES + wave) * 16 + col;
     float sum = l[rt][0];
+    const float back = i0 < i1 ? row_ref[row] / kUnit : 0.0f;
     if constexpr (PARTS == 2) {
       sum += __shfl_xor(sum, 16, 64);
       sum += __shfl_xor(sum, 32, 64);

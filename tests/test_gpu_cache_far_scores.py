@@ -82,3 +82,21 @@ def test_far_scores_behind_a_prefix(extra, dtype):
                                prefix=tuple(up(wide, np.array([before], np.int32))))
         check_attention(y, q * 0, records, (starts, lengths, table), dim, 8, page,
                         prefix=(free, before))
+
+
+@pytest.mark.parametrize("heads,dim,dtype", [(256, 64, "f32"), (256, 128, "bf16")])
+def test_far_scores_over_many_records(heads, dim, dtype):
+    """So many key heads, and rows of each, that a tile of rows takes all of its tokens."""
+    rng = np.random.default_rng(dim)
+    n, new = 450, 250
+    b = batch_of(rng, [n], [new], 32)
+    cache = P.new_cache(b[3], heads, dim, 8, 32)
+    _, v = keys_values(rng, (n, heads, dim), torch.float32)
+    key = torch.from_numpy(np.abs(rng.standard_normal(dim)).astype(np.float32)).cuda()
+    P.cache_write(key.expand(n, heads, dim), v, cache, up(np.array([0, n], np.int32))[0],
+                  *up(*b[1:3]))
+    records = cache["records"][:, -2:].cpu().numpy()
+    for power in (24, 27, 31, 90):
+        q = queries(rng, new, heads, dim, dtype).abs() * 2.0 ** power
+        y = P.cached_attention(q, cache, *up(*b[:3]))[:, -2:]
+        check_attention(y, q[:, -2:] * 0, records, b[:3], dim, 8, 32)

@@ -141,3 +141,48 @@ def test_values_of_tokens_that_a_row_does_not_see(heads, kv_heads, dim, bits, dt
         q = queries(rng, 8, heads, dim, dtype)
         y = P.cached_attention(q, cache, *up(*b[:3]))
         check_by_what_is_seen(y, q, records, b[:3], dim, bits, 32)
+
+
+# So many key heads, and rows of each, that a tile of rows takes all of its tokens.
+MANY = [(256, 64, 8, "bf16"), (256, 64, 4, "f32"), (256, 128, 8, "bf16"), (300, 128, 4, "f32")]
+
+
+@pytest.mark.parametrize("power", [34, 90, 170])
+@pytest.mark.parametrize("heads,dim,bits,dtype", MANY)
+def test_values_behind_a_row_in_tiles(heads, dim, bits, dtype, power):
+    """Tokens from a multiple of 32 on have values 2^power above the others': rows of the
+    same tile that end before are as exact as without."""
+    rng = np.random.default_rng(dim + power)
+    n, new = 450, 250
+    b = batch_of(rng, [n], [new], 32)
+    cache = P.new_cache(b[3], heads, dim, bits, 32)
+    k, v = keys_values(rng, (n, heads, dim), torch.float32)
+    v[:352] *= 2.0 ** -min(power, 100)
+    v[352:] *= 2.0 ** (power - min(power, 100))
+    P.cache_write(k, v, cache, up(np.array([0, n], np.int32))[0], *up(*b[1:3]))
+    q = queries(rng, new, heads, dim, dtype)
+    y = P.cached_attention(q, cache, *up(*b[:3]))
+    rows = 352 - (n - new)                     # those that end before
+    cut = (np.array([0, rows], np.int32), [352], b[2])
+    for some in (slice(0, 3), slice(heads - 2, heads)):
+        records = cache["records"][:, some].cpu().numpy()
+        check_by_what_is_seen(y[:rows, some], q[:rows, some], records, cut, dim, bits, 32)
+        check_attention(y[:, some], q[:, some], records, b[:3], dim, bits, 32)
+
+
+@pytest.mark.parametrize("power", [9, 40, 110])
+@pytest.mark.parametrize("heads,dim,bits,dtype", MANY)
+def test_queries_far_above_others_over_many_records(heads, dim, bits, dtype, power):
+    rng = np.random.default_rng(dim + power)
+    n, new = 450, 250
+    b = batch_of(rng, [n], [new], 32)
+    cache = P.new_cache(b[3], heads, dim, bits, 32)
+    k, v = keys_values(rng, (n, heads, dim), torch.float32)
+    P.cache_write(k, v, cache, up(np.array([0, n], np.int32))[0], *up(*b[1:3]))
+    q = queries(rng, new, heads, dim, dtype)
+    q[[7, 130]] *= 2.0 ** power
+    q[200] = 0
+    y = P.cached_attention(q, cache, *up(*b[:3]))
+    for some in (slice(0, 2), slice(heads - 1, heads)):
+        records = cache["records"][:, some].cpu().numpy()
+        check_attention(y[:, some], q[:, some], records, b[:3], dim, bits, 32)
