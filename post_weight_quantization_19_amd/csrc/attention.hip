@@ -11,8 +11,8 @@
 // are near it; float32 queries in two float16 parts).  The result has a lane for four keys of one row, which is where the
 // next product, values times weights, wants its weights: P never leaves the
 // registers.  Weights are held as 2^8 at the running maximum, up to 2^12 before it is
-// raised, so that sums are rescaled rarely.  A partial result is the maximum less 8, and the
-// total and the sums of weights of 1 there.
+// raised, so that sums are rescaled rarely.  A partial result is the maximum less 8, and a
+// 256th of the total and of the sums (weights of 16 at most, so that many add up in float32).
 //
 // Two kernels, for few rows of a sequence and for many, and one that joins what the
 // workers of a row have found.  attend_rows is bound by memory where the cache is long,
@@ -69,16 +69,16 @@ __device__ __forceinline__ bool is_far(float base) {
   return fabsf(base) >= kFar && base != kNone;
 }
 __device__ __forceinline__ float weight_of(float acc, float sk, float base) {
-  float t = acc * sk;
-  pin(t);                              // (not an fma after all)
+#pragma clang fp contract(off)
+  const float t = acc * sk;            // (not an fma after all)
   return __builtin_amdgcn_exp2f(t - base);
 }
 __device__ __forceinline__ float base_of(float most) {
   return fabsf(most) < 4.0f * kFar ? most - 8.0f : most;
 }
-// In place of the tokens that all rows see: every record is looked at as one with hidden
-// tokens, where weights are taken by weight_of.  (Another branch for each record, or
-// more instructions in these, made prompts 1 to 2% slower; so it is up to 1%.)
+// In place of the number of tokens that all rows see: every record is looked at as one with
+// hidden tokens, where weights are taken by weight_of.  (Another branch for each record makes
+// a prompt chunk 2% slower; so it is the same, 4 short float32 prompts in 4 bits 4%.)
 constexpr int kAlways = INT32_MIN;
 
 __device__ __forceinline__ f16x2_t as_half2(uint32_t w) { return __builtin_bit_cast(f16x2_t, w); }
@@ -629,7 +629,7 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void attend_rows(const RowsP
     l += __shfl_xor(l, 16, 64);
     l += __shfl_xor(l, 32, 64);
     __syncthreads();
-    if (g == 0) sm[wave][col] = base, sl[wave][col] = l;
+    if (g == 0) sm[wave][col] = base, sl[wave][col] = l * (1.0f / 256.0f);
     __syncthreads();
     float all = kNone, sum = 0.0f;
 #pragma unroll
@@ -638,11 +638,12 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void attend_rows(const RowsP
     for (int i = 0; i < 4; ++i)
       sum += sm[i][col] == kNone ? sl[i][col] : sl[i][col] * exp2f(sm[i][col] - all);
     // the whole result's weights are divided by here
+    const float back = ref * (1.0f / 256.0f);
     const float part = (base == kNone ? 1.0f : exp2f(base - all)) *
                        (whole ? (sum == 0.0f ? 0.0f : 1.0f / sum) : 1.0f);
 #pragma unroll
     for (int n = 0; n < N; ++n)
-      *(f32x4_t*)&so[wave][col][16 * n + 4 * g] = o[n] * part * ref;
+      *(f32x4_t*)&so[wave][col][16 * n + 4 * g] = o[n] * part * back;
     __syncthreads();
     float* slot = a.slots + ((int64_t)h * (a.workers + a.items) + w + item) * kSlot<D>;
     for (int i = threadIdx.x; i < rows * (D / 4); i += 256) {
@@ -1217,11 +1218,12 @@ __global__ __launch_bounds__(512, 1) void attend_tiles(const TilesArgs a) {
   for (int rt = 0; rt < RT; ++rt) {
     const int row = (rt * WAVES + wave) * 16 + col;
     float sum = l[rt][0];
-    const float back = i0 < i1 ? row_ref[row] / kUnit : 0.0f;
+    const float back = i0 < i1 ? row_ref[row] / (kUnit * 256.0f) : 0.0f;
     if constexpr (PARTS == 2) {
       sum += __shfl_xor(sum, 16, 64);
       sum += __shfl_xor(sum, 32, 64);
     }
+    sum *= 1.0f / 256.0f;
     if (row >= rows) continue;
     if (a.slots == nullptr) {
       const float part = sum == 0.0f ? 0.0f : 1.0f / sum;

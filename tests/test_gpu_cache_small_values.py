@@ -45,3 +45,22 @@ def test_values_that_step_up_to_the_largest(new, extra, dtype):
     q = queries(rng, new, 4, dim, dtype)
     y = P.cached_attention(q, cache, *up(*b[:3]))
     check_attention(y, q, records, b[:3], dim, 8, page)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("new,extra", [(2, 0), (2, WIDE), (90, 2), (90, WIDE)])
+def test_values_near_the_largest(new, extra, dtype):
+    """Steps just below 2^84, equal weights: sums of 160 or 3000 tokens stay in float32."""
+    rng = np.random.default_rng(new)
+    page, dim = 32, 64
+    for n in (160, 3000):
+        b = batch_of(rng, [n], [new], page, extra=extra)
+        cache = P.new_cache(b[3], 1, dim, 8, page)
+        k, v = keys_values(rng, (n, 1, dim), torch.float32)
+        v = v.clamp(-8, 8) * (2.0 ** 84 * 255 / 16.2)
+        P.cache_write(k, v, cache, up(np.array([0, n], np.int32))[0], *up(*b[1:3]))
+        records = cache["records"].cpu().numpy()
+        for size in (0.0, 1.5):
+            q = queries(rng, new, 4, dim, dtype, size)
+            y = P.cached_attention(q, cache, *up(*b[:3]))
+            check_attention(y, q, records, b[:3], dim, 8, page)
