@@ -29,3 +29,183 @@ def test_outputs_between_the_heads_of_inputs():
         kv = torch.full(shape, 7.0, device="cuda")
         P.cache_read(cache, *args, 29, out=(pick(kv, 0), pick(kv, 1)))
         assert torch.equal(pick(kv, 0), k) and torch.equal(pick(kv, 1), v)
+
+
+def test_blocks_of_hundreds_of_sequences():
+    """More than 256 sequences in a batch so large (most rows of no sequence) that blocks of
+    32 tokens are written and read whole: their places are found 256 sequences at a time."""
+    rng = np.random.default_rng(41)
+    n, page, heads, dim, bits = 700, 32, 2, 64, 8
+    new = rng.integers(0, 80, n)
+    new[[255, 256, 511, 512]] = 33, 1, 0, 64
+    lens = new + rng.integers(0, 40, n)
+    starts, lengths, table, pages = batch_of(rng, list(lens), list(new), page, before=5)
+    used = slice(5, 5 + int(new.sum()))
+    rows = used.stop + max(32 * n, 3 * 2 ** 19 // (heads * dim))
+    k, v = keys_values(rng, (rows, heads, dim), torch.bfloat16)
+    cache, before = filled(rng, pages, heads, dim, bits, page)
+    b = up(starts, lengths, table)
+    P.cache_write(k, v, cache, *b)
+    want = C.unpack(before, dim, bits)
+    s = np.repeat(np.arange(n), new)
+    p = np.arange(len(s)) - np.repeat(starts[1:] - 5, new) + np.repeat(lens, new)
+    at = (table[s, p // page], slice(None), p % page // 32)
+    for of, x in enumerate((k, v)):
+        vals = C.quantize(x[used].float().cpu().numpy(), bits)
+        for dst, src in zip(want, vals):
+            dst[at[0], :, at[2], of, p % 32] = src
+    for got, exp in zip(C.unpack(cache["records"].cpu().numpy(), dim, bits), want):
+        assert np.array_equal(got, exp)
+    out = [torch.full((rows, heads, dim), 7.0, device="cuda") for _ in range(2)]
+    P.cache_read(cache, *b, rows, out=tuple(out))
+    for got, x in zip(out, (k, v)):
+        vals = C.values(*C.quantize(x[used].float().cpu().numpy(), bits))
+        assert np.array_equal(f64(got[used]), vals)
+        assert (got[:5] == 7).all() and (got[used.stop:] == 7).all()
+
+
+@pytest.mark.parametrize("dtype,bits,extra", [("bf16", 8, 0), ("f32", 4, 0), ("bf16", 4, 30)])
+def test_one_long_sequence_among_short_ones(dtype, bits, extra):
+    """A row of more parts (390) than its waves join at a time (256), among rows of one."""
+    rng = np.random.default_rng(42)
+    lens = [1] * 7 + [100000] + [1] * 8
+    b = batch_of(rng, lens, [1] * 16, 64, extra=extra)
+    cache, records = filled(rng, b[3], 1, 64, bits, 64)
+    for size in (1.5, 0.0):
+        q = queries(rng, 16, 2, 64, dtype, size)
+        y = P.cached_attention(q, cache, *up(*b[:3]))
+        check_attention(y, q, records, b[:3], 64, bits, 64)
+
+
+@pytest.mark.parametrize("dtype,dim", [("bf16", 128), ("f32", 64), ("bf16", 256)])
+@pytest.mark.parametrize("extra", [0, 40000])
+def test_all_tokens_of_many_rows(extra, dtype, dim):
+    """Not causal, in tiles of rows, without a prefix and with one."""
+    rng = np.random.default_rng(43)
+    lens, new, page = [400, 90, 0, 300], [300, 90, 5, 1], 32
+    b = batch_of(rng, lens, new, page, spare=8, extra=extra)
+    free = np.array([p for p in range(b[3]) if p not in set(b[2].ravel())][:4], np.int32)
+    cache, records = filled(rng, b[3], 2, dim, 8, page)
+    q = queries(rng, sum(new), 8, dim, dtype)
+    y = P.cached_attention(q, cache, *up(*b[:3]), causal=False)
+    check_attention(y, q, records, b[:3], dim, 8, page, causal=False)
+    y = P.cached_attention(q, cache, *up(*b[:3]), causal=False,
+                           prefix=tuple(up(free, np.array([70], np.int32))))
+    check_attention(y, q, records, b[:3], dim, 8, page, causal=False, prefix=(free, 70))
+
+
+@pytest.mark.parametrize("page", [512, 1024, 2048, 4096])
+@pytest.mark.parametrize("dtype,bits", [("bf16", 4), ("f32", 8)])
+def test_large_pages(page, dtype, bits):
+    rng = np.random.default_rng(page)
+    lens, new = [5000, 700, 4097, 33], [40, 700, 1, 33]
+    b = batch_of(rng, lens, new, page)
+    cache, _ = filled(rng, b[3], 2, 64, bits, page)
+    args = up(*b[:3])
+    k, v = keys_values(rng, (sum(new), 2, 64), DT[dtype])
+    P.cache_write(k, v, cache, *args)
+    got = P.cache_read(cache, *args, sum(new), dtype=torch.float32)
+    for y, x in zip(got, (k, v)):
+        assert np.array_equal(f64(y), C.values(*C.quantize(x.float().cpu().numpy(), bits)))
+    records = cache["records"].cpu().numpy()
+    q = queries(rng, sum(new), 4, 64, dtype)
+    y = P.cached_attention(q, cache, *args)
+    check_attention(y, q, records, b[:3], 64, bits, page)
+
+
+@pytest.mark.parametrize("lens,new", [([300, 20], [1, 2]), ([1500, 3], [1, 3]),
+                                      ([450, 60], [250, 60])])
+def test_more_key_heads_than_workers(lens, new):
+    """600 key heads: one worker each, one split, or a workgroup each."""
+    rng = np.random.default_rng(44)
+    b = batch_of(rng, lens, new, 32)
+    cache = P.new_cache(b[3], 600, 64, 4, 32)
+    full = up(np.concatenate([[0], np.cumsum(lens)]).astype(np.int32))[0]
+    k, v = keys_values(rng, (sum(lens), 600, 64), torch.bfloat16)
+    P.cache_write(k, v, cache, full, *up(*b[1:3]))
+    q = queries(rng, sum(new), 1200, 64, "bf16")
+    y = P.cached_attention(q, cache, *up(*b[:3]))
+    for h in (0, 299, 511, 512, 599):
+        records = cache["records"][:, h:h + 1].cpu().numpy()
+        check_attention(y[:, 2 * h:2 * h + 2], q[:, 2 * h:2 * h + 2], records, b[:3], 64, 4, 32)
+
+
+@pytest.mark.parametrize("dtype,new,extra", [("bf16", 1, 0), ("f32", 3, 0), ("bf16", 600, 0),
+                                             ("f32", 200, 100)])
+def test_long_sequences(dtype, new, extra):
+    """70001 tokens: hundreds of tiles, or thousands of records, of a sequence in a row."""
+    rng = np.random.default_rng(45)
+    lens = [70001, 9000]
+    b = batch_of(rng, lens, [new, min(new, 2)], 64, extra=extra)
+    cache, records = filled(rng, b[3], 1, 64, 8, 64)
+    q = queries(rng, new + min(new, 2), 2, 64, dtype)
+    y = P.cached_attention(q, cache, *up(*b[:3]))
+    check_attention(y, q, records, b[:3], 64, 8, 64)
+
+
+@pytest.mark.parametrize("wide", [0, 40000])
+def test_captured_graph_with_other_prefixes(wide):
+    """Replayed with other prefixes, none among them, other tokens and lengths."""
+    rng = np.random.default_rng(46)
+    heads, kv_heads, dim, bits, page, n = 6, 2, 64, 8, 32, 5
+    cache, records = filled(rng, 60, kv_heads, dim, bits, page)
+    starts = torch.zeros(n + 1, dtype=torch.int32, device="cuda")
+    lengths = torch.zeros(n, dtype=torch.int32, device="cuda")
+    table = torch.full((n, 6), -1, dtype=torch.int32, device="cuda")
+    pages = torch.full((10 + wide,), -1, dtype=torch.int32, device="cuda")
+    length = torch.zeros(1, dtype=torch.int32, device="cuda")
+    q = torch.zeros((12, heads, dim), device="cuda")
+    out = torch.zeros_like(q)
+
+    def step():
+        P.cached_attention(q, cache, starts, lengths, table, prefix=(pages, length), out=out)
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step()
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step()
+    for before in (100, 0, 317, 1, 64):
+        order = rng.permutation(60).astype(np.int32)
+        new = rng.integers(0, 3, n)
+        lens = new + rng.integers(0, 100, n)
+        st, ln, tb, _ = batch_of(rng, list(lens), list(new), page, pages=60)
+        starts.copy_(torch.from_numpy(st))
+        lengths.copy_(torch.from_numpy(ln))
+        table.fill_(-1)
+        table[:, :tb.shape[1]].copy_(torch.from_numpy(tb))
+        pages[:10].copy_(torch.from_numpy(order[:10]))
+        length.fill_(before)
+        q.copy_(queries(rng, 12, heads, dim, "f32"))
+        out.fill_(9)
+        graph.replay()
+        check_attention(out, q, records, (st, ln, tb), dim, bits, page,
+                        prefix=(order[:10], before))
+        assert (out[st[-1]:] == 9).all()
+        eager = P.cached_attention(q, cache, starts, lengths, table, prefix=(pages, length))
+        assert torch.equal(eager[:st[-1]], out[:st[-1]])
+
+
+def test_two_calls_at_once():
+    """Calls on two streams over one cache, each with its own workspace."""
+    rng = np.random.default_rng(47)
+    b = batch_of(rng, [3000, 700], [1, 200], 64)
+    cache, records = filled(rng, b[3], 2, 128, 8, 64)
+    args = up(*b[:3])
+    qs = [queries(rng, 201, 8, 128, "bf16") for _ in range(2)]
+    want = [P.cached_attention(q, cache, *args) for q in qs]
+    check_attention(want[0], qs[0], records, b[:3], 128, 8, 64)
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    got = [[], []]
+    for s in streams:
+        s.wait_stream(torch.cuda.current_stream())
+    for _ in range(5):
+        for i, s in enumerate(streams):
+            with torch.cuda.stream(s):
+                got[i].append(P.cached_attention(qs[i], cache, *args))
+    torch.cuda.synchronize()
+    for i in range(2):
+        assert all(torch.equal(y, want[i]) for y in got[i])
