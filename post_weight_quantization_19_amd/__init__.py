@@ -797,7 +797,7 @@ def cache_write(k: torch.Tensor, v: torch.Tensor, cache: dict, starts: torch.Ten
     if (k.requires_grad or v.requires_grad) and torch.is_grad_enabled():
         _no_gradient(k, v)
     c, b, heads, dim, _ = _cache_args(cache, starts, lengths, table, dev)
-    shape = (k.shape[0], heads, dim)
+    shape = (*k.shape[:1], heads, dim)
     kts, khs = _heads(k, "k", shape, k.dtype, dev)
     vts, vhs = _heads(v, "v", shape, k.dtype, dev)
     status = lib().pwq_cache_write(c, b, k.data_ptr(), kts, khs, v.data_ptr(), vts, vhs,
