@@ -138,22 +138,8 @@ __device__ __forceinline__ int up_field(float top) {
   return max(min(267 - (int)(__float_as_uint(top) >> 23), 253), 1);
 }
 
-struct __attribute__((packed, aligned(1))) any16 { uint32_t v[4]; };
 struct __attribute__((packed, aligned(1))) any8 { uint32_t v[2]; };
-// Eight elements of q in float32, and four of out (any alignment).
-__device__ __forceinline__ void load_row8(const float* p, float (&x)[8]) {
-  const any16 a = ((const any16*)p)[0], b = ((const any16*)p)[1];
-#pragma unroll
-  for (int e = 0; e < 4; ++e) x[e] = __uint_as_float(a.v[e]), x[4 + e] = __uint_as_float(b.v[e]);
-}
-__device__ __forceinline__ void load_row8(const uint16_t* p, float (&x)[8]) {
-  const any16 a = *(const any16*)p;
-#pragma unroll
-  for (int e = 0; e < 4; ++e) {
-    x[2 * e] = __uint_as_float(a.v[e] << 16);
-    x[2 * e + 1] = __uint_as_float(a.v[e] & 0xffff0000u);
-  }
-}
+// Four elements of out (any alignment).
 __device__ __forceinline__ void store_row4(float* p, const float (&y)[4]) {
   *(any16*)p = any16{{__float_as_uint(y[0]), __float_as_uint(y[1]), __float_as_uint(y[2]),
                       __float_as_uint(y[3])}};
@@ -302,7 +288,7 @@ struct RowsArgs {
   CacheView cache;
   CacheBatch batch;
   CacheTensor q, out;
-  int group, heads, causal, capacity, direct, whole;   // whole: a worker for each item
+  int group, causal, capacity, direct, whole;   // whole: a worker for each item
   int64_t workers, items;
   float scale;
   float* slots;
@@ -395,7 +381,7 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void attend_rows(const RowsP
                      (int64_t)head * a.q.hs + 8 * g;
       float x[J][8], mine = 0.0f;
 #pragma unroll
-      for (int j = 0; j < J; ++j) load_row8(src + 32 * j, x[j]);
+      for (int j = 0; j < J; ++j) load8(src + 32 * j, x[j]);
 #pragma unroll
       for (int j = 0; j < J; ++j)
 #pragma unroll
@@ -672,7 +658,7 @@ struct TilesArgs {
   CacheView cache;
   CacheBatch batch;
   CacheTensor q, out;
-  int group, heads, causal, capacity;
+  int group, causal, capacity;
   int64_t splits, items;
   float scale;
   float* slots;            // NULL: one split, results written to out
@@ -747,7 +733,7 @@ __global__ __launch_bounds__(512, 1) void attend_tiles(const TilesArgs a) {
     const T* src = (const T*)a.q.p + (int64_t)(q.r0 + r / a.group) * a.q.ts +
                    (int64_t)(h * a.group + r % a.group) * a.q.hs + 8 * g;
 #pragma unroll
-    for (int j = 0; j < J; ++j) load_row8(src + 32 * j, raw[rt][j]);
+    for (int j = 0; j < J; ++j) load8(src + 32 * j, raw[rt][j]);
   }
   int least = __builtin_amdgcn_readfirstlane(visible[0]);   // the first row sees least
   float f = 0.0f;
@@ -1550,11 +1536,11 @@ hipError_t launch_cached_attention(const AttentionLaunch& a, const AttentionPlan
   l.join.own_per_head = p.tiles ? p.items * p.splits : p.workers + p.items;
   l.join.own_rows = p.tiles ? tile : kRows, l.join.own_tiles = p.tiles;
   if (p.tiles)
-    l.tiles[0] = TilesArgs{a.cache, a.batch, a.q, a.out, group, a.heads, a.causal, capacity,
+    l.tiles[0] = TilesArgs{a.cache, a.batch, a.q, a.out, group, a.causal, capacity,
                            p.splits, p.items, a.scale, p.own_bytes ? (float*)w.own : nullptr,
                            p.own_bytes ? (Found*)w.found : nullptr};
   else
-    l.rows.a[0] = RowsArgs{a.cache, a.batch, a.q, a.out, group, a.heads, a.causal, capacity,
+    l.rows.a[0] = RowsArgs{a.cache, a.batch, a.q, a.out, group, a.causal, capacity,
                            a.prefix.nseq == 0, p.whole, p.workers, p.items, a.scale,
                            (float*)w.own, (Found*)w.found};
   l.rows.a[1].cache = a.cache;
@@ -1563,10 +1549,10 @@ hipError_t launch_cached_attention(const AttentionLaunch& a, const AttentionPlan
     b.starts = a.batch.starts, b.starts_step = a.batch.nseq, b.ntok = a.batch.ntok;
     const int before = capacity_of(a.prefix, a.cache);
     if (p.prefix_tiles)
-      l.tiles[1] = TilesArgs{a.cache, b, a.q, a.out, group, a.heads, 0, before, p.prefix_splits,
+      l.tiles[1] = TilesArgs{a.cache, b, a.q, a.out, group, 0, before, p.prefix_splits,
                              p.prefix_items, a.scale, (float*)w.prefix, nullptr};
     else
-      l.rows.a[1] = RowsArgs{a.cache, b, a.q, a.out, group, a.heads, 0, before, 0, 0,
+      l.rows.a[1] = RowsArgs{a.cache, b, a.q, a.out, group, 0, before, 0, 0,
                              p.prefix_workers, p.prefix_items, a.scale, (float*)w.prefix,
                              (Found*)w.prefix_found};
     l.join.before = (const float*)w.prefix;

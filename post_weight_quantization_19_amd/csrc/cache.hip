@@ -18,24 +18,7 @@
 namespace pwq {
 namespace {
 
-struct __attribute__((packed, aligned(1))) any16 { uint32_t v[4]; };
-
-// Eight consecutive elements (any alignment) in float32, and back.
-template <typename T>
-__device__ __forceinline__ void load8(const T* p, float (&x)[8]) {
-  if constexpr (std::is_same_v<T, float>) {
-    const any16 a = ((const any16*)p)[0], b = ((const any16*)p)[1];
-#pragma unroll
-    for (int e = 0; e < 4; ++e) x[e] = __uint_as_float(a.v[e]), x[4 + e] = __uint_as_float(b.v[e]);
-  } else {
-    const any16 a = *(const any16*)p;
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      x[2 * e] = __uint_as_float(a.v[e] << 16);
-      x[2 * e + 1] = __uint_as_float(a.v[e] & 0xffff0000u);
-    }
-  }
-}
+// Eight float32 to consecutive elements (any alignment).
 template <typename T>
 __device__ __forceinline__ void store8(T* p, const float (&x)[8]) {
   if constexpr (std::is_same_v<T, float>) {

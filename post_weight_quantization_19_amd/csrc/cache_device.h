@@ -83,6 +83,25 @@ __device__ __forceinline__ const uint8_t* record_of(const CacheView& c, const in
   return c.records + (at + (block & ((1 << c.blocks_shift) - 1))) * c.record_bytes;
 }
 
+struct __attribute__((packed, aligned(1))) any16 { uint32_t v[4]; };
+
+// Eight consecutive elements (any alignment) in float32.
+template <typename T>
+__device__ __forceinline__ void load8(const T* p, float (&x)[8]) {
+  if constexpr (std::is_same_v<T, float>) {
+    const any16 a = ((const any16*)p)[0], b = ((const any16*)p)[1];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) x[e] = __uint_as_float(a.v[e]), x[4 + e] = __uint_as_float(b.v[e]);
+  } else {
+    const any16 a = *(const any16*)p;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      x[2 * e] = __uint_as_float(a.v[e] << 16);
+      x[2 * e + 1] = __uint_as_float(a.v[e] & 0xffff0000u);
+    }
+  }
+}
+
 // A word's parts.
 __device__ __forceinline__ float word_step(uint32_t w) { return __uint_as_float(w & ~255u); }
 __device__ __forceinline__ int word_zero(uint32_t w) { return (int)(w & 255u); }
