@@ -122,23 +122,24 @@ pwq_status pwq_cache_read(const pwq_cache* cache, const pwq_batch* batch, void* 
  *   ws     : pwq_cached_attention_workspace_size bytes, 256-byte aligned.
  * Keys multiply as their codes, exactly, and values too but where said.  Rows of a
  * sequence are taken 16 together, or 128 or 256 where there are many.  A power of two
- * scales a row's queries so that the largest element fits float16 (128 or 256: scales
- * all of these rows' alike, where the largest of none but rows of zeros is more than 2^8 below
- * another's):
+ * scales a row's queries so that the largest element fits float16 (128 or 256 together:
+ * all of them alike, where no row's largest, but of rows of zeros, is more than 2^8
+ * below another's):
  *   PWQ_BF16 : an element is exact where it is above 2^-22 of the row's largest, else
  *              off by 2^-30 of it.  A token's weight times its step is rounded to
- *              float16 once (2^-12).  Where rows are taken 128 or 256 together weight, step and
- *              step times code are each rounded (3 times 2^-12).
+ *              float16 once (2^-12).  Where rows are taken 128 or 256 together weight,
+ *              step and step times code are each rounded (3 times 2^-12).
  *   PWQ_F32  : two float16 parts, for elements as for weights: within 2^-22, or 2^-30
  *              of the row's largest element.
  * A weight is off by 2^-33 of the largest so far at least (2^-25 where scores pass
- * 2^25), and a step (128 or 256 together, PWQ_BF16) by 2^-30 of the largest of the
- * sequence's steps: of the tokens that the row sees, and where 128 or 256 are taken together
- * also of up to 31 behind them, to the next multiple of 32.  Sums, maxima and totals are float32, in a fixed order; how a
+ * 2^25), and a step (128 or 256 together, PWQ_BF16) by 2^-30 of the largest step.  The
+ * largest are those of the tokens that the row sees; where 128 or 256 are taken
+ * together, the largest step also of the up to 31 tokens behind them that share a
+ * record with the last.  Sums, maxima and totals are float32, in a fixed order; how a
  * sequence is split, and so the last bits of its rows, depends on the sizes and starts
  * and lengths of the whole batch.  A row of q with an infinity or NaN, or with a token
- * it sees that reads as NaN, gives NaN; other rows are unaffected.  Scores, and steps
- * times 2^44, have to stay within float32.
+ * it sees that reads as NaN, gives NaN; other rows are unaffected.  Scores, scale times
+ * an element of q, and steps times 2^44 have to stay within float32.
  * ---------------------------------------------------------------------- */
 size_t pwq_cached_attention_workspace_size(const pwq_cache* cache, const pwq_batch* batch,
                                            const pwq_batch* prefix, int32_t heads, int32_t dtype,

@@ -19,13 +19,13 @@
 // and by the chain of launch, batch lookup, table, records and join where it is short:
 // one token behind 131071 (277 MB at 8 key heads of 128 channels in 8 bits) takes 60 us
 // with cold caches, 4.6 TB/s, where a large copy reaches 5.03; one token behind 512 takes
-// 11.2, of which 3.8 are a launch and 0.9 each tile of 128 tokens (workgroups of eight
+// 10.9, of which 3.8 are a launch and 0.9 each tile of 128 tokens (workgroups of eight
 // waves there gain 0.7, and lose up to 8 us with 64 sequences).  In 4 bits (64 sequences of 1
-// .. 16384 tokens, 46 us) it does twice the work per byte, and spreading codes to float16,
-// not memory, is what bounds it.  attend_tiles is bound by the issue of matrix and vector
-// instructions of the two waves of a SIMD, 43% and 49% of the cycles: 2048 bf16 tokens behind
-// 8192, 32 heads, 344 us, 898 TFLOP/s, where a large bf16 product of the library reaches
-// 1206.
+// .. 16384 tokens, 45 us) it does twice the work per byte, and spreading codes to float16,
+// not memory, is what bounds it.  attend_tiles' matrix and vector instructions issue for 43%
+// and 50% of the cycles, and do not overlap: 2048 bf16 tokens behind 8192, 32 heads, 343 us at
+// the clock that lasting work has (409 at first), 900 TFLOP/s, where a large bf16 product
+// of the library reaches 1206.
 #include "cache_device.h"
 
 #include <algorithm>
@@ -1259,7 +1259,7 @@ constexpr int kMostParts = 1024;   // of a row
 // prefix: WAVES waves a row, 4 / WAVES rows a workgroup.  All maxima and totals are read at
 // once, then the sums with as many loads in flight.  A row of few parts is a chain of three
 // loads (5.2 us for 32 rows of 8 chats' prefix and own tokens); many rows are bytes: 128
-// tokens x 32 heads of a 32768-token prefix in 16 splits, 34 MB, 12.4 us.
+// tokens x 32 heads of a 32768-token prefix in 16 splits, 34 MB, 11.6 us.
 template <typename T, int D, int WAVES>
 __global__ __launch_bounds__(256) void join_rows(const JoinArgs j) {
   constexpr int ROWS = 4 / WAVES, MOST = kMostParts / ROWS, PER = MOST / (64 * WAVES);
