@@ -127,8 +127,8 @@ pwq_status pwq_cache_read(const pwq_cache* cache, const pwq_batch* batch, void* 
  * below another's):
  *   PWQ_BF16 : an element is exact where it is above 2^-22 of the row's largest, else
  *              off by 2^-30 of it.  A token's weight times its step is rounded to
- *              float16 once (2^-12).  Where rows are taken 128 or 256 together weight,
- *              step and step times code are each rounded (3 times 2^-12).
+ *              float16 once (2^-11).  Where rows are taken 128 or 256 together weight,
+ *              step and step times code are each rounded (3 times 2^-11).
  *   PWQ_F32  : two float16 parts, for elements as for weights: within 2^-22, or 2^-30
  *              of the row's largest element.
  * A weight is off by 2^-33 of the largest so far at least (2^-25 where scores pass

@@ -104,7 +104,8 @@ def test_queries_of_all_sizes_in_a_tile(dtype):
 
 def check_by_what_is_seen(y, q, records, b, dim, bits, page):
     """check_attention of one sequence, where a row's bound counts the steps of the values
-    that it sees (a step of 2^-33 of the largest so far, times a code of at most 255)."""
+    that it sees (a step of 2^-33 of the largest so far, times a code of at most 255).  A rounding to
+    float16, of 11 significant bits, is off by 2^-11 at most."""
     starts, lens, table = b
     new, group, bf16 = starts[1], q.shape[1] // records.shape[1], q.dtype == torch.bfloat16
     k, v, there = C.stored(records, table[0], lens[0], dim, bits, page)
@@ -116,7 +117,7 @@ def check_by_what_is_seen(y, q, records, b, dim, bits, page):
         steps = (vh.max(-1).clip(0) - vh.min(-1).clip(max=0)) / (2 ** bits - 1) * 1.02
         step = np.where(seen, steps, 0).max(1)[:, None]
         off = score * ((dim + 4 + 1.45) * 2.0 ** -24 + (0 if bf16 else 2.0 ** -22))
-        rel = 2 * off + 2.0 ** -21 + (3 * 2.0 ** -12 if bf16 else 2.0 ** -22)
+        rel = 2 * off + 2.0 ** -21 + (3 * 2.0 ** -11 if bf16 else 2.0 ** -22)
         rel = rel + (n / 16 + 64) * 2.0 ** -24
         tol = rel[:, None] * (size + np.abs(want)) + (n + 9) * 2.0 ** -33 * step * 255
         tol = tol * 1.01 + (2.0 ** -8 * 1.01 if bf16 else 2.0 ** -23) * np.abs(want)
