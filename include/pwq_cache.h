@@ -132,11 +132,10 @@ pwq_status pwq_cache_read(const pwq_cache* cache, const pwq_batch* batch, void* 
  *   PWQ_F32  : two float16 parts, for elements as for weights: within 2^-22, or 2^-30
  *              of the row's largest element.
  * A weight is off by 2^-33 of the largest so far at least (2^-25 where scores pass
- * 2^25), and a step (128 or 256 together, PWQ_BF16) by 2^-30 of the largest step.  The
- * largest are those of the tokens that the row sees; where 128 or 256 are taken
- * together, the largest step also of the up to 31 tokens behind them that share a
- * record with the last.  Sums, maxima and totals are float32, in a fixed order; how a
- * sequence is split, and so the last bits of its rows, depends on the sizes and starts
+ * 2^25), and a step (128 or 256 together, PWQ_BF16) by 2^-30 of the largest of the steps
+ * that the row sees, or 2^-22 of itself.  Neither other rows nor tokens that a row does
+ * not see make it less exact.  Sums, maxima and totals are float32, in a fixed order; how
+ * a sequence is split, and so the last bits of its rows, depends on the sizes and starts
  * and lengths of the whole batch.  A row of q with an infinity or NaN, or with a token
  * it sees that reads as NaN, gives NaN; other rows are unaffected.  Scores, scale times
  * an element of q, and steps times 2^44 have to stay within float32.

@@ -112,6 +112,44 @@ __device__ __forceinline__ uint32_t bias4(int z0, int z1) {
   return 0xd400d400u | (uint32_t)(z0 & 15) << 4 | (uint32_t)(z1 & 15) << 20;
 }
 
+// A lane's eight codes of keys (4 bits: of w0 alone), or of values (4 bits: channels 16 n + a
+// of an even n, or odd), less their zero points, as a fragment of float16.
+template <int BITS>
+__device__ __forceinline__ uint4 key_fragment(uint32_t w0, uint32_t w1, uint32_t b0, uint32_t b4) {
+  if constexpr (BITS == 8)
+    return make_uint4(bytes_less(w0, 0x04010400u, b0), bytes_less(w0, 0x04030402u, b0),
+                      bytes_less(w1, 0x04010400u, b0), bytes_less(w1, 0x04030402u, b0));
+  else
+    return make_uint4(low_less(w0, b0), high_less(w0, b4), low_less(w0 >> 8, b0),
+                      high_less(w0 >> 8, b4));
+}
+template <int BITS>
+__device__ __forceinline__ uint4 value_fragment(uint32_t w0, uint32_t w1, bool odd,
+                                                const uint32_t (&z0)[4], const uint32_t (&z4)[4]) {
+  if constexpr (BITS == 8)
+    return make_uint4(bytes_less(w0, 0x04010400u, z0[0]), bytes_less(w0, 0x04030402u, z0[1]),
+                      bytes_less(w1, 0x04010400u, z0[2]), bytes_less(w1, 0x04030402u, z0[3]));
+  else if (!odd)
+    return make_uint4(low_less(w0, z0[0]), low_less(w0 >> 8, z0[1]), low_less(w1, z0[2]),
+                      low_less(w1 >> 8, z0[3]));
+  else
+    return make_uint4(high_less(w0, z4[0]), high_less(w0 >> 8, z4[1]), high_less(w1, z4[2]),
+                      high_less(w1 >> 8, z4[3]));
+}
+// -(1024 + z) and -(64 + z) of values' zero points, two tokens to a word in the order of a
+// fragment; vx the words of tokens 4 g + i, 16 + 4 g + i.
+template <int BITS>
+__device__ __forceinline__ void value_zeros(const u32x4_t (&vx)[2], uint32_t (&z0)[4],
+                                            uint32_t (&z4)[4]) {
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const int first = BITS == 8 ? k % 2 * 2 : k % 2, other = BITS == 8 ? 1 : 2;
+    const uint32_t z = __builtin_amdgcn_perm(vx[k / 2][first + other], vx[k / 2][first],
+                                             0x0c040c00u);
+    z0[k] = z | 0xe400e400u, z4[k] = (z & 0x000f000fu) << 4 | 0xd400d400u;
+  }
+}
+
 // Weights of a record's tokens 4 g + i (x[i]) and 16 + 4 g + i (x[4 + i]) in the order of
 // a value fragment; x becomes what float16 leaves of it.  (REST: x is held in a register
 // first.  Where the compiler sees the product that x is, it rounds it to float16 twice,
@@ -478,18 +516,9 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void attend_rows(const RowsP
           const uint32_t b0 = bias0(z, z), b4 = bias4(z, z);
 #pragma unroll
           for (int j = 0; j < J; ++j) {
-            uint4 frag;
-            if constexpr (BITS == 8) {
-              const int k = (t * J + j) * 2;
-              const uint32_t w0 = kr[k / 4][k % 4], w1 = kr[k / 4][k % 4 + 1];
-              frag = make_uint4(bytes_less(w0, 0x04010400u, b0), bytes_less(w0, 0x04030402u, b0),
-                                bytes_less(w1, 0x04010400u, b0), bytes_less(w1, 0x04030402u, b0));
-            } else {
-              const int k = t * J + j;
-              const uint32_t w0 = kr[k / 4][k % 4], w1 = w0 >> 8;
-              frag = make_uint4(low_less(w0, b0), high_less(w0, b4), low_less(w1, b0),
-                                high_less(w1, b4));
-            }
+            const int k = (t * J + j) * (BITS / 4);
+            const uint4 frag = key_fragment<BITS>(kr[k / 4][k % 4],
+                                                  BITS == 8 ? kr[k / 4][k % 4 + 1] : 0, b0, b4);
 #pragma unroll
             for (int part = 0; part < PARTS; ++part)
               acc[t] = mfma(as_half8(frag), qf[part][j], acc[t]);
@@ -577,31 +606,12 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void attend_rows(const RowsP
         for (int part = 0; part < PARTS; ++part) pf[part] = weight_part<BITS, PARTS == 2>(x);
         // values
         uint32_t z0[4], z4[4];
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const int first = BITS == 8 ? k % 2 * 2 : k % 2, other = BITS == 8 ? 1 : 2;
-          const uint32_t z = __builtin_amdgcn_perm(vx[k / 2][first + other], vx[k / 2][first],
-                                                   0x0c040c00u);
-          z0[k] = z | 0xe400e400u, z4[k] = (z & 0x000f000fu) << 4 | 0xd400d400u;
-        }
+        value_zeros<BITS>(vx, z0, z4);
 #pragma unroll
         for (int k = 0; k < N; ++k) {
-          uint4 frag;
-          if constexpr (BITS == 8) {
-            const uint32_t w0 = vr[k / 2][k % 2 * 2], w1 = vr[k / 2][k % 2 * 2 + 1];
-            frag = make_uint4(bytes_less(w0, 0x04010400u, z0[0]),
-                              bytes_less(w0, 0x04030402u, z0[1]),
-                              bytes_less(w1, 0x04010400u, z0[2]),
-                              bytes_less(w1, 0x04030402u, z0[3]));
-          } else {
-            const uint32_t w0 = vr[k / 4][k / 2 % 2 * 2], w1 = vr[k / 4][k / 2 % 2 * 2 + 1];
-            if (k % 2 == 0)
-              frag = make_uint4(low_less(w0, z0[0]), low_less(w0 >> 8, z0[1]),
-                                low_less(w1, z0[2]), low_less(w1 >> 8, z0[3]));
-            else
-              frag = make_uint4(high_less(w0, z4[0]), high_less(w0 >> 8, z4[1]),
-                                high_less(w1, z4[2]), high_less(w1 >> 8, z4[3]));
-          }
+          const int at = BITS == 8 ? k : k / 2;
+          const uint4 frag = value_fragment<BITS>(vr[at / 2][at % 2 * 2], vr[at / 2][at % 2 * 2 + 1],
+                                                  k % 2, z0, z4);
 #pragma unroll
           for (int part = 0; part < PARTS; ++part)
             o[k] = mfma(as_half8(frag), as_half8(pf[part]), o[k]);
@@ -697,6 +707,7 @@ __global__ __launch_bounds__(512, 1) void attend_tiles(const TilesArgs a) {
   __shared__ __align__(16) uint32_t one_h[4];  // four times two ones
   __shared__ float2 about[4];                  // of a record: its ref; its tokens that are there
   __shared__ int entries[WAVES][64];           // table entries, a wave's own
+  __shared__ int apart[16], apart_count;       // records left to the end
   const int h = (int)(block_index() % a.cache.heads);
   const int64_t rest = block_index() / a.cache.heads;
   const int64_t split = rest % a.splits, item = a.items - 1 - rest / a.splits;
@@ -736,6 +747,8 @@ __global__ __launch_bounds__(512, 1) void attend_tiles(const TilesArgs a) {
     for (int j = 0; j < J; ++j) load8(src + 32 * j, raw[rt][j]);
   }
   int least = __builtin_amdgcn_readfirstlane(visible[0]);   // the first row sees least
+  const int least_of_all = visible_of(0);
+  if (threadIdx.x == 0) apart_count = 0;
   float f = 0.0f;
   // All rows are scaled alike, by their largest, where none is more than 2^8 below it (rows of
   // zeros aside): f goes into the keys' steps, for all.  Else each by its own, scores are brought
@@ -854,15 +867,26 @@ __global__ __launch_bounds__(512, 1) void attend_tiles(const TilesArgs a) {
     st.there = w.there;
   };
   // Wave 0: a record's steps and zero points for all; ref is raised where a value's step is
-  // above 8 of it.
+  // above 8 of it.  The unit is one for all rows: a record of which some rows do not see all
+  // tokens, whose values' steps are further apart than 2^8, is one without tokens here (there
+  // are 9 of them at most), and is left to the end, where each row has its own unit.
   float ref = 0.0f, staged_ref = 0.0f, unit = 0.0f;     // of the sums; of the values staged
+  int staged = i0, parted = 0;                          // the record; those left
   auto steps = [&](const Words& st, int buf) __attribute__((always_inline)) {
     if (wave != 0) return;
     const float step = word_step(st.word);
     const int k = lane & 31;
-    const bool there = k < st.there;
+    int count = st.there;
+    float sv = lane >= 32 && k < count && step == step ? step : 0.0f;
+    if (__builtin_expect(staged * 32 + count > least_of_all && staged < i1, 0)) {
+      if (wave_min(sv > 0.0f ? sv : __FLT_MAX__) * 256.0f < wave_max(sv)) {
+        if (lane == 0) apart[parted] = staged, apart_count = parted + 1;
+        ++parted, count = 0, sv = 0.0f;
+      }
+    }
+    ++staged;
+    const bool there = k < count;
     const uint64_t nan = __ballot(step != step) >> 32;
-    const float sv = lane >= 32 && there && step == step ? step : 0.0f;
     if (__builtin_expect(__any(sv > staged_ref * 8.0f), 0)) {
       staged_ref = __uint_as_float(
           __float_as_uint(fminf(fmaxf(wave_max(sv), 0x1p-126f * kUnit), 0x1p100f)) & 0x7f800000u);
@@ -882,7 +906,7 @@ __global__ __launch_bounds__(512, 1) void attend_tiles(const TilesArgs a) {
       else step_h[buf][at] = (_Float16)(sv * unit);
       zero_v[buf][at] = (uint16_t)zero;
     }
-    if (lane == 0) about[buf] = make_float2(staged_ref, (float)st.there);
+    if (lane == 0) about[buf] = make_float2(staged_ref, (float)count);
     __builtin_amdgcn_s_waitcnt(0xc07f);        // there before the barrier (lgkmcnt(0))
   };
   // What a task needs of them, read a turn ahead.
@@ -1196,6 +1220,97 @@ __global__ __launch_bounds__(512, 1) void attend_tiles(const TilesArgs a) {
       const int last = (i1 - 1 - i0) & 3;
       rescale(i1 - 1);
       multiply(last, 0, no, [](auto) {});
+    }
+    // The records left, as attend_rows takes them: spread in this wave's registers.
+    const int left = __builtin_amdgcn_readfirstlane(apart_count);
+    for (int a_record = 0; a_record < left; ++a_record) {
+      const int i = __builtin_amdgcn_readfirstlane(apart[a_record]), p0 = 32 * i;
+      const int page = __builtin_amdgcn_readfirstlane(table[i >> a.cache.blocks_shift]);
+      const uint8_t* rec = head_base + page * page_bytes + (i & in_page) * R::bytes;
+      const int n = min(most - p0, 32);
+      const uint8_t* mine = rec + (uint32_t)(lane * 16);
+      u32x4_t kx[2], vx[2];
+      uint32_t kw[2], z0[4], z4[4];
+#pragma unroll
+      for (int t = 0; t < 2; ++t) {
+        kw[t] = *(const uint32_t*)(rec + (uint32_t)(R::words + 64 * t + 4 * col));
+        kx[t] = *(const u32x4_t*)(rec + (uint32_t)(R::words + 64 * t + 16 * g));
+        vx[t] = *(const u32x4_t*)(rec + (uint32_t)(R::words + 128 + 64 * t + 16 * g));
+      }
+      value_zeros<BITS>(vx, z0, z4);
+#pragma unroll
+      for (int rt = 0; rt < RT; ++rt) {
+#pragma clang fp contract(off)                 // (as in weight_of)
+        const int row = (rt * WAVES + wave) * 16 + col;
+        const int seen = min(visible[rt] - p0, n) - 4 * g;
+        const float scale = row_scale[row];
+        float x[8], sv[8], t[8], m = kNone, largest = 0.0f;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          f32x4_t acc = {0, 0, 0, 0};
+          const int z = word_zero(kw[h]);
+#pragma unroll
+          for (int j = 0; j < J; ++j) {
+            const int k = (h * J + j) * BITS;
+            const uint32_t* w = (const uint32_t*)(mine + k / 16 * 1024 + k % 16);
+            const f16x8_t frag = as_half8(key_fragment<BITS>(w[0], BITS == 8 ? w[1] : 0,
+                                                             bias0(z, z), bias4(z, z)));
+#pragma unroll
+            for (int part = 0; part < PARTS; ++part) acc = mfma(frag, qf[rt][part][j], acc);
+          }
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const int k = 4 * h + e;
+            t[k] = acc[e] * scale * (word_step(kx[h][e]) * f);
+            sv[k] = word_step(vx[h][e]);
+            if (16 * h + e >= seen) sv[k] = 0.0f, t[k] = kNone;
+            if (sv[k] != sv[k]) t[k] = sv[k], sv[k] = 0.0f;
+            m = fmaxf(m, t[k]), largest = fmaxf(largest, sv[k]);
+          }
+        }
+        m = fmaxf(m, __shfl_xor(m, 16, 64));
+        m = fmaxf(m, __shfl_xor(m, 32, 64));
+        largest = fmaxf(largest, __shfl_xor(largest, 16, 64));
+        largest = fmaxf(largest, __shfl_xor(largest, 32, 64));
+        const float next = fmaxf(base[rt], base_of(m));
+        float factor = base[rt] == kNone ? 0.0f : __builtin_amdgcn_exp2f(base[rt] - next);
+        base[rt] = next;
+        l[rt] *= factor;
+        float own = row_ref[row];
+        if (largest > own * 8.0f) {
+          const float to = __uint_as_float(
+              __float_as_uint(fminf(fmaxf(largest, 0x1p-126f * kUnit), 0x1p100f)) & 0x7f800000u);
+          factor *= own / to;
+          own = to;
+          row_ref[row] = to;
+        }
+        float sum = 0.0f;
+        const float over = own > 0.0f ? 1.0f / own : 0.0f;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          const float e = t[k] == kNone ? 0.0f : __builtin_amdgcn_exp2f(t[k] - next);
+          sum += e;
+          x[k] = e * (sv[k] * over);
+        }
+        if constexpr (PARTS == 1) {                // (l: the whole row's in every lane)
+          sum += __shfl_xor(sum, 16, 64);
+          sum += __shfl_xor(sum, 32, 64);
+        }
+        l[rt] += sum;
+        uint4 pf[PARTS];
+#pragma unroll
+        for (int part = 0; part < PARTS; ++part) pf[part] = weight_part<BITS, PARTS == 2>(x);
+#pragma unroll
+        for (int k = 0; k < N; ++k) {
+          const int at = (BITS == 8 ? k : k / 2) * 8;
+          const uint32_t* w = (const uint32_t*)(mine + R::codes + at / 16 * 1024 + at % 16);
+          const f16x8_t frag = as_half8(value_fragment<BITS>(w[0], w[1], k % 2, z0, z4));
+          f32x4_t y = {0, 0, 0, 0};
+#pragma unroll
+          for (int part = 0; part < PARTS; ++part) y = mfma(frag, as_half8(pf[part]), y);
+          o[rt][k] = o[rt][k] * factor + y * kUnit;
+        }
+      }
     }
   }
   if (!busy) return;

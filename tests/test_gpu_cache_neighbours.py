@@ -187,3 +187,30 @@ def test_queries_far_above_others_over_many_records(heads, dim, bits, dtype, pow
     for some in (slice(0, 2), slice(heads - 1, heads)):
         records = cache["records"][:, some].cpu().numpy()
         check_attention(y[:, some], q[:, some], records, b[:3], dim, bits, 32)
+
+
+@pytest.mark.parametrize("power", [9, 20, 34, 90])
+@pytest.mark.parametrize("heads,dim,bits,dtype", MANY + [(4, 64, 8, "bf16"), (2, 128, 4, "f32"),
+                                                         (3, 256, 8, "bf16"), (3, 256, 4, "f32")])
+def test_values_in_the_record_of_a_row_in_tiles(heads, dim, bits, dtype, power):
+    """Tokens here and there with values 2^power above the others', in the 32 tokens that rows
+    end in: a row is as exact as what it sees lets it be.  Some read as NaN."""
+    rng = np.random.default_rng(dim + power)
+    n, new = 450, 250
+    b = batch_of(rng, [n], [new], 32, extra=0 if heads > 200 else WIDE)
+    cache = P.new_cache(b[3], heads, dim, bits, 32)
+    k, v = keys_values(rng, (n, heads, dim), torch.float32)
+    for t in (203, 230, 231, 290, 300, 310, 395, 448):
+        v[t] *= 2.0 ** power
+    v[[350, 351]] = 0
+    v[430, :, 5] = float("nan")
+    k[440, :, 7] = float("inf")
+    P.cache_write(k, v, cache, up(np.array([0, n], np.int32))[0], *up(*b[1:3]))
+    q = queries(rng, new, heads, dim, dtype)
+    y = P.cached_attention(q, cache, *up(*b[:3]))
+    rows = 430 - (n - new)
+    assert torch.isnan(y[rows:]).all() and not torch.isnan(y[:rows]).any()
+    cut = (np.array([0, rows], np.int32), [430], b[2])
+    for some in (slice(0, 2), slice(heads - 1, heads)):
+        records = cache["records"][:, some].cpu().numpy()
+        check_by_what_is_seen(y[:rows, some], q[:rows, some], records, cut, dim, bits, 32)
