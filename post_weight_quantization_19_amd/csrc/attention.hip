@@ -582,7 +582,7 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void attend_rows(const RowsP
           largest = fmaxf(largest, __shfl_xor(largest, 32, 64));
           if (largest > ref * 8.0f) {
             const float to = __uint_as_float(
-                __float_as_uint(fminf(fmaxf(largest, 0x1p-126f), 0x1p100f)) & 0x7f800000u);
+                __float_as_uint(fminf(fmaxf(largest, 0x1p-126f), 0x1p127f)) & 0x7f800000u);
             factor *= ref / to;
             ref = to, unit = 1.0f / to;
           }
@@ -889,7 +889,7 @@ __global__ __launch_bounds__(512, 1) void attend_tiles(const TilesArgs a) {
     const uint64_t nan = __ballot(step != step) >> 32;
     if (__builtin_expect(__any(sv > staged_ref * 8.0f), 0)) {
       staged_ref = __uint_as_float(
-          __float_as_uint(fminf(fmaxf(wave_max(sv), 0x1p-126f * kUnit), 0x1p100f)) & 0x7f800000u);
+          __float_as_uint(fminf(fmaxf(wave_max(sv), 0x1p-126f * kUnit), 0x1p127f)) & 0x7f800000u);
       unit = kUnit / staged_ref;
     }
     const uint32_t zero = 0xe400u | (uint32_t)word_zero(st.word);
@@ -1279,7 +1279,7 @@ __global__ __launch_bounds__(512, 1) void attend_tiles(const TilesArgs a) {
         float own = row_ref[row];
         if (largest > own * 8.0f) {
           const float to = __uint_as_float(
-              __float_as_uint(fminf(fmaxf(largest, 0x1p-126f * kUnit), 0x1p100f)) & 0x7f800000u);
+              __float_as_uint(fminf(fmaxf(largest, 0x1p-126f * kUnit), 0x1p127f)) & 0x7f800000u);
           factor *= own / to;
           own = to;
           row_ref[row] = to;

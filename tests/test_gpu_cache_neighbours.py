@@ -214,3 +214,28 @@ def test_values_in_the_record_of_a_row_in_tiles(heads, dim, bits, dtype, power):
     for some in (slice(0, 2), slice(heads - 1, heads)):
         records = cache["records"][:, some].cpu().numpy()
         check_by_what_is_seen(y[:rows, some], q[:rows, some], records, cut, dim, bits, 32)
+
+
+@pytest.mark.parametrize("heads,dim,bits,dtype", MANY + [(4, 64, 8, "bf16"), (2, 128, 4, "f32"),
+                                                         (3, 256, 8, "bf16"), (3, 256, 4, "f32")])
+@pytest.mark.parametrize("new", [8, 250])
+def test_the_largest_values_and_keys_behind_a_row(new, heads, dim, bits, dtype):
+    """Tokens behind a row with values and keys near float32's largest: the row is as without,
+    whether they share its record, or some of it, or none."""
+    rng = np.random.default_rng(dim)
+    n = 450
+    b = batch_of(rng, [n], [new], 32, extra=0 if heads > 200 or new == 8 else WIDE)
+    for first in (447, 446, 420, 416):
+        if first < n - new + 1:
+            continue
+        cache = P.new_cache(b[3], heads, dim, bits, 32)
+        k, v = keys_values(rng, (n, heads, dim), torch.float32)
+        k[first:], v[first:] = 1.6e38 * torch.sign(k[first:]), 1.6e38 * torch.sign(v[first:])
+        P.cache_write(k, v, cache, up(np.array([0, n], np.int32))[0], *up(*b[1:3]))
+        q = queries(rng, new, heads, dim, dtype)
+        y = P.cached_attention(q, cache, *up(*b[:3]))
+        rows = first - (n - new)
+        cut = (np.array([0, rows], np.int32), [first], b[2])
+        for some in (slice(0, 2), slice(heads - 1, heads)):
+            records = cache["records"][:, some].cpu().numpy()
+            check_by_what_is_seen(y[:rows, some], q[:rows, some], records, cut, dim, bits, 32)
