@@ -22,9 +22,9 @@
 // 10.9, of which 3.8 are a launch and 0.9 each tile of 128 tokens (workgroups of eight
 // waves there gain 0.7, and lose up to 8 us with 64 sequences).  In 4 bits (64 sequences of 1
 // .. 16384 tokens, 45 us) it does twice the work per byte, and spreading codes to float16,
-// not memory, is what bounds it.  attend_tiles' matrix and vector instructions issue for 43%
-// and 50% of the cycles, and do not overlap: 2048 bf16 tokens behind 8192, 32 heads, 343 us at
-// the clock that lasting work has (409 at first), 900 TFLOP/s, where a large bf16 product
+// not memory, is what bounds it.  attend_tiles' matrix and vector instructions issue for 42%
+// and 49% of the cycles, and do not overlap: 2048 bf16 tokens behind 8192, 32 heads, 347 us at
+// the clock that lasting work has (420 at first), 890 TFLOP/s, where a large bf16 product
 // of the library reaches 1206.
 #include "cache_device.h"
 

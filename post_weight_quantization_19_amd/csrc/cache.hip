@@ -10,9 +10,9 @@
 //
 // Measured with the caches' own bytes warm, us (writing, reading; bf16, 8 key heads of 128
 // channels in 8 bits unless said otherwise): one token 3.5, 2.5; 256 sequences' next tokens in
-// 4 bits 5.8, 4.6; 10589 tokens of 6 prompts 22.6 and 14.7 (66 MB each, 2.9 and 4.5 TB/s;
+// 4 bits 5.7, 4.5; 10589 tokens of 6 prompts 22.6 and 14.8 (66 MB each, 2.9 and 4.5 TB/s;
 // writing's quantization, and its byte stores to LDS, not memory, are what is left), in
-// float32 24.0 and 22.0 (109 MB, 4.5 and 5.0 TB/s); 65536 tokens read 89.5 (407 MB, 4.5 TB/s,
+// float32 23.6 and 22.0 (109 MB, 4.6 and 5.0 TB/s); 65536 tokens read 89.6 (407 MB, 4.5 TB/s,
 // where a large copy reaches 5.03).
 #include "cache_device.h"
 
