@@ -8,9 +8,9 @@
 // Keys times queries: 16x16x32 float16 matrix products, 16 keys x 32 channels of
 // codes (exact: |c - z| <= 255) by 32 channels x 16 rows of q' (scaled so that a row's
 // largest is in 2^13 .. 2^14, in attend_tiles the largest of rows taken together where all
-// are near it; float32 queries in two float16 parts).  The result has a lane for four keys of one row, which is where the
-// next product, values times weights, wants its weights: P never leaves the
-// registers.  Weights are held as 2^8 at the running maximum, up to 2^12 before it is
+// are near it; float32 queries in two float16 parts).  The result has a lane for four keys
+// of one row, which is where the next product, values times weights, wants its weights: P
+// never leaves the registers.  Weights are held as 2^8 at the running maximum, up to 2^12 before it is
 // raised, so that sums are rescaled rarely.  A partial result is the maximum less 8, and a
 // 256th of the total and of the sums (weights of 16 at most, so that many add up in float32).
 //
@@ -61,9 +61,9 @@ __device__ __forceinline__ f32x4_t mfma(f16x8_t a, f16x8_t b, f32x4_t c) {
 // base.  The maximum is a rounded product, off by half of float32's spacing: from 2^25 on
 // that is 2 and more, and at 2^30 the largest weight may be anything in 2^-56 .. 2^72 (a
 // single token gave 0 or NaN).  weight_of takes the rounded product too, so that the largest
-// score less the maximum is exact.  It is for rows whose maximum is that far from 0, and used where
-// a maximum has just been raised.  Weights are held as 2^8 at the maximum as far as float32
-// tells scores 8 apart.
+// score less the maximum is exact.  It is for rows whose maximum is that far from 0, and used
+// where a maximum has just been raised.  Weights are held as 2^8 at the maximum as far as
+// float32 tells scores 8 apart.
 constexpr float kFar = 0x1p25f;
 __device__ __forceinline__ bool is_far(float base) {
   return fabsf(base) >= kFar && base != kNone;
@@ -610,8 +610,8 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void attend_rows(const RowsP
 #pragma unroll
         for (int k = 0; k < N; ++k) {
           const int at = BITS == 8 ? k : k / 2;
-          const uint4 frag = value_fragment<BITS>(vr[at / 2][at % 2 * 2], vr[at / 2][at % 2 * 2 + 1],
-                                                  k % 2, z0, z4);
+          const uint32_t w0 = vr[at / 2][at % 2 * 2], w1 = vr[at / 2][at % 2 * 2 + 1];
+          const uint4 frag = value_fragment<BITS>(w0, w1, k % 2, z0, z4);
 #pragma unroll
           for (int part = 0; part < PARTS; ++part)
             o[k] = mfma(as_half8(frag), as_half8(pf[part]), o[k]);

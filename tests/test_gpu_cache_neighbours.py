@@ -104,8 +104,8 @@ def test_queries_of_all_sizes_in_a_tile(dtype):
 
 def check_by_what_is_seen(y, q, records, b, dim, bits, page):
     """check_attention of one sequence, where a row's bound counts the steps of the values
-    that it sees (a step of 2^-33 of the largest so far, times a code of at most 255).  A rounding to
-    float16, of 11 significant bits, is off by 2^-11 at most."""
+    that it sees (a step of 2^-33 of the largest so far, times a code of at most 255).  A
+    rounding to float16, of 11 significant bits, is off by 2^-11 at most."""
     starts, lens, table = b
     new, group, bf16 = starts[1], q.shape[1] // records.shape[1], q.dtype == torch.bfloat16
     k, v, there = C.stored(records, table[0], lens[0], dim, bits, page)
